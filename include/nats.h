@@ -551,6 +551,167 @@ nats_status nats_nha_fwd_profiled(const nats_nha_dims* dims, const void* q, cons
                                   const float* log_alpha, void* out, void* workspace, size_t workspace_bytes,
                                   nats_stream_t stream, nats_profile* prof);
 
+/* ------------------------------------- query / key norm and rotation
+ * RMSNorm of each head's query and key row and the rotary position rotation
+ * in one pass, ahead of an attention layer or a cache: for a row x of d
+ * entries at position p,
+ *   n = sqrt(mean(x^2) + eps),  z = w x / n  (z = x without the norm),
+ *   y = z with pair i < rot / 2 turned by the angle p inv_freq[i]:
+ *     (y_a, y_b) = (z_a cos - z_b sin, z_b cos + z_a sin),
+ *   (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved; entries
+ *   from rot on are z unchanged.
+ * A weight of d^(-1/2) in every entry makes it the L2 norm that the Gated
+ * DeltaNet branch of nats_hybrid_fwd wants of its keys.
+ * Angles are formed in 64-bit fixed-point turns, so that they hold at any
+ * int64 position to the precision of inv_freq (about 1e-9 rad at a million).
+ *
+ * Operands are indexed [B, H, L, d] through element strides (the last one is
+ * 1), so q and k may lie inside one projection's output and the results in a
+ * layer's contiguous layout or in place (out = in, same strides); other
+ * overlaps of inputs and outputs are not allowed.  Rows whose addresses are
+ * multiples of four elements (16 bytes fp32, 8 bytes bf16) move in vectors,
+ * others entry by entry. */
+typedef struct {
+  int64_t b, h, t; /* elements between sequences, heads, tokens */
+} nats_strides;
+
+typedef struct {
+  int32_t B, L;        /* sequences, tokens of each */
+  int32_t Hq, Hk;      /* query and key heads (either may be 0) */
+  int32_t d;           /* head size, 64 or 128 */
+  int32_t rot;         /* rotated entries: a multiple of 8, 0 .. d */
+  int32_t interleaved; /* pairs: 0 (i, i + rot / 2), 1 (2 i, 2 i + 1) */
+  int32_t norm;        /* 1: RMSNorm; 0: rotation alone (weights and eps not used) */
+  int32_t dtype;       /* nats_dtype of q, k and the outputs */
+  float eps;
+} nats_rope_dims;
+
+/* Forward.  w_q, w_k fp32 [d] or NULL (unit); inv_freq double [rot / 2]
+ * (NULL only when rot is 0); pos int64 [B, L] with pos_stride_b elements
+ * between sequences (0: shared), or NULL: token t is at position pos0 + t.
+ * q / k and their outputs may be NULL when Hq / Hk is 0.  All pointers device
+ * but the strides and dims.  Errors before any launch: NATS_ERR_NULL,
+ * NATS_ERR_SHAPE (negative extents, rot), NATS_ERR_DTYPE, NATS_ERR_UNSUPPORTED
+ * (d; B L (Hq + Hk) beyond 2^40), NATS_ERR_VALUE (eps), NATS_ERR_ALIGN (a
+ * pointer not aligned to its element); NATS_ERR_CUDA on a failed launch. */
+nats_status nats_qk_norm_rope(const nats_rope_dims* dims, const void* q, const nats_strides* q_st, const void* k,
+                              const nats_strides* k_st, const float* w_q, const float* w_k, const double* inv_freq,
+                              const int64_t* pos, int64_t pos_stride_b, int64_t pos0, void* q_out,
+                              const nats_strides* q_out_st, void* k_out, const nats_strides* k_out_st,
+                              nats_stream_t stream);
+
+/* Its gradient: dq_out, dk_out (the gradients of the outputs, grad_dtype)
+ * give dq, dk (dx_dtype) and dw_q, dw_k (fp32 [d], overwritten; both NULL:
+ * not computed; not computed without the norm: then they must be NULL):
+ *   u = y's gradient turned back,  dw = sum over rows of u x / n,
+ *   dx = (w u - x <w u, x> / (d n^2)) / n   (dx = u without the norm).
+ * q, k are the forward's inputs.  fp32 inputs take fp32 gradients only (both
+ * types NATS_F32); bf16 inputs any.  dq / dk may lie in place of dq_out /
+ * dk_out when type and strides agree.  dw sums are taken in a fixed order
+ * (the same inputs give the same bits).  workspace: device scratch of
+ * nats_qk_norm_rope_bwd_workspace_size bytes, 16-byte aligned (NULL when dw
+ * is not asked for).  Errors as the forward, and NATS_ERR_WORKSPACE. */
+size_t nats_qk_norm_rope_bwd_workspace_size(const nats_rope_dims* dims);
+nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype, int32_t dx_dtype,
+                                  const void* dq_out, const nats_strides* dq_out_st, const void* dk_out,
+                                  const nats_strides* dk_out_st, const void* q, const nats_strides* q_st,
+                                  const void* k, const nats_strides* k_st, const float* w_q, const float* w_k,
+                                  const double* inv_freq, const int64_t* pos, int64_t pos_stride_b, int64_t pos0,
+                                  void* dq, const nats_strides* dq_st, void* dk, const nats_strides* dk_st,
+                                  float* dw_q, float* dw_k, void* workspace, size_t workspace_bytes,
+                                  nats_stream_t stream);
+
+/* ------------------------------------------------ paged key / value cache
+ * A pool of pages shared by B sequences: page n holds `page` consecutive
+ * token slots of every key head, k_pages / v_pages [n_pages, Hk, page, d].
+ * Slot j of sequence b is row j % page of page table[b, j / page].  lens[b]
+ * slots are in use.  weight (or NULL) holds one fp32 number per slot and key
+ * head, the attention weight that nats_paged_decode has summed there and
+ * nats_paged_evict goes by.  The caller owns and assigns the pages; sequences
+ * may share pages that none of them writes.
+ * The kernels check what the host cannot see: a table entry outside
+ * [0, n_pages), a length outside [0, max_pages page] or an append outside the
+ * table sets err[0] to 1 (never cleared by the library); such a slot is
+ * neither read nor written (an attention leaves it out), lengths are taken
+ * as the nearest valid ones.
+ * All pointers device, k_pages and v_pages 16-byte aligned, contiguous.  At
+ * most 2^30 slots a sequence (max_pages page; else NATS_ERR_UNSUPPORTED). */
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* weight;        /* [n_pages, Hk, page] or NULL */
+  const int32_t* table; /* [B, max_pages]; entries behind a sequence's pages are not read */
+  const int32_t* lens;  /* [B] */
+  int32_t* err;         /* [1] */
+  int32_t n_pages;
+  int32_t page;         /* slots of a page: a multiple of 16 */
+  int32_t Hk;           /* key heads */
+  int32_t d;            /* 64 or 128 */
+  int32_t B;
+  int32_t max_pages;
+  int32_t dtype;        /* nats_dtype of the pages */
+} nats_paged_cache;
+
+/* Appends dims->L new tokens of each sequence: token t < n_new[b] (NULL: all
+ * L) of sequence b goes to slot start[b] + t (start NULL: lens[b]); lens is
+ * not changed (the caller adds n_new before the next decode).  Keys (and
+ * queries, with Hq > 0) take the norm and rotation of nats_qk_norm_rope on
+ * the way (dims->norm 0 and rot 0: a copy); values are copied.  A token's
+ * position for the rotation is pos[b, t] (pos_stride_b as above) or, with
+ * pos NULL, its slot.  q_out rows of tokens from n_new[b] on are left as they
+ * were.  weight, if the cache has it, becomes 0 in the new slots.  No two
+ * tokens of a call may go to one slot.  dims->B, Hk, d, dtype must be the
+ * cache's.  Errors as nats_qk_norm_rope, those of the cache's fields
+ * (NATS_ERR_NULL, _SHAPE, _UNSUPPORTED, _DTYPE, _ALIGN); NATS_ERR_CUDA. */
+nats_status nats_paged_append(const nats_paged_cache* cache, const nats_rope_dims* dims, const void* q,
+                              const nats_strides* q_st, const void* k, const nats_strides* k_st, const void* v,
+                              const nats_strides* v_st, const float* w_q, const float* w_k, const double* inv_freq,
+                              const int32_t* start, const int32_t* n_new, const int64_t* pos, int64_t pos_stride_b,
+                              void* q_out, const nats_strides* q_out_st, nats_stream_t stream);
+
+/* Attention of one new token of each sequence over its slots j < lens[b]
+ * (append the token first for it to see itself): query head h reads key head
+ * h / (Hq / Hk),
+ *   out[b, h] = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
+ * zero for an empty sequence.  q [B, Hq, d] with element strides q_stride_b,
+ * q_stride_h; out [B, Hq, d] contiguous (the cache's dtype); lse (or NULL)
+ * fp32 [B, Hq]: log2 of the sum of 2^(scale log2 e q . k_j), -inf for an
+ * empty sequence.  accumulate != 0 adds the group's weights, sum over its
+ * query heads of p_j, to cache->weight in every slot.  The work is cut into
+ * 64-slot tiles dealt evenly to the GPU whatever the lengths are (they are
+ * read on the device), partial results are joined by a second kernel in a
+ * fixed order.  scale 0 => 1/sqrt(d).  Sequences that share pages must not
+ * accumulate in one call.  workspace: device scratch of
+ * nats_paged_decode_workspace_size bytes, 16-byte aligned; calls that share
+ * it must be ordered by the caller.  Errors before any launch: NATS_ERR_NULL,
+ * _SHAPE (Hq not a multiple of Hk, the cache's fields), _UNSUPPORTED, _DTYPE,
+ * _VALUE (scale), _ALIGN (q, its strides and out: 16 bytes), _WORKSPACE;
+ * NATS_ERR_CUDA on a failed launch. */
+size_t nats_paged_decode_workspace_size(const nats_paged_cache* cache, int32_t Hq, int32_t accumulate);
+nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float scale, const void* q,
+                              int64_t q_stride_b, int64_t q_stride_h, void* out, float* lse, int32_t accumulate,
+                              void* workspace, size_t workspace_bytes, nats_stream_t stream);
+
+/* Eviction by accumulated attention weight.  Of a sequence with n = lens[b] >
+ * budget slots, every key head keeps `budget`: the first `sinks`, the last
+ * `recent`, and of those between the budget - sinks - recent with the largest
+ * weight (ties to the lower slot; NaN counts as the lowest); with n <= budget
+ * it keeps all.  The kept rows (key, value, weight) are copied in their order
+ * to slots 0, 1, .. of the pages out_table[b] ([B, out_max_pages], the same
+ * pool; lens_out[b] = min(n, budget) slots), which none of the cache's
+ * sequences may be using; the old pages stay as they were.  keep (or NULL)
+ * int32 [B, Hk, budget]: the slots kept, in order, -1 behind the last.
+ * lens_out int32 [B] must not be cache->lens.  workspace as above
+ * (nats_paged_evict_workspace_size bytes).  Errors before any launch:
+ * NATS_ERR_NULL (also for a cache without weight), _SHAPE (budget < 0, out
+ * pages that hold less than budget), _VALUE (sinks or recent negative, or
+ * sinks + recent > budget; out_table or lens_out the cache's own), those of
+ * the cache's fields, _ALIGN, _WORKSPACE; NATS_ERR_CUDA. */
+size_t nats_paged_evict_workspace_size(const nats_paged_cache* cache, int32_t budget);
+nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_table, int32_t out_max_pages,
+                             int32_t budget, int32_t recent, int32_t sinks, int32_t* lens_out, int32_t* keep,
+                             void* workspace, size_t workspace_bytes, nats_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

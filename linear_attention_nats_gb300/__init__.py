@@ -17,7 +17,8 @@ from . import _native
 from ._native import NATS_BF16, NATS_F32, NatsError, check, dims  # noqa: F401
 
 __all__ = ["select", "hybrid_fwd", "hybrid_fwd_x", "nha_fwd", "DecodeState", "decode_step", "workspace_size", "NatsError",
-           "dims", "NATS_BF16", "NATS_F32"]
+           "dims", "NATS_BF16", "NATS_F32", "qk_norm_rope", "qk_norm_rope_bwd", "rope_inv_freq", "PagedCache",
+           "paged_append", "paged_decode", "paged_evict", "paged_workspace_size"]
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -394,3 +395,7 @@ def nha_fwd(q, k, v, log_alpha, *, window: int, scale: float = 0.0, out=None, wo
         check(_native.lib.nats_nha_workspace_check(ctypes.byref(dm), _p(workspace), _stream(stream)),
               "nats_nha_workspace_check")
     return out
+
+
+from .rope import qk_norm_rope, qk_norm_rope_bwd, rope_inv_freq  # noqa: E402
+from .paged import PagedCache, paged_append, paged_decode, paged_evict, paged_workspace_size  # noqa: E402

@@ -32,7 +32,10 @@ EXPORTS = ("nats_status_string", "nats_last_cuda_error", "nats_workspace_size", 
            "nats_bwd_workspace_size", "nats_hybrid_bwd", "nats_hybrid_bwd_profiled", "nats_hybrid_bwd_streams",
            "nats_score_bwd",
            "nats_nha_workspace_size", "nats_nha_fwd",
-           "nats_nha_workspace_check", "nats_nha_fwd_profiled")
+           "nats_nha_workspace_check", "nats_nha_fwd_profiled",
+           "nats_qk_norm_rope", "nats_qk_norm_rope_bwd_workspace_size", "nats_qk_norm_rope_bwd", "nats_paged_append",
+           "nats_paged_decode_workspace_size", "nats_paged_decode", "nats_paged_evict_workspace_size",
+           "nats_paged_evict")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -70,6 +73,21 @@ class NhaDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("L", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("slots", ctypes.c_int32), ("window", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class Strides(ctypes.Structure):
+    """nats_strides: elements between sequences, heads and tokens."""
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "L", "Hq", "Hk", "d", "rot", "interleaved", "norm", "dtype")] + [
+        ("eps", ctypes.c_float)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "weight", "table", "lens", "err")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page", "Hk", "d", "B", "max_pages", "dtype")]
 
 
 def nha_dims(B, H, L, d=128, slots=64, window=512, dtype=NATS_BF16, scale=0.0) -> NhaDims:
@@ -150,6 +168,25 @@ def _load() -> ctypes.CDLL:
     lib.nats_nha_fwd_profiled.argtypes = [ctypes.POINTER(NhaDims)] + [P] * 6 + [ctypes.c_size_t, P,
                                                                                 ctypes.POINTER(Profile)]
     lib.nats_nha_fwd_profiled.restype = ctypes.c_int
+    S, R, C, I32, I64, SZ = (ctypes.POINTER(Strides), ctypes.POINTER(RopeDims), ctypes.POINTER(PagedCache),
+                             ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t)
+    lib.nats_qk_norm_rope.argtypes = [R, P, S, P, S, P, P, P, P, I64, I64, P, S, P, S, P]
+    lib.nats_qk_norm_rope.restype = ctypes.c_int
+    lib.nats_qk_norm_rope_bwd_workspace_size.argtypes = [R]
+    lib.nats_qk_norm_rope_bwd_workspace_size.restype = SZ
+    lib.nats_qk_norm_rope_bwd.argtypes = [R, I32, I32, P, S, P, S, P, S, P, S, P, P, P, P, I64, I64, P, S, P, S, P, P,
+                                          P, SZ, P]
+    lib.nats_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.nats_paged_append.argtypes = [C, R, P, S, P, S, P, S, P, P, P, P, P, P, I64, P, S, P]
+    lib.nats_paged_append.restype = ctypes.c_int
+    lib.nats_paged_decode_workspace_size.argtypes = [C, I32, I32]
+    lib.nats_paged_decode_workspace_size.restype = SZ
+    lib.nats_paged_decode.argtypes = [C, I32, ctypes.c_float, P, I64, I64, P, P, I32, P, SZ, P]
+    lib.nats_paged_decode.restype = ctypes.c_int
+    lib.nats_paged_evict_workspace_size.argtypes = [C, I32]
+    lib.nats_paged_evict_workspace_size.restype = SZ
+    lib.nats_paged_evict.argtypes = [C, P, I32, I32, I32, I32, P, P, P, SZ, P]
+    lib.nats_paged_evict.restype = ctypes.c_int
     return lib
 
 

@@ -80,11 +80,7 @@ thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 // layer forward on this thread replaces by a cudaErrorInvalidValue; -1 none
 thread_local int g_fail_stage = -1;
 
-nats_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return NATS_OK;
-  g_last_cuda_error = e;
-  return NATS_ERR_CUDA;
-}
+nats_status cuda_status(cudaError_t e) { return (nats_status)record_cuda_error(e); }
 
 // Optional per-stage event records around each launch group.
 struct Stages {
@@ -146,6 +142,12 @@ Side* side_of_current_device() {
 }
 
 }  // namespace
+
+int record_cuda_error(cudaError_t e) {
+  if (e == cudaSuccess) return NATS_OK;
+  g_last_cuda_error = e;
+  return NATS_ERR_CUDA;
+}
 
 // Argument checks of the layer forward other than the workspace (shared with
 // the allocation-free entry point, so both report the same error first).

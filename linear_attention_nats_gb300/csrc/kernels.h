@@ -7,6 +7,9 @@ namespace nats {
 
 // dtype: 0 = bf16, 1 = fp32 (nats_dtype).
 
+// The nats_status of a CUDA call; an error is kept for nats_last_cuda_error.
+int record_cuda_error(cudaError_t e);
+
 cudaError_t launch_score(const Problem& p, int dtype, const void* q, const void* k, const float* w_s,
                          const float* b_s, uint8_t* sel, float* scores, cudaStream_t st);
 

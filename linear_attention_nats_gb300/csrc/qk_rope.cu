@@ -1,0 +1,609 @@
+// qk_rope.cu - RMSNorm of each head's query and key row with the rotary
+// position rotation in the same pass (nats_qk_norm_rope), its gradient
+// (nats_qk_norm_rope_bwd), and the same pass with the key and value rows
+// going to the pages of a cache (nats_paged_append).
+//
+//   n = sqrt(mean(x^2) + eps),  z = w x / n,  y = R(p) z
+//   u = R(p)^T dy,  dw = sum u x / n,  dx = (w u - x <w u, x> / (d n^2)) / n
+//
+// Bound by HBM: a row is read once and written once, its d entries held in
+// the registers of d / 8 lanes (8 entries a lane), statistics and rotation in
+// fp32.  A lane's entries are two quads chosen so that both members of each
+// pair are its own and the rotation needs no exchange: quads l and l + rot/8
+// for pairs (i, i + rot/2), quads 2l and 2l + 1 for pairs (2i, 2i + 1); in
+// both, the lane's four pairs are 4l .. 4l + 3.  A warp keeps one token's
+// cosines and sines and walks over the heads with them.
+//
+// Angles.  p f in fp32 is off by 2^-24 of the angle, whole radians at far
+// positions, and fp64 is slow on this chip.  The frequency becomes a 64-bit
+// fixed-point fraction of a turn, F = frac(f / 2 pi) 2^64, and the phase is
+// p F mod 2^64, exact whole turns dropping out of the product by themselves;
+// its upper 32 bits go to sincospif.
+#include <cmath>
+
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace nats {
+namespace {
+
+constexpr int kWarps = 8;  // warps per CTA
+
+// f / (2 pi) in turns times 2^64, modulo 2^64, from the bits of the double f:
+// the 53-bit mantissa times 2^64 / (2 pi) rounded to an integer (62 bits),
+// shifted by the exponent.  Integer work only.  2^64 / (2 pi) =
+// 2935890503282001226.3...
+__device__ __forceinline__ uint64_t turns_fixed(double f) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int e = (int)(bits >> 52) & 0x7ff;
+  if (e == 0 || e == 0x7ff) return 0;  // below 2^-1022: no turn at any position; not a number: none either
+  const uint64_t m = (bits & 0xfffffffffffffull) | (1ull << 52);
+  constexpr uint64_t kInv2Pi = 2935890503282001226ull;
+  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  const int s = 1075 - e;  // f = m 2^-s
+  uint64_t r;
+  if (s <= 0)
+    r = -s >= 64 ? 0 : lo << -s;
+  else if (s < 64)
+    r = (lo >> s) | (hi << (64 - s));
+  else
+    r = s >= 128 ? 0 : hi >> (s - 64);
+  return (bits >> 63) ? 0 - r : r;
+}
+
+struct Operand {
+  const void* p;
+  long long b, h, t;
+};
+
+// Two quads of a row: loads, stores and conversions.
+template <typename T, bool VEC>
+struct Quads;
+template <>
+struct Quads<__nv_bfloat16, true> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* o) {
+    const uint2 u = *(const uint2*)p;
+    o[0] = __uint_as_float(u.x << 16), o[1] = __uint_as_float(u.x & 0xffff0000u);
+    o[2] = __uint_as_float(u.y << 16), o[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* o) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+    uint2 u;
+    u.x = *(const uint32_t*)&a, u.y = *(const uint32_t*)&b;
+    *(uint2*)p = u;
+  }
+};
+template <>
+struct Quads<float, true> {
+  static __device__ __forceinline__ void load(const float* p, float* o) {
+    const float4 u = *(const float4*)p;
+    o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* o) {
+    *(float4*)p = make_float4(o[0], o[1], o[2], o[3]);
+  }
+};
+template <typename T>
+struct Quads<T, false> {
+  static __device__ __forceinline__ void load(const T* p, float* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = to_f32(p[i]);
+  }
+  static __device__ __forceinline__ void store(T* p, const float* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = from_f32<T>(o[i]);
+  }
+};
+
+// What a lane knows of its row: its two quads and its four pairs' turns.
+struct LaneMap {
+  int qa, qb;   // entry offsets of the two quads
+  bool turned;  // whether the lane's entries are rotated at all
+  int pair0;    // its first pair
+};
+template <bool INTER>
+__device__ __forceinline__ LaneMap lane_map(int l, int rot) {
+  LaneMap m;
+  m.turned = 8 * l < rot;
+  m.pair0 = 4 * l;
+  if (INTER || !m.turned) {
+    m.qa = 8 * l;  // the rows' entries from rot on lie in pairs of quads, as the lanes from rot / 8 on do
+    m.qb = 8 * l + 4;
+  } else {
+    m.qa = 4 * l;
+    m.qb = 4 * l + rot / 2;
+  }
+  return m;
+}
+
+// cos and sin of the lane's four pairs at position p (1 and 0 where nothing turns)
+__device__ __forceinline__ void angles(const uint64_t* F, bool turned, long long p, float* c, float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = 1.f, s[i] = 0.f;
+    if (turned) {
+      const uint64_t ph = (uint64_t)p * F[i];
+      sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &s[i], &c[i]);
+    }
+  }
+}
+
+// x[0..3] the lane's first quad, x[4..7] its second
+template <bool INTER>
+__device__ __forceinline__ void turn(float* x, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = INTER ? 2 * i : i, b = INTER ? 2 * i + 1 : i + 4;
+    const float xa = x[a], xb = x[b];
+    x[a] = xa * c[i] - xb * s[i];
+    x[b] = xb * c[i] + xa * s[i];
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+struct RopeArgs {
+  Operand q, k, v;     // v: append only
+  Operand qo, ko;      // outputs (ko: not for append)
+  const float *wq, *wk;
+  const double* inv_freq;
+  const int64_t* pos;
+  long long pos_b, pos0;
+  int B, L, Hq, Hk, rot;
+  int norm;
+  float eps;
+  int rows_per_item, items_per_token;  // a warp's share of a token's rows
+  // append
+  PagedView pg;
+  void *k_pages, *v_pages;
+  float* weight;
+  const int32_t *start, *n_new;
+};
+
+// One warp per item (a token and a run of its rows): q rows, then k rows,
+// then (append) v rows.
+template <typename T, int D, bool INTER, bool PAGED, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(RopeArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % LPR, sub = lane / LPR;
+  const long long item = (long long)blockIdx.x * kWarps + warp;
+  const long long tok = item / a.items_per_token;
+  if (tok >= (long long)a.B * a.L) return;
+  const int b = (int)(tok / a.L), t = (int)(tok % a.L);
+  const int rows = a.Hq + a.Hk + (PAGED ? a.Hk : 0);
+  const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
+  const int r1 = min(rows, r0 + a.rows_per_item);
+  long long p = a.pos0 + t;
+  int pg = -1, slot = 0;
+  if (PAGED) {
+    if (a.n_new && t >= a.n_new[b]) return;
+    const long long at = (long long)(a.start ? a.start[b] : a.pg.lens[b]) + t;
+    p = at;
+    if (at >= 0 && at < a.pg.cap()) {
+      pg = a.pg.page_of(b, (int)at / a.pg.page);
+      slot = (int)at % a.pg.page;
+    }
+    if (pg < 0 && lane == 0 && r0 == 0) *a.pg.err = 1;
+  }
+  if (a.pos) p = a.pos[b * a.pos_b + t];
+  const LaneMap m = lane_map<INTER>(l, a.rot);
+  float c[4], s[4], wq[8], wk[8];
+  {
+    uint64_t F[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(a.inv_freq[m.pair0 + i]) : 0;
+    angles(F, m.turned, p, c, s);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = (i < 4 ? m.qa : m.qb - 4) + i;
+    wq[i] = a.wq ? a.wq[e] : 1.f;
+    wk[i] = a.wk ? a.wk[e] : 1.f;
+  }
+  for (int r = r0; r < r1; r += RPW) {
+    const int row = r + sub;
+    const bool on = row < r1;
+    const bool is_q = row < a.Hq, is_v = PAGED && row >= a.Hq + a.Hk;
+    const int h = is_q ? row : is_v ? row - a.Hq - a.Hk : row - a.Hq;
+    const Operand& in = is_q ? a.q : is_v ? a.v : a.k;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (on) {
+      const T* src = (const T*)in.p + b * in.b + h * in.h + t * in.t;
+      Quads<T, VEC>::load(src + m.qa, x);
+      Quads<T, VEC>::load(src + m.qb, x + 4);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+    ss = row_sum<LPR>(ss);
+    if (!is_v) {
+      if (a.norm) {
+        const float rn = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= rn * (is_q ? wq[i] : wk[i]);
+      }
+      turn<INTER>(x, c, s);
+    }
+    if (!on) continue;
+    T* dst;
+    if (!PAGED || is_q) {
+      const Operand& out = is_q ? a.qo : a.ko;
+      dst = (T*)out.p + b * out.b + h * out.h + t * out.t;
+    } else {
+      if (pg < 0) continue;
+      const long long at = a.pg.row(pg, h, slot);
+      dst = (T*)(is_v ? a.v_pages : a.k_pages) + at * D;
+      if (!is_v && a.weight && l == 0) a.weight[at] = 0.f;
+    }
+    Quads<T, VEC>::store(dst + m.qa, x);
+    Quads<T, VEC>::store(dst + m.qb, x + 4);
+  }
+}
+
+struct RopeBwdArgs {
+  Operand gq, gk, q, k, dq, dk;
+  const float *wq, *wk;
+  const double* inv_freq;
+  const int64_t* pos;
+  long long pos_b, pos0;
+  int B, L, Hq, Hk, rot, norm;
+  float eps;
+  int rows_per_item, items_per_token;
+  float* part;  // [grid, 2, D] or NULL
+};
+
+// The same mapping on a fixed grid whose warps stride over the items and keep
+// their shares of dw_q, dw_k in registers (8 entries of each a lane).
+template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeBwdArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  __shared__ float red[kWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % LPR, sub = lane / LPR;
+  const LaneMap m = lane_map<INTER>(l, a.rot);
+  uint64_t F[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(a.inv_freq[m.pair0 + i]) : 0;
+  float wq[8], wk[8], aq[8], ak[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = (i < 4 ? m.qa : m.qb - 4) + i;
+    wq[i] = a.wq ? a.wq[e] : 1.f;
+    wk[i] = a.wk ? a.wk[e] : 1.f;
+    aq[i] = ak[i] = 0.f;
+  }
+  const int rows = a.Hq + a.Hk;
+  const long long n_items = (long long)a.B * a.L * a.items_per_token;
+  for (long long item = (long long)blockIdx.x * kWarps + warp; item < n_items; item += (long long)gridDim.x * kWarps) {
+    const long long tok = item / a.items_per_token;
+    const int b = (int)(tok / a.L), t = (int)(tok % a.L);
+    const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
+    const int r1 = min(rows, r0 + a.rows_per_item);
+    float c[4], s[4];
+    angles(F, m.turned, a.pos ? a.pos[b * a.pos_b + t] : a.pos0 + t, c, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = -s[i];
+    for (int r = r0; r < r1; r += RPW) {
+      const int row = r + sub;
+      const bool on = row < r1, is_q = row < a.Hq;
+      const int h = is_q ? row : row - a.Hq;
+      float x[8], u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = u[i] = 0.f;
+      if (on) {
+        const Operand& gi = is_q ? a.gq : a.gk;
+        const GI* g = (const GI*)gi.p + b * gi.b + h * gi.h + t * gi.t;
+        Quads<GI, VEC>::load(g + m.qa, u);
+        Quads<GI, VEC>::load(g + m.qb, u + 4);
+        if (a.norm) {
+          const Operand& xi = is_q ? a.q : a.k;
+          const T* src = (const T*)xi.p + b * xi.b + h * xi.h + t * xi.t;
+          Quads<T, VEC>::load(src + m.qa, x);
+          Quads<T, VEC>::load(src + m.qb, x + 4);
+        }
+      }
+      turn<INTER>(u, c, s);
+      if (a.norm) {
+        float ss = 0.f, gx = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss += x[i] * x[i];
+          gx += u[i] * (is_q ? wq[i] : wk[i]) * x[i];
+        }
+        ss = row_sum<LPR>(ss);
+        gx = row_sum<LPR>(gx);
+        const float rn = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+        const float cx = gx * rn * rn * (1.f / D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float ux = u[i] * x[i] * rn;  // zero in rows that are not `on`, unless n is 0 there
+          if (on) (is_q ? aq[i] : ak[i]) += ux;
+          u[i] = rn * (u[i] * (is_q ? wq[i] : wk[i]) - cx * x[i]);
+        }
+      }
+      if (on) {
+        const Operand& o = is_q ? a.dq : a.dk;
+        GO* dst = (GO*)o.p + b * o.b + h * o.h + t * o.t;
+        Quads<GO, VEC>::store(dst + m.qa, u);
+        Quads<GO, VEC>::store(dst + m.qb, u + 4);
+      }
+    }
+  }
+  if (!a.part) return;
+  // the CTA's sums: over the rows of a warp, then over the warps in order
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = which ? ak[i] : aq[i];
+#pragma unroll
+      for (int o = 16; o >= LPR; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (sub == 0) red[warp][(i < 4 ? m.qa : m.qb - 4) + i] = v;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += kWarps * 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += red[w][e];
+      a.part[((long long)blockIdx.x * 2 + which) * D + e] = v;
+    }
+    __syncthreads();
+  }
+}
+
+// dw[e] = sum over the partials, in order: 8 runs of partials per column
+template <int D>
+__global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk) {
+  __shared__ float red[8][32];
+  const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D
+  float v = 0.f;
+  for (int i = threadIdx.y; i < n; i += 8) v += part[(long long)i * 2 * D + col];
+  red[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0) {
+    v = 0.f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) v += red[y][threadIdx.x];
+    float* o = col < D ? dwq : dwk;
+    if (o) o[col % D] = v;
+  }
+}
+
+constexpr int kSMs = 152;
+constexpr int kBwdGrid = kSMs * 3;
+
+// Rows a warp takes of one token: all of them when the tokens alone fill the
+// GPU (64 warps an SM), else split evenly so that short calls spread out.
+void split_rows(long long tokens, int rows, int rpw, int* per_item, int* items) {
+  const long long want = (long long)kSMs * 64;
+  const int most = (rows + rpw - 1) / rpw;
+  long long n = tokens > 0 ? (want + tokens - 1) / tokens : 1;
+  if (n > most) n = most;
+  if (n < 1) n = 1;
+  int per = (most + (int)n - 1) / (int)n * rpw;
+  *per_item = per;
+  *items = (rows + per - 1) / per;
+}
+
+Operand operand(const void* p, const nats_strides* s) {
+  return s ? Operand{p, s->b, s->h, s->t} : Operand{p, 0, 0, 0};
+}
+
+// quads of this operand start at multiples of their size
+bool vec_ok(const Operand& o, int es) {
+  if (!o.p) return true;
+  return ((uintptr_t)o.p % (4 * es)) == 0 && o.b % 4 == 0 && o.h % 4 == 0 && o.t % 4 == 0;
+}
+
+bool elem_ok(const void* p, int es) { return ((uintptr_t)p % es) == 0; }
+
+nats_status check_rope(const nats_rope_dims* d) {
+  if (!d) return NATS_ERR_NULL;
+  if (d->dtype != NATS_BF16 && d->dtype != NATS_F32) return NATS_ERR_DTYPE;
+  if (d->B < 0 || d->L < 0 || d->Hq < 0 || d->Hk < 0) return NATS_ERR_SHAPE;
+  if (d->d != 64 && d->d != 128) return NATS_ERR_UNSUPPORTED;
+  if (d->rot < 0 || d->rot > d->d || d->rot % 8 != 0) return NATS_ERR_SHAPE;
+  if (d->norm && (!std::isfinite(d->eps) || d->eps < 0.f)) return NATS_ERR_VALUE;
+  if ((long long)d->Hq + 2LL * d->Hk > (1LL << 30)) return NATS_ERR_UNSUPPORTED;
+  const double rows = (double)d->B * d->L * ((double)d->Hq + 2.0 * d->Hk);
+  if (rows > 1099511627776.0 || (double)d->B * d->L > 4294967296.0) return NATS_ERR_UNSUPPORTED;
+  return NATS_OK;
+}
+
+template <bool PAGED>
+cudaError_t launch_fwd(RopeArgs& a, int dtype, int d, bool inter, bool vec, cudaStream_t st) {
+  const long long tokens = (long long)a.B * a.L;
+  const int rows = a.Hq + a.Hk * (PAGED ? 2 : 1);
+  split_rows(tokens, rows, 32 / (d / 8), &a.rows_per_item, &a.items_per_token);
+  const long long items = tokens * a.items_per_token;
+  const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
+#define NATS_ROPE(T, D, I, V) rope_fwd_kernel<T, D, I, PAGED, V><<<grid, kWarps * 32, 0, st>>>(a)
+#define NATS_ROPE_V(T, D, I) (vec ? NATS_ROPE(T, D, I, true) : NATS_ROPE(T, D, I, false))
+#define NATS_ROPE_I(T, D) (inter ? NATS_ROPE_V(T, D, true) : NATS_ROPE_V(T, D, false))
+  if (dtype == NATS_BF16)
+    d == 128 ? NATS_ROPE_I(__nv_bfloat16, 128) : NATS_ROPE_I(__nv_bfloat16, 64);
+  else
+    d == 128 ? NATS_ROPE_I(float, 128) : NATS_ROPE_I(float, 64);
+  return cudaGetLastError();
+}
+
+template <typename T, typename GI, typename GO>
+void launch_bwd(const RopeBwdArgs& a, int d, bool inter, bool vec, unsigned grid, cudaStream_t st) {
+#define NATS_BWD(D, I, V) rope_bwd_kernel<T, GI, GO, D, I, V><<<grid, kWarps * 32, 0, st>>>(a)
+#define NATS_BWD_V(D, I) (vec ? NATS_BWD(D, I, true) : NATS_BWD(D, I, false))
+#define NATS_BWD_I(D) (inter ? NATS_BWD_V(D, true) : NATS_BWD_V(D, false))
+  d == 128 ? NATS_BWD_I(128) : NATS_BWD_I(64);
+}
+
+}  // namespace
+}  // namespace nats
+
+using namespace nats;
+
+extern "C" {
+
+nats_status nats_qk_norm_rope(const nats_rope_dims* dims, const void* q, const nats_strides* q_st, const void* k,
+                              const nats_strides* k_st, const float* w_q, const float* w_k, const double* inv_freq,
+                              const int64_t* pos, int64_t pos_stride_b, int64_t pos0, void* q_out,
+                              const nats_strides* q_out_st, void* k_out, const nats_strides* k_out_st,
+                              nats_stream_t stream) {
+  const nats_status s = check_rope(dims);
+  if (s != NATS_OK) return s;
+  if (dims->B == 0 || dims->L == 0 || dims->Hq + dims->Hk == 0) return NATS_OK;
+  if (dims->Hq > 0 && (!q || !q_st || !q_out || !q_out_st)) return NATS_ERR_NULL;
+  if (dims->Hk > 0 && (!k || !k_st || !k_out || !k_out_st)) return NATS_ERR_NULL;
+  if (dims->rot > 0 && !inv_freq) return NATS_ERR_NULL;
+  const int es = dims->dtype == NATS_BF16 ? 2 : 4;
+  RopeArgs a = {};
+  if (dims->Hq > 0) a.q = operand(q, q_st), a.qo = operand(q_out, q_out_st);
+  if (dims->Hk > 0) a.k = operand(k, k_st), a.ko = operand(k_out, k_out_st);
+  const Operand* ops[] = {&a.q, &a.k, &a.qo, &a.ko};
+  bool vec = true;
+  for (const Operand* o : ops) {
+    if (!elem_ok(o->p, es)) return NATS_ERR_ALIGN;
+    vec = vec && vec_ok(*o, es);
+  }
+  if (!elem_ok(w_q, 4) || !elem_ok(w_k, 4) || !elem_ok(inv_freq, 8) || !elem_ok(pos, 8)) return NATS_ERR_ALIGN;
+  a.wq = dims->norm ? w_q : nullptr, a.wk = dims->norm ? w_k : nullptr;
+  a.inv_freq = inv_freq, a.pos = pos, a.pos_b = pos_stride_b, a.pos0 = pos0;
+  a.B = dims->B, a.L = dims->L, a.Hq = dims->Hq, a.Hk = dims->Hk, a.rot = dims->rot;
+  a.norm = dims->norm, a.eps = dims->eps;
+  return (nats_status)record_cuda_error(
+      launch_fwd<false>(a, dims->dtype, dims->d, dims->interleaved != 0, vec, (cudaStream_t)stream));
+}
+
+nats_status nats_paged_append(const nats_paged_cache* cache, const nats_rope_dims* dims, const void* q,
+                              const nats_strides* q_st, const void* k, const nats_strides* k_st, const void* v,
+                              const nats_strides* v_st, const float* w_q, const float* w_k, const double* inv_freq,
+                              const int32_t* start, const int32_t* n_new, const int64_t* pos, int64_t pos_stride_b,
+                              void* q_out, const nats_strides* q_out_st, nats_stream_t stream) {
+  nats_status s = check_cache(cache);
+  if (s != NATS_OK) return s;
+  s = check_rope(dims);
+  if (s != NATS_OK) return s;
+  if (dims->B != cache->B || dims->Hk != cache->Hk || dims->d != cache->d) return NATS_ERR_SHAPE;
+  if (dims->dtype != cache->dtype) return NATS_ERR_DTYPE;
+  if (dims->B == 0 || dims->L == 0) return NATS_OK;
+  s = check_cache_pointers(cache);
+  if (s != NATS_OK) return s;
+  if (!k || !k_st || !v || !v_st) return NATS_ERR_NULL;
+  if (dims->Hq > 0 && (!q || !q_st || !q_out || !q_out_st)) return NATS_ERR_NULL;
+  if (dims->rot > 0 && !inv_freq) return NATS_ERR_NULL;
+  const int es = dims->dtype == NATS_BF16 ? 2 : 4;
+  RopeArgs a = {};
+  if (dims->Hq > 0) a.q = operand(q, q_st), a.qo = operand(q_out, q_out_st);
+  a.k = operand(k, k_st), a.v = operand(v, v_st);
+  const Operand* ops[] = {&a.q, &a.k, &a.v, &a.qo};
+  bool vec = true;
+  for (const Operand* o : ops) {
+    if (!elem_ok(o->p, es)) return NATS_ERR_ALIGN;
+    vec = vec && vec_ok(*o, es);
+  }
+  if (!elem_ok(w_q, 4) || !elem_ok(w_k, 4) || !elem_ok(inv_freq, 8) || !elem_ok(pos, 8) || !elem_ok(start, 4) ||
+      !elem_ok(n_new, 4))
+    return NATS_ERR_ALIGN;
+  a.wq = dims->norm ? w_q : nullptr, a.wk = dims->norm ? w_k : nullptr;
+  a.inv_freq = inv_freq, a.pos = pos, a.pos_b = pos_stride_b, a.pos0 = 0;
+  a.B = dims->B, a.L = dims->L, a.Hq = dims->Hq, a.Hk = dims->Hk, a.rot = dims->rot;
+  a.norm = dims->norm, a.eps = dims->eps;
+  a.pg = view_of(cache), a.k_pages = cache->k_pages, a.v_pages = cache->v_pages, a.weight = cache->weight;
+  a.start = start, a.n_new = n_new;
+  return (nats_status)record_cuda_error(
+      launch_fwd<true>(a, dims->dtype, dims->d, dims->interleaved != 0, vec, (cudaStream_t)stream));
+}
+
+size_t nats_qk_norm_rope_bwd_workspace_size(const nats_rope_dims* dims) {
+  if (check_rope(dims) != NATS_OK) return 0;
+  return sizeof(float) * kBwdGrid * 2 * dims->d;
+}
+
+nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype, int32_t dx_dtype,
+                                  const void* dq_out, const nats_strides* dq_out_st, const void* dk_out,
+                                  const nats_strides* dk_out_st, const void* q, const nats_strides* q_st,
+                                  const void* k, const nats_strides* k_st, const float* w_q, const float* w_k,
+                                  const double* inv_freq, const int64_t* pos, int64_t pos_stride_b, int64_t pos0,
+                                  void* dq, const nats_strides* dq_st, void* dk, const nats_strides* dk_st,
+                                  float* dw_q, float* dw_k, void* workspace, size_t workspace_bytes,
+                                  nats_stream_t stream) {
+  const nats_status s = check_rope(dims);
+  if (s != NATS_OK) return s;
+  if ((grad_dtype != NATS_BF16 && grad_dtype != NATS_F32) || (dx_dtype != NATS_BF16 && dx_dtype != NATS_F32))
+    return NATS_ERR_DTYPE;
+  if (dims->dtype == NATS_F32 && (grad_dtype != NATS_F32 || dx_dtype != NATS_F32)) return NATS_ERR_DTYPE;
+  if (!dims->norm && (dw_q || dw_k)) return NATS_ERR_VALUE;
+  const bool empty = dims->B == 0 || dims->L == 0 || dims->Hq + dims->Hk == 0;
+  if (!empty) {
+    if (dims->Hq > 0 && (!dq_out || !dq_out_st || !dq || !dq_st || (dims->norm && (!q || !q_st)))) return NATS_ERR_NULL;
+    if (dims->Hk > 0 && (!dk_out || !dk_out_st || !dk || !dk_st || (dims->norm && (!k || !k_st)))) return NATS_ERR_NULL;
+    if (dims->rot > 0 && !inv_freq) return NATS_ERR_NULL;
+  }
+  const int es = dims->dtype == NATS_BF16 ? 2 : 4, eg = grad_dtype == NATS_BF16 ? 2 : 4,
+            eo = dx_dtype == NATS_BF16 ? 2 : 4;
+  RopeBwdArgs a = {};
+  if (dims->Hq > 0) a.gq = operand(dq_out, dq_out_st), a.q = operand(q, q_st), a.dq = operand(dq, dq_st);
+  if (dims->Hk > 0) a.gk = operand(dk_out, dk_out_st), a.k = operand(k, k_st), a.dk = operand(dk, dk_st);
+  const Operand* ops[] = {&a.gq, &a.gk, &a.q, &a.k, &a.dq, &a.dk};
+  const int sizes[] = {eg, eg, es, es, eo, eo};
+  bool vec = true;
+  for (int i = 0; i < 6; ++i) {
+    if (!elem_ok(ops[i]->p, sizes[i])) return NATS_ERR_ALIGN;
+    vec = vec && vec_ok(*ops[i], sizes[i]);
+  }
+  if (!elem_ok(w_q, 4) || !elem_ok(w_k, 4) || !elem_ok(dw_q, 4) || !elem_ok(dw_k, 4) || !elem_ok(inv_freq, 8) ||
+      !elem_ok(pos, 8))
+    return NATS_ERR_ALIGN;
+  const bool dw = dw_q || dw_k;
+  if (dw && !empty) {
+    if (!workspace) return NATS_ERR_NULL;
+    if ((uintptr_t)workspace & 15u) return NATS_ERR_ALIGN;
+    if (workspace_bytes < nats_qk_norm_rope_bwd_workspace_size(dims)) return NATS_ERR_WORKSPACE;
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  if (empty) {
+    for (float* o : {dw_q, dw_k})
+      if (o) {
+        const int r = record_cuda_error(cudaMemsetAsync(o, 0, sizeof(float) * dims->d, st));
+        if (r != NATS_OK) return (nats_status)r;
+      }
+    return NATS_OK;
+  }
+  a.wq = dims->norm ? w_q : nullptr, a.wk = dims->norm ? w_k : nullptr;
+  a.inv_freq = inv_freq, a.pos = pos, a.pos_b = pos_stride_b, a.pos0 = pos0;
+  a.B = dims->B, a.L = dims->L, a.Hq = dims->Hq, a.Hk = dims->Hk, a.rot = dims->rot;
+  a.norm = dims->norm, a.eps = dims->eps;
+  a.part = dw ? (float*)workspace : nullptr;
+  const long long tokens = (long long)a.B * a.L;
+  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), &a.rows_per_item, &a.items_per_token);
+  const long long ctas = (tokens * a.items_per_token + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)(ctas < kBwdGrid ? ctas : kBwdGrid);
+  const bool inter = dims->interleaved != 0;
+  const int d = dims->d;
+  if (dims->dtype == NATS_F32)
+    launch_bwd<float, float, float>(a, d, inter, vec, grid, st);
+  else if (grad_dtype == NATS_F32 && dx_dtype == NATS_F32)
+    launch_bwd<__nv_bfloat16, float, float>(a, d, inter, vec, grid, st);
+  else if (grad_dtype == NATS_F32)
+    launch_bwd<__nv_bfloat16, float, __nv_bfloat16>(a, d, inter, vec, grid, st);
+  else if (dx_dtype == NATS_F32)
+    launch_bwd<__nv_bfloat16, __nv_bfloat16, float>(a, d, inter, vec, grid, st);
+  else
+    launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, grid, st);
+  int r = record_cuda_error(cudaGetLastError());
+  if (r != NATS_OK || !dw) return (nats_status)r;
+  const dim3 bd(32, 8);
+  if (d == 128)
+    rope_dw_kernel<128><<<8, bd, 0, st>>>(a.part, (int)grid, dw_q, dw_k);
+  else
+    rope_dw_kernel<64><<<4, bd, 0, st>>>(a.part, (int)grid, dw_q, dw_k);
+  return (nats_status)record_cuda_error(cudaGetLastError());
+}
+
+}  // extern "C"

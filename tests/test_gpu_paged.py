@@ -1,0 +1,540 @@
+"""The paged key / value cache - append, attention of one new token, eviction
+- against plain 64-bit forms."""
+
+import math
+
+import pytest
+import torch
+
+import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def nats():
+    from linear_attention_nats_gb300 import build
+
+    build.build()
+    import linear_attention_nats_gb300 as n
+
+    return n
+
+
+def _pool(rng, n_pages, Hk, page, d, dtype, garbage=True):
+    """Pages whose unused rows hold NaN and infinities (the caller fills the used ones)."""
+    k = torch.full((n_pages, Hk, page, d), math.nan if garbage else 0.0).to(dtype)
+    v = torch.full((n_pages, Hk, page, d), math.inf if garbage else 0.0).to(dtype)
+    return k, v
+
+
+def _filled(rng, lens, page, Hk, d, dtype, extra=0):
+    table, spare, n_pages = ref.assign(lens, page, rng, extra)
+    k, v = _pool(rng, n_pages, Hk, page, d, dtype)
+    for b, n in enumerate(lens):
+        j = torch.arange(int(n))
+        at = table[b].long()[j // page]
+        k[at, :, j % page] = torch.randn(int(n), Hk, d, generator=rng).to(dtype)
+        v[at, :, j % page] = torch.randn(int(n), Hk, d, generator=rng).to(dtype)
+    return table, spare, k, v
+
+
+def _cache(nats, table, lens, k, v, weight=None):
+    return nats.PagedCache(k.cuda(), v.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                           weight=None if weight is None else weight.cuda())
+
+
+# ------------------------------------------------------------------ decode
+
+DECODE = [
+    # lens, Hk, G, d, page, dtype
+    ([1], 1, 1, 64, 16, BF),
+    ([0], 2, 3, 128, 16, F32),
+    ([517], 16, 1, 128, 64, BF),
+    ([64, 63, 65, 0, 1], 2, 4, 128, 64, BF),
+    ([100, 0, 257, 16, 15, 17], 3, 2, 64, 48, F32),
+    ([300, 7], 1, 5, 128, 32, BF),
+    ([129, 2048], 2, 8, 64, 128, BF),
+    ([700, 31, 0, 0, 400], 2, 12, 128, 16, BF),
+    ([333, 95], 1, 16, 128, 64, BF),
+    ([210], 1, 24, 64, 16, F32),
+    ([9000, 3], 2, 3, 128, 16, F32),
+    ([20000], 1, 7, 128, 64, BF),
+    ([3] * 150 + [200] + [0] * 40, 1, 2, 64, 16, BF),
+]
+
+
+@pytest.mark.parametrize("lens,Hk,G,d,page,dtype", DECODE)
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_decode(nats, lens, Hk, G, d, page, dtype, accumulate):
+    rng = torch.Generator().manual_seed(len(lens) * 100 + G)
+    table, _, k, v = _filled(rng, lens, page, Hk, d, dtype)
+    B, Hq = len(lens), Hk * G
+    q = (2 * torch.randn(B, Hq, d, generator=rng)).to(dtype)
+    w0 = torch.rand(k.shape[:3], generator=rng)
+    c = _cache(nats, table, lens, k, v, w0 if accumulate else None)
+    out, lse = nats.paged_decode(c, q.cuda(), accumulate=accumulate, return_lse=True)
+    e, elog, ps, err, perr = ref.decode(q, k, v, table, lens)
+    diff = (out.cpu().double() - e).abs()
+    assert (diff <= ref.HALF[dtype] * (e.abs() + err) + err).all()
+    empty = torch.isinf(elog)
+    assert torch.equal(torch.isinf(lse.cpu()), empty) and (lse.cpu()[empty] < 0).all()
+    # log2 of a sum of factors each off by the p's own relative bound, then rounded
+    fin = ~empty
+    assert ((lse.cpu().double() - elog)[fin].abs() <= 2.0 ** -22 * elog[fin].abs() + (d + 8) * 2.0 ** -20 + 1e-5).all()
+    c.check()
+    if accumulate:
+        want, tol = w0.double(), torch.zeros(w0.shape, dtype=torch.float64)
+        for b, n in enumerate(lens):
+            j = torch.arange(n)
+            at = table[b].long()[j // page]
+            want[at, :, j % page] += ps[b].sum(1).T
+            tol[at, :, j % page] += perr[b].sum(1).T
+        got = c.weight.cpu().double()
+        assert ((got - want).abs() <= tol + ref.U * (want.abs() * 2 + G)).all()
+        assert torch.equal(got[tol == 0], want[tol == 0])
+
+
+def test_decode_strided_query_scale_and_out(nats):
+    rng = torch.Generator().manual_seed(1)
+    lens = [70, 5, 130]
+    table, _, k, v = _filled(rng, lens, 16, 2, 64, BF)
+    wide = torch.randn(3, 6, 3, 64, generator=rng).to(BF).cuda()
+    q = wide[:, :, 1]
+    c = _cache(nats, table, lens, k, v)
+    out = torch.full((3, 6, 64), 5.0, dtype=BF, device="cuda")
+    assert nats.paged_decode(c, q, scale=0.05, out=out) is out
+    e, _, _, err, _ = ref.decode(q.cpu(), k, v, table, lens, scale=0.05)
+    assert ((out.cpu().double() - e).abs() <= 2.0 ** -8 * (e.abs() + err) + err).all()
+
+
+def test_decode_repeats_bit_for_bit_and_shares_pages(nats):
+    """Two sequences over the same pages get the same bits, whatever their place in the line of tiles."""
+    rng = torch.Generator().manual_seed(2)
+    table, _, k, v = _filled(rng, [1000], 64, 2, 128, BF)
+    q = torch.randn(1, 8, 128, generator=rng).to(BF)
+    c = _cache(nats, table.repeat(2, 1), [1000, 1000], k, v)
+    a = nats.paged_decode(c, q.repeat(2, 1, 1).cuda())
+    b = nats.paged_decode(c, q.repeat(2, 1, 1).cuda())
+    assert torch.equal(a, b)
+    e, _, _, err, _ = ref.decode(q, k, v, table, [1000])
+    assert ((a.cpu().double() - e).abs() <= 2.0 ** -8 * (e.abs() + err) + err).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_leaves_out_bad_pages_and_reports_them(nats, dtype):
+    rng = torch.Generator().manual_seed(3)
+    lens, page = [100, 80], 16
+    table, _, k, v = _filled(rng, lens, page, 2, 64, dtype)
+    bad = table.clone()
+    bad[0, 2], bad[1, 0] = k.shape[0], -7  # slots 32..47 of sequence 0, 0..15 of sequence 1
+    skip = [(0, j) for j in range(32, 48)] + [(1, j) for j in range(16)]
+    w0 = torch.rand(k.shape[:3], generator=rng)
+    c = _cache(nats, bad, lens, k, v, w0)
+    q = torch.randn(2, 8, 64, generator=rng).to(dtype)
+    out = nats.paged_decode(c, q.cuda(), accumulate=True)
+    e, _, _, err, _ = ref.decode(q, k, v, table, lens, skip=skip)
+    assert ((out.cpu().double() - e).abs() <= ref.HALF[dtype] * (e.abs() + err) + err).all()
+    with pytest.raises(nats.NatsError):
+        c.check()
+    skipped = torch.stack([table[0, 2], table[1, 0]]).long()
+    assert torch.equal(c.weight.cpu()[skipped], w0[skipped])
+
+
+def test_decode_lengths_out_of_range(nats):
+    rng = torch.Generator().manual_seed(4)
+    table, _, k, v = _filled(rng, [64, 64], 16, 1, 64, BF)
+    q = torch.randn(2, 4, 64, generator=rng).to(BF)
+    c = _cache(nats, table, [1000, -3], k, v)  # taken as 64 and 0
+    out = nats.paged_decode(c, q.cuda())
+    e, _, _, err, _ = ref.decode(q, k, v, table, [64, 0])
+    assert ((out.cpu().double() - e).abs() <= 2.0 ** -8 * (e.abs() + err) + err).all()
+    with pytest.raises(nats.NatsError):
+        c.check()
+
+
+def test_decode_values_that_are_not_finite(nats):
+    """Such values in slots behind a sequence do not matter (every other test has them there); in a used slot of one
+    key head they reach that head's queries alone."""
+    rng = torch.Generator().manual_seed(5)
+    table, _, k, v = _filled(rng, [50], 16, 2, 64, BF)
+    v[table[0, 1].long(), 0, 3, 7] = math.nan
+    c = _cache(nats, table, [50], k, v)
+    out = nats.paged_decode(c, torch.randn(1, 4, 64, generator=rng).to(BF).cuda())
+    bad = torch.isnan(out.cpu())
+    assert bad[0, :2, 7].all() and bad.sum() == 2
+
+
+def test_decode_peaked_scores(nats):
+    """One slot that takes nearly everything, and scores far below it."""
+    rng = torch.Generator().manual_seed(6)
+    for dtype in (BF, F32):
+        table, _, k, v = _filled(rng, [400], 16, 1, 128, dtype)
+        q = torch.randn(1, 4, 128, generator=rng).to(dtype)
+        k[table[0, 11].long(), 0, 5] = 20 * q[0, 0]
+        c = _cache(nats, table, [400], k, v)
+        out = nats.paged_decode(c, q.cuda())
+        e, _, _, err, _ = ref.decode(q, k, v, table, [400])
+        assert ((out.cpu().double() - e).abs() <= ref.HALF[dtype] * (e.abs() + err) + err).all()
+
+
+def test_decode_beyond_32_bit_offsets(nats):
+    """A pool of more than 2^31 entries: its last pages hold the sequence."""
+    Hk, page, d = 8, 128, 128
+    n_pages = (1 << 31) // (Hk * page * d) + 40
+    rng = torch.Generator().manual_seed(7)
+    k = torch.empty((n_pages, Hk, page, d), dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    w = torch.empty((n_pages, Hk, page), device="cuda")
+    table = torch.arange(n_pages - 1, n_pages - 25, -1, dtype=torch.int32)[None]
+    lens = [24 * page - 5]
+    kk, vv = torch.randn(24, Hk, page, d, generator=rng).to(BF), torch.randn(24, Hk, page, d, generator=rng).to(BF)
+    k[-24:], v[-24:], w[-24:] = kk.cuda(), vv.cuda(), 0
+    c = nats.PagedCache(k, v, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), weight=w)
+    q = torch.randn(1, 16, d, generator=rng).to(BF)
+    out = nats.paged_decode(c, q.cuda(), accumulate=True)
+    small = (table - (n_pages - 24)).int()
+    e, _, ps, err, perr = ref.decode(q, kk, vv, small, lens)
+    assert ((out.cpu().double() - e).abs() <= 2.0 ** -8 * (e.abs() + err) + err).all()
+    assert abs(float(w[-24:].double().sum()) - 16) < 1e-3
+    # eviction within it: from the last pages to the ones before them
+    outt = torch.arange(n_pages - 40, n_pages - 32, dtype=torch.int32)[None].cuda()
+    keep, n = nats.paged_evict(c, outt, 8 * page, recent=17, sinks=4, return_keep=True)
+    want = ref.evict(w[-24:].cpu(), small, lens, page, 8 * page, 17, 4)
+    assert torch.equal(keep.cpu(), want)
+    i = torch.arange(8 * page)
+    for h in range(Hk):
+        src = want[0, h].long()
+        assert torch.equal(k[n_pages - 40:n_pages - 32, h].reshape(-1, d).cpu(), kk[small[0].long()[src // page], h, src % page])
+        assert torch.equal(v[n_pages - 40:n_pages - 32, h].reshape(-1, d).cpu(), vv[small[0].long()[src // page], h, src % page])
+
+
+def test_decode_on_another_stream_and_captured(nats):
+    rng = torch.Generator().manual_seed(8)
+    lens = [300, 40, 0, 1000]
+    table, _, k, v = _filled(rng, lens, 16, 2, 64, BF)
+    c = _cache(nats, table, lens, k, v, torch.zeros(k.shape[:3]))
+    q = torch.randn(4, 6, 64, generator=rng).to(BF).cuda()
+    want = nats.paged_decode(c, q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = nats.paged_decode(c, q, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = nats.paged_decode(c, q, accumulate=True)
+    q.copy_(torch.randn(4, 6, 64, generator=rng).to(BF))
+    c.lens.copy_(torch.tensor([17, 640, 3, 900], dtype=torch.int32).clamp(max=c.max_pages * 16))
+    lens2 = [17, 40, 0, 900]  # pages only hold these; the rest of the table is -1
+    c.lens.copy_(torch.tensor(lens2, dtype=torch.int32))
+    c.weight.zero_()
+    g.replay()
+    e, _, _, err, _ = ref.decode(q.cpu(), k, v, table, lens2)
+    assert ((out.cpu().double() - e).abs() <= 2.0 ** -8 * (e.abs() + err) + err).all()
+    assert torch.equal(out, nats.paged_decode(c, q))
+    # every sequence's weights sum to its query heads
+    assert abs(float(c.weight.double().sum()) - 3 * 6) < 1e-4
+
+
+# ------------------------------------------------------------------ append
+
+APPEND = [
+    # T, n_new, start, Hq, Hk, d, page, dtype, norm, rot, interleaved
+    (1, None, [5, 0, 31], 4, 2, 64, 16, BF, True, 64, False),
+    (40, [40, 0, 13], [0, 9, 20], 6, 2, 128, 16, BF, True, 128, False),
+    (33, [33, 1, 32], [15, 16, 17], 3, 3, 64, 48, F32, True, 32, True),
+    (7, None, [3, 60, 64], 0, 1, 128, 64, BF, True, 112, False),
+    (21, [5, 21, 0], None, 2, 1, 64, 32, F32, False, 64, False),
+    (130, [100, 130, 64], [1, 2, 3], 4, 4, 128, 128, BF, False, 0, False),
+]
+
+
+@pytest.mark.parametrize("T,n_new,start,Hq,Hk,d,page,dtype,norm,rot,inter", APPEND)
+def test_append(nats, T, n_new, start, Hq, Hk, d, page, dtype, norm, rot, inter):
+    B = 3
+    rng = torch.Generator().manual_seed(T)
+    lens = [11, 0, 30]
+    first = lens if start is None else start
+    table, _, n_pages = ref.assign([p + T for p in first], page, rng, 2)
+    k0 = torch.randn(n_pages, Hk, page, d, generator=rng).to(dtype)
+    v0 = torch.randn(n_pages, Hk, page, d, generator=rng).to(dtype)
+    w0 = torch.rand(n_pages, Hk, page, generator=rng)
+    qkv = torch.randn(B, T, (Hq + 2 * Hk) * d, generator=rng).to(dtype)
+    split = lambda t: [t[..., a * d:b * d].unflatten(-1, (b - a, d)).transpose(1, 2)
+                       for a, b in ((0, Hq), (Hq, Hq + Hk), (Hq + Hk, Hq + 2 * Hk))]
+    q, k, v = split(qkv)
+    gq, gk, gv = split(qkv.cuda())
+    wq, wk = 1 + 0.3 * torch.randn(d, generator=rng), 1 + 0.3 * torch.randn(d, generator=rng)
+    f = torch.tensor([1e6 ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64) if rot else None
+    c = _cache(nats, table, lens, k0, v0, w0)
+    out_q = torch.full((B, Hq, T, d), 9.0, dtype=dtype, device="cuda") if Hq else None
+    dev = lambda x, dt=torch.int32: None if x is None else torch.tensor(x, dtype=dt).cuda()
+    r = nats.paged_append(c, gk, gv, start=dev(start), n_new=dev(n_new), q=gq if Hq else None, out_q=out_q, norm=norm,
+                          w_q=wq.cuda(), w_k=wk.cuda(), inv_freq=None if f is None else f.cuda(), interleaved=inter)
+    assert r is out_q
+    c.check()
+    counts = [T] * B if n_new is None else n_new
+    pos = torch.tensor(first)[:, None] + torch.arange(T)
+    kr, kz = ref.norm_rotate(k, wk, pos, f, inter, norm, 1e-6), ref.norm_rotate(k, wk, pos, None, inter, norm, 1e-6)
+    kb = ref.rope_bound(kr, kz, rot, inter, dtype)
+    gotk, gotv, gotw = c.k_pages.cpu(), c.v_pages.cpu(), c.weight.cpu()
+    untouched = torch.ones(n_pages, page, dtype=torch.bool)
+    for b in range(B):
+        j = first[b] + torch.arange(counts[b])
+        at, sl = table[b].long()[j // page], j % page
+        untouched[at, sl] = False
+        n = counts[b]
+        assert ((gotk[at, :, sl].transpose(0, 1).double() - kr[b, :, :n]).abs() <= kb[b, :, :n]).all()
+        assert torch.equal(gotv[at, :, sl].transpose(0, 1), v[b, :, :n])
+        assert (gotw[at, :, sl] == 0).all()
+    for got, was in ((gotk, k0), (gotv, v0), (gotw, w0)):
+        assert torch.equal(got.transpose(1, 2)[untouched], was.transpose(1, 2)[untouched])
+    if Hq:
+        qr, qz = ref.norm_rotate(q, wq, pos, f, inter, norm, 1e-6), ref.norm_rotate(q, wq, pos, None, inter, norm, 1e-6)
+        qb = ref.rope_bound(qr, qz, rot, inter, dtype)
+        for b in range(B):
+            n = counts[b]
+            assert ((out_q[b, :, :n].cpu().double() - qr[b, :, :n]).abs() <= qb[b, :, :n]).all()
+            assert (out_q[b, :, n:] == 9).all()
+
+
+def test_append_given_positions_and_new_query(nats):
+    rng = torch.Generator().manual_seed(9)
+    c = nats.PagedCache.empty(4, 16, 1, 64, 2, 2, dtype=F32)
+    c.table.copy_(torch.tensor([[3, 1], [0, 2]], dtype=torch.int32))
+    x = torch.randn(2, 1, 5, 64, generator=rng).cuda()
+    pos = torch.tensor([[7, 900, 3, 2, 1], [5, 5, 5, 5, 5]]).cuda()
+    f = nats.rope_inv_freq(64)
+    oq = nats.paged_append(c, x, x, q=x, norm=True, inv_freq=f, positions=pos,
+                           n_new=torch.tensor([5, 2], dtype=torch.int32).cuda())
+    want, _ = nats.qk_norm_rope(x, x, None, None, f, pos)
+    assert torch.equal(oq[0], want[0]) and torch.equal(oq[1, :, :2], want[1, :, :2]) and (oq[1, :, 2:] == 0).all()
+    assert torch.equal(c.k_pages[3, 0, :5], want[0, 0]) and torch.equal(c.k_pages[0, 0, :2], want[1, 0, :2])
+    assert (c.k_pages[0, 0, 2:] == 0).all() and (c.lens == 0).all()
+
+
+def test_append_outside_the_table_or_pool(nats):
+    """Tokens behind the table, before slot 0 or on a page that is not the pool's are left out and reported; the
+    others, and the queries, are written."""
+    c = nats.PagedCache.empty(3, 16, 2, 64, 3, 2, dtype=BF)
+    c.table.copy_(torch.tensor([[1, -1], [0, 2], [99, 0]], dtype=torch.int32))
+    x = torch.ones(3, 2, 4, 64, dtype=BF, device="cuda")
+    start = torch.tensor([14, 30, -2], dtype=torch.int32).cuda()
+    oq = nats.paged_append(c, x, 2 * x, start=start, q=x)
+    assert (oq == 1).all()
+    k = c.k_pages[:, 0, :, 0].cpu()
+    want = torch.zeros(3, 16)
+    want[1, 14:] = 1  # sequence 0: slots 14, 15; 16, 17 have no page
+    want[2, 14:] = 1  # sequence 1: slots 30, 31; 32, 33 lie behind the table
+    assert torch.equal(k.float(), want) and torch.equal(c.v_pages[:, 1, :, 3].cpu().float(), 2 * want)
+    with pytest.raises(nats.NatsError):
+        c.check()
+
+
+def test_append_captured_follows_the_lengths(nats):
+    c = nats.PagedCache.empty(4, 16, 1, 64, 1, 4, dtype=BF)
+    c.table.copy_(torch.arange(4, dtype=torch.int32)[None])
+    x = torch.zeros(1, 1, 1, 64, dtype=BF, device="cuda")
+    nats.paged_append(c, x, x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nats.paged_append(c, x, x)
+        c.lens.add_(1)
+    for i in range(40):
+        x.fill_(i + 1)
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c.k_pages[:, 0, :, 0].reshape(-1).cpu().float(),
+                       torch.cat([torch.arange(1, 41), torch.zeros(24, dtype=torch.int64)]).float())
+    assert int(c.lens) == 40
+
+
+# ------------------------------------------------------------------- evict
+
+EVICT = [
+    # lens, Hk, d, page, dtype, budget, recent, sinks, weights
+    ([100], 1, 64, 16, BF, 40, 0, 0, "spread"),
+    ([100, 39, 40, 41, 0, 1], 2, 64, 16, F32, 40, 10, 2, "spread"),
+    ([2112, 1500], 3, 128, 64, BF, 1000, 256, 4, "spread"),
+    ([500, 300], 2, 128, 48, BF, 128, 0, 4, "ties"),
+    ([500], 2, 64, 32, F32, 65, 64, 1, "ties"),
+    ([500], 1, 64, 16, BF, 33, 20, 13, "spread"),
+    ([300, 200], 2, 64, 128, BF, 100, 3, 1, "odd"),
+    ([5000], 1, 64, 16, F32, 4097, 1, 0, "equal"),
+    ([30000, 1025], 1, 64, 64, BF, 1025, 100, 4, "spread"),
+    ([64, 10], 1, 64, 16, BF, 0, 0, 0, "spread"),
+]
+
+
+@pytest.mark.parametrize("lens,Hk,d,page,dtype,budget,recent,sinks,kind", EVICT)
+def test_evict(nats, lens, Hk, d, page, dtype, budget, recent, sinks, kind):
+    rng = torch.Generator().manual_seed(budget + len(lens))
+    per = -(-budget // page) + 1
+    table, spare, k, v = _filled(rng, lens, page, Hk, d, dtype, extra=per * len(lens) + 1)
+    shape = k.shape[:3]
+    w = {"spread": torch.exp(3 * torch.randn(shape, generator=rng)),
+         "ties": torch.randint(0, 4, shape, generator=rng).float(),
+         "equal": torch.full(shape, 2.5),
+         "odd": torch.randint(-3, 3, shape, generator=rng).float()}[kind]
+    if kind == "odd":  # the values that order strangely: both zeros, infinities, NaN, the lowest and the smallest
+        strange = torch.tensor([0.0, -0.0, math.inf, -math.inf, math.nan, -math.nan, 1e-45, -1e-45, -3.4e38])
+        w = strange[torch.randint(0, 9, shape, generator=rng)]
+    out_table = spare[:per * len(lens)].reshape(len(lens), per).clone()
+    c = _cache(nats, table, lens, k, v, w)
+    keep, n = nats.paged_evict(c, out_table.cuda(), budget, recent=recent, sinks=sinks, return_keep=True)
+    c.check()
+    want = ref.evict(w, table, lens, page, budget, recent, sinks)
+    assert torch.equal(keep.cpu(), want)
+    assert n.cpu().tolist() == [min(x, budget) for x in lens] and c.lens.cpu().tolist() == lens
+    gk, gv, gw = c.k_pages.cpu(), c.v_pages.cpu(), c.weight.cpu()
+    ints = {BF: torch.int16, F32: torch.int32}[dtype]
+    touched = torch.zeros(shape[0], page, dtype=torch.bool)
+    for b, m in enumerate(n.cpu().tolist()):
+        i = torch.arange(m)
+        at, sl = out_table[b].long()[i // page], i % page
+        touched[at, sl] = True
+        for h in range(Hk):
+            src = want[b, h, :m].long()
+            fr = (table[b].long()[src // page], h, src % page)
+            assert torch.equal(gk[at, h, sl].view(ints), k[fr].view(ints))
+            assert torch.equal(gv[at, h, sl].view(ints), v[fr].view(ints))
+            assert torch.equal(gw[at, h, sl].view(torch.int32), w[fr].view(torch.int32))
+    for got, was in ((gk, k), (gv, v)):
+        assert torch.equal(got.transpose(1, 2)[~touched].view(ints), was.transpose(1, 2)[~touched].view(ints))
+    assert torch.equal(gw.transpose(1, 2)[~touched].view(torch.int32), w.transpose(1, 2)[~touched].view(torch.int32))
+
+
+def test_evict_bad_entries_are_reported(nats):
+    rng = torch.Generator().manual_seed(10)
+    table, spare, k, v = _filled(rng, [64], 16, 1, 64, F32, extra=2)
+    w = torch.rand(k.shape[:3], generator=rng)
+    bad = table.clone()
+    bad[0, 1] = -1  # its slots count as the lowest weight
+    c = _cache(nats, bad, [64], k, v, w)
+    keep, _ = nats.paged_evict(c, spare[None].cuda(), 32, return_keep=True)
+    assert not ((keep >= 16) & (keep < 32)).any()
+    c.check()  # none of them is copied
+    c2 = _cache(nats, table, [64], k, v, w)
+    nats.paged_evict(c2, torch.tensor([[int(spare[0]), 1 << 20]], dtype=torch.int32).cuda(), 32)
+    with pytest.raises(nats.NatsError):
+        c2.check()
+
+
+def test_evict_captured(nats):
+    rng = torch.Generator().manual_seed(11)
+    table, spare, k, v = _filled(rng, [200, 90], 16, 2, 64, BF, extra=8)
+    w = torch.rand(k.shape[:3], generator=rng)
+    c = _cache(nats, table, [200, 90], k, v, w)
+    ot = spare.reshape(2, 4).contiguous().cuda()
+    nats.paged_evict(c, ot, 60)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        keep, n = nats.paged_evict(c, ot, 60, recent=5, return_keep=True)
+    w2 = torch.rand(k.shape[:3], generator=rng)
+    c.weight.copy_(w2)
+    c.lens.copy_(torch.tensor([100, 50], dtype=torch.int32))
+    g.replay()
+    assert torch.equal(keep.cpu(), ref.evict(w2, table, [100, 50], 16, 60, 5, 0)) and n.tolist() == [60, 50]
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("dtype,Hq,Hk,d,page", [(BF, 8, 2, 64, 16), (F32, 4, 4, 128, 32), (BF, 6, 1, 128, 64)])
+def test_prompt_steps_and_eviction_together(nats, dtype, Hq, Hk, d, page):
+    """A ragged prompt, decode steps that sum weights, an eviction, more steps: each step's output against the 64-bit
+    attention over what the cache holds, the kept slots against the sort of the cache's own weights, and every key
+    against its own norm and rotation in 64 bits."""
+    B, budget, recent, sinks = 3, 96, 24, 2
+    rng = torch.Generator().manual_seed(12)
+    prompt = [150, 40, 97]
+    most = 20
+    n_pages = 3 * B * most
+    c = nats.PagedCache.empty(n_pages, page, Hk, d, B, most, dtype=dtype, weight=True)
+    pages = torch.randperm(n_pages, generator=rng).to(torch.int32)
+    c.table.copy_(pages[:B * most].reshape(B, most))
+    fresh = pages[B * most:2 * B * most].reshape(B, most).contiguous().cuda()
+    f = nats.rope_inv_freq(d, 1e6)
+    wq, wk = torch.full((d,), 1.5, device="cuda"), torch.full((d,), 1.2, device="cuda")
+    seen = torch.zeros(B, dtype=torch.int32, device="cuda")  # tokens so far: the rotation's positions
+
+    def tokens(T, n_new):
+        qkv = torch.randn(B, T, (Hq + 2 * Hk) * d, generator=rng).to(dtype).cuda()
+        q, k, v = (t.unflatten(-1, (-1, d)).transpose(1, 2) for t in qkv.split([Hq * d, Hk * d, Hk * d], -1))
+        pos = seen[:, None].long() + torch.arange(T, device="cuda")
+        at = c.lens.clone()
+        oq = nats.paged_append(c, k, v, n_new=n_new, q=q, norm=True, w_q=wq, w_k=wk, inv_freq=f, positions=pos)
+        kr = ref.norm_rotate(k.cpu(), wk.cpu(), pos.cpu(), f.cpu(), False, True, 1e-6)
+        kz = ref.norm_rotate(k.cpu(), wk.cpu(), pos.cpu(), None, False, True, 1e-6)
+        bound = ref.rope_bound(kr, kz, d, False, dtype)
+        c.lens.add_(n_new)
+        seen.add_(n_new)
+        pool = c.k_pages.cpu()
+        for b in range(B):
+            m = int(n_new[b])
+            got = ref.slots(pool, c.table.cpu(), b, int(c.lens[b]), page)[:, int(at[b]):]
+            assert ((got.double() - kr[b, :, :m]).abs() <= bound[b, :, :m]).all()
+        return oq
+
+    def step():
+        q = tokens(1, torch.ones(B, dtype=torch.int32, device="cuda"))[:, :, 0]
+        before = c.weight.double().sum()
+        out = nats.paged_decode(c, q, accumulate=True)
+        e, _, _, err, _ = ref.decode(q.cpu(), c.k_pages.cpu(), c.v_pages.cpu(), c.table.cpu(), c.lens.tolist())
+        assert ((out.cpu().double() - e).abs() <= ref.HALF[dtype] * (e.abs() + err) + err).all()
+        assert abs(float(c.weight.double().sum() - before) - B * Hq) < 1e-3 * Hq
+
+    tokens(150, torch.tensor(prompt, dtype=torch.int32, device="cuda"))
+    for _ in range(3):
+        step()
+    lens = c.lens.tolist()
+    keep, n = nats.paged_evict(c, fresh, budget, recent=recent, sinks=sinks, return_keep=True)
+    assert torch.equal(keep.cpu(), ref.evict(c.weight.cpu(), c.table.cpu(), lens, page, budget, recent, sinks))
+    c.table.copy_(fresh)
+    c.lens.copy_(n)
+    for _ in range(3):
+        step()
+    c.check()
+    assert c.lens.tolist() == [min(x, budget) + 3 for x in lens] and seen.tolist() == [p + 6 for p in prompt]
+
+
+def test_refusals(nats):
+    c = nats.PagedCache.empty(4, 16, 2, 64, 2, 2, dtype=BF)
+    cw = nats.PagedCache.empty(4, 16, 2, 64, 2, 2, dtype=BF, weight=True)
+    q = torch.zeros(2, 4, 64, dtype=BF, device="cuda")
+    k = torch.zeros(2, 2, 1, 64, dtype=BF, device="cuda")
+    ot = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        nats.paged_decode(c, q, accumulate=True)  # no weights
+    with pytest.raises(ValueError):
+        nats.paged_evict(c, ot, 8)
+    with pytest.raises(ValueError):
+        nats.paged_decode(c, q[:1])
+    with pytest.raises(TypeError):
+        nats.paged_decode(c, q.float())
+    with pytest.raises(nats.NatsError):
+        nats.paged_decode(c, q[:, :3])  # not a multiple of the key heads
+    with pytest.raises(nats.NatsError):
+        nats.paged_decode(c, q, scale=float("nan"))
+    with pytest.raises(nats.NatsError):
+        nats.paged_decode(c, q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        nats.paged_append(c, k[:, :1], k[:, :1])
+    with pytest.raises(TypeError):
+        nats.paged_append(c, k, k, start=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(nats.NatsError):
+        nats.paged_evict(cw, ot, 8, recent=6, sinks=3)
+    with pytest.raises(nats.NatsError):
+        nats.paged_evict(cw, ot, 33)  # two pages hold 32
+    with pytest.raises(nats.NatsError):
+        nats.paged_evict(cw, cw.table, 8)
+    with pytest.raises(nats.NatsError):
+        nats.paged_evict(cw, ot, 8, lens_out=cw.lens)
+    with pytest.raises(ValueError):
+        nats.PagedCache(c.k_pages, c.v_pages[:2], c.table, c.lens)
+    with pytest.raises(TypeError):
+        nats.PagedCache(c.k_pages, c.v_pages, c.table.long(), c.lens)
+    with pytest.raises(AttributeError):
+        c.table = c.table.clone()
