@@ -25,7 +25,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSMs = 152;
 constexpr int kMaxCtas = kSMs * 4;
-constexpr int kMaxHeads = 8;  // query heads of a unit, at most
+constexpr int kMaxHeads = 16;  // query heads of a unit, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct DecodeArgs {
@@ -118,14 +118,6 @@ __device__ __forceinline__ Run my_run(const PagedView& pg, int U, long long* pre
 
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float* o);
-template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* o) {
-  const uint4 u = *(const uint4*)p;
-  o[0] = __uint_as_float(u.x << 16), o[1] = __uint_as_float(u.x & 0xffff0000u);
-  o[2] = __uint_as_float(u.y << 16), o[3] = __uint_as_float(u.y & 0xffff0000u);
-  o[4] = __uint_as_float(u.z << 16), o[5] = __uint_as_float(u.z & 0xffff0000u);
-  o[6] = __uint_as_float(u.w << 16), o[7] = __uint_as_float(u.w & 0xffff0000u);
-}
 template <>
 __device__ __forceinline__ void load8(const float* p, float* o) {
   const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
@@ -269,6 +261,238 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
   }
 }
 
+// ------------------------------------------------ bf16: tensor-core products
+
+// Sixteen bytes of a page, read once: past L1.
+__device__ __forceinline__ uint4 ldg_once(const void* p) {
+  uint4 u;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+      : "l"(p));
+  return u;
+}
+
+// c += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the transpose of an 8 x 8 matrix of 16-bit entries held two a lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *(const uint32_t*)&v;
+}
+
+// how far a score may rise above the running maximum (in powers of two)
+// before the sums are rescaled: 2^8 leaves fp32 its full precision
+constexpr float kSlack = 8.f;
+
+// A unit of up to 8 NH heads.  Each warp takes 16 slots of every tile, on its
+// own: both products run with the slots or the entries on the rows of the
+// 16 x 8 x 16 instruction and the heads on its 8 columns,
+//   S^T [16 slots x 8 heads] += K [16 x 16 entries] Q^T,
+//   O^T [16 entries x 8 heads] += V^T [16 x 16 slots] P^T,
+// so few heads waste little, and which entry (slot) carries which index of a
+// sum is free, so that every operand is a plain 16-byte load of a row:
+//   K: lane 4g + c holds entries 32 x + 8 c .. + 7 of slots g and g + 8 for
+//      each 32-entry block x, the same entries that it holds of head g's q;
+//   V: it holds entries 8 g .. + 7 (and 64 + 8 g .. + 7) of slots 2c, 2c + 1,
+//      2c + 8, 2c + 9, and pairs of slots are packed with byte permutes.
+// No shared memory in the loop.  P moves from S^T's to P^T's layout by an
+// 8 x 8 transpose; it is carried as two bf16, high and low part, so that the
+// rounding of p (2^-8 each) does not double the output's own.
+// A tile's K registers are refilled for the next tile as soon as the scores
+// are done, V's when the values are: about 8 KB in flight a warp.
+template <int D, int NH>
+__global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(DecodeArgs a) {
+  constexpr int KB = D / 32;        // 32-entry blocks of a key row
+  constexpr int VS = D / 64;        // 8-entry segments of a value row a lane holds
+  constexpr int MT = D / 16;        // 16-entry tiles of O^T
+  constexpr int GT = 8 * NH;
+  __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
+  const int U = a.pg.Hk * a.ngroups;
+  const Run run = my_run(a.pg, U, a.prefix);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const __nv_bfloat16 *kp = (const __nv_bfloat16*)a.k, *vp = (const __nv_bfloat16*)a.v;
+  long long cur = run.s, pre = run.pre;
+  int b = run.b0;
+  while (cur < run.e) {
+    const int n = a.pg.length(b), nt = tiles_of(n);
+    if (cur >= (pre + nt) * U) {
+      pre += nt;
+      ++b;
+      continue;
+    }
+    const long long local = cur - pre * U;
+    const int u = (int)(local / nt), t0 = (int)(local % nt);
+    const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
+    const int hk = u / a.ngroups, g0 = (u % a.ngroups) * GT;
+    const int heads = min(GT, a.G - g0), h0 = hk * a.G + g0;
+    uint4 q[NH][KB];
+    float o[NH][MT][4], mx[NH][2], sum[NH][2];
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+#pragma unroll
+      for (int y = 0; y < KB; ++y) {
+        q[x][y] = make_uint4(0, 0, 0, 0);
+        if (8 * x + g < heads)
+          q[x][y] = *(const uint4*)((const __nv_bfloat16*)a.q + b * a.q_b + (h0 + 8 * x + g) * a.q_h + 32 * y + 8 * c);
+      }
+#pragma unroll
+      for (int y = 0; y < MT; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[x][y][i] = 0.f;
+      mx[x][0] = mx[x][1] = -INFINITY;
+      sum[x][0] = sum[x][1] = 0.f;
+    }
+    uint4 k[2][KB], v[4][VS];
+    // row of this warp's first slot in tile t, or -1: past the end or without a page
+    auto first_row = [&](int t) -> long long {
+      const int j0 = t * kTile + warp * 16;
+      if (t >= t1 || j0 >= n) return -1;
+      const int pg = a.pg.page_of(b, j0 / a.pg.page);
+      if (pg < 0) {
+        if (lane == 0) *a.pg.err = 1;
+        return -1;
+      }
+      return a.pg.row(pg, hk, j0 % a.pg.page);
+    };
+    auto load_k = [&](long long row) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int y = 0; y < KB; ++y)
+          k[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(kp + (row + g + 8 * i) * D + 32 * y + 8 * c);
+    };
+    // values of slots behind the sequence are zero: 0 x NaN would not be
+    auto load_v = [&](long long row, int left) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int y = 0; y < VS; ++y)
+          v[i][y] = row < 0 || r >= left ? make_uint4(0, 0, 0, 0) : ldg_once(vp + (row + r) * D + 64 * y + 8 * g);
+      }
+    };
+    long long row = first_row(t0), next = first_row(t0 + 1);
+    load_k(row);
+    load_v(row, n - t0 * kTile - warp * 16);
+    for (int t = t0; t < t1; ++t) {
+      const int j0 = t * kTile + warp * 16;
+      const long long after = first_row(t + 2);
+      float s[NH][4];
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+        s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+#pragma unroll
+        for (int y = 0; y < KB; ++y) {
+          mma16816(s[x], k[0][y].x, k[1][y].x, k[0][y].y, k[1][y].y, q[x][y].x, q[x][y].y);
+          mma16816(s[x], k[0][y].z, k[1][y].z, k[0][y].w, k[1][y].w, q[x][y].z, q[x][y].w);
+        }
+      }
+      load_k(next);
+      const bool lo = row >= 0 && j0 + g < n, hi = row >= 0 && j0 + g + 8 < n;
+      uint32_t ph[NH][2], pl[NH][2];
+      bool rises = false;
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] = (i < 2 ? lo : hi) ? s[x][i] * a.scale2 : -INFINITY;
+        if (a.scores) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + g + 8 * (i >> 1), h = 8 * x + 2 * c + (i & 1);
+            if (j < n && h < heads)
+              a.scores[(((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G + g0 + h] = s[x][i];
+          }
+        }
+        rises |= fmaxf(s[x][0], s[x][2]) > mx[x][0] + kSlack || fmaxf(s[x][1], s[x][3]) > mx[x][1] + kSlack;
+      }
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float m = fmaxf(s[x][i], s[x][i + 2]);
+#pragma unroll
+            for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+            m = fmaxf(m, mx[x][i]);
+            const float f = part_scale(mx[x][i], m);
+            mx[x][i] = m;
+            sum[x][i] *= f;
+#pragma unroll
+            for (int y = 0; y < MT; ++y) o[x][y][i] *= f, o[x][y][i + 2] *= f;
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // (a head without a slot yet has no maximum to subtract: its scores are all -inf)
+          s[x][i] = s[x][i] == -INFINITY ? 0.f : exp2f(s[x][i] - mx[x][i & 1]);
+          sum[x][i & 1] += s[x][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = pack_bf16(s[x][2 * i], s[x][2 * i + 1]);
+          const float l0 = s[x][2 * i] - __uint_as_float(w << 16), l1 = s[x][2 * i + 1] - __uint_as_float(w & 0xffff0000u);
+          ph[x][i] = transpose8(w);
+          pl[x][i] = transpose8(pack_bf16(l0, l1));
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < MT; ++y) {
+        // rows g and g + 8 of tile y: entries 8g + y and 64 + 8g + y (D = 64: 8g + y and 8g + 4 + y)
+        const int ya = y, sa = 0, yb = D == 128 ? y : y + 4, sb = D == 128 ? VS - 1 : 0;
+        auto pair = [&](int s0, int e, int sg) {
+          const uint32_t* r0 = (const uint32_t*)&v[s0][sg];
+          const uint32_t* r1 = (const uint32_t*)&v[s0 + 1][sg];
+          return __byte_perm(r0[e / 2], r1[e / 2], e % 2 ? 0x7632 : 0x5410);
+        };
+        const uint32_t a0 = pair(0, ya, sa), a1 = pair(0, yb, sb), a2 = pair(2, ya, sa), a3 = pair(2, yb, sb);
+#pragma unroll
+        for (int x = 0; x < NH; ++x) {
+          mma16816(o[x][y], a0, a1, a2, a3, ph[x][0], ph[x][1]);
+          mma16816(o[x][y], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+        }
+      }
+      load_v(next, n - j0 - kTile);
+      row = next;
+      next = after;
+    }
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int z = 4; z < 32; z <<= 1) sum[x][i] += __shfl_xor_sync(0xffffffffu, sum[x][i], z);
+        const int h = 8 * x + 2 * c + i;
+        if (g == 0) sml[(warp * GT + h) * 2] = mx[x][i], sml[(warp * GT + h) * 2 + 1] = sum[x][i];
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          float* at = so + (warp * GT + h) * D + 8 * g + y;
+          at[0] = o[x][y][i];
+          at[D == 128 ? 64 : 4] = o[x][y][i + 2];
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == nt;
+    finish_unit<__nv_bfloat16, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
+    __syncthreads();
+    cur += t1 - t0;
+  }
+}
+
 // The CTA whose run holds tile x of the line (the run of CTA i of n is
 // [i T / n, (i + 1) T / n)).
 __device__ __forceinline__ int cta_of(long long x, long long T, int n) { return (int)(((x + 1) * n - 1) / T); }
@@ -376,21 +600,39 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
   return NATS_OK;
 }
 
-template <typename T, int D>
-cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
-  const int ctas = kSMs * 3;
-  a.GT = a.G == 1 ? 1 : a.G == 2 ? 2 : 4;
-  a.ngroups = (a.G + a.GT - 1) / a.GT;
-  if (a.GT == 1)
-    decode_simt_kernel<T, D, 1><<<ctas, kThreads, 0, st>>>(a);
-  else if (a.GT == 2)
-    decode_simt_kernel<T, D, 2><<<ctas, kThreads, 0, st>>>(a);
-  else
-    decode_simt_kernel<T, D, 4><<<ctas, kThreads, 0, st>>>(a);
+// fp32: units of up to four heads on the lanes.  bf16: eight heads a unit on
+// the tensor cores, sixteen where a group has more than eight (two products'
+// worth of registers, but the rows are read once).
+template <int D>
+cudaError_t launch(DecodeArgs& a, int dtype, cudaStream_t st) {
+  int ctas;
+  if (dtype == NATS_BF16) {
+    a.GT = a.G <= 8 ? 8 : 16;
+    a.ngroups = (a.G + a.GT - 1) / a.GT;
+    ctas = kSMs * (a.GT == 8 ? 3 : 2);
+    if (a.GT == 8)
+      decode_mma_kernel<D, 1><<<ctas, kThreads, 0, st>>>(a);
+    else
+      decode_mma_kernel<D, 2><<<ctas, kThreads, 0, st>>>(a);
+  } else {
+    ctas = kSMs * 3;
+    a.GT = a.G == 1 ? 1 : a.G == 2 ? 2 : 4;
+    a.ngroups = (a.G + a.GT - 1) / a.GT;
+    if (a.GT == 1)
+      decode_simt_kernel<float, D, 1><<<ctas, kThreads, 0, st>>>(a);
+    else if (a.GT == 2)
+      decode_simt_kernel<float, D, 2><<<ctas, kThreads, 0, st>>>(a);
+    else
+      decode_simt_kernel<float, D, 4><<<ctas, kThreads, 0, st>>>(a);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.pg.B * a.Hq;
-  decode_join_kernel<T, D><<<(unsigned)((rows + kWarps - 1) / kWarps), kThreads, 0, st>>>(a, ctas);
+  const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
+  if (dtype == NATS_BF16)
+    decode_join_kernel<__nv_bfloat16, D><<<grid, kThreads, 0, st>>>(a, ctas);
+  else
+    decode_join_kernel<float, D><<<grid, kThreads, 0, st>>>(a, ctas);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.scores) return e;
   decode_weight_kernel<<<kSMs * 8, kThreads, 0, st>>>(a);
@@ -429,11 +671,7 @@ nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float s
   a.Hq = Hq, a.G = Hq / cache->Hk;
   a.scale2 = (scale > 0.f ? scale : 1.0f / std::sqrt((float)cache->d)) * kLog2e;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e;
-  if (cache->dtype == NATS_BF16)
-    e = cache->d == 128 ? launch<__nv_bfloat16, 128>(a, st) : launch<__nv_bfloat16, 64>(a, st);
-  else
-    e = cache->d == 128 ? launch<float, 128>(a, st) : launch<float, 64>(a, st);
+  const cudaError_t e = cache->d == 128 ? launch<128>(a, cache->dtype, st) : launch<64>(a, cache->dtype, st);
   return (nats_status)record_cuda_error(e);
 }
 
