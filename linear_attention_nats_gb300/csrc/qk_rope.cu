@@ -56,42 +56,49 @@ struct Operand {
   long long b, h, t;
 };
 
-// Two quads of a row: loads, stores and conversions.
+// Four entries of a row as they are stored, and their conversions.
 template <typename T, bool VEC>
-struct Quads;
+struct Quad;
 template <>
-struct Quads<__nv_bfloat16, true> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* o) {
-    const uint2 u = *(const uint2*)p;
+struct Quad<__nv_bfloat16, true> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs((const uint2*)p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *(uint2*)p = u; }
+  __device__ __forceinline__ void get(float* o) const {
     o[0] = __uint_as_float(u.x << 16), o[1] = __uint_as_float(u.x & 0xffff0000u);
     o[2] = __uint_as_float(u.y << 16), o[3] = __uint_as_float(u.y & 0xffff0000u);
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* o) {
+  __device__ __forceinline__ void set(const float* o) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
-    uint2 u;
     u.x = *(const uint32_t*)&a, u.y = *(const uint32_t*)&b;
-    *(uint2*)p = u;
   }
 };
 template <>
-struct Quads<float, true> {
-  static __device__ __forceinline__ void load(const float* p, float* o) {
-    const float4 u = *(const float4*)p;
-    o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* o) {
-    *(float4*)p = make_float4(o[0], o[1], o[2], o[3]);
-  }
+struct Quad<float, true> {
+  float4 u;
+  __device__ __forceinline__ void load(const float* p) { u = __ldcs((const float4*)p); }
+  __device__ __forceinline__ void store(float* p) const { *(float4*)p = u; }
+  __device__ __forceinline__ void get(float* o) const { o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w; }
+  __device__ __forceinline__ void set(const float* o) { u = make_float4(o[0], o[1], o[2], o[3]); }
 };
 template <typename T>
-struct Quads<T, false> {
-  static __device__ __forceinline__ void load(const T* p, float* o) {
+struct Quad<T, false> {
+  T u[4];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = to_f32(p[i]);
+    for (int i = 0; i < 4; ++i) u[i] = p[i];
   }
-  static __device__ __forceinline__ void store(T* p, const float* o) {
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = from_f32<T>(o[i]);
+    for (int i = 0; i < 4; ++i) p[i] = u[i];
+  }
+  __device__ __forceinline__ void get(float* o) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = to_f32(u[i]);
+  }
+  __device__ __forceinline__ void set(const float* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = from_f32<T>(o[i]);
   }
 };
 
@@ -165,11 +172,69 @@ struct RopeArgs {
   const int32_t *start, *n_new;
 };
 
+// The lane's eight weights (ones without).
+__device__ __forceinline__ void lane_weights(const float* w, const LaneMap& m, float* o) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = w ? w[(i < 4 ? m.qa : m.qb - 4) + i] : 1.f;
+}
+
+constexpr int kRowsAhead = 4;  // row loads a lane has in flight
+
+// Rows h0 .. h1 - 1 of one token and one kind (query, key, or a value to
+// copy): kRowsAhead rows of every D / 8 lanes are requested together.
+// row_at(h) is the destination of row h, or NULL to leave it.
+template <typename T, int D, bool INTER, bool VEC, bool COPY, class RowAt>
+__device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h0, int h1, const float* w, bool norm,
+                                         float eps, const LaneMap& m, const float* c, const float* s, int sub,
+                                         RowAt row_at) {
+  constexpr int RPW = 32 / (D / 8);
+  float wl[8];
+  if (!COPY) lane_weights(w, m, wl);
+  for (int h = h0 + sub; h - sub < h1; h += kRowsAhead * RPW) {
+    Quad<T, VEC> qa[kRowsAhead], qb[kRowsAhead];
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i) {
+      const int r = h + i * RPW;
+      if (r < h1) {
+        qa[i].load(src + r * stride_h + m.qa);
+        qb[i].load(src + r * stride_h + m.qb);
+      } else {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        qa[i].set(zero), qb[i].set(zero);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i) {
+      const int r = h + i * RPW;
+      if (!COPY) {
+        float x[8];
+        qa[i].get(x), qb[i].get(x + 4);
+        if (norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+          ss = row_sum<D / 8>(ss);
+          const float rn = 1.f / sqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= rn * wl[e];
+        }
+        turn<INTER>(x, c, s);
+        qa[i].set(x), qb[i].set(x + 4);
+      }
+      if (r >= h1) continue;
+      T* dst = row_at(r);
+      if (!dst) continue;
+      qa[i].store(dst + m.qa);
+      qb[i].store(dst + m.qb);
+    }
+  }
+}
+
 // One warp per item (a token and a run of its rows): q rows, then k rows,
 // then (append) v rows.
 template <typename T, int D, bool INTER, bool PAGED, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(RopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
+  constexpr int LPR = D / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const long long item = (long long)blockIdx.x * kWarps + warp;
@@ -193,58 +258,39 @@ __global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(RopeArgs a) {
   }
   if (a.pos) p = a.pos[b * a.pos_b + t];
   const LaneMap m = lane_map<INTER>(l, a.rot);
-  float c[4], s[4], wq[8], wk[8];
+  float c[4], s[4];
   {
     uint64_t F[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(a.inv_freq[m.pair0 + i]) : 0;
     angles(F, m.turned, p, c, s);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = (i < 4 ? m.qa : m.qb - 4) + i;
-    wq[i] = a.wq ? a.wq[e] : 1.f;
-    wk[i] = a.wk ? a.wk[e] : 1.f;
+  if (r0 < a.Hq) {
+    T* dst = (T*)a.qo.p + b * a.qo.b + t * a.qo.t;
+    fwd_rows<T, D, INTER, VEC, false>((const T*)a.q.p + b * a.q.b + t * a.q.t, a.q.h, r0, min(r1, a.Hq), a.wq, a.norm,
+                                      a.eps, m, c, s, sub, [&](int h) { return dst + h * a.qo.h; });
   }
-  for (int r = r0; r < r1; r += RPW) {
-    const int row = r + sub;
-    const bool on = row < r1;
-    const bool is_q = row < a.Hq, is_v = PAGED && row >= a.Hq + a.Hk;
-    const int h = is_q ? row : is_v ? row - a.Hq - a.Hk : row - a.Hq;
-    const Operand& in = is_q ? a.q : is_v ? a.v : a.k;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (on) {
-      const T* src = (const T*)in.p + b * in.b + h * in.h + t * in.t;
-      Quads<T, VEC>::load(src + m.qa, x);
-      Quads<T, VEC>::load(src + m.qb, x + 4);
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-    ss = row_sum<LPR>(ss);
-    if (!is_v) {
-      if (a.norm) {
-        const float rn = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= rn * (is_q ? wq[i] : wk[i]);
-      }
-      turn<INTER>(x, c, s);
-    }
-    if (!on) continue;
-    T* dst;
-    if (!PAGED || is_q) {
-      const Operand& out = is_q ? a.qo : a.ko;
-      dst = (T*)out.p + b * out.b + h * out.h + t * out.t;
+  const int k0 = max(r0 - a.Hq, 0), k1 = min(r1 - a.Hq, a.Hk);
+  if (k0 < k1) {
+    const T* src = (const T*)a.k.p + b * a.k.b + t * a.k.t;
+    if (PAGED) {
+      fwd_rows<T, D, INTER, VEC, false>(src, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub, [&](int h) -> T* {
+        if (pg < 0) return nullptr;
+        const long long at = a.pg.row(pg, h, slot);
+        if (a.weight && l == 0) a.weight[at] = 0.f;
+        return (T*)a.k_pages + at * D;
+      });
     } else {
-      if (pg < 0) continue;
-      const long long at = a.pg.row(pg, h, slot);
-      dst = (T*)(is_v ? a.v_pages : a.k_pages) + at * D;
-      if (!is_v && a.weight && l == 0) a.weight[at] = 0.f;
+      T* dst = (T*)a.ko.p + b * a.ko.b + t * a.ko.t;
+      fwd_rows<T, D, INTER, VEC, false>(src, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub,
+                                        [&](int h) { return dst + h * a.ko.h; });
     }
-    Quads<T, VEC>::store(dst + m.qa, x);
-    Quads<T, VEC>::store(dst + m.qb, x + 4);
+  }
+  if (PAGED) {
+    const int v0 = max(r0 - a.Hq - a.Hk, 0), v1 = min(r1 - a.Hq - a.Hk, a.Hk);
+    if (v0 < v1 && pg >= 0)
+      fwd_rows<T, D, INTER, VEC, true>((const T*)a.v.p + b * a.v.b + t * a.v.t, a.v.h, v0, v1, nullptr, false, 0.f, m,
+                                       c, s, sub, [&](int h) { return (T*)a.v_pages + a.pg.row(pg, h, slot) * D; });
   }
 }
 
@@ -260,11 +306,76 @@ struct RopeBwdArgs {
   float* part;  // [grid, 2, D] or NULL
 };
 
+constexpr int kRowsAheadBwd = 2;
+
+// Gradients of rows h0 .. h1 - 1 of one token and one kind; acc gathers the
+// lane's share of dw.
+template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
+__device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* src, long long x_h, GO* dst,
+                                         long long d_h, int h0, int h1, const float* w, bool norm, float eps,
+                                         const LaneMap& m, const float* c, const float* s, int sub, float* acc) {
+  constexpr int RPW = 32 / (D / 8);
+  float wl[8];
+  lane_weights(w, m, wl);
+  for (int h = h0 + sub; h - sub < h1; h += kRowsAheadBwd * RPW) {
+    Quad<GI, VEC> ga[kRowsAheadBwd], gb[kRowsAheadBwd];
+    Quad<T, VEC> xa[kRowsAheadBwd], xb[kRowsAheadBwd];
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kRowsAheadBwd; ++i) {
+      const int r = h + i * RPW;
+      if (r < h1) {
+        ga[i].load(g + r * g_h + m.qa);
+        gb[i].load(g + r * g_h + m.qb);
+      } else {
+        ga[i].set(zero), gb[i].set(zero);
+      }
+      if (r < h1 && norm) {
+        xa[i].load(src + r * x_h + m.qa);
+        xb[i].load(src + r * x_h + m.qb);
+      } else {
+        xa[i].set(zero), xb[i].set(zero);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsAheadBwd; ++i) {
+      const int r = h + i * RPW;
+      float u[8];
+      ga[i].get(u), gb[i].get(u + 4);
+      turn<INTER>(u, c, s);
+      if (norm) {
+        float x[8], ss = 0.f, gx = 0.f;
+        xa[i].get(x), xb[i].get(x + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          ss += x[e] * x[e];
+          gx += u[e] * wl[e] * x[e];
+        }
+        ss = row_sum<D / 8>(ss);
+        gx = row_sum<D / 8>(gx);
+        const float rn = 1.f / sqrtf(ss * (1.f / D) + eps);
+        const float cx = gx * rn * rn * (1.f / D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (r < h1) acc[e] += u[e] * (x[e] * rn);
+          u[e] = rn * (u[e] * wl[e] - cx * x[e]);
+        }
+      }
+      if (r >= h1) continue;
+      Quad<GO, VEC> o;
+      o.set(u);
+      o.store(dst + r * d_h + m.qa);
+      o.set(u + 4);
+      o.store(dst + r * d_h + m.qb);
+    }
+  }
+}
+
 // The same mapping on a fixed grid whose warps stride over the items and keep
 // their shares of dw_q, dw_k in registers (8 entries of each a lane).
 template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeBwdArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
+__global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeBwdArgs a) {
+  constexpr int LPR = D / 8;
   __shared__ float red[kWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
@@ -272,14 +383,9 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeBwdArgs a) {
   uint64_t F[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(a.inv_freq[m.pair0 + i]) : 0;
-  float wq[8], wk[8], aq[8], ak[8];
+  float aq[8], ak[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = (i < 4 ? m.qa : m.qb - 4) + i;
-    wq[i] = a.wq ? a.wq[e] : 1.f;
-    wk[i] = a.wk ? a.wk[e] : 1.f;
-    aq[i] = ak[i] = 0.f;
-  }
+  for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
   const int rows = a.Hq + a.Hk;
   const long long n_items = (long long)a.B * a.L * a.items_per_token;
   for (long long item = (long long)blockIdx.x * kWarps + warp; item < n_items; item += (long long)gridDim.x * kWarps) {
@@ -291,51 +397,17 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeBwdArgs a) {
     angles(F, m.turned, a.pos ? a.pos[b * a.pos_b + t] : a.pos0 + t, c, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = -s[i];
-    for (int r = r0; r < r1; r += RPW) {
-      const int row = r + sub;
-      const bool on = row < r1, is_q = row < a.Hq;
-      const int h = is_q ? row : row - a.Hq;
-      float x[8], u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = u[i] = 0.f;
-      if (on) {
-        const Operand& gi = is_q ? a.gq : a.gk;
-        const GI* g = (const GI*)gi.p + b * gi.b + h * gi.h + t * gi.t;
-        Quads<GI, VEC>::load(g + m.qa, u);
-        Quads<GI, VEC>::load(g + m.qb, u + 4);
-        if (a.norm) {
-          const Operand& xi = is_q ? a.q : a.k;
-          const T* src = (const T*)xi.p + b * xi.b + h * xi.h + t * xi.t;
-          Quads<T, VEC>::load(src + m.qa, x);
-          Quads<T, VEC>::load(src + m.qb, x + 4);
-        }
-      }
-      turn<INTER>(u, c, s);
-      if (a.norm) {
-        float ss = 0.f, gx = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss += x[i] * x[i];
-          gx += u[i] * (is_q ? wq[i] : wk[i]) * x[i];
-        }
-        ss = row_sum<LPR>(ss);
-        gx = row_sum<LPR>(gx);
-        const float rn = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-        const float cx = gx * rn * rn * (1.f / D);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float ux = u[i] * x[i] * rn;  // zero in rows that are not `on`, unless n is 0 there
-          if (on) (is_q ? aq[i] : ak[i]) += ux;
-          u[i] = rn * (u[i] * (is_q ? wq[i] : wk[i]) - cx * x[i]);
-        }
-      }
-      if (on) {
-        const Operand& o = is_q ? a.dq : a.dk;
-        GO* dst = (GO*)o.p + b * o.b + h * o.h + t * o.t;
-        Quads<GO, VEC>::store(dst + m.qa, u);
-        Quads<GO, VEC>::store(dst + m.qb, u + 4);
-      }
-    }
+    if (r0 < a.Hq)
+      bwd_rows<T, GI, GO, D, INTER, VEC>((const GI*)a.gq.p + b * a.gq.b + t * a.gq.t, a.gq.h,
+                                         (const T*)a.q.p + b * a.q.b + t * a.q.t, a.q.h,
+                                         (GO*)a.dq.p + b * a.dq.b + t * a.dq.t, a.dq.h, r0, min(r1, a.Hq), a.wq, a.norm,
+                                         a.eps, m, c, s, sub, aq);
+    const int k0 = max(r0 - a.Hq, 0), k1 = min(r1 - a.Hq, a.Hk);
+    if (k0 < k1)
+      bwd_rows<T, GI, GO, D, INTER, VEC>((const GI*)a.gk.p + b * a.gk.b + t * a.gk.t, a.gk.h,
+                                         (const T*)a.k.p + b * a.k.b + t * a.k.t, a.k.h,
+                                         (GO*)a.dk.p + b * a.dk.b + t * a.dk.t, a.dk.h, k0, k1, a.wk, a.norm, a.eps, m,
+                                         c, s, sub, ak);
   }
   if (!a.part) return;
   // the CTA's sums: over the rows of a warp, then over the warps in order
@@ -359,26 +431,27 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeBwdArgs a) {
   }
 }
 
-// dw[e] = sum over the partials, in order: 8 runs of partials per column
+// dw[e] = sum over the partials, in order: 32 runs of partials per column
 template <int D>
 __global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][32];
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D
   float v = 0.f;
-  for (int i = threadIdx.y; i < n; i += 8) v += part[(long long)i * 2 * D + col];
+#pragma unroll 8
+  for (int i = threadIdx.y; i < n; i += 32) v += part[(long long)i * 2 * D + col];
   red[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y == 0) {
     v = 0.f;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) v += red[y][threadIdx.x];
+    for (int y = 0; y < 32; ++y) v += red[y][threadIdx.x];
     float* o = col < D ? dwq : dwk;
     if (o) o[col % D] = v;
   }
 }
 
 constexpr int kSMs = 152;
-constexpr int kBwdGrid = kSMs * 3;
+constexpr int kBwdGrid = kSMs * 2;
 
 // Rows a warp takes of one token: all of them when the tokens alone fill the
 // GPU (64 warps an SM), else split evenly so that short calls spread out.
@@ -598,7 +671,7 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
     launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, grid, st);
   int r = record_cuda_error(cudaGetLastError());
   if (r != NATS_OK || !dw) return (nats_status)r;
-  const dim3 bd(32, 8);
+  const dim3 bd(32, 32);
   if (d == 128)
     rope_dw_kernel<128><<<8, bd, 0, st>>>(a.part, (int)grid, dw_q, dw_k);
   else
