@@ -20,6 +20,7 @@
 // p F mod 2^64, exact whole turns dropping out of the product by themselves;
 // its upper 32 bits go to sincospif.
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged.cuh"
@@ -62,6 +63,7 @@ struct Quad;
 template <>
 struct Quad<__nv_bfloat16, true> {
   uint2 u;
+  __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs((const uint2*)p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *(uint2*)p = u; }
   __device__ __forceinline__ void get(float* o) const {
@@ -76,6 +78,7 @@ struct Quad<__nv_bfloat16, true> {
 template <>
 struct Quad<float, true> {
   float4 u;
+  __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const float* p) { u = __ldcs((const float4*)p); }
   __device__ __forceinline__ void store(float* p) const { *(float4*)p = u; }
   __device__ __forceinline__ void get(float* o) const { o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w; }
@@ -84,6 +87,10 @@ struct Quad<float, true> {
 template <typename T>
 struct Quad<T, false> {
   T u[4];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = from_f32<T>(0.f);
+  }
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = p[i];
@@ -181,27 +188,39 @@ __device__ __forceinline__ void lane_weights(const float* w, const LaneMap& m, f
 constexpr int kRowsAhead = 4;  // row loads a lane has in flight
 
 // Rows h0 .. h1 - 1 of one token and one kind (query, key, or a value to
-// copy): kRowsAhead rows of every D / 8 lanes are requested together.
-// row_at(h) is the destination of row h, or NULL to leave it.
+// copy), their first row at src: kRowsAhead rows of every D / 8 lanes are
+// requested together.  row_at(h) is the destination of row h, or NULL to
+// leave it.  With the weights taken into the token's cosines and sines, a pair
+// costs four products and the row's 1 / n two:
+//   y_a = (x_a w_a c - x_b w_b s) / n,  y_b = (x_b w_b c + x_a w_a s) / n.
 template <typename T, int D, bool INTER, bool VEC, bool COPY, class RowAt>
 __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h0, int h1, const float* w, bool norm,
                                          float eps, const LaneMap& m, const float* c, const float* s, int sub,
                                          RowAt row_at) {
   constexpr int RPW = 32 / (D / 8);
-  float wl[8];
-  if (!COPY) lane_weights(w, m, wl);
-  for (int h = h0 + sub; h - sub < h1; h += kRowsAhead * RPW) {
+  float ca[4], sa[4], cb[4], sb[4];
+  if (!COPY) {
+    float wl[8];
+    lane_weights(w, m, wl);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float wa = wl[INTER ? 2 * i : i], wb = wl[INTER ? 2 * i + 1 : i + 4];
+      ca[i] = wa * c[i], sa[i] = wa * s[i], cb[i] = wb * c[i], sb[i] = wb * s[i];
+    }
+  }
+  const long long step = RPW * stride_h;
+  const T *pa = src + (h0 + sub) * stride_h + m.qa, *pb = pa + (m.qb - m.qa);
+  auto rows = [&](int h, auto full) {
     Quad<T, VEC> qa[kRowsAhead], qb[kRowsAhead];
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
-      const int r = h + i * RPW;
-      if (r < h1) {
-        qa[i].load(src + r * stride_h + m.qa);
-        qb[i].load(src + r * stride_h + m.qb);
+      if (full || h + i * RPW < h1) {
+        qa[i].load(pa);
+        qb[i].load(pb);
       } else {
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        qa[i].set(zero), qb[i].set(zero);
+        qa[i].zero(), qb[i].zero();
       }
+      pa += step, pb += step;
     }
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
@@ -209,25 +228,32 @@ __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h
       if (!COPY) {
         float x[8];
         qa[i].get(x), qb[i].get(x + 4);
+        float rn = 1.f;
         if (norm) {
           float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-          ss = row_sum<D / 8>(ss);
-          const float rn = 1.f / sqrtf(ss * (1.f / D) + eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= rn * wl[e];
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+          rn = rsqrtf(fmaf(row_sum<D / 8>(ss), 1.f / D, eps));
         }
-        turn<INTER>(x, c, s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int ia = INTER ? 2 * e : e, ib = INTER ? 2 * e + 1 : e + 4;
+          const float xa = x[ia], xb = x[ib];
+          x[ia] = rn * fmaf(xa, ca[e], -(xb * sb[e]));
+          x[ib] = rn * fmaf(xb, cb[e], xa * sa[e]);
+        }
         qa[i].set(x), qb[i].set(x + 4);
       }
-      if (r >= h1) continue;
+      if (!full && r >= h1) continue;
       T* dst = row_at(r);
       if (!dst) continue;
       qa[i].store(dst + m.qa);
       qb[i].store(dst + m.qb);
     }
-  }
+  };
+  int h = h0;
+  for (; h + kRowsAhead * RPW <= h1; h += kRowsAhead * RPW) rows(h + sub, std::true_type{});
+  if (h < h1) rows(h + sub, std::false_type{});
 }
 
 // One warp per item (a token and a run of its rows): q rows, then k rows,
@@ -317,58 +343,69 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
   constexpr int RPW = 32 / (D / 8);
   float wl[8];
   lane_weights(w, m, wl);
-  for (int h = h0 + sub; h - sub < h1; h += kRowsAheadBwd * RPW) {
+  const int dq = m.qb - m.qa;
+  const GI* pg = g + (h0 + sub) * g_h + m.qa;
+  const T* px = src + (h0 + sub) * x_h + m.qa;
+  GO* pd = dst + (h0 + sub) * d_h + m.qa;
+  const long long sg = RPW * g_h, sx = RPW * x_h, sd = RPW * d_h;
+  auto rows = [&](int h, auto full) {
     Quad<GI, VEC> ga[kRowsAheadBwd], gb[kRowsAheadBwd];
     Quad<T, VEC> xa[kRowsAheadBwd], xb[kRowsAheadBwd];
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kRowsAheadBwd; ++i) {
-      const int r = h + i * RPW;
-      if (r < h1) {
-        ga[i].load(g + r * g_h + m.qa);
-        gb[i].load(g + r * g_h + m.qb);
+      const bool on = full || h + i * RPW < h1;
+      if (on) {
+        ga[i].load(pg);
+        gb[i].load(pg + dq);
       } else {
-        ga[i].set(zero), gb[i].set(zero);
+        ga[i].zero(), gb[i].zero();
       }
-      if (r < h1 && norm) {
-        xa[i].load(src + r * x_h + m.qa);
-        xb[i].load(src + r * x_h + m.qb);
+      if (on && norm) {
+        xa[i].load(px);
+        xb[i].load(px + dq);
       } else {
-        xa[i].set(zero), xb[i].set(zero);
+        xa[i].zero(), xb[i].zero();
       }
+      pg += sg, px += sx;
     }
 #pragma unroll
     for (int i = 0; i < kRowsAheadBwd; ++i) {
-      const int r = h + i * RPW;
+      const bool on = full || h + i * RPW < h1;
       float u[8];
       ga[i].get(u), gb[i].get(u + 4);
       turn<INTER>(u, c, s);
       if (norm) {
-        float x[8], ss = 0.f, gx = 0.f;
+        float x[8], ss = 0.f, gx = 0.f, t[8];
         xa[i].get(x), xb[i].get(x + 4);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          ss += x[e] * x[e];
-          gx += u[e] * wl[e] * x[e];
+          t[e] = u[e] * x[e];
+          ss = fmaf(x[e], x[e], ss);
+          gx = fmaf(t[e], wl[e], gx);
         }
         ss = row_sum<D / 8>(ss);
         gx = row_sum<D / 8>(gx);
-        const float rn = 1.f / sqrtf(ss * (1.f / D) + eps);
+        const float rn = rsqrtf(fmaf(ss, 1.f / D, eps));
         const float cx = gx * rn * rn * (1.f / D);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (r < h1) acc[e] += u[e] * (x[e] * rn);
-          u[e] = rn * (u[e] * wl[e] - cx * x[e]);
+          if (on) acc[e] = fmaf(t[e], rn, acc[e]);
+          u[e] = rn * fmaf(u[e], wl[e], -(cx * x[e]));
         }
       }
-      if (r >= h1) continue;
-      Quad<GO, VEC> o;
-      o.set(u);
-      o.store(dst + r * d_h + m.qa);
-      o.set(u + 4);
-      o.store(dst + r * d_h + m.qb);
+      if (on) {
+        Quad<GO, VEC> o;
+        o.set(u);
+        o.store(pd);
+        o.set(u + 4);
+        o.store(pd + dq);
+      }
+      pd += sd;
     }
-  }
+  };
+  int h = h0;
+  for (; h + kRowsAheadBwd * RPW <= h1; h += kRowsAheadBwd * RPW) rows(h + sub, std::true_type{});
+  if (h < h1) rows(h + sub, std::false_type{});
 }
 
 // The same mapping on a fixed grid whose warps stride over the items and keep
