@@ -185,6 +185,17 @@ __device__ __forceinline__ void lane_weights(const float* w, const LaneMap& m, f
   for (int i = 0; i < 8; ++i) o[i] = w ? w[(i < 4 ? m.qa : m.qb - 4) + i] : 1.f;
 }
 
+// Rows h0 .. h1 - 1 at src to L2, a lane a 128-byte line: the whole item's
+// reads are under way while the warp still forms its angles.
+template <typename T, int D>
+__device__ __forceinline__ void prefetch_rows(const T* src, long long stride_h, int h0, int h1, int lane) {
+  constexpr int kLines = D * (int)sizeof(T) / 128;
+  for (int i = lane; i < (h1 - h0) * kLines; i += 32) {
+    const T* p = src + (h0 + i / kLines) * stride_h + (i % kLines) * (128 / (int)sizeof(T));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  }
+}
+
 constexpr int kRowsAhead = 4;  // row loads a lane has in flight
 
 // Rows h0 .. h1 - 1 of one token and one kind (query, key, or a value to
@@ -270,10 +281,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const int rows = a.Hq + a.Hk + (PAGED ? a.Hk : 0);
   const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
   const int r1 = min(rows, r0 + a.rows_per_item);
+  if (PAGED && a.n_new && t >= a.n_new[b]) return;
+  const int k0 = max(r0 - a.Hq, 0), k1 = min(r1 - a.Hq, a.Hk);
+  const T *qs = (const T*)a.q.p + b * a.q.b + t * a.q.t, *ks = (const T*)a.k.p + b * a.k.b + t * a.k.t;
+  prefetch_rows<T, D>(qs, a.q.h, r0, min(r1, a.Hq), lane);
+  prefetch_rows<T, D>(ks, a.k.h, k0, k1, lane);
+  const int v0 = max(r0 - a.Hq - a.Hk, 0), v1 = PAGED ? min(r1 - a.Hq - a.Hk, a.Hk) : 0;
+  const T* vs = PAGED ? (const T*)a.v.p + b * a.v.b + t * a.v.t : nullptr;
+  if (PAGED) prefetch_rows<T, D>(vs, a.v.h, v0, v1, lane);
   long long p = a.pos0 + t;
   int pg = -1, slot = 0;
   if (PAGED) {
-    if (a.n_new && t >= a.n_new[b]) return;
     const long long at = (long long)(a.start ? a.start[b] : a.pg.lens[b]) + t;
     p = at;
     if (at >= 0 && at < a.pg.cap()) {
@@ -293,14 +311,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   }
   if (r0 < a.Hq) {
     T* dst = (T*)a.qo.p + b * a.qo.b + t * a.qo.t;
-    fwd_rows<T, D, INTER, VEC, false>((const T*)a.q.p + b * a.q.b + t * a.q.t, a.q.h, r0, min(r1, a.Hq), a.wq, a.norm,
+    fwd_rows<T, D, INTER, VEC, false>(qs, a.q.h, r0, min(r1, a.Hq), a.wq, a.norm,
                                       a.eps, m, c, s, sub, [&](int h) { return dst + h * a.qo.h; });
   }
-  const int k0 = max(r0 - a.Hq, 0), k1 = min(r1 - a.Hq, a.Hk);
   if (k0 < k1) {
-    const T* src = (const T*)a.k.p + b * a.k.b + t * a.k.t;
     if (PAGED) {
-      fwd_rows<T, D, INTER, VEC, false>(src, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub, [&](int h) -> T* {
+      fwd_rows<T, D, INTER, VEC, false>(ks, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub, [&](int h) -> T* {
         if (pg < 0) return nullptr;
         const long long at = a.pg.row(pg, h, slot);
         if (a.weight && l == 0) a.weight[at] = 0.f;
@@ -308,14 +324,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
       });
     } else {
       T* dst = (T*)a.ko.p + b * a.ko.b + t * a.ko.t;
-      fwd_rows<T, D, INTER, VEC, false>(src, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub,
+      fwd_rows<T, D, INTER, VEC, false>(ks, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub,
                                         [&](int h) { return dst + h * a.ko.h; });
     }
   }
   if (PAGED) {
-    const int v0 = max(r0 - a.Hq - a.Hk, 0), v1 = min(r1 - a.Hq - a.Hk, a.Hk);
     if (v0 < v1 && pg >= 0)
-      fwd_rows<T, D, INTER, VEC, true>((const T*)a.v.p + b * a.v.b + t * a.v.t, a.v.h, v0, v1, nullptr, false, 0.f, m,
+      fwd_rows<T, D, INTER, VEC, true>(vs, a.v.h, v0, v1, nullptr, false, 0.f, m,
                                        c, s, sub, [&](int h) { return (T*)a.v_pages + a.pg.row(pg, h, slot) * D; });
   }
 }

@@ -538,3 +538,28 @@ def test_refusals(nats):
         nats.PagedCache(c.k_pages, c.v_pages, c.table.long(), c.lens)
     with pytest.raises(AttributeError):
         c.table = c.table.clone()
+
+
+@pytest.mark.parametrize("B,Hk,n,page,budget,recent,sinks", [
+    (1, 1, 300000, 64, 70000, 100, 4), (1, 2, 1000000, 64, 3, 1, 1), (2, 30, 40000, 16, 39000, 0, 0),
+    (1, 200, 9000, 48, 100, 7, 0)])
+def test_evict_long_sequences(nats, B, Hk, n, page, budget, recent, sinks):
+    """Heads of several CTAs, and shares longer than a CTA holds: the kept slots of a stable sort."""
+    torch.manual_seed(n)
+    pg, per = -(-n // page), -(-budget // page)
+    N = B * (pg + per)
+    k = torch.zeros(N, Hk, page, 64, dtype=BF, device="cuda")
+    w = 3 * torch.randn(N, Hk, page, device="cuda")
+    if n % 20000 == 0:  # with many ties
+        w = w.round() / 3
+    order = torch.randperm(N, device="cuda").int()
+    table, ot = order[:B * pg].reshape(B, pg).contiguous(), order[B * pg:].reshape(B, per).contiguous()
+    lens = torch.tensor([n - 3 * b for b in range(B)], dtype=torch.int32, device="cuda")
+    c = nats.PagedCache(k, k.clone(), table, lens, weight=w)
+    ww = w[table.long()].transpose(1, 2).reshape(B, Hk, -1)[:, :, :n].clone()
+    j, L = torch.arange(n, device="cuda"), lens.long()[:, None, None]
+    key = torch.where((j < sinks) | (j >= L - recent), math.inf, ww)
+    key = torch.where(j < L, key, -math.inf)
+    want = key.sort(dim=-1, descending=True, stable=True).indices[..., :budget].sort(dim=-1).values.int()
+    keep, _ = nats.paged_evict(c, ot, budget, recent=recent, sinks=sinks, return_keep=True)
+    assert torch.equal(keep, want)
