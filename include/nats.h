@@ -634,8 +634,8 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
  * table sets err[0] to 1 (never cleared by the library); such a slot is
  * neither read nor written (an attention leaves it out), lengths are taken
  * as the nearest valid ones.
- * All pointers device, k_pages and v_pages 16-byte aligned, contiguous.  At
- * most 2^30 slots a sequence (max_pages page; else NATS_ERR_UNSUPPORTED). */
+ * All pointers device, k_pages, v_pages and weight 16-byte aligned,
+ * contiguous.  At most 2^30 slots a sequence (max_pages page; else NATS_ERR_UNSUPPORTED). */
 typedef struct {
   void* k_pages;
   void* v_pages;

@@ -54,8 +54,8 @@ inline nats_status check_cache_pointers(const nats_paged_cache* c) {
   if (!c->lens || !c->err) return NATS_ERR_NULL;
   if (c->max_pages > 0 && !c->table) return NATS_ERR_NULL;
   if (c->n_pages > 0 && (!c->k_pages || !c->v_pages)) return NATS_ERR_NULL;
-  if (((uintptr_t)c->k_pages | (uintptr_t)c->v_pages) & 15u) return NATS_ERR_ALIGN;
-  if (((uintptr_t)c->table | (uintptr_t)c->lens | (uintptr_t)c->err | (uintptr_t)c->weight) & 3u) return NATS_ERR_ALIGN;
+  if (((uintptr_t)c->k_pages | (uintptr_t)c->v_pages | (uintptr_t)c->weight) & 15u) return NATS_ERR_ALIGN;
+  if (((uintptr_t)c->table | (uintptr_t)c->lens | (uintptr_t)c->err) & 3u) return NATS_ERR_ALIGN;
   return NATS_OK;
 }
 

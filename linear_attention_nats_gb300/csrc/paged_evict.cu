@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;            // two a thread
+constexpr int kBins = 2048;            // two groups of 32 a warp
 constexpr int kKeysHeld = 32768;       // slots of a CTA's share in shared memory; a longer share is read again
 constexpr int kSMs = 152;
 constexpr int kMaxCluster = 8;
@@ -49,12 +49,6 @@ __device__ __forceinline__ uint32_t order_bits(float w) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// The weight's image of slot j (a slot without a page counts as the lowest).
-__device__ __forceinline__ uint32_t slot_bits(const EvictArgs& a, int b, int h, int j) {
-  const int pg = a.pg.page_of(b, j / a.pg.page);
-  return pg < 0 ? order_bits(-INFINITY) : order_bits(a.weight[a.pg.row(pg, h, j % a.pg.page)]);
-}
-
 // Inclusive sum over the CTA's threads in thread order; *total gets all of it.
 __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -77,10 +71,41 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   return x + before;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, int held) {
+// One warp: of 32 PER counts in every CTA of the cluster, summed over them, the
+// index of the one that holds the rest-th from the top; *above, the sum of those above it.
+template <int PER>
+__device__ __forceinline__ int find_from_top(cooperative_groups::cluster_group& cluster, int* counts, int C, int rest,
+                                             int* above) {
+  const int lane = threadIdx.x & 31;
+  int v[PER] = {};  // from the top: lane 0 has the highest
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < C) {
+      const int* c = cluster.map_shared_rank(counts, r) + 32 * PER - 1 - PER * lane;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] += c[-i];
+    }
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) mine += v[i];
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  int before = upto - mine, at = 32 * PER - 1 - PER * lane;
+  const bool here = before < rest && rest <= upto;
+  if (PER == 2 && here && rest > before + v[0]) before += v[0], --at;
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  *above = __shfl_sync(0xffffffffu, before, src);
+  return __shfl_sync(0xffffffffu, at, src);
+}
+
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a, int held) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];  // the share's first `held` weights, as order_bits
-  __shared__ int hist[3][kBins];
+  __shared__ int hist[3][kBins], groups[3][kBins / 32];
   __shared__ int sums[kSelWarps], pick[2], counts[2];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -98,47 +123,71 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     for (int i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) keep[i] = i;
     return;
   }
-  // the candidates are the slots m0 <= j < m1, of which `need` stay
+  // the candidates are the slots m0 <= j < m1, of which `need` stay; the others
+  // stay whatever they weigh: their image is above every weight's
   const int m0 = a.sinks, m1 = n - a.recent, need = a.budget - a.sinks - a.recent;
-  // this CTA's share and, of it, this warp's run: contiguous, whole warps wide
-  const int run = (n + C * kSelThreads - 1) / (C * kSelThreads) * 32;
-  const int s0 = min((long long)n, (long long)rank * run * kSelWarps), w0 = s0 + warp * run;
-  const int w1 = min(n, w0 + run);
+  constexpr uint32_t kAlways = 0xffffffffu;
+  // this CTA's share and, of it, this warp's run: contiguous, 128 slots or a multiple
+  const int run = (n + C * kSelWarps * 128 - 1) / (C * kSelWarps * 128) * 128;
+  const int s0 = min((long long)n, (long long)rank * run * kSelWarps);
+  const int w0 = min((long long)n, s0 + (long long)warp * run), w1 = min(n, w0 + run);
   for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  auto key = [&](int j) { return j - s0 < held ? keys[j - s0] : slot_bits(a, b, h, j); };
-  uint32_t prefix = 0, mask = 0;
+  // the images of slots j .. j + 3 (j a multiple of 4, so of one page); 0, below
+  // every weight's, behind the last
+  auto image4 = [&](int j) {
+    const int pg = a.pg.page_of(b, j / a.pg.page);
+    const float4 w = pg < 0 ? make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY)  // no page: the lowest
+                            : *(const float4*)(a.weight + a.pg.row(pg, h, j % a.pg.page));
+    uint32_t u[4] = {order_bits(w.x), order_bits(w.y), order_bits(w.z), order_bits(w.w)};
+    if (j < m0 || j + 3 >= m1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + i < m0 || j + i >= m1) u[i] = j + i < n ? kAlways : 0;
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  };
+  auto key4 = [&](int j) { return j - s0 < held ? *(const uint4*)(keys + (j - s0)) : image4(j); };
+  {
+#pragma unroll 2
+    for (int j = w0 + 4 * lane; j < w1; j += 128) {
+      const uint4 u = image4(j);
+      if (j - s0 < held) *(uint4*)(keys + (j - s0)) = u;  // (held is a multiple of 4)
+      if (need > 0) {
+        if (u.x + 1 > 1) atomicAdd(&hist[0][u.x >> 21], 1);  // neither 0 nor kAlways
+        if (u.y + 1 > 1) atomicAdd(&hist[0][u.y >> 21], 1);
+        if (u.z + 1 > 1) atomicAdd(&hist[0][u.z >> 21], 1);
+        if (u.w + 1 > 1) atomicAdd(&hist[0][u.w >> 21], 1);
+      }
+    }
+    __syncwarp();
+  }
+  uint32_t prefix = need > 0 ? 0 : kAlways - 1, mask = 0;  // no candidate stays: only kAlways is above
   int rest = need;  // of the candidates that share the prefix, how many stay
   if (need > 0) {
-#pragma unroll 4
-    for (int j = w0 + lane; j < w1; j += 32) {
-      const uint32_t u = slot_bits(a, b, h, j);
-      if (j - s0 < held) keys[j - s0] = u;
-      if (j >= m0 && j < m1) atomicAdd(&hist[0][u >> 21], 1);
-    }
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
       if (pass > 0)
-        for (int j = w0 + lane; j < w1; j += 32) {
-          const uint32_t u = key(j);
-          if (j >= m0 && j < m1 && (u & mask) == prefix) atomicAdd(&hist[pass][(u >> shift) & (bins - 1)], 1);
+        for (int j = w0 + 4 * lane; j < w1; j += 128) {
+          const uint4 u = key4(j);
+          // (kAlways, should the prefix be its own, is no weight; the prefix is never 0's)
+          if ((u.x & mask) == prefix && u.x != kAlways) atomicAdd(&hist[pass][(u.x >> shift) & (bins - 1)], 1);
+          if ((u.y & mask) == prefix && u.y != kAlways) atomicAdd(&hist[pass][(u.y >> shift) & (bins - 1)], 1);
+          if ((u.z & mask) == prefix && u.z != kAlways) atomicAdd(&hist[pass][(u.z >> shift) & (bins - 1)], 1);
+          if ((u.w & mask) == prefix && u.w != kAlways) atomicAdd(&hist[pass][(u.w >> shift) & (bins - 1)], 1);
         }
+      // sums of 32 bins each (two a warp), so that the search reads little of the other CTAs
+      __syncthreads();
+      const int g_hi = __reduce_add_sync(0xffffffffu, hist[pass][64 * warp + 32 + lane]);
+      const int g_lo = __reduce_add_sync(0xffffffffu, hist[pass][64 * warp + lane]);
+      if (lane == 0) groups[pass][2 * warp] = g_lo, groups[pass][2 * warp + 1] = g_hi;
       cluster.sync();
-      // bins from the top, two a thread, summed over the cluster
-      int hi = 0, lo = 0;
-      const int top = bins - 1 - 2 * tid;
-      if (top > 0)
-        for (int r = 0; r < C; ++r) {
-          const int2 v = *(const int2*)cluster.map_shared_rank(&hist[pass][top - 1], r);
-          hi += v.y, lo += v.x;
-        }
-      int total;
-      const int upto = block_scan(hi + lo, sums, &total);
-      const int before = upto - hi - lo;
-      if (before < rest && rest <= upto) {
-        const bool in_hi = rest <= before + hi;
-        pick[0] = in_hi ? top : top - 1;
-        pick[1] = rest - (in_hi ? before : before + hi);
+      if (warp == 0) {
+        // the group from the top in which the rest-th lies, then the bin within it
+        int above, more;
+        const int gr = find_from_top<2>(cluster, groups[pass], C, rest, &above);
+        const int bin = find_from_top<1>(cluster, hist[pass] + 32 * gr, C, rest - above, &more);
+        if (lane == 0) pick[0] = 32 * gr + bin, pick[1] = rest - above - more;
       }
       __syncthreads();
       prefix |= (uint32_t)pick[0] << shift;
@@ -146,43 +195,55 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
       rest = pick[1];
     }
   }
-  // threshold `prefix`: heavier candidates stay, and the first `rest` equal ones
-  auto look = [&](int j, bool& sure, bool& tie) {
-    sure = j < w1 && (j < m0 || j >= m1), tie = false;
-    if (need > 0 && j < w1 && j >= m0 && j < m1) {
-      const uint32_t u = key(j);
-      sure = u > prefix, tie = u == prefix;
-    }
-  };
+  // threshold `prefix`: heavier slots stay, and the first `rest` equal ones
   int nsure = 0, ntie = 0;
-  for (int j = w0 + lane; j - lane < w1; j += 32) {
-    bool sure, tie;
-    look(j, sure, tie);
-    nsure += __popc(__ballot_sync(0xffffffffu, sure));
-    ntie += __popc(__ballot_sync(0xffffffffu, tie));
+  for (int j = w0 + 4 * lane; j < w1; j += 128) {
+    const uint4 u = key4(j);
+    nsure += (u.x > prefix) + (u.y > prefix) + (u.z > prefix) + (u.w > prefix);
+    ntie += (u.x == prefix) + (u.y == prefix) + (u.z == prefix) + (u.w == prefix);
   }
+  nsure = __reduce_add_sync(0xffffffffu, nsure), ntie = __reduce_add_sync(0xffffffffu, ntie);
   int total_sure, total_tie;
   const int sure_upto = block_scan(lane == 0 ? nsure : 0, sums, &total_sure);
   const int tie_upto = block_scan(lane == 0 ? ntie : 0, sums, &total_tie);
   if (tid == 0) counts[0] = total_sure, counts[1] = total_tie;
   cluster.sync();
   int sure0 = __shfl_sync(0xffffffffu, sure_upto, 0) - nsure, tie0 = __shfl_sync(0xffffffffu, tie_upto, 0) - ntie;
-  for (int r = 0; r < rank; ++r) {
-    const int* c = cluster.map_shared_rank(counts, r);
-    sure0 += c[0], tie0 += c[1];
-  }
+#pragma unroll
+  for (int r = 0; r < kMaxCluster - 1; ++r)
+    if (r < rank) {
+      const int* c = cluster.map_shared_rank(counts, r);
+      sure0 += c[0], tie0 += c[1];
+    }
   cluster.sync();  // no CTA leaves while another reads its counts
-  const uint32_t lower = (1u << lane) - 1;
-  for (int j = w0 + lane; j - lane < w1; j += 32) {
-    bool sure, tie;
-    look(j, sure, tie);
-    const uint32_t bs = __ballot_sync(0xffffffffu, sure), bt = __ballot_sync(0xffffffffu, tie);
-    // kept before slot j: the sure ones, and of the ties before it the first `rest`
-    const int ties = tie0 + __popc(bt & lower);
-    const int at = sure0 + __popc(bs & lower) + min(ties, rest);
-    if (sure || (tie && ties < rest)) keep[at] = j;
-    sure0 += __popc(bs);
-    tie0 += __popc(bt);
+  for (int j0 = w0; j0 < w1; j0 += 128) {
+    const int j = j0 + 4 * lane;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (j < w1) u = key4(j);
+    // sure ones (upper half) and ties (lower half) before this lane's four slots
+    uint32_t mine = (u.x > prefix) + (u.y > prefix) + (u.z > prefix) + (u.w > prefix);
+    mine = mine << 16 | ((u.x == prefix) + (u.y == prefix) + (u.z == prefix) + (u.w == prefix));
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    int sure = sure0 + (int)((upto - mine) >> 16), ties = tie0 + (int)((upto - mine) & 0xffff);
+    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // kept before slot j + i: the sure ones, and of the ties the first `rest`
+      const int at = sure + min(ties, rest);
+      if (v[i] > prefix) keep[at] = j + i, ++sure;
+      if (v[i] == prefix) {
+        if (ties < rest) keep[at] = j + i;
+        ++ties;
+      }
+    }
+    sure0 += all >> 16;
+    tie0 += all & 0xffff;
   }
 }
 
@@ -226,7 +287,7 @@ cudaError_t launch_select(const EvictArgs& a, long long cap, cudaStream_t st) {
   const long long heads = (long long)a.pg.B * a.pg.Hk;
   int C = 1;
   while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 4096) C *= 2;
-  const long long share = (cap + C * kSelThreads - 1) / (C * kSelThreads) * kSelThreads;
+  const long long warps = C * kSelWarps, share = (cap + warps * 128 - 1) / (warps * 128) * 128 * kSelWarps;
   const int held = (int)(share < kKeysHeld ? share : kKeysHeld);
   if (held * 4 > 16384) {  // beyond what a kernel has without asking
     const cudaError_t e =
