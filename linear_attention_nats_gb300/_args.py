@@ -1,15 +1,23 @@
-"""Argument checks shared by the operator modules: tensors of one device, and
-the stream that a call runs on."""
+"""Argument checks and the call itself, shared by the operator modules.
+
+A small call's time is this file's: each check is one comparison on the way
+through, and what explains a refusal is worked out only once one has failed."""
 
 from __future__ import annotations
 
-import contextlib
+from functools import lru_cache
 
 import torch
 
-from ._native import NATS_BF16, NATS_F32, Strides
+from . import _native
+from ._native import NATS_BF16, NATS_F32, RopeDims, Strides
 
 _CODES = {torch.bfloat16: NATS_BF16, torch.float32: NATS_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+# the C structs of sizes and strides, by their values (never written after)
+strides = lru_cache(maxsize=4096)(Strides)
+rope_dims = lru_cache(maxsize=4096)(RopeDims)
 
 
 def dtype_code(t: torch.Tensor, name: str) -> int:
@@ -19,63 +27,71 @@ def dtype_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def need(t, name, dtype=None, shape=None, device=None, contiguous=True):
-    """Checks one tensor argument and returns its address (None for None)."""
-    if t is None:
-        return None
+def cuda_device(t: torch.Tensor, name: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if dtype is not None and t.dtype != dtype:
+    return t.device
+
+
+def _refuse(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def need(t, name, dtype, shape, device):
+    """The address of a contiguous tensor argument (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.device == device and (shape is None or t.shape == shape) and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device)
 
 
 def heads(t, name, dtype, shape, device):
     """A [B, H, L, d] operand with any strides but the last: its address and strides."""
-    p = need(t, name, dtype, shape, device, contiguous=False)
-    b, h, t_, e = t.stride()
-    if e != 1 and t.shape[3] > 1 and t.numel() > 0:
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        _refuse(t, name, dtype, shape, device)
+    b, h, s, e = t.stride()
+    if e != 1 and t.numel() > 0:
         raise ValueError(f"{name}: the entries of a row must be contiguous (last stride 1, got {e})")
-    return p, Strides(b, h, t_)
+    return t.data_ptr(), strides(b, h, s)
 
 
-def distinct(t, name):
-    """Refuses an output some of whose elements share an address (an expanded tensor)."""
-    for n, s in zip(t.shape, t.stride()):
-        if s == 0 and n > 1:
-            raise ValueError(f"{name} is written and must not be an expanded tensor")
+def heads_out(t, name, dtype, shape, device):
+    """The same for an output, which must not be an expanded tensor (entries that share an address)."""
+    p, st = heads(t, name, dtype, shape, device)
+    if 0 in t.stride():
+        for n, s in zip(t.shape, t.stride()):
+            if s == 0 and n > 1:
+                raise ValueError(f"{name} is written and must not be an expanded tensor")
+    return p, st
 
 
-@contextlib.contextmanager
-def launch(device, stream, made=()):
-    """The handle of the stream a call runs on, with `device` the current one.
-    `made`: tensors allocated for the call (on the current stream), which a
-    call on another stream keeps alive until it has run."""
-    cur = torch.cuda.current_stream(device)
-    s = cur if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    if s != cur:
-        for t in made:
-            if t is not None:
-                t.record_stream(s)
-    if device.index == torch.cuda.current_device():
-        yield s.cuda_stream
+def call(fn, where, device, stream, made, *args):
+    """fn(*args, stream) on the tensors' device.  `made`: tensors allocated for
+    the call (on the current stream), which a call on another stream keeps
+    alive until it has run."""
+    idx = device.index
+    handle = _raw_stream(idx)
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.cuda_stream != handle:
+            handle = stream.cuda_stream
+            for t in made:
+                if t is not None:
+                    t.record_stream(stream)
+    if idx == torch._C._cuda_getDevice():
+        code = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            yield s.cuda_stream
-
-
-def workspace(given, size, device):
-    """The caller's workspace, or a new one (second value: whether it is new), its address and its bytes."""
-    if given is None:
-        w = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
-        return w, True
-    need(given, "workspace", torch.uint8, None, device)
-    return given, False
+        with torch.cuda.device(idx):
+            code = fn(*args, handle)
+    if code:
+        raise _native.NatsError(code, where)

@@ -200,6 +200,7 @@ def __getattr__(name):
     if name == "lib":
         if _lib is None:
             _lib = _load()
+        globals()["lib"] = _lib  # found without this function from now on
         return _lib
     raise AttributeError(name)
 

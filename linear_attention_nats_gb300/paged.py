@@ -8,7 +8,6 @@ from typing import Optional
 import torch
 
 from . import _args, _native
-from ._native import RopeDims, check
 from .rope import _rotation
 
 
@@ -30,9 +29,9 @@ class PagedCache:
         if table.dim() != 2:
             raise ValueError("table must be [B, max_pages]")
         B, most = table.shape
-        dev = k_pages.device
+        dev = _args.cuda_device(k_pages, "k_pages")
         code = _args.dtype_code(k_pages, "k_pages")
-        pk = _args.need(k_pages, "k_pages")
+        pk = _args.need(k_pages, "k_pages", k_pages.dtype, None, dev)
         pv = _args.need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev)
         pt = _args.need(table, "table", torch.int32, None, dev)
         pl = _args.need(lens, "lens", torch.int32, (B,), dev)
@@ -91,8 +90,9 @@ def paged_append(cache: PagedCache, k, v, *, start=None, n_new=None, q=None, out
     dev, dt = cache.device, cache.dtype
     if (B, Hk, d) != (cache.B, cache.Hk, cache.d):
         raise ValueError(f"k must be [{cache.B}, {cache.Hk}, T, {cache.d}], got {tuple(k.shape)}")
-    pk, sk = _args.heads(k, "k", dt, k.shape, dev)
-    pv, sv = _args.heads(v, "v", dt, k.shape, dev)
+    ks = k.shape
+    pk, sk = _args.heads(k, "k", dt, ks, dev)
+    pv, sv = _args.heads(v, "v", dt, ks, dev)
     ps = _args.need(start, "start", torch.int32, (B,), dev)
     pn = _args.need(n_new, "n_new", torch.int32, (B,), dev)
     pwq, pwk = _args.need(w_q, "w_q", torch.float32, (d,), dev), _args.need(w_k, "w_k", torch.float32, (d,), dev)
@@ -100,19 +100,18 @@ def paged_append(cache: PagedCache, k, v, *, start=None, n_new=None, q=None, out
     Hq, made = 0, []
     pq = sq = poq = soq = None
     if q is not None:
-        if q.dim() != 4 or q.shape[0] != B or q.shape[2] != T or q.shape[3] != d:
-            raise ValueError(f"q must be [{B}, Hq, {T}, {d}], got {tuple(q.shape)}")
-        Hq = q.shape[1]
-        pq, sq = _args.heads(q, "q", dt, q.shape, dev)
+        qs = q.shape
+        if len(qs) != 4 or qs[0] != B or qs[2] != T or qs[3] != d:
+            raise ValueError(f"q must be [{B}, Hq, {T}, {d}], got {tuple(qs)}")
+        Hq = qs[1]
+        pq, sq = _args.heads(q, "q", dt, qs, dev)
         if out_q is None:
-            out_q = (torch.empty if n_new is None else torch.zeros)((B, Hq, T, d), dtype=dt, device=dev)
+            out_q = (torch.empty if n_new is None else torch.zeros)(qs, dtype=dt, device=dev)
             made.append(out_q)
-        poq, soq = _args.heads(out_q, "out_q", dt, q.shape, dev)
-        _args.distinct(out_q, "out_q")
-    dm = RopeDims(B, T, Hq, Hk, d, rot, int(interleaved), int(norm), cache._c.dtype, eps)
-    with _args.launch(dev, stream, made) as st:
-        check(_native.lib.nats_paged_append(cache._c, dm, pq, sq, pk, sk, pv, sv, pwq, pwk, pf, ps, pn, pp, pb, poq,
-                                            soq, st), "nats_paged_append")
+        poq, soq = _args.heads_out(out_q, "out_q", dt, qs, dev)
+    dm = _args.rope_dims(B, T, Hq, Hk, d, rot, interleaved, norm, cache._c.dtype, eps)
+    _args.call(_native.lib.nats_paged_append, "nats_paged_append", dev, stream, made, cache._c, dm, pq, sq, pk, sk, pv,
+               sv, pwq, pwk, pf, ps, pn, pp, pb, poq, soq)
     return out_q
 
 
@@ -124,35 +123,32 @@ def paged_decode(cache: PagedCache, q, *, scale: float = 0.0, accumulate: bool =
     accumulate adds each slot's attention weight, summed over the query heads
     of its key head, to cache.weight.  workspace: uint8 tensor of
     paged_workspace_size(cache, Hq=Hq, accumulate=accumulate) bytes, or None."""
-    dev, dt = cache.device, cache.dtype
-    if q.dim() != 3 or q.shape[0] != cache.B or q.shape[2] != cache.d:
-        raise ValueError(f"q must be [{cache.B}, Hq, {cache.d}], got {tuple(q.shape)}")
-    B, Hq, d = q.shape
-    pq = _args.need(q, "q", dt, None, dev, contiguous=False)
+    dev, dt, c = cache.device, cache.dtype, cache._c
+    qs = q.shape
+    if len(qs) != 3 or qs[0] != cache.B or qs[2] != cache.d:
+        raise ValueError(f"q must be [{cache.B}, Hq, {cache.d}], got {tuple(qs)}")
+    if q.dtype is not dt or q.device != dev:
+        _args._refuse(q, "q", dt, None, dev)
     qb, qh, qe = q.stride()
     if qe != 1 and q.numel() > 0:
         raise ValueError("q: the entries of a row must be contiguous")
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs a cache with weights")
-    made = []
+    made, Hq, lib = [], qs[1], _native.lib
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=dt, device=dev)
+        out = torch.empty(qs, dtype=dt, device=dev)
         made.append(out)
-        po = out.data_ptr()
-    else:
-        po = _args.need(out, "out", dt, q.shape, dev)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    made.append(lse)
+    po, lse, pl = _args.need(out, "out", dt, qs, dev), None, None
+    if return_lse:
+        lse = torch.empty(qs[:2], dtype=torch.float32, device=dev)
+        pl = lse.data_ptr()
+        made.append(lse)
     if workspace is None:
-        workspace, _ = _args.workspace(
-            None, _native.lib.nats_paged_decode_workspace_size(cache._c, Hq, int(accumulate)), dev)
+        workspace = torch.empty(lib.nats_paged_decode_workspace_size(c, Hq, accumulate), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    else:
-        _args.need(workspace, "workspace", torch.uint8, None, dev)
-    with _args.launch(dev, stream, made) as st:
-        check(_native.lib.nats_paged_decode(cache._c, Hq, scale, pq, qb, qh, po, None if lse is None else lse.data_ptr(),
-                                            int(accumulate), workspace.data_ptr(), workspace.numel(), st),
-              "nats_paged_decode")
+    pw = _args.need(workspace, "workspace", torch.uint8, None, dev)
+    _args.call(lib.nats_paged_decode, "nats_paged_decode", dev, stream, made, c, Hq, scale, q.data_ptr(), qb, qh, po, pl,
+               accumulate, pw, workspace.numel())
     return (out, lse) if return_lse else out
 
 
@@ -166,7 +162,7 @@ def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, s
     (keep, lengths) with keep int32 [B, Hk, budget], the kept slots, -1 behind
     the last.  The caller then puts out_table and the lengths into the cache
     and frees the old pages."""
-    dev = cache.device
+    dev, c, lib = cache.device, cache._c, _native.lib
     if cache.weight is None:
         raise ValueError("eviction needs a cache with weights")
     if out_table.dim() != 2 or out_table.shape[0] != cache.B:
@@ -177,17 +173,15 @@ def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, s
         lens_out = torch.empty((cache.B,), dtype=torch.int32, device=dev)
         made.append(lens_out)
     pl = _args.need(lens_out, "lens_out", torch.int32, (cache.B,), dev)
-    keep = None
+    keep, pk = None, None
     if return_keep:
         keep = torch.empty((cache.B, cache.Hk, max(budget, 0)), dtype=torch.int32, device=dev)
+        pk = keep.data_ptr()
         made.append(keep)
     if workspace is None:
-        workspace, _ = _args.workspace(None, _native.lib.nats_paged_evict_workspace_size(cache._c, budget), dev)
+        workspace = torch.empty(lib.nats_paged_evict_workspace_size(c, budget), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    else:
-        _args.need(workspace, "workspace", torch.uint8, None, dev)
-    with _args.launch(dev, stream, made) as st:
-        check(_native.lib.nats_paged_evict(cache._c, pt, out_table.shape[1], budget, recent, sinks, pl,
-                                           None if keep is None else keep.data_ptr(), workspace.data_ptr(),
-                                           workspace.numel(), st), "nats_paged_evict")
+    pw = _args.need(workspace, "workspace", torch.uint8, None, dev)
+    _args.call(lib.nats_paged_evict, "nats_paged_evict", dev, stream, made, c, pt, out_table.shape[1], budget, recent,
+               sinks, pl, pk, pw, workspace.numel())
     return (keep, lens_out) if return_keep else lens_out

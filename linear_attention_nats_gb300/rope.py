@@ -6,13 +6,11 @@ lie inside one projection's output, `qkv.view(B, L, 3, H, d)[:, :, 0].transpose(
 
 from __future__ import annotations
 
-import ctypes
 from typing import Optional
 
 import torch
 
 from . import _args, _native
-from ._native import RopeDims, check
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -22,20 +20,20 @@ def rope_inv_freq(rot: int, base: float = 10000.0, device="cuda") -> torch.Tenso
 
 def _rotation(inv_freq, positions, B, L, device):
     """rot, and the addresses / stride of the frequencies and positions."""
-    if inv_freq is None:
-        rot, pf = 0, None
-    else:
+    rot, pf, pp, pb = 0, None, None, 0
+    if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise ValueError(f"inv_freq must have shape (rot / 2,), got {tuple(inv_freq.shape)}")
         pf = _args.need(inv_freq, "inv_freq", torch.float64, None, device)
         rot = 2 * inv_freq.shape[0]
-    pp, pb = None, 0
     if positions is not None:
-        shape = (L,) if positions.dim() == 1 else (B, L)
-        pp = _args.need(positions, "positions", torch.int64, shape, device, contiguous=False)
-        if L > 1 and positions.stride(-1) != 1:
+        shape = (B, L) if positions.dim() == 2 else (L,)
+        if positions.dtype is not torch.int64 or positions.device != device or positions.shape != shape:
+            _args._refuse(positions, "positions", torch.int64, shape, device)
+        st = positions.stride()
+        if st[-1] != 1 and L > 1:
             raise ValueError("positions of a sequence must be contiguous")
-        pb = 0 if positions.dim() == 1 else positions.stride(0)
+        pp, pb = positions.data_ptr(), st[0] if len(st) == 2 else 0
     return rot, pf, pp, pb
 
 
@@ -58,29 +56,26 @@ def qk_norm_rope(q, k, w_q=None, w_k=None, inv_freq=None, positions=None, *, pos
     Returns (q', k') in the layer's contiguous [B, H, L, d], or in out_q, out_k
     (any strides but the last; the inputs themselves for in place)."""
     _check_pair(q, k)
-    B, Hq, L, d = q.shape
-    Hk = k.shape[1]
-    dev, dt = q.device, q.dtype
+    qs, ks = q.shape, k.shape
+    B, Hq, L, d = qs
+    dev, dt = _args.cuda_device(q, "q"), q.dtype
     code = _args.dtype_code(q, "q")
-    pq, sq = _args.heads(q, "q", dt, q.shape, dev)
-    pk, sk = _args.heads(k, "k", dt, k.shape, dev)
+    pq, sq = _args.heads(q, "q", dt, qs, dev)
+    pk, sk = _args.heads(k, "k", dt, ks, dev)
     pwq, pwk = _args.need(w_q, "w_q", torch.float32, (d,), dev), _args.need(w_k, "w_k", torch.float32, (d,), dev)
     rot, pf, pp, pb = _rotation(inv_freq, positions, B, L, dev)
     made = []
     if out_q is None:
-        out_q = torch.empty((B, Hq, L, d), dtype=dt, device=dev)
+        out_q = torch.empty(qs, dtype=dt, device=dev)
         made.append(out_q)
     if out_k is None:
-        out_k = torch.empty((B, Hk, L, d), dtype=dt, device=dev)
+        out_k = torch.empty(ks, dtype=dt, device=dev)
         made.append(out_k)
-    poq, soq = _args.heads(out_q, "out_q", dt, q.shape, dev)
-    pok, sok = _args.heads(out_k, "out_k", dt, k.shape, dev)
-    _args.distinct(out_q, "out_q")
-    _args.distinct(out_k, "out_k")
-    dm = RopeDims(B, L, Hq, Hk, d, rot, int(interleaved), int(norm), code, eps)
-    with _args.launch(dev, stream, made) as st:
-        check(_native.lib.nats_qk_norm_rope(dm, pq, sq, pk, sk, pwq, pwk, pf, pp, pb, pos0, poq, soq, pok, sok, st),
-              "nats_qk_norm_rope")
+    poq, soq = _args.heads_out(out_q, "out_q", dt, qs, dev)
+    pok, sok = _args.heads_out(out_k, "out_k", dt, ks, dev)
+    dm = _args.rope_dims(B, L, Hq, ks[1], d, rot, interleaved, norm, code, eps)
+    _args.call(_native.lib.nats_qk_norm_rope, "nats_qk_norm_rope", dev, stream, made, dm, pq, sq, pk, sk, pwq, pwk, pf,
+               pp, pb, pos0, poq, soq, pok, sok)
     return out_q, out_k
 
 
@@ -94,43 +89,42 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, inv_freq=None, po
     weight_grads and norm, dw_q, dw_k (fp32 [d]).  q, k and the other arguments
     are the forward's."""
     _check_pair(q, k)
-    B, Hq, L, d = q.shape
-    Hk = k.shape[1]
-    dev, dt, gt = q.device, q.dtype, dq_out.dtype
+    qs, ks = q.shape, k.shape
+    B, Hq, L, d = qs
+    dev, dt, gt = _args.cuda_device(q, "q"), q.dtype, dq_out.dtype
     code = _args.dtype_code(q, "q")
     gcode = _args.dtype_code(dq_out, "dq_out")
-    pq, sq = _args.heads(q, "q", dt, q.shape, dev)
-    pk, sk = _args.heads(k, "k", dt, k.shape, dev)
-    pgq, sgq = _args.heads(dq_out, "dq_out", gt, q.shape, dev)
-    pgk, sgk = _args.heads(dk_out, "dk_out", gt, k.shape, dev)
+    pq, sq = _args.heads(q, "q", dt, qs, dev)
+    pk, sk = _args.heads(k, "k", dt, ks, dev)
+    pgq, sgq = _args.heads(dq_out, "dq_out", gt, qs, dev)
+    pgk, sgk = _args.heads(dk_out, "dk_out", gt, ks, dev)
     pwq, pwk = _args.need(w_q, "w_q", torch.float32, (d,), dev), _args.need(w_k, "w_k", torch.float32, (d,), dev)
     rot, pf, pp, pb = _rotation(inv_freq, positions, B, L, dev)
     made = []
     if dq is None:
-        dq = torch.empty((B, Hq, L, d), dtype=dt if dk is None else dk.dtype, device=dev)
+        dq = torch.empty(qs, dtype=dt if dk is None else dk.dtype, device=dev)
         made.append(dq)
+    xt = dq.dtype
     if dk is None:
-        dk = torch.empty((B, Hk, L, d), dtype=dq.dtype, device=dev)
+        dk = torch.empty(ks, dtype=xt, device=dev)
         made.append(dk)
     xcode = _args.dtype_code(dq, "dq")
-    pdq, sdq = _args.heads(dq, "dq", dq.dtype, q.shape, dev)
-    pdk, sdk = _args.heads(dk, "dk", dq.dtype, k.shape, dev)
-    _args.distinct(dq, "dq")
-    _args.distinct(dk, "dk")
-    dm = RopeDims(B, L, Hq, Hk, d, rot, int(interleaved), int(norm), code, eps)
+    pdq, sdq = _args.heads_out(dq, "dq", xt, qs, dev)
+    pdk, sdk = _args.heads_out(dk, "dk", xt, ks, dev)
+    dm = _args.rope_dims(B, L, Hq, ks[1], d, rot, interleaved, norm, code, eps)
+    lib = _native.lib
     res = {"dq": dq, "dk": dk}
-    pws, nws, pdw = None, 0, (None, None)
+    pws, nws, pdw_q, pdw_k = None, 0, None, None
     if weight_grads and norm:
         dw = torch.empty((2, d), dtype=torch.float32, device=dev)
         res["dw_q"], res["dw_k"] = dw[0], dw[1]
-        pdw = (dw.data_ptr(), dw.data_ptr() + 4 * d)
-        ws, new = _args.workspace(workspace, _native.lib.nats_qk_norm_rope_bwd_workspace_size(dm), dev)
-        pws, nws = ws.data_ptr(), ws.numel()
+        pdw_q = dw.data_ptr()
+        pdw_k = pdw_q + 4 * d
         made.append(dw)
-        if new:
-            made.append(ws)
-    with _args.launch(dev, stream, made) as st:
-        check(_native.lib.nats_qk_norm_rope_bwd(dm, gcode, xcode, pgq, sgq, pgk, sgk, pq, sq, pk, sk, pwq, pwk, pf, pp,
-                                                pb, pos0, pdq, sdq, pdk, sdk, *pdw, pws, nws, st),
-              "nats_qk_norm_rope_bwd")
+        if workspace is None:
+            workspace = torch.empty(lib.nats_qk_norm_rope_bwd_workspace_size(dm), dtype=torch.uint8, device=dev)
+            made.append(workspace)
+        pws, nws = _args.need(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
+    _args.call(lib.nats_qk_norm_rope_bwd, "nats_qk_norm_rope_bwd", dev, stream, made, dm, gcode, xcode, pgq, sgq, pgk,
+               sgk, pq, sq, pk, sk, pwq, pwk, pf, pp, pb, pos0, pdq, sdq, pdk, sdk, pdw_q, pdw_k, pws, nws)
     return res
