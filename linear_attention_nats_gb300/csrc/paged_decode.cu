@@ -24,7 +24,7 @@ constexpr int kTile = 64;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSMs = 152;
-constexpr int kMaxCtas = kSMs * 4;
+constexpr int kMaxCtas = kSMs * 3;
 constexpr int kMaxHeads = 16;  // query heads of a unit, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -116,15 +116,6 @@ __device__ __forceinline__ Run my_run(const PagedView& pg, int U, long long* pre
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* o);
-template <>
-__device__ __forceinline__ void load8(const float* p, float* o) {
-  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
-  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
-  o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-}
-
 // e^(m - M) factors in base 2, with 0 for an empty part
 __device__ __forceinline__ float part_scale(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
 
@@ -164,104 +155,17 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const float* so
   }
 }
 
-// Eight entries of a row a lane, D / 8 lanes a row, fp32 arithmetic.
-template <typename T, int D, int GT>
-__global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
-  const int U = a.pg.Hk * a.ngroups;
-  const Run run = my_run(a.pg, U, a.prefix);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
-  long long cur = run.s, pre = run.pre;
-  int b = run.b0;
-  while (cur < run.e) {
-    const int n = a.pg.length(b), nt = tiles_of(n);
-    if (cur >= (pre + nt) * U) {
-      pre += nt;
-      ++b;
-      continue;
-    }
-    const long long local = cur - pre * U;
-    const int u = (int)(local / nt), t0 = (int)(local % nt);
-    const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
-    const int hk = u / a.ngroups, g0 = (u % a.ngroups) * GT;
-    const int heads = min(GT, a.G - g0), h0 = hk * a.G + g0;
-    float q[GT][8], o[GT][8], mx[GT], sum[GT];
-#pragma unroll
-    for (int g = 0; g < GT; ++g) {
-      mx[g] = -INFINITY, sum[g] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[g][i] = o[g][i] = 0.f;
-      if (g < heads) {
-        load8((const T*)a.q + b * a.q_b + (h0 + g) * a.q_h + 8 * l, q[g]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[g][i] *= a.scale2;
-      }
-    }
-    for (int t = t0; t < t1; ++t) {
-      const int j0 = t * kTile + warp * 16;
-      if (j0 >= n) break;
-      const int pg = a.pg.page_of(b, j0 / a.pg.page);
-      if (pg < 0 && lane == 0) *a.pg.err = 1;
-      const long long row0 = pg < 0 ? 0 : a.pg.row(pg, hk, j0 % a.pg.page);
-#pragma unroll 4
-      for (int st = 0; st < 16; st += RPW) {
-        const int j = j0 + st + sub;
-        const bool on = j < n && pg >= 0;
-        float k[8], v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = v[i] = 0.f;
-        if (on) {
-          load8((const T*)a.k + (row0 + st + sub) * D + 8 * l, k);
-          load8((const T*)a.v + (row0 + st + sub) * D + 8 * l, v);
-        }
-#pragma unroll
-        for (int g = 0; g < GT; ++g) {
-          float s = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s = fmaf(q[g][i], k[i], s);
-#pragma unroll
-          for (int x = LPR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-          if (!on) s = -INFINITY;
-          if (a.scores && l == 0 && j < n && g < heads)
-            a.scores[(((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G + g0 + g] = s;
-          const float mn = fmaxf(mx[g], s);
-          const float f = part_scale(mx[g], mn), p = s == -INFINITY ? 0.f : exp2f(s - mn);
-          mx[g] = mn;
-          sum[g] = sum[g] * f + p;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[g][i] = fmaf(o[g][i], f, p * v[i]);
-        }
-      }
-    }
-    // the rows of a warp, then its warps
-#pragma unroll
-    for (int g = 0; g < GT; ++g) {
-      float M = mx[g];
-#pragma unroll
-      for (int x = 16; x >= LPR; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-      const float f = part_scale(mx[g], M);
-      sum[g] *= f;
-#pragma unroll
-      for (int x = 16; x >= LPR; x >>= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float y = o[g][i] * f;
-#pragma unroll
-        for (int x = 16; x >= LPR; x >>= 1) y += __shfl_xor_sync(0xffffffffu, y, x);
-        if (sub == 0) so[(warp * GT + g) * D + 8 * l + i] = y;
-      }
-      if (lane == 0) sml[(warp * GT + g) * 2] = M, sml[(warp * GT + g) * 2 + 1] = sum[g];
-    }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == nt;
-    finish_unit<T, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
-    __syncthreads();
-    cur += t1 - t0;
-  }
-}
-
-// ------------------------------------------------ bf16: tensor-core products
+// ------------------------------------------------------ the two products
+//
+// Each warp takes 16 slots of every tile, on its own, and up to 8 NH heads of
+// a unit.  Both products run on the tensor cores with the slots or the
+// entries on the 16 rows of an instruction and the heads on its 8 columns,
+//   S^T [16 slots x 8 heads] += K Q^T,   O^T [16 entries x 8 heads] += V^T P^T,
+// so few heads waste little, and which entry (slot) carries which index of a
+// sum is free, so that every operand is a plain 16-byte load of a row and the
+// loop needs no shared memory.  Lane 4 g + c holds slots g and g + 8 of S^T
+// for heads 2 c, 2 c + 1, in
+//   s[0], s[1] (slot g), s[2], s[3] (slot g + 8).
 
 // Sixteen bytes of a page, read once: past L1.
 __device__ __forceinline__ uint4 ldg_once(const void* p) {
@@ -272,57 +176,208 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
   return u;
 }
 
-// c += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// bf16 rows, D entries.  K: the lane holds entries 32 y + 8 c .. + 7 of its two
+// slots for each block y, the same entries that it holds of head g's q.  V: it
+// holds entries 8 g .. + 7 (and 64 + 8 g .. + 7) of slots 2c, 2c + 1, 2c + 8,
+// 2c + 9; pairs of slots are packed with byte permutes.  P moves from S^T's
+// layout to P^T's by an 8 x 8 transpose and is carried as two bf16, high and
+// low part, so that its rounding (2^-8 each) does not add to the output's own.
+template <int D>
+struct Bf16 {
+  using T = __nv_bfloat16;
+  static constexpr int kD = D;
+  static constexpr int KB = D / 32, VS = D / 64, MT = D / 16;
+  struct Q { uint4 r[KB]; };
+  struct K { uint4 r[2][KB]; };
+  struct V { uint4 r[4][VS]; };
 
-// the transpose of an 8 x 8 matrix of 16-bit entries held two a lane
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
+  // c += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators
+  static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+  // the transpose of an 8 x 8 matrix of 16-bit entries held two a lane
+  static __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t*)&v;
+  }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *(const uint32_t*)&v;
-}
+  static __device__ __forceinline__ void load_q(Q& q, const T* p, bool on, int c) {
+#pragma unroll
+    for (int y = 0; y < KB; ++y) q.r[y] = on ? *(const uint4*)(p + 32 * y + 8 * c) : make_uint4(0, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void load_k(K& k, const T* p, int row, int g, int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int y = 0; y < KB; ++y)
+        k.r[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(p + (long long)(row + g + 8 * i) * D + 32 * y + 8 * c);
+  }
+  // (values of slots behind the sequence are zero: 0 x NaN would not be)
+  static __device__ __forceinline__ void load_v(V& v, const T* p, int row, int left, int g, int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+      for (int y = 0; y < VS; ++y)
+        v.r[i][y] = row < 0 || r >= left ? make_uint4(0, 0, 0, 0) : ldg_once(p + (long long)(row + r) * D + 64 * y + 8 * g);
+    }
+  }
+  static __device__ __forceinline__ void scores(float (&s)[4], const K& k, const Q& q) {
+#pragma unroll
+    for (int y = 0; y < KB; ++y) {
+      mma(s, k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y, q.r[y].x, q.r[y].y);
+      mma(s, k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w, q.r[y].z, q.r[y].w);
+    }
+  }
+  template <int NH>
+  static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int, int) {
+    uint32_t ph[NH][2], pl[NH][2];
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w = pack(p[x][2 * i], p[x][2 * i + 1]);
+        ph[x][i] = transpose8(w);
+        pl[x][i] = transpose8(pack(p[x][2 * i] - __uint_as_float(w << 16),
+                                   p[x][2 * i + 1] - __uint_as_float(w & 0xffff0000u)));
+      }
+#pragma unroll
+    for (int y = 0; y < MT; ++y) {
+      // rows g and g + 8 of tile y: entries 8g + y and 64 + 8g + y (D = 64: 8g + y and 8g + 4 + y)
+      const int yb = D == 128 ? y : y + 4, sb = VS - 1;
+      auto pair = [&](int s0, int e, int sg) {
+        const uint32_t *r0 = (const uint32_t*)&v.r[s0][sg], *r1 = (const uint32_t*)&v.r[s0 + 1][sg];
+        return __byte_perm(r0[e / 2], r1[e / 2], e % 2 ? 0x7632 : 0x5410);
+      };
+      const uint32_t a0 = pair(0, y, 0), a1 = pair(0, yb, sb), a2 = pair(2, y, 0), a3 = pair(2, yb, sb);
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+        mma(o[x][y], a0, a1, a2, a3, ph[x][0], ph[x][1]);
+        mma(o[x][y], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+      }
+    }
+  }
+  // the entry of row g (row g + 8) of tile y
+  static __device__ __forceinline__ int entry(int y, int g, int upper) {
+    return 8 * g + y + (upper ? (D == 128 ? 64 : 4) : 0);
+  }
+};
+
+// fp32 rows on the tf32 instructions, each factor as two (the upper 10 bits of
+// the significand, cut off, and what is left; the split-precision product of
+// Markidis et al., 2018): x y = x_h y_h + x_h y_l + x_l y_h to 2^-21.  K: the
+// lane holds entries 16 y + 4 c .. + 3 of its slots; V: entries 4 g + 32 y ..
+// + 3 of slots c, c + 4, c + 8, c + 12.  P reaches its layout by shuffles.
+template <int D>
+struct F32 {
+  using T = float;
+  static constexpr int kD = D;
+  static constexpr int KB = D / 16, VS = D / 32, MT = D / 16;
+  struct Q { float4 r[KB]; };
+  struct K { uint4 r[2][KB]; };
+  struct V { uint4 r[4][VS]; };
+
+  static __device__ __forceinline__ uint32_t high(uint32_t x) { return x & 0xffffe000u; }
+  static __device__ __forceinline__ uint32_t low(uint32_t x) {
+    return __float_as_uint(__uint_as_float(x) - __uint_as_float(high(x)));
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+  // c += A B in split precision, the small products first
+  static __device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = high(a[i]), l[i] = low(a[i]);
+    mma(c, l[0], l[1], l[2], l[3], high(b0), high(b1));
+    mma(c, h[0], h[1], h[2], h[3], low(b0), low(b1));
+    mma(c, h[0], h[1], h[2], h[3], high(b0), high(b1));
+  }
+
+  static __device__ __forceinline__ void load_q(Q& q, const T* p, bool on, int c) {
+#pragma unroll
+    for (int y = 0; y < KB; ++y) q.r[y] = on ? *(const float4*)(p + 16 * y + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  static __device__ __forceinline__ void load_k(K& k, const T* p, int row, int g, int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int y = 0; y < KB; ++y)
+        k.r[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(p + (long long)(row + g + 8 * i) * D + 16 * y + 4 * c);
+  }
+  static __device__ __forceinline__ void load_v(V& v, const T* p, int row, int left, int g, int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int y = 0; y < VS; ++y)
+        v.r[i][y] = row < 0 || c + 4 * i >= left ? make_uint4(0, 0, 0, 0)
+                                                 : ldg_once(p + (long long)(row + c + 4 * i) * D + 32 * y + 4 * g);
+  }
+  static __device__ __forceinline__ void scores(float (&s)[4], const K& k, const Q& q) {
+#pragma unroll
+    for (int y = 0; y < KB; ++y) {
+      const uint32_t a[4] = {k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y};
+      mma3(s, a, __float_as_uint(q.r[y].x), __float_as_uint(q.r[y].y));
+      const uint32_t b[4] = {k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w};
+      mma3(s, b, __float_as_uint(q.r[y].z), __float_as_uint(q.r[y].w));
+    }
+  }
+  template <int NH>
+  static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int g,
+                                                int c) {
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+      // slots c, c + 4, c + 8, c + 12 of head g: from the lanes with that slot (and 8 on) and the head's pair
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int src = 4 * (c + 4 * i) + g / 2;
+        const float e0 = __shfl_sync(0xffffffffu, p[x][0], src), e1 = __shfl_sync(0xffffffffu, p[x][1], src);
+        const float e2 = __shfl_sync(0xffffffffu, p[x][2], src), e3 = __shfl_sync(0xffffffffu, p[x][3], src);
+        b[i] = __float_as_uint(g % 2 ? e1 : e0), b[i + 2] = __float_as_uint(g % 2 ? e3 : e2);
+      }
+#pragma unroll
+      for (int y = 0; y < MT; ++y) {
+        // rows g and g + 8 of tile y: entry y % 4 of the lane's segments 2 (y / 4) and 2 (y / 4) + 1
+        auto at = [&](int slot, int seg) { return ((const uint32_t*)&v.r[slot][2 * (y / 4) + seg])[y % 4]; };
+        const uint32_t a[4] = {at(0, 0), at(0, 1), at(1, 0), at(1, 1)}, a2[4] = {at(2, 0), at(2, 1), at(3, 0), at(3, 1)};
+        mma3(o[x][y], a, b[0], b[1]);
+        mma3(o[x][y], a2, b[2], b[3]);
+      }
+    }
+  }
+  static __device__ __forceinline__ int entry(int y, int g, int upper) {
+    return 32 * (2 * (y / 4) + upper) + 4 * g + y % 4;
+  }
+};
 
 // how far a score may rise above the running maximum (in powers of two)
 // before the sums are rescaled: 2^8 leaves fp32 its full precision
 constexpr float kSlack = 8.f;
 
-// A unit of up to 8 NH heads.  Each warp takes 16 slots of every tile, on its
-// own: both products run with the slots or the entries on the rows of the
-// 16 x 8 x 16 instruction and the heads on its 8 columns,
-//   S^T [16 slots x 8 heads] += K [16 x 16 entries] Q^T,
-//   O^T [16 entries x 8 heads] += V^T [16 x 16 slots] P^T,
-// so few heads waste little, and which entry (slot) carries which index of a
-// sum is free, so that every operand is a plain 16-byte load of a row:
-//   K: lane 4g + c holds entries 32 x + 8 c .. + 7 of slots g and g + 8 for
-//      each 32-entry block x, the same entries that it holds of head g's q;
-//   V: it holds entries 8 g .. + 7 (and 64 + 8 g .. + 7) of slots 2c, 2c + 1,
-//      2c + 8, 2c + 9, and pairs of slots are packed with byte permutes.
-// No shared memory in the loop.  P moves from S^T's to P^T's layout by an
-// 8 x 8 transpose; it is carried as two bf16, high and low part, so that the
-// rounding of p (2^-8 each) does not double the output's own.
 // A tile's K registers are refilled for the next tile as soon as the scores
-// are done, V's when the values are: about 8 KB in flight a warp.
-template <int D, int NH>
-__global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(DecodeArgs a) {
-  constexpr int KB = D / 32;        // 32-entry blocks of a key row
-  constexpr int VS = D / 64;        // 8-entry segments of a value row a lane holds
-  constexpr int MT = D / 16;        // 16-entry tiles of O^T
-  constexpr int GT = 8 * NH;
+// are done, V's when the values are, page entries read two tiles ahead.
+template <class X, int NH, bool ACC, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) {
+  using T = typename X::T;
+  constexpr int D = X::kD, MT = X::MT, GT = 8 * NH;
+  cudaTriggerProgrammaticLaunchCompletion();  // the join may be launched; it waits for this kernel's end
   __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
   const int U = a.pg.Hk * a.ngroups;
   const Run run = my_run(a.pg, U, a.prefix);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const __nv_bfloat16 *kp = (const __nv_bfloat16*)a.k, *vp = (const __nv_bfloat16*)a.v;
+  const T *kp = (const T*)a.k, *vp = (const T*)a.v;
   long long cur = run.s, pre = run.pre;
   int b = run.b0;
   while (cur < run.e) {
@@ -337,16 +392,11 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(D
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
     const int hk = u / a.ngroups, g0 = (u % a.ngroups) * GT;
     const int heads = min(GT, a.G - g0), h0 = hk * a.G + g0;
-    uint4 q[NH][KB];
+    typename X::Q q[NH];
     float o[NH][MT][4], mx[NH][2], sum[NH][2];
 #pragma unroll
     for (int x = 0; x < NH; ++x) {
-#pragma unroll
-      for (int y = 0; y < KB; ++y) {
-        q[x][y] = make_uint4(0, 0, 0, 0);
-        if (8 * x + g < heads)
-          q[x][y] = *(const uint4*)((const __nv_bfloat16*)a.q + b * a.q_b + (h0 + 8 * x + g) * a.q_h + 32 * y + 8 * c);
-      }
+      X::load_q(q[x], (const T*)a.q + b * a.q_b + (h0 + 8 * x + g) * a.q_h, 8 * x + g < heads, c);
 #pragma unroll
       for (int y = 0; y < MT; ++y)
 #pragma unroll
@@ -354,9 +404,8 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(D
       mx[x][0] = mx[x][1] = -INFINITY;
       sum[x][0] = sum[x][1] = 0.f;
     }
-    uint4 k[2][KB], v[4][VS];
     // row of this warp's first slot in tile t, or -1: past the end or without a page
-    auto first_row = [&](int t) -> long long {
+    auto first_row = [&](int t) -> int {
       const int j0 = t * kTile + warp * 16;
       if (t >= t1 || j0 >= n) return -1;
       const int pg = a.pg.page_of(b, j0 / a.pg.page);
@@ -364,50 +413,30 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(D
         if (lane == 0) *a.pg.err = 1;
         return -1;
       }
-      return a.pg.row(pg, hk, j0 % a.pg.page);
+      return (int)a.pg.row(pg, hk, j0 % a.pg.page);
     };
-    auto load_k = [&](long long row) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int y = 0; y < KB; ++y)
-          k[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(kp + (row + g + 8 * i) * D + 32 * y + 8 * c);
-    };
-    // values of slots behind the sequence are zero: 0 x NaN would not be
-    auto load_v = [&](long long row, int left) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-        for (int y = 0; y < VS; ++y)
-          v[i][y] = row < 0 || r >= left ? make_uint4(0, 0, 0, 0) : ldg_once(vp + (row + r) * D + 64 * y + 8 * g);
-      }
-    };
-    long long row = first_row(t0), next = first_row(t0 + 1);
-    load_k(row);
-    load_v(row, n - t0 * kTile - warp * 16);
+    typename X::K k;
+    typename X::V v;
+    int row = first_row(t0), next = first_row(t0 + 1);
+    X::load_k(k, kp, row, g, c);
+    X::load_v(v, vp, row, n - t0 * kTile - warp * 16, g, c);
     for (int t = t0; t < t1; ++t) {
       const int j0 = t * kTile + warp * 16;
-      const long long after = first_row(t + 2);
+      const int after = first_row(t + 2);
       float s[NH][4];
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
         s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-#pragma unroll
-        for (int y = 0; y < KB; ++y) {
-          mma16816(s[x], k[0][y].x, k[1][y].x, k[0][y].y, k[1][y].y, q[x][y].x, q[x][y].y);
-          mma16816(s[x], k[0][y].z, k[1][y].z, k[0][y].w, k[1][y].w, q[x][y].z, q[x][y].w);
-        }
+        X::scores(s[x], k, q[x]);
       }
-      load_k(next);
+      X::load_k(k, kp, next, g, c);
       const bool lo = row >= 0 && j0 + g < n, hi = row >= 0 && j0 + g + 8 < n;
-      uint32_t ph[NH][2], pl[NH][2];
       bool rises = false;
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[x][i] = (i < 2 ? lo : hi) ? s[x][i] * a.scale2 : -INFINITY;
-        if (a.scores) {
+        if (ACC) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + g + 8 * (i >> 1), h = 8 * x + 2 * c + (i & 1);
@@ -434,38 +463,15 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(D
           }
       }
 #pragma unroll
-      for (int x = 0; x < NH; ++x) {
+      for (int x = 0; x < NH; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // (a head without a slot yet has no maximum to subtract: its scores are all -inf)
           s[x][i] = s[x][i] == -INFINITY ? 0.f : exp2f(s[x][i] - mx[x][i & 1]);
           sum[x][i & 1] += s[x][i];
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w = pack_bf16(s[x][2 * i], s[x][2 * i + 1]);
-          const float l0 = s[x][2 * i] - __uint_as_float(w << 16), l1 = s[x][2 * i + 1] - __uint_as_float(w & 0xffff0000u);
-          ph[x][i] = transpose8(w);
-          pl[x][i] = transpose8(pack_bf16(l0, l1));
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < MT; ++y) {
-        // rows g and g + 8 of tile y: entries 8g + y and 64 + 8g + y (D = 64: 8g + y and 8g + 4 + y)
-        const int ya = y, sa = 0, yb = D == 128 ? y : y + 4, sb = D == 128 ? VS - 1 : 0;
-        auto pair = [&](int s0, int e, int sg) {
-          const uint32_t* r0 = (const uint32_t*)&v[s0][sg];
-          const uint32_t* r1 = (const uint32_t*)&v[s0 + 1][sg];
-          return __byte_perm(r0[e / 2], r1[e / 2], e % 2 ? 0x7632 : 0x5410);
-        };
-        const uint32_t a0 = pair(0, ya, sa), a1 = pair(0, yb, sb), a2 = pair(2, ya, sa), a3 = pair(2, yb, sb);
-#pragma unroll
-        for (int x = 0; x < NH; ++x) {
-          mma16816(o[x][y], a0, a1, a2, a3, ph[x][0], ph[x][1]);
-          mma16816(o[x][y], a0, a1, a2, a3, pl[x][0], pl[x][1]);
-        }
-      }
-      load_v(next, n - j0 - kTile);
+      X::template values<NH>(o, v, s, g, c);
+      X::load_v(v, vp, next, n - j0 - kTile, g, c);
       row = next;
       next = after;
     }
@@ -477,28 +483,38 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_mma_kernel(D
         for (int z = 4; z < 32; z <<= 1) sum[x][i] += __shfl_xor_sync(0xffffffffu, sum[x][i], z);
         const int h = 8 * x + 2 * c + i;
         if (g == 0) sml[(warp * GT + h) * 2] = mx[x][i], sml[(warp * GT + h) * 2 + 1] = sum[x][i];
+        float* at = so + (warp * GT + h) * D;
 #pragma unroll
         for (int y = 0; y < MT; ++y) {
-          float* at = so + (warp * GT + h) * D + 8 * g + y;
-          at[0] = o[x][y][i];
-          at[D == 128 ? 64 : 4] = o[x][y][i + 2];
+          at[X::entry(y, g, 0)] = o[x][y][i];
+          at[X::entry(y, g, 1)] = o[x][y][i + 2];
         }
       }
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    finish_unit<__nv_bfloat16, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
+    finish_unit<T, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
     __syncthreads();
     cur += t1 - t0;
   }
 }
 
+// a * b / c for 0 <= a, b and 0 < c, 32-bit where the product allows
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+  const long long ab = a * b;
+  return (ab | c) >> 32 ? ab / c : (long long)((uint32_t)ab / (uint32_t)c);
+}
 // The CTA whose run holds tile x of the line (the run of CTA i of n is
 // [i T / n, (i + 1) T / n)).
-__device__ __forceinline__ int cta_of(long long x, long long T, int n) { return (int)(((x + 1) * n - 1) / T); }
+__device__ __forceinline__ int cta_of(long long x, long long T, int n) {
+  const long long y = (x + 1) * n - 1;
+  return (y | T) >> 32 ? (int)(y / T) : (int)((uint32_t)y / (uint32_t)T);
+}
 
 // A warp per (sequence, query head): joins the partials of a unit that lies
-// in more than one run, and writes the rows of empty sequences.
+// in more than one run, and writes the rows of empty sequences.  Latency is
+// all it costs: the lanes read the partials' maxima and sums side by side,
+// then every lane its entries of all of them.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(DecodeArgs a, int ctas) {
   constexpr int E = D / 32;
@@ -506,29 +522,42 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(DecodeArgs a, int
   const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= (long long)a.pg.B * a.Hq) return;
   const int b = (int)(i / a.Hq), h = (int)(i % a.Hq);
-  const long long pre = a.prefix[b], nt = a.prefix[b + 1] - pre, total = a.prefix[a.pg.B];
+  const int hk = h / a.G, g = (h % a.G) % a.GT, u = hk * a.ngroups + (h % a.G) / a.GT;
   const int U = a.pg.Hk * a.ngroups;
+  cudaGridDependencySynchronize();
+  const long long pre = a.prefix[b], nt = a.prefix[b + 1] - pre, total = a.prefix[a.pg.B];
   float o[E], M = -INFINITY, l = 0.f;
 #pragma unroll
   for (int x = 0; x < E; ++x) o[x] = 0.f;
   if (nt > 0) {
-    const int hk = h / a.G, g = (h % a.G) % a.GT, u = hk * a.ngroups + (h % a.G) / a.GT;
     const long long x0 = pre * U + u * nt, T_ = total * U;
     ctas = ctas_used(T_, ctas);
     const int c0 = cta_of(x0, T_, ctas), c1 = cta_of(x0 + nt - 1, T_, ctas);
     if (c0 == c1) return;  // written by its CTA
     // a CTA whose run begins in the unit (or before it with the unit as its first) used slot 0
-    const long long first = 2LL * c0 + (T_ * c0 / ctas == x0 ? 0 : 1);
-    for (int c = c0; c <= c1; ++c) {
-      const long long slot = c == c0 ? first : 2LL * c;
-      M = fmaxf(M, a.part_ml[(slot * a.GT + g) * 2]);
+    const long long first = 2LL * c0 + (mul_div(T_, c0, ctas) == x0 ? 0 : 1);
+    auto slot_of = [&](int c) { return (c == c0 ? first : 2LL * c) * a.GT + g; };
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float2 ml = *(const float2*)(a.part_ml + 2 * slot_of(c));
+      const float m = fmaxf(M, ml.x);
+      l = l * part_scale(M, m) + ml.y * part_scale(ml.x, m);
+      M = m;
     }
+    float m = warp_max(M);
+    l = warp_sum(l * part_scale(M, m));
+    M = m;
+#pragma unroll 8
     for (int c = c0; c <= c1; ++c) {
-      const long long slot = c == c0 ? first : 2LL * c;
-      const float f = part_scale(a.part_ml[(slot * a.GT + g) * 2], M);
-      l += f * a.part_ml[(slot * a.GT + g) * 2 + 1];
-#pragma unroll
-      for (int x = 0; x < E; ++x) o[x] += f * a.part_o[(slot * a.GT + g) * D + lane * E + x];
+      const long long s = slot_of(c);
+      const float f = part_scale(a.part_ml[2 * s], M);
+      const float* p = a.part_o + s * D + lane * E;
+      if (E == 4) {
+        const float4 v = *(const float4*)p;
+        o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
+      } else {
+        const float2 v = *(const float2*)p;
+        o[0] += f * v.x, o[1] += f * v.y;
+      }
     }
   }
 #pragma unroll
@@ -540,10 +569,13 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(DecodeArgs a, int
   }
 }
 
-// weight[slot] += sum over the group's heads of 2^(score - lse): every slot
-// has one thread, so nothing is summed in an order that varies.
+// weight[slot] += sum over the group's heads of 2^(score - lse): a thread
+// takes four slots (of one page, their scores contiguous), so nothing is
+// summed in an order that varies.  G > 0: that many heads, else a.G.
+template <int G>
 __global__ void __launch_bounds__(kThreads) decode_weight_kernel(DecodeArgs a) {
-  const int U = a.pg.Hk;
+  cudaGridDependencySynchronize();
+  const int U = a.pg.Hk, heads = G ? G : a.G;
   const Run run = my_run(a.pg, U, nullptr);
   long long cur = run.s, pre = run.pre;
   int b = run.b0;
@@ -557,15 +589,35 @@ __global__ void __launch_bounds__(kThreads) decode_weight_kernel(DecodeArgs a) {
     const long long local = cur - pre * U;
     const int hk = (int)(local / nt), t0 = (int)(local % nt);
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
-    const float* lse = a.lse_ws + (long long)b * a.Hq + hk * a.G;
-    for (int j = t0 * kTile + threadIdx.x; j < min(n, t1 * kTile); j += kThreads) {
+    const float* lse = a.lse_ws + (long long)b * a.Hq + hk * heads;
+    float ls[G ? G : 1];
+#pragma unroll
+    for (int g = 0; g < G; ++g) ls[g] = lse[g];
+    const float* scores = a.scores + ((long long)b * a.pg.Hk + hk) * a.pg.cap() * heads;
+    for (int j = t0 * kTile + 4 * threadIdx.x; j < min(n, t1 * kTile); j += 4 * kThreads) {
       const int pg = a.pg.page_of(b, j / a.pg.page);
       if (pg < 0) continue;
-      const float* s = a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G;
-      float w = 0.f;
-      for (int g = 0; g < a.G; ++g) w += s[g] == -INFINITY ? 0.f : exp2f(s[g] - lse[g]);
+      float w[4] = {0.f, 0.f, 0.f, 0.f};
+      const float4* s4 = (const float4*)(scores + (long long)j * heads);
+      auto add = [&](float (&w)[4], float s, int e) {  // the e-th of the four slots' scores
+        const int k = e / heads;
+        const float lg = G ? ls[e % (G ? G : 1)] : lse[e % heads];
+        const float x = s == -INFINITY ? 0.f : exp2f(s - lg);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i == k) w[i] += x;
+      };
+#pragma unroll
+      for (int i = 0; i < (G ? G : 1); ++i)
+        for (int ii = i; ii < heads; ii += G ? G : 1) {
+          const float4 s = s4[ii];
+          add(w, s.x, 4 * ii), add(w, s.y, 4 * ii + 1), add(w, s.z, 4 * ii + 2), add(w, s.w, 4 * ii + 3);
+        }
       float* at = a.weight + a.pg.row(pg, hk, j % a.pg.page);
-      *at += w;
+      const float4 was = *(const float4*)at;
+      // (scores behind the sequence were not written)
+      *(float4*)at = make_float4(was.x + w[0], j + 1 < n ? was.y + w[1] : was.y, j + 2 < n ? was.z + w[2] : was.z,
+                                 j + 3 < n ? was.w + w[3] : was.w);
     }
     cur += t1 - t0;
   }
@@ -595,48 +647,64 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
   const nats_status s = check_cache(c);
   if (s != NATS_OK) return s;
   if (Hq < 0 || Hq % c->Hk != 0) return NATS_ERR_SHAPE;
-  if ((long long)c->B * Hq > (1LL << 31) - 1) return NATS_ERR_UNSUPPORTED;
+  // rows of a pool and of the batch's queries are 32-bit
+  if ((long long)c->B * Hq > (1LL << 31) - 1 || (double)c->n_pages * c->Hk * c->page > 2147483647.0)
+    return NATS_ERR_UNSUPPORTED;
   if (accumulate && (double)c->B * Hq * c->max_pages * c->page > 1099511627776.0) return NATS_ERR_UNSUPPORTED;
   return NATS_OK;
 }
 
-// fp32: units of up to four heads on the lanes.  bf16: eight heads a unit on
-// the tensor cores, sixteen where a group has more than eight (two products'
-// worth of registers, but the rows are read once).
+// A kernel that starts while the one before it in the stream still runs, and
+// waits for it (to end) itself: its launch is then off the path.
+template <class... P, class... A>
+cudaError_t after(void (*kernel)(P...), unsigned grid, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Units of eight heads; bf16 groups of more than eight in units of sixteen,
+// whose rows are then read once (fp32 has not the registers: their second
+// reading comes from L2).
 template <int D>
 cudaError_t launch(DecodeArgs& a, int dtype, cudaStream_t st) {
-  int ctas;
-  if (dtype == NATS_BF16) {
-    a.GT = a.G <= 8 ? 8 : 16;
-    a.ngroups = (a.G + a.GT - 1) / a.GT;
-    ctas = kSMs * (a.GT == 8 ? 3 : 2);
-    if (a.GT == 8)
-      decode_mma_kernel<D, 1><<<ctas, kThreads, 0, st>>>(a);
-    else
-      decode_mma_kernel<D, 2><<<ctas, kThreads, 0, st>>>(a);
-  } else {
-    ctas = kSMs * 3;
-    a.GT = a.G == 1 ? 1 : a.G == 2 ? 2 : 4;
-    a.ngroups = (a.G + a.GT - 1) / a.GT;
-    if (a.GT == 1)
-      decode_simt_kernel<float, D, 1><<<ctas, kThreads, 0, st>>>(a);
-    else if (a.GT == 2)
-      decode_simt_kernel<float, D, 2><<<ctas, kThreads, 0, st>>>(a);
-    else
-      decode_simt_kernel<float, D, 4><<<ctas, kThreads, 0, st>>>(a);
-  }
+  const bool wide = dtype == NATS_BF16 && a.G > 8;
+  a.GT = wide ? 16 : 8;
+  a.ngroups = (a.G + a.GT - 1) / a.GT;
+  const int per_sm = dtype == NATS_BF16 && !wide ? 3 : 2, ctas = kSMs * per_sm;
+  const bool acc = a.scores != nullptr;
+#define NATS_DECODE(X, NH, BLOCKS)                                                 \
+  (acc ? decode_kernel<X, NH, true, BLOCKS><<<ctas, kThreads, 0, st>>>(a)          \
+       : decode_kernel<X, NH, false, BLOCKS><<<ctas, kThreads, 0, st>>>(a))
+  if (dtype != NATS_BF16)
+    NATS_DECODE(F32<D>, 1, 2);
+  else if (wide)
+    NATS_DECODE(Bf16<D>, 2, 2);
+  else
+    NATS_DECODE(Bf16<D>, 1, 3);
+#undef NATS_DECODE
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.pg.B * a.Hq;
   const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
-  if (dtype == NATS_BF16)
-    decode_join_kernel<__nv_bfloat16, D><<<grid, kThreads, 0, st>>>(a, ctas);
-  else
-    decode_join_kernel<float, D><<<grid, kThreads, 0, st>>>(a, ctas);
-  e = cudaGetLastError();
+  e = dtype == NATS_BF16 ? after(decode_join_kernel<__nv_bfloat16, D>, grid, st, a, ctas)
+                         : after(decode_join_kernel<float, D>, grid, st, a, ctas);
   if (e != cudaSuccess || !a.scores) return e;
-  decode_weight_kernel<<<kSMs * 8, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const unsigned wide_grid = kSMs * 8;
+  switch (a.G) {
+    case 1: return after(decode_weight_kernel<1>, wide_grid, st, a);
+    case 2: return after(decode_weight_kernel<2>, wide_grid, st, a);
+    case 4: return after(decode_weight_kernel<4>, wide_grid, st, a);
+    case 8: return after(decode_weight_kernel<8>, wide_grid, st, a);
+    default: return after(decode_weight_kernel<0>, wide_grid, st, a);
+  }
 }
 
 }  // namespace
