@@ -11,7 +11,7 @@
 // A run that covers a pair's tiles from first to last writes its output; the
 // others leave (max, sum, weighted values) in the workspace, two slots a CTA
 // (a run begins at most one pair that it does not finish and ends at most one
-// that it did not begin), and decode_join_kernel adds them up in order.
+// that it did not begin), and decode_finish_kernel adds them up in order.
 #include <cmath>
 
 #include "kernels.h"
@@ -372,7 +372,7 @@ template <class X, int NH, bool ACC, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) {
   using T = typename X::T;
   constexpr int D = X::kD, MT = X::MT, GT = 8 * NH;
-  cudaTriggerProgrammaticLaunchCompletion();  // the join may be launched; it waits for this kernel's end
+  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel may be launched; it waits for this one's end
   __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
   const int U = a.pg.Hk * a.ngroups;
   const Run run = my_run(a.pg, U, a.prefix);
@@ -511,115 +511,160 @@ __device__ __forceinline__ int cta_of(long long x, long long T, int n) {
   return (y | T) >> 32 ? (int)(y / T) : (int)((uint32_t)y / (uint32_t)T);
 }
 
-// A warp per (sequence, query head): joins the partials of a unit that lies
-// in more than one run, and writes the rows of empty sequences.  Latency is
-// all it costs: the lanes read the partials' maxima and sums side by side,
-// then every lane its entries of all of them.
+// The partials of a unit that lies in more than one run: CTAs c0 .. c1, the
+// first one's slot; `one`: its only CTA has written the result itself.
+struct Parts {
+  int c0, c1;
+  long long first;
+  bool one;
+  __device__ __forceinline__ long long slot(int c) const { return c == c0 ? first : 2LL * c; }
+};
+__device__ __forceinline__ Parts parts_of(long long pre, long long nt, long long total, int u, int U, int grid) {
+  const long long x0 = pre * U + u * nt, T = total * U;
+  const int n = ctas_used(T, grid);
+  Parts p;
+  p.c0 = cta_of(x0, T, n);
+  p.c1 = cta_of(x0 + nt - 1, T, n);
+  p.one = p.c0 == p.c1;
+  // a CTA whose run begins in the unit (or before it with the unit as its first) used slot 0
+  p.first = 2LL * p.c0 + (mul_div(T, p.c0, n) == x0 ? 0 : 1);
+  return p;
+}
+// One warp: maximum and sum of head g's partials, the lanes side by side.
+__device__ __forceinline__ void join_sums(const DecodeArgs& a, const Parts& p, int g, float& M, float& l) {
+  const int lane = threadIdx.x & 31;
+  M = -INFINITY, l = 0.f;
+  for (int c = p.c0 + lane; c <= p.c1; c += 32) {
+    const float2 ml = *(const float2*)(a.part_ml + 2 * (p.slot(c) * a.GT + g));
+    const float m = fmaxf(M, ml.x);
+    l = l * part_scale(M, m) + ml.y * part_scale(ml.x, m);
+    M = m;
+  }
+  const float m = warp_max(M);
+  l = warp_sum(l * part_scale(M, m));
+  M = m;
+}
+__device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : M + log2f(l); }
+
+// Row i = (sequence, query head), one warp: joins the unit's partials, or
+// writes the row of an empty sequence.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(DecodeArgs a, int ctas) {
+__device__ __forceinline__ void join_row(const DecodeArgs& a, int grid, long long i) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= (long long)a.pg.B * a.Hq) return;
   const int b = (int)(i / a.Hq), h = (int)(i % a.Hq);
   const int hk = h / a.G, g = (h % a.G) % a.GT, u = hk * a.ngroups + (h % a.G) / a.GT;
-  const int U = a.pg.Hk * a.ngroups;
-  cudaGridDependencySynchronize();
-  const long long pre = a.prefix[b], nt = a.prefix[b + 1] - pre, total = a.prefix[a.pg.B];
+  const long long pre = a.prefix[b], nt = a.prefix[b + 1] - pre;
   float o[E], M = -INFINITY, l = 0.f;
 #pragma unroll
   for (int x = 0; x < E; ++x) o[x] = 0.f;
   if (nt > 0) {
-    const long long x0 = pre * U + u * nt, T_ = total * U;
-    ctas = ctas_used(T_, ctas);
-    const int c0 = cta_of(x0, T_, ctas), c1 = cta_of(x0 + nt - 1, T_, ctas);
-    if (c0 == c1) return;  // written by its CTA
-    // a CTA whose run begins in the unit (or before it with the unit as its first) used slot 0
-    const long long first = 2LL * c0 + (mul_div(T_, c0, ctas) == x0 ? 0 : 1);
-    auto slot_of = [&](int c) { return (c == c0 ? first : 2LL * c) * a.GT + g; };
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2 ml = *(const float2*)(a.part_ml + 2 * slot_of(c));
-      const float m = fmaxf(M, ml.x);
-      l = l * part_scale(M, m) + ml.y * part_scale(ml.x, m);
-      M = m;
-    }
-    float m = warp_max(M);
-    l = warp_sum(l * part_scale(M, m));
-    M = m;
+    const Parts p = parts_of(pre, nt, a.prefix[a.pg.B], u, a.pg.Hk * a.ngroups, grid);
+    if (p.one) return;
+    join_sums(a, p, g, M, l);
 #pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const long long s = slot_of(c);
+    for (int c = p.c0; c <= p.c1; ++c) {
+      const long long s = p.slot(c) * a.GT + g;
       const float f = part_scale(a.part_ml[2 * s], M);
-      const float* p = a.part_o + s * D + lane * E;
+      const float* at = a.part_o + s * D + lane * E;
       if (E == 4) {
-        const float4 v = *(const float4*)p;
+        const float4 v = *(const float4*)at;
         o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
       } else {
-        const float2 v = *(const float2*)p;
+        const float2 v = *(const float2*)at;
         o[0] += f * v.x, o[1] += f * v.y;
       }
     }
   }
 #pragma unroll
   for (int x = 0; x < E; ++x) ((T*)a.out)[i * D + lane * E + x] = from_f32<T>(l == 0.f ? 0.f : o[x] / l);
-  if (lane == 0) {
-    const float v = l == 0.f ? -INFINITY : M + log2f(l);
-    a.lse_ws[i] = v;
-    if (a.lse) a.lse[i] = v;
-  }
+  if (a.lse && lane == 0) a.lse[i] = lse_of(M, l);
 }
 
-// weight[slot] += sum over the group's heads of 2^(score - lse): a thread
-// takes four slots (of one page, their scores contiguous), so nothing is
-// summed in an order that varies.  G > 0: that many heads, else a.G.
-template <int G>
-__global__ void __launch_bounds__(kThreads) decode_weight_kernel(DecodeArgs a) {
-  cudaGridDependencySynchronize();
-  const int U = a.pg.Hk, heads = G ? G : a.G;
-  const Run run = my_run(a.pg, U, nullptr);
-  long long cur = run.s, pre = run.pre;
-  int b = run.b0;
-  while (cur < run.e) {
-    const int n = a.pg.length(b), nt = tiles_of(n);
-    if (cur >= (pre + nt) * U) {
-      pre += nt;
+// Part `idx` of `count` of the tile line: weight[slot] += sum over the group's
+// heads of 2^(score - lse), the lse from the partials again (so this need not
+// wait for the joined rows).  A thread a slot: nothing is summed in an order
+// that varies.
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int grid, int idx, int count) {
+  extern __shared__ float lse[];  // [G]
+  __shared__ int found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hk = a.pg.Hk, G = a.G;
+  const long long total = a.prefix[a.pg.B], T = total * Hk;
+  const int used = ctas_used(T, count);
+  if (idx >= used) return;
+  const long long s = T * idx / used, e = T * (idx + 1) / used;
+  for (int b = tid; b < a.pg.B; b += kThreads)
+    if (a.prefix[b] * Hk <= s && s < a.prefix[b + 1] * Hk) found = b;
+  __syncthreads();
+  int b = found;
+  for (long long cur = s; cur < e;) {
+    const long long pre = a.prefix[b], nt = a.prefix[b + 1] - pre;
+    if (cur >= (pre + nt) * Hk) {
       ++b;
       continue;
     }
-    const long long local = cur - pre * U;
-    const int hk = (int)(local / nt), t0 = (int)(local % nt);
-    const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
-    const float* lse = a.lse_ws + (long long)b * a.Hq + hk * heads;
-    float ls[G ? G : 1];
-#pragma unroll
-    for (int g = 0; g < G; ++g) ls[g] = lse[g];
-    const float* scores = a.scores + ((long long)b * a.pg.Hk + hk) * a.pg.cap() * heads;
-    for (int j = t0 * kTile + 4 * threadIdx.x; j < min(n, t1 * kTile); j += 4 * kThreads) {
-      const int pg = a.pg.page_of(b, j / a.pg.page);
-      if (pg < 0) continue;
-      float w[4] = {0.f, 0.f, 0.f, 0.f};
-      const float4* s4 = (const float4*)(scores + (long long)j * heads);
-      auto add = [&](float (&w)[4], float s, int e) {  // the e-th of the four slots' scores
-        const int k = e / heads;
-        const float lg = G ? ls[e % (G ? G : 1)] : lse[e % heads];
-        const float x = s == -INFINITY ? 0.f : exp2f(s - lg);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i == k) w[i] += x;
-      };
-#pragma unroll
-      for (int i = 0; i < (G ? G : 1); ++i)
-        for (int ii = i; ii < heads; ii += G ? G : 1) {
-          const float4 s = s4[ii];
-          add(w, s.x, 4 * ii), add(w, s.y, 4 * ii + 1), add(w, s.z, 4 * ii + 2), add(w, s.w, 4 * ii + 3);
-        }
-      float* at = a.weight + a.pg.row(pg, hk, j % a.pg.page);
-      const float4 was = *(const float4*)at;
-      // (scores behind the sequence were not written)
-      *(float4*)at = make_float4(was.x + w[0], j + 1 < n ? was.y + w[1] : was.y, j + 2 < n ? was.z + w[2] : was.z,
-                                 j + 3 < n ? was.w + w[3] : was.w);
+    const long long local = cur - pre * Hk;
+    const int hk = (int)(local / nt), t0 = (int)(local % nt), t1 = (int)min(nt, t0 + (e - cur));
+    const int n = a.pg.length(b);
+    for (int g = warp; g < G; g += kWarps) {
+      const Parts p = parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, grid);
+      float M, l;
+      if (!p.one) join_sums(a, p, g % a.GT, M, l);
+      if (lane == 0) lse[g] = p.one ? a.lse_ws[(long long)b * a.Hq + hk * G + g] : lse_of(M, l);
     }
+    __syncthreads();
+    const float* scores = a.scores + ((long long)b * Hk + hk) * a.pg.cap() * G;
+    const int end = min(n, t1 * kTile);
+    constexpr int kSlots = 4;  // a thread's slots in flight
+    for (int j = t0 * kTile + tid; j < end; j += kSlots * kThreads) {
+      float w[kSlots];
+      const float* x[kSlots];
+      float* at[kSlots];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        const int ji = j + i * kThreads;
+        const int pg = ji < end ? a.pg.page_of(b, ji / a.pg.page) : -1;
+        at[i] = pg < 0 ? nullptr : a.weight + a.pg.row(pg, hk, ji % a.pg.page);
+        x[i] = scores + (long long)min(ji, end - 1) * G;
+        w[i] = 0.f;
+      }
+      auto add = [&](int i, float v, int g) { w[i] += v == -INFINITY ? 0.f : exp2f(v - lse[g]); };
+      if (G % 4 == 0) {
+        for (int g = 0; g < G; g += 4) {
+          float4 v[kSlots];
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) v[i] = __ldg((const float4*)(x[i] + g));
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) add(i, v[i].x, g), add(i, v[i].y, g + 1), add(i, v[i].z, g + 2), add(i, v[i].w, g + 3);
+        }
+      } else {
+        for (int g = 0; g < G; ++g) {
+          float v[kSlots];
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) v[i] = __ldg(x[i] + g);
+#pragma unroll
+          for (int i = 0; i < kSlots; ++i) add(i, v[i], g);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (at[i]) *at[i] += w[i];
+    }
+    __syncthreads();
     cur += t1 - t0;
+  }
+}
+
+// The first CTAs join, a row a warp; the others (accumulation) add weights.
+// Both read what the decode kernel left and wait for its end.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int grid, int join_ctas) {
+  cudaGridDependencySynchronize();
+  if ((int)blockIdx.x < join_ctas) {
+    const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (i < (long long)a.pg.B * a.Hq) join_row<T, D>(a, grid, i);
+  } else {
+    add_weights(a, grid, blockIdx.x - join_ctas, gridDim.x - join_ctas);
   }
 }
 
@@ -647,6 +692,8 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
   const nats_status s = check_cache(c);
   if (s != NATS_OK) return s;
   if (Hq < 0 || Hq % c->Hk != 0) return NATS_ERR_SHAPE;
+  // a group's lse fit shared memory
+  if (Hq / c->Hk > 4096) return NATS_ERR_UNSUPPORTED;
   // rows of a pool and of the batch's queries are 32-bit
   if ((long long)c->B * Hq > (1LL << 31) - 1 || (double)c->n_pages * c->Hk * c->page > 2147483647.0)
     return NATS_ERR_UNSUPPORTED;
@@ -657,10 +704,11 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
 // A kernel that starts while the one before it in the stream still runs, and
 // waits for it (to end) itself: its launch is then off the path.
 template <class... P, class... A>
-cudaError_t after(void (*kernel)(P...), unsigned grid, cudaStream_t st, A... args) {
+cudaError_t after(void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -692,19 +740,11 @@ cudaError_t launch(DecodeArgs& a, int dtype, cudaStream_t st) {
 #undef NATS_DECODE
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.pg.B * a.Hq;
-  const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
-  e = dtype == NATS_BF16 ? after(decode_join_kernel<__nv_bfloat16, D>, grid, st, a, ctas)
-                         : after(decode_join_kernel<float, D>, grid, st, a, ctas);
-  if (e != cudaSuccess || !a.scores) return e;
-  const unsigned wide_grid = kSMs * 8;
-  switch (a.G) {
-    case 1: return after(decode_weight_kernel<1>, wide_grid, st, a);
-    case 2: return after(decode_weight_kernel<2>, wide_grid, st, a);
-    case 4: return after(decode_weight_kernel<4>, wide_grid, st, a);
-    case 8: return after(decode_weight_kernel<8>, wide_grid, st, a);
-    default: return after(decode_weight_kernel<0>, wide_grid, st, a);
-  }
+  const int join = (int)(((long long)a.pg.B * a.Hq + kWarps - 1) / kWarps);
+  const unsigned grid = join + (acc ? kSMs * 8 : 0);
+  const size_t smem = acc ? 4 * (size_t)a.G : 0;
+  return dtype == NATS_BF16 ? after(decode_finish_kernel<__nv_bfloat16, D>, grid, smem, st, a, ctas, join)
+                            : after(decode_finish_kernel<float, D>, grid, smem, st, a, ctas, join);
 }
 
 }  // namespace
