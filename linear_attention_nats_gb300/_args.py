@@ -74,6 +74,14 @@ def heads_out(t, name, dtype, shape, device):
     return p, st
 
 
+def new_heads(shape, dtype, device, made):
+    """A new contiguous [B, H, L, d] output (added to `made`), its address and strides."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    made.append(t)
+    _, h, s, e = shape
+    return t, t.data_ptr(), strides(h * s * e, s * e, e)
+
+
 def call(fn, where, device, stream, made, *args):
     """fn(*args, stream) on the tensors' device.  `made`: tensors allocated for
     the call (on the current stream), which a call on another stream keeps

@@ -428,6 +428,7 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
 template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeBwdArgs a) {
   constexpr int LPR = D / 8;
+  cudaTriggerProgrammaticLaunchCompletion();  // rope_dw_kernel may be launched; it waits for this kernel's end
   __shared__ float red[kWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeBwdArgs a)
 template <int D>
 __global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk) {
   __shared__ float red[32][32];
+  cudaGridDependencySynchronize();
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D
   float v = 0.f;
 #pragma unroll 8
@@ -505,10 +507,9 @@ __global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk)
 constexpr int kSMs = 152;
 constexpr int kBwdGrid = kSMs * 2;
 
-// Rows a warp takes of one token: all of them when the tokens alone fill the
-// GPU (64 warps an SM), else split evenly so that short calls spread out.
-void split_rows(long long tokens, int rows, int rpw, int* per_item, int* items) {
-  const long long want = (long long)kSMs * 64;
+// Rows a warp takes of one token: all of them when the tokens alone give
+// `want` warps their work, else split evenly so that short calls spread out.
+void split_rows(long long tokens, int rows, int rpw, long long want, int* per_item, int* items) {
   const int most = (rows + rpw - 1) / rpw;
   long long n = tokens > 0 ? (want + tokens - 1) / tokens : 1;
   if (n > most) n = most;
@@ -547,7 +548,7 @@ template <bool PAGED>
 cudaError_t launch_fwd(RopeArgs& a, int dtype, int d, bool inter, bool vec, cudaStream_t st) {
   const long long tokens = (long long)a.B * a.L;
   const int rows = a.Hq + a.Hk * (PAGED ? 2 : 1);
-  split_rows(tokens, rows, 32 / (d / 8), &a.rows_per_item, &a.items_per_token);
+  split_rows(tokens, rows, 32 / (d / 8), (long long)kSMs * 64, &a.rows_per_item, &a.items_per_token);
   const long long items = tokens * a.items_per_token;
   const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
 #define NATS_ROPE(T, D, I, V) rope_fwd_kernel<T, D, I, PAGED, V><<<grid, kWarps * 32, 0, st>>>(a)
@@ -706,7 +707,7 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
   a.norm = dims->norm, a.eps = dims->eps;
   a.part = dw ? (float*)workspace : nullptr;
   const long long tokens = (long long)a.B * a.L;
-  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), &a.rows_per_item, &a.items_per_token);
+  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), kBwdGrid * kWarps, &a.rows_per_item, &a.items_per_token);
   const long long ctas = (tokens * a.items_per_token + kWarps - 1) / kWarps;
   const unsigned grid = (unsigned)(ctas < kBwdGrid ? ctas : kBwdGrid);
   const bool inter = dims->interleaved != 0;
@@ -723,12 +724,19 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
     launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, grid, st);
   int r = record_cuda_error(cudaGetLastError());
   if (r != NATS_OK || !dw) return (nats_status)r;
-  const dim3 bd(32, 32);
-  if (d == 128)
-    rope_dw_kernel<128><<<8, bd, 0, st>>>(a.part, (int)grid, dw_q, dw_k);
-  else
-    rope_dw_kernel<64><<<4, bd, 0, st>>>(a.part, (int)grid, dw_q, dw_k);
-  return (nats_status)record_cuda_error(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * d / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const float* part = a.part;
+  r = record_cuda_error(cudaLaunchKernelEx(&cfg, d == 128 ? rope_dw_kernel<128> : rope_dw_kernel<64>, part, (int)grid,
+                                           dw_q, dw_k));
+  return (nats_status)r;
 }
 
 }  // extern "C"

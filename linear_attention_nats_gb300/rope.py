@@ -66,13 +66,13 @@ def qk_norm_rope(q, k, w_q=None, w_k=None, inv_freq=None, positions=None, *, pos
     rot, pf, pp, pb = _rotation(inv_freq, positions, B, L, dev)
     made = []
     if out_q is None:
-        out_q = torch.empty(qs, dtype=dt, device=dev)
-        made.append(out_q)
+        out_q, poq, soq = _args.new_heads(qs, dt, dev, made)
+    else:
+        poq, soq = _args.heads_out(out_q, "out_q", dt, qs, dev)
     if out_k is None:
-        out_k = torch.empty(ks, dtype=dt, device=dev)
-        made.append(out_k)
-    poq, soq = _args.heads_out(out_q, "out_q", dt, qs, dev)
-    pok, sok = _args.heads_out(out_k, "out_k", dt, ks, dev)
+        out_k, pok, sok = _args.new_heads(ks, dt, dev, made)
+    else:
+        pok, sok = _args.heads_out(out_k, "out_k", dt, ks, dev)
     dm = _args.rope_dims(B, L, Hq, ks[1], d, rot, interleaved, norm, code, eps)
     _args.call(_native.lib.nats_qk_norm_rope, "nats_qk_norm_rope", dev, stream, made, dm, pq, sq, pk, sk, pwq, pwk, pf,
                pp, pb, pos0, poq, soq, pok, sok)
@@ -101,26 +101,25 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, inv_freq=None, po
     pwq, pwk = _args.need(w_q, "w_q", torch.float32, (d,), dev), _args.need(w_k, "w_k", torch.float32, (d,), dev)
     rot, pf, pp, pb = _rotation(inv_freq, positions, B, L, dev)
     made = []
+    xt = dq.dtype if dq is not None else dk.dtype if dk is not None else dt
     if dq is None:
-        dq = torch.empty(qs, dtype=dt if dk is None else dk.dtype, device=dev)
-        made.append(dq)
-    xt = dq.dtype
+        dq, pdq, sdq = _args.new_heads(qs, xt, dev, made)
+    else:
+        pdq, sdq = _args.heads_out(dq, "dq", xt, qs, dev)
     if dk is None:
-        dk = torch.empty(ks, dtype=xt, device=dev)
-        made.append(dk)
+        dk, pdk, sdk = _args.new_heads(ks, xt, dev, made)
+    else:
+        pdk, sdk = _args.heads_out(dk, "dk", xt, ks, dev)
     xcode = _args.dtype_code(dq, "dq")
-    pdq, sdq = _args.heads_out(dq, "dq", xt, qs, dev)
-    pdk, sdk = _args.heads_out(dk, "dk", xt, ks, dev)
     dm = _args.rope_dims(B, L, Hq, ks[1], d, rot, interleaved, norm, code, eps)
     lib = _native.lib
     res = {"dq": dq, "dk": dk}
     pws, nws, pdw_q, pdw_k = None, 0, None, None
     if weight_grads and norm:
-        dw = torch.empty((2, d), dtype=torch.float32, device=dev)
-        res["dw_q"], res["dw_k"] = dw[0], dw[1]
-        pdw_q = dw.data_ptr()
-        pdw_k = pdw_q + 4 * d
-        made.append(dw)
+        res["dw_q"] = dw_q = torch.empty((d,), dtype=torch.float32, device=dev)
+        res["dw_k"] = dw_k = torch.empty((d,), dtype=torch.float32, device=dev)
+        pdw_q, pdw_k = dw_q.data_ptr(), dw_k.data_ptr()
+        made += [dw_q, dw_k]
         if workspace is None:
             workspace = torch.empty(lib.nats_qk_norm_rope_bwd_workspace_size(dm), dtype=torch.uint8, device=dev)
             made.append(workspace)
