@@ -347,7 +347,7 @@ struct RopeBwdArgs {
   float* part;  // [grid, 2, D] or NULL
 };
 
-constexpr int kRowsAheadBwd = 2;
+constexpr int kWarpsBwd = 4;
 
 // Gradients of rows h0 .. h1 - 1 of one token and one kind; acc gathers the
 // lane's share of dw.
@@ -355,7 +355,7 @@ template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
 __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* src, long long x_h, GO* dst,
                                          long long d_h, int h0, int h1, const float* w, bool norm, float eps,
                                          const LaneMap& m, const float* c, const float* s, int sub, float* acc) {
-  constexpr int RPW = 32 / (D / 8);
+  constexpr int RPW = 32 / (D / 8), kAhead = 8 / RPW;  // eight rows of a warp in flight
   float wl[8];
   lane_weights(w, m, wl);
   const int dq = m.qb - m.qa;
@@ -364,10 +364,10 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
   GO* pd = dst + (h0 + sub) * d_h + m.qa;
   const long long sg = RPW * g_h, sx = RPW * x_h, sd = RPW * d_h;
   auto rows = [&](int h, auto full) {
-    Quad<GI, VEC> ga[kRowsAheadBwd], gb[kRowsAheadBwd];
-    Quad<T, VEC> xa[kRowsAheadBwd], xb[kRowsAheadBwd];
+    Quad<GI, VEC> ga[kAhead], gb[kAhead];
+    Quad<T, VEC> xa[kAhead], xb[kAhead];
 #pragma unroll
-    for (int i = 0; i < kRowsAheadBwd; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       const bool on = full || h + i * RPW < h1;
       if (on) {
         ga[i].load(pg);
@@ -384,7 +384,7 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
       pg += sg, px += sx;
     }
 #pragma unroll
-    for (int i = 0; i < kRowsAheadBwd; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       const bool on = full || h + i * RPW < h1;
       float u[8];
       ga[i].get(u), gb[i].get(u + 4);
@@ -419,17 +419,17 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
     }
   };
   int h = h0;
-  for (; h + kRowsAheadBwd * RPW <= h1; h += kRowsAheadBwd * RPW) rows(h + sub, std::true_type{});
+  for (; h + kAhead * RPW <= h1; h += kAhead * RPW) rows(h + sub, std::true_type{});
   if (h < h1) rows(h + sub, std::false_type{});
 }
 
 // The same mapping on a fixed grid whose warps stride over the items and keep
 // their shares of dw_q, dw_k in registers (8 entries of each a lane).
 template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeBwdArgs a) {
+__global__ void __launch_bounds__(kWarpsBwd * 32, 3) rope_bwd_kernel(RopeBwdArgs a) {
   constexpr int LPR = D / 8;
   cudaTriggerProgrammaticLaunchCompletion();  // rope_dw_kernel may be launched; it waits for this kernel's end
-  __shared__ float red[kWarps][D];
+  __shared__ float red[kWarpsBwd][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const LaneMap m = lane_map<INTER>(l, a.rot);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeBwdArgs a)
   for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
   const int rows = a.Hq + a.Hk;
   const long long n_items = (long long)a.B * a.L * a.items_per_token;
-  for (long long item = (long long)blockIdx.x * kWarps + warp; item < n_items; item += (long long)gridDim.x * kWarps) {
+  for (long long item = (long long)blockIdx.x * kWarpsBwd + warp; item < n_items; item += (long long)gridDim.x * kWarpsBwd) {
     const long long tok = item / a.items_per_token;
     const int b = (int)(tok / a.L), t = (int)(tok % a.L);
     const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
@@ -474,10 +474,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeBwdArgs a)
       if (sub == 0) red[warp][(i < 4 ? m.qa : m.qb - 4) + i] = v;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < D; e += kWarps * 32) {
+    for (int e = threadIdx.x; e < D; e += kWarpsBwd * 32) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w][e];
+      for (int w = 0; w < kWarpsBwd; ++w) v += red[w][e];
       a.part[((long long)blockIdx.x * 2 + which) * D + e] = v;
     }
     __syncthreads();
@@ -505,7 +505,7 @@ __global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk)
 }
 
 constexpr int kSMs = 152;
-constexpr int kBwdGrid = kSMs * 2;
+constexpr int kBwdGrid = kSMs * 3;
 
 // Rows a warp takes of one token: all of them when the tokens alone give
 // `want` warps their work, else split evenly so that short calls spread out.
@@ -563,7 +563,7 @@ cudaError_t launch_fwd(RopeArgs& a, int dtype, int d, bool inter, bool vec, cuda
 
 template <typename T, typename GI, typename GO>
 void launch_bwd(const RopeBwdArgs& a, int d, bool inter, bool vec, unsigned grid, cudaStream_t st) {
-#define NATS_BWD(D, I, V) rope_bwd_kernel<T, GI, GO, D, I, V><<<grid, kWarps * 32, 0, st>>>(a)
+#define NATS_BWD(D, I, V) rope_bwd_kernel<T, GI, GO, D, I, V><<<grid, kWarpsBwd * 32, 0, st>>>(a)
 #define NATS_BWD_V(D, I) (vec ? NATS_BWD(D, I, true) : NATS_BWD(D, I, false))
 #define NATS_BWD_I(D) (inter ? NATS_BWD_V(D, true) : NATS_BWD_V(D, false))
   d == 128 ? NATS_BWD_I(128) : NATS_BWD_I(64);
@@ -707,8 +707,8 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
   a.norm = dims->norm, a.eps = dims->eps;
   a.part = dw ? (float*)workspace : nullptr;
   const long long tokens = (long long)a.B * a.L;
-  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), kBwdGrid * kWarps, &a.rows_per_item, &a.items_per_token);
-  const long long ctas = (tokens * a.items_per_token + kWarps - 1) / kWarps;
+  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), kBwdGrid * kWarpsBwd, &a.rows_per_item, &a.items_per_token);
+  const long long ctas = (tokens * a.items_per_token + kWarpsBwd - 1) / kWarpsBwd;
   const unsigned grid = (unsigned)(ctas < kBwdGrid ? ctas : kBwdGrid);
   const bool inter = dims->interleaved != 0;
   const int d = dims->d;
