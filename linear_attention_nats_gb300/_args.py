@@ -27,79 +27,79 @@ def dtype_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def cuda_device(t: torch.Tensor, name: str) -> torch.device:
+def cuda_index(t: torch.Tensor, name: str) -> int:
+    """The index of the tensor's CUDA device."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _refuse(t, name, dtype, shape, device):
+def refuse(t, name, dtype, shape, dev):
+    """Raises what is wrong with a tensor argument that has failed a check."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def need(t, name, dtype, shape, device):
-    """The address of a contiguous tensor argument (None for None)."""
+def need(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor argument on device `dev` (None for None)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.device == device and (shape is None or t.shape == shape) and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and (shape is None or t.shape == shape) and t.is_contiguous():
         return t.data_ptr()
-    _refuse(t, name, dtype, shape, device)
+    refuse(t, name, dtype, shape, dev)
 
 
-def heads(t, name, dtype, shape, device):
+def heads(t, name, dtype, shape, dev):
     """A [B, H, L, d] operand with any strides but the last: its address and strides."""
-    if t.dtype is not dtype or t.device != device or t.shape != shape:
-        _refuse(t, name, dtype, shape, device)
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        refuse(t, name, dtype, shape, dev)
     b, h, s, e = t.stride()
     if e != 1 and t.numel() > 0:
         raise ValueError(f"{name}: the entries of a row must be contiguous (last stride 1, got {e})")
     return t.data_ptr(), strides(b, h, s)
 
 
-def heads_out(t, name, dtype, shape, device):
+def heads_out(t, name, dtype, shape, dev):
     """The same for an output, which must not be an expanded tensor (entries that share an address)."""
-    p, st = heads(t, name, dtype, shape, device)
-    if 0 in t.stride():
+    p, st = heads(t, name, dtype, shape, dev)
+    if not (st.b and st.h and st.t):
         for n, s in zip(t.shape, t.stride()):
             if s == 0 and n > 1:
                 raise ValueError(f"{name} is written and must not be an expanded tensor")
     return p, st
 
 
-def new_heads(shape, dtype, device, made):
+def new_heads(shape, dtype, dev, made):
     """A new contiguous [B, H, L, d] output (added to `made`), its address and strides."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=dev)
     made.append(t)
     _, h, s, e = shape
     return t, t.data_ptr(), strides(h * s * e, s * e, e)
 
 
-def call(fn, where, device, stream, made, *args):
-    """fn(*args, stream) on the tensors' device.  `made`: tensors allocated for
-    the call (on the current stream), which a call on another stream keeps
-    alive until it has run."""
-    idx = device.index
-    handle = _raw_stream(idx)
+def call(fn, where, dev, stream, made, *args):
+    """fn(*args, stream) on device `dev`.  `made`: tensors allocated for the
+    call (on the current stream), which a call on another stream keeps alive
+    until it has run."""
+    handle = _raw_stream(dev)
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
         if stream.cuda_stream != handle:
             handle = stream.cuda_stream
             for t in made:
-                if t is not None:
-                    t.record_stream(stream)
-    if idx == torch._C._cuda_getDevice():
+                t.record_stream(stream)
+    if dev == torch._C._cuda_getDevice():
         code = fn(*args, handle)
     else:
-        with torch.cuda.device(idx):
+        with torch.cuda.device(dev):
             code = fn(*args, handle)
     if code:
         raise _native.NatsError(code, where)

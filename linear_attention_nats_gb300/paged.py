@@ -29,7 +29,7 @@ class PagedCache:
         if table.dim() != 2:
             raise ValueError("table must be [B, max_pages]")
         B, most = table.shape
-        dev = _args.cuda_device(k_pages, "k_pages")
+        dev = _args.cuda_index(k_pages, "k_pages")
         code = _args.dtype_code(k_pages, "k_pages")
         pk = _args.need(k_pages, "k_pages", k_pages.dtype, None, dev)
         pv = _args.need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev)
@@ -37,7 +37,7 @@ class PagedCache:
         pl = _args.need(lens, "lens", torch.int32, (B,), dev)
         pw = _args.need(weight, "weight", torch.float32, (n, Hk, page), dev)
         self._t = (k_pages, v_pages, table, lens, weight, torch.zeros((1,), dtype=torch.int32, device=dev))
-        self.device, self.dtype = dev, k_pages.dtype
+        self._dev, self.device, self.dtype = dev, k_pages.device, k_pages.dtype
         self.n_pages, self.Hk, self.page, self.d, self.B, self.max_pages = n, Hk, page, d, B, most
         self._c = _native.PagedCache(pk, pv, pw, pt, pl, self._t[5].data_ptr(), n, page, Hk, d, B, most, code)
 
@@ -87,7 +87,7 @@ def paged_append(cache: PagedCache, k, v, *, start=None, n_new=None, q=None, out
     if k.dim() != 4:
         raise ValueError("k must be [B, Hk, T, d]")
     B, Hk, T, d = k.shape
-    dev, dt = cache.device, cache.dtype
+    dev, dt = cache._dev, cache.dtype
     if (B, Hk, d) != (cache.B, cache.Hk, cache.d):
         raise ValueError(f"k must be [{cache.B}, {cache.Hk}, T, {cache.d}], got {tuple(k.shape)}")
     ks = k.shape
@@ -123,12 +123,12 @@ def paged_decode(cache: PagedCache, q, *, scale: float = 0.0, accumulate: bool =
     accumulate adds each slot's attention weight, summed over the query heads
     of its key head, to cache.weight.  workspace: uint8 tensor of
     paged_workspace_size(cache, Hq=Hq, accumulate=accumulate) bytes, or None."""
-    dev, dt, c = cache.device, cache.dtype, cache._c
+    dev, dt, c = cache._dev, cache.dtype, cache._c
     qs = q.shape
     if len(qs) != 3 or qs[0] != cache.B or qs[2] != cache.d:
         raise ValueError(f"q must be [{cache.B}, Hq, {cache.d}], got {tuple(qs)}")
-    if q.dtype is not dt or q.device != dev:
-        _args._refuse(q, "q", dt, None, dev)
+    if q.dtype is not dt or q.get_device() != dev:
+        _args.refuse(q, "q", dt, None, dev)
     qb, qh, qe = q.stride()
     if qe != 1 and q.numel() > 0:
         raise ValueError("q: the entries of a row must be contiguous")
@@ -162,7 +162,7 @@ def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, s
     (keep, lengths) with keep int32 [B, Hk, budget], the kept slots, -1 behind
     the last.  The caller then puts out_table and the lengths into the cache
     and frees the old pages."""
-    dev, c, lib = cache.device, cache._c, _native.lib
+    dev, c, lib = cache._dev, cache._c, _native.lib
     if cache.weight is None:
         raise ValueError("eviction needs a cache with weights")
     if out_table.dim() != 2 or out_table.shape[0] != cache.B:

@@ -28,8 +28,8 @@ def _rotation(inv_freq, positions, B, L, device):
         rot = 2 * inv_freq.shape[0]
     if positions is not None:
         shape = (B, L) if positions.dim() == 2 else (L,)
-        if positions.dtype is not torch.int64 or positions.device != device or positions.shape != shape:
-            _args._refuse(positions, "positions", torch.int64, shape, device)
+        if positions.dtype is not torch.int64 or positions.get_device() != device or positions.shape != shape:
+            _args.refuse(positions, "positions", torch.int64, shape, device)
         st = positions.stride()
         if st[-1] != 1 and L > 1:
             raise ValueError("positions of a sequence must be contiguous")
@@ -37,11 +37,14 @@ def _rotation(inv_freq, positions, B, L, device):
     return rot, pf, pp, pb
 
 
-def _check_pair(q, k):
-    if q.dim() != 4 or k.dim() != 4:
+def _pair(q, k):
+    """The shapes of q and k, which differ in their heads alone."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("q and k must be [B, H, L, d]")
-    if q.shape[0] != k.shape[0] or q.shape[2:] != k.shape[2:]:
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
+    if ks != (qs[0], ks[1], qs[2], qs[3]):
+        raise ValueError(f"q {tuple(qs)} and k {tuple(ks)} differ in more than their heads")
+    return qs, ks
 
 
 def qk_norm_rope(q, k, w_q=None, w_k=None, inv_freq=None, positions=None, *, pos0: int = 0, interleaved: bool = False,
@@ -55,10 +58,9 @@ def qk_norm_rope(q, k, w_q=None, w_k=None, inv_freq=None, positions=None, *, pos
     pairs (2i, 2i + 1) in place of (i, i + rot / 2); norm=False rotates alone.
     Returns (q', k') in the layer's contiguous [B, H, L, d], or in out_q, out_k
     (any strides but the last; the inputs themselves for in place)."""
-    _check_pair(q, k)
-    qs, ks = q.shape, k.shape
+    qs, ks = _pair(q, k)
     B, Hq, L, d = qs
-    dev, dt = _args.cuda_device(q, "q"), q.dtype
+    dev, dt = _args.cuda_index(q, "q"), q.dtype
     code = _args.dtype_code(q, "q")
     pq, sq = _args.heads(q, "q", dt, qs, dev)
     pk, sk = _args.heads(k, "k", dt, ks, dev)
@@ -88,10 +90,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, inv_freq=None, po
     the given tensors' own: bf16 or fp32, any strides but the last) and, with
     weight_grads and norm, dw_q, dw_k (fp32 [d]).  q, k and the other arguments
     are the forward's."""
-    _check_pair(q, k)
-    qs, ks = q.shape, k.shape
+    qs, ks = _pair(q, k)
     B, Hq, L, d = qs
-    dev, dt, gt = _args.cuda_device(q, "q"), q.dtype, dq_out.dtype
+    dev, dt, gt = _args.cuda_index(q, "q"), q.dtype, dq_out.dtype
     code = _args.dtype_code(q, "q")
     gcode = _args.dtype_code(dq_out, "dq_out")
     pq, sq = _args.heads(q, "q", dt, qs, dev)
