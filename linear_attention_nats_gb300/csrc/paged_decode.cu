@@ -24,7 +24,7 @@ constexpr int kTile = 64;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSMs = 152;
-constexpr int kMaxCtas = kSMs * 3;
+constexpr int kMaxCtas = kSMs * 4;
 constexpr int kMaxHeads = 16;  // query heads of a unit, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -295,14 +295,16 @@ struct F32 {
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
-  // c += A B in split precision, the small products first
-  static __device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  // A B in split precision into two accumulators, the full products' and the
+  // small ones' (independent chains, added at the end)
+  static __device__ __forceinline__ void mma3(float (&c)[4], float (&small)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = high(a[i]), l[i] = low(a[i]);
-    mma(c, l[0], l[1], l[2], l[3], high(b0), high(b1));
-    mma(c, h[0], h[1], h[2], h[3], low(b0), low(b1));
     mma(c, h[0], h[1], h[2], h[3], high(b0), high(b1));
+    mma(small, l[0], l[1], l[2], l[3], high(b0), high(b1));
+    mma(small, h[0], h[1], h[2], h[3], low(b0), low(b1));
   }
 
   static __device__ __forceinline__ void load_q(Q& q, const T* p, bool on, int c) {
@@ -325,13 +327,16 @@ struct F32 {
                                                  : ldg_once(p + (long long)(row + c + 4 * i) * D + 32 * y + 4 * g);
   }
   static __device__ __forceinline__ void scores(float (&s)[4], const K& k, const Q& q) {
+    float more[3][4] = {};
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
       const uint32_t a[4] = {k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y};
-      mma3(s, a, __float_as_uint(q.r[y].x), __float_as_uint(q.r[y].y));
+      mma3(s, more[0], a, __float_as_uint(q.r[y].x), __float_as_uint(q.r[y].y));
       const uint32_t b[4] = {k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w};
-      mma3(s, b, __float_as_uint(q.r[y].z), __float_as_uint(q.r[y].w));
+      mma3(more[1], more[2], b, __float_as_uint(q.r[y].z), __float_as_uint(q.r[y].w));
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] += more[1][i] + (more[0][i] + more[2][i]);
   }
   template <int NH>
   static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int g,
@@ -352,8 +357,11 @@ struct F32 {
         // rows g and g + 8 of tile y: entry y % 4 of the lane's segments 2 (y / 4) and 2 (y / 4) + 1
         auto at = [&](int slot, int seg) { return ((const uint32_t*)&v.r[slot][2 * (y / 4) + seg])[y % 4]; };
         const uint32_t a[4] = {at(0, 0), at(0, 1), at(1, 0), at(1, 1)}, a2[4] = {at(2, 0), at(2, 1), at(3, 0), at(3, 1)};
-        mma3(o[x][y], a, b[0], b[1]);
-        mma3(o[x][y], a2, b[2], b[3]);
+        float small[4] = {};
+        mma3(o[x][y], small, a, b[0], b[1]);
+        mma3(o[x][y], small, a2, b[2], b[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[x][y][i] += small[i];
       }
     }
   }
@@ -726,17 +734,19 @@ cudaError_t launch(DecodeArgs& a, int dtype, cudaStream_t st) {
   const bool wide = dtype == NATS_BF16 && a.G > 8;
   a.GT = wide ? 16 : 8;
   a.ngroups = (a.G + a.GT - 1) / a.GT;
-  const int per_sm = dtype == NATS_BF16 && !wide ? 3 : 2, ctas = kSMs * per_sm;
+  // CTAs an SM has registers for
+  constexpr int kBlocks = D == 64 ? 4 : 3, kBlocksF32 = D == 64 ? 3 : 2, kBlocksWide = 2;
+  const int ctas = kSMs * (dtype != NATS_BF16 ? kBlocksF32 : wide ? kBlocksWide : kBlocks);
   const bool acc = a.scores != nullptr;
 #define NATS_DECODE(X, NH, BLOCKS)                                                 \
   (acc ? decode_kernel<X, NH, true, BLOCKS><<<ctas, kThreads, 0, st>>>(a)          \
        : decode_kernel<X, NH, false, BLOCKS><<<ctas, kThreads, 0, st>>>(a))
   if (dtype != NATS_BF16)
-    NATS_DECODE(F32<D>, 1, 2);
+    NATS_DECODE(F32<D>, 1, kBlocksF32);
   else if (wide)
-    NATS_DECODE(Bf16<D>, 2, 2);
+    NATS_DECODE(Bf16<D>, 2, kBlocksWide);
   else
-    NATS_DECODE(Bf16<D>, 1, 3);
+    NATS_DECODE(Bf16<D>, 1, kBlocks);
 #undef NATS_DECODE
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
