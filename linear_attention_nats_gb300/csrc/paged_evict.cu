@@ -104,6 +104,7 @@ __device__ __forceinline__ int find_from_top(cooperative_groups::cluster_group& 
 
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a, int held) {
   namespace cg = cooperative_groups;
+  cudaTriggerProgrammaticLaunchCompletion();  // the copy may be launched; it waits for this kernel's end
   extern __shared__ uint32_t keys[];  // the share's first `held` weights, as order_bits
   __shared__ int hist[3][kBins], groups[3][kBins / 32];
   __shared__ int sums[kSelWarps], pick[2], counts[2];
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
 // Kept rows i0 .. i0 + 63 of one head: keys, values and weights.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictArgs a, int tiles) {
   __shared__ long long from[kCopyRows], to[kCopyRows];
+  cudaGridDependencySynchronize();
   const int bh = blockIdx.x / tiles, i0 = (blockIdx.x % tiles) * kCopyRows;
   const int b = bh / a.pg.Hk, h = bh % a.pg.Hk;
   const int left = min(a.pg.length(b), a.budget);
@@ -352,8 +354,16 @@ nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_t
   const int r = record_cuda_error(launch_select(a, (long long)cache->max_pages * cache->page, st));
   if (r != NATS_OK || budget == 0) return (nats_status)r;
   const int tiles = (budget + kCopyRows - 1) / kCopyRows;
-  evict_copy_kernel<<<(unsigned)((long long)cache->B * cache->Hk * tiles), kCopyThreads, 0, st>>>(a, tiles);
-  return (nats_status)record_cuda_error(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)cache->B * cache->Hk * tiles));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return (nats_status)record_cuda_error(cudaLaunchKernelEx(&cfg, evict_copy_kernel, a, tiles));
 }
 
 }  // extern "C"
