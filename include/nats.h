@@ -20,7 +20,13 @@
  *   item 4  Each branch output is RMS-normalised on its own; the output is
  *           w N_soft + (1 - w) N_lin with w = sigmoid(q . W_g[h] + b_g[h]).
  *
- * Conventions common to every entry point:
+ * Around the layers stand the operators that a model needs to use them in
+ * training and serving: the norm and rotation of queries and keys with its
+ * gradient, and a paged key / value cache with its append, the attention of
+ * one new token over it and its eviction by accumulated attention weight.
+ *
+ * Conventions common to every entry point (the operators' sections give their
+ * own layouts and shapes):
  *   - Layout: Q, K [B, H, L, dk], V and the output [B, H, L, dv], all
  *     contiguous, row-major, element type `dtype` (bf16 or fp32).  g and
  *     beta are fp32 [B, H, L].  Selection codes are uint8 [B, H, N] with
@@ -680,8 +686,8 @@ nats_status nats_paged_append(const nats_paged_cache* cache, const nats_rope_dim
  * query heads of p_j, to cache->weight in every slot.  The work is cut into
  * 64-slot tiles dealt evenly to the GPU whatever the lengths are (they are
  * read on the device), partial results are joined by a second kernel in a
- * fixed order.  scale 0 => 1/sqrt(d).  Sequences that share pages must not
- * accumulate in one call.  workspace: device scratch of
+ * fixed order.  scale 0 => 1/sqrt(d).  out must not overlap q.  In a call that
+ * accumulates no page may be in the table twice (within or across sequences).  workspace: device scratch of
  * nats_paged_decode_workspace_size bytes, 16-byte aligned; calls that share
  * it must be ordered by the caller.  Errors before any launch: NATS_ERR_NULL,
  * _SHAPE (Hq not a multiple of Hk, the cache's fields), _UNSUPPORTED, _DTYPE,
@@ -698,8 +704,8 @@ nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float s
  * weight (ties to the lower slot; NaN counts as the lowest); with n <= budget
  * it keeps all.  The kept rows (key, value, weight) are copied in their order
  * to slots 0, 1, .. of the pages out_table[b] ([B, out_max_pages], the same
- * pool; lens_out[b] = min(n, budget) slots), which none of the cache's
- * sequences may be using; the old pages stay as they were.  keep (or NULL)
+ * pool; lens_out[b] = min(n, budget) slots), which must be distinct and which
+ * none of the cache's sequences may be using; the old pages stay as they were.  keep (or NULL)
  * int32 [B, Hk, budget]: the slots kept, in order, -1 behind the last.
  * lens_out int32 [B] must not be cache->lens.  workspace as above
  * (nats_paged_evict_workspace_size bytes).  Errors before any launch:

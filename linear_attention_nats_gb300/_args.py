@@ -47,6 +47,13 @@ def refuse(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def int32(**values):
+    """Refuses integers that a 32-bit argument would cut off."""
+    for name, v in values.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def need(t, name, dtype, shape, dev):
     """The address of a contiguous tensor argument on device `dev` (None for None)."""
     if t is None:

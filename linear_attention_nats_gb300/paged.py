@@ -69,6 +69,7 @@ class PagedCache:
 def paged_workspace_size(cache: PagedCache, *, Hq: int = 0, accumulate: bool = False, budget: int = 0) -> int:
     """Bytes of workspace that serve paged_decode with Hq query heads and
     paged_evict to `budget` (0 when a size is not supported)."""
+    _args.int32(Hq=Hq, budget=budget)
     a = int(_native.lib.nats_paged_decode_workspace_size(cache._c, Hq, int(accumulate)))
     b = int(_native.lib.nats_paged_evict_workspace_size(cache._c, budget))
     return max(a, b) if a and b else 0
@@ -167,6 +168,7 @@ def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, s
         raise ValueError("eviction needs a cache with weights")
     if out_table.dim() != 2 or out_table.shape[0] != cache.B:
         raise ValueError(f"out_table must be [{cache.B}, pages], got {tuple(out_table.shape)}")
+    _args.int32(budget=budget, recent=recent, sinks=sinks)
     pt = _args.need(out_table, "out_table", torch.int32, None, dev)
     made = []
     if lens_out is None:

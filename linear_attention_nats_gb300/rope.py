@@ -37,6 +37,12 @@ def _rotation(inv_freq, positions, B, L, device):
     return rot, pf, pp, pb
 
 
+def _pos0(pos0):
+    if not -(1 << 62) <= pos0 < 1 << 62:
+        raise ValueError(f"pos0 = {pos0} is out of range")
+    return pos0
+
+
 def _pair(q, k):
     """The shapes of q and k, which differ in their heads alone."""
     qs, ks = q.shape, k.shape
@@ -77,7 +83,7 @@ def qk_norm_rope(q, k, w_q=None, w_k=None, inv_freq=None, positions=None, *, pos
         pok, sok = _args.heads_out(out_k, "out_k", dt, ks, dev)
     dm = _args.rope_dims(B, L, Hq, ks[1], d, rot, interleaved, norm, code, eps)
     _args.call(_native.lib.nats_qk_norm_rope, "nats_qk_norm_rope", dev, stream, made, dm, pq, sq, pk, sk, pwq, pwk, pf,
-               pp, pb, pos0, poq, soq, pok, sok)
+               pp, pb, _pos0(pos0), poq, soq, pok, sok)
     return out_q, out_k
 
 
@@ -126,5 +132,5 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, inv_freq=None, po
             made.append(workspace)
         pws, nws = _args.need(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
     _args.call(lib.nats_qk_norm_rope_bwd, "nats_qk_norm_rope_bwd", dev, stream, made, dm, gcode, xcode, pgq, sgq, pgk,
-               sgk, pq, sq, pk, sk, pwq, pwk, pf, pp, pb, pos0, pdq, sdq, pdk, sdk, pdw_q, pdw_k, pws, nws)
+               sgk, pq, sq, pk, sk, pwq, pwk, pf, pp, pb, _pos0(pos0), pdq, sdq, pdk, sdk, pdw_q, pdw_k, pws, nws)
     return res

@@ -199,6 +199,12 @@ def test_decode_beyond_32_bit_offsets(nats):
     e, _, ps, err, perr = ref.decode(q, kk, vv, small, lens)
     assert ((out.cpu().double() - e).abs() <= 2.0 ** -8 * (e.abs() + err) + err).all()
     assert abs(float(w[-24:].double().sum()) - 16) < 1e-3
+    # a token appended there
+    x = torch.randn(1, Hk, 3, d, generator=rng).to(BF).cuda()
+    nats.paged_append(c, x, 2 * x, start=torch.tensor([100], dtype=torch.int32).cuda())
+    assert torch.equal(k[-1, :, 100:103], x[0]) and torch.equal(v[-1, :, 100:103], 2 * x[0])
+    kk[-1, :, 100:103], vv[-1, :, 100:103] = x[0].cpu(), 2 * x[0].cpu()
+    assert (w[-1, :, 100:103] == 0).all()
     # eviction within it: from the last pages to the ones before them
     outt = torch.arange(n_pages - 40, n_pages - 32, dtype=torch.int32)[None].cuda()
     keep, n = nats.paged_evict(c, outt, 8 * page, recent=17, sinks=4, return_keep=True)
@@ -237,6 +243,37 @@ def test_decode_on_another_stream_and_captured(nats):
     assert torch.equal(out, nats.paged_decode(c, q))
     # every sequence's weights sum to its query heads
     assert abs(float(c.weight.double().sum()) - 3 * 6) < 1e-4
+
+
+def test_decode_calls_in_a_row_share_a_workspace(nats):
+    """Calls behind one another on one stream, with one workspace and lengths that change between them, each give
+    what they give alone; so do two calls at once on two streams with a workspace each."""
+    rng = torch.Generator().manual_seed(13)
+    table, _, k, v = _filled(rng, [1500, 700, 900, 64], 16, 2, 128, BF)
+    c = _cache(nats, table, [1500, 700, 900, 64], k, v, torch.zeros(k.shape[:3]))
+    all_lens = [[1500, 700, 900, 64], [3, 0, 900, 1], [0, 0, 0, 0], [1499, 1, 17, 33], [64, 640, 128, 64]]
+    lens = [torch.tensor(x, dtype=torch.int32).cuda() for x in all_lens]
+    qs = [torch.randn(4, 10, 128, generator=rng).to(BF).cuda() for _ in lens]
+    alone = []
+    for q, n in zip(qs, lens):
+        c.lens.copy_(n)
+        alone.append(nats.paged_decode(c, q))
+        torch.cuda.synchronize()
+    ws = torch.empty(nats.paged_workspace_size(c, Hq=10, accumulate=True), dtype=torch.uint8, device="cuda")
+    got = []
+    for i in range(40):
+        c.lens.copy_(lens[i % 5])
+        got.append(nats.paged_decode(c, qs[i % 5], workspace=ws, accumulate=i % 2 == 1))
+    assert all(torch.equal(x, alone[i % 5]) for i, x in enumerate(got))
+    weights = sum(10 * sum(n > 0 for n in all_lens[i % 5]) for i in range(1, 40, 2))
+    assert abs(float(c.weight.double().sum()) - weights) < 1e-3
+    c.lens.copy_(lens[0])
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for x in s:
+        x.wait_stream(torch.cuda.current_stream())
+    both = [nats.paged_decode(c, qs[0], stream=s[i % 2]) for i in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, alone[0]) for x in both)
 
 
 # ------------------------------------------------------------------ append
@@ -299,6 +336,24 @@ def test_append(nats, T, n_new, start, Hq, Hk, d, page, dtype, norm, rot, inter)
             n = counts[b]
             assert ((out_q[b, :, :n].cpu().double() - qr[b, :, :n]).abs() <= qb[b, :, :n]).all()
             assert (out_q[b, :, n:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_from_odd_addresses(nats, dtype):
+    """Rows that start at odd entries move entry by entry, to the same values."""
+    rng = torch.Generator().manual_seed(14)
+    T, Hq, Hk, d = 9, 3, 2, 64
+    buf = torch.randn(2, T, (Hq + 2 * Hk) * d + 3, generator=rng).to(dtype).cuda()
+    parts = [buf[..., 1 + a * d:1 + b * d].unflatten(-1, (b - a, d)).transpose(1, 2) for a, b in ((0, 3), (3, 5), (5, 7))]
+    f = nats.rope_inv_freq(64)
+    res = []
+    for q, k, v in (parts, [p.contiguous() for p in parts]):
+        c = nats.PagedCache.empty(4, 16, Hk, d, 2, 2, dtype=dtype)
+        c.table.copy_(torch.tensor([[3, 1], [0, 2]], dtype=torch.int32))
+        q = nats.paged_append(c, k, v, q=q, norm=True, inv_freq=f, start=torch.tensor([10, 0], dtype=torch.int32).cuda())
+        res.append((q, c.k_pages, c.v_pages))
+    assert all(torch.equal(x, y) for x, y in zip(*res))
+    assert torch.equal(res[0][2][0, :, :9], parts[2][1])
 
 
 def test_append_given_positions_and_new_query(nats):
@@ -530,6 +585,8 @@ def test_refusals(nats):
         nats.paged_evict(cw, ot, 33)  # two pages hold 32
     with pytest.raises(nats.NatsError):
         nats.paged_evict(cw, cw.table, 8)
+    with pytest.raises(ValueError):
+        nats.paged_evict(cw, ot, (1 << 32) + 8)
     with pytest.raises(nats.NatsError):
         nats.paged_evict(cw, ot, 8, lens_out=cw.lens)
     with pytest.raises(ValueError):

@@ -221,6 +221,24 @@ def test_other_stream_and_graph(nats):
     assert all(torch.equal(x, y) for x, y in zip(o, want)) and all(torch.equal(b[n], grad[n]) for n in grad)
 
 
+def test_offsets_beyond_32_bits(nats):
+    """Rows 2^20 entries apart: the last tokens lie behind the 2^31st entry."""
+    T, S = 2200, 1 << 20
+    buf = torch.empty(T * S, dtype=BF, device="cuda")
+    q = buf.as_strided((1, 3, T, 64), (0, 128, S, 1))
+    k = buf.as_strided((1, 2, T, 64), (0, 128, S, 1), 512)
+    rng = torch.Generator().manual_seed(9)
+    q0, k0 = torch.randn(1, 3, T, 64, generator=rng).to(BF), torch.randn(1, 2, T, 64, generator=rng).to(BF)
+    q.copy_(q0), k.copy_(k0)
+    f = nats.rope_inv_freq(64)
+    want = nats.qk_norm_rope(q0.cuda(), k0.cuda(), None, None, f, pos0=5)
+    grad = nats.qk_norm_rope_bwd(*want, q0.cuda(), k0.cuda(), None, None, f, pos0=5)
+    got = nats.qk_norm_rope_bwd(*want, q, k, None, None, f, pos0=5)
+    assert all(torch.equal(got[n], grad[n]) for n in grad)
+    nats.qk_norm_rope(q, k, None, None, f, pos0=5, out_q=q, out_k=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
 def test_refusals(nats):
     x = torch.zeros(1, 2, 4, 64, device="cuda")
     f = nats.rope_inv_freq(64)
@@ -246,6 +264,12 @@ def test_refusals(nats):
         nats.qk_norm_rope(x, x, None, None, nats.rope_inv_freq(72))  # beyond d
     with pytest.raises(nats.NatsError):
         nats.qk_norm_rope(x, x, None, None, f, eps=-1.0)
+    with pytest.raises(ValueError):
+        nats.qk_norm_rope(x, x, None, None, f, pos0=1 << 63)
+    with pytest.raises(ValueError):
+        nats.qk_norm_rope(x, x, None, None, f, torch.zeros(2, 4, dtype=torch.int64, device="cuda"))
+    with pytest.raises(TypeError):
+        nats.qk_norm_rope(x, x, None, None, f, torch.zeros(1, 4, dtype=torch.int32, device="cuda"))
     with pytest.raises(nats.NatsError):
         nats.qk_norm_rope_bwd(x.bfloat16(), x.bfloat16(), x, x, None, None, f)  # fp32 inputs, bf16 gradients
 
