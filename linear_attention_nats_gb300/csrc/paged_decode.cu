@@ -271,11 +271,11 @@ struct Bf16 {
   }
 };
 
-// fp32 rows on the tf32 instructions, each factor as two (the upper 10 bits of
-// the significand, cut off, and what is left; the split-precision product of
-// Markidis et al., 2018): x y = x_h y_h + x_h y_l + x_l y_h to 2^-21.  K: the
-// lane holds entries 16 y + 4 c .. + 3 of its slots; V: entries 4 g + 32 y ..
-// + 3 of slots c, c + 4, c + 8, c + 12.  P reaches its layout by shuffles.
+// fp32 rows on the tf32 instructions, each factor as the sum of two (the
+// split-precision product of Markidis et al., 2018, with rounded parts):
+// x y = x_h y_h + x_h y_l + x_l y_h to about 2^-23.  K: the lane holds entries
+// 16 y + 4 c .. + 3 of its slots; V: entries 4 g + 32 y .. + 3 of slots c,
+// c + 4, c + 8, c + 12.  P reaches its layout by shuffles.
 template <int D>
 struct F32 {
   using T = float;
@@ -285,9 +285,12 @@ struct F32 {
   struct K { uint4 r[2][KB]; };
   struct V { uint4 r[4][VS]; };
 
-  static __device__ __forceinline__ uint32_t high(uint32_t x) { return x & 0xffffe000u; }
-  static __device__ __forceinline__ uint32_t low(uint32_t x) {
-    return __float_as_uint(__uint_as_float(x) - __uint_as_float(high(x)));
+  // x = h + l, both rounded to tf32 (10 bits of significand).  h by an integer
+  // addition (the instruction ignores the lower 13 bits); l by a conversion,
+  // which keeps a NaN one
+  static __device__ __forceinline__ void split(uint32_t x, uint32_t& h, uint32_t& l) {
+    h = (x + 0x1000u) & 0xffffe000u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(l) : "f"(__uint_as_float(x) - __uint_as_float(h)));
   }
   static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -295,16 +298,18 @@ struct F32 {
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
-  // A B in split precision into two accumulators, the full products' and the
-  // small ones' (independent chains, added at the end)
+  // A B in split precision: the full products into c, the small ones into
+  // `small`.  The instruction cuts its sums off where fp32 additions round, so
+  // c is a fresh accumulator, added outside, wherever a sum is long.
   static __device__ __forceinline__ void mma3(float (&c)[4], float (&small)[4], const uint32_t (&a)[4], uint32_t b0,
                                               uint32_t b1) {
-    uint32_t h[4], l[4];
+    uint32_t h[4], l[4], hb[2], lb[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = high(a[i]), l[i] = low(a[i]);
-    mma(c, h[0], h[1], h[2], h[3], high(b0), high(b1));
-    mma(small, l[0], l[1], l[2], l[3], high(b0), high(b1));
-    mma(small, h[0], h[1], h[2], h[3], low(b0), low(b1));
+    for (int i = 0; i < 4; ++i) split(a[i], h[i], l[i]);
+    split(b0, hb[0], lb[0]), split(b1, hb[1], lb[1]);
+    mma(c, h[0], h[1], h[2], h[3], hb[0], hb[1]);
+    mma(small, l[0], l[1], l[2], l[3], hb[0], hb[1]);
+    mma(small, h[0], h[1], h[2], h[3], lb[0], lb[1]);
   }
 
   static __device__ __forceinline__ void load_q(Q& q, const T* p, bool on, int c) {
@@ -327,16 +332,19 @@ struct F32 {
                                                  : ldg_once(p + (long long)(row + c + 4 * i) * D + 32 * y + 4 * g);
   }
   static __device__ __forceinline__ void scores(float (&s)[4], const K& k, const Q& q) {
-    float more[3][4] = {};
+    float small[2][4] = {};
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
-      const uint32_t a[4] = {k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y};
-      mma3(s, more[0], a, __float_as_uint(q.r[y].x), __float_as_uint(q.r[y].y));
-      const uint32_t b[4] = {k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w};
-      mma3(more[1], more[2], b, __float_as_uint(q.r[y].z), __float_as_uint(q.r[y].w));
+      float c0[4] = {}, c1[4] = {};
+      const uint32_t a0[4] = {k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y};
+      mma3(c0, small[0], a0, __float_as_uint(q.r[y].x), __float_as_uint(q.r[y].y));
+      const uint32_t a1[4] = {k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w};
+      mma3(c1, small[1], a1, __float_as_uint(q.r[y].z), __float_as_uint(q.r[y].w));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += c0[i] + c1[i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] += more[1][i] + (more[0][i] + more[2][i]);
+    for (int i = 0; i < 4; ++i) s[i] += small[0][i] + small[1][i];
   }
   template <int NH>
   static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int g,
@@ -357,11 +365,11 @@ struct F32 {
         // rows g and g + 8 of tile y: entry y % 4 of the lane's segments 2 (y / 4) and 2 (y / 4) + 1
         auto at = [&](int slot, int seg) { return ((const uint32_t*)&v.r[slot][2 * (y / 4) + seg])[y % 4]; };
         const uint32_t a[4] = {at(0, 0), at(0, 1), at(1, 0), at(1, 1)}, a2[4] = {at(2, 0), at(2, 1), at(3, 0), at(3, 1)};
-        float small[4] = {};
-        mma3(o[x][y], small, a, b[0], b[1]);
-        mma3(o[x][y], small, a2, b[2], b[3]);
+        float full[4] = {}, small[4] = {};
+        mma3(full, small, a, b[0], b[1]);
+        mma3(full, small, a2, b[2], b[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[x][y][i] += small[i];
+        for (int i = 0; i < 4; ++i) o[x][y][i] += full[i] + small[i];
       }
     }
   }
@@ -443,16 +451,17 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[x][i] = (i < 2 ? lo : hi) ? s[x][i] * a.scale2 : -INFINITY;
+        for (int i = 0; i < 4; ++i) s[x][i] = (i < 2 ? lo : hi) ? s[x][i] : -INFINITY;
         if (ACC) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + g + 8 * (i >> 1), h = 8 * x + 2 * c + (i & 1);
             if (j < n && h < heads)
-              a.scores[(((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G + g0 + h] = s[x][i];
+              a.scores[(((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G + g0 + h] = s[x][i] * a.scale2;
           }
         }
-        rises |= fmaxf(s[x][0], s[x][2]) > mx[x][0] + kSlack || fmaxf(s[x][1], s[x][3]) > mx[x][1] + kSlack;
+        rises |= fmaxf(s[x][0], s[x][2]) * a.scale2 > mx[x][0] + kSlack ||
+                 fmaxf(s[x][1], s[x][3]) * a.scale2 > mx[x][1] + kSlack;
       }
       if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
             float m = fmaxf(s[x][i], s[x][i + 2]);
 #pragma unroll
             for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-            m = fmaxf(m, mx[x][i]);
+            m = fmaxf(m * a.scale2, mx[x][i]);
             const float f = part_scale(mx[x][i], m);
             mx[x][i] = m;
             sum[x][i] *= f;
@@ -474,8 +483,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       for (int x = 0; x < NH; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // (a head without a slot yet has no maximum to subtract: its scores are all -inf)
-          s[x][i] = s[x][i] == -INFINITY ? 0.f : exp2f(s[x][i] - mx[x][i & 1]);
+          // the scaled score is not rounded before the maximum is subtracted
+          // (a head without a slot yet has no maximum: its scores are all -inf)
+          s[x][i] = s[x][i] == -INFINITY ? 0.f : exp2f(fmaf(s[x][i], a.scale2, -mx[x][i & 1]));
           sum[x][i & 1] += s[x][i];
         }
       X::template values<NH>(o, v, s, g, c);

@@ -155,16 +155,21 @@ def test_decode_lengths_out_of_range(nats):
         c.check()
 
 
-def test_decode_values_that_are_not_finite(nats):
-    """Such values in slots behind a sequence do not matter (every other test has them there); in a used slot of one
-    key head they reach that head's queries alone."""
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_values_that_are_not_finite(nats, dtype):
+    """Such values in slots behind a sequence do not matter (every other test has them there); a NaN in a used slot of
+    one key head reaches that head's queries alone: of a value, its entry; of a key, all."""
     rng = torch.Generator().manual_seed(5)
-    table, _, k, v = _filled(rng, [50], 16, 2, 64, BF)
-    v[table[0, 1].long(), 0, 3, 7] = math.nan
-    c = _cache(nats, table, [50], k, v)
-    out = nats.paged_decode(c, torch.randn(1, 4, 64, generator=rng).to(BF).cuda())
-    bad = torch.isnan(out.cpu())
-    assert bad[0, :2, 7].all() and bad.sum() == 2
+    q = torch.randn(1, 4, 64, generator=rng).to(dtype).cuda()
+    for bits in (math.nan, -math.nan):
+        table, _, k, v = _filled(rng, [50], 16, 2, 64, dtype)
+        v[table[0, 1].long(), 0, 3, 7] = bits
+        bad = torch.isnan(nats.paged_decode(_cache(nats, table, [50], k, v), q).cpu())
+        assert bad[0, :2, 7].all() and bad.sum() == 2
+        table, _, k, v = _filled(rng, [50], 16, 2, 64, dtype)
+        k[table[0, 2].long(), 1, 5, 11] = bits
+        bad = torch.isnan(nats.paged_decode(_cache(nats, table, [50], k, v), q).cpu())
+        assert bad[0, 2:].all() and not bad[0, :2].any()
 
 
 def test_decode_peaked_scores(nats):
