@@ -130,16 +130,34 @@ __device__ __forceinline__ LaneMap lane_map(int l, int rot) {
   return m;
 }
 
-// cos and sin of the lane's four pairs at position p (1 and 0 where nothing turns)
-__device__ __forceinline__ void angles(const uint64_t* F, bool turned, long long p, float* c, float* s) {
+// cos and sin of the lane's four pairs at position p (1 and 0 where nothing
+// turns).  The 32 / LPR rows of a warp have the same pairs, so each of them
+// works out its share of the four (F: that share's frequencies) and the lanes
+// exchange them.
+template <int LPR>
+__device__ __forceinline__ void angles(const uint64_t* F, bool turned, long long p, int l, float* c, float* s) {
+  constexpr int N = 4 / (32 / LPR);
+  float cm[N], sm[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = 1.f, s[i] = 0.f;
+  for (int i = 0; i < N; ++i) {
+    cm[i] = 1.f, sm[i] = 0.f;
     if (turned) {
       const uint64_t ph = (uint64_t)p * F[i];
-      sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &s[i], &c[i]);
+      sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &sm[i], &cm[i]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = __shfl_sync(0xffffffffu, cm[i % N], LPR * (i / N) + l);
+    s[i] = __shfl_sync(0xffffffffu, sm[i % N], LPR * (i / N) + l);
+  }
+}
+// the frequencies of the lane's share
+template <int LPR>
+__device__ __forceinline__ void lane_turns(const double* inv_freq, const LaneMap& m, int sub, uint64_t* F) {
+  constexpr int N = 4 / (32 / LPR);
+#pragma unroll
+  for (int i = 0; i < N; ++i) F[i] = m.turned ? turns_fixed(inv_freq[m.pair0 + sub * N + i]) : 0;
 }
 
 // x[0..3] the lane's first quad, x[4..7] its second
@@ -304,10 +322,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const LaneMap m = lane_map<INTER>(l, a.rot);
   float c[4], s[4];
   {
-    uint64_t F[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(a.inv_freq[m.pair0 + i]) : 0;
-    angles(F, m.turned, p, c, s);
+    uint64_t F[LPR / 8];
+    lane_turns<LPR>(a.inv_freq, m, sub, F);
+    angles<LPR>(F, m.turned, p, l, c, s);
   }
   if (r0 < a.Hq) {
     T* dst = (T*)a.qo.p + b * a.qo.b + t * a.qo.t;
@@ -348,6 +365,9 @@ struct RopeBwdArgs {
 };
 
 constexpr int kWarpsBwd = 4;
+// CTAs an SM has registers for, with eight rows of each warp in flight
+template <typename T, typename GI>
+constexpr int kBwdBlocks = sizeof(T) + sizeof(GI) == 4 ? 4 : 3;
 
 // Gradients of rows h0 .. h1 - 1 of one token and one kind; acc gathers the
 // lane's share of dw.
@@ -426,16 +446,15 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
 // The same mapping on a fixed grid whose warps stride over the items and keep
 // their shares of dw_q, dw_k in registers (8 entries of each a lane).
 template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kWarpsBwd * 32, 3) rope_bwd_kernel(RopeBwdArgs a) {
+__global__ void __launch_bounds__(kWarpsBwd * 32, kBwdBlocks<T, GI>) rope_bwd_kernel(RopeBwdArgs a) {
   constexpr int LPR = D / 8;
   cudaTriggerProgrammaticLaunchCompletion();  // rope_dw_kernel may be launched; it waits for this kernel's end
   __shared__ float red[kWarpsBwd][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const LaneMap m = lane_map<INTER>(l, a.rot);
-  uint64_t F[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(a.inv_freq[m.pair0 + i]) : 0;
+  uint64_t F[LPR / 8];
+  lane_turns<LPR>(a.inv_freq, m, sub, F);
   float aq[8], ak[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
@@ -447,7 +466,7 @@ __global__ void __launch_bounds__(kWarpsBwd * 32, 3) rope_bwd_kernel(RopeBwdArgs
     const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
     const int r1 = min(rows, r0 + a.rows_per_item);
     float c[4], s[4];
-    angles(F, m.turned, a.pos ? a.pos[b * a.pos_b + t] : a.pos0 + t, c, s);
+    angles<LPR>(F, m.turned, a.pos ? a.pos[b * a.pos_b + t] : a.pos0 + t, l, c, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = -s[i];
     if (r0 < a.Hq)
@@ -505,13 +524,14 @@ __global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk)
 }
 
 constexpr int kSMs = 152;
-constexpr int kBwdGrid = kSMs * 3;
+constexpr int kBwdGrid = kSMs * 4;  // at most
 
 // Rows a warp takes of one token: all of them when the tokens alone give
-// `want` warps their work, else split evenly so that short calls spread out.
+// `want` warps (those that run at once) their work, else an even share, so
+// that short calls spread out but stay one wave.
 void split_rows(long long tokens, int rows, int rpw, long long want, int* per_item, int* items) {
   const int most = (rows + rpw - 1) / rpw;
-  long long n = tokens > 0 ? (want + tokens - 1) / tokens : 1;
+  long long n = tokens > 0 ? want / tokens : 1;
   if (n > most) n = most;
   if (n < 1) n = 1;
   int per = (most + (int)n - 1) / (int)n * rpw;
@@ -548,7 +568,7 @@ template <bool PAGED>
 cudaError_t launch_fwd(RopeArgs& a, int dtype, int d, bool inter, bool vec, cudaStream_t st) {
   const long long tokens = (long long)a.B * a.L;
   const int rows = a.Hq + a.Hk * (PAGED ? 2 : 1);
-  split_rows(tokens, rows, 32 / (d / 8), (long long)kSMs * 64, &a.rows_per_item, &a.items_per_token);
+  split_rows(tokens, rows, 32 / (d / 8), (long long)kSMs * 3 * kWarps, &a.rows_per_item, &a.items_per_token);
   const long long items = tokens * a.items_per_token;
   const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
 #define NATS_ROPE(T, D, I, V) rope_fwd_kernel<T, D, I, PAGED, V><<<grid, kWarps * 32, 0, st>>>(a)
@@ -707,9 +727,11 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
   a.norm = dims->norm, a.eps = dims->eps;
   a.part = dw ? (float*)workspace : nullptr;
   const long long tokens = (long long)a.B * a.L;
-  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), kBwdGrid * kWarpsBwd, &a.rows_per_item, &a.items_per_token);
+  const int most = kSMs * (dims->dtype == NATS_BF16 && grad_dtype == NATS_BF16 ? kBwdBlocks<__nv_bfloat16, __nv_bfloat16>
+                                                                             : kBwdBlocks<float, float>);
+  split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), most * kWarpsBwd, &a.rows_per_item, &a.items_per_token);
   const long long ctas = (tokens * a.items_per_token + kWarpsBwd - 1) / kWarpsBwd;
-  const unsigned grid = (unsigned)(ctas < kBwdGrid ? ctas : kBwdGrid);
+  const unsigned grid = (unsigned)(ctas < most ? ctas : most);
   const bool inter = dims->interleaved != 0;
   const int d = dims->d;
   if (dims->dtype == NATS_F32)
