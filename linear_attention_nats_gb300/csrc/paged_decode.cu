@@ -116,19 +116,26 @@ __device__ __forceinline__ Run my_run(const PagedView& pg, int U, long long* pre
   return r;
 }
 
-// e^(m - M) factors in base 2, with 0 for an empty part
-__device__ __forceinline__ float part_scale(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
+// 2^x, the hardware's approximation (2 ulp; results below 2^-126 are 0)
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The maximum of no scores: below any real one, and finite, so that a score of
+// -inf less it is still -inf and two of it subtract to 0 (their sums are 0).
+constexpr float kNoMax = -1e38f;
+// the factor that brings sums taken at maximum m to maximum M >= m
+__device__ __forceinline__ float part_scale(float m, float M) { return pow2(m - M); }
 
-// A unit's result from the CTA's warps (shared memory) to the output or to
-// partial slot `slot` (-1: the output).
+// A unit's result from the CTA's warps (shared memory: so [kWarps][GT][D], sml
+// [kWarps][GT][2]) to the output or to partial slot `slot` (-1: the output).
 template <typename T, int D, int GT>
 __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const float* so, const float* sml, int b, int h0,
                                             int heads, long long slot) {
-  // so [kWarps][GT][D], sml [kWarps][GT][2]
-  for (int i = threadIdx.x; i < GT * D; i += kThreads) {
+  for (int i = threadIdx.x; i < heads * D; i += kThreads) {
     const int g = i / D, e = i % D;
-    if (g >= heads) break;
-    float M = -INFINITY;
+    float M = kNoMax;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * GT + g) * 2]);
     float l = 0.f, o = 0.f;
@@ -157,8 +164,8 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const float* so
 
 // ------------------------------------------------------ the two products
 //
-// Each warp takes 16 slots of every tile, on its own, and up to 8 NH heads of
-// a unit.  Both products run on the tensor cores with the slots or the
+// Each warp takes 16 slots of every tile, on its own, and the up to 8 NH heads
+// of a unit.  Both products run on the tensor cores with the slots or the
 // entries on the 16 rows of an instruction and the heads on its 8 columns,
 //   S^T [16 slots x 8 heads] += K Q^T,   O^T [16 entries x 8 heads] += V^T P^T,
 // so few heads waste little, and which entry (slot) carries which index of a
@@ -213,28 +220,24 @@ struct Bf16 {
 #pragma unroll
     for (int y = 0; y < KB; ++y) q.r[y] = on ? *(const uint4*)(p + 32 * y + 8 * c) : make_uint4(0, 0, 0, 0);
   }
-  static __device__ __forceinline__ void load_k(K& k, const T* p, int row, int g, int c) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int y = 0; y < KB; ++y)
-        k.r[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(p + (long long)(row + g + 8 * i) * D + 32 * y + 8 * c);
-  }
-  // (values of slots behind the sequence are zero: 0 x NaN would not be)
-  static __device__ __forceinline__ void load_v(V& v, const T* p, int row, int left, int g, int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-      for (int y = 0; y < VS; ++y)
-        v.r[i][y] = row < 0 || r >= left ? make_uint4(0, 0, 0, 0) : ldg_once(p + (long long)(row + r) * D + 64 * y + 8 * g);
-    }
-  }
-  static __device__ __forceinline__ void scores(float (&s)[4], const K& k, const Q& q) {
+  // where the lane's 16 bytes lie: entries from its first of the 16 slots' first
+  // row (k_base, v_base), and from there
+  static __device__ __forceinline__ int k_base(int g, int c) { return g * D + 8 * c; }
+  static constexpr __device__ int k_off(int i, int y) { return 8 * i * D + 32 * y; }
+  static __device__ __forceinline__ int v_slot(int i, int c) { return 2 * c + (i & 1) + 8 * (i >> 1); }
+  static __device__ __forceinline__ int v_base(int g, int c) { return 2 * c * D + 8 * g; }
+  static constexpr __device__ int v_off(int i, int y) { return ((i & 1) + 8 * (i >> 1)) * D + 64 * y; }
+  // ka(i, y): the lane's 16 bytes of its slot i in block y
+  template <int NH, class KA>
+  static __device__ __forceinline__ void scores(float (&s)[NH][4], KA ka, const Q (&q)[NH]) {
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
-      mma(s, k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y, q.r[y].x, q.r[y].y);
-      mma(s, k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w, q.r[y].z, q.r[y].w);
+      const uint4 k0 = ka(0, y), k1 = ka(1, y);
+#pragma unroll
+      for (int x = 0; x < NH; ++x) {
+        mma(s[x], k0.x, k1.x, k0.y, k1.y, q[x].r[y].x, q[x].r[y].y);
+        mma(s[x], k0.z, k1.z, k0.w, k1.w, q[x].r[y].z, q[x].r[y].w);
+      }
     }
   }
   template <int NH>
@@ -316,61 +319,51 @@ struct F32 {
 #pragma unroll
     for (int y = 0; y < KB; ++y) q.r[y] = on ? *(const float4*)(p + 16 * y + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  static __device__ __forceinline__ void load_k(K& k, const T* p, int row, int g, int c) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int y = 0; y < KB; ++y)
-        k.r[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(p + (long long)(row + g + 8 * i) * D + 16 * y + 4 * c);
-  }
-  static __device__ __forceinline__ void load_v(V& v, const T* p, int row, int left, int g, int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int y = 0; y < VS; ++y)
-        v.r[i][y] = row < 0 || c + 4 * i >= left ? make_uint4(0, 0, 0, 0)
-                                                 : ldg_once(p + (long long)(row + c + 4 * i) * D + 32 * y + 4 * g);
-  }
-  static __device__ __forceinline__ void scores(float (&s)[4], const K& k, const Q& q) {
+  static __device__ __forceinline__ int k_base(int g, int c) { return g * D + 4 * c; }
+  static constexpr __device__ int k_off(int i, int y) { return 8 * i * D + 16 * y; }
+  static __device__ __forceinline__ int v_slot(int i, int c) { return c + 4 * i; }
+  static __device__ __forceinline__ int v_base(int g, int c) { return c * D + 4 * g; }
+  static constexpr __device__ int v_off(int i, int y) { return 4 * i * D + 32 * y; }
+  template <int NH, class KA>
+  static __device__ __forceinline__ void scores(float (&s)[NH][4], KA ka, const Q (&q)[NH]) {
+    static_assert(NH == 1, "units of eight heads");
     float small[2][4] = {};
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
+      const uint4 k0 = ka(0, y), k1 = ka(1, y);
+      const float4 qy = q[0].r[y];
       float c0[4] = {}, c1[4] = {};
-      const uint32_t a0[4] = {k.r[0][y].x, k.r[1][y].x, k.r[0][y].y, k.r[1][y].y};
-      mma3(c0, small[0], a0, __float_as_uint(q.r[y].x), __float_as_uint(q.r[y].y));
-      const uint32_t a1[4] = {k.r[0][y].z, k.r[1][y].z, k.r[0][y].w, k.r[1][y].w};
-      mma3(c1, small[1], a1, __float_as_uint(q.r[y].z), __float_as_uint(q.r[y].w));
+      const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
+      mma3(c0, small[0], a0, __float_as_uint(qy.x), __float_as_uint(qy.y));
+      mma3(c1, small[1], a1, __float_as_uint(qy.z), __float_as_uint(qy.w));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += c0[i] + c1[i];
+      for (int i = 0; i < 4; ++i) s[0][i] += c0[i] + c1[i];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] += small[0][i] + small[1][i];
+    for (int i = 0; i < 4; ++i) s[0][i] += small[0][i] + small[1][i];
   }
   template <int NH>
   static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int g,
                                                 int c) {
+    // slots c, c + 4, c + 8, c + 12 of head g: from the lanes with that slot (and 8 on) and the head's pair
+    uint32_t b[4];
 #pragma unroll
-    for (int x = 0; x < NH; ++x) {
-      // slots c, c + 4, c + 8, c + 12 of head g: from the lanes with that slot (and 8 on) and the head's pair
-      uint32_t b[4];
+    for (int i = 0; i < 2; ++i) {
+      const int src = 4 * (c + 4 * i) + g / 2;
+      const float e0 = __shfl_sync(0xffffffffu, p[0][0], src), e1 = __shfl_sync(0xffffffffu, p[0][1], src);
+      const float e2 = __shfl_sync(0xffffffffu, p[0][2], src), e3 = __shfl_sync(0xffffffffu, p[0][3], src);
+      b[i] = __float_as_uint(g % 2 ? e1 : e0), b[i + 2] = __float_as_uint(g % 2 ? e3 : e2);
+    }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int src = 4 * (c + 4 * i) + g / 2;
-        const float e0 = __shfl_sync(0xffffffffu, p[x][0], src), e1 = __shfl_sync(0xffffffffu, p[x][1], src);
-        const float e2 = __shfl_sync(0xffffffffu, p[x][2], src), e3 = __shfl_sync(0xffffffffu, p[x][3], src);
-        b[i] = __float_as_uint(g % 2 ? e1 : e0), b[i + 2] = __float_as_uint(g % 2 ? e3 : e2);
-      }
+    for (int y = 0; y < MT; ++y) {
+      // rows g and g + 8 of tile y: entry y % 4 of the lane's segments 2 (y / 4) and 2 (y / 4) + 1
+      auto at = [&](int slot, int seg) { return ((const uint32_t*)&v.r[slot][2 * (y / 4) + seg])[y % 4]; };
+      const uint32_t a[4] = {at(0, 0), at(0, 1), at(1, 0), at(1, 1)}, a2[4] = {at(2, 0), at(2, 1), at(3, 0), at(3, 1)};
+      float full[4] = {}, small[4] = {};
+      mma3(full, small, a, b[0], b[1]);
+      mma3(full, small, a2, b[2], b[3]);
 #pragma unroll
-      for (int y = 0; y < MT; ++y) {
-        // rows g and g + 8 of tile y: entry y % 4 of the lane's segments 2 (y / 4) and 2 (y / 4) + 1
-        auto at = [&](int slot, int seg) { return ((const uint32_t*)&v.r[slot][2 * (y / 4) + seg])[y % 4]; };
-        const uint32_t a[4] = {at(0, 0), at(0, 1), at(1, 0), at(1, 1)}, a2[4] = {at(2, 0), at(2, 1), at(3, 0), at(3, 1)};
-        float full[4] = {}, small[4] = {};
-        mma3(full, small, a, b[0], b[1]);
-        mma3(full, small, a2, b[2], b[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[x][y][i] += full[i] + small[i];
-      }
+      for (int i = 0; i < 4; ++i) o[0][y][i] += full[i] + small[i];
     }
   }
   static __device__ __forceinline__ int entry(int y, int g, int upper) {
@@ -382,18 +375,143 @@ struct F32 {
 // before the sums are rescaled: 2^8 leaves fp32 its full precision
 constexpr float kSlack = 8.f;
 
-// A tile's K registers are refilled for the next tile as soon as the scores
-// are done, V's when the values are, page entries read two tiles ahead.
-template <class X, int NH, bool ACC, int BLOCKS>
+// The lane's keys and values of the 16 slots from `row` on (-1: none), zero
+// behind the sequence (0 x NaN would not be).
+template <class X>
+__device__ __forceinline__ void load_k(typename X::K& k, const typename X::T* p, int row, int g, int c) {
+  const typename X::T* at = p + (long long)row * X::kD + X::k_base(g, c);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int y = 0; y < X::KB; ++y) k.r[i][y] = row < 0 ? make_uint4(0, 0, 0, 0) : ldg_once(at + X::k_off(i, y));
+}
+template <class X>
+__device__ __forceinline__ void load_v(typename X::V& v, const typename X::T* p, int row, int left, int g, int c) {
+  const typename X::T* at = p + (long long)row * X::kD + X::v_base(g, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int y = 0; y < X::VS; ++y)
+      v.r[i][y] = row < 0 || X::v_slot(i, c) >= left ? make_uint4(0, 0, 0, 0) : ldg_once(at + X::v_off(i, y));
+}
+
+// A unit's heads as one warp holds them: queries, and the running maximum, sum
+// and weighted values of its slots.
+template <class X, int NH>
+struct Unit {
+  static constexpr int MT = X::MT;
+  typename X::Q q[NH];
+  // rise: the raw score from which the sums are rescaled
+  float o[NH][MT][4], mx[NH][2], sum[NH][2], rise[NH][2];
+
+  __device__ __forceinline__ void start(const typename X::T* q0, long long q_h, int heads, int g, int c) {
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+      X::load_q(q[x], q0 + (8 * x + g) * q_h, 8 * x + g < heads, c);
+#pragma unroll
+      for (int y = 0; y < MT; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[x][y][i] = 0.f;
+      mx[x][0] = mx[x][1] = kNoMax;
+      rise[x][0] = rise[x][1] = -INFINITY;
+      sum[x][0] = sum[x][1] = 0.f;
+    }
+  }
+
+  // The raw scores s of 16 slots become their weights; lo, hi: whether slots g
+  // and g + 8 count (all: every slot does).  at: where the slots' scores go
+  // (accumulation), slot 0's first head, of `left` slots.
+  template <bool ACC>
+  __device__ __forceinline__ void weigh(float (&s)[NH][4], float scale2, bool all, bool lo, bool hi, float* at, int G,
+                                        int left, int heads, int g, int c) {
+    if (!all) {
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] = (i < 2 ? lo : hi) ? s[x][i] : -INFINITY;
+    }
+    bool rises = false;
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+      if (ACC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = g + 8 * (i >> 1), h = 8 * x + 2 * c + (i & 1);
+          if (j < left && h < heads) at[(long long)j * G + h] = s[x][i] * scale2;
+        }
+      }
+      rises |= fmaxf(s[x][0], s[x][2]) > rise[x][0] || fmaxf(s[x][1], s[x][3]) > rise[x][1];
+    }
+    if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float m = fmaxf(s[x][i], s[x][i + 2]);
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+          m = fmaxf(m * scale2, mx[x][i]);
+          const float f = part_scale(mx[x][i], m);
+          mx[x][i] = m;
+          if (m > kNoMax) rise[x][i] = (m + kSlack) / scale2;
+          sum[x][i] *= f;
+#pragma unroll
+          for (int y = 0; y < MT; ++y) o[x][y][i] *= f, o[x][y][i + 2] *= f;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the scaled score is not rounded before the maximum is subtracted
+        s[x][i] = pow2(fmaf(s[x][i], scale2, -mx[x][i & 1]));
+        sum[x][i & 1] += s[x][i];
+      }
+  }
+
+  // to shared memory, so [8 NH][D], sml [8 NH][2] of this warp
+  __device__ __forceinline__ void put(float* so, float* sml, int g, int c) {
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int z = 4; z < 32; z <<= 1) sum[x][i] += __shfl_xor_sync(0xffffffffu, sum[x][i], z);
+        const int h = 8 * x + 2 * c + i;
+        if (g == 0) sml[h * 2] = mx[x][i], sml[h * 2 + 1] = sum[x][i];
+        float* at = so + h * X::kD;
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          at[X::entry(y, g, 0)] = o[x][y][i];
+          at[X::entry(y, g, 1)] = o[x][y][i + 2];
+        }
+      }
+  }
+};
+
+// Copies 16 bytes to shared memory (zeros unless `on`) without a register.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+// STAGES == 0 (units of eight heads): a step's K registers are refilled for the
+// next one as soon as the scores are done, V's when the values are.  STAGES > 0
+// (sixteen: their queries and sums leave no registers for rows in flight): the
+// lane's rows come through a ring in shared memory of which it reads only what
+// it copied itself, so the ring needs no barrier.  Page entries are read a step
+// ahead of their rows.
+template <class X, int NH, int STAGES, bool ACC, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) {
   using T = typename X::T;
-  constexpr int D = X::kD, MT = X::MT, GT = 8 * NH;
+  constexpr int D = X::kD, GT = 8 * NH, KB = X::KB, VS = X::VS, kChunks = 2 * KB + 4 * VS;
   cudaTriggerProgrammaticLaunchCompletion();  // the next kernel may be launched; it waits for this one's end
-  __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
+  __shared__ float so[STAGES ? 1 : kWarps * GT * D], sml[kWarps * GT * 2];
+  extern __shared__ uint4 ring_all[];  // [kWarps][STAGES][kChunks][32]; at the end of a unit the warps' results
   const int U = a.pg.Hk * a.ngroups;
   const Run run = my_run(a.pg, U, a.prefix);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const T *kp = (const T*)a.k, *vp = (const T*)a.v;
+  float* const out = STAGES ? (float*)ring_all : so;
   long long cur = run.s, pre = run.pre;
   int b = run.b0;
   while (cur < run.e) {
@@ -408,18 +526,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
     const int hk = u / a.ngroups, g0 = (u % a.ngroups) * GT;
     const int heads = min(GT, a.G - g0), h0 = hk * a.G + g0;
-    typename X::Q q[NH];
-    float o[NH][MT][4], mx[NH][2], sum[NH][2];
-#pragma unroll
-    for (int x = 0; x < NH; ++x) {
-      X::load_q(q[x], (const T*)a.q + b * a.q_b + (h0 + 8 * x + g) * a.q_h, 8 * x + g < heads, c);
-#pragma unroll
-      for (int y = 0; y < MT; ++y)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[x][y][i] = 0.f;
-      mx[x][0] = mx[x][1] = -INFINITY;
-      sum[x][0] = sum[x][1] = 0.f;
-    }
+    Unit<X, NH> unit;
+    unit.start((const T*)a.q + b * a.q_b + h0 * a.q_h, a.q_h, heads, g, c);
     // row of this warp's first slot in tile t, or -1: past the end or without a page
     auto first_row = [&](int t) -> int {
       const int j0 = t * kTile + warp * 16;
@@ -431,87 +539,81 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       }
       return (int)a.pg.row(pg, hk, j0 % a.pg.page);
     };
-    typename X::K k;
-    typename X::V v;
-    int row = first_row(t0), next = first_row(t0 + 1);
-    X::load_k(k, kp, row, g, c);
-    X::load_v(v, vp, row, n - t0 * kTile - warp * 16, g, c);
-    for (int t = t0; t < t1; ++t) {
+    auto step = [&](int t, bool on, auto ka, auto after_scores, const typename X::V& v) {
       const int j0 = t * kTile + warp * 16;
-      const int after = first_row(t + 2);
-      float s[NH][4];
-#pragma unroll
-      for (int x = 0; x < NH; ++x) {
-        s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-        X::scores(s[x], k, q[x]);
+      float s[NH][4] = {};
+      X::scores(s, ka, unit.q);
+      after_scores();
+      float* at = ACC ? a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j0) * a.G + g0 : nullptr;
+      unit.template weigh<ACC>(s, a.scale2, on && j0 + 16 <= n, on && j0 + g < n, on && j0 + g + 8 < n, at, a.G, n - j0,
+                               heads, g, c);
+      X::values(unit.o, v, s, g, c);
+    };
+    if constexpr (STAGES == 0) {
+      typename X::K k;
+      typename X::V v;
+      int row = first_row(t0), next = first_row(t0 + 1);
+      load_k<X>(k, kp, row, g, c);
+      load_v<X>(v, vp, row, n - t0 * kTile - warp * 16, g, c);
+      for (int t = t0; t < t1; ++t) {
+        const int after = first_row(t + 2);
+        step(t, row >= 0, [&](int i, int y) { return k.r[i][y]; }, [&] { load_k<X>(k, kp, next, g, c); }, v);
+        load_v<X>(v, vp, next, n - (t + 1) * kTile - warp * 16, g, c);
+        row = next;
+        next = after;
       }
-      X::load_k(k, kp, next, g, c);
-      const bool lo = row >= 0 && j0 + g < n, hi = row >= 0 && j0 + g + 8 < n;
-      bool rises = false;
+    } else {
+      uint4* ring = ring_all + (size_t)warp * STAGES * kChunks * 32 + lane;
+      uint32_t have = 0;  // bit t % 32: tile t has a page
+      auto fetch = [&](int t, int row) {
+        const int left = n - t * kTile - warp * 16;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + (t - t0) % STAGES * kChunks * 32);
+        have = (have & ~(1u << (t & 31))) | (row >= 0 ? 1u << (t & 31) : 0u);
+        const bool on = row >= 0;  // (else from the pool's first rows, of which nothing is read)
+        const T *ka = kp + (long long)max(row, 0) * D + X::k_base(g, c), *va = vp + (long long)max(row, 0) * D + X::v_base(g, c);
 #pragma unroll
-      for (int x = 0; x < NH; ++x) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[x][i] = (i < 2 ? lo : hi) ? s[x][i] : -INFINITY;
-        if (ACC) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + g + 8 * (i >> 1), h = 8 * x + 2 * c + (i & 1);
-            if (j < n && h < heads)
-              a.scores[(((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G + g0 + h] = s[x][i] * a.scale2;
-          }
-        }
-        rises |= fmaxf(s[x][0], s[x][2]) * a.scale2 > mx[x][0] + kSlack ||
-                 fmaxf(s[x][1], s[x][3]) * a.scale2 > mx[x][1] + kSlack;
-      }
-      if (__any_sync(0xffffffffu, rises)) {
-#pragma unroll
-        for (int x = 0; x < NH; ++x)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float m = fmaxf(s[x][i], s[x][i + 2]);
-#pragma unroll
-            for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-            m = fmaxf(m * a.scale2, mx[x][i]);
-            const float f = part_scale(mx[x][i], m);
-            mx[x][i] = m;
-            sum[x][i] *= f;
-#pragma unroll
-            for (int y = 0; y < MT; ++y) o[x][y][i] *= f, o[x][y][i + 2] *= f;
-          }
-      }
-#pragma unroll
-      for (int x = 0; x < NH; ++x)
+          for (int y = 0; y < KB; ++y) cp_async16(to + (i * KB + y) * 512, ka + X::k_off(i, y), on);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // the scaled score is not rounded before the maximum is subtracted
-          // (a head without a slot yet has no maximum: its scores are all -inf)
-          s[x][i] = s[x][i] == -INFINITY ? 0.f : exp2f(fmaf(s[x][i], a.scale2, -mx[x][i & 1]));
-          sum[x][i & 1] += s[x][i];
+          const bool in = on && X::v_slot(i, c) < left;
+#pragma unroll
+          for (int y = 0; y < VS; ++y) cp_async16(to + (2 * KB + i * VS + y) * 512, va + X::v_off(i, y), in);
         }
-      X::template values<NH>(o, v, s, g, c);
-      X::load_v(v, vp, next, n - j0 - kTile, g, c);
-      row = next;
-      next = after;
-    }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      int next = first_row(t0);
 #pragma unroll
-    for (int x = 0; x < NH; ++x) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int z = 4; z < 32; z <<= 1) sum[x][i] += __shfl_xor_sync(0xffffffffu, sum[x][i], z);
-        const int h = 8 * x + 2 * c + i;
-        if (g == 0) sml[(warp * GT + h) * 2] = mx[x][i], sml[(warp * GT + h) * 2 + 1] = sum[x][i];
-        float* at = so + (warp * GT + h) * D;
-#pragma unroll
-        for (int y = 0; y < MT; ++y) {
-          at[X::entry(y, g, 0)] = o[x][y][i];
-          at[X::entry(y, g, 1)] = o[x][y][i + 2];
-        }
+      for (int i = 0; i < STAGES - 1; ++i) {
+        const int row = next;
+        next = first_row(t0 + i + 1);
+        fetch(t0 + i, row);
       }
+      for (int t = t0; t < t1; ++t) {
+        const int row = next;
+        next = first_row(t + STAGES);
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        const uint4* at = ring + (t - t0) % STAGES * kChunks * 32;
+        typename X::V v;
+        step(t, (have >> (t & 31)) & 1, [&](int i, int y) { return at[(i * KB + y) * 32]; },
+             [&] {
+#pragma unroll
+               for (int i = 0; i < 4; ++i)
+#pragma unroll
+                 for (int y = 0; y < VS; ++y) v.r[i][y] = at[(2 * KB + i * VS + y) * 32];
+               // the stage read last: its registers have been used
+               fetch(t + STAGES - 1, row);
+             },
+             v);
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();  // the ring becomes the results' place
     }
+    unit.put(out + warp * GT * D, sml + warp * GT * 2, g, c);
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    finish_unit<T, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
+    finish_unit<T, D, GT>(a, out, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
     __syncthreads();
     cur += t1 - t0;
   }
@@ -551,7 +653,7 @@ __device__ __forceinline__ Parts parts_of(long long pre, long long nt, long long
 // One warp: maximum and sum of head g's partials, the lanes side by side.
 __device__ __forceinline__ void join_sums(const DecodeArgs& a, const Parts& p, int g, float& M, float& l) {
   const int lane = threadIdx.x & 31;
-  M = -INFINITY, l = 0.f;
+  M = kNoMax, l = 0.f;
   for (int c = p.c0 + lane; c <= p.c1; c += 32) {
     const float2 ml = *(const float2*)(a.part_ml + 2 * (p.slot(c) * a.GT + g));
     const float m = fmaxf(M, ml.x);
@@ -564,24 +666,26 @@ __device__ __forceinline__ void join_sums(const DecodeArgs& a, const Parts& p, i
 }
 __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : M + log2f(l); }
 
-// Row i = (sequence, query head), one warp: joins the unit's partials, or
-// writes the row of an empty sequence.
-template <typename T, int D>
+// Row i = (sequence, query head): joins the unit's partials, or writes the row
+// of an empty sequence.  W warps share the partials: one where there are rows
+// enough, the whole CTA for few.
+template <typename T, int D, int W>
 __device__ __forceinline__ void join_row(const DecodeArgs& a, int grid, long long i) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  __shared__ float red[W > 1 ? W * D : 1];
+  const int lane = threadIdx.x & 31, w = W > 1 ? threadIdx.x >> 5 : 0;
   const int b = (int)(i / a.Hq), h = (int)(i % a.Hq);
   const int hk = h / a.G, g = (h % a.G) % a.GT, u = hk * a.ngroups + (h % a.G) / a.GT;
   const long long pre = a.prefix[b], nt = a.prefix[b + 1] - pre;
-  float o[E], M = -INFINITY, l = 0.f;
+  float o[E], M = kNoMax, l = 0.f;
 #pragma unroll
   for (int x = 0; x < E; ++x) o[x] = 0.f;
   if (nt > 0) {
     const Parts p = parts_of(pre, nt, a.prefix[a.pg.B], u, a.pg.Hk * a.ngroups, grid);
-    if (p.one) return;
+    if (p.one) return;  // (every warp of the row)
     join_sums(a, p, g, M, l);
 #pragma unroll 8
-    for (int c = p.c0; c <= p.c1; ++c) {
+    for (int c = p.c0 + w; c <= p.c1; c += W) {
       const long long s = p.slot(c) * a.GT + g;
       const float f = part_scale(a.part_ml[2 * s], M);
       const float* at = a.part_o + s * D + lane * E;
@@ -593,7 +697,18 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, int grid, long lon
         o[0] += f * v.x, o[1] += f * v.y;
       }
     }
+    if (W > 1) {
+#pragma unroll
+      for (int x = 0; x < E; ++x) red[w * D + lane * E + x] = o[x];
+      __syncthreads();
+      if (w > 0) return;
+#pragma unroll
+      for (int r = 1; r < W; ++r)
+#pragma unroll
+        for (int x = 0; x < E; ++x) o[x] += red[r * D + lane * E + x];
+    }
   }
+  if (w > 0) return;
 #pragma unroll
   for (int x = 0; x < E; ++x) ((T*)a.out)[i * D + lane * E + x] = from_f32<T>(l == 0.f ? 0.f : o[x] / l);
   if (a.lse && lane == 0) a.lse[i] = lse_of(M, l);
@@ -646,7 +761,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int grid, int i
         x[i] = scores + (long long)min(ji, end - 1) * G;
         w[i] = 0.f;
       }
-      auto add = [&](int i, float v, int g) { w[i] += v == -INFINITY ? 0.f : exp2f(v - lse[g]); };
+      auto add = [&](int i, float v, int g) { w[i] += v == -INFINITY ? 0.f : pow2(v - lse[g]); };
       if (G % 4 == 0) {
         for (int g = 0; g < G; g += 4) {
           float4 v[kSlots];
@@ -673,14 +788,14 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int grid, int i
   }
 }
 
-// The first CTAs join, a row a warp; the others (accumulation) add weights.
-// Both read what the decode kernel left and wait for its end.
-template <typename T, int D>
+// The first CTAs join; the others (accumulation) add weights.  Both read what
+// the decode kernel left and wait for its end.
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int grid, int join_ctas) {
   cudaGridDependencySynchronize();
   if ((int)blockIdx.x < join_ctas) {
-    const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (i < (long long)a.pg.B * a.Hq) join_row<T, D>(a, grid, i);
+    const long long i = W > 1 ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (i < (long long)a.pg.B * a.Hq) join_row<T, D, W>(a, grid, i);
   } else {
     add_weights(a, grid, blockIdx.x - join_ctas, gridDim.x - join_ctas);
   }
@@ -736,35 +851,42 @@ cudaError_t after(void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Units of eight heads; bf16 groups of more than eight in units of sixteen,
-// whose rows are then read once (fp32 has not the registers: their second
-// reading comes from L2).
-template <int D>
-cudaError_t launch(DecodeArgs& a, int dtype, cudaStream_t st) {
-  const bool wide = dtype == NATS_BF16 && a.G > 8;
-  a.GT = wide ? 16 : 8;
+// BLOCKS: the CTAs an SM has registers (or shared memory) for.
+template <class X, int NH, int STAGES, int BLOCKS>
+cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
+  using T = typename X::T;
+  constexpr int D = X::kD;
+  constexpr size_t kRing = (size_t)kWarps * STAGES * (2 * X::KB + 4 * X::VS) * 32 * 16;
+  static_assert(STAGES == 0 || kRing >= sizeof(float) * kWarps * 8 * NH * D, "the results take the ring's place");
+  a.GT = 8 * NH;
   a.ngroups = (a.G + a.GT - 1) / a.GT;
-  // CTAs an SM has registers for
-  constexpr int kBlocks = D == 64 ? 4 : 3, kBlocksF32 = D == 64 ? 3 : 2, kBlocksWide = 2;
-  const int ctas = kSMs * (dtype != NATS_BF16 ? kBlocksF32 : wide ? kBlocksWide : kBlocks);
   const bool acc = a.scores != nullptr;
-#define NATS_DECODE(X, NH, BLOCKS)                                                 \
-  (acc ? decode_kernel<X, NH, true, BLOCKS><<<ctas, kThreads, 0, st>>>(a)          \
-       : decode_kernel<X, NH, false, BLOCKS><<<ctas, kThreads, 0, st>>>(a))
-  if (dtype != NATS_BF16)
-    NATS_DECODE(F32<D>, 1, kBlocksF32);
-  else if (wide)
-    NATS_DECODE(Bf16<D>, 2, kBlocksWide);
-  else
-    NATS_DECODE(Bf16<D>, 1, kBlocks);
-#undef NATS_DECODE
-  cudaError_t e = cudaGetLastError();
+  const int ctas = kSMs * BLOCKS;
+  auto kernel = acc ? decode_kernel<X, NH, STAGES, true, BLOCKS> : decode_kernel<X, NH, STAGES, false, BLOCKS>;
+  if (kRing > 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRing);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<ctas, kThreads, kRing, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int join = (int)(((long long)a.pg.B * a.Hq + kWarps - 1) / kWarps);
+  // a CTA a row while the rows are no more than two waves of CTAs, so that a
+  // long unit's many partials (up to one a CTA) are read by four warps
+  const long long rows = (long long)a.pg.B * a.Hq;
+  const bool few = rows <= kSMs * 16;
+  const int join = (int)(few ? rows : (rows + kWarps - 1) / kWarps);
   const unsigned grid = join + (acc ? kSMs * 8 : 0);
   const size_t smem = acc ? 4 * (size_t)a.G : 0;
-  return dtype == NATS_BF16 ? after(decode_finish_kernel<__nv_bfloat16, D>, grid, smem, st, a, ctas, join)
-                            : after(decode_finish_kernel<float, D>, grid, smem, st, a, ctas, join);
+  return few ? after(decode_finish_kernel<T, D, kWarps>, grid, smem, st, a, ctas, join)
+             : after(decode_finish_kernel<T, D, 1>, grid, smem, st, a, ctas, join);
+}
+
+// Units of eight heads; bf16 groups of more than eight in units of sixteen,
+// whose rows are then read once.
+cudaError_t launch(DecodeArgs& a, int dtype, int d, cudaStream_t st) {
+  if (dtype != NATS_BF16) return d == 128 ? launch<F32<128>, 1, 0, 2>(a, st) : launch<F32<64>, 1, 0, 3>(a, st);
+  if (a.G > 8) return d == 128 ? launch<Bf16<128>, 2, 3, 2>(a, st) : launch<Bf16<64>, 2, 4, 3>(a, st);
+  return d == 128 ? launch<Bf16<128>, 1, 0, 3>(a, st) : launch<Bf16<64>, 1, 0, 4>(a, st);
 }
 
 }  // namespace
@@ -794,12 +916,14 @@ nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float s
   if ((q_stride_b * es) % 16 != 0 || (q_stride_h * es) % 16 != 0 || ((uintptr_t)lse & 3u)) return NATS_ERR_ALIGN;
   DecodeArgs a;
   if (workspace_bytes < layout(cache, Hq, accumulate != 0, (char*)workspace, &a)) return NATS_ERR_WORKSPACE;
-  a.pg = view_of(cache), a.k = cache->k_pages, a.v = cache->v_pages, a.weight = cache->weight;
+  a.pg = view_of(cache);
+  if (cache->n_pages == 0) a.pg.max_pages = 0;  // no slot can have a page
+  a.k = cache->k_pages, a.v = cache->v_pages, a.weight = cache->weight;
   a.q = q, a.q_b = q_stride_b, a.q_h = q_stride_h, a.out = out, a.lse = lse;
   a.Hq = Hq, a.G = Hq / cache->Hk;
   a.scale2 = (scale > 0.f ? scale : 1.0f / std::sqrt((float)cache->d)) * kLog2e;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = cache->d == 128 ? launch<128>(a, cache->dtype, st) : launch<64>(a, cache->dtype, st);
+  const cudaError_t e = launch(a, cache->dtype, cache->d, st);
   return (nats_status)record_cuda_error(e);
 }
 

@@ -62,6 +62,9 @@ DECODE = [
     ([210], 1, 24, 64, 16, F32),
     ([9000, 3], 2, 3, 128, 16, F32),
     ([20000], 1, 7, 128, 64, BF),
+    ([130, 50, 0, 1000], 1, 40, 64, 16, BF),
+    ([257, 64], 2, 20, 128, 32, F32),
+    ([5000, 300], 1, 32, 128, 64, BF),
     ([3] * 150 + [200] + [0] * 40, 1, 2, 64, 16, BF),
 ]
 
