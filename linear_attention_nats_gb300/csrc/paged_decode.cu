@@ -227,12 +227,11 @@ struct Bf16 {
   static __device__ __forceinline__ int v_slot(int i, int c) { return 2 * c + (i & 1) + 8 * (i >> 1); }
   static __device__ __forceinline__ int v_base(int g, int c) { return 2 * c * D + 8 * g; }
   static constexpr __device__ int v_off(int i, int y) { return ((i & 1) + 8 * (i >> 1)) * D + 64 * y; }
-  // ka(i, y): the lane's 16 bytes of its slot i in block y
-  template <int NH, class KA>
-  static __device__ __forceinline__ void scores(float (&s)[NH][4], KA ka, const Q (&q)[NH]) {
+  template <int NH>
+  static __device__ __forceinline__ void scores(float (&s)[NH][4], const K& k, const Q (&q)[NH]) {
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
-      const uint4 k0 = ka(0, y), k1 = ka(1, y);
+      const uint4 k0 = k.r[0][y], k1 = k.r[1][y];
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
         mma(s[x], k0.x, k1.x, k0.y, k1.y, q[x].r[y].x, q[x].r[y].y);
@@ -324,13 +323,13 @@ struct F32 {
   static __device__ __forceinline__ int v_slot(int i, int c) { return c + 4 * i; }
   static __device__ __forceinline__ int v_base(int g, int c) { return c * D + 4 * g; }
   static constexpr __device__ int v_off(int i, int y) { return 4 * i * D + 32 * y; }
-  template <int NH, class KA>
-  static __device__ __forceinline__ void scores(float (&s)[NH][4], KA ka, const Q (&q)[NH]) {
+  template <int NH>
+  static __device__ __forceinline__ void scores(float (&s)[NH][4], const K& k, const Q (&q)[NH]) {
     static_assert(NH == 1, "units of eight heads");
     float small[2][4] = {};
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
-      const uint4 k0 = ka(0, y), k1 = ka(1, y);
+      const uint4 k0 = k.r[0][y], k1 = k.r[1][y];
       const float4 qy = q[0].r[y];
       float c0[4] = {}, c1[4] = {};
       const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
@@ -489,29 +488,19 @@ struct Unit {
   }
 };
 
-// Copies 16 bytes to shared memory (zeros unless `on`) without a register.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-
-// STAGES == 0 (units of eight heads): a step's K registers are refilled for the
-// next one as soon as the scores are done, V's when the values are.  STAGES > 0
-// (sixteen: their queries and sums leave no registers for rows in flight): the
-// lane's rows come through a ring in shared memory of which it reads only what
-// it copied itself, so the ring needs no barrier.  Page entries are read a step
-// ahead of their rows.
-template <class X, int NH, int STAGES, bool ACC, int BLOCKS>
+// A step's K registers are refilled for the next one as soon as the scores are
+// done, V's when the values are, so that a warp has some 8 KB on their way all
+// the time; page entries are read a step ahead of their rows.
+template <class X, int NH, bool ACC, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) {
   using T = typename X::T;
-  constexpr int D = X::kD, GT = 8 * NH, KB = X::KB, VS = X::VS, kChunks = 2 * KB + 4 * VS;
+  constexpr int D = X::kD, GT = 8 * NH;
   cudaTriggerProgrammaticLaunchCompletion();  // the next kernel may be launched; it waits for this one's end
-  __shared__ float so[STAGES ? 1 : kWarps * GT * D], sml[kWarps * GT * 2];
-  extern __shared__ uint4 ring_all[];  // [kWarps][STAGES][kChunks][32]; at the end of a unit the warps' results
+  __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
   const int U = a.pg.Hk * a.ngroups;
   const Run run = my_run(a.pg, U, a.prefix);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const T *kp = (const T*)a.k, *vp = (const T*)a.v;
-  float* const out = STAGES ? (float*)ring_all : so;
   long long cur = run.s, pre = run.pre;
   int b = run.b0;
   while (cur < run.e) {
@@ -539,81 +528,28 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       }
       return (int)a.pg.row(pg, hk, j0 % a.pg.page);
     };
-    auto step = [&](int t, bool on, auto ka, auto after_scores, const typename X::V& v) {
-      const int j0 = t * kTile + warp * 16;
+    typename X::K k;
+    typename X::V v;
+    int row = first_row(t0), next = first_row(t0 + 1);
+    load_k<X>(k, kp, row, g, c);
+    load_v<X>(v, vp, row, n - t0 * kTile - warp * 16, g, c);
+    for (int t = t0; t < t1; ++t) {
+      const int j0 = t * kTile + warp * 16, after = first_row(t + 2);
       float s[NH][4] = {};
-      X::scores(s, ka, unit.q);
-      after_scores();
+      X::scores(s, k, unit.q);
+      load_k<X>(k, kp, next, g, c);
       float* at = ACC ? a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j0) * a.G + g0 : nullptr;
-      unit.template weigh<ACC>(s, a.scale2, on && j0 + 16 <= n, on && j0 + g < n, on && j0 + g + 8 < n, at, a.G, n - j0,
-                               heads, g, c);
+      unit.template weigh<ACC>(s, a.scale2, row >= 0 && j0 + 16 <= n, row >= 0 && j0 + g < n, row >= 0 && j0 + g + 8 < n,
+                               at, a.G, n - j0, heads, g, c);
       X::values(unit.o, v, s, g, c);
-    };
-    if constexpr (STAGES == 0) {
-      typename X::K k;
-      typename X::V v;
-      int row = first_row(t0), next = first_row(t0 + 1);
-      load_k<X>(k, kp, row, g, c);
-      load_v<X>(v, vp, row, n - t0 * kTile - warp * 16, g, c);
-      for (int t = t0; t < t1; ++t) {
-        const int after = first_row(t + 2);
-        step(t, row >= 0, [&](int i, int y) { return k.r[i][y]; }, [&] { load_k<X>(k, kp, next, g, c); }, v);
-        load_v<X>(v, vp, next, n - (t + 1) * kTile - warp * 16, g, c);
-        row = next;
-        next = after;
-      }
-    } else {
-      uint4* ring = ring_all + (size_t)warp * STAGES * kChunks * 32 + lane;
-      uint32_t have = 0;  // bit t % 32: tile t has a page
-      auto fetch = [&](int t, int row) {
-        const int left = n - t * kTile - warp * 16;
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + (t - t0) % STAGES * kChunks * 32);
-        have = (have & ~(1u << (t & 31))) | (row >= 0 ? 1u << (t & 31) : 0u);
-        const bool on = row >= 0;  // (else from the pool's first rows, of which nothing is read)
-        const T *ka = kp + (long long)max(row, 0) * D + X::k_base(g, c), *va = vp + (long long)max(row, 0) * D + X::v_base(g, c);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int y = 0; y < KB; ++y) cp_async16(to + (i * KB + y) * 512, ka + X::k_off(i, y), on);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = on && X::v_slot(i, c) < left;
-#pragma unroll
-          for (int y = 0; y < VS; ++y) cp_async16(to + (2 * KB + i * VS + y) * 512, va + X::v_off(i, y), in);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-      int next = first_row(t0);
-#pragma unroll
-      for (int i = 0; i < STAGES - 1; ++i) {
-        const int row = next;
-        next = first_row(t0 + i + 1);
-        fetch(t0 + i, row);
-      }
-      for (int t = t0; t < t1; ++t) {
-        const int row = next;
-        next = first_row(t + STAGES);
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        const uint4* at = ring + (t - t0) % STAGES * kChunks * 32;
-        typename X::V v;
-        step(t, (have >> (t & 31)) & 1, [&](int i, int y) { return at[(i * KB + y) * 32]; },
-             [&] {
-#pragma unroll
-               for (int i = 0; i < 4; ++i)
-#pragma unroll
-                 for (int y = 0; y < VS; ++y) v.r[i][y] = at[(2 * KB + i * VS + y) * 32];
-               // the stage read last: its registers have been used
-               fetch(t + STAGES - 1, row);
-             },
-             v);
-      }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();  // the ring becomes the results' place
+      load_v<X>(v, vp, next, n - j0 - kTile, g, c);
+      row = next;
+      next = after;
     }
-    unit.put(out + warp * GT * D, sml + warp * GT * 2, g, c);
+    unit.put(so + warp * GT * D, sml + warp * GT * 2, g, c);
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    finish_unit<T, D, GT>(a, out, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
+    finish_unit<T, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
     __syncthreads();
     cur += t1 - t0;
   }
@@ -851,23 +787,19 @@ cudaError_t after(void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// BLOCKS: the CTAs an SM has registers (or shared memory) for.
-template <class X, int NH, int STAGES, int BLOCKS>
+// BLOCKS: the CTAs an SM has registers for.
+template <class X, int NH, int BLOCKS>
 cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
   using T = typename X::T;
   constexpr int D = X::kD;
-  constexpr size_t kRing = (size_t)kWarps * STAGES * (2 * X::KB + 4 * X::VS) * 32 * 16;
-  static_assert(STAGES == 0 || kRing >= sizeof(float) * kWarps * 8 * NH * D, "the results take the ring's place");
   a.GT = 8 * NH;
   a.ngroups = (a.G + a.GT - 1) / a.GT;
   const bool acc = a.scores != nullptr;
   const int ctas = kSMs * BLOCKS;
-  auto kernel = acc ? decode_kernel<X, NH, STAGES, true, BLOCKS> : decode_kernel<X, NH, STAGES, false, BLOCKS>;
-  if (kRing > 0) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRing);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<ctas, kThreads, kRing, st>>>(a);
+  if (acc)
+    decode_kernel<X, NH, true, BLOCKS><<<ctas, kThreads, 0, st>>>(a);
+  else
+    decode_kernel<X, NH, false, BLOCKS><<<ctas, kThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a CTA a row while the rows are no more than two waves of CTAs, so that a
@@ -882,11 +814,11 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
 }
 
 // Units of eight heads; bf16 groups of more than eight in units of sixteen,
-// whose rows are then read once.
+// whose rows are then read once (fp32 has not the registers).
 cudaError_t launch(DecodeArgs& a, int dtype, int d, cudaStream_t st) {
-  if (dtype != NATS_BF16) return d == 128 ? launch<F32<128>, 1, 0, 2>(a, st) : launch<F32<64>, 1, 0, 3>(a, st);
-  if (a.G > 8) return d == 128 ? launch<Bf16<128>, 2, 3, 2>(a, st) : launch<Bf16<64>, 2, 4, 3>(a, st);
-  return d == 128 ? launch<Bf16<128>, 1, 0, 3>(a, st) : launch<Bf16<64>, 1, 0, 4>(a, st);
+  if (dtype != NATS_BF16) return d == 128 ? launch<F32<128>, 1, 2>(a, st) : launch<F32<64>, 1, 3>(a, st);
+  if (a.G > 8) return d == 128 ? launch<Bf16<128>, 2, 2>(a, st) : launch<Bf16<64>, 2, 3>(a, st);
+  return d == 128 ? launch<Bf16<128>, 1, 3>(a, st) : launch<Bf16<64>, 1, 4>(a, st);
 }
 
 }  // namespace
