@@ -37,7 +37,7 @@ struct DecodeArgs {
   float* lse;
   int Hq, G, GT, ngroups;  // heads of a group, of a unit, units of a group
   float scale2;            // scale log2 e
-  long long* prefix;       // [B + 1] tiles before each sequence
+  long long* prefix;       // [B + 2] tiles before each sequence, all, and the CTAs that share them
   float* lse_ws;           // [B, Hq]
   float* part_ml;          // [2 ctas, GT, 2]
   float* part_o;           // [2 ctas, GT, D]
@@ -49,6 +49,12 @@ __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile;
 
 // CTAs that share T tiles: none has an empty run.
 __device__ __forceinline__ int ctas_used(long long T, int grid) { return (int)min(T, (long long)grid); }
+// Of the decode kernel: runs of at least four tiles where units would otherwise
+// fall into more than 32 parts each, whose joining then costs more than the
+// shorter runs save (1 x 8192 slots, 2 key heads: 18 us without, 12.6 with).
+__device__ __forceinline__ int decode_ctas(long long T, long long units, int grid) {
+  return ctas_used(min(T, max(32 * units, T / 4)), grid);
+}
 
 // This CTA's run [s, e) of the tile line, and the sequence b0 (with `pre`
 // tiles before it) in which it starts.  Every thread calls it; CTA 0 also
@@ -58,24 +64,30 @@ struct Run {
   int b0;
 };
 __device__ __forceinline__ Run my_run(const PagedView& pg, int U, long long* prefix) {
-  __shared__ long long red[kWarps + 1], found[2];
+  __shared__ long long red[kWarps], found[2];
+  __shared__ int red_seqs[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long mine = 0;
-  for (int b = tid; b < pg.B; b += kThreads) mine += tiles_of(pg.length(b));
+  int seqs = 0;  // that have slots
+  for (int b = tid; b < pg.B; b += kThreads) {
+    const int t = tiles_of(pg.length(b));
+    mine += t, seqs += t > 0;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) red[warp] = mine;
+  seqs = __reduce_add_sync(0xffffffffu, seqs);
+  if (lane == 0) red[warp] = mine, red_seqs[warp] = seqs;
   if (tid == 0) found[0] = found[1] = 0;
   __syncthreads();
-  long long total = 0;
+  long long total = 0, units = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += red[w];
+  for (int w = 0; w < kWarps; ++w) total += red[w], units += red_seqs[w];
   Run r;
   const long long T = total * U;
-  const int n = ctas_used(T, gridDim.x), i = min((int)blockIdx.x, n);
+  const int n = decode_ctas(T, units * U, gridDim.x), i = min((int)blockIdx.x, n);
   r.s = n ? T * i / n : 0;
   r.e = i < n ? T * (i + 1) / n : r.s;
-  const bool first = blockIdx.x == 0 && prefix;
+  const bool first = blockIdx.x == 0;
   long long run = 0;
   for (int b1 = 0; b1 < pg.B && (first || run * U <= r.s); b1 += kThreads) {
     const int b = b1 + tid;
@@ -109,7 +121,7 @@ __device__ __forceinline__ Run my_run(const PagedView& pg, int U, long long* pre
     }
     run += chunk;
   }
-  if (first && tid == 0) prefix[pg.B] = total;
+  if (first && tid == 0) prefix[pg.B] = total, prefix[pg.B + 1] = n;
   __syncthreads();
   r.b0 = (int)found[0];
   r.pre = found[1];
@@ -575,9 +587,8 @@ struct Parts {
   bool one;
   __device__ __forceinline__ long long slot(int c) const { return c == c0 ? first : 2LL * c; }
 };
-__device__ __forceinline__ Parts parts_of(long long pre, long long nt, long long total, int u, int U, int grid) {
+__device__ __forceinline__ Parts parts_of(long long pre, long long nt, long long total, int u, int U, int n) {
   const long long x0 = pre * U + u * nt, T = total * U;
-  const int n = ctas_used(T, grid);
   Parts p;
   p.c0 = cta_of(x0, T, n);
   p.c1 = cta_of(x0 + nt - 1, T, n);
@@ -606,7 +617,7 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 // of an empty sequence.  W warps share the partials: one where there are rows
 // enough, the whole CTA for few.
 template <typename T, int D, int W>
-__device__ __forceinline__ void join_row(const DecodeArgs& a, int grid, long long i) {
+__device__ __forceinline__ void join_row(const DecodeArgs& a, long long i) {
   constexpr int E = D / 32;
   __shared__ float red[W > 1 ? W * D : 1];
   const int lane = threadIdx.x & 31, w = W > 1 ? threadIdx.x >> 5 : 0;
@@ -617,7 +628,7 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, int grid, long lon
 #pragma unroll
   for (int x = 0; x < E; ++x) o[x] = 0.f;
   if (nt > 0) {
-    const Parts p = parts_of(pre, nt, a.prefix[a.pg.B], u, a.pg.Hk * a.ngroups, grid);
+    const Parts p = parts_of(pre, nt, a.prefix[a.pg.B], u, a.pg.Hk * a.ngroups, (int)a.prefix[a.pg.B + 1]);
     if (p.one) return;  // (every warp of the row)
     join_sums(a, p, g, M, l);
 #pragma unroll 8
@@ -654,11 +665,12 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, int grid, long lon
 // heads of 2^(score - lse), the lse from the partials again (so this need not
 // wait for the joined rows).  A thread a slot: nothing is summed in an order
 // that varies.
-__device__ __forceinline__ void add_weights(const DecodeArgs& a, int grid, int idx, int count) {
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int count) {
   extern __shared__ float lse[];  // [G]
   __shared__ int found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hk = a.pg.Hk, G = a.G;
   const long long total = a.prefix[a.pg.B], T = total * Hk;
+  const int ctas = (int)a.prefix[a.pg.B + 1];  // of the decode kernel
   const int used = ctas_used(T, count);
   if (idx >= used) return;
   const long long s = T * idx / used, e = T * (idx + 1) / used;
@@ -676,7 +688,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int grid, int i
     const int hk = (int)(local / nt), t0 = (int)(local % nt), t1 = (int)min(nt, t0 + (e - cur));
     const int n = a.pg.length(b);
     for (int g = warp; g < G; g += kWarps) {
-      const Parts p = parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, grid);
+      const Parts p = parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, ctas);
       float M, l;
       if (!p.one) join_sums(a, p, g % a.GT, M, l);
       if (lane == 0) lse[g] = p.one ? a.lse_ws[(long long)b * a.Hq + hk * G + g] : lse_of(M, l);
@@ -727,13 +739,13 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int grid, int i
 // The first CTAs join; the others (accumulation) add weights.  Both read what
 // the decode kernel left and wait for its end.
 template <typename T, int D, int W>
-__global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int grid, int join_ctas) {
+__global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int join_ctas) {
   cudaGridDependencySynchronize();
   if ((int)blockIdx.x < join_ctas) {
     const long long i = W > 1 ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (i < (long long)a.pg.B * a.Hq) join_row<T, D, W>(a, grid, i);
+    if (i < (long long)a.pg.B * a.Hq) join_row<T, D, W>(a, i);
   } else {
-    add_weights(a, grid, blockIdx.x - join_ctas, gridDim.x - join_ctas);
+    add_weights(a, blockIdx.x - join_ctas, gridDim.x - join_ctas);
   }
 }
 
@@ -748,7 +760,7 @@ size_t layout(const nats_paged_cache* c, int Hq, bool accumulate, char* base, De
     return p;
   };
   DecodeArgs d = {};
-  d.prefix = (long long*)take(8 * ((size_t)c->B + 1));
+  d.prefix = (long long*)take(8 * ((size_t)c->B + 2));
   d.lse_ws = (float*)take(4 * (size_t)c->B * Hq);
   d.part_ml = (float*)take(4 * 2 * (size_t)kMaxCtas * kMaxHeads * 2);
   d.part_o = (float*)take(4 * 2 * (size_t)kMaxCtas * kMaxHeads * c->d);
@@ -809,8 +821,8 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
   const int join = (int)(few ? rows : (rows + kWarps - 1) / kWarps);
   const unsigned grid = join + (acc ? kSMs * 8 : 0);
   const size_t smem = acc ? 4 * (size_t)a.G : 0;
-  return few ? after(decode_finish_kernel<T, D, kWarps>, grid, smem, st, a, ctas, join)
-             : after(decode_finish_kernel<T, D, 1>, grid, smem, st, a, ctas, join);
+  return few ? after(decode_finish_kernel<T, D, kWarps>, grid, smem, st, a, join)
+             : after(decode_finish_kernel<T, D, 1>, grid, smem, st, a, join);
 }
 
 // Units of eight heads; bf16 groups of more than eight in units of sixteen,

@@ -185,7 +185,7 @@ def test_tile_line_is_covered_once_and_joined(seed):
     nt = [-(-n // 64) for n in lens]
     pre = [sum(nt[:b]) for b in range(len(nt) + 1)]
     T = pre[-1] * U
-    ctas = min(ctas, T)
+    ctas = min(ctas, T, max(32 * U * sum(x > 0 for x in nt), T // 4))  # decode_ctas
     partial, direct = {}, set()
     used = set()
     for c in range(ctas):
