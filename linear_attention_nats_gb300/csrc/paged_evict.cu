@@ -21,12 +21,11 @@
 namespace nats {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;            // two groups of 32 a warp
+constexpr int kBins = 2048;
 constexpr int kKeysHeld = 32768;       // slots of a CTA's share in shared memory; a longer share is read again
 constexpr int kSMs = 152;
 constexpr int kMaxCluster = 8;
+constexpr int kShortShare = 8192, kShortThreads = 512;  // slots of a share, threads of its CTA
 constexpr int kCopyRows = 64;
 constexpr int kCopyThreads = 256;
 
@@ -50,6 +49,7 @@ __device__ __forceinline__ uint32_t order_bits(float w) {
 }
 
 // Inclusive sum over the CTA's threads in thread order; *total gets all of it.
+template <int WARPS>
 __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -59,7 +59,7 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int w = warp_sums[lane];
+  int w = lane < WARPS ? warp_sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, o);
@@ -102,8 +102,10 @@ __device__ __forceinline__ int find_from_top(cooperative_groups::cluster_group& 
   return __shfl_sync(0xffffffffu, at, src);
 }
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a, int held) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(EvictArgs a, int held) {
   namespace cg = cooperative_groups;
+  constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
   cudaTriggerProgrammaticLaunchCompletion();  // the copy may be launched; it waits for this kernel's end
   extern __shared__ uint32_t keys[];  // the share's first `held` weights, as order_bits
   __shared__ int hist[3][kBins], groups[3][kBins / 32];
@@ -177,11 +179,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
           if ((u.z & mask) == prefix && u.z != kAlways) atomicAdd(&hist[pass][(u.z >> shift) & (bins - 1)], 1);
           if ((u.w & mask) == prefix && u.w != kAlways) atomicAdd(&hist[pass][(u.w >> shift) & (bins - 1)], 1);
         }
-      // sums of 32 bins each (two a warp), so that the search reads little of the other CTAs
+      // sums of 32 bins each, so that the search reads little of the other CTAs
       __syncthreads();
-      const int g_hi = __reduce_add_sync(0xffffffffu, hist[pass][64 * warp + 32 + lane]);
-      const int g_lo = __reduce_add_sync(0xffffffffu, hist[pass][64 * warp + lane]);
-      if (lane == 0) groups[pass][2 * warp] = g_lo, groups[pass][2 * warp + 1] = g_hi;
+#pragma unroll
+      for (int i = warp; i < kBins / 32; i += kSelWarps) {
+        const int sum = __reduce_add_sync(0xffffffffu, hist[pass][32 * i + lane]);
+        if (lane == 0) groups[pass][i] = sum;
+      }
       cluster.sync();
       if (warp == 0) {
         // the group from the top in which the rest-th lies, then the bin within it
@@ -205,8 +209,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
   }
   nsure = __reduce_add_sync(0xffffffffu, nsure), ntie = __reduce_add_sync(0xffffffffu, ntie);
   int total_sure, total_tie;
-  const int sure_upto = block_scan(lane == 0 ? nsure : 0, sums, &total_sure);
-  const int tie_upto = block_scan(lane == 0 ? ntie : 0, sums, &total_tie);
+  const int sure_upto = block_scan<kSelWarps>(lane == 0 ? nsure : 0, sums, &total_sure);
+  const int tie_upto = block_scan<kSelWarps>(lane == 0 ? ntie : 0, sums, &total_tie);
   if (tid == 0) counts[0] = total_sure, counts[1] = total_tie;
   cluster.sync();
   int sure0 = __shfl_sync(0xffffffffu, sure_upto, 0) - nsure, tie0 = __shfl_sync(0xffffffffu, tie_upto, 0) - ntie;
@@ -283,22 +287,18 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictArgs a, i
   }
 }
 
-// CTAs of a head: as many as fill the GPU, while a share is worth its part of
-// the cluster's barriers (4096 slots).
-cudaError_t launch_select(const EvictArgs& a, long long cap, cudaStream_t st) {
-  const long long heads = (long long)a.pg.B * a.pg.Hk;
-  int C = 1;
-  while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 4096) C *= 2;
-  const long long warps = C * kSelWarps, share = (cap + warps * 128 - 1) / (warps * 128) * 128 * kSelWarps;
+template <int THREADS>
+cudaError_t launch_select(const EvictArgs& a, long long cap, int C, cudaStream_t st) {
+  const long long warps = C * THREADS / 32, share = (cap + warps * 128 - 1) / (warps * 128) * 128 * (THREADS / 32);
   const int held = (int)(share < kKeysHeld ? share : kKeysHeld);
   if (held * 4 > 16384) {  // beyond what a kernel has without asking
     const cudaError_t e =
-        cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
+        cudaFuncSetAttribute(evict_select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(heads * C));
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.gridDim = dim3((unsigned)((long long)a.pg.B * a.pg.Hk * C));
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = (size_t)held * 4;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -306,7 +306,19 @@ cudaError_t launch_select(const EvictArgs& a, long long cap, cudaStream_t st) {
   at[0].val.clusterDim = {(unsigned)C, 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a, held);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS>, a, held);
+}
+
+// CTAs of a head: as many as fill the GPU, while a share is worth its part of
+// the cluster's barriers (4096 slots).  Short shares by small CTAs, since a
+// warp's fixed steps (barriers, scans) then outweigh its slots': 64 x 8 heads
+// of 1000 slots 55.6 us in all with 512 threads, 64.0 with 1024; long ones by
+// large CTAs: one head of 131,072 34.5 us with 1024, 37.5 with 512.
+cudaError_t launch_select(const EvictArgs& a, long long cap, cudaStream_t st) {
+  const long long heads = (long long)a.pg.B * a.pg.Hk;
+  int C = 1;
+  while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 4096) C *= 2;
+  return cap / C <= kShortShare ? launch_select<kShortThreads>(a, cap, C, st) : launch_select<1024>(a, cap, C, st);
 }
 
 nats_status check_evict(const nats_paged_cache* c, int32_t budget) {
