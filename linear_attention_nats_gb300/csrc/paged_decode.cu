@@ -686,7 +686,17 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
     }
     const long long local = cur - pre * Hk;
     const int hk = (int)(local / nt), t0 = (int)(local % nt), t1 = (int)min(nt, t0 + (e - cur));
-    const int n = a.pg.length(b);
+    const int end = min(a.pg.length(b), t1 * kTile);
+    constexpr int kSlots = 4;  // a thread's slots in flight; their pages are read an iteration ahead
+    int j = t0 * kTile + tid, pg[kSlots];
+    auto pages = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        const int ji = j + i * kThreads;
+        pg[i] = ji < end ? a.pg.page_of(b, ji / a.pg.page) : -1;
+      }
+    };
+    pages(j);
     for (int g = warp; g < G; g += kWarps) {
       const Parts p = parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, ctas);
       float M, l;
@@ -695,20 +705,18 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
     }
     __syncthreads();
     const float* scores = a.scores + ((long long)b * Hk + hk) * a.pg.cap() * G;
-    const int end = min(n, t1 * kTile);
-    constexpr int kSlots = 4;  // a thread's slots in flight
-    for (int j = t0 * kTile + tid; j < end; j += kSlots * kThreads) {
+    for (; j < end; j += kSlots * kThreads) {
       float w[kSlots];
       const float* x[kSlots];
       float* at[kSlots];
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         const int ji = j + i * kThreads;
-        const int pg = ji < end ? a.pg.page_of(b, ji / a.pg.page) : -1;
-        at[i] = pg < 0 ? nullptr : a.weight + a.pg.row(pg, hk, ji % a.pg.page);
+        at[i] = pg[i] < 0 ? nullptr : a.weight + a.pg.row(pg[i], hk, ji % a.pg.page);
+        w[i] = at[i] ? *at[i] : 0.f;
         x[i] = scores + (long long)min(ji, end - 1) * G;
-        w[i] = 0.f;
       }
+      pages(j + kSlots * kThreads);
       auto add = [&](int i, float v, int g) { w[i] += v == -INFINITY ? 0.f : pow2(v - lse[g]); };
       if (G % 4 == 0) {
         for (int g = 0; g < G; g += 4) {
@@ -729,7 +737,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       }
 #pragma unroll
       for (int i = 0; i < kSlots; ++i)
-        if (at[i]) *at[i] += w[i];
+        if (at[i]) *at[i] = w[i];
     }
     __syncthreads();
     cur += t1 - t0;
