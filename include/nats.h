@@ -679,20 +679,24 @@ nats_status nats_paged_append(const nats_paged_cache* cache, const nats_rope_dim
  * (append the token first for it to see itself): query head h reads key head
  * h / (Hq / Hk),
  *   out[b, h] = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
- * zero for an empty sequence.  q [B, Hq, d] with element strides q_stride_b,
+ * zero for an empty sequence.  Entries in use are expected finite: a NaN or an
+ * infinity makes what it reaches (a key's: the group's rows, a value's: that
+ * entry of them) NaN, or infinite where the formula says so; entries of slots
+ * not in use never matter.  q [B, Hq, d] with element strides q_stride_b,
  * q_stride_h; out [B, Hq, d] contiguous (the cache's dtype); lse (or NULL)
  * fp32 [B, Hq]: log2 of the sum of 2^(scale log2 e q . k_j), -inf for an
  * empty sequence.  accumulate != 0 adds the group's weights, sum over its
  * query heads of p_j, to cache->weight in every slot.  The work is cut into
  * 64-slot tiles dealt evenly to the GPU whatever the lengths are (they are
  * read on the device), partial results are joined by a second kernel in a
- * fixed order.  scale 0 => 1/sqrt(d).  out must not overlap q.  In a call that
- * accumulates no page may be in the table twice (within or across sequences).  workspace: device scratch of
- * nats_paged_decode_workspace_size bytes, 16-byte aligned; calls that share
- * it must be ordered by the caller.  Errors before any launch: NATS_ERR_NULL,
- * _SHAPE (Hq not a multiple of Hk, the cache's fields), _UNSUPPORTED, _DTYPE,
- * _VALUE (scale), _ALIGN (q, its strides and out: 16 bytes), _WORKSPACE;
- * NATS_ERR_CUDA on a failed launch. */
+ * fixed order.  scale 0 => 1/sqrt(d).  out must not overlap q.  In a call
+ * that accumulates no page may be in the table twice (within or across
+ * sequences).  workspace: device scratch of nats_paged_decode_workspace_size
+ * bytes, 16-byte aligned; calls that share it must be ordered by the caller.
+ * Errors before any launch: NATS_ERR_NULL, _SHAPE (Hq not a multiple of Hk,
+ * the cache's fields), _UNSUPPORTED (more than 4096 query heads a key head, a
+ * pool of 2^31 rows), _DTYPE, _VALUE (scale), _ALIGN (q, its strides and out:
+ * 16 bytes), _WORKSPACE; NATS_ERR_CUDA on a failed launch. */
 size_t nats_paged_decode_workspace_size(const nats_paged_cache* cache, int32_t Hq, int32_t accumulate);
 nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float scale, const void* q,
                               int64_t q_stride_b, int64_t q_stride_h, void* out, float* lse, int32_t accumulate,

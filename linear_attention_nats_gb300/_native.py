@@ -193,10 +193,27 @@ def _load() -> ctypes.CDLL:
 _lib = None
 
 
+def _load_operators():
+    """The operators' native binding, given the functions of the library that is loaded."""
+    try:
+        from . import _operators
+    except ImportError as e:
+        raise ImportError(f"_operators.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'` ({e})")
+    names = ("nats_qk_norm_rope", "nats_qk_norm_rope_bwd", "nats_qk_norm_rope_bwd_workspace_size", "nats_paged_append",
+             "nats_paged_decode", "nats_paged_decode_workspace_size", "nats_paged_evict",
+             "nats_paged_evict_workspace_size")
+    lib = __getattr__("lib")
+    _operators.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, NatsError)
+    return _operators
+
+
 def __getattr__(name):
-    # `lib` loads on first use, so that the build helper in this package can
-    # be imported before the library exists.
+    # `lib` (and `operators`) load on first use, so that the build helper in
+    # this package can be imported before the library exists.
     global _lib
+    if name == "operators":
+        globals()["operators"] = _load_operators()
+        return globals()["operators"]
     if name == "lib":
         if _lib is None:
             _lib = _load()

@@ -1,7 +1,8 @@
-"""In-tree build of libnats.so with nvcc for sm_103a (no cmake, no torch).
+"""In-tree build of libnats.so with nvcc for sm_103a (no cmake, no torch), and
+of _operators.so, the operators' torch-facing binding, with g++.
 
 Each translation unit under csrc/ compiles in parallel to an object under
-_build/, then nvcc links the shared library next to this file.
+_build/, then the two shared libraries are linked next to this file.
 """
 
 from __future__ import annotations
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnats.so")
+BINDING = os.path.join(PKG, "_operators.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -37,20 +40,24 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _binding_source():
+    return os.path.join(CSRC, "binding.cpp")
+
+
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
+    return _sources() + [_binding_source()] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
         os.path.join(ROOT, "include", "nats.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile libnats.so if any source changed; returns its path.
+    """Compile libnats.so and _operators.so if any source changed; returns the first one's path.
 
     Serialised across processes with a file lock (several ranks may call it)."""
     if not force and up_to_date():
@@ -64,6 +71,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             return _build_locked(verbose, extra_flags)
         finally:
             fcntl.flock(lk, fcntl.LOCK_UN)
+
+
+def _build_binding(verbose) -> None:
+    """_operators.so: one file against Python's and torch's headers, linked to torch's own libraries."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           "-I" + os.path.join(ROOT, "include"), _binding_source(), "-o", tmp, "-L" + libs, "-Wl,-rpath," + libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def _build_locked(verbose, extra_flags) -> str:
@@ -83,8 +113,10 @@ def _build_locked(verbose, extra_flags) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_build_binding, verbose)
         list(ex.map(compile_one, zip(srcs, objs)))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -12,6 +12,12 @@
 // others leave (max, sum, weighted values) in the workspace, two slots a CTA
 // (a run begins at most one pair that it does not finish and ends at most one
 // that it did not begin), and decode_finish_kernel adds them up in order.
+//
+// Measured on one GB300 (HBM copy rate 6.8 TB/s): 32 contexts of 3000 to 8192
+// slots, 32 query and 8 key heads of 128, bf16: 118 us, 5.9 TB/s, the tensor
+// pipe 13 % busy; 4 contexts of up to 131,072 with weights 295 us, 5.6 TB/s (and
+// 134 MB of scores between the kernels); fp32 the same way, 5.8 TB/s at 8 x
+// 16384; 517 slots of one sequence 9.6 us, which is the two kernels' latency.
 #include <cmath>
 
 #include "kernels.h"
@@ -834,7 +840,10 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
 }
 
 // Units of eight heads; bf16 groups of more than eight in units of sixteen,
-// whose rows are then read once (fp32 has not the registers).
+// whose rows are then read once: 16 x 16384 slots, 12 heads a group, 141 us
+// (6 of 10 of the copy rate: two warps a scheduler are too few); their heads
+// dealt to several warps 161 us.  fp32 has not the registers and reads the
+// rows of such a group twice.
 cudaError_t launch(DecodeArgs& a, int dtype, int d, cudaStream_t st) {
   if (dtype != NATS_BF16) return d == 128 ? launch<F32<128>, 1, 2>(a, st) : launch<F32<64>, 1, 3>(a, st);
   if (a.G > 8) return d == 128 ? launch<Bf16<128>, 2, 2>(a, st) : launch<Bf16<64>, 2, 3>(a, st);

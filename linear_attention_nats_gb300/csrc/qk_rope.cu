@@ -19,6 +19,12 @@
 // fixed-point fraction of a turn, F = frac(f / 2 pi) 2^64, and the phase is
 // p F mod 2^64, exact whole turns dropping out of the product by themselves;
 // its upper 32 bits go to sincospif.
+//
+// Measured on one GB300 (4 x 8192 tokens, 16 query and 16 key heads of 128,
+// bf16; HBM copy rate 6.8 TB/s): forward 88 us, 6.1 TB/s; gradient from fp32 to
+// bf16 176 us, 6.1 TB/s; one token 3.7 us (position, angle and row are one
+// chain of loads).  8 ragged prompts of up to 4096 tokens into a cache, 32 + 8
+// + 8 heads: 100 us, 5.8 TB/s.
 #include <cmath>
 #include <type_traits>
 
@@ -286,7 +292,9 @@ __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h
 }
 
 // One warp per item (a token and a run of its rows): q rows, then k rows,
-// then (append) v rows.
+// then (append) v rows.  Three CTAs an SM, four rows of a lane requested
+// together and the item's rows prefetched: 1.7 times the rate of one row at a
+// time (151 us for the 4 x 8192 tokens above).
 template <typename T, int D, bool INTER, bool PAGED, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   constexpr int LPR = D / 8;
@@ -444,7 +452,10 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
 }
 
 // The same mapping on a fixed grid whose warps stride over the items and keep
-// their shares of dw_q, dw_k in registers (8 entries of each a lane).
+// their shares of dw_q, dw_k in registers (8 entries of each a lane).  Bytes
+// in flight bound it: 12 warps an SM with eight rows each 176 us, 16 with four
+// 191 us; prefetching the next item to L2 as well 227 us (the prefetched rows
+// push each other out).
 template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kWarpsBwd * 32, kBwdBlocks<T, GI>) rope_bwd_kernel(RopeBwdArgs a) {
   constexpr int LPR = D / 8;

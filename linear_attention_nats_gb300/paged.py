@@ -1,14 +1,32 @@
 """The paged key / value cache: append, attention of one new token, eviction
-(nats_paged_append, nats_paged_decode, nats_paged_evict)."""
+(nats_paged_append, nats_paged_decode, nats_paged_evict).  The checks of the
+operators' arguments are in csrc/binding.cpp."""
 
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
 
-from . import _args, _native
-from .rope import _rotation
+from . import _native
+
+_CODES = {torch.bfloat16: _native.NATS_BF16, torch.float32: _native.NATS_F32}
+
+
+def _field(t, name, dtype, shape, device):
+    """The address of one of the cache's tensors."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 class PagedCache:
@@ -29,17 +47,20 @@ class PagedCache:
         if table.dim() != 2:
             raise ValueError("table must be [B, max_pages]")
         B, most = table.shape
-        dev = _args.cuda_index(k_pages, "k_pages")
-        code = _args.dtype_code(k_pages, "k_pages")
-        pk = _args.need(k_pages, "k_pages", k_pages.dtype, None, dev)
-        pv = _args.need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev)
-        pt = _args.need(table, "table", torch.int32, None, dev)
-        pl = _args.need(lens, "lens", torch.int32, (B,), dev)
-        pw = _args.need(weight, "weight", torch.float32, (n, Hk, page), dev)
-        self._t = (k_pages, v_pages, table, lens, weight, torch.zeros((1,), dtype=torch.int32, device=dev))
-        self._dev, self.device, self.dtype = dev, k_pages.device, k_pages.dtype
+        if not k_pages.is_cuda:
+            raise ValueError("k_pages must be a CUDA tensor")
+        if k_pages.dtype not in _CODES:
+            raise TypeError(f"k_pages must be bfloat16 or float32, got {k_pages.dtype}")
+        dev = k_pages.device
+        err = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self._t = (k_pages, v_pages, table, lens, weight, err)
+        self.device, self.dtype = dev, k_pages.dtype
         self.n_pages, self.Hk, self.page, self.d, self.B, self.max_pages = n, Hk, page, d, B, most
-        self._c = _native.PagedCache(pk, pv, pw, pt, pl, self._t[5].data_ptr(), n, page, Hk, d, B, most, code)
+        self._c = _native.PagedCache(
+            _field(k_pages, "k_pages", k_pages.dtype, None, dev), _field(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev),
+            _field(weight, "weight", torch.float32, (n, Hk, page), dev), _field(table, "table", torch.int32, None, dev),
+            _field(lens, "lens", torch.int32, (B,), dev), err.data_ptr(), n, page, Hk, d, B, most, _CODES[k_pages.dtype])
+        self._addr, self._dev = ctypes.addressof(self._c), dev.index
 
     k_pages = property(lambda self: self._t[0])
     v_pages = property(lambda self: self._t[1])
@@ -69,7 +90,9 @@ class PagedCache:
 def paged_workspace_size(cache: PagedCache, *, Hq: int = 0, accumulate: bool = False, budget: int = 0) -> int:
     """Bytes of workspace that serve paged_decode with Hq query heads and
     paged_evict to `budget` (0 when a size is not supported)."""
-    _args.int32(Hq=Hq, budget=budget)
+    for name, v in (("Hq", Hq), ("budget", budget)):
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} is out of range")
     a = int(_native.lib.nats_paged_decode_workspace_size(cache._c, Hq, int(accumulate)))
     b = int(_native.lib.nats_paged_evict_workspace_size(cache._c, budget))
     return max(a, b) if a and b else 0
@@ -85,35 +108,8 @@ def paged_append(cache: PagedCache, k, v, *, start=None, n_new=None, q=None, out
     on the way (at `positions`, int64 [B, T], or their slots).  Returns q' (in
     out_q, whose rows from n_new[b] on are left as they were, or in a new
     tensor, zero there), or None without q.  cache.lens is not changed."""
-    if k.dim() != 4:
-        raise ValueError("k must be [B, Hk, T, d]")
-    B, Hk, T, d = k.shape
-    dev, dt = cache._dev, cache.dtype
-    if (B, Hk, d) != (cache.B, cache.Hk, cache.d):
-        raise ValueError(f"k must be [{cache.B}, {cache.Hk}, T, {cache.d}], got {tuple(k.shape)}")
-    ks = k.shape
-    pk, sk = _args.heads(k, "k", dt, ks, dev)
-    pv, sv = _args.heads(v, "v", dt, ks, dev)
-    ps = _args.need(start, "start", torch.int32, (B,), dev)
-    pn = _args.need(n_new, "n_new", torch.int32, (B,), dev)
-    pwq, pwk = _args.need(w_q, "w_q", torch.float32, (d,), dev), _args.need(w_k, "w_k", torch.float32, (d,), dev)
-    rot, pf, pp, pb = _rotation(inv_freq, positions, B, T, dev)
-    Hq, made = 0, []
-    pq = sq = poq = soq = None
-    if q is not None:
-        qs = q.shape
-        if len(qs) != 4 or qs[0] != B or qs[2] != T or qs[3] != d:
-            raise ValueError(f"q must be [{B}, Hq, {T}, {d}], got {tuple(qs)}")
-        Hq = qs[1]
-        pq, sq = _args.heads(q, "q", dt, qs, dev)
-        if out_q is None:
-            out_q = (torch.empty if n_new is None else torch.zeros)(qs, dtype=dt, device=dev)
-            made.append(out_q)
-        poq, soq = _args.heads_out(out_q, "out_q", dt, qs, dev)
-    dm = _args.rope_dims(B, T, Hq, Hk, d, rot, interleaved, norm, cache._c.dtype, eps)
-    _args.call(_native.lib.nats_paged_append, "nats_paged_append", dev, stream, made, cache._c, dm, pq, sq, pk, sk, pv,
-               sv, pwq, pwk, pf, ps, pn, pp, pb, poq, soq)
-    return out_q
+    return _native.operators.paged_append(cache._addr, cache._dev, k, v, start, n_new, q, out_q, norm, w_q, w_k, inv_freq,
+                                          positions, interleaved, eps, stream)
 
 
 def paged_decode(cache: PagedCache, q, *, scale: float = 0.0, accumulate: bool = False, return_lse: bool = False,
@@ -124,33 +120,9 @@ def paged_decode(cache: PagedCache, q, *, scale: float = 0.0, accumulate: bool =
     accumulate adds each slot's attention weight, summed over the query heads
     of its key head, to cache.weight.  workspace: uint8 tensor of
     paged_workspace_size(cache, Hq=Hq, accumulate=accumulate) bytes, or None."""
-    dev, dt, c = cache._dev, cache.dtype, cache._c
-    qs = q.shape
-    if len(qs) != 3 or qs[0] != cache.B or qs[2] != cache.d:
-        raise ValueError(f"q must be [{cache.B}, Hq, {cache.d}], got {tuple(qs)}")
-    if q.dtype is not dt or q.get_device() != dev:
-        _args.refuse(q, "q", dt, None, dev)
-    qb, qh, qe = q.stride()
-    if qe != 1 and q.numel() > 0:
-        raise ValueError("q: the entries of a row must be contiguous")
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs a cache with weights")
-    made, Hq, lib = [], qs[1], _native.lib
-    if out is None:
-        out = torch.empty(qs, dtype=dt, device=dev)
-        made.append(out)
-    po, lse, pl = _args.need(out, "out", dt, qs, dev), None, None
-    if return_lse:
-        lse = torch.empty(qs[:2], dtype=torch.float32, device=dev)
-        pl = lse.data_ptr()
-        made.append(lse)
-    if workspace is None:
-        workspace = torch.empty(lib.nats_paged_decode_workspace_size(c, Hq, accumulate), dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    pw = _args.need(workspace, "workspace", torch.uint8, None, dev)
-    _args.call(lib.nats_paged_decode, "nats_paged_decode", dev, stream, made, c, Hq, scale, q.data_ptr(), qb, qh, po, pl,
-               accumulate, pw, workspace.numel())
-    return (out, lse) if return_lse else out
+    return _native.operators.paged_decode(cache._addr, cache._dev, q, scale, accumulate, return_lse, out, workspace, stream)
 
 
 def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, sinks: int = 0, lens_out=None,
@@ -163,27 +135,7 @@ def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, s
     (keep, lengths) with keep int32 [B, Hk, budget], the kept slots, -1 behind
     the last.  The caller then puts out_table and the lengths into the cache
     and frees the old pages."""
-    dev, c, lib = cache._dev, cache._c, _native.lib
     if cache.weight is None:
         raise ValueError("eviction needs a cache with weights")
-    if out_table.dim() != 2 or out_table.shape[0] != cache.B:
-        raise ValueError(f"out_table must be [{cache.B}, pages], got {tuple(out_table.shape)}")
-    _args.int32(budget=budget, recent=recent, sinks=sinks)
-    pt = _args.need(out_table, "out_table", torch.int32, None, dev)
-    made = []
-    if lens_out is None:
-        lens_out = torch.empty((cache.B,), dtype=torch.int32, device=dev)
-        made.append(lens_out)
-    pl = _args.need(lens_out, "lens_out", torch.int32, (cache.B,), dev)
-    keep, pk = None, None
-    if return_keep:
-        keep = torch.empty((cache.B, cache.Hk, max(budget, 0)), dtype=torch.int32, device=dev)
-        pk = keep.data_ptr()
-        made.append(keep)
-    if workspace is None:
-        workspace = torch.empty(lib.nats_paged_evict_workspace_size(c, budget), dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    pw = _args.need(workspace, "workspace", torch.uint8, None, dev)
-    _args.call(lib.nats_paged_evict, "nats_paged_evict", dev, stream, made, c, pt, out_table.shape[1], budget, recent,
-               sinks, pl, pk, pw, workspace.numel())
-    return (keep, lens_out) if return_keep else lens_out
+    return _native.operators.paged_evict(cache._addr, cache._dev, out_table, budget, recent, sinks, lens_out, return_keep,
+                                         workspace, stream)

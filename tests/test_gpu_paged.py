@@ -284,6 +284,47 @@ def test_decode_calls_in_a_row_share_a_workspace(nats):
     assert all(torch.equal(x, alone[0]) for x in both)
 
 
+def test_outputs_of_another_stream_share_no_memory_with_pending_work(nats):
+    """A block freed while the current stream still has a write to it under way is not handed to a call on another
+    stream; nor is what such a call returned, freed while the current stream still reads it, handed out again."""
+    rng = torch.Generator().manual_seed(15)
+    table, _, k, v = _filled(rng, [300], 16, 2, 128, BF)
+    c = _cache(nats, table, [300], k, v)
+    q = torch.randn(1, 8, 128, generator=rng).to(BF).cuda()
+    f = nats.rope_inv_freq(128)
+    x = torch.randn(1, 8, 64, 128, generator=rng).to(BF).cuda()
+    n_new = torch.tensor([1], dtype=torch.int32).cuda()
+    kv = torch.zeros(1, 2, 64, 128, dtype=BF, device="cuda")
+    start = torch.tensor([0], dtype=torch.int32).cuda()
+    c2 = nats.PagedCache.empty(4, 16, 2, 128, 1, 4)
+    c2.table.copy_(torch.arange(4, dtype=torch.int32)[None])
+    calls = [lambda s: nats.paged_decode(c, q, stream=s), lambda s: nats.qk_norm_rope(x, x, None, None, f, stream=s)[0],
+             lambda s: nats.paged_append(c2, kv, kv, start=start, n_new=n_new, q=x, stream=s)]
+    want = [call(None) for call in calls]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, w in zip(calls, want):
+        for _ in range(3):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+            for _ in range(8):
+                torch.empty_like(w).fill_(7)  # freed with its write still to run
+            got = call(s)
+            s.synchronize()
+            assert torch.equal(got.cpu(), w.cpu())
+            torch.cuda.synchronize()
+            assert torch.equal(got, w)
+            with torch.cuda.stream(s):
+                keep = got.clone()
+            s.synchronize()
+            torch.cuda._sleep(20_000_000)
+            late = got * 1  # the current stream reads it late
+            del got
+            others = [call(s).fill_(9) for _ in range(4)]
+            torch.cuda.synchronize()
+            assert torch.equal(late, keep)
+            del others
+
+
 # ------------------------------------------------------------------ append
 
 APPEND = [
