@@ -21,6 +21,7 @@
 #include <cmath>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace nats {
@@ -513,7 +514,7 @@ template <class X, int NH, bool ACC, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) {
   using T = typename X::T;
   constexpr int D = X::kD, GT = 8 * NH;
-  cudaTriggerProgrammaticLaunchCompletion();  // the next kernel may be launched; it waits for this one's end
+  begin();
   __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
   const int U = a.pg.Hk * a.ngroups;
   const Run run = my_run(a.pg, U, a.prefix);
@@ -750,11 +751,10 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
   }
 }
 
-// The first CTAs join; the others (accumulation) add weights.  Both read what
-// the decode kernel left and wait for its end.
+// The first CTAs join; the others (accumulation) add weights.
 template <typename T, int D, int W>
 __global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int join_ctas) {
-  cudaGridDependencySynchronize();
+  begin();
   if ((int)blockIdx.x < join_ctas) {
     const long long i = W > 1 ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (i < (long long)a.pg.B * a.Hq) join_row<T, D, W>(a, i);
@@ -796,23 +796,6 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
   return NATS_OK;
 }
 
-// A kernel that starts while the one before it in the stream still runs, and
-// waits for it (to end) itself: its launch is then off the path.
-template <class... P, class... A>
-cudaError_t after(void (*kernel)(P...), unsigned grid, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // BLOCKS: the CTAs an SM has registers for.
 template <class X, int NH, int BLOCKS>
 cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
@@ -822,11 +805,8 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
   a.ngroups = (a.G + a.GT - 1) / a.GT;
   const bool acc = a.scores != nullptr;
   const int ctas = kSMs * BLOCKS;
-  if (acc)
-    decode_kernel<X, NH, true, BLOCKS><<<ctas, kThreads, 0, st>>>(a);
-  else
-    decode_kernel<X, NH, false, BLOCKS><<<ctas, kThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = acc ? after(decode_kernel<X, NH, true, BLOCKS>, ctas, kThreads, 0, st, 0, a)
+                            : after(decode_kernel<X, NH, false, BLOCKS>, ctas, kThreads, 0, st, 0, a);
   if (e != cudaSuccess) return e;
   // a CTA a row while the rows are no more than two waves of CTAs, so that a
   // long unit's many partials (up to one a CTA) are read by four warps
@@ -835,8 +815,8 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
   const int join = (int)(few ? rows : (rows + kWarps - 1) / kWarps);
   const unsigned grid = join + (acc ? kSMs * 8 : 0);
   const size_t smem = acc ? 4 * (size_t)a.G : 0;
-  return few ? after(decode_finish_kernel<T, D, kWarps>, grid, smem, st, a, join)
-             : after(decode_finish_kernel<T, D, 1>, grid, smem, st, a, join);
+  return few ? after(decode_finish_kernel<T, D, kWarps>, grid, kThreads, smem, st, 0, a, join)
+             : after(decode_finish_kernel<T, D, 1>, grid, kThreads, smem, st, 0, a, join);
 }
 
 // Units of eight heads; bf16 groups of more than eight in units of sixteen,

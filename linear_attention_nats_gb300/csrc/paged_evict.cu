@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace nats {
@@ -109,7 +110,7 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(EvictArgs a, int held) {
   namespace cg = cooperative_groups;
   constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
-  cudaTriggerProgrammaticLaunchCompletion();  // the copy may be launched; it waits for this kernel's end
+  begin();
   extern __shared__ uint32_t keys[];  // the share's first `held` weights, as order_bits
   __shared__ int hist[3][kBins], groups[3][kBins / 32];
   __shared__ int sums[kSelWarps], pick[2], counts[2];
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
 // Kept rows i0 .. i0 + 63 of one head: keys, values and weights.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictArgs a, int tiles) {
   __shared__ long long from[kCopyRows], to[kCopyRows];
-  cudaGridDependencySynchronize();
+  begin();
   const int bh = blockIdx.x / tiles, i0 = (blockIdx.x % tiles) * kCopyRows;
   const int b = bh / a.pg.Hk, h = bh % a.pg.Hk;
   const int left = min(a.pg.length(b), a.budget);
@@ -299,17 +300,8 @@ cudaError_t launch_select(const EvictArgs& a, long long cap, int C, cudaStream_t
         cudaFuncSetAttribute(evict_select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)a.pg.B * a.pg.Hk * C));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (size_t)held * 4;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)C, 1, 1};
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS>, a, held);
+  return after(evict_select_kernel<THREADS>, (unsigned)((long long)a.pg.B * a.pg.Hk * C), THREADS, (size_t)held * 4, st, C,
+               a, held);
 }
 
 // CTAs of a head: as many as fill the GPU, while a share is worth its part of
@@ -369,16 +361,8 @@ nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_t
   const int r = record_cuda_error(launch_select(a, (long long)cache->max_pages * cache->page, st));
   if (r != NATS_OK || budget == 0) return (nats_status)r;
   const int tiles = (budget + kCopyRows - 1) / kCopyRows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)cache->B * cache->Hk * tiles));
-  cfg.blockDim = dim3(kCopyThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return (nats_status)record_cuda_error(cudaLaunchKernelEx(&cfg, evict_copy_kernel, a, tiles));
+  return (nats_status)record_cuda_error(after(
+      evict_copy_kernel, (unsigned)((long long)cache->B * cache->Hk * tiles), kCopyThreads, 0, st, 0, a, tiles));
 }
 
 }  // extern "C"

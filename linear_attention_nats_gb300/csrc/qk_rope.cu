@@ -29,6 +29,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace nats {
@@ -298,6 +299,7 @@ __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h
 template <typename T, int D, bool INTER, bool PAGED, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   constexpr int LPR = D / 8;
+  begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const long long item = (long long)blockIdx.x * kWarps + warp;
@@ -459,8 +461,8 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
 template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kWarpsBwd * 32, kBwdBlocks<T, GI>) rope_bwd_kernel(RopeBwdArgs a) {
   constexpr int LPR = D / 8;
-  cudaTriggerProgrammaticLaunchCompletion();  // rope_dw_kernel may be launched; it waits for this kernel's end
   __shared__ float red[kWarpsBwd][D];
+  begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const LaneMap m = lane_map<INTER>(l, a.rot);
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kWarpsBwd * 32, kBwdBlocks<T, GI>) rope_bwd_ke
 template <int D>
 __global__ void rope_dw_kernel(const float* part, int n, float* dwq, float* dwk) {
   __shared__ float red[32][32];
-  cudaGridDependencySynchronize();
+  begin();
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D
   float v = 0.f;
 #pragma unroll 8
@@ -582,22 +584,19 @@ cudaError_t launch_fwd(RopeArgs& a, int dtype, int d, bool inter, bool vec, cuda
   split_rows(tokens, rows, 32 / (d / 8), (long long)kSMs * 3 * kWarps, &a.rows_per_item, &a.items_per_token);
   const long long items = tokens * a.items_per_token;
   const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
-#define NATS_ROPE(T, D, I, V) rope_fwd_kernel<T, D, I, PAGED, V><<<grid, kWarps * 32, 0, st>>>(a)
+#define NATS_ROPE(T, D, I, V) after(rope_fwd_kernel<T, D, I, PAGED, V>, grid, kWarps * 32, 0, st, 0, a)
 #define NATS_ROPE_V(T, D, I) (vec ? NATS_ROPE(T, D, I, true) : NATS_ROPE(T, D, I, false))
 #define NATS_ROPE_I(T, D) (inter ? NATS_ROPE_V(T, D, true) : NATS_ROPE_V(T, D, false))
-  if (dtype == NATS_BF16)
-    d == 128 ? NATS_ROPE_I(__nv_bfloat16, 128) : NATS_ROPE_I(__nv_bfloat16, 64);
-  else
-    d == 128 ? NATS_ROPE_I(float, 128) : NATS_ROPE_I(float, 64);
-  return cudaGetLastError();
+  if (dtype == NATS_BF16) return d == 128 ? NATS_ROPE_I(__nv_bfloat16, 128) : NATS_ROPE_I(__nv_bfloat16, 64);
+  return d == 128 ? NATS_ROPE_I(float, 128) : NATS_ROPE_I(float, 64);
 }
 
 template <typename T, typename GI, typename GO>
-void launch_bwd(const RopeBwdArgs& a, int d, bool inter, bool vec, unsigned grid, cudaStream_t st) {
-#define NATS_BWD(D, I, V) rope_bwd_kernel<T, GI, GO, D, I, V><<<grid, kWarpsBwd * 32, 0, st>>>(a)
+cudaError_t launch_bwd(const RopeBwdArgs& a, int d, bool inter, bool vec, unsigned grid, cudaStream_t st) {
+#define NATS_BWD(D, I, V) after(rope_bwd_kernel<T, GI, GO, D, I, V>, grid, kWarpsBwd * 32, 0, st, 0, a)
 #define NATS_BWD_V(D, I) (vec ? NATS_BWD(D, I, true) : NATS_BWD(D, I, false))
 #define NATS_BWD_I(D) (inter ? NATS_BWD_V(D, true) : NATS_BWD_V(D, false))
-  d == 128 ? NATS_BWD_I(128) : NATS_BWD_I(64);
+  return d == 128 ? NATS_BWD_I(128) : NATS_BWD_I(64);
 }
 
 }  // namespace
@@ -745,31 +744,22 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
   const unsigned grid = (unsigned)(ctas < most ? ctas : most);
   const bool inter = dims->interleaved != 0;
   const int d = dims->d;
+  cudaError_t e;
   if (dims->dtype == NATS_F32)
-    launch_bwd<float, float, float>(a, d, inter, vec, grid, st);
+    e = launch_bwd<float, float, float>(a, d, inter, vec, grid, st);
   else if (grad_dtype == NATS_F32 && dx_dtype == NATS_F32)
-    launch_bwd<__nv_bfloat16, float, float>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, float, float>(a, d, inter, vec, grid, st);
   else if (grad_dtype == NATS_F32)
-    launch_bwd<__nv_bfloat16, float, __nv_bfloat16>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, float, __nv_bfloat16>(a, d, inter, vec, grid, st);
   else if (dx_dtype == NATS_F32)
-    launch_bwd<__nv_bfloat16, __nv_bfloat16, float>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, __nv_bfloat16, float>(a, d, inter, vec, grid, st);
   else
-    launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, grid, st);
-  int r = record_cuda_error(cudaGetLastError());
+    e = launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, grid, st);
+  const int r = record_cuda_error(e);
   if (r != NATS_OK || !dw) return (nats_status)r;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * d / 32);
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   const float* part = a.part;
-  r = record_cuda_error(cudaLaunchKernelEx(&cfg, d == 128 ? rope_dw_kernel<128> : rope_dw_kernel<64>, part, (int)grid,
-                                           dw_q, dw_k));
-  return (nats_status)r;
+  return (nats_status)record_cuda_error(after(d == 128 ? rope_dw_kernel<128> : rope_dw_kernel<64>, 2 * d / 32,
+                                              dim3(32, 32), 0, st, 0, part, (int)grid, dw_q, dw_k));
 }
 
 }  // extern "C"

@@ -527,6 +527,41 @@ def test_evict_bad_entries_are_reported(nats):
         c2.check()
 
 
+def test_every_operator_captured_behind_copies_and_forks(nats):
+    """A graph in which each operator's kernels follow a memory copy, a fill, another stream's work and each other."""
+    rng = torch.Generator().manual_seed(16)
+    table, spare, k, v = _filled(rng, [200, 90], 16, 2, 64, BF, extra=8)
+    c = _cache(nats, table, [200, 90], k, v, torch.zeros(k.shape[:3]))
+    ot = spare.reshape(2, 4).contiguous().cuda()
+    f, n = nats.rope_inv_freq(64), torch.tensor([200, 90], dtype=torch.int32).cuda()
+    host = torch.randn(2, 6, 1, 64, generator=rng).to(BF).pin_memory()
+    x, kv = torch.empty(2, 6, 1, 64, dtype=BF, device="cuda"), torch.randn(2, 2, 1, 64, generator=rng).to(BF).cuda()
+    start = n - 1
+
+    def steps(side):
+        x.copy_(host, non_blocking=True)
+        q = nats.paged_append(c, kv, kv, start=start, q=x, norm=True, inv_freq=f)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            r = nats.qk_norm_rope(x, x, None, None, f)
+            g = nats.qk_norm_rope_bwd(*r, x, x, None, None, f)
+        c.weight.zero_()
+        out = nats.paged_decode(c, q[:, :, 0], accumulate=True)
+        torch.cuda.current_stream().wait_stream(side)
+        keep, m = nats.paged_evict(c, ot, 60, recent=5, return_keep=True)
+        return [q, out, r[0], g["dq"], g["dw_q"], c.weight, keep, m]
+
+    want = [t.clone() for t in steps(torch.cuda.Stream())]
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = steps(side)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_evict_captured(nats):
     rng = torch.Generator().manual_seed(11)
     table, spare, k, v = _filled(rng, [200, 90], 16, 2, 64, BF, extra=8)
