@@ -261,6 +261,7 @@ __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
       const int r = h + i * RPW;
+      if (!full && r - sub >= h1) break;  // (none of the warp's rows)
       if (!COPY) {
         float x[8];
         qa[i].get(x), qb[i].get(x + 4);
@@ -416,6 +417,7 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const bool on = full || h + i * RPW < h1;
+      if (!full && h - sub + i * RPW >= h1) break;  // (none of the warp's rows)
       float u[8];
       ga[i].get(u), gb[i].get(u + 4);
       turn<INTER>(u, c, s);
