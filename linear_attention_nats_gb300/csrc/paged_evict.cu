@@ -29,6 +29,7 @@ constexpr int kBins = 2048;
 constexpr int kKeysHeld = 32768;       // slots of a CTA's share in shared memory; a longer share is read again
 constexpr int kSMs = 152;
 constexpr int kMaxCluster = 8;
+constexpr int kFusedRows = 512, kFusedBytes = 65536;  // of a head's keys that the selecting CTA copies itself
 constexpr int kShortShare = 8192, kShortThreads = 512;  // slots of a share, threads of its CTA
 constexpr int kCopyRows = 64;
 constexpr int kCopyThreads = 256;
@@ -106,7 +107,40 @@ __device__ __forceinline__ int find_from_top(cooperative_groups::cluster_group& 
   return __shfl_sync(0xffffffffu, at, src);
 }
 
+// Rows i0 .. i0 + rows - 1 kept of one head, slot src[i - i0] each: keys, values
+// and weights.  from, to: shared memory for `rows` of them.
 template <int THREADS>
+__device__ __forceinline__ void copy_rows(const EvictArgs& a, int b, int h, int i0, int rows, const int32_t* src,
+                                          long long* from, long long* to) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i < rows; i += THREADS) {
+    const int j = src[i], k = i0 + i;
+    const int pf = a.pg.page_of(b, j / a.pg.page);
+    const int pt = a.out_table[(long long)b * a.out_pages + k / a.pg.page];
+    const bool ok = pf >= 0 && (unsigned)pt < (unsigned)a.pg.n_pages;
+    from[i] = ok ? a.pg.row(pf, h, j % a.pg.page) : -1;
+    to[i] = ok ? a.pg.row(pt, h, k % a.pg.page) : -1;
+    if (ok)
+      a.weight[to[i]] = a.weight[from[i]];
+    else
+      *a.pg.err = 1;
+  }
+  __syncthreads();
+  const int per = a.row_bytes / 16, total = rows * per;
+#pragma unroll 4
+  for (int x = tid; x < total; x += THREADS) {
+    const int r = x / per, c = x % per;
+    if (from[r] < 0) continue;
+    const long long f = from[r] * a.row_bytes + c * 16, t = to[r] * a.row_bytes + c * 16;
+    const uint4 kk = *(const uint4*)(a.k + f), vv = *(const uint4*)(a.v + f);
+    *(uint4*)(a.k + t) = kk;
+    *(uint4*)(a.v + t) = vv;
+  }
+}
+
+// COPY (one CTA a head, a small budget): it also copies the head's rows, and no
+// second kernel follows.
+template <int THREADS, bool COPY>
 __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(EvictArgs a, int held) {
   namespace cg = cooperative_groups;
   constexpr int kSelThreads = THREADS, kSelWarps = THREADS / 32;
@@ -114,6 +148,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
   extern __shared__ uint32_t keys[];  // the share's first `held` weights, as order_bits
   __shared__ int hist[3][kBins], groups[3][kBins / 32];
   __shared__ int sums[kSelWarps], pick[2], counts[2];
+  __shared__ long long from[COPY ? kFusedRows : 1], to[COPY ? kFusedRows : 1];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int bh = blockIdx.x / C, b = bh / a.pg.Hk, h = bh % a.pg.Hk;
@@ -128,6 +163,10 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
   for (int i = left + rank * kSelThreads + tid; i < a.budget; i += C * kSelThreads) keep[i] = -1;
   if (n <= a.budget) {  // (the whole cluster)
     for (int i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) keep[i] = i;
+    if constexpr (COPY) {
+      __syncthreads();
+      copy_rows<THREADS>(a, b, h, 0, n, keep, from, to);
+    }
     return;
   }
   // the candidates are the slots m0 <= j < m1, of which `need` stay; the others
@@ -138,8 +177,10 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
   const int run = (n + C * kSelWarps * 128 - 1) / (C * kSelWarps * 128) * 128;
   const int s0 = min((long long)n, (long long)rank * run * kSelWarps);
   const int w0 = min((long long)n, s0 + (long long)warp * run), w1 = min(n, w0 + run);
-  for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
-  __syncthreads();
+  if (n > THREADS) {
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+  }
   // the images of slots j .. j + 3 (j a multiple of 4, so of one page); 0, below
   // every weight's, behind the last
   auto image4 = [&](int j) {
@@ -155,6 +196,35 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
     return make_uint4(u[0], u[1], u[2], u[3]);
   };
   auto key4 = [&](int j) { return j - s0 < held ? *(const uint4*)(keys + (j - s0)) : image4(j); };
+  if (C == 1 && n <= THREADS) {
+    // a slot a thread: it stays if fewer than `budget` are heavier or, as heavy, before it
+    for (int j = 4 * tid; j < n; j += 4 * THREADS) *(uint4*)(keys + j) = image4(j);
+    __syncthreads();
+    bool stays = false;
+    if (tid < n) {
+      const uint32_t mine = keys[tid];
+      const int own = tid & ~3;
+      int ahead = 0;
+      for (int j = 0; j < own; j += 4) {
+        const uint4 u = *(const uint4*)(keys + j);
+        ahead += (u.x >= mine) + (u.y >= mine) + (u.z >= mine) + (u.w >= mine);
+      }
+      for (int j = own; j < own + 4; ++j) ahead += j < tid ? keys[j] >= mine : keys[j] > mine;
+      for (int j = own + 4; j < n; j += 4) {
+        const uint4 u = *(const uint4*)(keys + j);
+        ahead += (u.x > mine) + (u.y > mine) + (u.z > mine) + (u.w > mine);
+      }
+      stays = ahead < a.budget;
+    }
+    int total;
+    const int upto = block_scan<kSelWarps>(stays, sums, &total);
+    if (stays) keep[upto - 1] = tid;
+    if constexpr (COPY) {
+      __syncthreads();
+      copy_rows<THREADS>(a, b, h, 0, a.budget, keep, from, to);
+    }
+    return;
+  }
   {
 #pragma unroll 2
     for (int j = w0 + 4 * lane; j < w1; j += 128) {
@@ -254,9 +324,13 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
     sure0 += all >> 16;
     tie0 += all & 0xffff;
   }
+  if constexpr (COPY) {
+    __syncthreads();
+    copy_rows<THREADS>(a, b, h, 0, a.budget, keep, from, to);
+  }
 }
 
-// Kept rows i0 .. i0 + 63 of one head: keys, values and weights.
+// Kept rows i0 .. i0 + 63 of one head.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictArgs a, int tiles) {
   __shared__ long long from[kCopyRows], to[kCopyRows];
   begin();
@@ -264,56 +338,37 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictArgs a, i
   const int b = bh / a.pg.Hk, h = bh % a.pg.Hk;
   const int left = min(a.pg.length(b), a.budget);
   if (i0 >= left) return;
-  const int rows = min(kCopyRows, left - i0);
-  const int tid = threadIdx.x;
-  if (tid < rows) {
-    const int i = i0 + tid, j = a.keep[(long long)bh * a.budget + i];
-    const int pf = a.pg.page_of(b, j / a.pg.page);
-    const int pt = a.out_table[(long long)b * a.out_pages + i / a.pg.page];
-    const bool ok = pf >= 0 && (unsigned)pt < (unsigned)a.pg.n_pages;
-    from[tid] = ok ? a.pg.row(pf, h, j % a.pg.page) : -1;
-    to[tid] = ok ? a.pg.row(pt, h, i % a.pg.page) : -1;
-    if (ok)
-      a.weight[to[tid]] = a.weight[from[tid]];
-    else
-      *a.pg.err = 1;
-  }
-  __syncthreads();
-  const int per = a.row_bytes / 16, total = rows * per;
-#pragma unroll 4
-  for (int x = tid; x < total; x += kCopyThreads) {
-    const int r = x / per, c = x % per;
-    if (from[r] < 0) continue;
-    const long long f = from[r] * a.row_bytes + c * 16, t = to[r] * a.row_bytes + c * 16;
-    const uint4 kk = *(const uint4*)(a.k + f), vv = *(const uint4*)(a.v + f);
-    *(uint4*)(a.k + t) = kk;
-    *(uint4*)(a.v + t) = vv;
-  }
+  copy_rows<kCopyThreads>(a, b, h, i0, min(kCopyRows, left - i0), a.keep + (long long)bh * a.budget + i0, from, to);
 }
 
-template <int THREADS>
+template <int THREADS, bool COPY>
 cudaError_t launch_select(const EvictArgs& a, long long cap, int C, cudaStream_t st) {
   const long long warps = C * THREADS / 32, share = (cap + warps * 128 - 1) / (warps * 128) * 128 * (THREADS / 32);
   const int held = (int)(share < kKeysHeld ? share : kKeysHeld);
-  if (held * 4 > 16384) {  // beyond what a kernel has without asking
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
+  auto kernel = evict_select_kernel<THREADS, COPY>;
+  if (held * 4 > 8192) {  // beyond what a kernel has without asking
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysHeld * 4);
     if (e != cudaSuccess) return e;
   }
-  return after(evict_select_kernel<THREADS>, (unsigned)((long long)a.pg.B * a.pg.Hk * C), THREADS, (size_t)held * 4, st, C,
-               a, held);
+  return after(kernel, (unsigned)((long long)a.pg.B * a.pg.Hk * C), THREADS, (size_t)held * 4, st, C, a, held);
 }
 
 // CTAs of a head: as many as fill the GPU, while a share is worth its part of
 // the cluster's barriers (4096 slots).  Short shares by small CTAs, since a
 // warp's fixed steps (barriers, scans) then outweigh its slots': 64 x 8 heads
 // of 1000 slots 55.6 us in all with 512 threads, 64.0 with 1024; long ones by
-// large CTAs: one head of 131,072 34.5 us with 1024, 37.5 with 512.
-cudaError_t launch_select(const EvictArgs& a, long long cap, cudaStream_t st) {
+// large CTAs: one head of 131,072 34.5 us with 1024, 37.5 with 512.  *copied:
+// the kernel copies too, which pays while a CTA's rows are few.
+cudaError_t launch_select(const EvictArgs& a, long long cap, bool* copied, cudaStream_t st) {
   const long long heads = (long long)a.pg.B * a.pg.Hk;
   int C = 1;
   while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 4096) C *= 2;
-  return cap / C <= kShortShare ? launch_select<kShortThreads>(a, cap, C, st) : launch_select<1024>(a, cap, C, st);
+  *copied = C == 1 && a.budget <= kFusedRows && (long long)a.budget * a.row_bytes <= kFusedBytes;
+  if (cap / C > kShortShare) {
+    *copied = false;
+    return launch_select<1024, false>(a, cap, C, st);
+  }
+  return *copied ? launch_select<kShortThreads, true>(a, cap, C, st) : launch_select<kShortThreads, false>(a, cap, C, st);
 }
 
 nats_status check_evict(const nats_paged_cache* c, int32_t budget) {
@@ -358,8 +413,9 @@ nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_t
   a.lens_out = lens_out, a.keep = keep ? keep : (int32_t*)workspace;
   a.row_bytes = cache->d * (cache->dtype == NATS_BF16 ? 2 : 4);
   cudaStream_t st = (cudaStream_t)stream;
-  const int r = record_cuda_error(launch_select(a, (long long)cache->max_pages * cache->page, st));
-  if (r != NATS_OK || budget == 0) return (nats_status)r;
+  bool copied = false;
+  const int r = record_cuda_error(launch_select(a, (long long)cache->max_pages * cache->page, &copied, st));
+  if (r != NATS_OK || budget == 0 || copied) return (nats_status)r;
   const int tiles = (budget + kCopyRows - 1) / kCopyRows;
   return (nats_status)record_cuda_error(after(
       evict_copy_kernel, (unsigned)((long long)cache->B * cache->Hk * tiles), kCopyThreads, 0, st, 0, a, tiles));

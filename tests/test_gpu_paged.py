@@ -470,6 +470,10 @@ EVICT = [
     ([5000], 1, 64, 16, F32, 4097, 1, 0, "equal"),
     ([30000, 1025], 1, 64, 64, BF, 1025, 100, 4, "spread"),
     ([64, 10], 1, 64, 16, BF, 0, 0, 0, "spread"),
+    ([500, 450, 301], 2, 128, 32, F32, 300, 20, 4, "odd"),
+    ([512, 513, 511], 2, 64, 64, BF, 200, 10, 2, "odd"),
+    ([5000, 600], 1, 64, 16, BF, 200, 10, 2, "odd"),
+    ([5000, 600], 1, 128, 16, F32, 600, 0, 600, "odd"),
 ]
 
 
