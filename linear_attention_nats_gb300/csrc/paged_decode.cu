@@ -52,7 +52,23 @@ struct DecodeArgs {
   float* weight;
 };
 
-__device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int n) { return (int)((uint32_t)(n + kTile - 1) / kTile); }
+
+// a / b and a % b, 32-bit where a allows
+__device__ __forceinline__ long long div_rem(long long a, int b, int* rest) {
+  if ((unsigned long long)a >> 32) {
+    *rest = (int)(a % b);
+    return a / b;
+  }
+  const uint32_t q = (uint32_t)a / (uint32_t)b;
+  *rest = (int)((uint32_t)a - q * (uint32_t)b);
+  return q;
+}
+// a * b / c for 0 <= a, b and 0 < c
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+  const long long ab = a * b;
+  return (ab | c) >> 32 ? ab / c : (long long)((uint32_t)ab / (uint32_t)c);
+}
 
 // CTAs that share T tiles: none has an empty run.
 __device__ __forceinline__ int ctas_used(long long T, int grid) { return (int)min(T, (long long)grid); }
@@ -74,54 +90,65 @@ __device__ __forceinline__ Run my_run(const PagedView& pg, int U, long long* pre
   __shared__ long long red[kWarps], found[2];
   __shared__ int red_seqs[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long mine = 0;
-  int seqs = 0;  // that have slots
-  for (int b = tid; b < pg.B; b += kThreads) {
-    const int t = tiles_of(pg.length(b));
-    mine += t, seqs += t > 0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  seqs = __reduce_add_sync(0xffffffffu, seqs);
-  if (lane == 0) red[warp] = mine, red_seqs[warp] = seqs;
-  if (tid == 0) found[0] = found[1] = 0;
-  __syncthreads();
-  long long total = 0, units = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += red[w], units += red_seqs[w];
-  Run r;
-  const long long T = total * U;
-  const int n = decode_ctas(T, units * U, gridDim.x), i = min((int)blockIdx.x, n);
-  r.s = n ? T * i / n : 0;
-  r.e = i < n ? T * (i + 1) / n : r.s;
   const bool first = blockIdx.x == 0;
-  long long run = 0;
-  for (int b1 = 0; b1 < pg.B && (first || run * U <= r.s); b1 += kThreads) {
+  long long total = 0, units = 0, run = 0;
+  Run r = {0, 0, 0, 0};
+  int n = 0;
+  // a first pass for the sums, a second one for the place; the chunk of the
+  // first pass is kept, so that a batch of up to kThreads sequences is read once
+  long long mine = 0;
+  int seqs = 0, kept = 0;
+  for (int b = tid; b < pg.B; b += kThreads) {
+    kept = tiles_of(pg.length(b));
+    mine += kept, seqs += kept > 0;
+  }
+  for (int b1 = 0; b1 == 0 || (b1 < pg.B && (first || run * U <= r.s)); b1 += kThreads) {
     const int b = b1 + tid;
-    long long x = 0;
+    int own = 0;
     if (b < pg.B) {
-      x = tiles_of(pg.length(b));
+      own = pg.B <= kThreads ? kept : tiles_of(pg.length(b));
       if (first) {
         const int raw = pg.lens[b];
         if (raw < 0 || raw > pg.cap()) *pg.err = 1;
       }
     }
-    const long long own = x;
+    // (up to 2^24 tiles a sequence: 32 of them fit 32 bits)
+    uint32_t x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
-    if (lane == 31) red[warp] = x;
-    __syncthreads();
-    long long chunk = 0;
+    long long all = x;
+    if (b1 == 0) {
+      if (pg.B > kThreads) {
+        all = mine;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      }
+      seqs = __reduce_add_sync(0xffffffffu, seqs);
+      if (lane == 31) red[warp] = all, red_seqs[warp] = seqs;
+      if (tid == 0) found[0] = found[1] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) total += red[w], units += red_seqs[w];
+      const long long T = total * U;
+      n = decode_ctas(T, units * U, gridDim.x);
+      const int i = min((int)blockIdx.x, n);
+      r.s = n ? mul_div(T, i, n) : 0;
+      r.e = i < n ? mul_div(T, i + 1, n) : r.s;
+    }
+    if (pg.B > kThreads) {  // (else red holds the warps' sums of this chunk already)
+      __syncthreads();
+      if (lane == 31) red[warp] = x;
+      __syncthreads();
+    }
+    long long before = run + x - own, chunk = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) x += red[w];
+      if (w < warp) before += red[w];
       chunk += red[w];
     }
-    const long long before = run + x - own;
     if (b < pg.B) {
       if (first) prefix[b] = before;
       if (before * U <= r.s && r.s < (before + own) * U) found[0] = b, found[1] = before;
@@ -141,42 +168,57 @@ __device__ __forceinline__ float pow2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *(float4*)p = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *(uint2*)p = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+}
 // The maximum of no scores: below any real one, and finite, so that a score of
 // -inf less it is still -inf and two of it subtract to 0 (their sums are 0).
 constexpr float kNoMax = -1e38f;
 // the factor that brings sums taken at maximum m to maximum M >= m
 __device__ __forceinline__ float part_scale(float m, float M) { return pow2(m - M); }
 
-// A unit's result from the CTA's warps (shared memory: so [kWarps][GT][D], sml
-// [kWarps][GT][2]) to the output or to partial slot `slot` (-1: the output).
-template <typename T, int D, int GT>
+// Where entry e of a row stands in shared memory: rows padded to D + 4, and
+// within a row such that the lanes that hold neighbouring entry tiles (X::place)
+// write to different banks.
+template <int D>
+constexpr int kPitch = D + 4;
+
+// A unit's result from the CTA's warps (shared memory: so [kWarps][GT][pitch],
+// sml [kWarps][GT][2]) to the output or to partial slot `slot` (-1: the
+// output), four entries a thread.
+template <class X, int GT>
 __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const float* so, const float* sml, int b, int h0,
                                             int heads, long long slot) {
-  for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-    const int g = i / D, e = i % D;
-    float M = kNoMax;
+  using T = typename X::T;
+  constexpr int D = X::kD;
+  for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
+    const int g = i / (D / 4), e = 4 * (i % (D / 4));
+    float f[kWarps], M = kNoMax, l = 0.f, o[4] = {};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * GT + g) * 2]);
-    float l = 0.f, o = 0.f;
+    for (int w = 0; w < kWarps; ++w) f[w] = sml[(w * GT + g) * 2], M = fmaxf(M, f[w]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = part_scale(sml[(w * GT + g) * 2], M);
-      l += f * sml[(w * GT + g) * 2 + 1];
-      o += f * so[(w * GT + g) * D + e];
+      f[w] = part_scale(f[w], M);
+      l += f[w] * sml[(w * GT + g) * 2 + 1];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] += f[w] * so[(w * GT + g) * kPitch<D> + X::place(e + x)];
     }
     if (slot < 0) {
-      ((T*)a.out)[((long long)b * a.Hq + h0 + g) * D + e] = from_f32<T>(l == 0.f ? 0.f : o / l);
+      const float r = l == 0.f ? 0.f : 1.f / l;
+      T* out = (T*)a.out + ((long long)b * a.Hq + h0 + g) * D + e;
+      store4(out, o[0] * r, o[1] * r, o[2] * r, o[3] * r);
       if (e == 0) {
         const float v = l == 0.f ? -INFINITY : M + log2f(l);
         a.lse_ws[(long long)b * a.Hq + h0 + g] = v;
         if (a.lse) a.lse[(long long)b * a.Hq + h0 + g] = v;
       }
     } else {
-      a.part_o[(slot * GT + g) * D + e] = o;
-      if (e == 0) {
-        a.part_ml[(slot * GT + g) * 2] = M;
-        a.part_ml[(slot * GT + g) * 2 + 1] = l;
-      }
+      *(float4*)(a.part_o + (slot * GT + g) * D + e) = make_float4(o[0], o[1], o[2], o[3]);
+      if (e == 0) *(float2*)(a.part_ml + (slot * GT + g) * 2) = make_float2(M, l);
     }
   }
 }
@@ -290,6 +332,8 @@ struct Bf16 {
   static __device__ __forceinline__ int entry(int y, int g, int upper) {
     return 8 * g + y + (upper ? (D == 128 ? 64 : 4) : 0);
   }
+  // entry 8 g + y of each 64 at 8 y + g
+  static __device__ __forceinline__ int place(int e) { return (e & 64) + 8 * (e & 7) + ((e >> 3) & 7); }
 };
 
 // fp32 rows on the tf32 instructions, each factor as the sum of two (the
@@ -387,6 +431,8 @@ struct F32 {
   static __device__ __forceinline__ int entry(int y, int g, int upper) {
     return 32 * (2 * (y / 4) + upper) + 4 * g + y % 4;
   }
+  // entry 4 g + y of each 32 at 8 y + g
+  static __device__ __forceinline__ int place(int e) { return (e & ~31) + 8 * (e & 3) + ((e >> 2) & 7); }
 };
 
 // how far a score may rise above the running maximum (in powers of two)
@@ -487,7 +533,7 @@ struct Unit {
       }
   }
 
-  // to shared memory, so [8 NH][D], sml [8 NH][2] of this warp
+  // to shared memory, so [8 NH][pitch], sml [8 NH][2] of this warp
   __device__ __forceinline__ void put(float* so, float* sml, int g, int c) {
 #pragma unroll
     for (int x = 0; x < NH; ++x)
@@ -497,11 +543,11 @@ struct Unit {
         for (int z = 4; z < 32; z <<= 1) sum[x][i] += __shfl_xor_sync(0xffffffffu, sum[x][i], z);
         const int h = 8 * x + 2 * c + i;
         if (g == 0) sml[h * 2] = mx[x][i], sml[h * 2 + 1] = sum[x][i];
-        float* at = so + h * X::kD;
+        float* at = so + h * kPitch<X::kD>;
 #pragma unroll
         for (int y = 0; y < MT; ++y) {
-          at[X::entry(y, g, 0)] = o[x][y][i];
-          at[X::entry(y, g, 1)] = o[x][y][i + 2];
+          at[X::place(X::entry(y, g, 0))] = o[x][y][i];
+          at[X::place(X::entry(y, g, 1))] = o[x][y][i + 2];
         }
       }
   }
@@ -515,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
   using T = typename X::T;
   constexpr int D = X::kD, GT = 8 * NH;
   begin();
-  __shared__ float so[kWarps * GT * D], sml[kWarps * GT * 2];
+  __shared__ float so[kWarps * GT * kPitch<D>], sml[kWarps * GT * 2];
   const int U = a.pg.Hk * a.ngroups;
   const Run run = my_run(a.pg, U, a.prefix);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -529,23 +575,23 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       ++b;
       continue;
     }
-    const long long local = cur - pre * U;
-    const int u = (int)(local / nt), t0 = (int)(local % nt);
+    int t0;
+    const int u = (int)div_rem(cur - pre * U, nt, &t0);
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
     const int hk = u / a.ngroups, g0 = (u % a.ngroups) * GT;
     const int heads = min(GT, a.G - g0), h0 = hk * a.G + g0;
     Unit<X, NH> unit;
     unit.start((const T*)a.q + b * a.q_b + h0 * a.q_h, a.q_h, heads, g, c);
-    // row of this warp's first slot in tile t, or -1: past the end or without a page
+    // row of this warp's first slot in tile t, or -1: past the end or without a
+    // page (noted, and reported after the loop: a branch here would wait for
+    // the entry)
+    bool bad = false;
     auto first_row = [&](int t) -> int {
       const int j0 = t * kTile + warp * 16;
-      if (t >= t1 || j0 >= n) return -1;
-      const int pg = a.pg.page_of(b, j0 / a.pg.page);
-      if (pg < 0) {
-        if (lane == 0) *a.pg.err = 1;
-        return -1;
-      }
-      return (int)a.pg.row(pg, hk, j0 % a.pg.page);
+      const bool in = t < t1 && j0 < n;
+      const int pg = in ? a.pg.page_of(b, (uint32_t)j0 / (uint32_t)a.pg.page) : -1;
+      bad |= in && pg < 0;
+      return pg < 0 ? -1 : (int)a.pg.row(pg, hk, (uint32_t)j0 % (uint32_t)a.pg.page);
     };
     typename X::K k;
     typename X::V v;
@@ -565,20 +611,16 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       row = next;
       next = after;
     }
-    unit.put(so + warp * GT * D, sml + warp * GT * 2, g, c);
+    if (bad && lane == 0) *a.pg.err = 1;
+    unit.put(so + warp * GT * kPitch<D>, sml + warp * GT * 2, g, c);
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    finish_unit<T, D, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
+    finish_unit<X, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
     __syncthreads();
     cur += t1 - t0;
   }
 }
 
-// a * b / c for 0 <= a, b and 0 < c, 32-bit where the product allows
-__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
-  const long long ab = a * b;
-  return (ab | c) >> 32 ? ab / c : (long long)((uint32_t)ab / (uint32_t)c);
-}
 // The CTA whose run holds tile x of the line (the run of CTA i of n is
 // [i T / n, (i + 1) T / n)).
 __device__ __forceinline__ int cta_of(long long x, long long T, int n) {
@@ -680,7 +722,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
   const int ctas = (int)a.prefix[a.pg.B + 1];  // of the decode kernel
   const int used = ctas_used(T, count);
   if (idx >= used) return;
-  const long long s = T * idx / used, e = T * (idx + 1) / used;
+  const long long s = mul_div(T, idx, used), e = mul_div(T, idx + 1, used);
   for (int b = tid; b < a.pg.B; b += kThreads)
     if (a.prefix[b] * Hk <= s && s < a.prefix[b + 1] * Hk) found = b;
   __syncthreads();
@@ -692,7 +734,8 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       continue;
     }
     const long long local = cur - pre * Hk;
-    const int hk = (int)(local / nt), t0 = (int)(local % nt), t1 = (int)min(nt, t0 + (e - cur));
+    int t0;
+    const int hk = (int)div_rem(local, (int)nt, &t0), t1 = (int)min(nt, t0 + (e - cur));
     const int end = min(a.pg.length(b), t1 * kTile);
     constexpr int kSlots = 4;  // a thread's slots in flight; their pages are read an iteration ahead
     int j = t0 * kTile + tid, pg[kSlots];
