@@ -747,11 +747,27 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       }
     };
     pages(j);
-    for (int g = warp; g < G; g += kWarps) {
-      const Parts p = parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, ctas);
-      float M, l;
-      if (!p.one) join_sums(a, p, g % a.GT, M, l);
-      if (lane == 0) lse[g] = p.one ? a.lse_ws[(long long)b * a.Hq + hk * G + g] : lse_of(M, l);
+    // a unit's heads by a thread each where its parts are few, else by a warp each
+    const Parts p0 = parts_of(pre, nt, total, hk * a.ngroups, Hk * a.ngroups, ctas);
+    const bool few = p0.c1 - p0.c0 < 16;
+    for (int g = few ? tid : warp; g < G; g += few ? kThreads : kWarps) {
+      const Parts p = g < a.GT ? p0 : parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, ctas);
+      float M = kNoMax, l = 0.f;
+      if (p.one) {
+        lse[g] = a.lse_ws[(long long)b * a.Hq + hk * G + g];
+      } else if (few) {
+#pragma unroll 4
+        for (int c = p.c0; c <= p.c1; ++c) {
+          const float2 ml = *(const float2*)(a.part_ml + 2 * (p.slot(c) * a.GT + g % a.GT));
+          const float m = fmaxf(M, ml.x);
+          l = l * part_scale(M, m) + ml.y * part_scale(ml.x, m);
+          M = m;
+        }
+        lse[g] = lse_of(M, l);
+      } else {
+        join_sums(a, p, g % a.GT, M, l);
+        if (lane == 0) lse[g] = lse_of(M, l);
+      }
     }
     __syncthreads();
     const float* scores = a.scores + ((long long)b * Hk + hk) * a.pg.cap() * G;
