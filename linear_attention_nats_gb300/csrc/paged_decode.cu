@@ -187,21 +187,21 @@ __device__ __forceinline__ float part_scale(float m, float M) { return pow2(m - 
 template <int D>
 constexpr int kPitch = D + 4;
 
-// A unit's result from the CTA's warps (shared memory: so [kWarps][GT][pitch],
-// sml [kWarps][GT][2]) to the output or to partial slot `slot` (-1: the
-// output), four entries a thread.
-template <class X, int GT>
+// A unit's result from W warps (shared memory: so [W][GT][pitch], sml [W][GT][2])
+// to the output or to partial slot `slot` (-1: the output), four entries a
+// thread of 32 W.
+template <class X, int GT, int W>
 __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const float* so, const float* sml, int b, int h0,
-                                            int heads, long long slot) {
+                                            int heads, long long slot, int tid) {
   using T = typename X::T;
   constexpr int D = X::kD;
-  for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
+  for (int i = tid; i < heads * (D / 4); i += 32 * W) {
     const int g = i / (D / 4), e = 4 * (i % (D / 4));
-    float f[kWarps], M = kNoMax, l = 0.f, o[4] = {};
+    float f[W], M = kNoMax, l = 0.f, o[4] = {};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) f[w] = sml[(w * GT + g) * 2], M = fmaxf(M, f[w]);
+    for (int w = 0; w < W; ++w) f[w] = sml[(w * GT + g) * 2], M = fmaxf(M, f[w]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       f[w] = part_scale(f[w], M);
       l += f[w] * sml[(w * GT + g) * 2 + 1];
 #pragma unroll
@@ -569,53 +569,83 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
   long long cur = run.s, pre = run.pre;
   int b = run.b0;
   while (cur < run.e) {
-    const int n = a.pg.length(b), nt = tiles_of(n);
+    int n = a.pg.length(b);
+    const int nt = tiles_of(n);
     if (cur >= (pre + nt) * U) {
       pre += nt;
       ++b;
       continue;
     }
     int t0;
-    const int u = (int)div_rem(cur - pre * U, nt, &t0);
+    int u = (int)div_rem(cur - pre * U, nt, &t0);
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
+    // Units of one tile that follow one another go to a warp each, 16 slots
+    // after the other, and need no join of warps; else the warps share the unit's
+    // tiles, 16 slots of each.
+    int units = 0, mb = b;  // such units, and this warp's sequence (n, u: its slots and unit)
+    if (nt == 1) {
+      long long before = pre;
+      int s = b, len = n, tiles = nt, wn = n, wu = u;
+      for (; units < kWarps && cur + units < run.e; ++units) {
+        while (cur + units >= (before + tiles) * U) {
+          before += tiles;
+          len = a.pg.length(++s), tiles = tiles_of(len);
+        }
+        if (tiles != 1) break;
+        if (units == warp) mb = s, wn = len, wu = (int)(cur + units - before * U);
+      }
+      if (units > 1) n = wn, u = wu;
+    }
+    const bool alone = units > 1;  // a unit a warp
+    const int slot0 = alone ? 0 : t0 * kTile + warp * 16, stride = alone ? 16 : kTile;
+    const int steps = alone ? (warp < units ? (n + 15) / 16 : 0) : t1 - t0;
     const int hk = u / a.ngroups, g0 = (u % a.ngroups) * GT;
-    const int heads = min(GT, a.G - g0), h0 = hk * a.G + g0;
+    const int heads = alone && warp >= units ? 0 : min(GT, a.G - g0), h0 = hk * a.G + g0;
     Unit<X, NH> unit;
-    unit.start((const T*)a.q + b * a.q_b + h0 * a.q_h, a.q_h, heads, g, c);
-    // row of this warp's first slot in tile t, or -1: past the end or without a
-    // page (noted, and reported after the loop: a branch here would wait for
-    // the entry)
+    unit.start((const T*)a.q + mb * a.q_b + h0 * a.q_h, a.q_h, heads, g, c);
+    // row of the first slot of step st, or -1: past the end or without a page
+    // (noted, and reported after the loop: a branch here would wait for the
+    // entry)
     bool bad = false;
-    auto first_row = [&](int t) -> int {
-      const int j0 = t * kTile + warp * 16;
-      const bool in = t < t1 && j0 < n;
-      const int pg = in ? a.pg.page_of(b, (uint32_t)j0 / (uint32_t)a.pg.page) : -1;
+    auto first_row = [&](int st) -> int {
+      const int j0 = slot0 + st * stride;
+      const bool in = st < steps && j0 < n;
+      const int pg = in ? a.pg.page_of(mb, (uint32_t)j0 / (uint32_t)a.pg.page) : -1;
       bad |= in && pg < 0;
       return pg < 0 ? -1 : (int)a.pg.row(pg, hk, (uint32_t)j0 % (uint32_t)a.pg.page);
     };
     typename X::K k;
     typename X::V v;
-    int row = first_row(t0), next = first_row(t0 + 1);
+    int row = first_row(0), next = first_row(1);
     load_k<X>(k, kp, row, g, c);
-    load_v<X>(v, vp, row, n - t0 * kTile - warp * 16, g, c);
-    for (int t = t0; t < t1; ++t) {
-      const int j0 = t * kTile + warp * 16, after = first_row(t + 2);
+    load_v<X>(v, vp, row, n - slot0, g, c);
+    for (int st = 0; st < steps; ++st) {
+      const int j0 = slot0 + st * stride, after = first_row(st + 2);
       float s[NH][4] = {};
       X::scores(s, k, unit.q);
       load_k<X>(k, kp, next, g, c);
-      float* at = ACC ? a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j0) * a.G + g0 : nullptr;
+      float* at = ACC ? a.scores + (((long long)mb * a.pg.Hk + hk) * a.pg.cap() + j0) * a.G + g0 : nullptr;
       unit.template weigh<ACC>(s, a.scale2, row >= 0 && j0 + 16 <= n, row >= 0 && j0 + g < n, row >= 0 && j0 + g + 8 < n,
                                at, a.G, n - j0, heads, g, c);
       X::values(unit.o, v, s, g, c);
-      load_v<X>(v, vp, next, n - j0 - kTile, g, c);
+      load_v<X>(v, vp, next, n - j0 - stride, g, c);
       row = next;
       next = after;
     }
     if (bad && lane == 0) *a.pg.err = 1;
-    unit.put(so + warp * GT * kPitch<D>, sml + warp * GT * 2, g, c);
+    float *mine = so + warp * GT * kPitch<D>, *mine_ml = sml + warp * GT * 2;
+    unit.put(mine, mine_ml, g, c);
+    if (alone) {
+      __syncwarp();
+      finish_unit<X, GT, 1>(a, mine, mine_ml, mb, h0, heads, -1, lane);
+      __syncwarp();
+      cur += units;
+      continue;
+    }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    finish_unit<X, GT>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1));
+    finish_unit<X, GT, kWarps>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1),
+                               threadIdx.x);
     __syncthreads();
     cur += t1 - t0;
   }
