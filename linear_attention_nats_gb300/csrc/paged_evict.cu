@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
   const int run = (n + C * kSelWarps * 128 - 1) / (C * kSelWarps * 128) * 128;
   const int s0 = min((long long)n, (long long)rank * run * kSelWarps);
   const int w0 = min((long long)n, s0 + (long long)warp * run), w1 = min(n, w0 + run);
-  if (n > THREADS) {
+  const bool counted = C == 1 && n <= THREADS;  // ranked by counting: no histogram
+  if (!counted) {
     for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
   }
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) evict_select_kernel(E
     return make_uint4(u[0], u[1], u[2], u[3]);
   };
   auto key4 = [&](int j) { return j - s0 < held ? *(const uint4*)(keys + (j - s0)) : image4(j); };
-  if (C == 1 && n <= THREADS) {
+  if (counted) {
     // a slot a thread: it stays if fewer than `budget` are heavier or, as heavy, before it
     for (int j = 4 * tid; j < n; j += 4 * THREADS) *(uint4*)(keys + j) = image4(j);
     __syncthreads();

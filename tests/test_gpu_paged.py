@@ -515,6 +515,27 @@ def test_evict(nats, lens, Hk, d, page, dtype, budget, recent, sinks, kind):
     assert torch.equal(gw.transpose(1, 2)[~touched].view(torch.int32), w.transpose(1, 2)[~touched].view(torch.int32))
 
 
+@pytest.mark.parametrize("max_pages", [1024, 2048])  # clusters of eight CTAs of 512 and of 1024 threads
+@pytest.mark.parametrize("lens", [[300, 50], [512, 511], [513, 1], [1024, 1025], [101, 2048]])
+def test_evict_short_sequences_in_long_tables(nats, max_pages, lens):
+    rng = torch.Generator().manual_seed(max_pages + lens[0])
+    page, budget = 64, 100
+    table, spare, k, v = _filled(rng, lens, page, 2, 64, BF, extra=2 * len(lens))
+    w = torch.rand(k.shape[:3], generator=rng)
+    wide = torch.full((len(lens), max_pages), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    c = _cache(nats, wide, lens, k, v, w)
+    # what the kernels before left in shared memory must not matter: one of them ran on full sequences
+    long = nats.PagedCache(c.k_pages, c.v_pages, torch.full((1, max_pages), int(table[0, 0]), dtype=torch.int32).cuda(),
+                           torch.tensor([max_pages * page], dtype=torch.int32).cuda(), weight=c.weight)
+    nats.paged_evict(long, spare[None, :2].cuda(), budget)
+    c.k_pages.copy_(k), c.v_pages.copy_(v), c.weight.copy_(w)
+    keep, n = nats.paged_evict(c, spare.reshape(len(lens), 2).cuda(), budget, recent=7, sinks=3, return_keep=True)
+    c.check()
+    assert torch.equal(keep.cpu(), ref.evict(w, wide, lens, page, budget, 7, 3))
+    assert n.cpu().tolist() == [min(x, budget) for x in lens]
+
+
 def test_evict_bad_entries_are_reported(nats):
     rng = torch.Generator().manual_seed(10)
     table, spare, k, v = _filled(rng, [64], 16, 1, 64, F32, extra=2)
