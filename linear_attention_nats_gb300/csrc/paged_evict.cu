@@ -402,7 +402,7 @@ nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_t
   if (cache->B == 0) return NATS_OK;
   s = check_cache_pointers(cache);
   if (s != NATS_OK) return s;
-  if (!lens_out || !workspace || (budget > 0 && (!out_table || (cache->n_pages > 0 && !cache->weight)))) return NATS_ERR_NULL;
+  if (!lens_out || !workspace || (budget > 0 && !out_table) || (cache->n_pages > 0 && !cache->weight)) return NATS_ERR_NULL;
   if ((out_table && out_table == cache->table) || lens_out == cache->lens) return NATS_ERR_VALUE;
   if (((uintptr_t)workspace & 15u) || (((uintptr_t)out_table | (uintptr_t)lens_out | (uintptr_t)keep) & 3u))
     return NATS_ERR_ALIGN;

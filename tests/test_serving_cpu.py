@@ -123,6 +123,11 @@ def test_evict_refusals(nat):
     assert call(c=_cache(nat, B=0)) == 0
 
 
+def test_evict_to_nothing_still_reads_the_weights(nat):
+    c = _cache(nat, weight=None)
+    assert nat.lib.nats_paged_evict(c, None, 0, 0, 0, 0, A + 128, None, A, 1 << 40, None) == 1
+
+
 def test_append_refusals(nat):
     c = _cache(nat)
     s = nat.Strides(512, 256, 64)
