@@ -3,8 +3,8 @@
 // outputs, the stream, and the call into libnats' C ABI.
 //
 // A small call's time is its host's: in Python these checks took two to three
-// times as long as the launch they guard (one token's append 10.4 us a call,
-// of which the kernel 4.8).  Nothing is computed here; the functions of libnats
+// times as long as the launch they guard (a batch's append of one token each
+// 10.4 us a call, of which the kernel 4.8; now 3.8, the kernel's).  Nothing is computed here; the functions of libnats
 // are given by address when the module is set up, so that the one library that
 // the package has loaded is the one that is called.
 #include <Python.h>

@@ -14,10 +14,10 @@
 // that it did not begin), and decode_finish_kernel adds them up in order.
 //
 // Measured on one GB300 (HBM copy rate 6.8 TB/s): 32 contexts of 3000 to 8192
-// slots, 32 query and 8 key heads of 128, bf16: 118 us, 5.9 TB/s, the tensor
-// pipe 13 % busy; 4 contexts of up to 131,072 with weights 295 us, 5.6 TB/s (and
-// 134 MB of scores between the kernels); fp32 the same way, 5.8 TB/s at 8 x
-// 16384; 517 slots of one sequence 9.6 us, which is the two kernels' latency.
+// slots, 32 query and 8 key heads of 128, bf16: 112 us, 6.2 TB/s, the tensor
+// pipe 13 % busy; 4 contexts of up to 131,072 with weights 292 us, 5.7 TB/s (and
+// 134 MB of scores between the kernels); fp32 the same way, 5.6 TB/s at 8 x
+// 16384; 517 slots of one sequence 9.1 us, which is the two kernels' latency.
 #include <cmath>
 
 #include "kernels.h"
@@ -580,8 +580,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
     int u = (int)div_rem(cur - pre * U, nt, &t0);
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
     // Units of one tile that follow one another go to a warp each, 16 slots
-    // after the other, and need no join of warps; else the warps share the unit's
-    // tiles, 16 slots of each.
+    // after the other, and need no join of warps (175 sequences of up to 38 slots,
+    // 16 heads, with weights: 27 us, 35 with the warps side by side); else the
+    // warps share the unit's tiles, 16 slots of each.
     int units = 0, mb = b;  // such units, and this warp's sequence (n, u: its slots and unit)
     if (nt == 1) {
       long long before = pre;
@@ -909,10 +910,10 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
 }
 
 // Units of eight heads; bf16 groups of more than eight in units of sixteen,
-// whose rows are then read once: 16 x 16384 slots, 12 heads a group, 141 us
-// (6 of 10 of the copy rate: two warps a scheduler are too few); their heads
-// dealt to several warps 161 us.  fp32 has not the registers and reads the
-// rows of such a group twice.
+// whose rows are then read once: 16 x 16384 slots, 12 heads a group, 117 us
+// (83 % of the copy rate, with two warps a scheduler); their heads dealt to
+// several warps 161 us where this took 145.  fp32 has not the registers and
+// reads the rows of such a group twice.
 cudaError_t launch(DecodeArgs& a, int dtype, int d, cudaStream_t st) {
   if (dtype != NATS_BF16) return d == 128 ? launch<F32<128>, 1, 2>(a, st) : launch<F32<64>, 1, 3>(a, st);
   if (a.G > 8) return d == 128 ? launch<Bf16<128>, 2, 2>(a, st) : launch<Bf16<64>, 2, 3>(a, st);

@@ -15,7 +15,9 @@
 // accesses and is the floor: a kept row is read once and written once.
 // Measured on one GB300: 32 x 8 heads from 2112 to 2048 slots of 128 bf16
 // entries 72 us, of which the copy 57 (6.8 TB/s, the HBM copy rate); 4 x 8 heads
-// from up to 131,072 to 32,768 slots 194 us, the copy 162.
+// from up to 131,072 to 32,768 slots 193 us, the copy 162.  Requesting rows to
+// L2, or copying recent ones, beside the selection gained nothing (72 us to 74,
+// and 72 to 72): what the copy then reads earlier it writes no faster.
 #include <cooperative_groups.h>
 
 #include "kernels.h"

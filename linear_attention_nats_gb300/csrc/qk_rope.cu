@@ -22,7 +22,7 @@
 //
 // Measured on one GB300 (4 x 8192 tokens, 16 query and 16 key heads of 128,
 // bf16; HBM copy rate 6.8 TB/s): forward 88 us, 6.1 TB/s; gradient from fp32 to
-// bf16 176 us, 6.1 TB/s; one token 3.7 us (position, angle and row are one
+// bf16 176 us, 6.1 TB/s; one token 3.2 us (position, angle and row are one
 // chain of loads).  8 ragged prompts of up to 4096 tokens into a cache, 32 + 8
 // + 8 heads: 100 us, 5.8 TB/s.
 #include <cmath>
