@@ -553,6 +553,27 @@ struct Unit {
   }
 };
 
+// The weights of a key head's one tile, whose scores and sums the calling threads
+// have just written: weight[slot] += sum over the group's heads of 2^(score -
+// lse), thread t of `threads` a slot after the other, as add_weights does for
+// longer ones.  175 sequences of up to 38 slots, 16 heads: 22.5 us, 27 with
+// these tiles in add_weights too.
+__device__ __forceinline__ void add_one_tile(const DecodeArgs& a, int b, int hk, int n, int t, int threads) {
+  for (int j = t; j < n; j += threads) {
+    const int pg = a.pg.page_of(b, j / a.pg.page);
+    if (pg < 0) continue;
+    float* at = a.weight + a.pg.row(pg, hk, j % a.pg.page);
+    const float* x = a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G;
+    const float* lse = a.lse_ws + (long long)b * a.Hq + hk * a.G;
+    float w = *at;
+#pragma unroll 4
+    for (int g = 0; g < a.G; ++g) w += x[g] == -INFINITY ? 0.f : pow2(x[g] - lse[g]);
+    *at = w;
+  }
+}
+// (a group of more heads than a unit's is summed over its units: add_weights)
+__device__ __forceinline__ bool one_tile(const DecodeArgs& a, long long tiles) { return tiles == 1 && a.ngroups == 1; }
+
 // A step's K registers are refilled for the next one as soon as the scores are
 // done, V's when the values are, so that a warp has some 8 KB on their way all
 // the time; page entries are read a step ahead of their rows.
@@ -581,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
     const int t1 = (int)min((long long)nt, t0 + (run.e - cur));
     // Units of one tile that follow one another go to a warp each, 16 slots
     // after the other, and need no join of warps (175 sequences of up to 38 slots,
-    // 16 heads, with weights: 27 us, 35 with the warps side by side); else the
+    // 16 heads, with weights: 35 us to 27); else the
     // warps share the unit's tiles, 16 slots of each.
     int units = 0, mb = b;  // such units, and this warp's sequence (n, u: its slots and unit)
     if (nt == 1) {
@@ -640,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       __syncwarp();
       finish_unit<X, GT, 1>(a, mine, mine_ml, mb, h0, heads, -1, lane);
       __syncwarp();
+      if (ACC && warp < units && one_tile(a, 1)) add_one_tile(a, mb, hk, n, lane, 32);
       cur += units;
       continue;
     }
@@ -648,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
     finish_unit<X, GT, kWarps>(a, so, sml, b, h0, heads, whole ? -1 : 2LL * blockIdx.x + (cur == run.s ? 0 : 1),
                                threadIdx.x);
     __syncthreads();
+    if (ACC && one_tile(a, nt)) add_one_tile(a, b, hk, n, threadIdx.x, kThreads);
     cur += t1 - t0;
   }
 }
@@ -764,6 +787,10 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       ++b;
       continue;
     }
+    if (one_tile(a, nt)) {  // added by the decode kernel
+      cur = min(e, (pre + 1) * Hk);
+      continue;
+    }
     const long long local = cur - pre * Hk;
     int t0;
     const int hk = (int)div_rem(local, (int)nt, &t0), t1 = (int)min(nt, t0 + (e - cur));
@@ -841,7 +868,8 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
   }
 }
 
-// The first CTAs join; the others (accumulation) add weights.
+// The first CTAs join; the others (accumulation) add the weights of units of
+// more than one tile.
 template <typename T, int D, int W>
 __global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int join_ctas) {
   begin();

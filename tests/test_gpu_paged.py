@@ -146,6 +146,35 @@ def test_decode_leaves_out_bad_pages_and_reports_them(nats, dtype):
     assert torch.equal(c.weight.cpu()[skipped], w0[skipped])
 
 
+@pytest.mark.parametrize("lens,Hk,G,dtype", [([40, 60, 10, 64, 64], 2, 4, BF), ([40, 60, 10, 64, 64], 1, 12, BF),
+                                             ([50], 1, 3, F32), ([33, 48, 64, 17, 130, 20], 2, 12, F32)])
+def test_decode_weights_of_single_tiles_with_bad_pages(nats, lens, Hk, G, dtype):
+    """Sequences of one tile, alone or in a row: the weights of the slots that count, twice over, and no others'."""
+    rng = torch.Generator().manual_seed(18 + G)
+    page, d = 16, 64
+    table, _, k, v = _filled(rng, lens, page, Hk, d, dtype)
+    bad = table.clone()
+    bad[0, 1] = -1  # slots 16..31 of sequence 0
+    skip = [(0, j) for j in range(16, 32)]
+    w0 = torch.rand(k.shape[:3], generator=rng)
+    c = _cache(nats, bad, lens, k, v, w0)
+    q = torch.randn(len(lens), Hk * G, d, generator=rng).to(dtype)
+    for _ in range(2):
+        out = nats.paged_decode(c, q.cuda(), accumulate=True)
+    e, _, ps, err, perr = ref.decode(q, k, v, table, lens, skip=skip)
+    assert ((out.cpu().double() - e).abs() <= ref.HALF[dtype] * (e.abs() + err) + err).all()
+    want, tol = w0.double(), torch.zeros(w0.shape, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        j = torch.arange(n)
+        at = table[b].long()[j // page]
+        want[at, :, j % page] += 2 * ps[b].sum(1).T
+        tol[at, :, j % page] += 2 * perr[b].sum(1).T
+    got = c.weight.cpu().double()
+    # two rounds of G additions to a sum of at most 1 + 2 G
+    assert ((got - want).abs() <= tol + 2 * ref.U * (want.abs() * 2 + 2 * G)).all()
+    assert torch.equal(c.weight.cpu()[table[0, 1].long()], w0[table[0, 1].long()])
+
+
 def test_decode_lengths_out_of_range(nats):
     rng = torch.Generator().manual_seed(4)
     table, _, k, v = _filled(rng, [64, 64], 16, 1, 64, BF)
