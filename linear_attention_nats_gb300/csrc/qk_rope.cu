@@ -12,7 +12,8 @@
 // pair are its own and the rotation needs no exchange: quads l and l + rot/8
 // for pairs (i, i + rot/2), quads 2l and 2l + 1 for pairs (2i, 2i + 1); in
 // both, the lane's four pairs are 4l .. 4l + 3.  A warp keeps one token's
-// cosines and sines and walks over the heads with them.
+// cosines and sines and walks over the heads with them; where tokens are many
+// and their rows few, each group of d / 8 lanes does so with a token of its own.
 //
 // Angles.  p f in fp32 is off by 2^-24 of the angle, whole radians at far
 // positions, and fp64 is slow on this chip.  The frequency becomes a 64-bit
@@ -166,6 +167,33 @@ __device__ __forceinline__ void lane_turns(const double* inv_freq, const LaneMap
 #pragma unroll
   for (int i = 0; i < N; ++i) F[i] = m.turned ? turns_fixed(inv_freq[m.pair0 + sub * N + i]) : 0;
 }
+// How a warp's 32 / LPR groups of lanes share the work: rows of one token side
+// by side (angles above), or, where a token has few rows, a token each.
+template <int LPR, bool EACH>
+struct Share {
+  static constexpr int kTokens = EACH ? 32 / LPR : 1;  // of a warp
+  static constexpr int kRows = 32 / LPR / kTokens;     // of a token, side by side
+  uint64_t F[EACH ? 4 : LPR / 8];
+  __device__ __forceinline__ Share(const double* inv_freq, const LaneMap& m, int sub) {
+    if constexpr (EACH) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(inv_freq[m.pair0 + i]) : 0;
+    } else {
+      lane_turns<LPR>(inv_freq, m, sub, F);
+    }
+  }
+  __device__ __forceinline__ void at(bool turned, long long p, int l, float* c, float* s) const {
+    if constexpr (EACH) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = 1.f, s[i] = 0.f;
+        if (turned) sincospif((float)(int32_t)((uint64_t)p * F[i] >> 32) * 0x1p-31f, &s[i], &c[i]);
+      }
+    } else {
+      angles<LPR>(F, turned, p, l, c, s);
+    }
+  }
+};
 
 // x[0..3] the lane's first quad, x[4..7] its second
 template <bool INTER>
@@ -210,12 +238,12 @@ __device__ __forceinline__ void lane_weights(const float* w, const LaneMap& m, f
   for (int i = 0; i < 8; ++i) o[i] = w ? w[(i < 4 ? m.qa : m.qb - 4) + i] : 1.f;
 }
 
-// Rows h0 .. h1 - 1 at src to L2, a lane a 128-byte line: the whole item's
-// reads are under way while the warp still forms its angles.
-template <typename T, int D>
+// Rows h0 .. h1 - 1 at src to L2, each of LANES lanes a 128-byte line: the whole
+// item's reads are under way while its angles are still being formed.
+template <typename T, int D, int LANES>
 __device__ __forceinline__ void prefetch_rows(const T* src, long long stride_h, int h0, int h1, int lane) {
   constexpr int kLines = D * (int)sizeof(T) / 128;
-  for (int i = lane; i < (h1 - h0) * kLines; i += 32) {
+  for (int i = lane; i < (h1 - h0) * kLines; i += LANES) {
     const T* p = src + (h0 + i / kLines) * stride_h + (i % kLines) * (128 / (int)sizeof(T));
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
   }
@@ -224,16 +252,15 @@ __device__ __forceinline__ void prefetch_rows(const T* src, long long stride_h, 
 constexpr int kRowsAhead = 4;  // row loads a lane has in flight
 
 // Rows h0 .. h1 - 1 of one token and one kind (query, key, or a value to
-// copy), their first row at src: kRowsAhead rows of every D / 8 lanes are
-// requested together.  row_at(h) is the destination of row h, or NULL to
+// copy), their first row at src, RPW of them side by side (this lane's from
+// row `sub` on): kRowsAhead rows of every D / 8 lanes are requested together.  row_at(h) is the destination of row h, or NULL to
 // leave it.  With the weights taken into the token's cosines and sines, a pair
 // costs four products and the row's 1 / n two:
 //   y_a = (x_a w_a c - x_b w_b s) / n,  y_b = (x_b w_b c + x_a w_a s) / n.
-template <typename T, int D, bool INTER, bool VEC, bool COPY, class RowAt>
+template <typename T, int D, int RPW, bool INTER, bool VEC, bool COPY, class RowAt>
 __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h0, int h1, const float* w, bool norm,
                                          float eps, const LaneMap& m, const float* c, const float* s, int sub,
                                          RowAt row_at) {
-  constexpr int RPW = 32 / (D / 8);
   float ca[4], sa[4], cb[4], sb[4];
   if (!COPY) {
     float wl[8];
@@ -293,31 +320,39 @@ __device__ __forceinline__ void fwd_rows(const T* src, long long stride_h, int h
   if (h < h1) rows(h + sub, std::false_type{});
 }
 
-// One warp per item (a token and a run of its rows): q rows, then k rows,
-// then (append) v rows.  Three CTAs an SM, four rows of a lane requested
+// One warp per item (a token and a run of its rows; EACH: as many tokens as it
+// has groups of lanes): q rows, then k rows, then (append) v rows.  Three CTAs an SM, four rows of a lane requested
 // together and the item's rows prefetched: 1.7 times the rate of one row at a
 // time (151 us for the 4 x 8192 tokens above).
-template <typename T, int D, bool INTER, bool PAGED, bool VEC>
+template <typename T, int D, bool INTER, bool PAGED, bool VEC, bool EACH>
 __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   constexpr int LPR = D / 8;
   begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l = lane % LPR, sub = lane / LPR;
-  const long long item = (long long)blockIdx.x * kWarps + warp;
-  const long long tok = item / a.items_per_token;
-  if (tok >= (long long)a.B * a.L) return;
+  using Sh = Share<LPR, EACH>;
+  const int l = lane % LPR, group = lane / LPR, sub = EACH ? 0 : group, pl = EACH ? l : lane;
+  const long long tokens = (long long)a.B * a.L;
+  const long long item = ((long long)blockIdx.x * kWarps + warp) * Sh::kTokens + (EACH ? group : 0);
+  long long tok = item / a.items_per_token;
+  if (EACH ? item - group >= tokens : tok >= tokens) return;
+  bool live = tok < tokens;  // (EACH: the last token again without writing, where a group has none)
+  tok = min(tok, tokens - 1);
   const int b = (int)(tok / a.L), t = (int)(tok % a.L);
   const int rows = a.Hq + a.Hk + (PAGED ? a.Hk : 0);
-  const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
-  const int r1 = min(rows, r0 + a.rows_per_item);
-  if (PAGED && a.n_new && t >= a.n_new[b]) return;
+  const int r0 = EACH ? 0 : (int)(item % a.items_per_token) * a.rows_per_item;
+  const int r1 = EACH ? rows : min(rows, r0 + a.rows_per_item);
+  if (PAGED && a.n_new) {
+    live = live && t < a.n_new[b];
+    if (!__any_sync(0xffffffffu, live)) return;
+  }
   const int k0 = max(r0 - a.Hq, 0), k1 = min(r1 - a.Hq, a.Hk);
   const T *qs = (const T*)a.q.p + b * a.q.b + t * a.q.t, *ks = (const T*)a.k.p + b * a.k.b + t * a.k.t;
-  prefetch_rows<T, D>(qs, a.q.h, r0, min(r1, a.Hq), lane);
-  prefetch_rows<T, D>(ks, a.k.h, k0, k1, lane);
+  constexpr int kLanes = EACH ? LPR : 32;
+  prefetch_rows<T, D, kLanes>(qs, a.q.h, r0, min(r1, a.Hq), pl);
+  prefetch_rows<T, D, kLanes>(ks, a.k.h, k0, k1, pl);
   const int v0 = max(r0 - a.Hq - a.Hk, 0), v1 = PAGED ? min(r1 - a.Hq - a.Hk, a.Hk) : 0;
   const T* vs = PAGED ? (const T*)a.v.p + b * a.v.b + t * a.v.t : nullptr;
-  if (PAGED) prefetch_rows<T, D>(vs, a.v.h, v0, v1, lane);
+  if (PAGED) prefetch_rows<T, D, kLanes>(vs, a.v.h, v0, v1, pl);
   long long p = a.pos0 + t;
   int pg = -1, slot = 0;
   if (PAGED) {
@@ -327,24 +362,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
       pg = a.pg.page_of(b, (int)at / a.pg.page);
       slot = (int)at % a.pg.page;
     }
-    if (pg < 0 && lane == 0 && r0 == 0) *a.pg.err = 1;
+    if (pg < 0 && live && pl == 0 && r0 == 0) *a.pg.err = 1;
+    if (!live) pg = -1;
   }
   if (a.pos) p = a.pos[b * a.pos_b + t];
   const LaneMap m = lane_map<INTER>(l, a.rot);
   float c[4], s[4];
-  {
-    uint64_t F[LPR / 8];
-    lane_turns<LPR>(a.inv_freq, m, sub, F);
-    angles<LPR>(F, m.turned, p, l, c, s);
-  }
+  Sh(a.inv_freq, m, sub).at(m.turned, p, l, c, s);
+  constexpr int RPW = Sh::kRows;
   if (r0 < a.Hq) {
     T* dst = (T*)a.qo.p + b * a.qo.b + t * a.qo.t;
-    fwd_rows<T, D, INTER, VEC, false>(qs, a.q.h, r0, min(r1, a.Hq), a.wq, a.norm,
-                                      a.eps, m, c, s, sub, [&](int h) { return dst + h * a.qo.h; });
+    fwd_rows<T, D, RPW, INTER, VEC, false>(qs, a.q.h, r0, min(r1, a.Hq), a.wq, a.norm, a.eps, m, c, s, sub,
+                                           [&](int h) { return EACH && !live ? nullptr : dst + h * a.qo.h; });
   }
   if (k0 < k1) {
     if (PAGED) {
-      fwd_rows<T, D, INTER, VEC, false>(ks, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub, [&](int h) -> T* {
+      fwd_rows<T, D, RPW, INTER, VEC, false>(ks, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub, [&](int h) -> T* {
         if (pg < 0) return nullptr;
         const long long at = a.pg.row(pg, h, slot);
         if (a.weight && l == 0) a.weight[at] = 0.f;
@@ -352,14 +385,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
       });
     } else {
       T* dst = (T*)a.ko.p + b * a.ko.b + t * a.ko.t;
-      fwd_rows<T, D, INTER, VEC, false>(ks, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub,
-                                        [&](int h) { return dst + h * a.ko.h; });
+      fwd_rows<T, D, RPW, INTER, VEC, false>(ks, a.k.h, k0, k1, a.wk, a.norm, a.eps, m, c, s, sub,
+                                             [&](int h) { return EACH && !live ? nullptr : dst + h * a.ko.h; });
     }
   }
   if (PAGED) {
-    if (v0 < v1 && pg >= 0)
-      fwd_rows<T, D, INTER, VEC, true>(vs, a.v.h, v0, v1, nullptr, false, 0.f, m,
-                                       c, s, sub, [&](int h) { return (T*)a.v_pages + a.pg.row(pg, h, slot) * D; });
+    if (v0 < v1 && (EACH || pg >= 0))
+      fwd_rows<T, D, RPW, INTER, VEC, true>(vs, a.v.h, v0, v1, nullptr, false, 0.f, m, c, s, sub, [&](int h) -> T* {
+        return EACH && pg < 0 ? nullptr : (T*)a.v_pages + a.pg.row(pg, h, slot) * D;
+      });
   }
 }
 
@@ -382,11 +416,11 @@ constexpr int kBwdBlocks = sizeof(T) + sizeof(GI) == 4 ? 4 : 3;
 
 // Gradients of rows h0 .. h1 - 1 of one token and one kind; acc gathers the
 // lane's share of dw.
-template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
+template <typename T, typename GI, typename GO, int D, int RPW, bool INTER, bool VEC>
 __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* src, long long x_h, GO* dst,
                                          long long d_h, int h0, int h1, const float* w, bool norm, float eps,
-                                         const LaneMap& m, const float* c, const float* s, int sub, float* acc) {
-  constexpr int RPW = 32 / (D / 8), kAhead = 8 / RPW;  // eight rows of a warp in flight
+                                         const LaneMap& m, const float* c, const float* s, int sub, bool live, float* acc) {
+  constexpr int kAhead = RPW > 1 ? 8 / RPW : 4;  // eight rows of a warp in flight (RPW 1: four of each token)
   float wl[8];
   lane_weights(w, m, wl);
   const int dq = m.qb - m.qa;
@@ -399,7 +433,7 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
     Quad<T, VEC> xa[kAhead], xb[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const bool on = full || h + i * RPW < h1;
+      const bool on = live && (full || h + i * RPW < h1);
       if (on) {
         ga[i].load(pg);
         gb[i].load(pg + dq);
@@ -416,7 +450,7 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const bool on = full || h + i * RPW < h1;
+      const bool on = live && (full || h + i * RPW < h1);
       if (!full && h - sub + i * RPW >= h1) break;  // (none of the warp's rows)
       float u[8];
       ga[i].get(u), gb[i].get(u + 4);
@@ -459,42 +493,46 @@ __device__ __forceinline__ void bwd_rows(const GI* g, long long g_h, const T* sr
 // their shares of dw_q, dw_k in registers (8 entries of each a lane).  Bytes
 // in flight bound it: 12 warps an SM with eight rows each 176 us, 16 with four
 // 191 us; prefetching the next item to L2 as well 227 us (the prefetched rows
-// push each other out).
-template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC>
+// push each other out).  EACH: items of as many tokens as a warp has groups.
+template <typename T, typename GI, typename GO, int D, bool INTER, bool VEC, bool EACH>
 __global__ void __launch_bounds__(kWarpsBwd * 32, kBwdBlocks<T, GI>) rope_bwd_kernel(RopeBwdArgs a) {
   constexpr int LPR = D / 8;
   __shared__ float red[kWarpsBwd][D];
   begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l = lane % LPR, sub = lane / LPR;
+  using Sh = Share<LPR, EACH>;
+  constexpr int RPW = Sh::kRows;
+  const int l = lane % LPR, sub = lane / LPR, row0 = EACH ? 0 : sub;
   const LaneMap m = lane_map<INTER>(l, a.rot);
-  uint64_t F[LPR / 8];
-  lane_turns<LPR>(a.inv_freq, m, sub, F);
+  const Sh share(a.inv_freq, m, sub);
   float aq[8], ak[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
   const int rows = a.Hq + a.Hk;
   const long long n_items = (long long)a.B * a.L * a.items_per_token;
-  for (long long item = (long long)blockIdx.x * kWarpsBwd + warp; item < n_items; item += (long long)gridDim.x * kWarpsBwd) {
+  for (long long first = ((long long)blockIdx.x * kWarpsBwd + warp) * Sh::kTokens; first < n_items;
+       first += (long long)gridDim.x * kWarpsBwd * Sh::kTokens) {
+    const bool live = !EACH || first + sub < n_items;  // (else the last token again, for nothing)
+    const long long item = EACH ? min(first + sub, n_items - 1) : first;
     const long long tok = item / a.items_per_token;
     const int b = (int)(tok / a.L), t = (int)(tok % a.L);
-    const int r0 = (int)(item % a.items_per_token) * a.rows_per_item;
-    const int r1 = min(rows, r0 + a.rows_per_item);
+    const int r0 = EACH ? 0 : (int)(item % a.items_per_token) * a.rows_per_item;
+    const int r1 = EACH ? rows : min(rows, r0 + a.rows_per_item);
     float c[4], s[4];
-    angles<LPR>(F, m.turned, a.pos ? a.pos[b * a.pos_b + t] : a.pos0 + t, l, c, s);
+    share.at(m.turned, a.pos ? a.pos[b * a.pos_b + t] : a.pos0 + t, l, c, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = -s[i];
     if (r0 < a.Hq)
-      bwd_rows<T, GI, GO, D, INTER, VEC>((const GI*)a.gq.p + b * a.gq.b + t * a.gq.t, a.gq.h,
-                                         (const T*)a.q.p + b * a.q.b + t * a.q.t, a.q.h,
-                                         (GO*)a.dq.p + b * a.dq.b + t * a.dq.t, a.dq.h, r0, min(r1, a.Hq), a.wq, a.norm,
-                                         a.eps, m, c, s, sub, aq);
+      bwd_rows<T, GI, GO, D, RPW, INTER, VEC>((const GI*)a.gq.p + b * a.gq.b + t * a.gq.t, a.gq.h,
+                                              (const T*)a.q.p + b * a.q.b + t * a.q.t, a.q.h,
+                                              (GO*)a.dq.p + b * a.dq.b + t * a.dq.t, a.dq.h, r0, min(r1, a.Hq), a.wq,
+                                              a.norm, a.eps, m, c, s, row0, live, aq);
     const int k0 = max(r0 - a.Hq, 0), k1 = min(r1 - a.Hq, a.Hk);
     if (k0 < k1)
-      bwd_rows<T, GI, GO, D, INTER, VEC>((const GI*)a.gk.p + b * a.gk.b + t * a.gk.t, a.gk.h,
-                                         (const T*)a.k.p + b * a.k.b + t * a.k.t, a.k.h,
-                                         (GO*)a.dk.p + b * a.dk.b + t * a.dk.t, a.dk.h, k0, k1, a.wk, a.norm, a.eps, m,
-                                         c, s, sub, ak);
+      bwd_rows<T, GI, GO, D, RPW, INTER, VEC>((const GI*)a.gk.p + b * a.gk.b + t * a.gk.t, a.gk.h,
+                                              (const T*)a.k.p + b * a.k.b + t * a.k.t, a.k.h,
+                                              (GO*)a.dk.p + b * a.dk.b + t * a.dk.t, a.dk.h, k0, k1, a.wk, a.norm, a.eps,
+                                              m, c, s, row0, live, ak);
   }
   if (!a.part) return;
   // the CTA's sums: over the rows of a warp, then over the warps in order
@@ -579,24 +617,46 @@ nats_status check_rope(const nats_rope_dims* d) {
   return NATS_OK;
 }
 
+// Whether a warp's groups of lanes take a token each, its rows one after the
+// other, in place of one token's rows side by side: where the tokens are more
+// than the `wave` of warps that run at once and a token's rows are few, the
+// chain from a position to a row is what a warp waits for, and two to four of
+// them then run together.  `bytes`: of a token's rows, up to which the reads of
+// a warp's tokens still follow one another closely enough (measured on both
+// sides, time with a token each against without, 30,000 to 40,000 tokens):
+//   forward  bf16 d 128: 1 + 1 heads 25 / 42 us, 12 + 4 58 / 69, 20 + 4 68 / 66
+//            bf16 d 64: 1 + 1 14 / 36 us, 20 + 4 39 / 44, 16 + 16 63 / 61
+//            fp32 d 128: 4 + 4 54 / 58 us, 8 + 2 67 / 66
+//   gradient bf16 d 128: 1 + 1 39 / 66 us, 20 + 4 131 / 138, 24 + 4 151 / 150
+//            fp32 d 128: 8 + 2 104 / 110 us, 16 + 4 148 / 146
+// and with 3600 tokens (one wave) 12 + 4 heads 8.3 / 7.3 us forward.
+bool token_each(long long tokens, long long wave, int rows, int row_bytes, int most_rows, int bytes, bool vec) {
+  return vec && tokens > wave && rows <= most_rows && rows * row_bytes <= bytes;
+}
+
 template <bool PAGED>
 cudaError_t launch_fwd(RopeArgs& a, int dtype, int d, bool inter, bool vec, cudaStream_t st) {
   const long long tokens = (long long)a.B * a.L;
-  const int rows = a.Hq + a.Hk * (PAGED ? 2 : 1);
-  split_rows(tokens, rows, 32 / (d / 8), (long long)kSMs * 3 * kWarps, &a.rows_per_item, &a.items_per_token);
-  const long long items = tokens * a.items_per_token;
-  const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
-#define NATS_ROPE(T, D, I, V) after(rope_fwd_kernel<T, D, I, PAGED, V>, grid, kWarps * 32, 0, st, 0, a)
-#define NATS_ROPE_V(T, D, I) (vec ? NATS_ROPE(T, D, I, true) : NATS_ROPE(T, D, I, false))
+  const int rows = a.Hq + a.Hk * (PAGED ? 2 : 1), rpw = 32 / (d / 8);
+  const long long wave = (long long)kSMs * 3 * kWarps;
+  split_rows(tokens, rows, rpw, wave, &a.rows_per_item, &a.items_per_token);
+  const bool each = token_each(tokens, wave, rows, d * (dtype == NATS_BF16 ? 2 : 4), 24, 4096, vec);
+  const long long warps = each ? (tokens + rpw - 1) / rpw : tokens * a.items_per_token;
+  if (each) a.items_per_token = 1;
+  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+#define NATS_ROPE(T, D, I, V, E) after(rope_fwd_kernel<T, D, I, PAGED, V, E>, grid, kWarps * 32, 0, st, 0, a)
+#define NATS_ROPE_V(T, D, I) \
+  (each ? NATS_ROPE(T, D, I, true, true) : vec ? NATS_ROPE(T, D, I, true, false) : NATS_ROPE(T, D, I, false, false))
 #define NATS_ROPE_I(T, D) (inter ? NATS_ROPE_V(T, D, true) : NATS_ROPE_V(T, D, false))
   if (dtype == NATS_BF16) return d == 128 ? NATS_ROPE_I(__nv_bfloat16, 128) : NATS_ROPE_I(__nv_bfloat16, 64);
   return d == 128 ? NATS_ROPE_I(float, 128) : NATS_ROPE_I(float, 64);
 }
 
 template <typename T, typename GI, typename GO>
-cudaError_t launch_bwd(const RopeBwdArgs& a, int d, bool inter, bool vec, unsigned grid, cudaStream_t st) {
-#define NATS_BWD(D, I, V) after(rope_bwd_kernel<T, GI, GO, D, I, V>, grid, kWarpsBwd * 32, 0, st, 0, a)
-#define NATS_BWD_V(D, I) (vec ? NATS_BWD(D, I, true) : NATS_BWD(D, I, false))
+cudaError_t launch_bwd(const RopeBwdArgs& a, int d, bool inter, bool vec, bool each, unsigned grid, cudaStream_t st) {
+#define NATS_BWD(D, I, V, E) after(rope_bwd_kernel<T, GI, GO, D, I, V, E>, grid, kWarpsBwd * 32, 0, st, 0, a)
+#define NATS_BWD_V(D, I) \
+  (each ? NATS_BWD(D, I, true, true) : vec ? NATS_BWD(D, I, true, false) : NATS_BWD(D, I, false, false))
 #define NATS_BWD_I(D) (inter ? NATS_BWD_V(D, true) : NATS_BWD_V(D, false))
   return d == 128 ? NATS_BWD_I(128) : NATS_BWD_I(64);
 }
@@ -742,21 +802,25 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
   const int most = kSMs * (dims->dtype == NATS_BF16 && grad_dtype == NATS_BF16 ? kBwdBlocks<__nv_bfloat16, __nv_bfloat16>
                                                                              : kBwdBlocks<float, float>);
   split_rows(tokens, a.Hq + a.Hk, 32 / (dims->d / 8), most * kWarpsBwd, &a.rows_per_item, &a.items_per_token);
-  const long long ctas = (tokens * a.items_per_token + kWarpsBwd - 1) / kWarpsBwd;
+  const int rpw = 32 / (dims->d / 8);
+  const bool each = token_each(tokens, most * kWarpsBwd, a.Hq + a.Hk, dims->d * es, 32, 6144, vec);
+  if (each) a.items_per_token = 1;
+  const long long warps = each ? (tokens + rpw - 1) / rpw : tokens * a.items_per_token;
+  const long long ctas = (warps + kWarpsBwd - 1) / kWarpsBwd;
   const unsigned grid = (unsigned)(ctas < most ? ctas : most);
   const bool inter = dims->interleaved != 0;
   const int d = dims->d;
   cudaError_t e;
   if (dims->dtype == NATS_F32)
-    e = launch_bwd<float, float, float>(a, d, inter, vec, grid, st);
+    e = launch_bwd<float, float, float>(a, d, inter, vec, each, grid, st);
   else if (grad_dtype == NATS_F32 && dx_dtype == NATS_F32)
-    e = launch_bwd<__nv_bfloat16, float, float>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, float, float>(a, d, inter, vec, each, grid, st);
   else if (grad_dtype == NATS_F32)
-    e = launch_bwd<__nv_bfloat16, float, __nv_bfloat16>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, float, __nv_bfloat16>(a, d, inter, vec, each, grid, st);
   else if (dx_dtype == NATS_F32)
-    e = launch_bwd<__nv_bfloat16, __nv_bfloat16, float>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, __nv_bfloat16, float>(a, d, inter, vec, each, grid, st);
   else
-    e = launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, grid, st);
+    e = launch_bwd<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, d, inter, vec, each, grid, st);
   const int r = record_cuda_error(e);
   if (r != NATS_OK || !dw) return (nats_status)r;
   const float* part = a.part;

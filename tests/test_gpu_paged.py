@@ -416,6 +416,43 @@ def test_append(nats, T, n_new, start, Hq, Hk, d, page, dtype, norm, rot, inter)
             assert (out_q[b, :, n:] == 9).all()
 
 
+# more tokens than warps run at once, few rows each: a group of lanes takes a token of its own
+@pytest.mark.parametrize("T,n_new,start,Hq,Hk,d,page,dtype,norm,rot,inter", [
+    (1301, [1301, 0, 777], [5, 0, 31], 4, 2, 128, 16, BF, True, 128, False),
+    (1301, None, None, 1, 3, 64, 48, F32, True, 32, True),
+])
+def test_append_of_many_tokens(nats, T, n_new, start, Hq, Hk, d, page, dtype, norm, rot, inter):
+    test_append(nats, T, n_new, start, Hq, Hk, d, page, dtype, norm, rot, inter)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_append_of_many_tokens_outside_the_table_or_pool(nats, dtype, d):
+    """One call writes what calls of so few tokens write that the rows of one lie side by side, and reports the same."""
+    rng = torch.Generator().manual_seed(19)
+    B, T, page, Hk, Hq = 3, 1301, 16, 2, 1
+    table, _, n_pages = ref.assign([T, T, T], page, rng, 2)
+    table[1, 40], table[2, 5:] = n_pages, -1
+    table = table[:, :75]  # the last 101 tokens of each lie outside
+    start, n_new = torch.tensor([0, 3, 0], dtype=torch.int32), torch.tensor([1301, 1200, 1], dtype=torch.int32)
+    x = [torch.randn(B, h, T, d, generator=rng).to(dtype).cuda() for h in (Hq, Hk, Hk)]
+    f = nats.rope_inv_freq(d)
+    pools = []
+    for step in (T, 400):
+        w = torch.ones(n_pages, Hk, page)
+        c = _cache(nats, table, [0] * B, *_pool(rng, n_pages, Hk, page, d, dtype, garbage=False), w)
+        out = torch.full_like(x[0], 5.0)
+        for a in range(0, T, step):
+            q, k, v = (y[:, :, a:a + step] for y in x)
+            nats.paged_append(c, k, v, start=(start + a).cuda(), n_new=(n_new - a).clamp(min=0).cuda(), q=q,
+                              out_q=out[:, :, a:a + step], norm=True, inv_freq=f)
+        with pytest.raises(nats.NatsError):
+            c.check()
+        pools.append([c.k_pages, c.v_pages, c.weight, out])
+    for one, parts in zip(*pools):
+        assert torch.equal(one, parts)
+    assert (pools[0][3][2, :, 1:] == 5).all() and not (pools[0][3][0] == 5).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_append_from_odd_addresses(nats, dtype):
     """Rows that start at odd entries move entry by entry, to the same values."""

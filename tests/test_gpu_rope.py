@@ -110,6 +110,50 @@ def test_backward(nats, case, grad, dx):
         assert ((r["dw_" + n].cpu().double() - dw).abs() <= 256 * ref.U * pair + 1e-30).all()
 
 
+# more tokens than warps run at once, few rows each: a group of lanes takes a token of its own
+MANY = [
+    (3, 1307, 2, 1, 128, 128, False, BF, True, "fused", True),
+    (1, 3931, 1, 1, 128, 48, True, F32, True, "contiguous", True),
+    (2, 2001, 4, 2, 64, 32, True, BF, True, "fused", False),
+    (7, 701, 0, 3, 64, 64, False, F32, True, "contiguous", True),
+    (1, 4099, 13, 0, 128, 112, False, BF, False, "fused", False),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_forward_of_many_tokens(nats, case):
+    test_forward(nats, case)
+
+
+@pytest.mark.parametrize("case", MANY)
+@pytest.mark.parametrize("grad,dx", [("x", "x"), ("f32", "x")])
+def test_backward_of_many_tokens(nats, case, grad, dx):
+    test_backward(nats, case, grad, dx)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 128)])
+def test_many_tokens_in_place_and_in_parts(nats, dtype, d):
+    """The same bits in place, and from calls of so few tokens that the rows of one lie side by side."""
+    rng = torch.Generator().manual_seed(23)
+    q, k = torch.randn(1, 3, 4099, d, generator=rng).to(dtype).cuda(), torch.randn(1, 1, 4099, d, generator=rng).to(dtype).cuda()
+    g = [torch.randn(x.shape, generator=rng).to(dtype).cuda() for x in (q, k)]
+    f = nats.rope_inv_freq(d)
+    y = nats.qk_norm_rope(q, k, None, None, f, pos0=7)
+    r = nats.qk_norm_rope_bwd(*g, q, k, None, None, f, pos0=7)
+    for a in range(0, 4099, 1000):
+        part = [x[:, :, a:a + 1000] for x in (q, k, *g)]
+        for whole, p in zip(y, nats.qk_norm_rope(*part[:2], None, None, f, pos0=7 + a)):
+            assert torch.equal(whole[:, :, a:a + 1000], p)
+        rp = nats.qk_norm_rope_bwd(*part[2:], *part[:2], None, None, f, pos0=7 + a)
+        assert torch.equal(r["dq"][:, :, a:a + 1000], rp["dq"]) and torch.equal(r["dk"][:, :, a:a + 1000], rp["dk"])
+    gi = [x.clone() for x in g]
+    ri = nats.qk_norm_rope_bwd(*gi, q, k, None, None, f, pos0=7, dq=gi[0], dk=gi[1])
+    for n in ("dq", "dk", "dw_q", "dw_k"):
+        assert torch.equal(ri[n], r[n])
+    yi = nats.qk_norm_rope(q, k, None, None, f, pos0=7, out_q=q, out_k=k)
+    assert torch.equal(yi[0], y[0]) and torch.equal(yi[1], y[1])
+
+
 def test_backward_against_differences(nats):
     """<dx, v> = d/dt <dy, y(x + t v)> by central differences of the 64-bit
     forward; h = 1e-5 leaves h^2 of third derivatives, about 1e-9, and the
