@@ -31,7 +31,7 @@ constexpr int kBins = 2048;
 constexpr int kKeysHeld = 32768;       // slots of a CTA's share in shared memory; a longer share is read again
 constexpr int kSMs = 152;
 constexpr int kMaxCluster = 8;
-constexpr int kFusedRows = 512, kFusedBytes = 65536;  // of a head's keys that the selecting CTA copies itself
+constexpr int kFusedRows = 512, kFusedBytes = 65536;  // of a head's keys that the selecting CTA copies itself (launch_select)
 constexpr int kShortShare = 8192, kShortThreads = 512;  // slots of a share, threads of its CTA
 constexpr int kCopyRows = 64;
 constexpr int kCopyThreads = 256;
@@ -361,12 +361,16 @@ cudaError_t launch_select(const EvictArgs& a, long long cap, int C, cudaStream_t
 // warp's fixed steps (barriers, scans) then outweigh its slots': 64 x 8 heads
 // of 1000 slots 55.6 us in all with 512 threads, 64.0 with 1024; long ones by
 // large CTAs: one head of 131,072 34.5 us with 1024, 37.5 with 512.  *copied:
-// the kernel copies too, which pays while a CTA's rows are few.
+// the kernel copies too, which pays while a CTA's rows are few, more of them
+// where every SM has CTAs that select while others copy (64 x 16 heads of 700
+// slots to 400: 74 us, 90 with the copy apart; but 32 x 8 of 2112 to 2048, 91
+// against 72).
 cudaError_t launch_select(const EvictArgs& a, long long cap, bool* copied, cudaStream_t st) {
   const long long heads = (long long)a.pg.B * a.pg.Hk;
   int C = 1;
   while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 4096) C *= 2;
-  *copied = C == 1 && a.budget <= kFusedRows && (long long)a.budget * a.row_bytes <= kFusedBytes;
+  *copied = C == 1 && a.budget <= kFusedRows &&
+            (heads >= 2 * kSMs || (long long)a.budget * a.row_bytes <= kFusedBytes);
   if (cap / C > kShortShare) {
     *copied = false;
     return launch_select<1024, false>(a, cap, C, st);

@@ -602,6 +602,11 @@ def test_evict_short_sequences_in_long_tables(nats, max_pages, lens):
     assert n.cpu().tolist() == [min(x, budget) for x in lens]
 
 
+def test_evict_of_many_heads(nats):
+    """More heads than two to an SM: each is copied by the CTA that selects it."""
+    test_evict(nats, [600 - 13 * b for b in range(20)], 16, 64, 16, F32, 400, 30, 2, "ties")
+
+
 def test_evict_bad_entries_are_reported(nats):
     rng = torch.Generator().manual_seed(10)
     table, spare, k, v = _filled(rng, [64], 16, 1, 64, F32, extra=2)
