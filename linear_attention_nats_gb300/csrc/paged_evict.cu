@@ -357,18 +357,20 @@ cudaError_t launch_select(const EvictArgs& a, long long cap, int C, cudaStream_t
 }
 
 // CTAs of a head: as many as fill the GPU, while a share is worth its part of
-// the cluster's barriers (4096 slots).  Short shares by small CTAs, since a
-// warp's fixed steps (barriers, scans) then outweigh its slots': 64 x 8 heads
-// of 1000 slots 55.6 us in all with 512 threads, 64.0 with 1024; long ones by
-// large CTAs: one head of 131,072 34.5 us with 1024, 37.5 with 512.  *copied:
-// the kernel copies too, which pays while a CTA's rows are few, more of them
-// where every SM has CTAs that select while others copy (64 x 16 heads of 700
-// slots to 400: 74 us, 90 with the copy apart; but 32 x 8 of 2112 to 2048, 91
-// against 72).
+// the cluster's barriers (2048 slots: 16 heads of 9199 34 us, 41 with shares of
+// 4096; with 1024 32 heads of 5000 29 us, 25 with 2048; clusters of 16 gain
+// only past 8 x 32768 slots, 66 to 40 us for 2 heads of 400,000, and cost the
+// others 2 us).  Short shares by small CTAs, since a warp's fixed steps
+// (barriers, scans) then outweigh its slots': 64 x 8 heads of 1000 slots 55.6
+// us with 512 threads, 64.0 with 1024 (and the copy apart); long ones by large CTAs: one head
+// of 131,072 34.5 us with 1024, 37.5 with 512.  *copied: the kernel copies too,
+// which pays while a CTA's rows are few, more of them where every SM has CTAs
+// that select while others copy (64 x 16 heads of 700 slots to 400: 75 us, 90
+// with the copy apart; but 32 x 8 of 2112 to 2048, 91 against 72).
 cudaError_t launch_select(const EvictArgs& a, long long cap, bool* copied, cudaStream_t st) {
   const long long heads = (long long)a.pg.B * a.pg.Hk;
   int C = 1;
-  while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 4096) C *= 2;
+  while (C < kMaxCluster && heads * C < kSMs && cap / (2 * C) >= 2048) C *= 2;
   *copied = C == 1 && a.budget <= kFusedRows &&
             (heads >= 2 * kSMs || (long long)a.budget * a.row_bytes <= kFusedBytes);
   if (cap / C > kShortShare) {
