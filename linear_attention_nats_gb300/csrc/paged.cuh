@@ -17,7 +17,7 @@ struct PagedView {
   int32_t* err;
   int n_pages, page, Hk, B, max_pages;
 
-  __device__ __forceinline__ int cap() const { return max_pages * page; }
+  __host__ __device__ __forceinline__ int cap() const { return max_pages * page; }
   // lens[b] brought into 0 .. cap
   __device__ __forceinline__ int length(int b) const { return min(max(lens[b], 0), cap()); }
   // the page of slot block `i` of sequence b, or -1 when the entry is not one

@@ -16,7 +16,7 @@
 // Measured on one GB300 (HBM copy rate 6.8 TB/s): 32 contexts of 3000 to 8192
 // slots, 32 query and 8 key heads of 128, bf16: 112 us, 6.2 TB/s, the tensor
 // pipe 13 % busy; 4 contexts of up to 131,072 with weights 292 us, 5.7 TB/s (and
-// 134 MB of scores between the kernels); fp32 the same way, 5.6 TB/s at 8 x
+// 134 MB of scores between the kernels); fp32 the same way, 5.8 TB/s at 8 x
 // 16384; 517 slots of one sequence 9.1 us, which is the two kernels' latency.
 #include <cmath>
 
@@ -341,12 +341,12 @@ struct Bf16 {
 // x y = x_h y_h + x_h y_l + x_l y_h to about 2^-23.  K: the lane holds entries
 // 16 y + 4 c .. + 3 of its slots; V: entries 4 g + 32 y .. + 3 of slots c,
 // c + 4, c + 8, c + 12.  P reaches its layout by shuffles.
-template <int D>
+template <int D, bool QREG>
 struct F32 {
   using T = float;
   static constexpr int kD = D;
   static constexpr int KB = D / 16, VS = D / 32, MT = D / 16;
-  struct Q { float4 r[KB]; };
+  struct Q { float4 r[QREG ? KB : 1]; const T* p; };  // QREG: held in r, else read at p for every step (L1)
   struct K { uint4 r[2][KB]; };
   struct V { uint4 r[4][VS]; };
 
@@ -363,23 +363,35 @@ struct F32 {
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
-  // A B in split precision: the full products into c, the small ones into
-  // `small`.  The instruction cuts its sums off where fp32 additions round, so
+  // A B in split precision (A split already): the full products into c, the
+  // small ones into `small`.  The instruction cuts its sums off where fp32 additions round, so
   // c is a fresh accumulator, added outside, wherever a sum is long.
-  static __device__ __forceinline__ void mma3(float (&c)[4], float (&small)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
-    uint32_t h[4], l[4], hb[2], lb[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) split(a[i], h[i], l[i]);
+  struct Parts4 { uint32_t h[4], l[4]; };
+  static __device__ __forceinline__ Parts4 split4(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    Parts4 p;
+    split(a0, p.h[0], p.l[0]), split(a1, p.h[1], p.l[1]), split(a2, p.h[2], p.l[2]), split(a3, p.h[3], p.l[3]);
+    return p;
+  }
+  static __device__ __forceinline__ void mma3(float (&c)[4], float (&small)[4], const Parts4& a, uint32_t b0, uint32_t b1) {
+    uint32_t hb[2], lb[2];
     split(b0, hb[0], lb[0]), split(b1, hb[1], lb[1]);
-    mma(c, h[0], h[1], h[2], h[3], hb[0], hb[1]);
-    mma(small, l[0], l[1], l[2], l[3], hb[0], hb[1]);
-    mma(small, h[0], h[1], h[2], h[3], lb[0], lb[1]);
+    mma(c, a.h[0], a.h[1], a.h[2], a.h[3], hb[0], hb[1]);
+    mma(small, a.l[0], a.l[1], a.l[2], a.l[3], hb[0], hb[1]);
+    mma(small, a.h[0], a.h[1], a.h[2], a.h[3], lb[0], lb[1]);
   }
 
+  // (p is a row of q whether `on` or not)
   static __device__ __forceinline__ void load_q(Q& q, const T* p, bool on, int c) {
+    q.p = p + 4 * c;
+    if (!QREG) return;
 #pragma unroll
     for (int y = 0; y < KB; ++y) q.r[y] = on ? *(const float4*)(p + 16 * y + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  static __device__ __forceinline__ float4 q_at(const Q& q, int y) {
+    if (QREG) return q.r[y];
+    float4 v;  // (not to be held across steps)
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(q.p + 16 * y));
+    return v;
   }
   static __device__ __forceinline__ int k_base(int g, int c) { return g * D + 4 * c; }
   static constexpr __device__ int k_off(int i, int y) { return 8 * i * D + 16 * y; }
@@ -388,44 +400,54 @@ struct F32 {
   static constexpr __device__ int v_off(int i, int y) { return 4 * i * D + 32 * y; }
   template <int NH>
   static __device__ __forceinline__ void scores(float (&s)[NH][4], const K& k, const Q (&q)[NH]) {
-    static_assert(NH == 1, "units of eight heads");
-    float small[2][4] = {};
+    constexpr int kChains = NH == 1 ? 2 : 1;
+    float small[kChains][NH][4] = {};
 #pragma unroll
     for (int y = 0; y < KB; ++y) {
       const uint4 k0 = k.r[0][y], k1 = k.r[1][y];
-      const float4 qy = q[0].r[y];
-      float c0[4] = {}, c1[4] = {};
-      const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
-      mma3(c0, small[0], a0, __float_as_uint(qy.x), __float_as_uint(qy.y));
-      mma3(c1, small[1], a1, __float_as_uint(qy.z), __float_as_uint(qy.w));
+      const Parts4 a0 = split4(k0.x, k1.x, k0.y, k1.y), a1 = split4(k0.z, k1.z, k0.w, k1.w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] += c0[i] + c1[i];
+      for (int x = 0; x < NH; ++x) {
+        const float4 qy = q_at(q[x], y);
+        float c0[4] = {}, c1[4] = {};
+        mma3(c0, small[0][x], a0, __float_as_uint(qy.x), __float_as_uint(qy.y));
+        mma3(c1, small[kChains - 1][x], a1, __float_as_uint(qy.z), __float_as_uint(qy.w));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] += c0[i] + c1[i];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[0][i] += small[0][i] + small[1][i];
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[x][i] += kChains == 2 ? small[0][x][i] + small[kChains - 1][x][i] : small[0][x][i];
   }
   template <int NH>
   static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int g,
                                                 int c) {
     // slots c, c + 4, c + 8, c + 12 of head g: from the lanes with that slot (and 8 on) and the head's pair
-    uint32_t b[4];
+    uint32_t b[NH][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int src = 4 * (c + 4 * i) + g / 2;
-      const float e0 = __shfl_sync(0xffffffffu, p[0][0], src), e1 = __shfl_sync(0xffffffffu, p[0][1], src);
-      const float e2 = __shfl_sync(0xffffffffu, p[0][2], src), e3 = __shfl_sync(0xffffffffu, p[0][3], src);
-      b[i] = __float_as_uint(g % 2 ? e1 : e0), b[i + 2] = __float_as_uint(g % 2 ? e3 : e2);
-    }
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int src = 4 * (c + 4 * i) + g / 2;
+        const float e0 = __shfl_sync(0xffffffffu, p[x][0], src), e1 = __shfl_sync(0xffffffffu, p[x][1], src);
+        const float e2 = __shfl_sync(0xffffffffu, p[x][2], src), e3 = __shfl_sync(0xffffffffu, p[x][3], src);
+        b[x][i] = __float_as_uint(g % 2 ? e1 : e0), b[x][i + 2] = __float_as_uint(g % 2 ? e3 : e2);
+      }
 #pragma unroll
     for (int y = 0; y < MT; ++y) {
       // rows g and g + 8 of tile y: entry y % 4 of the lane's segments 2 (y / 4) and 2 (y / 4) + 1
       auto at = [&](int slot, int seg) { return ((const uint32_t*)&v.r[slot][2 * (y / 4) + seg])[y % 4]; };
-      const uint32_t a[4] = {at(0, 0), at(0, 1), at(1, 0), at(1, 1)}, a2[4] = {at(2, 0), at(2, 1), at(3, 0), at(3, 1)};
-      float full[4] = {}, small[4] = {};
-      mma3(full, small, a, b[0], b[1]);
-      mma3(full, small, a2, b[2], b[3]);
+      const Parts4 a = split4(at(0, 0), at(0, 1), at(1, 0), at(1, 1)), a2 = split4(at(2, 0), at(2, 1), at(3, 0), at(3, 1));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[0][y][i] += full[i] + small[i];
+      for (int x = 0; x < NH; ++x) {
+        float full[4] = {}, small[4] = {};
+        mma3(full, small, a, b[x][0], b[x][1]);
+        mma3(full, small, a2, b[x][2], b[x][3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[x][y][i] += full[i] + small[i];
+      }
     }
   }
   static __device__ __forceinline__ int entry(int y, int g, int upper) {
@@ -471,7 +493,8 @@ struct Unit {
   __device__ __forceinline__ void start(const typename X::T* q0, long long q_h, int heads, int g, int c) {
 #pragma unroll
     for (int x = 0; x < NH; ++x) {
-      X::load_q(q[x], q0 + (8 * x + g) * q_h, 8 * x + g < heads, c);
+      const bool on = 8 * x + g < heads;
+      X::load_q(q[x], q0 + (on ? 8 * x + g : 0) * q_h, on, c);
 #pragma unroll
       for (int y = 0; y < MT; ++y)
 #pragma unroll
@@ -937,13 +960,23 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
              : after(decode_finish_kernel<T, D, 1>, grid, kThreads, smem, st, 0, a, join);
 }
 
-// Units of eight heads; bf16 groups of more than eight in units of sixteen,
-// whose rows are then read once: 16 x 16384 slots, 12 heads a group, 117 us
-// (83 % of the copy rate, with two warps a scheduler); their heads dealt to
-// several warps 161 us where this took 145.  fp32 has not the registers and
-// reads the rows of such a group twice.
+// Units of eight heads; groups of more than eight in units of sixteen, whose
+// rows are then read, and in fp32 split, once.  bf16, 16 x 16384 slots, 12 heads
+// a group: 117 us (83 % of the copy rate, with two warps a scheduler); their
+// heads dealt to several warps 161 us where this took 145.  fp32, 8 x 16384, 12
+// heads a group: d 64 93 us (61 %), 123 in units of eight; d 128 206 us (56 %),
+// 239; but only where there are some four tiles a CTA, since units of eight are
+// twice as many to share out (14 x 86 slots, 4 key heads, d 128: 20 us, 15.6 in
+// units of eight).  fp32 queries of 128 are read again for every step (F32's
+// QREG; 8 x 16384, 4 heads a group: 134 us, 138 held in registers, some of them
+// spilled), those of 64 held (70.5 against 71.6).
 cudaError_t launch(DecodeArgs& a, int dtype, int d, cudaStream_t st) {
-  if (dtype != NATS_BF16) return d == 128 ? launch<F32<128>, 1, 2>(a, st) : launch<F32<64>, 1, 3>(a, st);
+  if (dtype != NATS_BF16) {
+    const long long tiles = (long long)a.pg.B * a.pg.Hk * ((a.pg.cap() + kTile - 1) / kTile);
+    if (a.G > 8 && tiles >= 8 * kSMs)
+      return d == 128 ? launch<F32<128, false>, 2, 2>(a, st) : launch<F32<64, true>, 2, 2>(a, st);
+    return d == 128 ? launch<F32<128, false>, 1, 2>(a, st) : launch<F32<64, true>, 1, 3>(a, st);
+  }
   if (a.G > 8) return d == 128 ? launch<Bf16<128>, 2, 2>(a, st) : launch<Bf16<64>, 2, 3>(a, st);
   return d == 128 ? launch<Bf16<128>, 1, 3>(a, st) : launch<Bf16<64>, 1, 4>(a, st);
 }

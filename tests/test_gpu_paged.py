@@ -100,6 +100,14 @@ def test_decode(nats, lens, Hk, G, d, page, dtype, accumulate):
         assert torch.equal(got[tol == 0], want[tol == 0])
 
 
+# groups of more than eight fp32 heads in tables of many tiles: units of sixteen
+@pytest.mark.parametrize("Hk,G,d", [(2, 12, 64), (2, 12, 128), (1, 16, 128), (1, 35, 64), (3, 9, 128)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_decode_wide_groups_of_many_sequences(nats, Hk, G, d, accumulate):
+    lens = [1024, 0, 1000, 64, 65, 1] + [(7 * i) % 200 for i in range(94)]
+    test_decode(nats, lens, Hk, G, d, 64, F32, accumulate)
+
+
 def test_decode_strided_query_scale_and_out(nats):
     rng = torch.Generator().manual_seed(1)
     lens = [70, 5, 130]
