@@ -248,13 +248,20 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
 // slots for each block y, the same entries that it holds of head g's q.  V: it
 // holds entries 8 g .. + 7 (and 64 + 8 g .. + 7) of slots 2c, 2c + 1, 2c + 8,
 // 2c + 9; pairs of slots are packed with byte permutes.  P moves from S^T's
-// layout to P^T's by an 8 x 8 transpose and is carried as two bf16, high and
-// low part, so that its rounding (2^-8 each) does not add to the output's own.
+// layout to P^T's by an 8 x 8 transpose and is carried as three bf16 parts, all
+// of its fp32.  The instruction cuts its sums off where fp32 additions round, so
+// a run of kRun steps' sums at most stands in its accumulators; they are then
+// added to the unit's in shared memory, each lane its own.  4 x 131072 slots, 4
+// heads a group: 0.06 % of the outputs are not the rounded exact value, with two
+// parts and one run 0.32 % (as fast: 290 us); fresh accumulators for every step
+// the same 0.06 %, 312 us.  Groups of 12, 16 x 16384 slots: 68.6 us, 64.5 with two.
 template <int D>
 struct Bf16 {
   using T = __nv_bfloat16;
   static constexpr int kD = D;
   static constexpr int KB = D / 32, VS = D / 64, MT = D / 16;
+  static constexpr int kParts = 3;  // of a weight
+  static constexpr int kRun = 16;   // steps that share the instruction's accumulators
   struct Q { uint4 r[KB]; };
   struct K { uint4 r[2][KB]; };
   struct V { uint4 r[4][VS]; };
@@ -302,15 +309,18 @@ struct Bf16 {
   }
   template <int NH>
   static __device__ __forceinline__ void values(float (&o)[NH][MT][4], const V& v, const float (&p)[NH][4], int, int) {
-    uint32_t ph[NH][2], pl[NH][2];
+    uint32_t ph[kParts][NH][2];
 #pragma unroll
     for (int x = 0; x < NH; ++x)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t w = pack(p[x][2 * i], p[x][2 * i + 1]);
-        ph[x][i] = transpose8(w);
-        pl[x][i] = transpose8(pack(p[x][2 * i] - __uint_as_float(w << 16),
-                                   p[x][2 * i + 1] - __uint_as_float(w & 0xffff0000u)));
+        float a = p[x][2 * i], b = p[x][2 * i + 1];
+#pragma unroll
+        for (int z = 0; z < kParts; ++z) {
+          const uint32_t w = pack(a, b);
+          ph[z][x][i] = transpose8(w);
+          a -= __uint_as_float(w << 16), b -= __uint_as_float(w & 0xffff0000u);
+        }
       }
 #pragma unroll
     for (int y = 0; y < MT; ++y) {
@@ -323,8 +333,8 @@ struct Bf16 {
       const uint32_t a0 = pair(0, y, 0), a1 = pair(0, yb, sb), a2 = pair(2, y, 0), a3 = pair(2, yb, sb);
 #pragma unroll
       for (int x = 0; x < NH; ++x) {
-        mma(o[x][y], a0, a1, a2, a3, ph[x][0], ph[x][1]);
-        mma(o[x][y], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+#pragma unroll
+        for (int z = kParts - 1; z >= 0; --z) mma(o[x][y], a0, a1, a2, a3, ph[z][x][0], ph[z][x][1]);
       }
     }
   }
@@ -346,6 +356,7 @@ struct F32 {
   using T = float;
   static constexpr int kD = D;
   static constexpr int KB = D / 16, VS = D / 32, MT = D / 16;
+  static constexpr int kRun = 0;  // (values adds outside the instruction)
   struct Q { float4 r[QREG ? KB : 1]; const T* p; };  // QREG: held in r, else read at p for every step (L1)
   struct K { uint4 r[2][KB]; };
   struct V { uint4 r[4][VS]; };
@@ -507,10 +518,11 @@ struct Unit {
 
   // The raw scores s of 16 slots become their weights; lo, hi: whether slots g
   // and g + 8 count (all: every slot does).  at: where the slots' scores go
-  // (accumulation), slot 0's first head, of `left` slots.
+  // (accumulation), slot 0's first head, of `left` slots.  so: where earlier
+  // runs' values lie, if there were any.
   template <bool ACC>
   __device__ __forceinline__ void weigh(float (&s)[NH][4], float scale2, bool all, bool lo, bool hi, float* at, int G,
-                                        int left, int heads, int g, int c) {
+                                        int left, int heads, float* so, bool earlier, int g, int c) {
     if (!all) {
 #pragma unroll
       for (int x = 0; x < NH; ++x)
@@ -544,6 +556,10 @@ struct Unit {
           sum[x][i] *= f;
 #pragma unroll
           for (int y = 0; y < MT; ++y) o[x][y][i] *= f, o[x][y][i + 2] *= f;
+          if (X::kRun > 0 && earlier) {
+#pragma unroll
+            for (int y = 0; y < MT; ++y) so[at_so(x, i, y, 0, g, c)] *= f, so[at_so(x, i, y, 1, g, c)] *= f;
+          }
         }
     }
 #pragma unroll
@@ -552,12 +568,43 @@ struct Unit {
       for (int i = 0; i < 4; ++i) {
         // the scaled score is not rounded before the maximum is subtracted
         s[x][i] = pow2(fmaf(s[x][i], scale2, -mx[x][i & 1]));
-        sum[x][i & 1] += s[x][i];
       }
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sum[x][i] += s[x][i] + s[x][i + 2];
   }
 
-  // to shared memory, so [8 NH][pitch], sml [8 NH][2] of this warp
-  __device__ __forceinline__ void put(float* so, float* sml, int g, int c) {
+  // where o[x][y][i] (upper: o[x][y][i + 2]) stands in this warp's so [8 NH][pitch]
+  static __device__ __forceinline__ int at_so(int x, int i, int y, int upper, int g, int c) {
+    return (8 * x + 2 * c + i) * kPitch<X::kD> + X::place(X::entry(y, g, upper));
+  }
+  // the values to shared memory, to what earlier runs left there if there were any
+  __device__ __forceinline__ void put_values(float* so, bool earlier, int g, int c) {
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          float *lo = so + at_so(x, i, y, 0, g, c), *hi = so + at_so(x, i, y, 1, g, c);
+          *lo = earlier ? *lo + o[x][y][i] : o[x][y][i];
+          *hi = earlier ? *hi + o[x][y][i + 2] : o[x][y][i + 2];
+        }
+  }
+  // A run's values added up (each lane its own entries), for the next run to begin at zero.
+  __device__ __forceinline__ void end_run(float* so, bool earlier, int g, int c) {
+    put_values(so, earlier, g, c);
+#pragma unroll
+    for (int x = 0; x < NH; ++x)
+#pragma unroll
+      for (int y = 0; y < MT; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[x][y][i] = 0.f;
+  }
+
+  // the unit's result to shared memory, so and sml [8 NH][2] of this warp
+  __device__ __forceinline__ void put(float* so, float* sml, bool earlier, int g, int c) {
 #pragma unroll
     for (int x = 0; x < NH; ++x)
 #pragma unroll
@@ -566,13 +613,8 @@ struct Unit {
         for (int z = 4; z < 32; z <<= 1) sum[x][i] += __shfl_xor_sync(0xffffffffu, sum[x][i], z);
         const int h = 8 * x + 2 * c + i;
         if (g == 0) sml[h * 2] = mx[x][i], sml[h * 2 + 1] = sum[x][i];
-        float* at = so + h * kPitch<X::kD>;
-#pragma unroll
-        for (int y = 0; y < MT; ++y) {
-          at[X::place(X::entry(y, g, 0))] = o[x][y][i];
-          at[X::place(X::entry(y, g, 1))] = o[x][y][i + 2];
-        }
       }
+    put_values(so, earlier, g, c);
   }
 };
 
@@ -662,6 +704,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
     typename X::K k;
     typename X::V v;
     int row = first_row(0), next = first_row(1);
+    float *mine = so + warp * GT * kPitch<D>, *mine_ml = sml + warp * GT * 2;
+    bool earlier = false;  // runs that have ended
     load_k<X>(k, kp, row, g, c);
     load_v<X>(v, vp, row, n - slot0, g, c);
     for (int st = 0; st < steps; ++st) {
@@ -671,15 +715,15 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       load_k<X>(k, kp, next, g, c);
       float* at = ACC ? a.scores + (((long long)mb * a.pg.Hk + hk) * a.pg.cap() + j0) * a.G + g0 : nullptr;
       unit.template weigh<ACC>(s, a.scale2, row >= 0 && j0 + 16 <= n, row >= 0 && j0 + g < n, row >= 0 && j0 + g + 8 < n,
-                               at, a.G, n - j0, heads, g, c);
+                               at, a.G, n - j0, heads, mine, earlier, g, c);
       X::values(unit.o, v, s, g, c);
       load_v<X>(v, vp, next, n - j0 - stride, g, c);
       row = next;
       next = after;
+      if (X::kRun > 0 && (st + 1) % max(X::kRun, 1) == 0) unit.end_run(mine, earlier, g, c), earlier = true;
     }
     if (bad && lane == 0) *a.pg.err = 1;
-    float *mine = so + warp * GT * kPitch<D>, *mine_ml = sml + warp * GT * 2;
-    unit.put(mine, mine_ml, g, c);
+    unit.put(mine, mine_ml, earlier, g, c);
     if (alone) {
       __syncwarp();
       finish_unit<X, GT, 1>(a, mine, mine_ml, mb, h0, heads, -1, lane);

@@ -1,0 +1,123 @@
+"""The paged decode's arithmetic where an ordinary error bound would hide a loss:
+scores that the products form exactly, so that what is left are the softmax's
+own roundings, against 64 bits."""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24  # half a step of fp32, relative
+
+
+@pytest.fixture(scope="module")
+def nats():
+    from linear_attention_nats_gb300 import build
+
+    build.build()
+    import linear_attention_nats_gb300 as n
+
+    return n
+
+
+def _shared(nats, k, v, B, n, page, weight=None):
+    """B sequences over the same pages, which hold k, v [Hk, n, d] in order."""
+    pages = lambda x: x.unflatten(1, (-1, page)).transpose(0, 1).contiguous()
+    table = torch.arange(k.shape[1] // page, dtype=torch.int32).repeat(B, 1)
+    return nats.PagedCache(pages(k).cuda(), pages(v).cuda(), table.cuda(),
+                           torch.full((B,), n, dtype=torch.int32).cuda(), weight=weight)
+
+
+def _settled(x, e):
+    """Entries whose rounding to bf16 an error of e cannot change: those further than e from a border between two."""
+    lo, hi = (x - e).to(F32).to(BF), (x + e).to(F32).to(BF)
+    return lo == hi
+
+
+# A weight 2^x, x = scale log2 e s - maximum with |x| <= 6: log2 e as fp32 (U of x), the sum's rounding (U of x) and the
+# exponential's 2^-22: (12 ln 2 + 4) U < 13 U.  What the sums of weights and values add is stated where it is used.
+WEIGHT = 13 * U
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bf16_output_of_two_slots_is_the_rounded_value(nats, d):
+    """Two slots with weights 1 and p: out = (v1 + p v2) / (1 + p) with p to nearly all of its fp32, v2 through every
+    significand.  Above the weights' own error: the products and sums of a step (6 steps cut off at 2^-23, of the
+    weighted magnitudes), the sum's three additions, the quotient and the product: 18 U."""
+    B = 1500
+    rng = torch.Generator().manual_seed(1)
+    q = torch.zeros(B, 1, d)
+    q[:, 0, 0] = (torch.rand(B, generator=rng) + 0.5).to(BF).float()
+    k = torch.zeros(1, 16 * B, d)
+    k[0, 1::16, 0] = -4 * torch.rand(B, generator=rng).to(BF).float()
+    v = torch.zeros(1, 16 * B, d)
+    v[0, 1::16] = (1 + torch.randint(0, 128, (B, d), generator=rng) / 128.0)
+    pages = lambda x: x.unflatten(1, (-1, 16)).transpose(0, 1).contiguous().to(BF).cuda()
+    c = nats.PagedCache(pages(k), pages(v), torch.arange(B, dtype=torch.int32)[:, None].cuda(),
+                        torch.full((B,), 2, dtype=torch.int32).cuda())
+    out = nats.paged_decode(c, q.to(BF).cuda(), scale=1.0).cpu()[:, 0]
+    p = torch.exp(q[:, 0, 0].double() * k[0, 1::16, 0].to(BF).double())[:, None]
+    v2 = v[0, 1::16].double()
+    e = p * v2 / (1 + p)
+    bound = WEIGHT * p * (v2 - e) / (1 + p) + 18 * U * e
+    sure = _settled(e, bound)
+    assert sure.double().mean() > 0.99
+    assert torch.equal(out[sure], e.to(BF)[sure])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bf16_output_of_many_steps_of_one_cta_is_the_rounded_value(nats, d):
+    """A unit that one CTA takes from end to end, 65,536 slots, with weights and values of one sign, so that errors that
+    lean one way would add up.  A lane's sum takes 1024 rounded additions and the values' 64 between their runs of 16
+    steps: errors of either sign, taken as independent (Higham and Mary, 2019: lambda sqrt(n) U, lambda = 6), 6 (32 + 8)
+    U.  Within a run three products a step are cut off at 2^-23 of a sum that grows to the run's own: 48 x 2^-23 at
+    most.  Joins, quotient and product: 20 U."""
+    n, page, B = 65536, 64, 152 * (4 if d == 64 else 3)
+    rng = torch.Generator().manual_seed(2)
+    k = torch.zeros(1, n, d)
+    k[0, :, 0] = -torch.rand(n, generator=rng)
+    share = torch.linspace(0.02, 0.98, d)
+    v = torch.where(torch.rand(n, d, generator=rng) < share, 1.0, 2 - 2.0 ** -7)[None]
+    q = torch.zeros(B, 1, d)
+    q[:, 0, 0] = 0.5 + torch.rand(B, generator=rng)
+    k, v, q = k.to(BF), v.to(BF), q.to(BF)
+    out = nats.paged_decode(_shared(nats, k, v, B, n, page), q.cuda(), scale=1.0).cpu()[:, 0]
+    p = torch.softmax((q[:, 0, :1].double().cuda() @ k[0, :, :1].double().cuda().T), -1)
+    e = (p @ v[0].double().cuda()).cpu()
+    bound = (WEIGHT * 0.5 + (6 * 40 + 48 * 2 + 20) * U) * e  # (values within half of e of it)
+    sure = _settled(e, bound)
+    assert sure.double().mean() > 0.95
+    assert torch.equal(out[sure], e.to(BF)[sure])
+
+
+@pytest.mark.parametrize("G,d", [(1, 64), (1, 128), (12, 64), (12, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_maximum_that_rises_through_a_long_run(nats, G, d, dtype):
+    """Scores that rise by some 90 powers of two over a CTA's run, now slowly, now in jumps, so that the sums of all
+    earlier steps are rescaled again and again; heads of one group rise at different places."""
+    n, page, B = 8192, 64, 640
+    rng = torch.Generator().manual_seed(3)
+    k = torch.zeros(1, n, d)
+    k[0, :, 0] = torch.linspace(-60, 0, n)
+    k[0, :, 1] = torch.where(torch.arange(n) < 5000, -40.0, 0.0)
+    k[0, :, 2] = -50.0 * torch.rand(n, generator=rng) * (torch.arange(n) % 700 != 1)
+    v = torch.randn(1, n, d, generator=rng)
+    q = torch.zeros(B, G, d)
+    for h in range(G):
+        q[:, h, h % 3] = 1.0
+    q[:, :, 3] = torch.randn(B, 1, generator=rng)
+    k[0, :, 3] = torch.randn(n, generator=rng)
+    k, v, q = k.to(dtype), v.to(dtype), q.to(dtype)
+    out = nats.paged_decode(_shared(nats, k, v, B, n, page), q.cuda(), scale=1.0).cpu().double()
+    qd, kd, vd = q.double().cuda(), k[0].double().cuda(), v[0].double().cuda()
+    s = qd @ kd.T
+    p = torch.softmax(s, -1)
+    e, mag = (p @ vd).cpu(), (p @ vd.abs()).cpu()
+    # a score: four products and their sum, each off by 2^-23 of |q| |k| <= 70, and its scaling: 8 x 2^-23 x 70; the
+    # weights that count lie within 20 of the maximum; sums as above, all steps' signs alike: (4 x 128 / 4 + 64) 2^-23
+    rel = 2 * (8 * 70 * 2.0 ** -23 + 20 * 2 * U + 4 * U) + (128 + 64) * 2.0 ** -23
+    half = 2.0 ** -8 if dtype == BF else U
+    assert ((out - e).abs() <= half * (e.abs() + rel * mag) + rel * mag).all()
