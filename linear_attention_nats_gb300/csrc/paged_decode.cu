@@ -630,10 +630,10 @@ __device__ __forceinline__ void add_one_tile(const DecodeArgs& a, int b, int hk,
     float* at = a.weight + a.pg.row(pg, hk, j % a.pg.page);
     const float* x = a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G;
     const float* lse = a.lse_ws + (long long)b * a.Hq + hk * a.G;
-    float w = *at;
+    float w = 0.f;  // the group's sum, added once: of a heavy slot's weight, each head's part alone may be below half a step
 #pragma unroll 4
     for (int g = 0; g < a.G; ++g) w += x[g] == -INFINITY ? 0.f : pow2(x[g] - lse[g]);
-    *at = w;
+    *at += w;
   }
 }
 // (a group of more heads than a unit's is summed over its units: add_weights)
@@ -897,14 +897,15 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
     __syncthreads();
     const float* scores = a.scores + ((long long)b * Hk + hk) * a.pg.cap() * G;
     for (; j < end; j += kSlots * kThreads) {
-      float w[kSlots];
+      float w[kSlots], was[kSlots];  // the group's sum, added once to the stored weight
       const float* x[kSlots];
       float* at[kSlots];
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         const int ji = j + i * kThreads;
         at[i] = pg[i] < 0 ? nullptr : a.weight + a.pg.row(pg[i], hk, ji % a.pg.page);
-        w[i] = at[i] ? *at[i] : 0.f;
+        was[i] = at[i] ? *at[i] : 0.f;
+        w[i] = 0.f;
         x[i] = scores + (long long)min(ji, end - 1) * G;
       }
       pages(j + kSlots * kThreads);
@@ -928,7 +929,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       }
 #pragma unroll
       for (int i = 0; i < kSlots; ++i)
-        if (at[i]) *at[i] = w[i];
+        if (at[i]) *at[i] = was[i] + w[i];
     }
     __syncthreads();
     cur += t1 - t0;

@@ -121,3 +121,21 @@ def test_maximum_that_rises_through_a_long_run(nats, G, d, dtype):
     rel = 2 * (8 * 70 * 2.0 ** -23 + 20 * 2 * U + 4 * U) + (128 + 64) * 2.0 ** -23
     half = 2.0 ** -8 if dtype == BF else U
     assert ((out - e).abs() <= half * (e.abs() + rel * mag) + rel * mag).all()
+
+
+@pytest.mark.parametrize("n,w0", [(64, 2.0 ** 20), (4096, 2.0 ** 14), (50, 3e5), (4000, 1000.0)])
+@pytest.mark.parametrize("G,dtype", [(8, BF), (8, F32), (24, BF)])
+def test_weights_of_heavy_slots_grow_by_the_groups_sum(nats, n, w0, G, dtype):
+    """Equal scores: each head gives every slot 1 / n, which of a heavy slot's weight is less than half a step, the
+    group's G / n is not.  One rounding a call (U of the weight), and the group's own sum: G + 8 roundings."""
+    calls, page, d = 64, 16, 64
+    N = -(-n // page) * page
+    weight = torch.full((N // page, 1, page), w0, device="cuda")
+    c = _shared(nats, torch.zeros(1, N, d, dtype=dtype), torch.ones(1, N, d, dtype=dtype), 1, n, page, weight)
+    q = torch.zeros(1, G, d, dtype=dtype, device="cuda")
+    for _ in range(calls):
+        nats.paged_decode(c, q, accumulate=True)
+    got = c.weight.cpu().double().reshape(-1)
+    want = w0 + calls * G / n
+    assert ((got[:n] - want).abs() <= calls * (U * want * (1 + U) + (G + 8) * U * G / n)).all()
+    assert (got[n:] == w0).all()
