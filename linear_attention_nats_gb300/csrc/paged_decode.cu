@@ -45,10 +45,10 @@ struct DecodeArgs {
   int Hq, G, GT, ngroups;  // heads of a group, of a unit, units of a group
   float scale2;            // scale log2 e
   long long* prefix;       // [B + 2] tiles before each sequence, all, and the CTAs that share them
-  float* lse_ws;           // [B, Hq]
-  float* part_ml;          // [2 ctas, GT, 2]
+  float2* ml_ws;           // [B, Hq] maximum and 1 / sum of the units of one CTA
+  float* part_ml;          // [2 ctas, GT, 2] maximum and sum
   float* part_o;           // [2 ctas, GT, D]
-  float* scores;           // [B, Hk, cap, G] or NULL
+  float* scores;           // [B, Hk, cap, G] or NULL: q . k, not yet scaled
   float* weight;
 };
 
@@ -180,6 +180,11 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float
 constexpr float kNoMax = -1e38f;
 // the factor that brings sums taken at maximum m to maximum M >= m
 __device__ __forceinline__ float part_scale(float m, float M) { return pow2(m - M); }
+__device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : M + log2f(l); }
+// 2^(scaled score - maximum m) of the raw score s.  The scaled score is not
+// rounded before the maximum is subtracted; the maximum is a rounded one, but the
+// same for a sum and all that is divided by it, so that its rounding cancels.
+__device__ __forceinline__ float weight_of(float s, float scale2, float m) { return pow2(fmaf(s, scale2, -m)); }
 
 // Where entry e of a row stands in shared memory: rows padded to D + 4, and
 // within a row such that the lanes that hold neighbouring entry tiles (X::place)
@@ -212,9 +217,8 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const float* so
       T* out = (T*)a.out + ((long long)b * a.Hq + h0 + g) * D + e;
       store4(out, o[0] * r, o[1] * r, o[2] * r, o[3] * r);
       if (e == 0) {
-        const float v = l == 0.f ? -INFINITY : M + log2f(l);
-        a.lse_ws[(long long)b * a.Hq + h0 + g] = v;
-        if (a.lse) a.lse[(long long)b * a.Hq + h0 + g] = v;
+        a.ml_ws[(long long)b * a.Hq + h0 + g] = make_float2(M, r);
+        if (a.lse) a.lse[(long long)b * a.Hq + h0 + g] = lse_of(M, l);
       }
     } else {
       *(float4*)(a.part_o + (slot * GT + g) * D + e) = make_float4(o[0], o[1], o[2], o[3]);
@@ -536,7 +540,7 @@ struct Unit {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = g + 8 * (i >> 1), h = 8 * x + 2 * c + (i & 1);
-          if (j < left && h < heads) at[(long long)j * G + h] = s[x][i] * scale2;
+          if (j < left && h < heads) at[(long long)j * G + h] = s[x][i];
         }
       }
       rises |= fmaxf(s[x][0], s[x][2]) > rise[x][0] || fmaxf(s[x][1], s[x][3]) > rise[x][1];
@@ -565,10 +569,7 @@ struct Unit {
 #pragma unroll
     for (int x = 0; x < NH; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // the scaled score is not rounded before the maximum is subtracted
-        s[x][i] = pow2(fmaf(s[x][i], scale2, -mx[x][i & 1]));
-      }
+      for (int i = 0; i < 4; ++i) s[x][i] = weight_of(s[x][i], scale2, mx[x][i & 1]);
 #pragma unroll
     for (int x = 0; x < NH; ++x)
 #pragma unroll
@@ -619,8 +620,8 @@ struct Unit {
 };
 
 // The weights of a key head's one tile, whose scores and sums the calling threads
-// have just written: weight[slot] += sum over the group's heads of 2^(score -
-// lse), thread t of `threads` a slot after the other, as add_weights does for
+// have just written: weight[slot] += sum over the group's heads of p = 2^(score -
+// maximum) / sum, thread t of `threads` a slot after the other, as add_weights does for
 // longer ones.  175 sequences of up to 38 slots, 16 heads: 22.5 us, 27 with
 // these tiles in add_weights too.
 __device__ __forceinline__ void add_one_tile(const DecodeArgs& a, int b, int hk, int n, int t, int threads) {
@@ -629,10 +630,10 @@ __device__ __forceinline__ void add_one_tile(const DecodeArgs& a, int b, int hk,
     if (pg < 0) continue;
     float* at = a.weight + a.pg.row(pg, hk, j % a.pg.page);
     const float* x = a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G;
-    const float* lse = a.lse_ws + (long long)b * a.Hq + hk * a.G;
+    const float2* ml = a.ml_ws + (long long)b * a.Hq + hk * a.G;
     float w = 0.f;  // the group's sum, added once: of a heavy slot's weight, each head's part alone may be below half a step
 #pragma unroll 4
-    for (int g = 0; g < a.G; ++g) w += x[g] == -INFINITY ? 0.f : pow2(x[g] - lse[g]);
+    for (int g = 0; g < a.G; ++g) w = fmaf(weight_of(x[g], a.scale2, ml[g].x), ml[g].y, w);
     *at += w;
   }
 }
@@ -781,7 +782,6 @@ __device__ __forceinline__ void join_sums(const DecodeArgs& a, const Parts& p, i
   l = warp_sum(l * part_scale(M, m));
   M = m;
 }
-__device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : M + log2f(l); }
 
 // Row i = (sequence, query head): joins the unit's partials, or writes the row
 // of an empty sequence.  W warps share the partials: one where there are rows
@@ -832,11 +832,11 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, long long i) {
 }
 
 // Part `idx` of `count` of the tile line: weight[slot] += sum over the group's
-// heads of 2^(score - lse), the lse from the partials again (so this need not
-// wait for the joined rows).  A thread a slot: nothing is summed in an order
+// heads of p = 2^(score - maximum) / sum, these two from the partials again (so
+// this need not wait for the joined rows).  A thread a slot: nothing is summed in an order
 // that varies.
 __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int count) {
-  extern __shared__ float lse[];  // [G]
+  extern __shared__ float2 ml_of[];  // [G] maximum and 1 / sum
   __shared__ int found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hk = a.pg.Hk, G = a.G;
   const long long total = a.prefix[a.pg.B], T = total * Hk;
@@ -879,7 +879,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       const Parts p = g < a.GT ? p0 : parts_of(pre, nt, total, hk * a.ngroups + g / a.GT, Hk * a.ngroups, ctas);
       float M = kNoMax, l = 0.f;
       if (p.one) {
-        lse[g] = a.lse_ws[(long long)b * a.Hq + hk * G + g];
+        ml_of[g] = a.ml_ws[(long long)b * a.Hq + hk * G + g];
       } else if (few) {
 #pragma unroll 4
         for (int c = p.c0; c <= p.c1; ++c) {
@@ -888,10 +888,10 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
           l = l * part_scale(M, m) + ml.y * part_scale(ml.x, m);
           M = m;
         }
-        lse[g] = lse_of(M, l);
+        ml_of[g] = make_float2(M, l == 0.f ? 0.f : 1.f / l);
       } else {
         join_sums(a, p, g % a.GT, M, l);
-        if (lane == 0) lse[g] = lse_of(M, l);
+        if (lane == 0) ml_of[g] = make_float2(M, l == 0.f ? 0.f : 1.f / l);
       }
     }
     __syncthreads();
@@ -909,22 +909,25 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
         x[i] = scores + (long long)min(ji, end - 1) * G;
       }
       pages(j + kSlots * kThreads);
-      auto add = [&](int i, float v, int g) { w[i] += v == -INFINITY ? 0.f : pow2(v - lse[g]); };
+      auto add = [&](int i, float v, float2 ml) { w[i] = fmaf(weight_of(v, a.scale2, ml.x), ml.y, w[i]); };
       if (G % 4 == 0) {
+#pragma unroll 1
         for (int g = 0; g < G; g += 4) {
           float4 v[kSlots];
 #pragma unroll
           for (int i = 0; i < kSlots; ++i) v[i] = __ldg((const float4*)(x[i] + g));
 #pragma unroll
-          for (int i = 0; i < kSlots; ++i) add(i, v[i].x, g), add(i, v[i].y, g + 1), add(i, v[i].z, g + 2), add(i, v[i].w, g + 3);
+          for (int i = 0; i < kSlots; ++i)
+            add(i, v[i].x, ml_of[g]), add(i, v[i].y, ml_of[g + 1]), add(i, v[i].z, ml_of[g + 2]), add(i, v[i].w, ml_of[g + 3]);
         }
       } else {
+#pragma unroll 2
         for (int g = 0; g < G; ++g) {
           float v[kSlots];
 #pragma unroll
           for (int i = 0; i < kSlots; ++i) v[i] = __ldg(x[i] + g);
 #pragma unroll
-          for (int i = 0; i < kSlots; ++i) add(i, v[i], g);
+          for (int i = 0; i < kSlots; ++i) add(i, v[i], ml_of[g]);
         }
       }
 #pragma unroll
@@ -937,9 +940,10 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
 }
 
 // The first CTAs join; the others (accumulation) add the weights of units of
-// more than one tile.
+// more than one tile.  Eight CTAs an SM, all of a launch's: 4 x 131072 slots 290
+// us, 296 with seven.
 template <typename T, int D, int W>
-__global__ void __launch_bounds__(kThreads) decode_finish_kernel(DecodeArgs a, int join_ctas) {
+__global__ void __launch_bounds__(kThreads, 8) decode_finish_kernel(DecodeArgs a, int join_ctas) {
   begin();
   if ((int)blockIdx.x < join_ctas) {
     const long long i = W > 1 ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -961,7 +965,7 @@ size_t layout(const nats_paged_cache* c, int Hq, bool accumulate, char* base, De
   };
   DecodeArgs d = {};
   d.prefix = (long long*)take(8 * ((size_t)c->B + 2));
-  d.lse_ws = (float*)take(4 * (size_t)c->B * Hq);
+  d.ml_ws = (float2*)take(8 * (size_t)c->B * Hq);
   d.part_ml = (float*)take(4 * 2 * (size_t)kMaxCtas * kMaxHeads * 2);
   d.part_o = (float*)take(4 * 2 * (size_t)kMaxCtas * kMaxHeads * c->d);
   d.scores = accumulate ? (float*)take(4 * (size_t)c->B * Hq * c->max_pages * c->page) : nullptr;
@@ -973,7 +977,7 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
   const nats_status s = check_cache(c);
   if (s != NATS_OK) return s;
   if (Hq < 0 || Hq % c->Hk != 0) return NATS_ERR_SHAPE;
-  // a group's lse fit shared memory
+  // a group's maxima and sums fit shared memory
   if (Hq / c->Hk > 4096) return NATS_ERR_UNSUPPORTED;
   // rows of a pool and of the batch's queries are 32-bit
   if ((long long)c->B * Hq > (1LL << 31) - 1 || (double)c->n_pages * c->Hk * c->page > 2147483647.0)
@@ -1000,7 +1004,7 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
   const bool few = rows <= kSMs * 16;
   const int join = (int)(few ? rows : (rows + kWarps - 1) / kWarps);
   const unsigned grid = join + (acc ? kSMs * 8 : 0);
-  const size_t smem = acc ? 4 * (size_t)a.G : 0;
+  const size_t smem = acc ? sizeof(float2) * (size_t)a.G : 0;
   return few ? after(decode_finish_kernel<T, D, kWarps>, grid, kThreads, smem, st, 0, a, join)
              : after(decode_finish_kernel<T, D, 1>, grid, kThreads, smem, st, 0, a, join);
 }

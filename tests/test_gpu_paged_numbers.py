@@ -139,3 +139,26 @@ def test_weights_of_heavy_slots_grow_by_the_groups_sum(nats, n, w0, G, dtype):
     want = w0 + calls * G / n
     assert ((got[:n] - want).abs() <= calls * (U * want * (1 + U) + (G + 8) * U * G / n)).all()
     assert (got[n:] == w0).all()
+
+
+@pytest.mark.parametrize("n", [50, 1000, 9000])
+@pytest.mark.parametrize("G,dtype", [(1, BF), (4, F32), (9, BF), (9, F32)])
+def test_weights_of_large_scores(nats, n, G, dtype):
+    """Scores of about 4096 (5909 in powers of two, where fp32 has steps of 2^-11) that lie close together and that the
+    products form exactly: the weights go by their distances.  A weight is off by WEIGHT where its distance counts
+    (|x| <= 12 doubles it), its sum by 64 + n / 4 roundings of positive numbers, its quotient by 2 U, the group's sum by
+    G U, and the stored one by its own rounding."""
+    page, d = 16, 64
+    N = -(-n // page) * page
+    rng = torch.Generator().manual_seed(5)
+    k = torch.zeros(1, N, d)
+    k[0, :, 0] = 4096
+    k[0, :, 1] = -torch.randint(0, 65, (N,), generator=rng) / 8.0
+    q = torch.zeros(1, G, d)
+    q[:, :, :2] = 1
+    c = _shared(nats, k.to(dtype), torch.randn(1, N, d, generator=rng).to(dtype), 1, n, page,
+                torch.zeros(N // page, 1, page, device="cuda"))
+    nats.paged_decode(c, q.to(dtype).cuda(), scale=1.0, accumulate=True)
+    want = G * torch.softmax((k[0, :n, 0] + k[0, :n, 1]).double(), -1)
+    got = c.weight.cpu().double().reshape(-1)[:n]
+    assert ((got - want).abs() <= (4 * WEIGHT + (64 + n / 4 + 2 + G + 1) * U) * want).all()
