@@ -29,6 +29,18 @@ def _field(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+def _kept(i, name):
+    """One of the cache's tensors: it may be changed in place (also by +=), not put in another's place."""
+    def get(self):
+        return self._t[i]
+
+    def put(self, t):
+        if t is not self._t[i]:
+            raise AttributeError(f"a cache keeps the {name} that it was made with; change it in place ({name}.copy_)")
+
+    return property(get, put)
+
+
 class PagedCache:
     """A pool of pages shared by B sequences (nats_paged_cache): k_pages,
     v_pages [n_pages, Hk, page, d] bf16 or fp32; table int32 [B, max_pages],
@@ -62,12 +74,8 @@ class PagedCache:
             _field(lens, "lens", torch.int32, (B,), dev), err.data_ptr(), n, page, Hk, d, B, most, _CODES[k_pages.dtype])
         self._addr, self._dev = ctypes.addressof(self._c), dev.index
 
-    k_pages = property(lambda self: self._t[0])
-    v_pages = property(lambda self: self._t[1])
-    table = property(lambda self: self._t[2])
-    lens = property(lambda self: self._t[3])
-    weight = property(lambda self: self._t[4])
-    err = property(lambda self: self._t[5])
+    k_pages, v_pages, table, lens, weight, err = (
+        _kept(i, name) for i, name in enumerate(("k_pages", "v_pages", "table", "lens", "weight", "err")))
 
     @classmethod
     def empty(cls, n_pages: int, page: int, Hk: int, d: int, B: int, max_pages: int, *, dtype=torch.bfloat16,
