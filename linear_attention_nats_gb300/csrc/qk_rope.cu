@@ -41,11 +41,11 @@ constexpr int kWarps = 8;  // warps per CTA
 // f / (2 pi) in turns times 2^64, modulo 2^64, from the bits of the double f:
 // the 53-bit mantissa times 2^64 / (2 pi) rounded to an integer (62 bits),
 // shifted by the exponent.  Integer work only.  2^64 / (2 pi) =
-// 2935890503282001226.3...
+// 2935890503282001226.3...  An infinity or NaN has no turns: see turned_by.
 __device__ __forceinline__ uint64_t turns_fixed(double f) {
   const uint64_t bits = (uint64_t)__double_as_longlong(f);
   const int e = (int)(bits >> 52) & 0x7ff;
-  if (e == 0 || e == 0x7ff) return 0;  // below 2^-1022: no turn at any position; not a number: none either
+  if (e == 0 || e == 0x7ff) return 0;  // below 2^-1022: no turn at any position
   const uint64_t m = (bits & 0xfffffffffffffull) | (1ull << 52);
   constexpr uint64_t kInv2Pi = 2935890503282001226ull;
   const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
@@ -58,6 +58,17 @@ __device__ __forceinline__ uint64_t turns_fixed(double f) {
   else
     r = s >= 128 ? 0 : hi >> (s - 64);
   return (bits >> 63) ? 0 - r : r;
+}
+
+// Whether f is an infinity or NaN.
+__device__ __forceinline__ bool endless(double f) {
+  return (((uint64_t)__double_as_longlong(f) >> 52) & 0x7ff) == 0x7ff;
+}
+// cos and sin of position p's turns of the frequency F; NaN, as the formula's,
+// for one that is not finite (bad)
+__device__ __forceinline__ void turned_by(uint64_t F, long long p, bool bad, float* c, float* s) {
+  sincospif((float)(int32_t)((uint64_t)p * F >> 32) * 0x1p-31f, s, c);
+  if (bad) *s = *c = __int_as_float(0x7fffffff);
 }
 
 struct Operand {
@@ -140,19 +151,17 @@ __device__ __forceinline__ LaneMap lane_map(int l, int rot) {
 
 // cos and sin of the lane's four pairs at position p (1 and 0 where nothing
 // turns).  The 32 / LPR rows of a warp have the same pairs, so each of them
-// works out its share of the four (F: that share's frequencies) and the lanes
-// exchange them.
+// works out its share of the four (F: that share's frequencies, bad: a bit for
+// each that is not finite) and the lanes exchange them.
 template <int LPR>
-__device__ __forceinline__ void angles(const uint64_t* F, bool turned, long long p, int l, float* c, float* s) {
+__device__ __forceinline__ void angles(const uint64_t* F, unsigned bad, bool turned, long long p, int l, float* c,
+                                       float* s) {
   constexpr int N = 4 / (32 / LPR);
   float cm[N], sm[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     cm[i] = 1.f, sm[i] = 0.f;
-    if (turned) {
-      const uint64_t ph = (uint64_t)p * F[i];
-      sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &sm[i], &cm[i]);
-    }
+    if (turned) turned_by(F[i], p, bad >> i & 1, &cm[i], &sm[i]);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -160,26 +169,21 @@ __device__ __forceinline__ void angles(const uint64_t* F, bool turned, long long
     s[i] = __shfl_sync(0xffffffffu, sm[i % N], LPR * (i / N) + l);
   }
 }
-// the frequencies of the lane's share
-template <int LPR>
-__device__ __forceinline__ void lane_turns(const double* inv_freq, const LaneMap& m, int sub, uint64_t* F) {
-  constexpr int N = 4 / (32 / LPR);
-#pragma unroll
-  for (int i = 0; i < N; ++i) F[i] = m.turned ? turns_fixed(inv_freq[m.pair0 + sub * N + i]) : 0;
-}
 // How a warp's 32 / LPR groups of lanes share the work: rows of one token side
 // by side (angles above), or, where a token has few rows, a token each.
 template <int LPR, bool EACH>
 struct Share {
   static constexpr int kTokens = EACH ? 32 / LPR : 1;  // of a warp
   static constexpr int kRows = 32 / LPR / kTokens;     // of a token, side by side
-  uint64_t F[EACH ? 4 : LPR / 8];
+  static constexpr int kPairs = EACH ? 4 : LPR / 8;    // of the lane's four, whose frequencies it holds
+  uint64_t F[kPairs];
+  unsigned bad = 0;
   __device__ __forceinline__ Share(const double* inv_freq, const LaneMap& m, int sub) {
-    if constexpr (EACH) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) F[i] = m.turned ? turns_fixed(inv_freq[m.pair0 + i]) : 0;
-    } else {
-      lane_turns<LPR>(inv_freq, m, sub, F);
+    for (int i = 0; i < kPairs; ++i) {
+      const double f = m.turned ? inv_freq[m.pair0 + (EACH ? 0 : sub * kPairs) + i] : 0.0;
+      F[i] = turns_fixed(f);
+      bad |= (unsigned)endless(f) << i;
     }
   }
   __device__ __forceinline__ void at(bool turned, long long p, int l, float* c, float* s) const {
@@ -187,10 +191,10 @@ struct Share {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         c[i] = 1.f, s[i] = 0.f;
-        if (turned) sincospif((float)(int32_t)((uint64_t)p * F[i] >> 32) * 0x1p-31f, &s[i], &c[i]);
+        if (turned) turned_by(F[i], p, bad >> i & 1, &c[i], &s[i]);
       }
     } else {
-      angles<LPR>(F, turned, p, l, c, s);
+      angles<LPR>(F, bad, turned, p, l, c, s);
     }
   }
 };
