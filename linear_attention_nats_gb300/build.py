@@ -2,16 +2,20 @@
 of _operators.so, the operators' torch-facing binding, with g++.
 
 Each translation unit under csrc/ compiles in parallel to an object under
-_build/, then the two shared libraries are linked next to this file.
+_build/, then the two shared libraries are linked next to this file.  libnats.so
+needs neither torch nor Python: it is built also where the binding cannot be.
 """
 
 from __future__ import annotations
 
 import fcntl
 import glob
+import importlib.metadata
 import os
+import platform
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -21,6 +25,7 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnats.so")
 BINDING = os.path.join(PKG, "_operators.so")
+STAMP = os.path.join(BUILD, "binding.txt")  # what the binding was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -44,20 +49,46 @@ def _binding_source():
     return os.path.join(CSRC, "binding.cpp")
 
 
-def _deps():
-    return _sources() + [_binding_source()] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
+def _lib_deps():
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
         os.path.join(ROOT, "include", "nats.h"), os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _binding_deps():
+    return [_binding_source(), os.path.join(ROOT, "include", "nats.h"), os.path.abspath(__file__)]
+
+
+def _abi() -> str:
+    """What a built binding goes with: this Python and this torch."""
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch_version = "none"
+    return f"python {sys.version}, torch {torch_version}, {platform.machine()}"
+
+
+def _newer(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _lib_deps())
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer(BINDING, _binding_deps()) or not os.path.exists(STAMP):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    with open(STAMP) as f:
+        return f.read() == _abi()
+
+
+def up_to_date() -> bool:
+    return _lib_up_to_date() and _binding_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile libnats.so and _operators.so if any source changed; returns the first one's path.
+    """Compile libnats.so and _operators.so where a source, or for the second Python or torch, has changed; returns
+    the first one's path.  A failure of the second leaves the first one built.
 
     Serialised across processes with a file lock (several ranks may call it)."""
     if not force and up_to_date():
@@ -68,7 +99,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         try:
             if not force and up_to_date():
                 return LIB
-            return _build_locked(verbose, extra_flags)
+            return _build_locked(force, verbose, extra_flags)
         finally:
             fcntl.flock(lk, fcntl.LOCK_UN)
 
@@ -94,9 +125,11 @@ def _build_binding(verbose) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(STAMP, "w") as f:
+        f.write(_abi())
 
 
-def _build_locked(verbose, extra_flags) -> str:
+def _build_lib(ex, verbose, extra_flags) -> None:
     nvcc = _nvcc()
     srcs = _sources()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
@@ -113,20 +146,27 @@ def _build_locked(verbose, extra_flags) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(_build_binding, verbose)
-        list(ex.map(compile_one, zip(srcs, objs)))
-        binding.result()
+    list(ex.map(compile_one, zip(srcs, objs)))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def _build_locked(force, verbose, extra_flags) -> str:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(_sources()) + 1, os.cpu_count() or 4))) as ex:
+        binding = None if _binding_up_to_date() and not force else ex.submit(_build_binding, verbose)
+        if force or not _lib_up_to_date():
+            _build_lib(ex, verbose, extra_flags)
+        if binding is not None:
+            try:
+                binding.result()
+            except Exception as e:
+                raise RuntimeError(f"libnats.so is built, its torch binding is not: {e}") from e
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose=True))

@@ -21,3 +21,68 @@ def test_cache_tensors_change_in_place_only():
     with pytest.raises(AttributeError):
         c.lens = c.lens + 1
     assert c.lens.tolist() == [1, 1]
+
+
+# --------------------------------------------------------------- the build
+
+@pytest.fixture
+def sandbox(tmp_path, monkeypatch):
+    """The build with its files in a folder of their own and compilers that only write what they are told to; returns
+    (build, the commands run, the names of programs that fail)."""
+    import os
+    import types
+
+    from linear_attention_nats_gb300 import build as b
+
+    for name, path in (("BUILD", "_build"), ("LIB", "libnats.so"), ("BINDING", "_operators.so"), ("STAMP", "_build/binding.txt")):
+        monkeypatch.setattr(b, name, str(tmp_path / path), raising=False)
+    ran, failing = [], set()
+
+    def run(cmd, **kw):
+        name = os.path.basename(cmd[0])
+        ran.append(name)
+        if name in failing:
+            return types.SimpleNamespace(returncode=1, stdout="", stderr="no headers")
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("built")
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+    monkeypatch.setenv("CXX", "g++")
+    return b, ran, failing
+
+
+def test_the_library_is_linked_where_its_binding_cannot_be(sandbox):
+    import os
+
+    b, ran, failing = sandbox
+    failing.add("g++")
+    with pytest.raises(RuntimeError, match="binding"):
+        b.build()
+    assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING) and not b.up_to_date()
+    ran.clear()
+    with pytest.raises(RuntimeError, match="binding"):
+        b.build()
+    assert ran == ["g++"]  # nothing of the library again
+    failing.clear()
+    b.build()
+    assert os.path.exists(b.BINDING) and b.up_to_date()
+
+
+def test_the_binding_is_built_again_for_another_python_or_torch(sandbox, monkeypatch):
+    import importlib.metadata
+
+    b, ran, _ = sandbox
+    b.build()
+    assert b.up_to_date() and "nvcc" in ran
+    ran.clear()
+    b.build()
+    assert ran == []
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda n: "0.0" if n == "torch" else version(n))
+    assert not b.up_to_date()
+    b.build()
+    assert ran == ["g++"] and b.up_to_date()
+    monkeypatch.setattr(b.sys, "version", "4.0")
+    b.build()
+    assert ran == ["g++", "g++"]
