@@ -1053,6 +1053,9 @@ nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float s
   if (s != NATS_OK) return s;
   if (!q || !out || !workspace || (accumulate && cache->n_pages > 0 && !cache->weight)) return NATS_ERR_NULL;
   const int es = cache->dtype == NATS_BF16 ? 2 : 4;
+  // (a stride that leads from nothing to nothing may be anything)
+  if (cache->B == 1) q_stride_b = 0;
+  if (Hq == 1) q_stride_h = 0;
   if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15u) return NATS_ERR_ALIGN;
   if ((q_stride_b * es) % 16 != 0 || (q_stride_h * es) % 16 != 0 || ((uintptr_t)lse & 3u)) return NATS_ERR_ALIGN;
   DecodeArgs a;

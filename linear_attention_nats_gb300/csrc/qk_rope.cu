@@ -596,8 +596,9 @@ void split_rows(long long tokens, int rows, int rpw, long long want, int* per_it
   *items = (rows + per - 1) / per;
 }
 
-Operand operand(const void* p, const nats_strides* s) {
-  return s ? Operand{p, s->b, s->h, s->t} : Operand{p, 0, 0, 0};
+// (a stride that leads from nothing to nothing may be anything: 0)
+Operand operand(const void* p, const nats_strides* s, int B, int H, int L) {
+  return s ? Operand{p, B > 1 ? s->b : 0, H > 1 ? s->h : 0, L > 1 ? s->t : 0} : Operand{p, 0, 0, 0};
 }
 
 // quads of this operand start at multiples of their size
@@ -685,8 +686,9 @@ nats_status nats_qk_norm_rope(const nats_rope_dims* dims, const void* q, const n
   if (dims->rot > 0 && !inv_freq) return NATS_ERR_NULL;
   const int es = dims->dtype == NATS_BF16 ? 2 : 4;
   RopeArgs a = {};
-  if (dims->Hq > 0) a.q = operand(q, q_st), a.qo = operand(q_out, q_out_st);
-  if (dims->Hk > 0) a.k = operand(k, k_st), a.ko = operand(k_out, k_out_st);
+  const auto of = [&](const void* p, const nats_strides* st, int H) { return operand(p, st, dims->B, H, dims->L); };
+  if (dims->Hq > 0) a.q = of(q, q_st, dims->Hq), a.qo = of(q_out, q_out_st, dims->Hq);
+  if (dims->Hk > 0) a.k = of(k, k_st, dims->Hk), a.ko = of(k_out, k_out_st, dims->Hk);
   const Operand* ops[] = {&a.q, &a.k, &a.qo, &a.ko};
   bool vec = true;
   for (const Operand* o : ops) {
@@ -721,8 +723,9 @@ nats_status nats_paged_append(const nats_paged_cache* cache, const nats_rope_dim
   if (dims->rot > 0 && !inv_freq) return NATS_ERR_NULL;
   const int es = dims->dtype == NATS_BF16 ? 2 : 4;
   RopeArgs a = {};
-  if (dims->Hq > 0) a.q = operand(q, q_st), a.qo = operand(q_out, q_out_st);
-  a.k = operand(k, k_st), a.v = operand(v, v_st);
+  const auto of = [&](const void* p, const nats_strides* st, int H) { return operand(p, st, dims->B, H, dims->L); };
+  if (dims->Hq > 0) a.q = of(q, q_st, dims->Hq), a.qo = of(q_out, q_out_st, dims->Hq);
+  a.k = of(k, k_st, dims->Hk), a.v = of(v, v_st, dims->Hk);
   const Operand* ops[] = {&a.q, &a.k, &a.v, &a.qo};
   bool vec = true;
   for (const Operand* o : ops) {
@@ -770,8 +773,11 @@ nats_status nats_qk_norm_rope_bwd(const nats_rope_dims* dims, int32_t grad_dtype
   const int es = dims->dtype == NATS_BF16 ? 2 : 4, eg = grad_dtype == NATS_BF16 ? 2 : 4,
             eo = dx_dtype == NATS_BF16 ? 2 : 4;
   RopeBwdArgs a = {};
-  if (dims->Hq > 0) a.gq = operand(dq_out, dq_out_st), a.q = operand(q, q_st), a.dq = operand(dq, dq_st);
-  if (dims->Hk > 0) a.gk = operand(dk_out, dk_out_st), a.k = operand(k, k_st), a.dk = operand(dk, dk_st);
+  const auto of = [&](const void* p, const nats_strides* st, int H) { return operand(p, st, dims->B, H, dims->L); };
+  if (dims->Hq > 0)
+    a.gq = of(dq_out, dq_out_st, dims->Hq), a.q = of(q, q_st, dims->Hq), a.dq = of(dq, dq_st, dims->Hq);
+  if (dims->Hk > 0)
+    a.gk = of(dk_out, dk_out_st, dims->Hk), a.k = of(k, k_st, dims->Hk), a.dk = of(dk, dk_st, dims->Hk);
   const Operand* ops[] = {&a.gq, &a.gk, &a.q, &a.k, &a.dq, &a.dk};
   const int sizes[] = {eg, eg, es, es, eo, eo};
   bool vec = true;

@@ -162,3 +162,26 @@ def test_weights_of_large_scores(nats, n, G, dtype):
     want = G * torch.softmax((k[0, :n, 0] + k[0, :n, 1]).double(), -1)
     got = c.weight.cpu().double().reshape(-1)[:n]
     assert ((got - want).abs() <= (4 * WEIGHT + (64 + n / 4 + 2 + G + 1) * U) * want).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_sequence_inside_wider_rows(nats, dtype):
+    """One sequence whose rows lie in a matrix of an odd width: the stride between sequences says nothing."""
+    rng = torch.Generator().manual_seed(6)
+    Hq, Hk, d, n = 4, 2, 64, 40
+    rows = torch.randn(3, (Hq + 2 * Hk) * d + 3, generator=rng).to(dtype).cuda()
+    q, k, v = (rows.as_strided((1, b - a, d), (rows.stride(0), d, 1), a * d) for a, b in ((0, 4), (4, 6), (6, 8)))
+    assert q.is_contiguous() and q.stride(0) % 2 == 1
+    f = nats.rope_inv_freq(d)
+    got = []
+    for copy in (lambda t: t, lambda t: torch.empty(t.shape, dtype=dtype, device="cuda").copy_(t)):
+        c = nats.PagedCache.empty(4, 16, Hk, d, 1, 4, dtype=dtype)
+        c.table.copy_(torch.arange(4, dtype=torch.int32)[None])
+        x = [copy(t)[:, :, None] for t in (q, k, v)]
+        for _ in range(n):
+            oq = nats.paged_append(c, x[1], x[2], q=x[0], norm=True, inv_freq=f)
+            c.lens.add_(1)
+        r = nats.qk_norm_rope(x[0], x[1], None, None, f, pos0=n - 1)
+        g = nats.qk_norm_rope_bwd(*r, x[0], x[1], None, None, f, pos0=n - 1)
+        got.append([nats.paged_decode(c, copy(q)), oq, c.k_pages, c.v_pages, *r, *g.values()])
+    assert all(torch.equal(a, b) for a, b in zip(*got))

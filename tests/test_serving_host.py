@@ -86,3 +86,24 @@ def test_the_binding_is_built_again_for_another_python_or_torch(sandbox, monkeyp
     monkeypatch.setattr(b.sys, "version", "4.0")
     b.build()
     assert ran == ["g++", "g++"]
+
+
+# ----------------------------------------------------------------- strides
+
+def test_decode_takes_any_stride_of_one_sequence_or_head():
+    """A stride between one row and nothing says nothing (torch leaves what it likes there, .contiguous() too): the
+    call goes on to its next check, a workspace that is too small."""
+    from linear_attention_nats_gb300 import build as b
+
+    b.build()
+    from linear_attention_nats_gb300 import _native as nat
+
+    A = 0x10000000
+
+    def call(B, Hq, qb, qh):
+        c = nat.PagedCache(A, A, A, A, A, A, 8, 16, 1, 64, B, 4, 0)
+        return nat.lib.nats_paged_decode(c, Hq, 0.0, A, qb, qh, A, None, 0, A, 0, None)
+
+    assert call(1, 4, 259, 64) == 5 and call(2, 4, 259, 64) == 4
+    assert call(3, 1, 64, 5) == 5 and call(3, 2, 64, 5) == 4
+    assert call(1, 1, 3, 5) == 5
