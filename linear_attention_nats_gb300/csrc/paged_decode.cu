@@ -48,9 +48,17 @@ struct DecodeArgs {
   float2* ml_ws;           // [B, Hq] maximum and 1 / sum of the units of one CTA
   float* part_ml;          // [2 ctas, GT, 2] maximum and sum
   float* part_o;           // [2 ctas, GT, D]
-  float* scores;           // [B, Hk, cap, G] or NULL: q . k, not yet scaled
+  float* scores;           // [B, Hk, cap, G], or pooled [n_pages, Hk, page, G], or NULL: q . k, not yet scaled
+  bool pooled;
   float* weight;
 };
+
+// The scores of a unit of sequence b and key head hk: from scores_of on, those of
+// slot j, in row `row` of the pool, G times scores_row further.
+__device__ __forceinline__ float* scores_of(const DecodeArgs& a, int b, int hk) {
+  return a.scores + (a.pooled ? 0 : ((long long)b * a.pg.Hk + hk) * a.pg.cap() * a.G);
+}
+__device__ __forceinline__ long long scores_row(const DecodeArgs& a, int j, int row) { return a.pooled ? row : j; }
 
 __device__ __forceinline__ int tiles_of(int n) { return (int)((uint32_t)(n + kTile - 1) / kTile); }
 
@@ -628,8 +636,9 @@ __device__ __forceinline__ void add_one_tile(const DecodeArgs& a, int b, int hk,
   for (int j = t; j < n; j += threads) {
     const int pg = a.pg.page_of(b, j / a.pg.page);
     if (pg < 0) continue;
-    float* at = a.weight + a.pg.row(pg, hk, j % a.pg.page);
-    const float* x = a.scores + (((long long)b * a.pg.Hk + hk) * a.pg.cap() + j) * a.G;
+    const int row = (int)a.pg.row(pg, hk, j % a.pg.page);
+    float* at = a.weight + row;
+    const float* x = scores_of(a, b, hk) + scores_row(a, j, row) * a.G;
     const float2* ml = a.ml_ws + (long long)b * a.Hq + hk * a.G;
     float w = 0.f;  // the group's sum, added once: of a heavy slot's weight, each head's part alone may be below half a step
 #pragma unroll 4
@@ -707,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
     int row = first_row(0), next = first_row(1);
     float *mine = so + warp * GT * kPitch<D>, *mine_ml = sml + warp * GT * 2;
     bool earlier = false;  // runs that have ended
+    float* const scores = ACC ? scores_of(a, mb, hk) + g0 : nullptr;
     load_k<X>(k, kp, row, g, c);
     load_v<X>(v, vp, row, n - slot0, g, c);
     for (int st = 0; st < steps; ++st) {
@@ -714,9 +724,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) decode_kernel(DecodeArgs a) 
       float s[NH][4] = {};
       X::scores(s, k, unit.q);
       load_k<X>(k, kp, next, g, c);
-      float* at = ACC ? a.scores + (((long long)mb * a.pg.Hk + hk) * a.pg.cap() + j0) * a.G + g0 : nullptr;
+      float* at = ACC ? scores + scores_row(a, j0, row) * a.G : nullptr;
       unit.template weigh<ACC>(s, a.scale2, row >= 0 && j0 + 16 <= n, row >= 0 && j0 + g < n, row >= 0 && j0 + g + 8 < n,
-                               at, a.G, n - j0, heads, mine, earlier, g, c);
+                               at, a.G, row >= 0 ? n - j0 : 0, heads, mine, earlier, g, c);
       X::values(unit.o, v, s, g, c);
       load_v<X>(v, vp, next, n - j0 - stride, g, c);
       row = next;
@@ -895,7 +905,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
       }
     }
     __syncthreads();
-    const float* scores = a.scores + ((long long)b * Hk + hk) * a.pg.cap() * G;
+    const float* const scores = scores_of(a, b, hk);
     for (; j < end; j += kSlots * kThreads) {
       float w[kSlots], was[kSlots];  // the group's sum, added once to the stored weight
       const float* x[kSlots];
@@ -903,10 +913,11 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int idx, int co
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         const int ji = j + i * kThreads;
-        at[i] = pg[i] < 0 ? nullptr : a.weight + a.pg.row(pg[i], hk, ji % a.pg.page);
+        const int row = (int)a.pg.row(max(pg[i], 0), hk, ji % a.pg.page);
+        at[i] = pg[i] < 0 ? nullptr : a.weight + row;
         was[i] = at[i] ? *at[i] : 0.f;
         w[i] = 0.f;
-        x[i] = scores + (long long)min(ji, end - 1) * G;
+        x[i] = scores + scores_row(a, min(ji, end - 1), row) * G;  // (without a page: any that can be read)
       }
       pages(j + kSlots * kThreads);
       auto add = [&](int i, float v, float2 ml) { w[i] = fmaf(weight_of(v, a.scale2, ml.x), ml.y, w[i]); };
@@ -956,6 +967,16 @@ __global__ void __launch_bounds__(kThreads, 8) decode_finish_kernel(DecodeArgs a
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
+// The scores that a call which accumulates keeps: of every slot of the table, or,
+// since no page is in the table twice then, of the pool, where the table (as long
+// as the longest allowed context) has more than twice the pool's slots.  32
+// sequences of 32 heads with tables of 131,072 slots over 4096 pages of 64: 34 MB,
+// 537 by the table.  The two take the same time (4 x 131072 slots 289 us each, 64
+// x 2000 51).
+double scores_by_table(const nats_paged_cache* c, int Hq) { return (double)c->B * Hq * c->max_pages * c->page; }
+double scores_by_pool(const nats_paged_cache* c, int Hq) { return (double)c->n_pages * c->page * Hq; }
+bool pooled(const nats_paged_cache* c, int Hq) { return scores_by_table(c, Hq) > 2 * scores_by_pool(c, Hq); }
+
 size_t layout(const nats_paged_cache* c, int Hq, bool accumulate, char* base, DecodeArgs* a) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -968,7 +989,9 @@ size_t layout(const nats_paged_cache* c, int Hq, bool accumulate, char* base, De
   d.ml_ws = (float2*)take(8 * (size_t)c->B * Hq);
   d.part_ml = (float*)take(4 * 2 * (size_t)kMaxCtas * kMaxHeads * 2);
   d.part_o = (float*)take(4 * 2 * (size_t)kMaxCtas * kMaxHeads * c->d);
-  d.scores = accumulate ? (float*)take(4 * (size_t)c->B * Hq * c->max_pages * c->page) : nullptr;
+  d.pooled = pooled(c, Hq);
+  const size_t scores = (size_t)(d.pooled ? scores_by_pool(c, Hq) : scores_by_table(c, Hq));
+  d.scores = accumulate ? (float*)take(4 * scores) : nullptr;
   if (a) *a = d;
   return off;
 }
@@ -982,7 +1005,7 @@ nats_status check_decode(const nats_paged_cache* c, int32_t Hq, int32_t accumula
   // rows of a pool and of the batch's queries are 32-bit
   if ((long long)c->B * Hq > (1LL << 31) - 1 || (double)c->n_pages * c->Hk * c->page > 2147483647.0)
     return NATS_ERR_UNSUPPORTED;
-  if (accumulate && (double)c->B * Hq * c->max_pages * c->page > 1099511627776.0) return NATS_ERR_UNSUPPORTED;
+  if (accumulate && std::fmin(scores_by_table(c, Hq), scores_by_pool(c, Hq)) > 1099511627776.0) return NATS_ERR_UNSUPPORTED;
   return NATS_OK;
 }
 

@@ -185,3 +185,48 @@ def test_one_sequence_inside_wider_rows(nats, dtype):
         g = nats.qk_norm_rope_bwd(*r, x[0], x[1], None, None, f, pos0=n - 1)
         got.append([nats.paged_decode(c, copy(q)), oq, c.k_pages, c.v_pages, *r, *g.values()])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("Hk,G,d,dtype", [(2, 4, 128, BF), (1, 9, 64, BF), (3, 1, 64, F32), (2, 12, 128, F32), (1, 40, 64, BF)])
+def test_weights_under_tables_longer_than_the_pool(nats, Hk, G, d, dtype):
+    """Tables for contexts far longer than the pool: what a call gives is what it gives with tables that just fit, bad
+    entries and the pool's last page among them."""
+    rng = torch.Generator().manual_seed(7 + G)
+    page, lens = 16, [700, 33, 0, 1, 64, 200]
+    need = [-(-n // page) for n in lens]
+    n_pages = sum(need)
+    shape = (n_pages, Hk, page, d)
+    k, v, w0 = torch.randn(shape, generator=rng), torch.randn(shape, generator=rng), torch.rand(shape[:3], generator=rng)
+    q = torch.randn(len(lens), Hk * G, d, generator=rng).to(dtype).cuda()
+    order, at, rows = torch.randperm(n_pages, generator=rng).int(), 0, []
+    for m in need:
+        rows.append(order[at:at + m].tolist())
+        at += m
+    rows[0][5], rows[1][1], rows[5][0] = -1, n_pages, -5
+    got = []
+    for width in (max(need), 40 * n_pages):
+        table = torch.full((len(lens), width), -1, dtype=torch.int32)
+        for b, r in enumerate(rows):
+            table[b, :len(r)] = torch.tensor(r, dtype=torch.int32)
+        c = nats.PagedCache(k.to(dtype).cuda(), v.to(dtype).cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                            weight=w0.cuda())
+        ws = torch.full((nats.paged_workspace_size(c, Hq=Hk * G, accumulate=True),), 255, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            out, lse = nats.paged_decode(c, q, accumulate=True, return_lse=True, workspace=ws)
+        got.append((out, lse, c.weight))
+        with pytest.raises(nats.NatsError):
+            c.check()
+    tight, wide = got
+    if dtype == F32 and G > 8:
+        # the wide table's units are of sixteen heads: other sums, the same values.  A score of either is off by (d + 8)
+        # 2^-23 of scale |q| |k|, a factor by twice that (its maximum too), outputs and weights by twice a factor's
+        score = (d + 8) * 2.0 ** -23 * d ** -0.5 * float(q.norm(dim=-1).max()) * float(k.norm(dim=-1).max())
+        tol = 2 * 4 * score * max(1.0, float(v.abs().max()))
+        for a, b in zip(tight, wide):
+            fin = torch.isfinite(a)
+            assert torch.equal(fin, torch.isfinite(b)) and ((a - b)[fin].abs() <= tol * (1 + a[fin].abs())).all()
+    else:
+        assert all(torch.equal(a, b) for a, b in zip(tight, wide))
+    # every sequence's weights sum to its query heads (the slots of bad entries have none)
+    per = sum(Hk * G for n in lens if n)
+    assert abs(float(wide[2].double().sum() - w0.double().sum()) - 2 * per) < 1e-3 * per

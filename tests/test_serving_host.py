@@ -107,3 +107,28 @@ def test_decode_takes_any_stride_of_one_sequence_or_head():
     assert call(1, 4, 259, 64) == 5 and call(2, 4, 259, 64) == 4
     assert call(3, 1, 64, 5) == 5 and call(3, 2, 64, 5) == 4
     assert call(1, 1, 3, 5) == 5
+
+
+# ---------------------------------------------------------------- workspace
+
+def test_weights_workspace_is_the_pools_where_tables_are_long():
+    """An accumulating call has no page in its table twice, so that scores of every slot of the pool are enough."""
+    from linear_attention_nats_gb300 import build as b
+
+    b.build()
+    from linear_attention_nats_gb300 import _native as nat
+
+    A = 0x10000000
+
+    def scores(B, Hq, n_pages, max_pages):
+        c = nat.PagedCache(A, A, A, A, A, A, n_pages, 64, 8, 128, B, max_pages, 0)
+        size = nat.lib.nats_paged_decode_workspace_size
+        return size(c, Hq, 1) - size(c, Hq, 0) if size(c, Hq, 1) else None
+
+    pool = 4 * 4096 * 64 * 32
+    assert scores(32, 32, 4096, 2048) == pool
+    assert scores(32, 32, 4096, 128) == pool  # as many slots as the pool
+    assert scores(32, 32, 65536, 128) == pool  # a part of a larger pool
+    # 2^41 slots and heads in the table, 2^27 in the pool; and too many of both
+    assert scores(1024, 128, 16384, 1 << 18) == 4 * 16384 * 64 * 128
+    assert scores(1024, 4096 * 8, 1 << 21, 1 << 18) is None
