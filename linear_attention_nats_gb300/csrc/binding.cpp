@@ -163,7 +163,8 @@ at::TensorOptions on(ScalarType s, int dev) {
 // The device and stream of one call.  What it allocates comes from that
 // stream's own memory, where work still to run on the current stream has no
 // part, and is marked as used on the current stream, where the caller will
-// read and free it.
+// read and free it.  What it is given is marked as used on the call's stream
+// (uses), so that the caller may free it before the call has run.
 struct Call {
   int dev;
   c10::cuda::CUDAStream cur;
@@ -194,6 +195,12 @@ struct Call {
       }
     }
     if (!other && c10::cuda::current_device() != dev) device.emplace((c10::DeviceIndex)dev);
+  }
+  template <class... O>
+  void uses(O*... args) const {
+    if (!other) return;
+    for (PyObject* o : {args...})
+      if (o != Py_None) THPVariable_Unpack(o).record_stream(other->current_stream());
   }
   Tensor made(const Tensor& t) const {
     if (other) t.record_stream(cur);
@@ -282,6 +289,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   done(fn.rope(&dm, hq.p, &hq.st, hk.p, &hk.st, wq, wk, r.inv_freq, r.pos, r.pos_b, pos0, hoq.p, &hoq.st, hok.p,
                &hok.st, call.stream),
        "nats_qk_norm_rope");
+  call.uses(a[0], a[1], a[2], a[3], a[4], a[5], a[10], a[11]);
   return pair(a[10] == Py_None ? THPVariable_Wrap(oq) : ref(a[10]), a[11] == Py_None ? THPVariable_Wrap(ok) : ref(a[11]));
   NATS_END
 }
@@ -323,6 +331,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    dw ? (float*)dwk.data_ptr() : nullptr, dw ? ws.data_ptr() : nullptr,
                    dw ? (size_t)ws.numel() : 0, call.stream),
        "nats_qk_norm_rope_bwd");
+  call.uses(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[12], a[13], dw ? a[15] : Py_None);
   PyObject* res = PyDict_New();
   if (!res) throw python_error();
   const auto put = [&](const char* name, PyObject* o) {
@@ -388,6 +397,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   done(fn.append(c, &dm, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, wq, wk, r.inv_freq, start, n_new, r.pos, r.pos_b,
                  hoq.p, &hoq.st, call.stream),
        "nats_paged_append");
+  call.uses(a[2], a[3], a[4], a[5], a[6], has_q ? a[7] : Py_None, a[9], a[10], a[11], a[12]);
   if (!has_q) Py_RETURN_NONE;
   return a[7] == Py_None ? THPVariable_Wrap(oq) : ref(a[7]);
   NATS_END
@@ -419,6 +429,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   done(fn.decode(c, Hq, scale, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(),
                  has_lse ? (float*)lse.data_ptr() : nullptr, accumulate, ws.data_ptr(), (size_t)ws.numel(), call.stream),
        "nats_paged_decode");
+  call.uses(a[2], a[6], a[7]);
   PyObject* o = a[6] == Py_None ? THPVariable_Wrap(out) : ref(a[6]);
   return has_lse ? pair(o, THPVariable_Wrap(lse)) : o;
   NATS_END
@@ -446,6 +457,7 @@ PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   done(fn.evict(c, pt, extent(table.size(1), "out_table"), budget, recent, sinks, (int32_t*)lens.data_ptr(),
                 has_keep ? (int32_t*)keep.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), call.stream),
        "nats_paged_evict");
+  call.uses(a[2], a[6], a[8]);
   PyObject* l = a[6] == Py_None ? THPVariable_Wrap(lens) : ref(a[6]);
   return has_keep ? pair(THPVariable_Wrap(keep), l) : l;
   NATS_END

@@ -87,6 +87,13 @@ class PagedCache:
                    torch.full((B, max_pages), -1, dtype=torch.int32, **z), torch.zeros((B,), dtype=torch.int32, **z),
                    weight=torch.zeros((n_pages, Hk, page), dtype=torch.float32, **z) if weight else None)
 
+    def _used_on(self, stream) -> None:
+        """The cache may be freed before a call on `stream` has run: its memory is not handed out again until then."""
+        if stream is not None:
+            for t in self._t:
+                if t is not None:
+                    t.record_stream(stream)
+
     def check(self) -> None:
         """Raises if a call since the cache was made met a table entry outside
         the pool, a length outside the table or an append behind it
@@ -116,6 +123,7 @@ def paged_append(cache: PagedCache, k, v, *, start=None, n_new=None, q=None, out
     on the way (at `positions`, int64 [B, T], or their slots).  Returns q' (in
     out_q, whose rows from n_new[b] on are left as they were, or in a new
     tensor, zero there), or None without q.  cache.lens is not changed."""
+    cache._used_on(stream)
     return _native.operators.paged_append(cache._addr, cache._dev, k, v, start, n_new, q, out_q, norm, w_q, w_k, inv_freq,
                                           positions, interleaved, eps, stream)
 
@@ -130,6 +138,7 @@ def paged_decode(cache: PagedCache, q, *, scale: float = 0.0, accumulate: bool =
     paged_workspace_size(cache, Hq=Hq, accumulate=accumulate) bytes, or None."""
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs a cache with weights")
+    cache._used_on(stream)
     return _native.operators.paged_decode(cache._addr, cache._dev, q, scale, accumulate, return_lse, out, workspace, stream)
 
 
@@ -145,5 +154,6 @@ def paged_evict(cache: PagedCache, out_table, budget: int, *, recent: int = 0, s
     and frees the old pages."""
     if cache.weight is None:
         raise ValueError("eviction needs a cache with weights")
+    cache._used_on(stream)
     return _native.operators.paged_evict(cache._addr, cache._dev, out_table, budget, recent, sinks, lens_out, return_keep,
                                          workspace, stream)
