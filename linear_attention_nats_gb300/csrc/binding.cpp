@@ -414,7 +414,10 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     q.sizes());
   check(q, "q", s, dev);
   TORCH_CHECK_VALUE(q.stride(2) == 1 || q.numel() == 0, "q: the entries of a row must be contiguous");
-  const float scale = (float)real(a[3]);
+  const double given = real(a[3]);
+  const float scale = (float)given;
+  // (0 asks for 1 / sqrt(d): a smaller scale than fp32 has must not become one)
+  TORCH_CHECK_VALUE(scale != 0.f || given == 0.0, "scale is out of range");
   const int accumulate = truth(a[4]);
   const bool has_lse = truth(a[5]);
   const int32_t Hq = extent(q.size(1), "Hq");

@@ -230,3 +230,42 @@ def test_weights_under_tables_longer_than_the_pool(nats, Hk, G, d, dtype):
     # every sequence's weights sum to its query heads (the slots of bad entries have none)
     per = sum(Hk * G for n in lens if n)
     assert abs(float(wide[2].double().sum() - w0.double().sum()) - 2 * per) < 1e-3 * per
+
+
+def test_scale_too_small_for_its_type_is_refused(nats):
+    """It would be taken as 0, which asks for 1 / sqrt(d)."""
+    c = nats.PagedCache.empty(2, 16, 1, 64, 1, 2)
+    q = torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    for scale in (1e-60, -1e-60):
+        with pytest.raises(ValueError):
+            nats.paged_decode(c, q, scale=scale)
+    nats.paged_decode(c, q, scale=1e-40)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_infinities_reach_no_further_than_a_nan(nats, dtype):
+    """An infinite value reaches its entry of its group's rows, an infinite key its group's rows and weights; all else
+    keeps its bits."""
+    rng = torch.Generator().manual_seed(8)
+    n, Hk, G, d, page = 300, 2, 3, 64, 16
+    pages = -(-n // page)
+    k, v = (torch.randn(pages, Hk, page, d, generator=rng).to(dtype) for _ in range(2))
+    q = torch.randn(1, Hk * G, d, generator=rng).to(dtype).cuda()
+
+    def run(k, v):
+        c = nats.PagedCache(k.cuda(), v.cuda(), torch.arange(pages, dtype=torch.int32)[None].cuda(),
+                            torch.tensor([n], dtype=torch.int32).cuda(), weight=torch.ones(pages, Hk, page, device="cuda"))
+        return nats.paged_decode(c, q, accumulate=True).cpu(), c.weight.cpu()
+
+    out, w = run(k, v)
+    for x in (math.inf, -math.inf):
+        bad = v.clone()
+        bad[3, 0, 5, 7] = x
+        o, u = run(k, bad)
+        assert not torch.isfinite(o[0, :G, 7]).any() and torch.equal(u, w)
+        o[0, :G, 7] = out[0, :G, 7]
+        assert torch.equal(o, out)
+        bad = k.clone()
+        bad[3, 1, 5, 7] = x
+        o, u = run(bad, v)
+        assert torch.equal(o[0, :G], out[0, :G]) and torch.equal(u[:, 0], w[:, 0])
