@@ -15,9 +15,10 @@
 //
 // Measured on one GB300 (HBM copy rate 6.8 TB/s): 32 contexts of 3000 to 8192
 // slots, 32 query and 8 key heads of 128, bf16: 112 us, 6.2 TB/s, the tensor
-// pipe 13 % busy; 4 contexts of up to 131,072 with weights 292 us, 5.7 TB/s (and
+// pipe 18 % busy; 4 contexts of up to 131,072 with weights 289 us, 5.7 TB/s (and
 // 134 MB of scores between the kernels); fp32 the same way, 5.8 TB/s at 8 x
-// 16384; 517 slots of one sequence 9.1 us, which is the two kernels' latency.
+// 16384; 517 slots of one sequence 9.1 us, the latencies of the two kernels one
+// after the other.
 #include <cmath>
 
 #include "kernels.h"
@@ -265,8 +266,9 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
 // a run of kRun steps' sums at most stands in its accumulators; they are then
 // added to the unit's in shared memory, each lane its own.  4 x 131072 slots, 4
 // heads a group: 0.06 % of the outputs are not the rounded exact value, with two
-// parts and one run 0.32 % (as fast: 290 us); fresh accumulators for every step
-// the same 0.06 %, 312 us.  Groups of 12, 16 x 16384 slots: 68.6 us, 64.5 with two.
+// parts and one run 0.32 % (as fast); fresh accumulators for every step the same
+// 0.06 %, 312 us where this took 290.  Groups of 12, 16 x 16384 slots, 8 key heads
+// of 128: 123 us, 117 with two parts.
 template <int D>
 struct Bf16 {
   using T = __nv_bfloat16;
@@ -590,16 +592,20 @@ struct Unit {
   }
   // the values to shared memory, to what earlier runs left there if there were any
   __device__ __forceinline__ void put_values(float* so, bool earlier, int g, int c) {
+    if (X::kRun > 0 && earlier) {
+#pragma unroll
+      for (int x = 0; x < NH; ++x)
+#pragma unroll
+        for (int y = 0; y < MT; ++y)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[x][y][i] += so[at_so(x, i & 1, y, i >> 1, g, c)];
+    }
 #pragma unroll
     for (int x = 0; x < NH; ++x)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int y = 0; y < MT; ++y)
 #pragma unroll
-        for (int y = 0; y < MT; ++y) {
-          float *lo = so + at_so(x, i, y, 0, g, c), *hi = so + at_so(x, i, y, 1, g, c);
-          *lo = earlier ? *lo + o[x][y][i] : o[x][y][i];
-          *hi = earlier ? *hi + o[x][y][i + 2] : o[x][y][i + 2];
-        }
+        for (int i = 0; i < 4; ++i) so[at_so(x, i & 1, y, i >> 1, g, c)] = o[x][y][i];
   }
   // A run's values added up (each lane its own entries), for the next run to begin at zero.
   __device__ __forceinline__ void end_run(float* so, bool earlier, int g, int c) {
@@ -631,7 +637,7 @@ struct Unit {
 // have just written: weight[slot] += sum over the group's heads of p = 2^(score -
 // maximum) / sum, thread t of `threads` a slot after the other, as add_weights does for
 // longer ones.  175 sequences of up to 38 slots, 16 heads: 22.5 us, 27 with
-// these tiles in add_weights too.
+// these tiles in add_weights too (24.0 with the weights' third part).
 __device__ __forceinline__ void add_one_tile(const DecodeArgs& a, int b, int hk, int n, int t, int threads) {
   for (int j = t; j < n; j += threads) {
     const int pg = a.pg.page_of(b, j / a.pg.page);
@@ -1034,12 +1040,15 @@ cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
 
 // Units of eight heads; groups of more than eight in units of sixteen, whose
 // rows are then read, and in fp32 split, once.  bf16, 16 x 16384 slots, 12 heads
-// a group: 117 us (83 % of the copy rate, with two warps a scheduler); their
+// a group: 123 us (78 % of the copy rate, with two warps a scheduler); their
 // heads dealt to several warps 161 us where this took 145.  fp32, 8 x 16384, 12
-// heads a group: d 64 93 us (61 %), 123 in units of eight; d 128 206 us (56 %),
+// heads a group: d 64 94 us (60 %), 123 in units of eight; d 128 206 us (56 %),
 // 239; but only where there are some four tiles a CTA, since units of eight are
-// twice as many to share out (14 x 86 slots, 4 key heads, d 128: 20 us, 15.6 in
-// units of eight).  fp32 queries of 128 are read again for every step (F32's
+// twice as many to share out (14 x 86 slots, 4 key heads, d 128: 14.8 us, 12.6 in
+// units of eight).  Lengths are on the device, so the table's capacity stands for
+// them here: short sequences in long tables get units of sixteen.  Groups of more
+// than sixteen read their rows once a unit (one key head, 1 x 131072 slots, d 128,
+// bf16: 16 heads 41 us, 64 52, 128 83).  fp32 queries of 128 are read again for every step (F32's
 // QREG; 8 x 16384, 4 heads a group: 134 us, 138 held in registers, some of them
 // spilled), those of 64 held (70.5 against 71.6).
 cudaError_t launch(DecodeArgs& a, int dtype, int d, cudaStream_t st) {
