@@ -269,3 +269,33 @@ def test_infinities_reach_no_further_than_a_nan(nats, dtype):
         bad[3, 1, 5, 7] = x
         o, u = run(bad, v)
         assert torch.equal(o[0, :G], out[0, :G]) and torch.equal(u[:, 0], w[:, 0])
+
+
+@pytest.mark.parametrize("n", [60, 3000])
+@pytest.mark.parametrize("G,dtype", [(2, BF), (2, F32), (12, BF), (12, F32)])
+def test_scores_up_to_the_stated_size(nats, n, G, dtype):
+    """Scores near 2^27 (2^27.5 in powers of two: steps of 16) that the products form exactly and that rise slot by slot:
+    outputs and weights go by their distances, multiples of 8.  Bounds as above, a weight's for its own distance x: (2 |x|
+    ln 2 + 4) U, and 2^-126 where fp32's exponential ends; the outputs of n / 16 steps: (n / 4 + 64) 2^-23 of the weighted
+    magnitudes, what is more than 12 away counting for nothing."""
+    page, d = 16, 64
+    N = -(-n // page) * page
+    rng = torch.Generator().manual_seed(9)
+    k = torch.zeros(1, N, d)
+    k[0, :, 0] = 2.0 ** 27
+    k[0, :n, 1] = -8.0 * torch.randint(0, 32, (n,), generator=rng).sort(descending=True).values
+    q = torch.zeros(1, G, d)
+    q[:, :, :2] = 1
+    v = torch.randn(1, N, d, generator=rng).to(dtype)
+    c = _shared(nats, k.to(dtype), v, 1, n, page, torch.zeros(N // page, 1, page, device="cuda"))
+    out, lse = nats.paged_decode(c, q.to(dtype).cuda(), scale=1.0, accumulate=True, return_lse=True)
+    p = torch.softmax((k[0, :n, 0].double() + k[0, :n, 1].double()), -1)
+    got = c.weight.cpu().double().reshape(-1)[:n]
+    x = (k[0, :n, 1].double().max() - k[0, :n, 1].double()) * math.log2(math.e)
+    rel = (2 * x * math.log(2) + 4) * U + 2 * WEIGHT + (64 + n / 4 + 2 + G + 1) * U
+    assert ((got - G * p).abs() <= rel * G * p + G * 2.0 ** -126).all()
+    e, mag = p @ v[0, :n].double(), p @ v[0, :n].double().abs()
+    rel = 8 * WEIGHT + (n / 4 + 64) * 2.0 ** -23
+    half = 2.0 ** -8 if dtype == BF else U
+    assert ((out.cpu().double()[0] - e).abs() <= half * (e.abs() + rel * mag) + rel * mag).all()
+    assert ((lse.cpu().double() - 2.0 ** 27 * math.log2(math.e)).abs() <= 16).all()
