@@ -568,8 +568,10 @@ nats_status nats_nha_fwd_profiled(const nats_nha_dims* dims, const void* q, cons
  *   from rot on are z unchanged.
  * A weight of d^(-1/2) in every entry makes it the L2 norm that the Gated
  * DeltaNet branch of nats_hybrid_fwd wants of its keys.
- * Angles are formed in 64-bit fixed-point turns, so that they hold at any
- * int64 position to the precision of inv_freq (about 1e-9 rad at a million).
+ * Angles are formed in 64-bit fixed-point turns: a frequency is cut at 2^-64
+ * turns (2 pi p 2^-64 rad at position p: 3e-13 at a million, 4e-7 at 2^40), whole
+ * turns drop out exactly, and what is left is rounded to fp32, up to 1e-7 rad at
+ * any position.  A frequency that is an infinity or NaN makes its pairs NaN.
  *
  * Operands are indexed [B, H, L, d] through element strides (the last one is
  * 1), so q and k may lie inside one projection's output and the results in a
@@ -679,24 +681,32 @@ nats_status nats_paged_append(const nats_paged_cache* cache, const nats_rope_dim
  * (append the token first for it to see itself): query head h reads key head
  * h / (Hq / Hk),
  *   out[b, h] = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
- * zero for an empty sequence.  Entries in use are expected finite: a NaN or an
- * infinity makes what it reaches (a key's: the group's rows, a value's: that
- * entry of them) NaN, or infinite where the formula says so; entries of slots
- * not in use never matter.  q [B, Hq, d] with element strides q_stride_b,
+ * zero for an empty sequence.  Entries in use are expected finite, and scores
+ * below 2^28 in magnitude (scale log2 e q . k).  A NaN or an infinity leaves what
+ * it reaches without a value (in general NaN, also where the formula has an
+ * infinity): a key's the group's rows and weights, a value's that entry of them,
+ * and nothing else; entries of slots not in use never matter.  q [B, Hq, d] with element strides q_stride_b,
  * q_stride_h; out [B, Hq, d] contiguous (the cache's dtype); lse (or NULL)
  * fp32 [B, Hq]: log2 of the sum of 2^(scale log2 e q . k_j), -inf for an
  * empty sequence.  accumulate != 0 adds the group's weights, sum over its
  * query heads of p_j, to cache->weight in every slot.  The work is cut into
  * 64-slot tiles dealt evenly to the GPU whatever the lengths are (they are
  * read on the device), partial results are joined by a second kernel in a
- * fixed order.  scale 0 => 1/sqrt(d).  out must not overlap q.  In a call
+ * fixed order: the same call gives the same bits, but a sequence's last bits may
+ * change with its place in the batch and the others' lengths.  The query heads of
+ * a key head are taken sixteen at a time (fp32 with few slots: eight); a group of
+ * more reads its keys and values once for each of these.  Weights are summed
+ * over a group in fp32 and added to the stored ones once a call.  scale 0 =>
+ * 1/sqrt(d).  out must not overlap q.  In a call
  * that accumulates no page may be in the table twice (within or across
  * sequences).  workspace: device scratch of nats_paged_decode_workspace_size
- * bytes, 16-byte aligned; calls that share it must be ordered by the caller.
+ * bytes (with accumulate 4 Hq bytes a slot of the tables or, where these have
+ * more than twice as many, of the pool), 16-byte aligned; calls that share it
+ * must be ordered by the caller.
  * Errors before any launch: NATS_ERR_NULL, _SHAPE (Hq not a multiple of Hk,
  * the cache's fields), _UNSUPPORTED (more than 4096 query heads a key head, a
- * pool of 2^31 rows), _DTYPE, _VALUE (scale), _ALIGN (q, its strides and out:
- * 16 bytes), _WORKSPACE; NATS_ERR_CUDA on a failed launch. */
+ * pool of 2^31 rows), _DTYPE, _VALUE (scale), _ALIGN (q, its strides where they
+ * lead to another row, and out: 16 bytes), _WORKSPACE; NATS_ERR_CUDA on a failed launch. */
 size_t nats_paged_decode_workspace_size(const nats_paged_cache* cache, int32_t Hq, int32_t accumulate);
 nats_status nats_paged_decode(const nats_paged_cache* cache, int32_t Hq, float scale, const void* q,
                               int64_t q_stride_b, int64_t q_stride_h, void* out, float* lse, int32_t accumulate,

@@ -366,7 +366,10 @@ cudaError_t launch_select(const EvictArgs& a, long long cap, int C, cudaStream_t
 // of 131,072 34.5 us with 1024, 37.5 with 512.  *copied: the kernel copies too,
 // which pays while a CTA's rows are few, more of them where every SM has CTAs
 // that select while others copy (64 x 16 heads of 700 slots to 400: 75 us, 90
-// with the copy apart; but 32 x 8 of 2112 to 2048, 91 against 72).
+// with the copy apart; but 32 x 8 of 2112 to 2048, 91 against 72).  Lengths are on
+// the device: all of this goes by the table's capacity, and short sequences in
+// long tables are evicted by what suits the longest (64 x 8 heads of 1000 slots
+// to 900: 86 us, in tables of 131,072 slots 157).
 cudaError_t launch_select(const EvictArgs& a, long long cap, bool* copied, cudaStream_t st) {
   const long long heads = (long long)a.pg.B * a.pg.Hk;
   int C = 1;

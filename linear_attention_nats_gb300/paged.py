@@ -134,7 +134,7 @@ def paged_decode(cache: PagedCache, q, *, scale: float = 0.0, accumulate: bool =
     slots j < cache.lens[b]; query head h reads key head h / (Hq / Hk).
     Returns out [B, Hq, d], or (out, lse) with lse fp32 [B, Hq] in base 2.
     accumulate adds each slot's attention weight, summed over the query heads
-    of its key head, to cache.weight.  workspace: uint8 tensor of
+    of its key head, to cache.weight (no page may then be in the table twice).  workspace: uint8 tensor of
     paged_workspace_size(cache, Hq=Hq, accumulate=accumulate) bytes, or None."""
     if accumulate and cache.weight is None:
         raise ValueError("accumulate needs a cache with weights")

@@ -26,7 +26,7 @@ def qk_norm_rope(q, k, w_q=None, w_k=None, inv_freq=None, positions=None, *, pos
 
     q [B, Hq, L, d], k [B, Hk, L, d] bf16 or fp32 (d 64 or 128); w_q, w_k fp32
     [d] or None (unit); inv_freq float64 [rot / 2] (rope_inv_freq; None: no
-    rotation); positions int64 [B, L] or [L], or None: pos0 + t; interleaved:
+    rotation; one that is not finite makes its pairs NaN); positions int64 [B, L] or [L], or None: pos0 + t; interleaved:
     pairs (2i, 2i + 1) in place of (i, i + rot / 2); norm=False rotates alone.
     Returns (q', k') in the layer's contiguous [B, H, L, d], or in out_q, out_k
     (any strides but the last; the inputs themselves for in place)."""
