@@ -299,3 +299,24 @@ def test_scores_up_to_the_stated_size(nats, n, G, dtype):
     half = 2.0 ** -8 if dtype == BF else U
     assert ((out.cpu().double()[0] - e).abs() <= half * (e.abs() + rel * mag) + rel * mag).all()
     assert ((lse.cpu().double() - 2.0 ** 27 * math.log2(math.e)).abs() <= 16).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_most_heads_a_group(nats, dtype):
+    """4096 query heads on one key head, with weights: sums and factors of a whole group in shared memory."""
+    import serving_ref as ref
+
+    rng = torch.Generator().manual_seed(10)
+    lens, page, d, G = [200, 10, 0], 16, 64, 4096
+    table, _, n_pages = ref.assign(lens, page, rng)
+    k, v = (torch.randn(n_pages, 1, page, d, generator=rng).to(dtype) for _ in range(2))
+    q = torch.randn(len(lens), G, d, generator=rng).to(dtype)
+    c = nats.PagedCache(k.cuda(), v.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                        weight=torch.zeros(n_pages, 1, page, device="cuda"))
+    out = nats.paged_decode(c, q.cuda(), accumulate=True)
+    e, _, ps, err, perr = ref.decode(q, k, v, table, lens)
+    assert ((out.cpu().double() - e).abs() <= ref.HALF[dtype] * (e.abs() + err) + err).all()
+    got = c.weight.cpu().double()
+    for b, n in enumerate(lens):
+        w, want = ref.slots(got, table, b, n, page)[0], ps[b].sum(1)[0]
+        assert ((w - want).abs() <= perr[b].sum(1)[0] + (G + 1) * U * want).all()

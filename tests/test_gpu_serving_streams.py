@@ -78,3 +78,25 @@ def test_arguments_may_be_freed_before_a_call_on_another_stream_has_run(nats, na
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del junk
+
+
+@pytest.mark.parametrize("name", ["rope", "back", "decode", "append", "evict"])
+def test_captured_on_a_forked_stream(nats, name):
+    """A graph whose call runs on a second stream, with arguments made and freed inside the capture."""
+    args, call = _calls(nats)[name]
+    want = [t.clone() for t in call({n: t.clone() for n, t in args.items()}, None)]
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        mine = {n: t.clone() for n, t in args.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(mine, side)
+        del mine
+        torch.cuda.current_stream().wait_stream(side)
+        out = [t.clone() for t in got]
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
