@@ -732,6 +732,118 @@ nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_t
                              int32_t budget, int32_t recent, int32_t sinks, int32_t* lens_out, int32_t* keep,
                              void* workspace, size_t workspace_bytes, nats_stream_t stream);
 
+/* ------------------------------------------------------------- layer norm
+ * Layer norm of rows of D entries, ahead of a layer's projections or of each
+ * head's output:
+ *   z = (x - mean(x)) r,  r = 1 / sqrt(mean((x - mean(x))^2) + eps),  y = w z + b.
+ * Rows are indexed [B, H, L, D] through element strides (the last one is 1;
+ * a plain [rows, D] has B = H = 1), so they may be the heads of a
+ * [B, L, H, D] tensor.  Any D from 1 to 16384; rows that start at multiples
+ * of 16 bytes with D a multiple of 16 bytes move in vectors, others entry by
+ * entry.  Statistics and sums in fp32, the squared distances taken from the
+ * mean itself. */
+typedef struct {
+  int32_t B, H, L; /* rows: B H L of them, below 2^31 */
+  int32_t D;       /* entries of a row */
+  int32_t dtype;   /* nats_dtype of x, y and their gradients */
+  float eps;
+} nats_norm_dims;
+
+/* Forward.  w, b fp32 [D] or NULL (1, 0).  out may be x with the same
+ * strides; other overlaps are not allowed.  All pointers device but strides
+ * and dims.  Errors before any launch: NATS_ERR_NULL, NATS_ERR_SHAPE (negative
+ * extents, D < 1), NATS_ERR_DTYPE, NATS_ERR_UNSUPPORTED (D above 16384, too
+ * many rows), NATS_ERR_VALUE (eps), NATS_ERR_ALIGN (a pointer not aligned to
+ * its element); NATS_ERR_CUDA on a failed launch. */
+nats_status nats_layer_norm(const nats_norm_dims* dims, const void* x, const nats_strides* x_st, const float* w,
+                            const float* b, void* out, const nats_strides* out_st, nats_stream_t stream);
+
+/* Its gradient: dout, the gradient of y, and the forward's x and w give, with
+ * t = w dout,
+ *   dx = r (t - mean(t) - z mean(t z)),  dw = sum over rows of dout z,
+ *   db = sum over rows of dout
+ * (dw, db fp32 [D], overwritten; NULL: not computed; zero without rows).  The
+ * statistics are formed again from x: the forward keeps nothing.  dx may be
+ * dout or x with the same strides.  Sums over rows are taken in a fixed order
+ * (the same inputs and sizes give the same bits).  workspace: device scratch
+ * of nats_layer_norm_bwd_workspace_size bytes, 16-byte aligned (NULL when
+ * neither dw nor db is asked for).  Errors as the forward, and
+ * NATS_ERR_WORKSPACE. */
+size_t nats_layer_norm_bwd_workspace_size(const nats_norm_dims* dims);
+nats_status nats_layer_norm_bwd(const nats_norm_dims* dims, const void* dout, const nats_strides* dout_st, const void* x,
+                                const nats_strides* x_st, const float* w, void* dx, const nats_strides* dx_st, float* dw,
+                                float* db, void* workspace, size_t workspace_bytes, nats_stream_t stream);
+
+/* ------------------------- linear attention with a decay for each head
+ * The fixed-decay linear attention that a stack puts between hybrid layers:
+ * with gamma = e^(log_decay[h]) and a state S [dv, dk] for each head,
+ *   S_t = gamma S_(t-1) + v_t k_t^T,   o_t = scale S_t q_t.
+ * The prompt form works on chunks of tokens (their scores with the decays
+ * between them, and the state ahead of them); a sequence is cut into segments
+ * where heads are too few for the GPU, the states ahead of the segments then
+ * come from passes of their own.  States are fp32 throughout, [B, H, d, d]
+ * with a value's entries as rows.  Operands are indexed [B, H, L, d] through
+ * element strides (the last one is 1), so q, k and v may lie inside one
+ * projection's output.
+ * log_decay fp32 [H], meant to be <= 0; 0 is plain linear attention, -inf
+ * leaves each token its own value alone.  It is a constant of the head and has
+ * no gradient.  lens int32 [B] (or NULL: L everywhere; values are taken as the
+ * nearest in 0 .. L): tokens from lens[b] on take no part, whatever they hold,
+ * and their rows of the outputs (gradients too) are zero; the last state is
+ * that after lens[b] tokens.  Tokens that take part are expected finite: a NaN
+ * or an infinity may reach every output of its head.
+ * bf16 operands that TMA can address (rows at multiples of 16 bytes, no
+ * expanded dimension) run on the tensor cores: scores and the state ahead of a
+ * chunk enter their products in bf16, the state itself is summed from
+ * exact products.  Others, and fp32, run in fp32 throughout. */
+typedef struct {
+  int32_t B, H, L;
+  int32_t d;     /* head size, 64 or 128 */
+  int32_t dtype; /* nats_dtype of q, k, v, out and their gradients */
+  float scale;   /* 0 => 1/sqrt(d) */
+} nats_decay_dims;
+
+/* Prompt.  state_in fp32 (or NULL: zero): the state ahead of the first token;
+ * state_out fp32 (or NULL): the one after the last; they may be the same
+ * memory.  out must not overlap an input.  workspace: device scratch of
+ * nats_decay_attn_workspace_size bytes (0 where no sequence is cut),
+ * 16-byte aligned.  All pointers device but strides and dims.  Errors before
+ * any launch: NATS_ERR_NULL, NATS_ERR_SHAPE (negative extents), NATS_ERR_DTYPE,
+ * NATS_ERR_UNSUPPORTED (d; B H above 2^22; L above 2^30), NATS_ERR_VALUE (scale
+ * negative, not finite or below fp32's smallest normal number), NATS_ERR_ALIGN
+ * (a pointer not aligned to its element, the workspace), NATS_ERR_WORKSPACE;
+ * NATS_ERR_CUDA on a failed launch. */
+size_t nats_decay_attn_workspace_size(const nats_decay_dims* dims);
+nats_status nats_decay_attn(const nats_decay_dims* dims, const void* q, const nats_strides* q_st, const void* k,
+                            const nats_strides* k_st, const void* v, const nats_strides* v_st, const float* log_decay,
+                            const int32_t* lens, const float* state_in, void* out, const nats_strides* out_st,
+                            float* state_out, void* workspace, size_t workspace_bytes, nats_stream_t stream);
+
+/* Its gradient: dout, the gradient of out, and dstate_out, that of the last
+ * state (or NULL: zero), give, with R_t = scale dout_t q_t^T + gamma R_(t+1)
+ * the gradient of S_t (R_L = scale dout_L q_L^T + dstate_out),
+ *   dq_t = scale S_t^T dout_t,  dk_t = R_t^T v_t,  dv_t = R_t k_t,
+ *   dstate_in = gamma R_1 (fp32, or NULL: not wanted),
+ * all overwritten.  The other arguments are the forward's; no output may
+ * overlap an input or another output.  Errors as the forward
+ * (NATS_ERR_VALUE also for dstate_in = dstate_out). */
+size_t nats_decay_attn_bwd_workspace_size(const nats_decay_dims* dims);
+nats_status nats_decay_attn_bwd(const nats_decay_dims* dims, const void* dout, const nats_strides* dout_st,
+                                const void* q, const nats_strides* q_st, const void* k, const nats_strides* k_st,
+                                const void* v, const nats_strides* v_st, const float* log_decay, const int32_t* lens,
+                                const float* state_in, const float* dstate_out, void* dq, const nats_strides* dq_st,
+                                void* dk, const nats_strides* dk_st, void* dv, const nats_strides* dv_st,
+                                float* dstate_in, void* workspace, size_t workspace_bytes, nats_stream_t stream);
+
+/* One new token of each sequence (dims->L = 1) on its kept state, which is
+ * updated in place (16-byte aligned).  q, k, v, out [B, H, d] through strides
+ * b and h (t is not used).  out must not overlap an input.  Errors as the
+ * prompt form, NATS_ERR_SHAPE also for L other than 1. */
+nats_status nats_decay_attn_step(const nats_decay_dims* dims, const void* q, const nats_strides* q_st, const void* k,
+                                 const nats_strides* k_st, const void* v, const nats_strides* v_st,
+                                 const float* log_decay, float* state, void* out, const nats_strides* out_st,
+                                 nats_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

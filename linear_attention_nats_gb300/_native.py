@@ -35,7 +35,10 @@ EXPORTS = ("nats_status_string", "nats_last_cuda_error", "nats_workspace_size", 
            "nats_nha_workspace_check", "nats_nha_fwd_profiled",
            "nats_qk_norm_rope", "nats_qk_norm_rope_bwd_workspace_size", "nats_qk_norm_rope_bwd", "nats_paged_append",
            "nats_paged_decode_workspace_size", "nats_paged_decode", "nats_paged_evict_workspace_size",
-           "nats_paged_evict")
+           "nats_paged_evict",
+           "nats_layer_norm", "nats_layer_norm_bwd_workspace_size", "nats_layer_norm_bwd",
+           "nats_decay_attn_workspace_size", "nats_decay_attn", "nats_decay_attn_bwd_workspace_size",
+           "nats_decay_attn_bwd", "nats_decay_attn_step")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -83,6 +86,14 @@ class Strides(ctypes.Structure):
 class RopeDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "L", "Hq", "Hk", "d", "rot", "interleaved", "norm", "dtype")] + [
         ("eps", ctypes.c_float)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "L", "D", "dtype")] + [("eps", ctypes.c_float)]
+
+
+class DecayDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "L", "d", "dtype")] + [("scale", ctypes.c_float)]
 
 
 class PagedCache(ctypes.Structure):
@@ -187,6 +198,21 @@ def _load() -> ctypes.CDLL:
     lib.nats_paged_evict_workspace_size.restype = SZ
     lib.nats_paged_evict.argtypes = [C, P, I32, I32, I32, I32, P, P, P, SZ, P]
     lib.nats_paged_evict.restype = ctypes.c_int
+    N, A = ctypes.POINTER(NormDims), ctypes.POINTER(DecayDims)
+    lib.nats_layer_norm.argtypes = [N, P, S, P, P, P, S, P]
+    lib.nats_layer_norm.restype = ctypes.c_int
+    lib.nats_layer_norm_bwd_workspace_size.argtypes = [N]
+    lib.nats_layer_norm_bwd_workspace_size.restype = SZ
+    lib.nats_layer_norm_bwd.argtypes = [N, P, S, P, S, P, P, S, P, P, P, SZ, P]
+    lib.nats_layer_norm_bwd.restype = ctypes.c_int
+    for f in (lib.nats_decay_attn_workspace_size, lib.nats_decay_attn_bwd_workspace_size):
+        f.argtypes, f.restype = [A], SZ
+    lib.nats_decay_attn.argtypes = [A, P, S, P, S, P, S, P, P, P, P, S, P, P, SZ, P]
+    lib.nats_decay_attn.restype = ctypes.c_int
+    lib.nats_decay_attn_bwd.argtypes = [A, P, S, P, S, P, S, P, S, P, P, P, P, P, S, P, S, P, S, P, P, SZ, P]
+    lib.nats_decay_attn_bwd.restype = ctypes.c_int
+    lib.nats_decay_attn_step.argtypes = [A, P, S, P, S, P, S, P, P, P, S, P]
+    lib.nats_decay_attn_step.restype = ctypes.c_int
     return lib
 
 
@@ -201,7 +227,9 @@ def _load_operators():
         raise ImportError(f"_operators.so is not built; run `python -c 'import __graft_entry__ as g; g.build()'` ({e})")
     names = ("nats_qk_norm_rope", "nats_qk_norm_rope_bwd", "nats_qk_norm_rope_bwd_workspace_size", "nats_paged_append",
              "nats_paged_decode", "nats_paged_decode_workspace_size", "nats_paged_evict",
-             "nats_paged_evict_workspace_size")
+             "nats_paged_evict_workspace_size", "nats_layer_norm", "nats_layer_norm_bwd",
+             "nats_layer_norm_bwd_workspace_size", "nats_decay_attn", "nats_decay_attn_workspace_size",
+             "nats_decay_attn_bwd", "nats_decay_attn_bwd_workspace_size", "nats_decay_attn_step")
     lib = __getattr__("lib")
     _operators.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, NatsError)
     return _operators

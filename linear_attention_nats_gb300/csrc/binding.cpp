@@ -1,5 +1,5 @@
 // binding.cpp - the torch-facing side of the operators around the layers
-// (norm + rotation, paged cache): checks of the tensors, allocation of the
+// (norm + rotation, paged cache, layer norm, linear attention with a decay): checks of the tensors, allocation of the
 // outputs, the stream, and the call into libnats' C ABI.
 //
 // A small call's time is its host's: in Python these checks took two to three
@@ -17,7 +17,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <optional>
+#include <vector>
 
 #include "../../include/nats.h"
 
@@ -36,6 +38,14 @@ struct Functions {
   decltype(&nats_paged_decode_workspace_size) decode_ws;
   decltype(&nats_paged_evict) evict;
   decltype(&nats_paged_evict_workspace_size) evict_ws;
+  decltype(&nats_layer_norm) norm;
+  decltype(&nats_layer_norm_bwd) norm_bwd;
+  decltype(&nats_layer_norm_bwd_workspace_size) norm_bwd_ws;
+  decltype(&nats_decay_attn) decay;
+  decltype(&nats_decay_attn_workspace_size) decay_ws;
+  decltype(&nats_decay_attn_bwd) decay_bwd;
+  decltype(&nats_decay_attn_bwd_workspace_size) decay_bwd_ws;
+  decltype(&nats_decay_attn_step) decay_step;
 } fn;
 PyObject* nats_error = nullptr;
 
@@ -243,6 +253,26 @@ PyObject* pair(PyObject* a, PyObject* b) {
   return t;
 }
 
+// A dict of results in the making.
+struct Dict {
+  PyObject* d = PyDict_New();
+  Dict() {
+    if (!d) throw python_error();
+  }
+  ~Dict() { Py_XDECREF(d); }
+  Dict(const Dict&) = delete;
+  void put(const char* name, PyObject* o) {
+    const int bad = o ? PyDict_SetItemString(d, name, o) : -1;
+    Py_XDECREF(o);
+    if (bad) throw python_error();
+  }
+  PyObject* give() {
+    PyObject* r = d;
+    d = nullptr;
+    return r;
+  }
+};
+
 #define NATS_BEGIN(count)                                                       \
   HANDLE_TH_ERRORS                                                              \
   try {                                                                         \
@@ -332,23 +362,14 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    dw ? (size_t)ws.numel() : 0, call.stream),
        "nats_qk_norm_rope_bwd");
   call.uses(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[12], a[13], dw ? a[15] : Py_None);
-  PyObject* res = PyDict_New();
-  if (!res) throw python_error();
-  const auto put = [&](const char* name, PyObject* o) {
-    const int bad = o ? PyDict_SetItemString(res, name, o) : -1;
-    Py_XDECREF(o);
-    if (bad) {
-      Py_DECREF(res);
-      throw python_error();
-    }
-  };
-  put("dq", a[12] == Py_None ? THPVariable_Wrap(dq) : ref(a[12]));
-  put("dk", a[13] == Py_None ? THPVariable_Wrap(dk) : ref(a[13]));
+  Dict res;
+  res.put("dq", a[12] == Py_None ? THPVariable_Wrap(dq) : ref(a[12]));
+  res.put("dk", a[13] == Py_None ? THPVariable_Wrap(dk) : ref(a[13]));
   if (dw) {
-    put("dw_q", THPVariable_Wrap(dwq));
-    put("dw_k", THPVariable_Wrap(dwk));
+    res.put("dw_q", THPVariable_Wrap(dwq));
+    res.put("dw_k", THPVariable_Wrap(dwk));
   }
-  return res;
+  return res.give();
   NATS_END
 }
 
@@ -466,6 +487,236 @@ PyObject* paged_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   NATS_END
 }
 
+// The leading dimensions of tensors of one shape, brought to three: those that
+// follow one another in memory in all of them are one.
+template <int N>
+struct Lead {
+  int64_t size[3] = {1, 1, 1};
+  nats_strides st[N];
+  bool empty = false;
+
+  Lead(const Tensor* const (&t)[N], const char* name) {
+    std::vector<int64_t> n;
+    std::vector<std::array<int64_t, N>> s;
+    const int64_t dims = t[0]->dim() - 1;
+    for (int64_t i = 0; i < dims; ++i) {
+      const int64_t e = t[0]->size(i);
+      if (e == 0) empty = true;
+      if (e == 1) continue;
+      std::array<int64_t, N> x;
+      bool joins = !n.empty();
+      for (int j = 0; j < N; ++j) {
+        x[j] = t[j]->stride(i);
+        joins = joins && s.back()[j] == x[j] * e;
+      }
+      if (joins) {
+        n.back() *= e, s.back() = x;
+      } else {
+        n.push_back(e), s.push_back(x);
+      }
+    }
+    if (empty) n.clear(), s.clear();
+    TORCH_CHECK_VALUE(n.size() <= 3, name, " has more than three leading dimensions that do not follow one another in memory");
+    for (int j = 0; j < N; ++j) {
+      int64_t* p[3] = {&st[j].b, &st[j].h, &st[j].t};
+      for (size_t i = 0; i < 3; ++i) *p[i] = 0;
+      for (size_t i = 0; i < n.size(); ++i) *p[3 - n.size() + i] = s[i][j];
+    }
+    for (size_t i = 0; i < n.size(); ++i) size[3 - n.size() + i] = n[i];
+    if (empty) size[2] = 0;
+  }
+};
+
+const Tensor& rows(const Tensor& t, const char* name, ScalarType s, IntArrayRef shape, int dev, bool out) {
+  check(t, name, s, dev);
+  check_shape(t, name, shape);
+  TORCH_CHECK_VALUE(t.stride(-1) == 1 || t.size(-1) <= 1 || t.numel() == 0, name,
+                    ": the entries of a row must be contiguous (last stride 1, got ", t.stride(-1), ")");
+  if (out)
+    for (int64_t i = 0; i < t.dim(); ++i)
+      TORCH_CHECK_VALUE(t.stride(i) != 0 || t.size(i) <= 1, name, " is written and must not be an expanded tensor");
+  return t;
+}
+
+// x, weight, bias, eps, out, stream
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NATS_BEGIN(6)
+  const Tensor& x = tensor(a[0], "x");
+  TORCH_CHECK_VALUE(x.dim() >= 1, "x must have at least one dimension");
+  const int dev = device_of(x, "x"), code = code_of(x, "x");
+  const ScalarType s = x.scalar_type();
+  const int64_t D = x.size(-1);
+  rows(x, "x", s, x.sizes(), dev, false);
+  const float* w = (const float*)contiguous(a[1], "weight", at::kFloat, {D}, dev);
+  const float* b = (const float*)contiguous(a[2], "bias", at::kFloat, {D}, dev);
+  const Call call(dev, a[5]);
+  const Tensor out = a[4] == Py_None ? call.empty(x.sizes(), s) : tensor(a[4], "out");
+  rows(out, "out", s, x.sizes(), dev, true);
+  const Tensor* const both[2] = {&x, &out};
+  const Lead<2> l(both, "x");
+  const nats_norm_dims dm = {extent(l.size[0], "x"), extent(l.size[1], "x"), extent(l.size[2], "x"), extent(D, "x"), code,
+                             (float)real(a[3])};
+  done(fn.norm(&dm, x.data_ptr(), &l.st[0], w, b, out.data_ptr(), &l.st[1], call.stream), "nats_layer_norm");
+  call.uses(a[0], a[1], a[2], a[4]);
+  return a[4] == Py_None ? THPVariable_Wrap(out) : ref(a[4]);
+  NATS_END
+}
+
+// dout, x, weight, eps, dx, weight_grads, workspace, stream
+PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NATS_BEGIN(8)
+  const Tensor &u = tensor(a[0], "dout"), &x = tensor(a[1], "x");
+  TORCH_CHECK_VALUE(x.dim() >= 1, "x must have at least one dimension");
+  const int dev = device_of(x, "x"), code = code_of(x, "x");
+  const ScalarType s = x.scalar_type();
+  const int64_t D = x.size(-1);
+  rows(x, "x", s, x.sizes(), dev, false);
+  rows(u, "dout", s, x.sizes(), dev, false);
+  const float* w = (const float*)contiguous(a[2], "weight", at::kFloat, {D}, dev);
+  const Call call(dev, a[7]);
+  const Tensor dx = a[4] == Py_None ? call.empty(x.sizes(), s) : tensor(a[4], "dx");
+  rows(dx, "dx", s, x.sizes(), dev, true);
+  const Tensor* const all[3] = {&u, &x, &dx};
+  const Lead<3> l(all, "x");
+  const nats_norm_dims dm = {extent(l.size[0], "x"), extent(l.size[1], "x"), extent(l.size[2], "x"), extent(D, "x"), code,
+                             (float)real(a[3])};
+  const bool sums = truth(a[5]);
+  Tensor dw, db, ws;
+  if (sums) {
+    dw = call.empty({D}, at::kFloat), db = call.empty({D}, at::kFloat);
+    ws = call.workspace(a[6], a[6] == Py_None ? fn.norm_bwd_ws(&dm) : 0);
+  }
+  done(fn.norm_bwd(&dm, u.data_ptr(), &l.st[0], x.data_ptr(), &l.st[1], w, dx.data_ptr(), &l.st[2],
+                   sums ? (float*)dw.data_ptr() : nullptr, sums ? (float*)db.data_ptr() : nullptr,
+                   sums ? ws.data_ptr() : nullptr, sums ? (size_t)ws.numel() : 0, call.stream),
+       "nats_layer_norm_bwd");
+  call.uses(a[0], a[1], a[2], a[4], sums ? a[6] : Py_None);
+  Dict res;
+  res.put("dx", a[4] == Py_None ? THPVariable_Wrap(dx) : ref(a[4]));
+  if (sums) {
+    res.put("dw", THPVariable_Wrap(dw));
+    res.put("db", THPVariable_Wrap(db));
+  }
+  return res.give();
+  NATS_END
+}
+
+float scale_of(PyObject* o) {
+  const double given = real(o);
+  const float scale = (float)given;
+  // (0 asks for 1 / sqrt(d): a smaller scale than fp32 has must not become one)
+  TORCH_CHECK_VALUE(scale != 0.f || given == 0.0, "scale is out of range");
+  return scale;
+}
+
+nats_decay_dims decay_dims(const Tensor& q, int code, PyObject* scale) {
+  TORCH_CHECK_VALUE(q.dim() == 4, "q must be [B, H, L, d], got ", q.sizes());
+  return {extent(q.size(0), "B"), extent(q.size(1), "H"), extent(q.size(2), "L"), extent(q.size(3), "d"), code,
+          scale_of(scale)};
+}
+
+// q, k, v, log_decay, scale, lens, state, return_state, state_out, out, workspace, stream
+PyObject* decay_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NATS_BEGIN(12)
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+  tensor(a[3], "log_decay");
+  const int dev = device_of(q, "q"), code = code_of(q, "q");
+  const ScalarType s = q.scalar_type();
+  const nats_decay_dims dm = decay_dims(q, code, a[4]);
+  const int64_t B = dm.B, H = dm.H, d = dm.d;
+  const Heads hq = heads(q, "q", s, q.sizes(), dev), hk = heads(k, "k", s, q.sizes(), dev),
+              hv = heads(v, "v", s, q.sizes(), dev);
+  const float* gp = (const float*)contiguous(a[3], "log_decay", at::kFloat, {H}, dev);
+  const int32_t* lens = (const int32_t*)contiguous(a[5], "lens", at::kInt, {B}, dev);
+  const float* s_in = (const float*)contiguous(a[6], "state", at::kFloat, {B, H, d, d}, dev);
+  const bool has_out = a[8] != Py_None, has_state = has_out || truth(a[7]);
+  const Call call(dev, a[11]);
+  Tensor so;
+  if (has_out)
+    contiguous(a[8], "state_out", at::kFloat, {B, H, d, d}, dev), so = THPVariable_Unpack(a[8]);
+  else if (has_state)
+    so = call.empty({B, H, d, d}, at::kFloat);
+  const Tensor out = a[9] == Py_None ? call.empty(q.sizes(), s) : tensor(a[9], "out");
+  const Heads ho = heads_out(out, "out", s, q.sizes(), dev);
+  const Tensor ws = call.workspace(a[10], a[10] == Py_None ? fn.decay_ws(&dm) : 0);
+  done(fn.decay(&dm, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, gp, lens, s_in, ho.p, &ho.st,
+                has_state ? (float*)so.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), call.stream),
+       "nats_decay_attn");
+  call.uses(a[0], a[1], a[2], a[3], a[5], a[6], a[8], a[9], a[10]);
+  PyObject* o = a[9] == Py_None ? THPVariable_Wrap(out) : ref(a[9]);
+  return has_state ? pair(o, has_out ? ref(a[8]) : THPVariable_Wrap(so)) : o;
+  NATS_END
+}
+
+// dout, q, k, v, log_decay, scale, lens, state, dstate_out, state_grad, dq, dk, dv, workspace, stream
+PyObject* decay_attn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NATS_BEGIN(15)
+  const Tensor &u = tensor(a[0], "dout"), &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  tensor(a[4], "log_decay");
+  const int dev = device_of(q, "q"), code = code_of(q, "q");
+  const ScalarType s = q.scalar_type();
+  const nats_decay_dims dm = decay_dims(q, code, a[5]);
+  const int64_t B = dm.B, H = dm.H, d = dm.d;
+  const Heads hu = heads(u, "dout", s, q.sizes(), dev), hq = heads(q, "q", s, q.sizes(), dev),
+              hk = heads(k, "k", s, q.sizes(), dev), hv = heads(v, "v", s, q.sizes(), dev);
+  const float* gp = (const float*)contiguous(a[4], "log_decay", at::kFloat, {H}, dev);
+  const int32_t* lens = (const int32_t*)contiguous(a[6], "lens", at::kInt, {B}, dev);
+  const float* s_in = (const float*)contiguous(a[7], "state", at::kFloat, {B, H, d, d}, dev);
+  const float* ds_out = (const float*)contiguous(a[8], "dstate_out", at::kFloat, {B, H, d, d}, dev);
+  const bool has_state = truth(a[9]);
+  const Call call(dev, a[14]);
+  Tensor ds, grads[3];
+  Heads hg[3];
+  const char* const names[3] = {"dq", "dk", "dv"};
+  if (has_state) ds = call.empty({B, H, d, d}, at::kFloat);
+  for (int i = 0; i < 3; ++i) {
+    grads[i] = a[10 + i] == Py_None ? call.empty(q.sizes(), s) : tensor(a[10 + i], names[i]);
+    hg[i] = heads_out(grads[i], names[i], s, q.sizes(), dev);
+  }
+  const Tensor ws = call.workspace(a[13], a[13] == Py_None ? fn.decay_bwd_ws(&dm) : 0);
+  done(fn.decay_bwd(&dm, hu.p, &hu.st, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, gp, lens, s_in, ds_out, hg[0].p,
+                    &hg[0].st, hg[1].p, &hg[1].st, hg[2].p, &hg[2].st, has_state ? (float*)ds.data_ptr() : nullptr,
+                    ws.data_ptr(), (size_t)ws.numel(), call.stream),
+       "nats_decay_attn_bwd");
+  call.uses(a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[8], a[10], a[11], a[12], a[13]);
+  Dict res;
+  for (int i = 0; i < 3; ++i) res.put(names[i], a[10 + i] == Py_None ? THPVariable_Wrap(grads[i]) : ref(a[10 + i]));
+  if (has_state) res.put("dstate", THPVariable_Wrap(ds));
+  return res.give();
+  NATS_END
+}
+
+// A [B, H, d] operand of single tokens.
+Heads token(const Tensor& t, const char* name, ScalarType s, IntArrayRef shape, int dev, bool out) {
+  rows(t, name, s, shape, dev, out);
+  return Heads{t.data_ptr(), {t.stride(0), t.stride(1), 0}};
+}
+
+// q, k, v, log_decay, state, scale, out, stream
+PyObject* decay_attn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NATS_BEGIN(8)
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+  tensor(a[3], "log_decay");
+  tensor(a[4], "state");
+  TORCH_CHECK_VALUE(q.dim() == 3, "q must be [B, H, d], got ", q.sizes());
+  const int dev = device_of(q, "q"), code = code_of(q, "q");
+  const ScalarType s = q.scalar_type();
+  const int64_t B = q.size(0), H = q.size(1), d = q.size(2);
+  const Heads hq = token(q, "q", s, q.sizes(), dev, false), hk = token(k, "k", s, q.sizes(), dev, false),
+              hv = token(v, "v", s, q.sizes(), dev, false);
+  const float* gp = (const float*)contiguous(a[3], "log_decay", at::kFloat, {H}, dev);
+  float* S = (float*)contiguous(a[4], "state", at::kFloat, {B, H, d, d}, dev);
+  const nats_decay_dims dm = {extent(B, "B"), extent(H, "H"), 1, extent(d, "d"), code, scale_of(a[5])};
+  const Call call(dev, a[7]);
+  const Tensor out = a[6] == Py_None ? call.empty(q.sizes(), s) : tensor(a[6], "out");
+  const Heads ho = token(out, "out", s, q.sizes(), dev, true);
+  done(fn.decay_step(&dm, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, gp, S, ho.p, &ho.st, call.stream),
+       "nats_decay_attn_step");
+  call.uses(a[0], a[1], a[2], a[3], a[4], a[6]);
+  return a[6] == Py_None ? THPVariable_Wrap(out) : ref(a[6]);
+  NATS_END
+}
+
 // setup(address of function by name, the error class)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   NATS_BEGIN(2)
@@ -485,15 +736,24 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   fn.decode_ws = (decltype(fn.decode_ws))get("nats_paged_decode_workspace_size");
   fn.evict = (decltype(fn.evict))get("nats_paged_evict");
   fn.evict_ws = (decltype(fn.evict_ws))get("nats_paged_evict_workspace_size");
+  fn.norm = (decltype(fn.norm))get("nats_layer_norm");
+  fn.norm_bwd = (decltype(fn.norm_bwd))get("nats_layer_norm_bwd");
+  fn.norm_bwd_ws = (decltype(fn.norm_bwd_ws))get("nats_layer_norm_bwd_workspace_size");
+  fn.decay = (decltype(fn.decay))get("nats_decay_attn");
+  fn.decay_ws = (decltype(fn.decay_ws))get("nats_decay_attn_workspace_size");
+  fn.decay_bwd = (decltype(fn.decay_bwd))get("nats_decay_attn_bwd");
+  fn.decay_bwd_ws = (decltype(fn.decay_bwd_ws))get("nats_decay_attn_bwd_workspace_size");
+  fn.decay_step = (decltype(fn.decay_step))get("nats_decay_attn_step");
   nats_error = ref(a[1]);
   Py_RETURN_NONE;
   NATS_END
 }
 
 #define NATS_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {NATS_METHOD(setup),        NATS_METHOD(qk_norm_rope), NATS_METHOD(qk_norm_rope_bwd),
-                         NATS_METHOD(paged_append), NATS_METHOD(paged_decode), NATS_METHOD(paged_evict),
-                         {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {NATS_METHOD(setup),        NATS_METHOD(qk_norm_rope),   NATS_METHOD(qk_norm_rope_bwd),
+                         NATS_METHOD(paged_append), NATS_METHOD(paged_decode),   NATS_METHOD(paged_evict),
+                         NATS_METHOD(layer_norm),   NATS_METHOD(layer_norm_bwd), NATS_METHOD(decay_attn),
+                         NATS_METHOD(decay_attn_bwd), NATS_METHOD(decay_attn_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, methods};
 
 }  // namespace
