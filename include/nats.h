@@ -835,6 +835,11 @@ nats_status nats_decay_attn_bwd(const nats_decay_dims* dims, const void* dout, c
                                 void* dk, const nats_strides* dk_st, void* dv, const nats_strides* dv_st,
                                 float* dstate_in, void* workspace, size_t workspace_bytes, nats_stream_t stream);
 
+/* Synchronises `stream` and reports NATS_ERR_INTERNAL if a bounded internal
+ * wait of a prompt form or gradient has expired on the current device since
+ * the last such report (its outputs are then not valid); NATS_ERR_CUDA. */
+nats_status nats_decay_attn_check(nats_stream_t stream);
+
 /* One new token of each sequence (dims->L = 1) on its kept state, which is
  * updated in place (16-byte aligned).  q, k, v, out [B, H, d] through strides
  * b and h (t is not used).  out must not overlap an input.  Errors as the

@@ -19,7 +19,7 @@ from ._native import NATS_BF16, NATS_F32, NatsError, check, dims  # noqa: F401
 __all__ = ["select", "hybrid_fwd", "hybrid_fwd_x", "nha_fwd", "DecodeState", "decode_step", "workspace_size", "NatsError",
            "dims", "NATS_BF16", "NATS_F32", "qk_norm_rope", "qk_norm_rope_bwd", "rope_inv_freq", "PagedCache",
            "paged_append", "paged_decode", "paged_evict", "paged_workspace_size", "layer_norm", "layer_norm_bwd", "decay_attn",
-           "decay_attn_bwd", "decay_attn_step"]
+           "decay_attn_bwd", "decay_attn_step", "decay_attn_check"]
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -401,4 +401,4 @@ def nha_fwd(q, k, v, log_alpha, *, window: int, scale: float = 0.0, out=None, wo
 from .rope import qk_norm_rope, qk_norm_rope_bwd, rope_inv_freq  # noqa: E402
 from .paged import PagedCache, paged_append, paged_decode, paged_evict, paged_workspace_size  # noqa: E402
 from .norm import layer_norm, layer_norm_bwd  # noqa: E402
-from .decay import decay_attn, decay_attn_bwd, decay_attn_step  # noqa: E402
+from .decay import decay_attn, decay_attn_bwd, decay_attn_check, decay_attn_step  # noqa: E402

@@ -101,6 +101,8 @@ inline bool rows_at(const Tokens& x, const nats_decay_dims* m, int bytes) {
 
 // The bf16 scans on the tensor cores (decay_attn_tc.cu).
 cudaError_t launch_tc(const Args& a, int d, bool states_only, cudaStream_t st);
+// Whether a bounded wait of theirs has expired on this device since the last question (synchronises st).
+cudaError_t expired_waits(int* out, cudaStream_t st);
 
 }  // namespace decay
 }  // namespace nats

@@ -342,7 +342,6 @@ nats_status run(Args& a, const nats_decay_dims* m, const float* log_decay, const
       vec = vec && rows_at(*x, m, m->dtype == NATS_BF16 ? 8 : 16);
       tc = tc && mapped(*x, m);
     }
-  tc = false;
   const Cut c = cut(m, nops, tc);
   const size_t one = part_bytes(m, c.segs);
   if (one) {
@@ -359,7 +358,7 @@ nats_status run(Args& a, const nats_decay_dims* m, const float* log_decay, const
   }
   const auto scans = [&](int first, int last, bool states) {
     a.first_op = first, a.last_op = last;
-    if (tc) return cudaErrorNotSupported;
+    if (tc) return launch_tc(a, m->d, states, st);
     if (m->dtype == NATS_BF16)
       return m->d == 64 ? launch_simt<__nv_bfloat16, 64>(a, states, st) : launch_simt<__nv_bfloat16, 128>(a, states, st);
     return m->d == 64 ? launch_simt<float, 64>(a, states, st) : launch_simt<float, 128>(a, states, st);
@@ -463,6 +462,12 @@ nats_status nats_decay_attn_bwd(const nats_decay_dims* dims, const void* dout, c
   a.op[1] = {tv, tu, tq, tokens(dk, dk_st), dstate_out, nullptr, d, 1, 1.f / scale, scale, nullptr, 0, 1};
   a.op[2] = {tk, tq, tu, tokens(dv, dv_st), dstate_out, dstate_in, 1, d, 1.f / scale, scale, nullptr, 0, 1};
   return run(a, dims, log_decay, lens, ws, workspace_bytes, st);
+}
+
+nats_status nats_decay_attn_check(nats_stream_t stream) {
+  int expired = 0;
+  const int r = record_cuda_error(expired_waits(&expired, (cudaStream_t)stream));
+  return r != NATS_OK ? (nats_status)r : expired ? NATS_ERR_INTERNAL : NATS_OK;
 }
 
 }  // extern "C"

@@ -48,3 +48,11 @@ def decay_attn_step(q, k, v, log_decay, state, *, scale: float = 0.0, out: Optio
     last) on `state`, fp32 [B, H, d, d], which is updated in place.  Returns
     out [B, H, d] (contiguous, or the given tensor)."""
     return _native.operators.decay_attn_step(q, k, v, log_decay, state, scale, out, stream)
+
+
+def decay_attn_check(stream=None) -> None:
+    """Synchronises with `stream` (None: the current one) and raises NatsError
+    if a kernel of decay_attn or decay_attn_bwd has given up on a bounded wait
+    on the current device since the last such report."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    _native.check(_native.lib.nats_decay_attn_check(s.cuda_stream), "nats_decay_attn_check")
