@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kMaxD = 16384;
-constexpr int kBwdCtas = 4 * kSMs;  // rows of partial sums that the workspace holds
+constexpr int kBwdCtas = 8 * kSMs;  // most CTAs of the gradient: rows of partial sums that the workspace holds
 
 struct Rows {
   char* p;
@@ -81,8 +81,8 @@ struct Piece<T, 1> {
 };
 
 // Sums of N numbers over the G threads of a row, left in all of them; a group
-// is part of a warp or a whole CTA.  `flip` changes from call to call, so that
-// one barrier a sum is enough.
+// is part of a warp or whole warps of the CTA.  `sm` is the group's own; `flip`
+// changes from call to call, so that one barrier a sum is enough.
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float* sm, int& flip) {
 #pragma unroll
@@ -95,8 +95,8 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* sm, int& flip) {
     flip ^= 1;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[i * W + (threadIdx.x >> 5)] = v[i];
-    __syncthreads();
+      for (int i = 0; i < N; ++i) s[i * W + (threadIdx.x % G >> 5)] = v[i];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / G), "n"(G) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float t = s[i * W];
@@ -106,26 +106,31 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* sm, int& flip) {
     }
   }
 }
+template <int G>
+constexpr int kSums = G > 32 ? 4 * (G / 32) : 1;  // floats of a group's sums
 
-// Thread j of a group holds pieces j, j + G, .. of its row, NV of them.
-template <class T, int VEC, int G, int NV>
-__global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs a) {
-  begin();
-  constexpr int kBlock = G < 128 ? 128 : G, kGroups = kBlock / G;
-  __shared__ float sm[G > 32 ? 4 * (G / 32) : 1];
-  int flip = 0;
-  const int j = threadIdx.x % G;
-  const long long at = (long long)blockIdx.x * kGroups + threadIdx.x / G;
-  const bool live = at < a.rows;
-  const int row = live ? (int)at : a.rows - 1;
-  const T* x = (const T*)row_at(a.x, a, row);
-  Piece<T, VEC> in[NV];
+// VEC consecutive weights.
+template <int VEC>
+__device__ __forceinline__ void weights(const float* p, float (&w)[VEC], float none) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * G + j) * VEC;
-    if (c < a.D) in[i].load(x + c);
-    else in[i].zero();
+  for (int e = 0; e < VEC; ++e) w[e] = none;
+  if (!p) return;
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      const float4 x = *(const float4*)(p + e);
+      w[e] = x.x, w[e + 1] = x.y, w[e + 2] = x.z, w[e + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[e] = p[e];
   }
+}
+
+// The mean and 1 / standard deviation of the row whose pieces a group holds
+// (zero behind its end).
+template <class T, int VEC, int G, int NV>
+__device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], const NormArgs& a, int j, float* sm, int& flip) {
   float s[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -143,112 +148,166 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs 
         s[0] = fmaf(d, d, s[0]);
       }
   group_sum<G>(s, sm, flip);
-  const float r = 1.f / sqrtf(fmaf(s[0], a.inv_d, a.eps));
+  return make_float2(mean, 1.f / sqrtf(fmaf(s[0], a.inv_d, a.eps)));
+}
+
+// Thread j of a group holds pieces j, j + G, .. of its row, NV of them.
+template <class T, int VEC, int G, int NV>
+__global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs a) {
+  begin();
+  __shared__ float sums[G < 128 ? 128 / G : 1][kSums<G>];
+  int flip = 0;
+  const int j = threadIdx.x % G;
+  const long long at = (long long)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
+  const bool live = at < a.rows;
+  const int row = live ? (int)at : a.rows - 1;
+  const T* x = (const T*)row_at(a.x, a, row);
+  Piece<T, VEC> in[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + j) * VEC;
+    if (c < a.D) in[i].load(x + c);
+    else in[i].zero();
+  }
+  const float2 st = statistics<T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
   if (!live) return;
   T* y = (T*)row_at(a.y, a, row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * G + j) * VEC;
     if (c >= a.D) continue;
-    float v[VEC];
+    float v[VEC], w[VEC], b[VEC];
+    weights(a.w ? a.w + c : nullptr, w, 1.f);
+    weights(a.bias ? a.bias + c : nullptr, b, 0.f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      v[e] = (in[i][e] - mean) * r;
-      const float w = a.w ? a.w[c + e] : 1.f, bias = a.bias ? a.bias[c + e] : 0.f;
-      v[e] = fmaf(v[e], w, bias);
-    }
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf((in[i][e] - st.x) * st.y, w[e], b[e]);
     Piece<T, VEC>::store(y + c, v);
   }
 }
 
-// The gradient: a CTA takes rows blockIdx.x kGroups + group, a grid further on
-// each time, the next row's pieces in flight while one is worked on; every
-// thread sums its own columns' parts of dw and db in registers, the groups of
-// a CTA are added in order, and norm_dw_kernel adds the CTAs'.
+template <int G>
+constexpr int kBwdBlock = G < 256 ? 256 : G;
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
+// The gradient: a group takes row (CTA kGroups + group), then a grid further
+// on; every thread sums its own columns' parts of dw and db in registers, the
+// groups of a CTA are added in order, and norm_dw_kernel adds the CTAs'.
+// Pieces of 16 bytes are copied ahead into shared memory, each by the thread
+// that will use it, and read from there in each pass over the row: kAhead rows
+// are held without a register, those of the sums leave no room for them.
+template <int G, int NV>
+constexpr int kAhead = 3 * 2 * NV * kBwdBlock<G> * 16 <= 200 * 1024 ? 3 : 1;  // (one: fp32 rows of more than 8192)
 template <class T, int VEC, int G, int NV>
-__global__ void __launch_bounds__(G < 128 ? 128 : G) norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) norm_bwd_kernel(const NormArgs a) {
   begin();
-  constexpr int kBlock = G < 128 ? 128 : G, kGroups = kBlock / G;
-  __shared__ float sm[G > 32 ? 4 * (G / 32) : 1];
+  constexpr int kBlock = kBwdBlock<G>, kGroups = kBlock / G;
+  constexpr bool kAsync = VEC * sizeof(T) == 16;
+  constexpr int kRing = kAhead<G, NV>;
+  __shared__ float sums[kGroups][kSums<G>];
+  extern __shared__ __align__(16) uint4 ring[];  // [kRing][2 NV][kBlock]
   int flip = 0;
   const int j = threadIdx.x % G;
   float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + j) * VEC;
+    weights(a.w && c < a.D ? a.w + c : nullptr, w[i], 1.f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = (i * G + j) * VEC + e;
-      w[i][e] = a.w && c < a.D ? a.w[c] : 1.f;
-      dw[i][e] = db[i][e] = 0.f;
-    }
-  Piece<T, VEC> nx[NV], nu[NV];
-  const auto fetch = [&](long long at) {
-    const int row = at < a.rows ? (int)at : a.rows - 1;
-    const T *x = (const T*)row_at(a.x, a, row), *u = (const T*)row_at(a.u, a, row);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * G + j) * VEC;
-      if (c < a.D) {
-        nx[i].load(x + c), nu[i].load(u + c);
-      } else {
-        nx[i].zero(), nu[i].zero();
-      }
-    }
-  };
+    for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
+  }
   const long long step = (long long)gridDim.x * kGroups;
   const long long first = (long long)blockIdx.x * kGroups;
-  if (first < a.rows) fetch(first + threadIdx.x / G);
+  const auto fetch = [&](long long base, int slot) {
+    const long long at = base + threadIdx.x / G;
+    if (base < a.rows) {
+      const int row = at < a.rows ? (int)at : a.rows - 1;
+      const T *x = (const T*)row_at(a.x, a, row), *u = (const T*)row_at(a.u, a, row);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * G + j) * VEC;
+        if (c < a.D) {
+          copy16(&ring[(slot * 2 * NV + 2 * i) * kBlock + threadIdx.x], x + c);
+          copy16(&ring[(slot * 2 * NV + 2 * i + 1) * kBlock + threadIdx.x], u + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int slot = 0;
+  if constexpr (kAsync) {
+#pragma unroll
+    for (int s = 0; s < kRing; ++s) fetch(first + s * step, s);
+  }
   // (all groups of a CTA go round alike: those behind the last row work on it again, and drop the result)
   for (long long base = first; base < a.rows; base += step) {
     const long long at = base + threadIdx.x / G;
     const bool live = at < a.rows;
+    const int row = live ? (int)at : a.rows - 1;
     Piece<T, VEC> in[NV], gu[NV];
+    const uint4* mine = &ring[slot * 2 * NV * kBlock + threadIdx.x];
+    if constexpr (kAsync) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    } else {
+      const T *x = (const T*)row_at(a.x, a, row), *u = (const T*)row_at(a.u, a, row);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) in[i] = nx[i], gu[i] = nu[i];
-    if (base + step < a.rows) fetch(at + step);
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s[0] += in[i][e];
-    group_sum<G>(s, sm, flip);
-    const float mean = s[0] * a.inv_d;
-    s[0] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((i * G + j) * VEC < a.D)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = in[i][e] - mean;
-          s[0] = fmaf(d, d, s[0]);
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * G + j) * VEC;
+        if (c < a.D) {
+          in[i].load(x + c), gu[i].load(u + c);
+        } else {
+          in[i].zero(), gu[i].zero();
         }
-    group_sum<G>(s, sm, flip);
-    const float r = 1.f / sqrtf(fmaf(s[0], a.inv_d, a.eps));
+      }
+    }
+    // the row's pieces, again for each pass
+    const auto pieces = [&](bool both) {
+      if constexpr (kAsync) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          in[i].zero(), gu[i].zero();
+          if ((i * G + j) * VEC < a.D) {
+            in[i].load((const T*)(mine + 2 * i * kBlock));
+            if (both) gu[i].load((const T*)(mine + (2 * i + 1) * kBlock));
+          }
+        }
+      }
+    };
+    pieces(false);
+    const float2 st = statistics<T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
+    pieces(true);
     float m[2] = {0.f, 0.f};  // sums of t and t z
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float z = (in[i][e] - mean) * r, u = gu[i][e], t = u * w[i][e];
+        const float z = (in[i][e] - st.x) * st.y, u = gu[i][e], t = u * w[i][e];
         m[0] += t;
         m[1] = fmaf(t, z, m[1]);
         if (live) dw[i][e] = fmaf(u, z, dw[i][e]), db[i][e] += u;
       }
-    group_sum<G>(m, sm, flip);
+    group_sum<G>(m, sums[threadIdx.x / G], flip);
     m[0] *= a.inv_d, m[1] *= a.inv_d;
-    if (!live) continue;
-    T* y = (T*)row_at(a.y, a, (int)at);
+    pieces(true);
+    T* y = (T*)row_at(a.y, a, row);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * G + j) * VEC;
-      if (c >= a.D) continue;
+      if (c >= a.D || !live) continue;
       float v[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float z = (in[i][e] - mean) * r;
-        v[e] = r * (fmaf(gu[i][e], w[i][e], -m[0]) - z * m[1]);
+        const float z = (in[i][e] - st.x) * st.y;
+        v[e] = st.y * (fmaf(gu[i][e], w[i][e], -m[0]) - z * m[1]);
       }
       Piece<T, VEC>::store(y + c, v);
+    }
+    if constexpr (kAsync) {
+      fetch(base + kRing * step, slot);
+      slot = slot + 1 == kRing ? 0 : slot + 1;
     }
   }
   if (!a.part) return;
@@ -299,41 +358,65 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
 
 // ----------------------------------------------------------------- launches
 
-template <class T, int VEC, int G, int NV>
-cudaError_t go(const NormArgs& a, bool bwd, int* ctas, cudaStream_t st) {
-  constexpr int kBlock = G < 128 ? 128 : G, kGroups = kBlock / G;
+template <bool BWD, class T, int VEC, int G, int NV>
+cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
+  if constexpr (!BWD) {
+    // few rows: a CTA each, so that more SMs have a part
+    const int block = G >= 128 ? G : a.rows < 8 * kSMs && G >= 32 ? G : 128;
+    const int groups = block / G;
+    return after(norm_kernel<T, VEC, G, NV>, (unsigned)(((long long)a.rows + groups - 1) / groups), dim3(block), 0, st, 0, a);
+  } else {
+  constexpr int kBlock = kBwdBlock<G>, kGroups = kBlock / G;
+  constexpr int smem = VEC * sizeof(T) == 16 ? kAhead<G, NV> * 2 * NV * kBlock * 16 : 0;
+  auto kern = norm_bwd_kernel<T, VEC, G, NV>;
+  int fit = 0;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kBlock, smem);
+  if (e != cudaSuccess) return e;
+  const int most = kSMs * (fit < kBwdCtas / kSMs ? fit : kBwdCtas / kSMs);
   const long long need = ((long long)a.rows + kGroups - 1) / kGroups;
-  if (!bwd) return after(norm_kernel<T, VEC, G, NV>, (unsigned)need, dim3(kBlock), 0, st, 0, a);
-  *ctas = (int)(need < kBwdCtas ? need : kBwdCtas);
-  return after(norm_bwd_kernel<T, VEC, G, NV>, (unsigned)*ctas, dim3(kBlock), 0, st, 0, a);
+  *ctas = (int)(need < most ? need : most);
+  return after(kern, (unsigned)*ctas, dim3(kBlock), smem, st, 0, a);
+  }
 }
 
-// Threads and pieces of a row by its length: short rows share a warp, long
-// ones take a CTA.
-template <class T>
-cudaError_t choose(const NormArgs& a, bool vec, bool bwd, int* ctas, cudaStream_t st) {
+// Threads and pieces of a row by its length: up to 64 entries a thread forward,
+// so that the steps of the row's sums are few beside its entries; 16 in the
+// gradient, which keeps two sums and a weight for each.
+template <bool BWD, class T>
+cudaError_t choose(const NormArgs& a, bool vec, int* ctas, cudaStream_t st) {
   constexpr int V = sizeof(T) == 2 ? 8 : 4;
+  constexpr int M = 32 / V;
   const int n = vec ? a.D / V : a.D;
 #define NATS_NORM(VEC, G, NV) \
-  if (n <= (G) * (NV)) return go<T, VEC, G, NV>(a, bwd, ctas, st)
+  if (n <= (G) * (NV)) return go<BWD, T, VEC, G, NV>(a, ctas, st)
   if (vec) {
     NATS_NORM(V, 8, 1);
     NATS_NORM(V, 16, 1);
     NATS_NORM(V, 32, 1);
     NATS_NORM(V, 32, 2);
-    NATS_NORM(V, 128, 1);
-    NATS_NORM(V, 256, 1);
-    NATS_NORM(V, 512, 1);
-    NATS_NORM(V, 512, 2);
-    NATS_NORM(V, 512, 4);
-    if constexpr (V == 4) NATS_NORM(V, 512, 8);
+    if constexpr (BWD) {
+      NATS_NORM(V, 32, M / 2);
+      NATS_NORM(V, 64, M / 2);
+      NATS_NORM(V, 128, M / 2);
+      NATS_NORM(V, 256, M / 2);
+      NATS_NORM(V, 512, M / 2);
+    } else {
+      NATS_NORM(V, 32, M);
+      NATS_NORM(V, 32, 2 * M);
+      NATS_NORM(V, 64, M);
+      NATS_NORM(V, 128, M);
+      NATS_NORM(V, 256, M);
+    }
+    NATS_NORM(V, 512, M);
   } else {
-    NATS_NORM(1, 32, 2);
-    NATS_NORM(1, 32, 8);
-    NATS_NORM(1, 128, 8);
-    NATS_NORM(1, 512, 4);
-    NATS_NORM(1, 512, 8);
-    NATS_NORM(1, 512, 32);
+    NATS_NORM(1, 32, 4);
+    NATS_NORM(1, 32, 16);
+    NATS_NORM(1, 64, 16);
+    NATS_NORM(1, 128, 16);
+    NATS_NORM(1, 256, 16);
+    NATS_NORM(1, 512, 16);
+    NATS_NORM(1, 1024, 16);
   }
 #undef NATS_NORM
   return cudaErrorInvalidValue;
@@ -377,10 +460,10 @@ nats_status nats_layer_norm(const nats_norm_dims* dims, const void* x, const nat
   a.w = w, a.bias = b;
   a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D;
   a.eps = dims->eps, a.inv_d = 1.f / dims->D;
-  const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims);
+  const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && elem_ok(w, 16) && elem_ok(b, 16);
   cudaStream_t st = (cudaStream_t)stream;
-  return (nats_status)record_cuda_error(es == 2 ? choose<__nv_bfloat16>(a, vec, false, nullptr, st)
-                                                : choose<float>(a, vec, false, nullptr, st));
+  return (nats_status)record_cuda_error(es == 2 ? choose<false, __nv_bfloat16>(a, vec, nullptr, st)
+                                                : choose<false, float>(a, vec, nullptr, st));
 }
 
 size_t nats_layer_norm_bwd_workspace_size(const nats_norm_dims* dims) {
@@ -419,10 +502,11 @@ nats_status nats_layer_norm_bwd(const nats_norm_dims* dims, const void* dout, co
   a.w = w, a.part = sums ? (float*)workspace : nullptr;
   a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D;
   a.eps = dims->eps, a.inv_d = 1.f / dims->D;
-  const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && vec_ok(a.u, dims);
+  const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && vec_ok(a.u, dims) &&
+                   elem_ok(w, 16);
   int ctas = 0;
-  const int r = record_cuda_error(es == 2 ? choose<__nv_bfloat16>(a, vec, true, &ctas, st)
-                                          : choose<float>(a, vec, true, &ctas, st));
+  const int r = record_cuda_error(es == 2 ? choose<true, __nv_bfloat16>(a, vec, &ctas, st)
+                                          : choose<true, float>(a, vec, &ctas, st));
   if (r != NATS_OK || !sums) return (nats_status)r;
   const float* part = a.part;
   return (nats_status)record_cuda_error(after(norm_dw_kernel, (unsigned)((2 * dims->D + 31) / 32), dim3(32, 32), 0, st, 0,
