@@ -9,11 +9,13 @@
 // The gradient forms mean and r again from x, which it reads anyway, so the
 // forward has nothing to keep.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/nats.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "tc.cuh"
 
 namespace nats {
 namespace {
@@ -31,10 +33,12 @@ struct NormArgs {
   const float *w, *bias;
   float* part;  // [CTAs, 2, D]
   int rows, H, L, D;
+  int flat;  // rows follow one another at one stride
   float eps, inv_d;
 };
 
 __device__ __forceinline__ char* row_at(const Rows& r, const NormArgs& a, int i) {
+  if (a.flat) return r.p + i * r.t;
   const int t = i % a.L, bh = i / a.L;
   return r.p + (bh / a.H) * r.b + (bh % a.H) * r.h + t * r.t;
 }
@@ -127,26 +131,50 @@ __device__ __forceinline__ void weights(const float* p, float (&w)[VEC], float n
   }
 }
 
+// Entries 2 k and 2 k + 1 of a thread's own, as a pair for the packed fp32
+// instructions (one for both).
+template <int K, class T, int VEC, int NV>
+__device__ __forceinline__ uint64_t pair_of(const Piece<T, VEC> (&in)[NV]) {
+  return tc::f2_pack(in[2 * K / VEC][2 * K % VEC], in[(2 * K + 1) / VEC][(2 * K + 1) % VEC]);
+}
+__device__ __forceinline__ uint64_t both(float x) { return tc::f2_pack(x, x); }
+__device__ __forceinline__ float sum_of(uint64_t v) {
+  float a, b;
+  tc::f2_unpack(v, a, b);
+  return a + b;
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
 // The mean and 1 / standard deviation of the row whose pieces a group holds
 // (zero behind its end).
 template <class T, int VEC, int G, int NV>
 __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], const NormArgs& a, int j, float* sm, int& flip) {
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s[0] += in[i][e];
+  constexpr int kPairs = NV * VEC / 2;
+  uint64_t t[2] = {0, 0};
+  each<kPairs>([&](auto k) { t[k % 2] = tc::f2_add(t[k % 2], pair_of<k>(in)); });
+  float s[1] = {sum_of(tc::f2_add(t[0], t[1]))};
   group_sum<G>(s, sm, flip);
   const float mean = s[0] * a.inv_d;
-  s[0] = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * G + j) * VEC < a.D)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = in[i][e] - mean;
-        s[0] = fmaf(d, d, s[0]);
-      }
+  const uint64_t less = both(-mean);
+  t[0] = t[1] = 0;
+  each<kPairs>([&](auto k) {
+    uint64_t d = tc::f2_add(pair_of<k>(in), less);
+    if constexpr (VEC == 1) {
+      float x, y;
+      tc::f2_unpack(d, x, y);
+      d = tc::f2_pack(2 * k * G + j < a.D ? x : 0.f, (2 * k + 1) * G + j < a.D ? y : 0.f);
+    } else if ((2 * k / VEC * G + j) * VEC >= a.D) {
+      d = 0;
+    }
+    t[k % 2] = tc::f2_fma(d, d, t[k % 2]);
+  });
+  s[0] = sum_of(tc::f2_add(t[0], t[1]));
   group_sum<G>(s, sm, flip);
   return make_float2(mean, 1.f / sqrtf(fmaf(s[0], a.inv_d, a.eps)));
 }
@@ -211,13 +239,17 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
   extern __shared__ __align__(16) uint4 ring[];  // [kRing][2 NV][kBlock]
   int flip = 0;
   const int j = threadIdx.x % G;
-  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+  constexpr int kPairs = NV * VEC / 2;
+  uint64_t w[kPairs], dw[kPairs], db[kPairs];  // of a thread's entries, in pairs
+  {
+    float x[NV * VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * G + j) * VEC;
-    weights(a.w && c < a.D ? a.w + c : nullptr, w[i], 1.f);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + j) * VEC;
+      weights(a.w && c < a.D ? a.w + c : nullptr, *(float(*)[VEC])&x[i * VEC], 1.f);
+    }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
+    for (int k = 0; k < kPairs; ++k) w[k] = tc::f2_pack(x[2 * k], x[2 * k + 1]), dw[k] = db[k] = 0;
   }
   const long long step = (long long)gridDim.x * kGroups;
   const long long first = (long long)blockIdx.x * kGroups;
@@ -279,31 +311,29 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
     pieces(false);
     const float2 st = statistics<T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
     pieces(true);
-    float m[2] = {0.f, 0.f};  // sums of t and t z
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float z = (in[i][e] - st.x) * st.y, u = gu[i][e], t = u * w[i][e];
-        m[0] += t;
-        m[1] = fmaf(t, z, m[1]);
-        if (live) dw[i][e] = fmaf(u, z, dw[i][e]), db[i][e] += u;
-      }
+    // with d = x - mean, z = r d
+    const uint64_t r2 = both(st.y), less = both(-st.x);
+    uint64_t t0 = 0, t1 = 0;  // sums of t and t d
+    each<kPairs>([&](auto k) {
+      const uint64_t d = tc::f2_add(pair_of<k>(in), less), u = pair_of<k>(gu), t = tc::f2_mul(u, w[k]);
+      t0 = tc::f2_add(t0, t);
+      t1 = tc::f2_fma(t, d, t1);
+      if (live) dw[k] = tc::f2_fma(tc::f2_mul(u, r2), d, dw[k]), db[k] = tc::f2_add(db[k], u);
+    });
+    float m[2] = {sum_of(t0), sum_of(t1)};
     group_sum<G>(m, sums[threadIdx.x / G], flip);
-    m[0] *= a.inv_d, m[1] *= a.inv_d;
+    const uint64_t m0 = both(-m[0] * a.inv_d), m1 = both(-(m[1] * st.y * a.inv_d) * st.y * st.y);
     pieces(true);
     T* y = (T*)row_at(a.y, a, row);
+    float v[NV * VEC];
+    each<kPairs>([&](auto k) {
+      const uint64_t d = tc::f2_add(pair_of<k>(in), less), t = tc::f2_fma(pair_of<k>(gu), w[k], m0);
+      tc::f2_unpack(tc::f2_fma(d, m1, tc::f2_mul(r2, t)), v[2 * k], v[2 * k + 1]);
+    });
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * G + j) * VEC;
-      if (c >= a.D || !live) continue;
-      float v[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float z = (in[i][e] - st.x) * st.y;
-        v[e] = st.y * (fmaf(gu[i][e], w[i][e], -m[0]) - z * m[1]);
-      }
-      Piece<T, VEC>::store(y + c, v);
+      if (c < a.D && live) Piece<T, VEC>::store(y + c, *(const float(*)[VEC])&v[i * VEC]);
     }
     if constexpr (kAsync) {
       fetch(base + kRing * step, slot);
@@ -312,26 +342,28 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
   }
   if (!a.part) return;
   float* part = a.part + (long long)blockIdx.x * 2 * a.D;
+  float sw[NV * VEC], sb[NV * VEC];
+#pragma unroll
+  for (int k = 0; k < kPairs; ++k) {
+    tc::f2_unpack(dw[k], sw[2 * k], sw[2 * k + 1]);
+    tc::f2_unpack(db[k], sb[2 * k], sb[2 * k + 1]);
+  }
   if constexpr (kGroups == 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int c = (i * G + j) * VEC + e;
-        if (c < a.D) part[c] = dw[i][e], part[a.D + c] = db[i][e];
-      }
+    for (int i = 0; i < NV * VEC; ++i) {
+      const int c = (i / VEC * G + j) * VEC + i % VEC;
+      if (c < a.D) part[c] = sw[i], part[a.D + c] = sb[i];
+    }
   } else {
     __shared__ float acc[2][G * NV * VEC];
     for (int g = 0; g < kGroups; ++g) {
       if ((int)threadIdx.x / G == g)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const int c = (i * G + j) * VEC + e;
-            acc[0][c] = g ? acc[0][c] + dw[i][e] : dw[i][e];
-            acc[1][c] = g ? acc[1][c] + db[i][e] : db[i][e];
-          }
+        for (int i = 0; i < NV * VEC; ++i) {
+          const int c = (i / VEC * G + j) * VEC + i % VEC;
+          acc[0][c] = g ? acc[0][c] + sw[i] : sw[i];
+          acc[1][c] = g ? acc[1][c] + sb[i] : sb[i];
+        }
       __syncthreads();
     }
     for (int c = threadIdx.x; c < a.D; c += kBlock) part[c] = acc[0][c], part[a.D + c] = acc[1][c];
@@ -458,7 +490,7 @@ nats_status nats_layer_norm(const nats_norm_dims* dims, const void* x, const nat
   NormArgs a = {};
   a.x = rows_of(x, x_st, es), a.y = rows_of(out, out_st, es);
   a.w = w, a.bias = b;
-  a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D;
+  a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D, a.flat = dims->B == 1 && dims->H == 1;
   a.eps = dims->eps, a.inv_d = 1.f / dims->D;
   const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && elem_ok(w, 16) && elem_ok(b, 16);
   cudaStream_t st = (cudaStream_t)stream;
@@ -500,7 +532,7 @@ nats_status nats_layer_norm_bwd(const nats_norm_dims* dims, const void* dout, co
   NormArgs a = {};
   a.x = rows_of(x, x_st, es), a.y = rows_of(dx, dx_st, es), a.u = rows_of(dout, dout_st, es);
   a.w = w, a.part = sums ? (float*)workspace : nullptr;
-  a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D;
+  a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D, a.flat = dims->B == 1 && dims->H == 1;
   a.eps = dims->eps, a.inv_d = 1.f / dims->D;
   const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && vec_ok(a.u, dims) &&
                    elem_ok(w, 16);
