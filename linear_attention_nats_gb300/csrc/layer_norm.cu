@@ -37,11 +37,15 @@ struct NormArgs {
   float eps, inv_d;
 };
 
-__device__ __forceinline__ char* row_at(const Rows& r, const NormArgs& a, int i) {
-  if (a.flat) return r.p + i * r.t;
-  const int t = i % a.L, bh = i / a.L;
-  return r.p + (bh / a.H) * r.b + (bh % a.H) * r.h + t * r.t;
+struct Row {
+  int b, h, t;
+};
+__device__ __forceinline__ Row row_of(const NormArgs& a, int i) {
+  if (a.flat) return {0, 0, i};
+  const int bh = i / a.L;
+  return {bh / a.H, bh % a.H, i - bh * a.L};
 }
+__device__ __forceinline__ char* row_at(const Rows& r, const Row& i) { return r.p + i.b * r.b + i.h * r.h + i.t * r.t; }
 
 // VEC entries of a row, read or written at once.
 template <class T, int VEC>
@@ -153,7 +157,7 @@ __device__ __forceinline__ void each(F&& f) {
 
 // The mean and 1 / standard deviation of the row whose pieces a group holds
 // (zero behind its end).
-template <class T, int VEC, int G, int NV>
+template <bool FULL, class T, int VEC, int G, int NV>
 __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], const NormArgs& a, int j, float* sm, int& flip) {
   constexpr int kPairs = NV * VEC / 2;
   uint64_t t[2] = {0, 0};
@@ -169,7 +173,7 @@ __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], cons
       float x, y;
       tc::f2_unpack(d, x, y);
       d = tc::f2_pack(2 * k * G + j < a.D ? x : 0.f, (2 * k + 1) * G + j < a.D ? y : 0.f);
-    } else if ((2 * k / VEC * G + j) * VEC >= a.D) {
+    } else if (!FULL && (2 * k / VEC * G + j) * VEC >= a.D) {
       d = 0;
     }
     t[k % 2] = tc::f2_fma(d, d, t[k % 2]);
@@ -180,7 +184,7 @@ __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], cons
 }
 
 // Thread j of a group holds pieces j, j + G, .. of its row, NV of them.
-template <class T, int VEC, int G, int NV>
+template <bool FULL, class T, int VEC, int G, int NV>
 __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs a) {
   begin();
   __shared__ float sums[G < 128 ? 128 / G : 1][kSums<G>];
@@ -188,22 +192,22 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs 
   const int j = threadIdx.x % G;
   const long long at = (long long)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
   const bool live = at < a.rows;
-  const int row = live ? (int)at : a.rows - 1;
-  const T* x = (const T*)row_at(a.x, a, row);
+  const Row row = row_of(a, live ? (int)at : a.rows - 1);
+  const T* x = (const T*)row_at(a.x, row);
   Piece<T, VEC> in[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * G + j) * VEC;
-    if (c < a.D) in[i].load(x + c);
+    if (FULL || c < a.D) in[i].load(x + c);
     else in[i].zero();
   }
-  const float2 st = statistics<T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
+  const float2 st = statistics<FULL, T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
   if (!live) return;
-  T* y = (T*)row_at(a.y, a, row);
+  T* y = (T*)row_at(a.y, row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * G + j) * VEC;
-    if (c >= a.D) continue;
+    if (!FULL && c >= a.D) continue;
     float v[VEC], w[VEC], b[VEC];
     weights(a.w ? a.w + c : nullptr, w, 1.f);
     weights(a.bias ? a.bias + c : nullptr, b, 0.f);
@@ -214,7 +218,10 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs 
 }
 
 template <int G>
-constexpr int kBwdBlock = G < 256 ? 256 : G;
+constexpr int kBwdBlock = G < 128 ? 128 : G;
+// CTAs of an SM that the registers are to allow
+template <int VEC, int G, int NV>
+constexpr int kBwdFit = VEC == 1 ? 1 : (NV * VEC > 16 ? 384 : 512) / kBwdBlock<G>;
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
@@ -229,8 +236,8 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // are held without a register, those of the sums leave no room for them.
 template <int G, int NV>
 constexpr int kAhead = 3 * 2 * NV * kBwdBlock<G> * 16 <= 200 * 1024 ? 3 : 1;  // (one: fp32 rows of more than 8192)
-template <class T, int VEC, int G, int NV>
-__global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) norm_bwd_kernel(const NormArgs a) {
+template <bool FULL, class T, int VEC, int G, int NV>
+__global__ void __launch_bounds__(kBwdBlock<G>, kBwdFit<VEC, G, NV>) norm_bwd_kernel(const NormArgs a) {
   begin();
   constexpr int kBlock = kBwdBlock<G>, kGroups = kBlock / G;
   constexpr bool kAsync = VEC * sizeof(T) == 16;
@@ -256,12 +263,12 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
   const auto fetch = [&](long long base, int slot) {
     const long long at = base + threadIdx.x / G;
     if (base < a.rows) {
-      const int row = at < a.rows ? (int)at : a.rows - 1;
-      const T *x = (const T*)row_at(a.x, a, row), *u = (const T*)row_at(a.u, a, row);
+      const Row row = row_of(a, at < a.rows ? (int)at : a.rows - 1);
+      const T *x = (const T*)row_at(a.x, row), *u = (const T*)row_at(a.u, row);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * G + j) * VEC;
-        if (c < a.D) {
+        if (FULL || c < a.D) {
           copy16(&ring[(slot * 2 * NV + 2 * i) * kBlock + threadIdx.x], x + c);
           copy16(&ring[(slot * 2 * NV + 2 * i + 1) * kBlock + threadIdx.x], u + c);
         }
@@ -278,13 +285,13 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
   for (long long base = first; base < a.rows; base += step) {
     const long long at = base + threadIdx.x / G;
     const bool live = at < a.rows;
-    const int row = live ? (int)at : a.rows - 1;
+    const Row row = row_of(a, live ? (int)at : a.rows - 1);
     Piece<T, VEC> in[NV], gu[NV];
     const uint4* mine = &ring[slot * 2 * NV * kBlock + threadIdx.x];
     if constexpr (kAsync) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
     } else {
-      const T *x = (const T*)row_at(a.x, a, row), *u = (const T*)row_at(a.u, a, row);
+      const T *x = (const T*)row_at(a.x, row), *u = (const T*)row_at(a.u, row);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * G + j) * VEC;
@@ -300,8 +307,8 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
       if constexpr (kAsync) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          in[i].zero(), gu[i].zero();
-          if ((i * G + j) * VEC < a.D) {
+          if (!FULL) in[i].zero(), gu[i].zero();
+          if (FULL || (i * G + j) * VEC < a.D) {
             in[i].load((const T*)(mine + 2 * i * kBlock));
             if (both) gu[i].load((const T*)(mine + (2 * i + 1) * kBlock));
           }
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
       }
     };
     pieces(false);
-    const float2 st = statistics<T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
+    const float2 st = statistics<FULL, T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
     pieces(true);
     // with d = x - mean, z = r d
     const uint64_t r2 = both(st.y), less = both(-st.x);
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
     group_sum<G>(m, sums[threadIdx.x / G], flip);
     const uint64_t m0 = both(-m[0] * a.inv_d), m1 = both(-(m[1] * st.y * a.inv_d) * st.y * st.y);
     pieces(true);
-    T* y = (T*)row_at(a.y, a, row);
+    T* y = (T*)row_at(a.y, row);
     float v[NV * VEC];
     each<kPairs>([&](auto k) {
       const uint64_t d = tc::f2_add(pair_of<k>(in), less), t = tc::f2_fma(pair_of<k>(gu), w[k], m0);
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kBwdBlock<G>, G <= 256 && VEC > 1 ? 2 : 1) nor
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * G + j) * VEC;
-      if (c < a.D && live) Piece<T, VEC>::store(y + c, *(const float(*)[VEC])&v[i * VEC]);
+      if ((FULL || c < a.D) && live) Piece<T, VEC>::store(y + c, *(const float(*)[VEC])&v[i * VEC]);
     }
     if constexpr (kAsync) {
       fetch(base + kRing * step, slot);
@@ -375,10 +382,13 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   begin();
   __shared__ float sm[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;  // of [dw | db]
-  float s = 0.f;
+  float s[8] = {};  // (eight reads in flight)
   if (c < 2 * D)
-    for (int i = threadIdx.y; i < n; i += 32) s += part[(long long)i * 2 * D + c];
-  sm[threadIdx.y][threadIdx.x] = s;
+    for (int i = threadIdx.y; i < n; i += 256)
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + 32 * u < n) s[u] += part[(long long)(i + 32 * u) * 2 * D + c];
+  sm[threadIdx.y][threadIdx.x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
   const float t = warp_sum(sm[threadIdx.x][threadIdx.y]);
   const int o = blockIdx.x * 32 + threadIdx.y;
@@ -390,17 +400,17 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
 
 // ----------------------------------------------------------------- launches
 
-template <bool BWD, class T, int VEC, int G, int NV>
+template <bool BWD, bool FULL, class T, int VEC, int G, int NV>
 cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
   if constexpr (!BWD) {
     // few rows: a CTA each, so that more SMs have a part
     const int block = G >= 128 ? G : a.rows < 8 * kSMs && G >= 32 ? G : 128;
     const int groups = block / G;
-    return after(norm_kernel<T, VEC, G, NV>, (unsigned)(((long long)a.rows + groups - 1) / groups), dim3(block), 0, st, 0, a);
+    return after(norm_kernel<FULL, T, VEC, G, NV>, (unsigned)(((long long)a.rows + groups - 1) / groups), dim3(block), 0, st, 0, a);
   } else {
   constexpr int kBlock = kBwdBlock<G>, kGroups = kBlock / G;
   constexpr int smem = VEC * sizeof(T) == 16 ? kAhead<G, NV> * 2 * NV * kBlock * 16 : 0;
-  auto kern = norm_bwd_kernel<T, VEC, G, NV>;
+  auto kern = norm_bwd_kernel<FULL, T, VEC, G, NV>;
   int fit = 0;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kBlock, smem);
@@ -421,7 +431,9 @@ cudaError_t choose(const NormArgs& a, bool vec, int* ctas, cudaStream_t st) {
   constexpr int M = 32 / V;
   const int n = vec ? a.D / V : a.D;
 #define NATS_NORM(VEC, G, NV) \
-  if (n <= (G) * (NV)) return go<BWD, T, VEC, G, NV>(a, ctas, st)
+  if (n <= (G) * (NV))        \
+  return (VEC) != 1 && n == (G) * (NV) ? go<BWD, (VEC) != 1, T, VEC, G, NV>(a, ctas, st) \
+                                      : go<BWD, false, T, VEC, G, NV>(a, ctas, st)
   if (vec) {
     NATS_NORM(V, 8, 1);
     NATS_NORM(V, 16, 1);
@@ -429,9 +441,9 @@ cudaError_t choose(const NormArgs& a, bool vec, int* ctas, cudaStream_t st) {
     NATS_NORM(V, 32, 2);
     if constexpr (BWD) {
       NATS_NORM(V, 32, M / 2);
-      NATS_NORM(V, 64, M / 2);
-      NATS_NORM(V, 128, M / 2);
-      NATS_NORM(V, 256, M / 2);
+      NATS_NORM(V, 32, M);
+      NATS_NORM(V, 64, M);
+      NATS_NORM(V, 128, M);
       NATS_NORM(V, 512, M / 2);
     } else {
       NATS_NORM(V, 32, M);
