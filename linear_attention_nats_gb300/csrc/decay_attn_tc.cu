@@ -14,9 +14,9 @@
 // summed from exact products and the state is as good as an fp32 recurrence;
 // P and the copy of S are rounded to bf16, half a step like the output's own.
 //
-// Roles (576 threads): warps 0-3 P, warps 4-7 state, warps 8-11 output, warps
-// 12-15 W V, warp 16 TMA producer, warp 17 TMEM owner and MMA issuer.  The
-// output takes the place of the chunk's V tile on its way out (TMA store).
+// Roles (608 threads): warps 0-3 P, warps 4-7 state, warps 8-11 output, warps
+// 12-15 W V, warp 16 TMA producer, warps 17 (X, Oi, Op; owner of TMEM) and 18
+// (dS) MMA issuers.  The output takes the place of the chunk's V tile on its way out (TMA store).
 // Every wait is bounded (tc::kWaitLimitNs); an expired one sets g_expired.
 #include <cmath>
 #include <mutex>
@@ -43,6 +43,16 @@ struct TcArgs {
   Maps m[kMaxOps];
 };
 
+// Decays between tokens.  Entry y of the table is gamma^m with m = 127 - y
+// forward, y - 31 backward, and 0 where m < 0, so that the decays from row i to
+// columns j, j + 1, .. are the entries from y = kFrom - i + j on (kFrom 127 or
+// 31) and the future's are zero.  It is held four times, the copy s shifted by s
+// entries, for reads of four entries wherever a row starts; kCopy puts the
+// copies' pieces in different banks.
+constexpr int kCopy = 168;
+constexpr int kPowBytes = 4 * kCopy * 4;
+constexpr int kPow128 = 160;  // gamma^128 (copy 0)
+
 template <int D, bool STATES>
 struct Lay {
   static constexpr int kTile = C * D * 2;      // Q or K: D / 64 slabs of 128 lines of 128 bytes
@@ -53,9 +63,9 @@ struct Lay {
   static constexpr int kStages = D == 128 && !STATES ? 2 : 3;
   static constexpr int offW = kStages * kStage;            // [half][part]
   static constexpr int offS = offW + 2 * kSplit * kHalf;   // D lines of 128 bytes
-  static constexpr int offPow = offS + (STATES ? 0 : D * 128);  // gamma^m, m = 0 .. 128
-  static constexpr int offBar = offPow + 136 * 4;
-  static constexpr int kNumBars = 32;
+  static constexpr int offPow = offS + (STATES ? 0 : D * 128);
+  static constexpr int offBar = offPow + kPowBytes;
+  static constexpr int kNumBars = 34;
   static constexpr int offTmem = offBar + kNumBars * 8;
   static constexpr int kBytes = offTmem + 16;
   static_assert(kBytes <= 232448, "shared memory");
@@ -76,7 +86,10 @@ enum {
   B_OREAD = 23,    // and read
   B_DONE = 24,
   B_D = 25,        // + chunk % 2: dS is complete
-  B_DREAD = 27     // + chunk % 2: and read (without outputs; with them B_S of the next chunk says so)
+  B_DREAD = 27,    // + chunk % 2: and read
+  B_DONE2 = 30,
+  B_VREAD = 31,    // + stage: W V has been formed from V
+  B_CLEAN = 29     // tokens behind the end are out of V (at most one chunk of a segment has any)
 };
 
 // TMEM columns
@@ -98,26 +111,61 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// The warp's first lane issues; the others go along, so that the descriptors
+// stay in uniform registers.
+__device__ __forceinline__ void mma_if(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err));
+}
+
 // 16-byte piece g of line r in a 128-byte-swizzled tile
 __device__ __forceinline__ uint32_t piece(int r, int g) { return (uint32_t)(r * 128 + ((g ^ (r & 7)) << 4)); }
 
 __device__ __forceinline__ float lo16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
+constexpr int kThreads = 608;
+
 template <int D, bool STATES>
-__global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__ TcArgs ta) {
+__global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ TcArgs ta) {
   using M = Lay<D, STATES>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = (uint64_t*)(smem + M::offBar);
   uint32_t* tmem_slot = (uint32_t*)(smem + M::offTmem);
-  float* pw = (float*)(smem + M::offPow);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* tab = (float*)(smem + M::offPow);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < M::kNumBars; ++i) {
-      const bool by_warps = i == B_P || i == B_P + 1 || i == B_W || i == B_W + 1 || i == B_S || i == B_OREAD || i == B_DREAD ||
-                            i == B_DREAD + 1;
-      tc::mbar_init(&bars[i], by_warps ? 4 : 1);
+      const bool four = i == B_P || i == B_P + 1 || i == B_W || i == B_W + 1 || i == B_S || i == B_OREAD || i == B_DREAD ||
+                        i == B_DREAD + 1 || i == B_CLEAN || i >= B_VREAD;
+      const bool two = !STATES && i >= B_QKFREE && i < B_QKFREE + 3;  // both MMA warps
+      tc::mbar_init(&bars[i], four ? 4 : two ? 2 : 1);
     }
     tc::fence_barrier_init();
   }
@@ -151,7 +199,13 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
   const int updates = STATES || (op.s_out && last_seg) ? N : N - 1;
   const auto chunk_at = [&](int c) { return back ? N - 1 - c : c; };
   const auto tokens_of = [&](int c) { return min(C, n_seg - chunk_at(c) * C); };
-  if (threadIdx.x <= C) pw[threadIdx.x] = power(g, threadIdx.x);
+  // a chunk whose tile holds tokens behind the sequence's end
+  const auto ragged_at = [&](int c) { return tokens_of(c) < C && t0 + n_seg < a.L; };
+  for (int e = threadIdx.x; e < 4 * kCopy; e += kThreads) {
+    const int y = e % kCopy + e / kCopy, m = back ? y - 31 : 127 - y;
+    tab[e] = e == kPow128 ? power(g, 128) : m >= 0 ? power(g, m) : 0.f;
+  }
+  const auto pw = [&](int m) { return m == 128 ? tab[kPow128] : tab[back ? m + 31 : 127 - m]; };
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -187,96 +241,114 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
       }
     }
   } else if (warp == 17) {
-    // ------------------------------------------------------------------ MMA
-    if (lane == 0 && N > 0) {
-      constexpr uint32_t idX = tc::idesc_bf16_f32(128, 128, false, false), idO = tc::idesc_bf16_f32(128, 64, false, true),
-                         idD = tc::idesc_bf16_f32(128, 64, true, true);
+    // ----------------------------------------------------- MMA: X, Oi and Op
+    if (!STATES && N > 0) {
+      const uint32_t leader = lane == 0;
+      constexpr uint32_t idX = tc::idesc_bf16_f32(128, 128, false, false), idO = tc::idesc_bf16_f32(128, 64, false, true);
       const uint32_t s0 = tc::smem_u32(smem);
       const uint64_t qd0 = tc::smem_desc_sw128(s0, 16, 1024);
       const uint64_t kd0 = tc::smem_desc_sw128(s0 + M::kQ, 16, 1024);
-      // K^T: features along M, 64 of them to a slab (for d = 64 rows 64 .. 127 are the V tile's: not read back)
-      const uint64_t kt0 = tc::smem_desc_sw128(s0 + M::kQ, 16384, 1024);
       const uint64_t vd0 = tc::smem_desc_sw128(s0 + M::kQ + M::kTile, 16384, 1024);
-      const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, 16384, 1024);
       const uint64_t sd0 = tc::smem_desc_sw128(s0 + M::offS, 16384, 1024);
-      bool ok = true;
-      const auto scores = [&](int c) {
-        const int s = c % M::kStages;
-        if (!tc::mbar_wait(&bars[B_QK + s], (c / M::kStages) & 1, err)) return false;
+      const auto scores = [&](int c, int s, int phase) {
+        if (!wait_all(&bars[B_QK + s], phase, err)) return false;
         tc::fence_after();
+        const uint64_t qd = tc::desc_add(qd0, s * M::kStage), kd = tc::desc_add(kd0, s * M::kStage);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = s * M::kStage + (kk >> 2) * 16384 + (kk & 3) * 32;
-          tc::mma_bf16(tmem + kColX + (c & 1) * 128, tc::desc_add(qd0, off), tc::desc_add(kd0, off), idX, kk > 0);
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_if(leader, tmem + kColX + (c & 1) * 128, tc::desc_add(qd, off), tc::desc_add(kd, off), idX, kk > 0);
         }
-        tc::mma_commit(&bars[B_X + (c & 1)]);
+        commit_if(leader, &bars[B_X + (c & 1)]);
         return true;
       };
-      if (!STATES) ok = scores(0);
+      bool ok = scores(0, 0, 0);
+      int s = 0, phase = 0;
       for (int c = 0; c < N && ok; ++c) {
-        const int s = c % M::kStages;
         const uint32_t sb = s * M::kStage;
-        if (STATES && !(ok = tc::mbar_wait(&bars[B_QK + s], (c / M::kStages) & 1, err))) break;
-        // dS (its buffer was read before the state ahead of the last chunk was in place)
-        if (STATES && c >= 2 && !(ok = tc::mbar_wait(&bars[B_DREAD + (c & 1)], ((c - 2) >> 1) & 1, err))) break;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!(ok = tc::mbar_wait(&bars[B_W + hf], c & 1, err))) break;
-          if (c >= updates) continue;
+        const int s1 = s + 1 == M::kStages ? 0 : s + 1, phase1 = s1 == 0 ? phase ^ 1 : phase;
+        // the next chunk's scores, into the buffer that the last one's P has left
+        if (c + 1 < N) {
+          if (c >= 1 && !(ok = wait_all(&bars[B_O], (c - 1) & 1, err))) break;
+          if (!(ok = scores(c + 1, s1, phase1))) break;
+        }
+        if (!(ok = wait_all(&bars[B_S], c & 1, err))) break;
+        if (c >= 1 && !(ok = wait_all(&bars[B_OREAD], (c - 1) & 1, err))) break;
+        tc::fence_after();
+        const uint64_t qd = tc::desc_add(qd0, sb), vd = tc::desc_add(vd0, sb);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_if(leader, tmem + kColOi, tc::desc_add(qd, (kk >> 2) * 16384 + (kk & 3) * 32), tc::desc_add(sd0, kk * 2048), idO,
+                 kk > 0);
+        commit_if(leader, &bars[B_SREAD]);
+        commit_if(leader, &bars[B_QKFREE + s]);
+        if (ragged_at(c) && !(ok = wait_all(&bars[B_CLEAN], 0, err))) break;
+        if (!(ok = wait_all(&bars[B_V + s], phase, err))) break;
+        if (!(ok = wait_all(&bars[B_P + (c & 1)], (c >> 1) & 1, err))) break;
+        tc::fence_after();
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk)
+          mma_ts_if(leader, tmem + kColOp, tmem + kColX + (c & 1) * 128 + kk * 8, tc::desc_add(vd, kk * 2048), idO, kk > 0);
+        commit_if(leader, &bars[B_O]);
+        s = s1, phase = phase1;
+      }
+      commit_if(leader, &bars[B_DONE]);
+      wait_all(&bars[B_DONE], 0, err);
+    }
+  } else if (warp == 18) {
+    // ----------------------------------------------------------- MMA: dS
+    if (N > 0) {
+      const uint32_t leader = lane == 0;
+      constexpr uint32_t idD = tc::idesc_bf16_f32(128, 64, true, true);
+      const uint32_t s0 = tc::smem_u32(smem);
+      // K^T: features along M, 64 of them to a slab (for d = 64 rows 64 .. 127 are the V tile's: not read back)
+      const uint64_t kt0 = tc::smem_desc_sw128(s0 + M::kQ, 16384, 1024);
+      const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, 16384, 1024);
+      bool ok = true;
+      int s = 0, phase = 0;
+      for (int c = 0; c < N; ++c) {
+        if (!(ok = wait_all(&bars[B_QK + s], phase, err))) break;
+        if (c < updates) {
+          if (c >= 2 && !(ok = wait_all(&bars[B_DREAD + (c & 1)], ((c - 2) >> 1) & 1, err))) break;
+          const uint64_t kt = tc::desc_add(kt0, s * M::kStage);
+          const uint32_t d = tmem + kColD + (c & 1) * 64;
+          if (!(ok = wait_all(&bars[B_W], c & 1, err))) break;
           tc::fence_after();
 #pragma unroll
           for (int p = 0; p < kSplit; ++p)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc::mma_bf16(tmem + kColD + (c & 1) * 64, tc::desc_add(kt0, sb + hf * 8192 + kk * 2048),
-                           tc::desc_add(wd0, (hf * kSplit + p) * M::kHalf + kk * 2048), idD, hf > 0 || p > 0 || kk > 0);
-          tc::mma_commit(&bars[B_WFREE + hf]);
-        }
-        if (!ok) break;
-        if (c < updates) tc::mma_commit(&bars[B_D + (c & 1)]);
-        if (STATES) {
-          tc::mma_commit(&bars[B_QKFREE + s]);
-          continue;
-        }
-        // the next chunk's scores, into the buffer that the last one's P has left
-        if (c + 1 < N) {
-          if (c >= 1 && !(ok = tc::mbar_wait(&bars[B_O], (c - 1) & 1, err))) break;
-          if (!(ok = scores(c + 1))) break;
-        }
-        if (!(ok = tc::mbar_wait(&bars[B_S], c & 1, err))) break;
-        if (c >= 1 && !(ok = tc::mbar_wait(&bars[B_OREAD], (c - 1) & 1, err))) break;
-        tc::fence_after();
+              mma_if(leader, d, tc::desc_add(kt, kk * 2048), tc::desc_add(wd0, p * M::kHalf + kk * 2048), idD, p > 0 || kk > 0);
+          commit_if(leader, &bars[B_WFREE]);
+          if (!(ok = wait_all(&bars[B_W + 1], c & 1, err))) break;
+          tc::fence_after();
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_bf16(tmem + kColOi, tc::desc_add(qd0, sb + (kk >> 2) * 16384 + (kk & 3) * 32),
-                       tc::desc_add(sd0, kk * 2048), idO, kk > 0);
-        tc::mma_commit(&bars[B_SREAD]);
-        tc::mma_commit(&bars[B_QKFREE + s]);
-        if (!(ok = tc::mbar_wait(&bars[B_P + (c & 1)], (c >> 1) & 1, err))) break;
-        tc::fence_after();
+          for (int p = 0; p < kSplit; ++p)
 #pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk)
-          tc::mma_bf16_ts(tmem + kColOp, tmem + kColX + (c & 1) * 128 + kk * 8, tc::desc_add(vd0, sb + kk * 2048), idO,
-                          kk > 0);
-        tc::mma_commit(&bars[B_O]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_if(leader, d, tc::desc_add(kt, 8192 + kk * 2048), tc::desc_add(wd0, (kSplit + p) * M::kHalf + kk * 2048),
+                     idD, 1);
+          commit_if(leader, &bars[B_WFREE + 1]);
+          commit_if(leader, &bars[B_D + (c & 1)]);
+        }
+        commit_if(leader, &bars[B_QKFREE + s]);
+        s = s + 1 == M::kStages ? 0 : s + 1;
+        phase ^= s == 0;
       }
-      tc::mma_commit(&bars[B_DONE]);
-      tc::mbar_wait(&bars[B_DONE], 0, err);
+      commit_if(leader, &bars[B_DONE2]);
+      wait_all(&bars[B_DONE2], 0, err);
     }
   } else if (warp < 4) {
     // -------------------------------------------------------------------- P
     if (!STATES) {
       const int w = warp;
       const uint32_t lane_off = (uint32_t)(32 * w) << 16;
-      const int i = 32 * w + lane;
-      // decays along a block's 32 columns, from the end next to the diagonal
-      uint64_t cf[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        cf[j] = back ? tc::f2_pack(pw[2 * j], pw[2 * j + 1]) : tc::f2_pack(pw[31 - 2 * j], pw[30 - 2 * j]);
+      // row i's decays: entry kFrom - i + j of the table for column j
+      const int from = (back ? 31 : 127) - (32 * w + lane);
+      const float* row = tab + (from & 3) * kCopy + (from & ~3);
       for (int c = 0; c < N; ++c) {
         const int n = tokens_of(c);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[B_X + (c & 1)], (c >> 1) & 1, err))) break;
+        if (!wait_all(&bars[B_X + (c & 1)], (c >> 1) & 1, err)) break;
         tc::fence_after();
         const uint32_t tx = tmem + kColX + (c & 1) * 128 + lane_off;
 #pragma unroll 1
@@ -286,21 +358,13 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
             float s[32];
             tc::tmem_ld32(tx + 32 * blk, s);
             tc::tmem_ld_wait();
-            if (blk != w) {
-              const float rf = pw[back ? 32 * blk - i : i - 32 * blk - 31];
-              const uint64_t r2 = tc::f2_pack(rf, rf);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float p0, p1;
-                tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[2 * j], s[2 * j + 1]), tc::f2_mul(cf[j], r2)), p0, p1);
-                s[2 * j] = p0, s[2 * j + 1] = p1;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int m = back ? j - lane : lane - j;
-                s[j] = m >= 0 ? s[j] * pw[m & 31] : 0.f;
-              }
+            for (int j = 0; j < 32; j += 4) {
+              const float4 f = *(const float4*)(row + 32 * blk + j);
+              float p0, p1, p2, p3;
+              tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[j], s[j + 1]), tc::f2_pack(f.x, f.y)), p0, p1);
+              tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[j + 2], s[j + 3]), tc::f2_pack(f.z, f.w)), p2, p3);
+              s[j] = p0, s[j + 1] = p1, s[j + 2] = p2, s[j + 3] = p3;
             }
             // (scores with tokens behind the end may be anything)
             if (32 * blk + 32 > n)
@@ -324,7 +388,7 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
     // ---------------------------------------------------------------- state
     const int w = warp - 4, r = 32 * w + lane;
     const uint32_t lane_off = (uint32_t)(32 * w) << 16;
-    const bool has = r < D;  // (warp-uniform)
+    const bool has = 32 * w < D;
     float S[kWidth];
     const long long at = (long long)bh * D * D;
     if (STATES || !has) {
@@ -358,26 +422,31 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
     };
     if (!STATES) publish();
     bool ok = true;
-    const Carry whole(g, C);
+    Carry carry(g, C);
     for (int c = 0; c < updates; ++c) {
       const int n = tokens_of(c);
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[B_D + (c & 1)], (c >> 1) & 1, err)))) break;
+      if (!(ok = wait_all(&bars[B_D + (c & 1)], (c >> 1) & 1, err))) break;
       tc::fence_after();
-      const Carry carry = n == C ? whole : Carry(g, n);
+      if (n < C) carry = Carry(g, n);
+      const uint64_t m2 = tc::f2_pack(carry.m, carry.m);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float d[32];
-        tc::tmem_ld32(tmem + kColD + (c & 1) * 64 + 32 * hf + lane_off, d);
+      for (int o = 0; o < kWidth; o += 16) {
+        float d[16];
+        tc::tmem_ld16(tmem + kColD + (c & 1) * 64 + o + lane_off, d);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[32 * hf + i] = carry(S[32 * hf + i], d[i]);
+        for (int i = 0; i < 16; i += 2) {
+          const uint64_t s2 = tc::f2_pack(S[o + i], S[o + i + 1]);
+          const uint64_t f2 = carry.slow ? tc::f2_fma(s2, m2, s2) : tc::f2_mul(s2, m2);
+          tc::f2_unpack(tc::f2_add(f2, tc::f2_pack(d[i], d[i + 1])), S[o + i], S[o + i + 1]);
+        }
       }
-      if (STATES) {
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_DREAD + (c & 1)]);
-      } else if (c + 1 < N) {
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[B_SREAD], c & 1, err)))) break;
+      if (n < C) carry = Carry(g, C);  // (backward the partial chunk is the first)
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars[B_DREAD + (c & 1)]);
+      if (!STATES && c + 1 < N) {
+        if (!(ok = wait_all(&bars[B_SREAD], c & 1, err))) break;
         publish();
       }
     }
@@ -397,33 +466,43 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
       const int w = warp - 8, i = 32 * w + lane;
       const uint32_t lane_off = (uint32_t)(32 * w) << 16;
       bool ok = true;
+      int s = 0, phase = 0;
+      const uint64_t sc2 = tc::f2_pack(a.scale, a.scale);
       for (int c = 0; c < N; ++c) {
-        const int s = c % M::kStages, n = tokens_of(c);
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[B_O], c & 1, err)))) break;
+        const int n = tokens_of(c);
+        const float wi = i < n ? pw(back ? n - 1 - i : i + 1) * a.scale : 0.f;
+        const uint64_t wi2 = tc::f2_pack(wi, wi);
+        if (!(ok = wait_all(&bars[B_VREAD + s], phase, err))) break;
+        if (!(ok = wait_all(&bars[B_O], c & 1, err))) break;
         tc::fence_after();
         uint8_t* tile = smem + s * M::kStage + M::kQ + M::kTile;
-        const float wi = i < n ? pw[back ? n - 1 - i : i + 1] * a.scale : 0.f;
-        uint32_t o[32];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float oi[32], po[32];
-          tc::tmem_ld32(tmem + kColOi + 32 * hf + lane_off, oi);
-          tc::tmem_ld32(tmem + kColOp + 32 * hf + lane_off, po);
+        for (int qt = 0; qt < 4; ++qt) {
+          float oi[16], po[16];
+          tc::tmem_ld16(tmem + kColOi + 16 * qt + lane_off, oi);
+          tc::tmem_ld16(tmem + kColOp + 16 * qt + lane_off, po);
           tc::tmem_ld_wait();
-          if (hf == 1) {
+          if (qt == 3) {
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars[B_OREAD]);
           }
+          uint32_t o[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float x0 = fmaf(oi[2 * j], wi, po[2 * j] * a.scale), x1 = fmaf(oi[2 * j + 1], wi, po[2 * j + 1] * a.scale);
-            o[16 * hf + j] = i < n ? tc::pack_bf16x2(x0, x1) : 0u;
+          for (int j = 0; j < 8; ++j) {
+            float x0, x1;
+            tc::f2_unpack(tc::f2_fma(tc::f2_pack(oi[2 * j], oi[2 * j + 1]), wi2,
+                                     tc::f2_mul(tc::f2_pack(po[2 * j], po[2 * j + 1]), sc2)),
+                          x0, x1);
+            o[j] = tc::pack_bf16x2(x0, x1);
           }
-        }
+          if (i >= n)
 #pragma unroll
-        for (int gg = 0; gg < 8; ++gg)
-          *(uint4*)(tile + piece(i, gg)) = make_uint4(o[4 * gg], o[4 * gg + 1], o[4 * gg + 2], o[4 * gg + 3]);
+            for (int j = 0; j < 8; ++j) o[j] = 0u;
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg)
+            *(uint4*)(tile + piece(i, 2 * qt + gg)) = make_uint4(o[4 * gg], o[4 * gg + 1], o[4 * gg + 2], o[4 * gg + 3]);
+        }
         tc::fence_proxy_async_smem();
         tc::named_barrier(1, 128);
         if (threadIdx.x == 256) {
@@ -432,6 +511,9 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
           tc::bulk_wait_read_all();
           tc::mbar_arrive(&bars[B_VFREE + s]);
         }
+        __syncwarp();
+        s = s + 1 == M::kStages ? 0 : s + 1;
+        phase ^= s == 0;
       }
       if (threadIdx.x == 256) tc::bulk_wait_all();
       // rows behind the sequence's end
@@ -439,64 +521,72 @@ __global__ void __launch_bounds__(576, 1) scan_tc_kernel(const __grid_constant__
       for (int e = threadIdx.x - 256; e < (t1 - t0 - N * C) * (kWidth / 8); e += 128)
         *(uint4*)(o + (t0 + N * C + e / (kWidth / 8)) * op.o.t + (e % (kWidth / 8)) * 8) = make_uint4(0, 0, 0, 0);
     }
-  } else {
+  } else if (warp < 16) {
     // ------------------------------------------------------------------ W V
     const int el = threadIdx.x - 384;
     bool ok = true;
+    int s = 0, phase = 0;
     for (int c = 0; c < N && ok; ++c) {
-      const int s = c % M::kStages, n = tokens_of(c);
+      const int n = tokens_of(c);
       uint8_t* kt = smem + s * M::kStage + M::kQ;
       uint8_t* vt = kt + M::kTile;
-      // tokens behind the end that the loads have brought along are taken out of K and V
-      const bool ragged = n < C && t0 + chunk_at(c) * C + n < a.L;
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[B_V + s], (c / M::kStages) & 1, err)))) break;
-      if (ragged) {
-        // (K once its scores are complete)
+      if (!(ok = wait_all(&bars[B_V + s], phase, err))) break;
+      if (ragged_at(c)) {
+        // tokens behind the end that the loads have brought along are taken out of K (once its scores are
+        // complete) and V
         uint64_t* ready = STATES ? &bars[B_QK + s] : &bars[B_X + (c & 1)];
-        const uint32_t ph = STATES ? (c / M::kStages) & 1 : (c >> 1) & 1;
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(ready, ph, err)))) break;
+        if (!(ok = wait_all(ready, STATES ? phase : (c >> 1) & 1, err))) break;
         for (int e = el; e < (C - n) * 8; e += 128) {
           *(uint4*)(vt + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
           for (int y = 0; y < D / 64; ++y) *(uint4*)(kt + y * 16384 + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
+        tc::fence_proxy_async_smem();
         tc::named_barrier(2, 128);
+        if (lane == 0) tc::mbar_arrive(&bars[B_CLEAN]);
       }
+      if (c < updates) {
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        // (also ahead of a chunk without a sum: B_W must not run two chunks ahead of the products)
-        if (c > 0 && !(ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[B_WFREE + hf], (c - 1) & 1, err)))) break;
-        if (c < updates) {
+        for (int hf = 0; hf < 2; ++hf) {
+          if (c > 0 && !(ok = wait_all(&bars[B_WFREE + hf], (c - 1) & 1, err))) break;
           uint8_t* dst = smem + M::offW + hf * kSplit * M::kHalf;
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
             const int row = it * 16 + (el >> 3), j = 64 * hf + row, gg = el & 7;
-            const float wj = j < n ? pw[back ? j + 1 : n - 1 - j] : 0.f;
+            const float wj = j < n ? pw(back ? j + 1 : n - 1 - j) : 0.f;
+            const uint64_t w2 = tc::f2_pack(wj, wj);
             const uint4 in = *(const uint4*)(vt + piece(j, gg));
             const uint32_t u[4] = {in.x, in.y, in.z, in.w};
             uint32_t p[kSplit][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x0 = lo16(u[e]) * wj, x1 = hi16(u[e]) * wj;
+              uint64_t x2 = tc::f2_mul(tc::f2_pack(lo16(u[e]), hi16(u[e])), w2);
 #pragma unroll
               for (int y = 0; y < kSplit; ++y) {
+                float x0, x1;
+                tc::f2_unpack(x2, x0, x1);
                 const uint32_t z = tc::pack_bf16x2(x0, x1);
                 p[y][e] = z;
-                x0 -= lo16(z), x1 -= hi16(z);
+                if (y + 1 < kSplit) x2 = tc::f2_sub(x2, tc::f2_pack(lo16(z), hi16(z)));
               }
             }
 #pragma unroll
             for (int y = 0; y < kSplit; ++y)
               *(uint4*)(dst + y * M::kHalf + piece(row, gg)) = make_uint4(p[y][0], p[y][1], p[y][2], p[y][3]);
           }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars[B_W + hf]);
         }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_W + hf]);
       }
-      if (STATES && ok) {
+      if (STATES) {
         tc::named_barrier(2, 128);
         if (el == 0) tc::mbar_arrive(&bars[B_VFREE + s]);
+      } else {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[B_VREAD + s]);
       }
+      s = s + 1 == M::kStages ? 0 : s + 1;
+      phase ^= s == 0;
     }
   }
   tc::fence_before();
@@ -546,7 +636,7 @@ cudaError_t launch(const TcArgs& ta, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const Args& a = ta.a;
   const long long grid = (long long)(a.last_op - a.first_op) * a.B * a.H * (D / kWidth) * (STATES ? a.segs - 1 : a.segs);
-  return after(kern, (unsigned)grid, dim3(576), smem, st, 0, ta);
+  return after(kern, (unsigned)grid, dim3(kThreads), smem, st, 0, ta);
 }
 
 }  // namespace
