@@ -14,9 +14,8 @@
 // summed from exact products and the state is as good as an fp32 recurrence;
 // P and the copy of S are rounded to bf16, half a step like the output's own.
 //
-// Roles (608 threads): warps 0-3 P, warps 4-7 state, warps 8-11 output, warps
-// 12-15 W V, warp 16 TMA producer, warps 17 (X, Oi, Op; owner of TMEM) and 18
-// (dS) MMA issuers.  The output takes the place of the chunk's V tile on its way out (TMA store).
+// Roles: four warps for P, four for the state, four for the output, eight for
+// W V, one for the loads, two that issue MMAs (X, Oi, Op; dS).  The output takes the place of the chunk's V tile on its way out (TMA store).
 // Every wait is bounded (tc::kWaitLimitNs); an expired one sets g_expired.
 #include <cmath>
 #include <mutex>
@@ -72,31 +71,35 @@ struct Lay {
 };
 
 enum {
-  B_QK = 0,        // + stage: Q and K have landed
-  B_V = 3,         // + stage: V has landed
-  B_QKFREE = 6,    // + stage
-  B_VFREE = 9,     // + stage
-  B_X = 12,        // + chunk % 2: X is complete
-  B_P = 14,        // + chunk % 2: P is in place
-  B_W = 16,        // + half: W V is in place
-  B_WFREE = 18,    // + half: its product with K is complete
-  B_S = 20,        // the state ahead of the chunk is in place
-  B_SREAD = 21,    // its product with Q is complete
-  B_O = 22,        // Oi and Op are complete
-  B_OREAD = 23,    // and read
-  B_DONE = 24,
-  B_D = 25,        // + chunk % 2: dS is complete
-  B_DREAD = 27,    // + chunk % 2: and read
-  B_DONE2 = 30,
-  B_VREAD = 31,    // + stage: W V has been formed from V
-  B_CLEAN = 29     // tokens behind the end are out of V (at most one chunk of a segment has any)
+  B_QK = 0,      // + stage: Q and K have landed
+  B_V = 3,       // + stage: V has landed
+  B_QKFREE = 6,  // + stage
+  B_VFREE = 9,   // + stage
+  B_VREAD = 12,  // + stage: W V has been formed from V
+  B_W = 15,      // + half: W V is in place
+  B_WFREE = 17,  // + half: its product with K is complete
+  B_X = 19,      // X is complete
+  B_XREAD = 20,  // and read
+  B_P = 21,      // P is in place
+  B_S = 22,      // the state ahead of the chunk is in place
+  B_SREAD = 23,  // its product with Q is complete
+  B_O = 24,      // Oi and Op are complete
+  B_OREAD = 25,  // and read
+  B_D = 26,      // dS is complete
+  B_DREAD = 27,  // and read
+  // of the chunk that holds tokens behind the end (at most one of a segment): its scores have been read; the tokens
+  // are out of K and V
+  B_RAGGED = 28,
+  B_CLEAN = 29,
+  B_DONE = 30,   // + MMA warp
 };
 
 // TMEM columns
-constexpr uint32_t kColX = 0;     // two X / P buffers of 128
-constexpr uint32_t kColOi = 256;  // 64
-constexpr uint32_t kColOp = 320;  // 64
-constexpr uint32_t kColD = 384;   // two dS buffers of 64
+constexpr uint32_t kColX = 0;     // 128
+constexpr uint32_t kColP = 128;   // 64: two bf16 to a column
+constexpr uint32_t kColOi = 192;  // 64
+constexpr uint32_t kColOp = 256;  // 64
+constexpr uint32_t kColD = 320;   // 64 for each part of W V
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int t, int h, int b, uint64_t* bar) {
   asm volatile(
@@ -149,7 +152,18 @@ __device__ __forceinline__ uint32_t piece(int r, int g) { return (uint32_t)(r * 
 __device__ __forceinline__ float lo16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-constexpr int kThreads = 608;
+// Warps of each role; the four of a warpgroup share a register budget (the
+// launch's 80 a thread are dealt out anew).
+constexpr int kThreads = 768;
+constexpr int kP = 0, kState = 4, kOut = 8, kW = 12, kLoad = 20, kMma = 21, kMmaD = 22;
+template <int R>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 
 template <int D, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ TcArgs ta) {
@@ -162,14 +176,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < M::kNumBars; ++i) {
-      const bool four = i == B_P || i == B_P + 1 || i == B_W || i == B_W + 1 || i == B_S || i == B_OREAD || i == B_DREAD ||
-                        i == B_DREAD + 1 || i == B_CLEAN || i >= B_VREAD;
-      const bool two = !STATES && i >= B_QKFREE && i < B_QKFREE + 3;  // both MMA warps
-      tc::mbar_init(&bars[i], four ? 4 : two ? 2 : 1);
+      const bool four = i == B_W || i == B_W + 1 || i == B_XREAD || i == B_P || i == B_S || i == B_OREAD || i == B_DREAD ||
+                        i == B_RAGGED;                                 // the warps of a role
+      const bool eight = i == B_CLEAN || (i >= B_VREAD && i < B_VREAD + 3);  // both W V groups'
+      const bool two = !STATES && i >= B_QKFREE && i < B_QKFREE + 3;   // both MMA warps
+      tc::mbar_init(&bars[i], eight ? 8 : four ? 4 : two ? 2 : 1);
     }
     tc::fence_barrier_init();
   }
-  if (warp == 17) {
+  if (warp == kMma) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
@@ -212,9 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
   const uint32_t tmem = *tmem_slot;
   int* err = &g_expired;
 
-  if (warp == 16) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0) {
+  if (warp >= kLoad) {
+    registers_down<40>();
+    if (warp == kLoad && lane == 0) {
+      // ----------------------------------------------------------- producer
       bool ok = true;
       int qk = 0, v = 0;
       for (int c = 0; c < N; ++c) {
@@ -224,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (!(ok = tc::mbar_wait(&bars[B_QKFREE + s], ph, err))) break;
         tc::mbar_arrive_expect_tx(&bars[B_QK + s], M::kQ + M::kTile);
         for (int y = 0; y < D / 64; ++y) {
-          if (!STATES) tma_load_4d(st + y * 16384, &maps.q, 64 * y, t, h, b, &bars[B_QK + s]);
           tma_load_4d(st + M::kQ + y * 16384, &maps.k, 64 * y, t, h, b, &bars[B_QK + s]);
+          if (!STATES) tma_load_4d(st + y * 16384, &maps.q, 64 * y, t, h, b, &bars[B_QK + s]);
         }
         ++qk;
         if (!(ok = tc::mbar_wait(&bars[B_VFREE + s], ph, err))) break;
@@ -239,10 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (nq > 0) tc::mbar_wait(&bars[B_QK + s], (nq - 1) & 1, nullptr);
         if (nv > 0) tc::mbar_wait(&bars[B_V + s], (nv - 1) & 1, nullptr);
       }
-    }
-  } else if (warp == 17) {
-    // ----------------------------------------------------- MMA: X, Oi and Op
-    if (!STATES && N > 0) {
+    } else if (!STATES && warp == kMma && N > 0) {
+      // --------------------------------------------------- MMA: X, Oi and Op
       const uint32_t leader = lane == 0;
       constexpr uint32_t idX = tc::idesc_bf16_f32(128, 128, false, false), idO = tc::idesc_bf16_f32(128, 64, false, true);
       const uint32_t s0 = tc::smem_u32(smem);
@@ -250,28 +264,23 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       const uint64_t kd0 = tc::smem_desc_sw128(s0 + M::kQ, 16, 1024);
       const uint64_t vd0 = tc::smem_desc_sw128(s0 + M::kQ + M::kTile, 16384, 1024);
       const uint64_t sd0 = tc::smem_desc_sw128(s0 + M::offS, 16384, 1024);
-      const auto scores = [&](int c, int s, int phase) {
+      const auto scores = [&](int s, int phase) {
         if (!wait_all(&bars[B_QK + s], phase, err)) return false;
         tc::fence_after();
         const uint64_t qd = tc::desc_add(qd0, s * M::kStage), kd = tc::desc_add(kd0, s * M::kStage);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_if(leader, tmem + kColX + (c & 1) * 128, tc::desc_add(qd, off), tc::desc_add(kd, off), idX, kk > 0);
+          mma_if(leader, tmem + kColX, tc::desc_add(qd, off), tc::desc_add(kd, off), idX, kk > 0);
         }
-        commit_if(leader, &bars[B_X + (c & 1)]);
+        commit_if(leader, &bars[B_X]);
         return true;
       };
-      bool ok = scores(0, 0, 0);
+      bool ok = scores(0, 0);
       int s = 0, phase = 0;
       for (int c = 0; c < N && ok; ++c) {
         const uint32_t sb = s * M::kStage;
         const int s1 = s + 1 == M::kStages ? 0 : s + 1, phase1 = s1 == 0 ? phase ^ 1 : phase;
-        // the next chunk's scores, into the buffer that the last one's P has left
-        if (c + 1 < N) {
-          if (c >= 1 && !(ok = wait_all(&bars[B_O], (c - 1) & 1, err))) break;
-          if (!(ok = scores(c + 1, s1, phase1))) break;
-        }
         if (!(ok = wait_all(&bars[B_S], c & 1, err))) break;
         if (c >= 1 && !(ok = wait_all(&bars[B_OREAD], (c - 1) & 1, err))) break;
         tc::fence_after();
@@ -282,129 +291,144 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                  kk > 0);
         commit_if(leader, &bars[B_SREAD]);
         commit_if(leader, &bars[B_QKFREE + s]);
+        // the next chunk's scores as soon as the last one's have been read
+        if (c + 1 < N) {
+          if (!(ok = wait_all(&bars[B_XREAD], c & 1, err))) break;
+          if (!(ok = scores(s1, phase1))) break;
+        }
         if (ragged_at(c) && !(ok = wait_all(&bars[B_CLEAN], 0, err))) break;
         if (!(ok = wait_all(&bars[B_V + s], phase, err))) break;
-        if (!(ok = wait_all(&bars[B_P + (c & 1)], (c >> 1) & 1, err))) break;
+        if (!(ok = wait_all(&bars[B_P], c & 1, err))) break;
         tc::fence_after();
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-          mma_ts_if(leader, tmem + kColOp, tmem + kColX + (c & 1) * 128 + kk * 8, tc::desc_add(vd, kk * 2048), idO, kk > 0);
+          mma_ts_if(leader, tmem + kColOp, tmem + kColP + kk * 8, tc::desc_add(vd, kk * 2048), idO, kk > 0);
         commit_if(leader, &bars[B_O]);
         s = s1, phase = phase1;
       }
       commit_if(leader, &bars[B_DONE]);
       wait_all(&bars[B_DONE], 0, err);
-    }
-  } else if (warp == 18) {
-    // ----------------------------------------------------------- MMA: dS
-    if (N > 0) {
+    } else if (warp == kMmaD && N > 0) {
+      // --------------------------------------------------------- MMA: dS
       const uint32_t leader = lane == 0;
-      constexpr uint32_t idD = tc::idesc_bf16_f32(128, 64, true, true);
+      constexpr uint32_t idD = tc::idesc_bf16_f32(128, 64 * kSplit, true, true);
       const uint32_t s0 = tc::smem_u32(smem);
-      // K^T: features along M, 64 of them to a slab (for d = 64 rows 64 .. 127 are the V tile's: not read back)
+      // K^T: features along M, 64 of them to a slab (for d = 64 rows 64 .. 127 are the V tile's: not read back);
+      // the parts of W V side by side along N
       const uint64_t kt0 = tc::smem_desc_sw128(s0 + M::kQ, 16384, 1024);
-      const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, 16384, 1024);
+      const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, M::kHalf, 1024);
       bool ok = true;
       int s = 0, phase = 0;
       for (int c = 0; c < N; ++c) {
         if (!(ok = wait_all(&bars[B_QK + s], phase, err))) break;
         if (c < updates) {
-          if (c >= 2 && !(ok = wait_all(&bars[B_DREAD + (c & 1)], ((c - 2) >> 1) & 1, err))) break;
+          if (c >= 1 && !(ok = wait_all(&bars[B_DREAD], (c - 1) & 1, err))) break;
           const uint64_t kt = tc::desc_add(kt0, s * M::kStage);
-          const uint32_t d = tmem + kColD + (c & 1) * 64;
           if (!(ok = wait_all(&bars[B_W], c & 1, err))) break;
           tc::fence_after();
 #pragma unroll
-          for (int p = 0; p < kSplit; ++p)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_if(leader, d, tc::desc_add(kt, kk * 2048), tc::desc_add(wd0, p * M::kHalf + kk * 2048), idD, p > 0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_if(leader, tmem + kColD, tc::desc_add(kt, kk * 2048), tc::desc_add(wd0, kk * 2048), idD, kk > 0);
           commit_if(leader, &bars[B_WFREE]);
           if (!(ok = wait_all(&bars[B_W + 1], c & 1, err))) break;
           tc::fence_after();
 #pragma unroll
-          for (int p = 0; p < kSplit; ++p)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_if(leader, d, tc::desc_add(kt, 8192 + kk * 2048), tc::desc_add(wd0, (kSplit + p) * M::kHalf + kk * 2048),
-                     idD, 1);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_if(leader, tmem + kColD, tc::desc_add(kt, 8192 + kk * 2048),
+                   tc::desc_add(wd0, kSplit * M::kHalf + kk * 2048), idD, 1);
           commit_if(leader, &bars[B_WFREE + 1]);
-          commit_if(leader, &bars[B_D + (c & 1)]);
+          commit_if(leader, &bars[B_D]);
         }
         commit_if(leader, &bars[B_QKFREE + s]);
         s = s + 1 == M::kStages ? 0 : s + 1;
         phase ^= s == 0;
       }
-      commit_if(leader, &bars[B_DONE2]);
-      wait_all(&bars[B_DONE2], 0, err);
+      commit_if(leader, &bars[B_DONE + 1]);
+      wait_all(&bars[B_DONE + 1], 0, err);
     }
-  } else if (warp < 4) {
+  } else if (warp < kState) {
     // -------------------------------------------------------------------- P
     if (!STATES) {
       const int w = warp;
       const uint32_t lane_off = (uint32_t)(32 * w) << 16;
+      const uint32_t tx = tmem + kColX + lane_off, tp = tmem + kColP + lane_off;
       // row i's decays: entry kFrom - i + j of the table for column j
       const int from = (back ? 31 : 127) - (32 * w + lane);
       const float* row = tab + (from & 3) * kCopy + (from & ~3);
+      uint32_t pk[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) pk[j] = 0u;
+      // blocks of 32 columns on the far side of the diagonal stay zero
+      for (int blk = 0; blk < 4; ++blk)
+        if (back ? blk < w : blk > w) tc::tmem_st16u(tp + 16 * blk, pk);
+      const int first = back ? w : 0, last = back ? 3 : w;
       for (int c = 0; c < N; ++c) {
         const int n = tokens_of(c);
-        if (!wait_all(&bars[B_X + (c & 1)], (c >> 1) & 1, err)) break;
+        if (!wait_all(&bars[B_X], c & 1, err)) break;
         tc::fence_after();
-        const uint32_t tx = tmem + kColX + (c & 1) * 128 + lane_off;
 #pragma unroll 1
-        for (int blk = 0; blk < 4; ++blk) {
-          uint32_t pk[16];
-          if ((back ? blk >= w : blk <= w) && 32 * blk < n) {
-            float s[32];
-            tc::tmem_ld32(tx + 32 * blk, s);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 f = *(const float4*)(row + 32 * blk + j);
-              float p0, p1, p2, p3;
-              tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[j], s[j + 1]), tc::f2_pack(f.x, f.y)), p0, p1);
-              tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[j + 2], s[j + 3]), tc::f2_pack(f.z, f.w)), p2, p3);
-              s[j] = p0, s[j + 1] = p1, s[j + 2] = p2, s[j + 3] = p3;
+        for (int blk = first; blk <= last; ++blk) {
+          float s[32];
+          tc::tmem_ld32(tx + 32 * blk, s);
+          tc::tmem_ld_wait();
+          if (blk == last) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              tc::mbar_arrive(&bars[B_XREAD]);
+              if (ragged_at(c)) tc::mbar_arrive(&bars[B_RAGGED]);
             }
-            // (scores with tokens behind the end may be anything)
-            if (32 * blk + 32 > n)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[j] = 32 * blk + j < n ? s[j] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = tc::pack_bf16x2(s[2 * j], s[2 * j + 1]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = 0u;
           }
-          tc::tmem_st16u(tx + 16 * blk, pk);  // over columns of X that have been read
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 f = *(const float4*)(row + 32 * blk + j);
+            float p0, p1, p2, p3;
+            tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[j], s[j + 1]), tc::f2_pack(f.x, f.y)), p0, p1);
+            tc::f2_unpack(tc::f2_mul(tc::f2_pack(s[j + 2], s[j + 3]), tc::f2_pack(f.z, f.w)), p2, p3);
+            s[j] = p0, s[j + 1] = p1, s[j + 2] = p2, s[j + 3] = p3;
+          }
+          // (scores with tokens behind the end may be anything)
+          if (32 * blk + 32 > n)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = 32 * blk + j < n ? s[j] : 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = tc::pack_bf16x2(s[2 * j], s[2 * j + 1]);
+          if (blk == first && c > 0) {  // the last chunk's P has been used
+            if (!wait_all(&bars[B_O], (c - 1) & 1, err)) {
+              c = N;
+              break;
+            }
+            tc::fence_after();
+          }
+          tc::tmem_st16u(tp + 16 * blk, pk);
         }
+        if (c == N) break;
         tc::tmem_st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_P + (c & 1)]);
+        if (lane == 0) tc::mbar_arrive(&bars[B_P]);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < kOut) {
     // ---------------------------------------------------------------- state
-    const int w = warp - 4, r = 32 * w + lane;
+    registers_up<152>();
+    const int w = warp - kState, r = 32 * w + lane;
     const uint32_t lane_off = (uint32_t)(32 * w) << 16;
     const bool has = 32 * w < D;
     float S[kWidth];
-    const long long at = (long long)bh * D * D;
-    if (STATES || !has) {
+    // entry (r, column i) of a state: p[i * st]
+    const auto column0 = [&](long long base, long long s_r, long long s_c) {
+      return base + r * s_r + slice * kWidth * s_c;
+    };
 #pragma unroll
-      for (int i = 0; i < kWidth; ++i) S[i] = 0.f;
-    } else if (a.segs > 1) {
-      const float* p = op.part + ((long long)bh * a.segs + seg) * D * D;
+    for (int i = 0; i < kWidth; ++i) S[i] = 0.f;
+    if (!STATES && has && (a.segs > 1 || op.s_in)) {
+      const bool cut = a.segs > 1;
+      const long long s_r = cut ? (op.part_t ? D : 1) : op.s_r, s_c = cut ? (op.part_t ? 1 : D) : op.s_c;
+      const float* p = (cut ? op.part : op.s_in) + column0((cut ? (long long)bh * a.segs + seg : bh) * D * D, s_r, s_c);
+      const float by = cut ? 1.f : op.in_scale;
 #pragma unroll
-      for (int i = 0; i < kWidth; ++i) {
-        const int col = slice * kWidth + i;
-        S[i] = p[op.part_t ? r * D + col : col * D + r];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWidth; ++i)
-        S[i] = op.s_in ? op.s_in[at + r * op.s_r + (slice * kWidth + i) * op.s_c] * op.in_scale : 0.f;
+      for (int i = 0; i < kWidth; ++i, p += s_c) S[i] = *p * by;
     }
     const auto publish = [&]() {  // the bf16 copy that the queries meet
       if (has) {
@@ -422,49 +446,60 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     };
     if (!STATES) publish();
     bool ok = true;
-    Carry carry(g, C);
     for (int c = 0; c < updates; ++c) {
-      const int n = tokens_of(c);
-      if (!(ok = wait_all(&bars[B_D + (c & 1)], (c >> 1) & 1, err))) break;
-      tc::fence_after();
-      if (n < C) carry = Carry(g, n);
+      const Carry carry(g, tokens_of(c));
+      // the sum of the old state's part and dS's: gamma^n S first, while dS is on its way
       const uint64_t m2 = tc::f2_pack(carry.m, carry.m);
+      if (carry.slow) {
+#pragma unroll
+        for (int i = 0; i < kWidth; i += 2) {
+          const uint64_t s2 = tc::f2_pack(S[i], S[i + 1]);
+          tc::f2_unpack(tc::f2_fma(s2, m2, s2), S[i], S[i + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWidth; i += 2)
+          tc::f2_unpack(tc::f2_mul(tc::f2_pack(S[i], S[i + 1]), m2), S[i], S[i + 1]);
+      }
+      if (!(ok = wait_all(&bars[B_D], c & 1, err))) break;
+      tc::fence_after();
 #pragma unroll
       for (int o = 0; o < kWidth; o += 16) {
-        float d[16];
-        tc::tmem_ld16(tmem + kColD + (c & 1) * 64 + o + lane_off, d);
+        float d[kSplit][16];
+#pragma unroll
+        for (int p = 0; p < kSplit; ++p) tc::tmem_ld16(tmem + kColD + 64 * p + o + lane_off, d[p]);
         tc::tmem_ld_wait();
+        if (o + 16 == kWidth) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars[B_DREAD]);
+        }
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const uint64_t s2 = tc::f2_pack(S[o + i], S[o + i + 1]);
-          const uint64_t f2 = carry.slow ? tc::f2_fma(s2, m2, s2) : tc::f2_mul(s2, m2);
-          tc::f2_unpack(tc::f2_add(f2, tc::f2_pack(d[i], d[i + 1])), S[o + i], S[o + i + 1]);
+          uint64_t x2 = tc::f2_pack(d[kSplit - 1][i], d[kSplit - 1][i + 1]);
+#pragma unroll
+          for (int p = kSplit - 2; p >= 0; --p) x2 = tc::f2_add(x2, tc::f2_pack(d[p][i], d[p][i + 1]));
+          tc::f2_unpack(tc::f2_add(tc::f2_pack(S[o + i], S[o + i + 1]), x2), S[o + i], S[o + i + 1]);
         }
       }
-      if (n < C) carry = Carry(g, C);  // (backward the partial chunk is the first)
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars[B_DREAD + (c & 1)]);
       if (!STATES && c + 1 < N) {
         if (!(ok = wait_all(&bars[B_SREAD], c & 1, err))) break;
         publish();
       }
     }
-    if (ok && has) {
-      if (STATES) {
-        float* p = op.part + ((long long)bh * a.segs + (back ? seg - 1 : seg + 1)) * D * D;
+    if (ok && has && (STATES || (op.s_out && last_seg))) {
+      float* p = STATES ? op.part + column0(((long long)bh * a.segs + (back ? seg - 1 : seg + 1)) * D * D, 1, D)
+                        : op.s_out + column0((long long)bh * D * D, op.s_r, op.s_c);
+      const long long s_c = STATES ? D : op.s_c;
 #pragma unroll
-        for (int i = 0; i < kWidth; ++i) p[(slice * kWidth + i) * D + r] = S[i];
-      } else if (op.s_out && last_seg) {
-#pragma unroll
-        for (int i = 0; i < kWidth; ++i) op.s_out[at + r * op.s_r + (slice * kWidth + i) * op.s_c] = S[i] * op.out_scale;
-      }
+      for (int i = 0; i < kWidth; ++i, p += s_c) *p = STATES ? S[i] : S[i] * op.out_scale;
     }
-  } else if (warp < 12) {
+  } else if (warp < kW) {
     // --------------------------------------------------------------- output
+    registers_down<72>();
     if (!STATES) {
-      const int w = warp - 8, i = 32 * w + lane;
-      const uint32_t lane_off = (uint32_t)(32 * w) << 16;
+      const int el = threadIdx.x - 32 * kOut, i = el;
+      const uint32_t lane_off = (uint32_t)(el & 96) << 16;
       bool ok = true;
       int s = 0, phase = 0;
       const uint64_t sc2 = tc::f2_pack(a.scale, a.scale);
@@ -505,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
         tc::fence_proxy_async_smem();
         tc::named_barrier(1, 128);
-        if (threadIdx.x == 256) {
+        if (el == 0) {
           tma_store_4d(&maps.o, tile, kWidth * slice, t0 + chunk_at(c) * C, h, b);
           tc::bulk_commit();
           tc::bulk_wait_read_all();
@@ -515,15 +550,16 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         s = s + 1 == M::kStages ? 0 : s + 1;
         phase ^= s == 0;
       }
-      if (threadIdx.x == 256) tc::bulk_wait_all();
+      if (el == 0) tc::bulk_wait_all();
       // rows behind the sequence's end
       __nv_bfloat16* o = (__nv_bfloat16*)op.o.p + b * op.o.b + h * op.o.h + slice * kWidth;
-      for (int e = threadIdx.x - 256; e < (t1 - t0 - N * C) * (kWidth / 8); e += 128)
+      for (int e = el; e < (t1 - t0 - N * C) * (kWidth / 8); e += 128)
         *(uint4*)(o + (t0 + N * C + e / (kWidth / 8)) * op.o.t + (e % (kWidth / 8)) * 8) = make_uint4(0, 0, 0, 0);
     }
-  } else if (warp < 16) {
-    // ------------------------------------------------------------------ W V
-    const int el = threadIdx.x - 384;
+  } else {
+    // ---------------------------------------- W V, a warpgroup to each half
+    registers_down<64>();
+    const int el = threadIdx.x - 32 * kW, hf = el >> 7, e0 = el & 127;
     bool ok = true;
     int s = 0, phase = 0;
     for (int c = 0; c < N && ok; ++c) {
@@ -532,58 +568,53 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       uint8_t* vt = kt + M::kTile;
       if (!(ok = wait_all(&bars[B_V + s], phase, err))) break;
       if (ragged_at(c)) {
-        // tokens behind the end that the loads have brought along are taken out of K (once its scores are
-        // complete) and V
-        uint64_t* ready = STATES ? &bars[B_QK + s] : &bars[B_X + (c & 1)];
-        if (!(ok = wait_all(ready, STATES ? phase : (c >> 1) & 1, err))) break;
-        for (int e = el; e < (C - n) * 8; e += 128) {
+        // tokens behind the end that the loads have brought along are taken out of K (once its scores have been
+        // read) and V
+        if (!(ok = STATES ? wait_all(&bars[B_QK + s], phase, err) : wait_all(&bars[B_RAGGED], 0, err))) break;
+        for (int e = el; e < (C - n) * 8; e += 256) {
           *(uint4*)(vt + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
           for (int y = 0; y < D / 64; ++y) *(uint4*)(kt + y * 16384 + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
         tc::fence_proxy_async_smem();
-        tc::named_barrier(2, 128);
+        tc::named_barrier(2, 256);
         if (lane == 0) tc::mbar_arrive(&bars[B_CLEAN]);
       }
       if (c < updates) {
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          if (c > 0 && !(ok = wait_all(&bars[B_WFREE + hf], (c - 1) & 1, err))) break;
-          uint8_t* dst = smem + M::offW + hf * kSplit * M::kHalf;
+        if (c > 0 && !(ok = wait_all(&bars[B_WFREE + hf], (c - 1) & 1, err))) break;
+        uint8_t* dst = smem + M::offW + hf * kSplit * M::kHalf;
+#pragma unroll 2
+        for (int it = 0; it < 4; ++it) {
+          const int row = it * 16 + (e0 >> 3), j = 64 * hf + row, gg = e0 & 7;
+          const float wj = j < n ? pw(back ? j + 1 : n - 1 - j) : 0.f;
+          const uint64_t w2 = tc::f2_pack(wj, wj);
+          const uint4 in = *(const uint4*)(vt + piece(j, gg));
+          const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+          uint32_t p[kSplit][4];
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int row = it * 16 + (el >> 3), j = 64 * hf + row, gg = el & 7;
-            const float wj = j < n ? pw(back ? j + 1 : n - 1 - j) : 0.f;
-            const uint64_t w2 = tc::f2_pack(wj, wj);
-            const uint4 in = *(const uint4*)(vt + piece(j, gg));
-            const uint32_t u[4] = {in.x, in.y, in.z, in.w};
-            uint32_t p[kSplit][4];
+          for (int e = 0; e < 4; ++e) {
+            uint64_t x2 = tc::f2_mul(tc::f2_pack(lo16(u[e]), hi16(u[e])), w2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint64_t x2 = tc::f2_mul(tc::f2_pack(lo16(u[e]), hi16(u[e])), w2);
-#pragma unroll
-              for (int y = 0; y < kSplit; ++y) {
-                float x0, x1;
-                tc::f2_unpack(x2, x0, x1);
-                const uint32_t z = tc::pack_bf16x2(x0, x1);
-                p[y][e] = z;
-                if (y + 1 < kSplit) x2 = tc::f2_sub(x2, tc::f2_pack(lo16(z), hi16(z)));
-              }
+            for (int y = 0; y < kSplit; ++y) {
+              float x0, x1;
+              tc::f2_unpack(x2, x0, x1);
+              const uint32_t z = tc::pack_bf16x2(x0, x1);
+              p[y][e] = z;
+              if (y + 1 < kSplit) x2 = tc::f2_sub(x2, tc::f2_pack(lo16(z), hi16(z)));
             }
-#pragma unroll
-            for (int y = 0; y < kSplit; ++y)
-              *(uint4*)(dst + y * M::kHalf + piece(row, gg)) = make_uint4(p[y][0], p[y][1], p[y][2], p[y][3]);
           }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bars[B_W + hf]);
+#pragma unroll
+          for (int y = 0; y < kSplit; ++y)
+            *(uint4*)(dst + y * M::kHalf + piece(row, gg)) = make_uint4(p[y][0], p[y][1], p[y][2], p[y][3]);
         }
-      }
-      if (STATES) {
-        tc::named_barrier(2, 128);
-        if (el == 0) tc::mbar_arrive(&bars[B_VFREE + s]);
-      } else {
+        tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_VREAD + s]);
+        if (lane == 0) tc::mbar_arrive(&bars[B_W + hf]);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars[B_VREAD + s]);
+      if (STATES) {
+        if (!(ok = wait_all(&bars[B_VREAD + s], phase, err))) break;
+        if (el == 0) tc::mbar_arrive(&bars[B_VFREE + s]);
       }
       s = s + 1 == M::kStages ? 0 : s + 1;
       phase ^= s == 0;
@@ -591,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == kMma) {
     tc::fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
