@@ -5,17 +5,19 @@
 // head) and 64 of the state's columns.  Per chunk, with Q, K, V its tiles, W
 // the tokens' weights gamma^(n - 1 - j + e), all rows in memory order:
 //   X  = Q K^T                    (128 x 128, K = d)
-//   P  = X * gamma^|i - j| on the past side, bf16 in place of X in TMEM
+//   P  = X * gamma^|i - j| on the past side, bf16, in TMEM
 //   Oi = Q S, Op = P V            (128 x 64)
 //   o  = scale (Op + gamma^(..) Oi)
 //   dS = K^T (W V)                (d x 64, K = 128), a fresh sum every chunk
 //   S  <- gamma^n S + dS          (fp32, in registers; its bf16 copy feeds Oi)
-// W V goes in as three bf16 numbers (their sum is its fp32 value), so dS is
-// summed from exact products and the state is as good as an fp32 recurrence;
-// P and the copy of S are rounded to bf16, half a step like the output's own.
+// W V goes in as three bf16 numbers whose sum is its fp32 value, so dS is
+// summed from exact products and a state that is given out is as good as an
+// fp32 recurrence's (two numbers, 2^-16, where it is not); P and the copy of S
+// that meets the queries are rounded to bf16, half a step each like the
+// output's own.
 //
 // Roles: four warps for P, four for the state, four for the output, eight for
-// W V, one for the loads, two that issue MMAs (X, Oi, Op; dS).  The output takes the place of the chunk's V tile on its way out (TMA store).
+// W V, one for the loads, two that issue MMAs (X, Oi, Op; dS).
 // Every wait is bounded (tc::kWaitLimitNs); an expired one sets g_expired.
 #include <cmath>
 #include <mutex>
@@ -32,8 +34,6 @@ namespace {
 __device__ int g_expired;  // a wait of a kernel of this file gave up (nats_decay_attn_check)
 
 constexpr int C = 128;
-constexpr int kSplit = 3;  // bf16 numbers that make up an fp32 one
-
 struct Maps {
   CUtensorMap q, k, v, o;
 };
@@ -52,19 +52,24 @@ constexpr int kCopy = 168;
 constexpr int kPowBytes = 4 * kCopy * 4;
 constexpr int kPow128 = 160;  // gamma^128 (copy 0)
 
-template <int D, bool STATES>
+// Shared memory.  PARTS: the bf16 numbers that make up an entry of W V.
+template <int D, bool STATES, int PARTS>
 struct Lay {
   static constexpr int kTile = C * D * 2;      // Q or K: D / 64 slabs of 128 lines of 128 bytes
   static constexpr int kV = C * kWidth * 2;    // 16 KiB
   static constexpr int kQ = STATES ? 0 : kTile;
   static constexpr int kStage = kQ + kTile + kV;
-  static constexpr int kHalf = 64 * kWidth * 2;  // 64 tokens of one part of W V
   static constexpr int kStages = D == 128 && !STATES ? 2 : 3;
-  static constexpr int offW = kStages * kStage;            // [half][part]
-  static constexpr int offS = offW + 2 * kSplit * kHalf;   // D lines of 128 bytes
-  static constexpr int offPow = offS + (STATES ? 0 : D * 128);
+  // tokens of W V that are held of each half of a chunk: all, or half of them at a time where there is no room
+  static constexpr int kStep = D == 128 && !STATES && PARTS == 3 ? 32 : 64;
+  static constexpr int kSteps = 64 / kStep;
+  static constexpr int kPart = kStep * kWidth * 2;
+  static constexpr int offW = kStages * kStage;               // [half][part]
+  static constexpr int offS = offW + 2 * PARTS * kPart;       // D lines of 128 bytes
+  static constexpr int offO = offS + (STATES ? 0 : D * 128);  // the output's tile
+  static constexpr int offPow = offO + (STATES ? 0 : kV);
   static constexpr int offBar = offPow + kPowBytes;
-  static constexpr int kNumBars = 34;
+  static constexpr int kNumBars = 32;
   static constexpr int offTmem = offBar + kNumBars * 8;
   static constexpr int kBytes = offTmem + 16;
   static_assert(kBytes <= 232448, "shared memory");
@@ -75,7 +80,6 @@ enum {
   B_V = 3,       // + stage: V has landed
   B_QKFREE = 6,  // + stage
   B_VFREE = 9,   // + stage
-  B_VREAD = 12,  // + stage: W V has been formed from V
   B_W = 15,      // + half: W V is in place
   B_WFREE = 17,  // + half: its product with K is complete
   B_X = 19,      // X is complete
@@ -165,9 +169,9 @@ __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-template <int D, bool STATES>
+template <int D, bool STATES, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ TcArgs ta) {
-  using M = Lay<D, STATES>;
+  using M = Lay<D, STATES, PARTS>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = (uint64_t*)(smem + M::offBar);
   uint32_t* tmem_slot = (uint32_t*)(smem + M::offTmem);
@@ -178,9 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     for (int i = 0; i < M::kNumBars; ++i) {
       const bool four = i == B_W || i == B_W + 1 || i == B_XREAD || i == B_P || i == B_S || i == B_OREAD || i == B_DREAD ||
                         i == B_RAGGED;                                 // the warps of a role
-      const bool eight = i == B_CLEAN || (i >= B_VREAD && i < B_VREAD + 3);  // both W V groups'
-      const bool two = !STATES && i >= B_QKFREE && i < B_QKFREE + 3;   // both MMA warps
-      tc::mbar_init(&bars[i], eight ? 8 : four ? 4 : two ? 2 : 1);
+      const bool two = !STATES && i >= B_QKFREE && i < B_QKFREE + 3;  // both MMA warps
+      const bool vfree = i >= B_VFREE && i < B_VFREE + 3;             // both W V groups, and P V
+      tc::mbar_init(&bars[i], vfree ? (STATES ? 8 : 9) : i == B_CLEAN ? 8 : four ? 4 : two ? 2 : 1);
     }
     tc::fence_barrier_init();
   }
@@ -304,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         for (int kk = 0; kk < C / 16; ++kk)
           mma_ts_if(leader, tmem + kColOp, tmem + kColP + kk * 8, tc::desc_add(vd, kk * 2048), idO, kk > 0);
         commit_if(leader, &bars[B_O]);
+        commit_if(leader, &bars[B_VFREE + s]);
         s = s1, phase = phase1;
       }
       commit_if(leader, &bars[B_DONE]);
@@ -311,12 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     } else if (warp == kMmaD && N > 0) {
       // --------------------------------------------------------- MMA: dS
       const uint32_t leader = lane == 0;
-      constexpr uint32_t idD = tc::idesc_bf16_f32(128, 64 * kSplit, true, true);
+      constexpr uint32_t idD = tc::idesc_bf16_f32(128, 64 * PARTS, true, true);
       const uint32_t s0 = tc::smem_u32(smem);
       // K^T: features along M, 64 of them to a slab (for d = 64 rows 64 .. 127 are the V tile's: not read back);
       // the parts of W V side by side along N
       const uint64_t kt0 = tc::smem_desc_sw128(s0 + M::kQ, 16384, 1024);
-      const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, M::kHalf, 1024);
+      const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, M::kPart, 1024);
       bool ok = true;
       int s = 0, phase = 0;
       for (int c = 0; c < N; ++c) {
@@ -324,19 +329,18 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (c < updates) {
           if (c >= 1 && !(ok = wait_all(&bars[B_DREAD], (c - 1) & 1, err))) break;
           const uint64_t kt = tc::desc_add(kt0, s * M::kStage);
-          if (!(ok = wait_all(&bars[B_W], c & 1, err))) break;
-          tc::fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_if(leader, tmem + kColD, tc::desc_add(kt, kk * 2048), tc::desc_add(wd0, kk * 2048), idD, kk > 0);
-          commit_if(leader, &bars[B_WFREE]);
-          if (!(ok = wait_all(&bars[B_W + 1], c & 1, err))) break;
-          tc::fence_after();
+          for (int x = 0; x < 2 * M::kSteps && ok; ++x) {
+            const int q = x >> 1, hf = x & 1;
+            if (!(ok = wait_all(&bars[B_W + hf], (c * M::kSteps + q) & 1, err))) break;
+            tc::fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_if(leader, tmem + kColD, tc::desc_add(kt, 8192 + kk * 2048),
-                   tc::desc_add(wd0, kSplit * M::kHalf + kk * 2048), idD, 1);
-          commit_if(leader, &bars[B_WFREE + 1]);
+            for (int kk = 0; kk < M::kStep / 16; ++kk)
+              mma_if(leader, tmem + kColD, tc::desc_add(kt, hf * 8192 + q * M::kStep * 128 + kk * 2048),
+                     tc::desc_add(wd0, hf * PARTS * M::kPart + kk * 2048), idD, x > 0 || kk > 0);
+            commit_if(leader, &bars[B_WFREE + hf]);
+          }
+          if (!ok) break;
           commit_if(leader, &bars[B_D]);
         }
         commit_if(leader, &bars[B_QKFREE + s]);
@@ -465,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       tc::fence_after();
 #pragma unroll
       for (int o = 0; o < kWidth; o += 16) {
-        float d[kSplit][16];
+        float d[PARTS][16];
 #pragma unroll
-        for (int p = 0; p < kSplit; ++p) tc::tmem_ld16(tmem + kColD + 64 * p + o + lane_off, d[p]);
+        for (int p = 0; p < PARTS; ++p) tc::tmem_ld16(tmem + kColD + 64 * p + o + lane_off, d[p]);
         tc::tmem_ld_wait();
         if (o + 16 == kWidth) {
           tc::fence_before();
@@ -476,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          uint64_t x2 = tc::f2_pack(d[kSplit - 1][i], d[kSplit - 1][i + 1]);
+          uint64_t x2 = tc::f2_pack(d[PARTS - 1][i], d[PARTS - 1][i + 1]);
 #pragma unroll
-          for (int p = kSplit - 2; p >= 0; --p) x2 = tc::f2_add(x2, tc::f2_pack(d[p][i], d[p][i + 1]));
+          for (int p = PARTS - 2; p >= 0; --p) x2 = tc::f2_add(x2, tc::f2_pack(d[p][i], d[p][i + 1]));
           tc::f2_unpack(tc::f2_add(tc::f2_pack(S[o + i], S[o + i + 1]), x2), S[o + i], S[o + i + 1]);
         }
       }
@@ -500,17 +504,16 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (!STATES) {
       const int el = threadIdx.x - 32 * kOut, i = el;
       const uint32_t lane_off = (uint32_t)(el & 96) << 16;
-      bool ok = true;
-      int s = 0, phase = 0;
+      uint8_t* tile = smem + M::offO;
       const uint64_t sc2 = tc::f2_pack(a.scale, a.scale);
       for (int c = 0; c < N; ++c) {
         const int n = tokens_of(c);
         const float wi = i < n ? pw(back ? n - 1 - i : i + 1) * a.scale : 0.f;
         const uint64_t wi2 = tc::f2_pack(wi, wi);
-        if (!(ok = wait_all(&bars[B_VREAD + s], phase, err))) break;
-        if (!(ok = wait_all(&bars[B_O], c & 1, err))) break;
+        const bool ok = wait_all(&bars[B_O], c & 1, err);
+        if (el == 0) tc::bulk_wait_read_all();  // the last chunk's tile has left
+        if (!tc::group_all(1, 128, ok)) break;
         tc::fence_after();
-        uint8_t* tile = smem + s * M::kStage + M::kQ + M::kTile;
 #pragma unroll
         for (int qt = 0; qt < 4; ++qt) {
           float oi[16], po[16];
@@ -543,12 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (el == 0) {
           tma_store_4d(&maps.o, tile, kWidth * slice, t0 + chunk_at(c) * C, h, b);
           tc::bulk_commit();
-          tc::bulk_wait_read_all();
-          tc::mbar_arrive(&bars[B_VFREE + s]);
         }
-        __syncwarp();
-        s = s + 1 == M::kStages ? 0 : s + 1;
-        phase ^= s == 0;
       }
       if (el == 0) tc::bulk_wait_all();
       // rows behind the sequence's end
@@ -560,17 +558,27 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     // ---------------------------------------- W V, a warpgroup to each half
     registers_down<64>();
     const int el = threadIdx.x - 32 * kW, hf = el >> 7, e0 = el & 127;
+    // the weights of this thread's rows, 64 hf + 16 it + e0 / 8
+    const auto weight = [&](int it, int n) {
+      const int j = 64 * hf + 16 * it + (e0 >> 3);
+      return j < n ? pw(back ? j + 1 : n - 1 - j) : 0.f;
+    };
+    float w[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) w[it] = weight(it, C);
     bool ok = true;
     int s = 0, phase = 0;
     for (int c = 0; c < N && ok; ++c) {
       const int n = tokens_of(c);
       uint8_t* kt = smem + s * M::kStage + M::kQ;
       uint8_t* vt = kt + M::kTile;
-      if (!(ok = wait_all(&bars[B_V + s], phase, err))) break;
+      ok = wait_all(&bars[B_V + s], phase, err);
+      if (!ragged_at(c) && !ok) break;
       if (ragged_at(c)) {
         // tokens behind the end that the loads have brought along are taken out of K (once its scores have been
         // read) and V
-        if (!(ok = STATES ? wait_all(&bars[B_QK + s], phase, err) : wait_all(&bars[B_RAGGED], 0, err))) break;
+        ok = ok && (STATES ? wait_all(&bars[B_QK + s], phase, err) : wait_all(&bars[B_RAGGED], 0, err));
+        if (!(ok = tc::group_all(2, 256, ok))) break;
         for (int e = el; e < (C - n) * 8; e += 256) {
           *(uint4*)(vt + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
           for (int y = 0; y < D / 64; ++y) *(uint4*)(kt + y * 16384 + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -580,42 +588,50 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (lane == 0) tc::mbar_arrive(&bars[B_CLEAN]);
       }
       if (c < updates) {
-        if (c > 0 && !(ok = wait_all(&bars[B_WFREE + hf], (c - 1) & 1, err))) break;
-        uint8_t* dst = smem + M::offW + hf * kSplit * M::kHalf;
-#pragma unroll 2
-        for (int it = 0; it < 4; ++it) {
-          const int row = it * 16 + (e0 >> 3), j = 64 * hf + row, gg = e0 & 7;
-          const float wj = j < n ? pw(back ? j + 1 : n - 1 - j) : 0.f;
-          const uint64_t w2 = tc::f2_pack(wj, wj);
-          const uint4 in = *(const uint4*)(vt + piece(j, gg));
-          const uint32_t u[4] = {in.x, in.y, in.z, in.w};
-          uint32_t p[kSplit][4];
+        uint8_t* dst = smem + M::offW + hf * PARTS * M::kPart;
+        constexpr int kIts = M::kStep / 16;  // 16-byte pieces of a thread in a step
+        if (n < C)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint64_t x2 = tc::f2_mul(tc::f2_pack(lo16(u[e]), hi16(u[e])), w2);
+          for (int it = 0; it < 4; ++it) w[it] = weight(it, n);
 #pragma unroll
-            for (int y = 0; y < kSplit; ++y) {
-              float x0, x1;
-              tc::f2_unpack(x2, x0, x1);
-              const uint32_t z = tc::pack_bf16x2(x0, x1);
-              p[y][e] = z;
-              if (y + 1 < kSplit) x2 = tc::f2_sub(x2, tc::f2_pack(lo16(z), hi16(z)));
+        for (int q = 0; q < M::kSteps; ++q) {
+          uint4 in[kIts];
+#pragma unroll
+          for (int it = 0; it < kIts; ++it) in[it] = *(const uint4*)(vt + piece(64 * hf + (q * kIts + it) * 16 + (e0 >> 3), e0 & 7));
+          if ((c > 0 || q > 0) && !(ok = wait_all(&bars[B_WFREE + hf], (c * M::kSteps + q - 1) & 1, err))) break;
+#pragma unroll
+          for (int it = 0; it < kIts; ++it) {
+            const float wj = w[q * kIts + it];
+            const uint64_t w2 = tc::f2_pack(wj, wj);
+            const uint32_t u[4] = {in[it].x, in[it].y, in[it].z, in[it].w};
+            uint32_t p[PARTS][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint64_t x2 = tc::f2_mul(tc::f2_pack(lo16(u[e]), hi16(u[e])), w2);
+#pragma unroll
+              for (int y = 0; y < PARTS; ++y) {
+                float x0, x1;
+                tc::f2_unpack(x2, x0, x1);
+                const uint32_t z = tc::pack_bf16x2(x0, x1);
+                p[y][e] = z;
+                if (y + 1 < PARTS) x2 = tc::f2_sub(x2, tc::f2_pack(lo16(z), hi16(z)));
+              }
             }
-          }
 #pragma unroll
-          for (int y = 0; y < kSplit; ++y)
-            *(uint4*)(dst + y * M::kHalf + piece(row, gg)) = make_uint4(p[y][0], p[y][1], p[y][2], p[y][3]);
+            for (int y = 0; y < PARTS; ++y)
+              *(uint4*)(dst + y * M::kPart + piece(it * 16 + (e0 >> 3), e0 & 7)) = make_uint4(p[y][0], p[y][1], p[y][2], p[y][3]);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars[B_W + hf]);
         }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars[B_W + hf]);
+        if (!ok) break;
+        if (n < C)
+#pragma unroll
+          for (int it = 0; it < 4; ++it) w[it] = weight(it, C);
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars[B_VREAD + s]);
-      if (STATES) {
-        if (!(ok = wait_all(&bars[B_VREAD + s], phase, err))) break;
-        if (el == 0) tc::mbar_arrive(&bars[B_VFREE + s]);
-      }
+      if (lane == 0) tc::mbar_arrive(&bars[B_VFREE + s]);
       s = s + 1 == M::kStages ? 0 : s + 1;
       phase ^= s == 0;
     }
@@ -659,10 +675,10 @@ bool make_map(CUtensorMap* map, const Tokens& x, const Args& a, int d) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool STATES>
+template <int D, bool STATES, int PARTS>
 cudaError_t launch(const TcArgs& ta, cudaStream_t st) {
-  auto kern = scan_tc_kernel<D, STATES>;
-  const int smem = Lay<D, STATES>::kBytes;
+  auto kern = scan_tc_kernel<D, STATES, PARTS>;
+  const int smem = Lay<D, STATES, PARTS>::kBytes;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const Args& a = ta.a;
@@ -679,8 +695,12 @@ cudaError_t launch_tc(const Args& a, int d, bool states_only, cudaStream_t st) {
     if (!make_map(&ta.m[i].q, a.op[i].q, a, d) || !make_map(&ta.m[i].k, a.op[i].k, a, d) ||
         !make_map(&ta.m[i].v, a.op[i].v, a, d) || !make_map(&ta.m[i].o, a.op[i].o, a, d))
       return cudaErrorInvalidValue;
-  if (states_only) return d == 64 ? launch<64, true>(ta, st) : launch<128, true>(ta, st);
-  return d == 64 ? launch<64, false>(ta, st) : launch<128, false>(ta, st);
+  if (states_only) return d == 64 ? launch<64, true, 3>(ta, st) : launch<128, true, 3>(ta, st);
+  // a state that is given out is as good as fp32 makes it; one that only meets the queries, in bf16, does with two parts
+  bool out = false;
+  for (int i = a.first_op; i < a.last_op; ++i) out = out || a.op[i].s_out;
+  if (out) return d == 64 ? launch<64, false, 3>(ta, st) : launch<128, false, 3>(ta, st);
+  return d == 64 ? launch<64, false, 2>(ta, st) : launch<128, false, 2>(ta, st);
 }
 
 cudaError_t expired_waits(int* out, cudaStream_t st) {
