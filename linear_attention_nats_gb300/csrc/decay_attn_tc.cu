@@ -146,8 +146,27 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
       "r"(leader)
       : "memory");
 }
+// Waits for the phase of parity `parity` to complete, asleep up to a
+// millisecond a try; gives up after seconds and records it.  Kept short, like
+// every loop here: the roles' code goes through one instruction cache, and
+// what is unrolled is fetched again for every chunk.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
+  const uint32_t at = tc::smem_u32(bar);
+  uint32_t ok = 0;
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20) && !ok; ++i)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity), "r"(1000000u)
+        : "memory");
+  if (!ok && err) *(volatile int*)err = 1;
+  return ok;
+}
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* err) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, err));
+  return __all_sync(0xffffffffu, wait(bar, parity, err));
 }
 
 // 16-byte piece g of line r in a 128-byte-swizzled tile
@@ -241,14 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const int s = c % M::kStages, ph = ((c / M::kStages) & 1) ^ 1;
         const int t = t0 + chunk_at(c) * C;
         uint8_t* st = smem + s * M::kStage;
-        if (!(ok = tc::mbar_wait(&bars[B_QKFREE + s], ph, err))) break;
+        if (!(ok = wait(&bars[B_QKFREE + s], ph, err))) break;
         tc::mbar_arrive_expect_tx(&bars[B_QK + s], M::kQ + M::kTile);
         for (int y = 0; y < D / 64; ++y) {
           tma_load_4d(st + M::kQ + y * 16384, &maps.k, 64 * y, t, h, b, &bars[B_QK + s]);
           if (!STATES) tma_load_4d(st + y * 16384, &maps.q, 64 * y, t, h, b, &bars[B_QK + s]);
         }
         ++qk;
-        if (!(ok = tc::mbar_wait(&bars[B_VFREE + s], ph, err))) break;
+        if (!(ok = wait(&bars[B_VFREE + s], ph, err))) break;
         tc::mbar_arrive_expect_tx(&bars[B_V + s], M::kV);
         tma_load_4d(st + M::kQ + M::kTile, &maps.v, kWidth * slice, t, h, b, &bars[B_V + s]);
         ++v;
@@ -256,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       // every copy issued has landed before the CTA may exit
       for (int s = 0; s < M::kStages; ++s) {
         const int nq = qk > s ? (qk - 1 - s) / M::kStages + 1 : 0, nv = v > s ? (v - 1 - s) / M::kStages + 1 : 0;
-        if (nq > 0) tc::mbar_wait(&bars[B_QK + s], (nq - 1) & 1, nullptr);
-        if (nv > 0) tc::mbar_wait(&bars[B_V + s], (nv - 1) & 1, nullptr);
+        if (nq > 0) wait(&bars[B_QK + s], (nq - 1) & 1, nullptr);
+        if (nv > 0) wait(&bars[B_V + s], (nv - 1) & 1, nullptr);
       }
     } else if (!STATES && warp == kMma && N > 0) {
       // --------------------------------------------------- MMA: X, Oi and Op
