@@ -249,14 +249,21 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   const int len = length(a, bh / a.H);
   float* part = op.part + (long long)bh * a.segs * D * D + at;
   float S = op.s_in ? op.s_in[(long long)bh * D * D + r * op.s_r + c * op.s_c] * op.in_scale : 0.f;
-  for (int i = 0; i < a.segs; ++i) {
-    const int seg = op.back ? a.segs - 1 - i : i;
-    if (i > 0) {
-      const int before = op.back ? seg + 1 : seg - 1;
-      const int n = max(0, min(min(before * a.seg + a.seg, a.L), len) - before * a.seg);
-      S = Carry(g, n)(S, part[(long long)seg * D * D]);
-    }
-    part[(long long)seg * D * D] = S;
+  const auto seg_at = [&](int i) { return op.back ? a.segs - 1 - i : i; };
+  part[(long long)seg_at(0) * D * D] = S;
+  for (int i = 1; i < a.segs; i += 8) {
+    float own[8];  // (eight reads in flight)
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u < a.segs) own[u] = part[(long long)seg_at(i + u) * D * D];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u < a.segs) {
+        const int before = seg_at(i + u - 1);
+        const int n = max(0, min(min(before * a.seg + a.seg, a.L), len) - before * a.seg);
+        S = Carry(g, n)(S, own[u]);
+        part[(long long)seg_at(i + u) * D * D] = S;
+      }
   }
 }
 

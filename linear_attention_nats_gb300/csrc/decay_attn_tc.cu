@@ -104,6 +104,13 @@ constexpr uint32_t kColP = 128;   // 64: two bf16 to a column
 constexpr uint32_t kColOi = 192;  // 64
 constexpr uint32_t kColOp = 256;  // 64
 constexpr uint32_t kColD = 320;   // 64 for each part of W V
+// (without outputs there is room for two dS, of chunks c % 2)
+template <bool STATES>
+__device__ __forceinline__ uint32_t col_d(int c) { return STATES ? (c & 1) * 192 : kColD; }
+template <bool STATES>
+__device__ __forceinline__ int bar_d(int c) { return STATES && (c & 1) ? B_X : B_D; }
+template <bool STATES>
+__device__ __forceinline__ int bar_dread(int c) { return STATES && (c & 1) ? B_XREAD : B_DREAD; }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int t, int h, int b, uint64_t* bar) {
   asm volatile(
@@ -346,7 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       for (int c = 0; c < N; ++c) {
         if (!(ok = wait_all(&bars[B_QK + s], phase, err))) break;
         if (c < updates) {
-          if (c >= 1 && !(ok = wait_all(&bars[B_DREAD], (c - 1) & 1, err))) break;
+          if (STATES) {
+            if (c >= 2 && !(ok = wait_all(&bars[bar_dread<true>(c)], ((c - 2) >> 1) & 1, err))) break;
+          } else if (c >= 1 && !(ok = wait_all(&bars[B_DREAD], (c - 1) & 1, err))) {
+            break;
+          }
           const uint64_t kt = tc::desc_add(kt0, s * M::kStage);
 #pragma unroll
           for (int x = 0; x < 2 * M::kSteps && ok; ++x) {
@@ -355,12 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             tc::fence_after();
 #pragma unroll
             for (int kk = 0; kk < M::kStep / 16; ++kk)
-              mma_if(leader, tmem + kColD, tc::desc_add(kt, hf * 8192 + q * M::kStep * 128 + kk * 2048),
+              mma_if(leader, tmem + col_d<STATES>(c), tc::desc_add(kt, hf * 8192 + q * M::kStep * 128 + kk * 2048),
                      tc::desc_add(wd0, hf * PARTS * M::kPart + kk * 2048), idD, x > 0 || kk > 0);
             commit_if(leader, &bars[B_WFREE + hf]);
           }
           if (!ok) break;
-          commit_if(leader, &bars[B_D]);
+          commit_if(leader, &bars[bar_d<STATES>(c)]);
         }
         commit_if(leader, &bars[B_QKFREE + s]);
         s = s + 1 == M::kStages ? 0 : s + 1;
@@ -484,18 +495,18 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         for (int i = 0; i < kWidth; i += 2)
           tc::f2_unpack(tc::f2_mul(tc::f2_pack(S[i], S[i + 1]), m2), S[i], S[i + 1]);
       }
-      if (!(ok = wait_all(&bars[B_D], c & 1, err))) break;
+      if (!(ok = wait_all(&bars[bar_d<STATES>(c)], STATES ? (c >> 1) & 1 : c & 1, err))) break;
       tc::fence_after();
 #pragma unroll
       for (int o = 0; o < kWidth; o += 16) {
         float d[PARTS][16];
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) tc::tmem_ld16(tmem + kColD + 64 * p + o + lane_off, d[p]);
+        for (int p = 0; p < PARTS; ++p) tc::tmem_ld16(tmem + col_d<STATES>(c) + 64 * p + o + lane_off, d[p]);
         tc::tmem_ld_wait();
         if (o + 16 == kWidth) {
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bars[B_DREAD]);
+          if (lane == 0) tc::mbar_arrive(&bars[bar_dread<STATES>(c)]);
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
@@ -714,10 +725,11 @@ cudaError_t launch_tc(const Args& a, int d, bool states_only, cudaStream_t st) {
     if (!make_map(&ta.m[i].q, a.op[i].q, a, d) || !make_map(&ta.m[i].k, a.op[i].k, a, d) ||
         !make_map(&ta.m[i].v, a.op[i].v, a, d) || !make_map(&ta.m[i].o, a.op[i].o, a, d))
       return cudaErrorInvalidValue;
-  if (states_only) return d == 64 ? launch<64, true, 3>(ta, st) : launch<128, true, 3>(ta, st);
   // a state that is given out is as good as fp32 makes it; one that only meets the queries, in bf16, does with two parts
   bool out = false;
   for (int i = a.first_op; i < a.last_op; ++i) out = out || a.op[i].s_out;
+  if (states_only && out) return d == 64 ? launch<64, true, 3>(ta, st) : launch<128, true, 3>(ta, st);
+  if (states_only) return d == 64 ? launch<64, true, 2>(ta, st) : launch<128, true, 2>(ta, st);
   if (out) return d == 64 ? launch<64, false, 3>(ta, st) : launch<128, false, 3>(ta, st);
   return d == 64 ? launch<64, false, 2>(ta, st) : launch<128, false, 2>(ta, st);
 }
