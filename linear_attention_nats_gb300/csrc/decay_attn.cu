@@ -4,6 +4,7 @@
 // fp32 kernel, which also takes bf16 operands that TMA cannot address.
 // decay.cuh has the mathematics, decay_attn_tc.cu the tensor-core kernel.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/nats.h"
 #include "decay.cuh"
@@ -14,7 +15,7 @@ namespace nats {
 namespace decay {
 namespace {
 
-constexpr int kC = 32;  // tokens of a chunk
+constexpr int kC = 64;  // tokens of a chunk
 
 template <class T>
 __device__ __forceinline__ float4 load4(const T* p, bool vec);
@@ -47,26 +48,86 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4], bo
   }
 }
 
+__device__ __forceinline__ void store2(float* p, float x, float y, bool vec) {
+  if (vec) *(float2*)p = make_float2(x, y);
+  else p[0] = x, p[1] = y;
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y, bool vec) {
+  if (vec) *(__nv_bfloat162*)p = __floats2bfloat162_rn(x, y);
+  else p[0] = __float2bfloat16_rn(x), p[1] = __float2bfloat16_rn(y);
+}
+
+// Row pitches: a fragment's 8 rows x 4 entries lie in different banks where it
+// is read along rows (kRow, kP), its 4 rows x 8 entries where along columns (kCol).
 template <int D>
-struct Simt {
-  static constexpr int kRow = D + 4;  // padded: 8 rows' 16-byte pieces lie in different banks
-  static constexpr int kP = kC + 1;
-  static constexpr int offQ = 0, offK = offQ + kC * kRow, offV = offK + kC * kRow, offS = offV + kC * kWidth,
-                       offP = offS + D * kWidth, offW = offP + kC * kP + 3, kFloats = offW + kC + 1;
+struct Split {
+  static constexpr int kRow = D + 4, kP = kC + 4, kCol = kWidth + 8;
+  static constexpr int offQ = 0, offK = offQ + kC * kRow, offV = offK + kC * kRow, offS = offV + kC * kCol,
+                       offP = offS + D * kCol, offW = offP + kC * kP, kFloats = offW + kC + 4;
+  static constexpr int kCtas = D == 64 ? 2 : 1;  // of an SM
 };
 
+// x as the sum of two tf32 numbers, off by half a step of the second: 2^-24.
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// acc += A B for a warp's 16 rows and 32 columns, k8 steps of 8.  a_at(k, row)
+// and b_at(k, column) read an entry; a lane's rows are lane / 4 and that + 8, its
+// columns of a tile of 8 lane / 4 as B's and 2 (lane % 4), + 1 as the sum's.
+// Each factor goes in as two tf32 numbers, the product of the two second ones
+// (2^-24) left out; the small products have a sum of their own.
+template <class A, class B>
+__device__ __forceinline__ void add_product(float (&acc)[4][4], int k8, const A& a_at, const B& b_at) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  float small[4][4] = {};
+#pragma unroll 2
+  for (int s = 0; s < k8; ++s) {
+    const int k = 8 * s + t;
+    uint32_t ah[4], al[4];
+    split(a_at(k, g), ah[0], al[0]);
+    split(a_at(k, g + 8), ah[1], al[1]);
+    split(a_at(k + 4, g), ah[2], al[2]);
+    split(a_at(k + 4, g + 8), ah[3], al[3]);
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      uint32_t bh[2], bl[2];
+      split(b_at(k, 8 * nt + g), bh[0], bl[0]);
+      split(b_at(k + 4, 8 * nt + g), bh[1], bl[1]);
+      mma8(acc[nt], ah, bh);
+      mma8(small[nt], ah, bl);
+      mma8(small[nt], al, bh);
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[nt][e] += small[nt][e];
+}
+
 // One CTA walks the chunks of one segment of one (scan, sequence, head, 64
-// state columns); the state is in registers (rows 8 (or 4) to a group of 16
-// threads) with a copy in shared memory for its product with the queries.
+// state columns).  Every product is 64 x 64 (the state d x 64) on the tf32
+// instructions in split precision, 16 rows and 32 columns to a warp, operands
+// in shared memory; the state is in registers, with a copy there for its product
+// with the queries.  (As fp32 FMAs, four rows and four columns to a thread, the
+// reads from shared memory took twice the time of the FMAs: 3 x 12 heads of 1021
+// tokens, d = 64, 83 us.)
 template <class T, int D, bool STATES>
-__global__ void __launch_bounds__(256) scan_simt_kernel(const Args a) {
+__global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const Args a) {
   begin();
-  using M = Simt<D>;
+  using M = Split<D>;
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm + M::offQ, *Ks = sm + M::offK, *Vs = sm + M::offV, *Ss = sm + M::offS, *Ps = sm + M::offP,
         *Ws = sm + M::offW;  // Ws[m] = gamma^m, m = 0 .. kC
   constexpr int kSlices = D / kWidth;
-  constexpr int R = D / 16;  // state rows of a thread
+  constexpr int G = D / 64;  // tiles of the state's rows, 64 rows apart
 
   const int segs = STATES ? a.segs - 1 : a.segs;
   long long x = blockIdx.x;
@@ -91,132 +152,123 @@ __global__ void __launch_bounds__(256) scan_simt_kernel(const Args a) {
   T* o = (T*)op.o.p + b * op.o.b + h * op.o.h + slice * kWidth;
 
   if (tid <= kC) Ws[tid] = power(g, tid);
-  const int r0 = (tid >> 4) * R, c4 = (tid & 15) * 4;
-  float S[R][4];
+  // the warp's rows and columns of every product; entry e of this lane in its tile nt of 8 columns is at
+  // (at_row(e), at_col(nt, e))
+  const int warp = tid >> 5, lane = tid & 31, wr = (warp >> 1) * 16, wc = (warp & 1) * 32;
+  const auto at_row = [&](int e) { return wr + (lane >> 2) + (e >> 1) * 8; };
+  const auto at_col = [&](int nt, int e) { return wc + 8 * nt + 2 * (lane & 3) + (e & 1); };
+  float S[G][4][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float s = 0.f;
-      if (!STATES) {
-        const int c = slice * kWidth + c4 + e;
-        if (a.segs > 1)
-          s = op.part[((long long)bh * a.segs + seg) * D * D + (op.part_t ? (r0 + r) * D + c : c * D + r0 + r)];
-        else if (op.s_in)
-          s = op.s_in[(long long)bh * D * D + (r0 + r) * op.s_r + c * op.s_c] * op.in_scale;
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 64 * gr + at_row(e), c = slice * kWidth + at_col(nt, e);
+        float s = 0.f;
+        if (!STATES) {
+          if (a.segs > 1)
+            s = op.part[((long long)bh * a.segs + seg) * D * D + (op.part_t ? row * D + c : c * D + row)];
+          else if (op.s_in)
+            s = op.s_in[(long long)bh * D * D + row * op.s_r + c * op.s_c] * op.in_scale;
+        }
+        S[gr][nt][e] = s;
       }
-      S[r][e] = s;
-      Ss[(r0 + r) * kWidth + c4 + e] = s;
-    }
   const int chunks = (n_seg + kC - 1) / kC;
   for (int cc = 0; cc < chunks; ++cc) {
     const int c = back ? chunks - 1 - cc : cc;
     const int base = t0 + c * kC, n = min(kC, n_seg - c * kC);
     __syncthreads();  // the chunk before has been read, S is in place
-    for (int i = tid; i < kC * (D / 4); i += 256) {
-      const int t = i / (D / 4), f = (i % (D / 4)) * 4;
-      // rows in the scan's order; those behind the end are zero
-      const long long src = base + (back ? n - 1 - t : t);
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!STATES) *(float4*)(Qs + t * M::kRow + f) = t < n ? load4(q + src * op.q.t + f, vec) : z;
-      *(float4*)(Ks + t * M::kRow + f) = t < n ? load4(k + src * op.k.t + f, vec) : z;
-    }
-    for (int i = tid; i < kC * (kWidth / 4); i += 256) {
-      const int t = i / (kWidth / 4), f = (i % (kWidth / 4)) * 4;
-      const long long src = base + (back ? n - 1 - t : t);
-      *(float4*)(Vs + t * kWidth + f) =
-          t < n ? load4(v + src * op.v.t + f, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // (all of a thread's reads of a tile are in flight at once)
+    const auto load = [&](const T* from, long long stride, float* to, int pitch, auto width) {
+      constexpr int kW = decltype(width)::value / 4, kN = kC * kW / 256;
+      float4 x[kN];
+#pragma unroll
+      for (int u = 0; u < kN; ++u) {
+        const int i = tid + 256 * u, t = i / kW, f = (i % kW) * 4;
+        // rows in the scan's order; those behind the end are zero
+        x[u] = t < n ? load4(from + (base + (back ? n - 1 - t : t)) * stride + f, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kN; ++u) {
+        const int i = tid + 256 * u;
+        *(float4*)(to + i / kW * pitch + (i % kW) * 4) = x[u];
+      }
+    };
+    load(k, op.k.t, Ks, M::kRow, std::integral_constant<int, D>{});
+    load(v, op.v.t, Vs, M::kCol, std::integral_constant<int, kWidth>{});
+    if (!STATES) load(q, op.q.t, Qs, M::kRow, std::integral_constant<int, D>{});
+    if (!STATES && cc == 0) {  // (the first state's reads run beside the first chunk's)
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Ss[(64 * gr + at_row(e)) * M::kCol + at_col(nt, e)] = S[gr][nt][e];
     }
     __syncthreads();
     if (!STATES) {
-      {  // P: rows ti, ti + 16, columns tj, tj + 16
-        const int ti = tid >> 4, tj = tid & 15;
-        float p[2][2] = {};
-        for (int f = 0; f < D; f += 4) {
-          const float4 q0 = *(const float4*)(Qs + ti * M::kRow + f), q1 = *(const float4*)(Qs + (ti + 16) * M::kRow + f);
-          const float4 k0 = *(const float4*)(Ks + tj * M::kRow + f), k1 = *(const float4*)(Ks + (tj + 16) * M::kRow + f);
-          const auto dot = [](float s, const float4& x, const float4& y) {
-            return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
-          };
-          p[0][0] = dot(p[0][0], q0, k0), p[0][1] = dot(p[0][1], q0, k1);
-          p[1][0] = dot(p[1][0], q1, k0), p[1][1] = dot(p[1][1], q1, k1);
-        }
+      const float *Qw = Qs + wr * M::kRow, *Kw = Ks + wc * M::kRow, *Pw = Ps + wr * M::kP;
+      if (wr + 15 >= wc) {  // (not a warp whose columns are all ahead of its rows)
+        float p[4][4] = {};
+        add_product(p, D / 8, [&](int f, int r) { return Qw[r * M::kRow + f]; },
+                    [&](int f, int j) { return Kw[j * M::kRow + f]; });
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int i = ti + 16 * y, j = tj + 16 * z;
-            Ps[i * M::kP + j] = j <= i ? p[y][z] * Ws[i - j] : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            const int m = at_row(e) - at_col(nt, e);
+            Ps[at_row(e) * M::kP + at_col(nt, e)] = m >= 0 ? p[nt][e] * Ws[m] : 0.f;
           }
       }
       __syncthreads();
-      // o: rows ti, ti + 16, columns c4 .. c4 + 3
-      const int ti = tid >> 4;
-      float acc[2][4] = {}, inter[2][4] = {};
-      for (int f = 0; f < D; f += 4) {
-        const float4 q0 = *(const float4*)(Qs + ti * M::kRow + f), q1 = *(const float4*)(Qs + (ti + 16) * M::kRow + f);
-        const float x0[4] = {q0.x, q0.y, q0.z, q0.w}, x1[4] = {q1.x, q1.y, q1.z, q1.w};
+      float acc[4][4] = {};
+      add_product(acc, D / 8, [&](int f, int r) { return Qw[r * M::kRow + f]; },
+                  [&](int f, int c) { return Ss[f * M::kCol + wc + c]; });
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 s = *(const float4*)(Ss + (f + u) * kWidth + c4);
-          const float y[4] = {s.x, s.y, s.z, s.w};
+      for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            inter[0][e] = fmaf(x0[u], y[e], inter[0][e]), inter[1][e] = fmaf(x1[u], y[e], inter[1][e]);
-        }
-      }
-      for (int j = 0; j < kC; ++j) {
-        const float4 w = *(const float4*)(Vs + j * kWidth + c4);
-        const float y[4] = {w.x, w.y, w.z, w.w};
-        const float p0 = Ps[ti * M::kP + j], p1 = Ps[(ti + 16) * M::kP + j];
+        for (int e = 0; e < 4; ++e) acc[nt][e] *= Ws[at_row(e) + 1 - (back ? 1 : 0)];
+      // (columns behind the warp's last row are zero)
+      add_product(acc, (wr + 16) / 8, [&](int j, int r) { return Pw[r * M::kP + j]; },
+                  [&](int j, int c) { return Vs[j * M::kCol + wc + c]; });
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[0][e] = fmaf(p0, y[e], acc[0][e]), acc[1][e] = fmaf(p1, y[e], acc[1][e]);
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int i = ti + 16 * y;
+      for (int e = 0; e < 4; e += 2) {
+        const int i = at_row(e);
         if (i >= n) continue;
-        const float w = Ws[i + 1 - (back ? 1 : 0)];
-        float r[4];
+        T* to = o + (base + (back ? n - 1 - i : i)) * op.o.t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = a.scale * fmaf(w, inter[y][e], acc[y][e]);
-        const long long dst = base + (back ? n - 1 - i : i);
-        store4(o + dst * op.o.t + c4, r, vec);
+        for (int nt = 0; nt < 4; ++nt)
+          store2(to + at_col(nt, 0), a.scale * acc[nt][e], a.scale * acc[nt][e + 1], vec);
       }
       __syncthreads();  // Ss has been read
     }
-    float add[R][4] = {};
-    for (int j = 0; j < n; ++j) {
-      const float w = Ws[n - 1 - j + (back ? 1 : 0)];
-      const float4 z = *(const float4*)(Vs + j * kWidth + c4);
-      const float y[4] = {z.x * w, z.y * w, z.z * w, z.w * w};
-      float x[R];
-#pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        const float4 f = *(const float4*)(Ks + j * M::kRow + r0 + r);
-        x[r] = f.x, x[r + 1] = f.y, x[r + 2] = f.z, x[r + 3] = f.w;
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) add[r][e] = fmaf(x[r], y[e], add[r][e]);
-    }
     const Carry carry(g, n);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int gr = 0; gr < G; ++gr) {
+      float add[4][4] = {};
+      // (tokens behind the end are zero; their weights are any)
+      add_product(add, (n + 7) / 8, [&](int j, int r) { return Ks[j * M::kRow + 64 * gr + wr + r]; },
+                  [&](int j, int c) { return Vs[j * M::kCol + wc + c] * Ws[max(0, n - 1 - j + (back ? 1 : 0))]; });
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[r][e] = carry(S[r][e], add[r][e]);
-      if (!STATES) *(float4*)(Ss + (r0 + r) * kWidth + c4) = make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          S[gr][nt][e] = carry(S[gr][nt][e], add[nt][e]);
+          if (!STATES) Ss[(64 * gr + at_row(e)) * M::kCol + at_col(nt, e)] = S[gr][nt][e];
+        }
     }
   }
   if (STATES) {
     // the segment's own sum, at the segment that takes it
-    const int to = back ? seg - 1 : seg + 1;
+    float* to = op.part + ((long long)bh * a.segs + (back ? seg - 1 : seg + 1)) * D * D;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        op.part[((long long)bh * a.segs + to) * D * D + (slice * kWidth + c4 + e) * D + r0 + r] = S[r][e];
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          to[(slice * kWidth + at_col(nt, e)) * D + 64 * gr + at_row(e)] = S[gr][nt][e];
     return;
   }
   // rows behind the sequence's end
@@ -226,11 +278,13 @@ __global__ void __launch_bounds__(256) scan_simt_kernel(const Args a) {
   }
   if (op.s_out && seg == (back ? 0 : a.segs - 1)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        op.s_out[(long long)bh * D * D + (r0 + r) * op.s_r + (slice * kWidth + c4 + e) * op.s_c] =
-            S[r][e] * op.out_scale;
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          op.s_out[(long long)bh * D * D + (64 * gr + at_row(e)) * op.s_r + (slice * kWidth + at_col(nt, e)) * op.s_c] =
+              S[gr][nt][e] * op.out_scale;
   }
 }
 
@@ -275,9 +329,9 @@ __global__ void pass_kernel(const float* __restrict__ in, float* __restrict__ ou
 }
 
 template <class T, int D>
-cudaError_t launch_simt(const Args& a, bool states, cudaStream_t st) {
-  auto kern = states ? scan_simt_kernel<T, D, true> : scan_simt_kernel<T, D, false>;
-  const int smem = Simt<D>::kFloats * 4;
+cudaError_t launch_split(const Args& a, bool states, cudaStream_t st) {
+  auto kern = states ? scan_split_kernel<T, D, true> : scan_split_kernel<T, D, false>;
+  const int smem = Split<D>::kFloats * 4;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long grid = (long long)(a.last_op - a.first_op) * a.B * a.H * (D / kWidth) * (states ? a.segs - 1 : a.segs);
@@ -313,8 +367,7 @@ Cut cut(const nats_decay_dims* m, int nops, bool tc) {
   const int C = tc ? kChunkTc : kC;
   const int chunks = (m->L + C - 1) / C;
   const long long units = (long long)nops * m->B * m->H * (m->d / kWidth);
-  // (fp32: two CTAs to an SM)
-  const int segs = segments(units, chunks, tc ? kSMs : 2 * kSMs);
+  const int segs = segments(units, chunks, tc ? kSMs : kSMs * (m->d == 64 ? Split<64>::kCtas : Split<128>::kCtas));
   return {segs, (chunks + segs - 1) / segs * C};
 }
 
@@ -367,8 +420,8 @@ nats_status run(Args& a, const nats_decay_dims* m, const float* log_decay, const
     a.first_op = first, a.last_op = last;
     if (tc) return launch_tc(a, m->d, states, st);
     if (m->dtype == NATS_BF16)
-      return m->d == 64 ? launch_simt<__nv_bfloat16, 64>(a, states, st) : launch_simt<__nv_bfloat16, 128>(a, states, st);
-    return m->d == 64 ? launch_simt<float, 64>(a, states, st) : launch_simt<float, 128>(a, states, st);
+      return m->d == 64 ? launch_split<__nv_bfloat16, 64>(a, states, st) : launch_split<__nv_bfloat16, 128>(a, states, st);
+    return m->d == 64 ? launch_split<float, 64>(a, states, st) : launch_split<float, 128>(a, states, st);
   };
   cudaError_t e = cudaSuccess;
   if (c.segs > 1) {
