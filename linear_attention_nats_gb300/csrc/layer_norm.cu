@@ -8,6 +8,7 @@
 // then the squared distances from it: no cancellation for rows far from zero).
 // The gradient forms mean and r again from x, which it reads anyway, so the
 // forward has nothing to keep.
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -77,6 +78,16 @@ struct Piece<__nv_bfloat16, 8> {
       u[i] = *(const uint32_t*)&h;
     }
     *(uint4*)p = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Piece<__nv_bfloat16, 2> {
+  uint32_t r;
+  __device__ __forceinline__ void zero() { r = 0; }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *(const uint32_t*)p; }
+  __device__ __forceinline__ float operator[](int e) const { return __uint_as_float(e ? r & 0xffff0000u : r << 16); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[2]) {
+    *(__nv_bfloat162*)p = __floats2bfloat162_rn(v[0], v[1]);
   }
 };
 template <class T>
@@ -217,11 +228,60 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs 
   }
 }
 
+// Rows of one piece a thread: a group takes R rows, a grid's groups apart,
+// their reads and the steps of their sums side by side.
+template <class T, int VEC, int G, int R>
+__global__ void __launch_bounds__(256) norm_short_kernel(const NormArgs a) {
+  begin();
+  const int j = threadIdx.x % G, c = j * VEC;
+  const int step = gridDim.x * (256 / G), at = blockIdx.x * (256 / G) + threadIdx.x / G;
+  Piece<T, VEC> in[R];
+  float w[VEC], b[VEC], s[R];
+  const bool mine = c < a.D;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    in[i].zero();
+    if (mine && (long long)at + (long long)i * step < a.rows) in[i].load((const T*)row_at(a.x, row_of(a, at + i * step)) + c);
+  }
+  weights(a.w && mine ? a.w + c : nullptr, w, 1.f);
+  weights(a.bias && mine ? a.bias + c : nullptr, b, 0.f);
+  int flip = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    s[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[i] += in[i][e];
+  }
+  group_sum<G>(s, nullptr, flip);
+  float mean[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    mean[i] = s[i] * a.inv_d, s[i] = 0.f;
+    if (mine)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = in[i][e] - mean[i];
+        s[i] = fmaf(d, d, s[i]);
+      }
+  }
+  group_sum<G>(s, nullptr, flip);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (!mine || (long long)at + (long long)i * step >= a.rows) continue;
+    const float r = 1.f / sqrtf(fmaf(s[i], a.inv_d, a.eps));
+    float v[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf((in[i][e] - mean[i]) * r, w[e], b[e]);
+    Piece<T, VEC>::store((T*)row_at(a.y, row_of(a, at + i * step)) + c, v);
+  }
+}
+
 template <int G>
 constexpr int kBwdBlock = G < 128 ? 128 : G;
 // CTAs of an SM that the registers are to allow
 template <int VEC, int G, int NV>
-constexpr int kBwdFit = VEC == 1 ? 1 : (NV * VEC > 16 ? 384 : 512) / kBwdBlock<G>;
+constexpr int kBwdFit = kBwdBlock<G> > 512 ? 1 : (NV * VEC > 16 ? 384 : 512) / kBwdBlock<G> < 1 ? 1
+                                                : (NV * VEC > 16 ? 384 : 512) / kBwdBlock<G>;
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
@@ -377,31 +437,42 @@ __global__ void __launch_bounds__(kBwdBlock<G>, kBwdFit<VEC, G, NV>) norm_bwd_ke
   }
 }
 
-// dw and db: 32 columns a CTA, 32 threads a column over the CTAs' sums.
+// dw and db: blockDim.x columns a CTA, blockDim.y threads (a power of two) a
+// column over the CTAs' sums, added by halves.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int n, int D, float* dw, float* db) {
   begin();
-  __shared__ float sm[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;  // of [dw | db]
-  float s[8] = {};  // (eight reads in flight)
+  __shared__ float sm[1024];
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;  // of [dw | db]
+  float s[8] = {};                                      // (eight reads in flight)
   if (c < 2 * D)
-    for (int i = threadIdx.y; i < n; i += 256)
+    for (int i = threadIdx.y; i < n; i += 8 * blockDim.y)
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (i + 32 * u < n) s[u] += part[(long long)(i + 32 * u) * 2 * D + c];
-  sm[threadIdx.y][threadIdx.x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-  __syncthreads();
-  const float t = warp_sum(sm[threadIdx.x][threadIdx.y]);
-  const int o = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && o < 2 * D) {
-    float* out = o < D ? dw : db;
-    if (out) out[o < D ? o : o - D] = t;
+      for (int u = 0; u < 8; ++u) {
+        const int at = i + u * blockDim.y;
+        if (at < n) s[u] += part[(long long)at * 2 * D + c];
+      }
+  float* mine = sm + threadIdx.y * blockDim.x + threadIdx.x;
+  *mine = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+  for (int h = blockDim.y / 2; h > 0; h >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.y < h) *mine += mine[h * blockDim.x];
   }
+  if (threadIdx.y > 0 || c >= 2 * D) return;
+  float* out = c < D ? dw : db;
+  if (out) out[c < D ? c : c - D] = *mine;
 }
 
 // ----------------------------------------------------------------- launches
 
 template <bool BWD, bool FULL, class T, int VEC, int G, int NV>
 cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
+  if constexpr (!BWD && G <= 32 && NV == 1 && VEC > 1) {
+    constexpr int R = 4;
+    if (a.rows >= 32 * kSMs * (256 / G)) {
+      const long long groups = ((long long)a.rows + R - 1) / R;
+      return after(norm_short_kernel<T, VEC, G, R>, (unsigned)((groups + 256 / G - 1) / (256 / G)), dim3(256), 0, st, 0, a);
+    }
+  }
   if constexpr (!BWD) {
     // few rows: a CTA each, so that more SMs have a part
     const int block = G >= 128 ? G : a.rows < 8 * kSMs && G >= 32 ? G : 128;
@@ -411,11 +482,20 @@ cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
   constexpr int kBlock = kBwdBlock<G>, kGroups = kBlock / G;
   constexpr int smem = VEC * sizeof(T) == 16 ? kAhead<G, NV> * 2 * NV * kBlock * 16 : 0;
   auto kern = norm_bwd_kernel<FULL, T, VEC, G, NV>;
-  int fit = 0;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kBlock, smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 0) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<int> fits{0};  // the same on every GPU that this library runs on
+  int fit = fits.load(std::memory_order_relaxed);
+  if (e == cudaSuccess && fit == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, kBlock, smem);
+    if (e == cudaSuccess) fits.store(fit, std::memory_order_relaxed);
+  }
   if (e != cudaSuccess) return e;
-  const int most = kSMs * (fit < kBwdCtas / kSMs ? fit : kBwdCtas / kSMs);
+  // as many CTAs as fit, but no more than one an SM where their sums would be more than a quarter of the rows' bytes
+  // (1024 rows of 2048, bf16: see below)
+  long long most = kSMs * (fit < kBwdCtas / kSMs ? fit : kBwdCtas / kSMs);
+  const long long few = (long long)a.rows * sizeof(T) * 3 / 32;
+  if (most > few) most = few > kSMs ? few : kSMs;
   const long long need = ((long long)a.rows + kGroups - 1) / kGroups;
   *ctas = (int)(need < most ? need : most);
   return after(kern, (unsigned)*ctas, dim3(kBlock), smem, st, 0, a);
@@ -426,13 +506,13 @@ cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
 // so that the steps of the row's sums are few beside its entries; 16 in the
 // gradient, which keeps two sums and a weight for each.
 template <bool BWD, class T>
-cudaError_t choose(const NormArgs& a, bool vec, int* ctas, cudaStream_t st) {
+cudaError_t choose(const NormArgs& a, bool vec, bool pairs, int* ctas, cudaStream_t st) {
   constexpr int V = sizeof(T) == 2 ? 8 : 4;
   constexpr int M = 32 / V;
   const int n = vec ? a.D / V : a.D;
 #define NATS_NORM(VEC, G, NV) \
   if (n <= (G) * (NV))        \
-  return (VEC) != 1 && n == (G) * (NV) ? go<BWD, (VEC) != 1, T, VEC, G, NV>(a, ctas, st) \
+  return (VEC) > 2 && n == (G) * (NV) ? go<BWD, ((VEC) > 2), T, VEC, G, NV>(a, ctas, st) \
                                       : go<BWD, false, T, VEC, G, NV>(a, ctas, st)
   if (vec) {
     NATS_NORM(V, 8, 1);
@@ -453,9 +533,26 @@ cudaError_t choose(const NormArgs& a, bool vec, int* ctas, cudaStream_t st) {
       NATS_NORM(V, 256, M);
     }
     NATS_NORM(V, 512, M);
-  } else {
+    return cudaErrorInvalidValue;
+  }
+  if constexpr (V == 8) {
+    if (pairs) {
+      const int n = a.D / 2;
+      NATS_NORM(2, 32, 4);
+      NATS_NORM(2, 32, 8);
+      if constexpr (!BWD) NATS_NORM(2, 32, 16);
+      NATS_NORM(2, 64, 8);
+      NATS_NORM(2, 128, 8);
+      NATS_NORM(2, 256, 8);
+      NATS_NORM(2, 512, 8);
+      NATS_NORM(2, 1024, 8);
+      return cudaErrorInvalidValue;
+    }
+  }
+  {
     NATS_NORM(1, 32, 4);
     NATS_NORM(1, 32, 16);
+    if constexpr (!BWD) NATS_NORM(1, 32, 32);
     NATS_NORM(1, 64, 16);
     NATS_NORM(1, 128, 16);
     NATS_NORM(1, 256, 16);
@@ -480,8 +577,8 @@ bool elem_ok(const void* p, int es) { return ((uintptr_t)p & (uintptr_t)(es - 1)
 Rows rows_of(const void* p, const nats_strides* st, int es) {
   return {(char*)const_cast<void*>(p), st->b * es, st->h * es, st->t * es};
 }
-bool vec_ok(const Rows& r, const nats_norm_dims* d) {
-  return elem_ok(r.p, 16) && (d->B == 1 || r.b % 16 == 0) && (d->H == 1 || r.h % 16 == 0) && (d->L == 1 || r.t % 16 == 0);
+bool rows_at(const Rows& r, const nats_norm_dims* d, int n) {
+  return elem_ok(r.p, n) && (d->B == 1 || r.b % n == 0) && (d->H == 1 || r.h % n == 0) && (d->L == 1 || r.t % n == 0);
 }
 
 }  // namespace
@@ -504,10 +601,11 @@ nats_status nats_layer_norm(const nats_norm_dims* dims, const void* x, const nat
   a.w = w, a.bias = b;
   a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D, a.flat = dims->B == 1 && dims->H == 1;
   a.eps = dims->eps, a.inv_d = 1.f / dims->D;
-  const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && elem_ok(w, 16) && elem_ok(b, 16);
+  const bool vec = dims->D % (16 / es) == 0 && rows_at(a.x, dims, 16) && rows_at(a.y, dims, 16) && elem_ok(w, 16) && elem_ok(b, 16);
+  const bool pairs = dims->D % 2 == 0 && rows_at(a.x, dims, 4) && rows_at(a.y, dims, 4);
   cudaStream_t st = (cudaStream_t)stream;
-  return (nats_status)record_cuda_error(es == 2 ? choose<false, __nv_bfloat16>(a, vec, nullptr, st)
-                                                : choose<false, float>(a, vec, nullptr, st));
+  return (nats_status)record_cuda_error(es == 2 ? choose<false, __nv_bfloat16>(a, vec, pairs, nullptr, st)
+                                                : choose<false, float>(a, vec, pairs, nullptr, st));
 }
 
 size_t nats_layer_norm_bwd_workspace_size(const nats_norm_dims* dims) {
@@ -546,15 +644,18 @@ nats_status nats_layer_norm_bwd(const nats_norm_dims* dims, const void* dout, co
   a.w = w, a.part = sums ? (float*)workspace : nullptr;
   a.rows = dims->B * dims->H * dims->L, a.H = dims->H, a.L = dims->L, a.D = dims->D, a.flat = dims->B == 1 && dims->H == 1;
   a.eps = dims->eps, a.inv_d = 1.f / dims->D;
-  const bool vec = dims->D % (16 / es) == 0 && vec_ok(a.x, dims) && vec_ok(a.y, dims) && vec_ok(a.u, dims) &&
+  const bool vec = dims->D % (16 / es) == 0 && rows_at(a.x, dims, 16) && rows_at(a.y, dims, 16) && rows_at(a.u, dims, 16) &&
                    elem_ok(w, 16);
+  const bool pairs = dims->D % 2 == 0 && rows_at(a.x, dims, 4) && rows_at(a.y, dims, 4) && rows_at(a.u, dims, 4);
   int ctas = 0;
-  const int r = record_cuda_error(es == 2 ? choose<true, __nv_bfloat16>(a, vec, &ctas, st)
-                                          : choose<true, float>(a, vec, &ctas, st));
+  const int r = record_cuda_error(es == 2 ? choose<true, __nv_bfloat16>(a, vec, pairs, &ctas, st)
+                                          : choose<true, float>(a, vec, pairs, &ctas, st));
   if (r != NATS_OK || !sums) return (nats_status)r;
   const float* part = a.part;
-  return (nats_status)record_cuda_error(after(norm_dw_kernel, (unsigned)((2 * dims->D + 31) / 32), dim3(32, 32), 0, st, 0,
-                                              part, ctas, (int)dims->D, dw, db));
+  // a short row's columns are few: fewer of them to a CTA, and more threads to each
+  const dim3 block = dims->D <= 512 ? dim3(8, 128) : dim3(32, ctas > 64 ? 32 : 8);
+  return (nats_status)record_cuda_error(
+      after(norm_dw_kernel, (2 * dims->D + block.x - 1) / block.x, block, 0, st, 0, part, ctas, (int)dims->D, dw, db));
 }
 
 }  // extern "C"

@@ -49,8 +49,8 @@ def check(nats, x, u, w, b, eps=1e-6):
 
 
 # lengths of rows at the edges of each way a row is held, whole pieces and entry by entry
-DS = [1, 2, 7, 31, 33, 64, 65, 128, 256, 257, 512, 777, 1000, 1024, 1025, 2048, 2049, 4096, 4104, 5000, 8192, 8200, 16383,
-      16384]
+DS = [1, 2, 7, 31, 33, 64, 65, 66, 128, 256, 257, 258, 512, 777, 1000, 1024, 1025, 2048, 2049, 2050, 4096, 4098, 4104, 5000, 8192,
+      8194, 8200, 16382, 16383, 16384]
 
 
 @TYPES
@@ -61,7 +61,8 @@ def test_rows(nats, N, D, dtype):
 
 
 @TYPES
-@pytest.mark.parametrize("shape", [(5000, 64), (3000, 128), (700, 2048), (2500, 100)], ids=str)
+@pytest.mark.parametrize("shape", [(5000, 64), (3000, 128), (700, 2048), (2500, 100), (160003, 64), (80001, 120), (40009, 256),
+                                   (900, 1030)], ids=str)
 def test_many_rows(nats, shape, dtype):
     check(nats, rows(shape, dtype), rows(shape, dtype, 2, 0.0), *weights(shape[-1]))
 
