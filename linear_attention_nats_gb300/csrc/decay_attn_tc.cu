@@ -159,7 +159,7 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
 // loop is kept short: the roles' code goes through one instruction cache, and
 // what is unrolled is fetched again for every chunk (4 x 16 heads of 8192 tokens:
 // 125 us; unrolled by four 226, with a clock read in the loop 165).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   const uint32_t at = tc::smem_u32(bar);
   uint32_t ok = 0;
 #pragma unroll 1
@@ -171,11 +171,10 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
         : "=r"(ok)
         : "r"(at), "r"(parity), "r"(10000u)
         : "memory");
-  if (!ok && err) *(volatile int*)err = 1;
   return ok;
 }
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* err) {
-  return __all_sync(0xffffffffu, wait(bar, parity, err));
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
 // 16-byte piece g of line r in a 128-byte-swizzled tile
@@ -245,9 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
   // chunks whose sums are wanted: all, or all but the last where no state goes on
   const int updates = STATES || (op.s_out && last_seg) ? N : N - 1;
   const auto chunk_at = [&](int c) { return back ? N - 1 - c : c; };
-  const auto tokens_of = [&](int c) { return min(C, n_seg - chunk_at(c) * C); };
+  // the one chunk that may hold fewer than C tokens
+  const int part_c = back ? 0 : N - 1, part_n = n_seg - (N - 1) * C;
+  const auto tokens_of = [&](int c) { return c == part_c ? part_n : C; };
   // a chunk whose tile holds tokens behind the sequence's end
-  const auto ragged_at = [&](int c) { return tokens_of(c) < C && t0 + n_seg < a.L; };
+  const int ragged_c = part_n < C && t0 + n_seg < a.L ? part_c : -1;
+  const auto ragged_at = [&](int c) { return c == ragged_c; };
   for (int e = threadIdx.x; e < 4 * kCopy; e += kThreads) {
     const int y = e % kCopy + e / kCopy, m = back ? y - 31 : 127 - y;
     tab[e] = e == kPow128 ? power(g, 128) : m >= 0 ? power(g, m) : 0.f;
@@ -257,26 +259,26 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
-  int* err = &g_expired;
+  // whether this warp's waits have all ended; a role that one left goes to the end, where it is recorded
+  bool ok = true;
 
   if (warp >= kLoad) {
     registers_down<40>();
     if (warp == kLoad && lane == 0) {
       // ----------------------------------------------------------- producer
-      bool ok = true;
       int qk = 0, v = 0;
       for (int c = 0; c < N; ++c) {
         const int s = c % M::kStages, ph = ((c / M::kStages) & 1) ^ 1;
         const int t = t0 + chunk_at(c) * C;
         uint8_t* st = smem + s * M::kStage;
-        if (!(ok = wait(&bars[B_QKFREE + s], ph, err))) break;
+        if (!(ok = wait(&bars[B_QKFREE + s], ph))) break;
         tc::mbar_arrive_expect_tx(&bars[B_QK + s], M::kQ + M::kTile);
         for (int y = 0; y < D / 64; ++y) {
           tma_load_4d(st + M::kQ + y * 16384, &maps.k, 64 * y, t, h, b, &bars[B_QK + s]);
           if (!STATES) tma_load_4d(st + y * 16384, &maps.q, 64 * y, t, h, b, &bars[B_QK + s]);
         }
         ++qk;
-        if (!(ok = wait(&bars[B_VFREE + s], ph, err))) break;
+        if (!(ok = wait(&bars[B_VFREE + s], ph))) break;
         tc::mbar_arrive_expect_tx(&bars[B_V + s], M::kV);
         tma_load_4d(st + M::kQ + M::kTile, &maps.v, kWidth * slice, t, h, b, &bars[B_V + s]);
         ++v;
@@ -284,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       // every copy issued has landed before the CTA may exit
       for (int s = 0; s < M::kStages; ++s) {
         const int nq = qk > s ? (qk - 1 - s) / M::kStages + 1 : 0, nv = v > s ? (v - 1 - s) / M::kStages + 1 : 0;
-        if (nq > 0) wait(&bars[B_QK + s], (nq - 1) & 1, nullptr);
-        if (nv > 0) wait(&bars[B_V + s], (nv - 1) & 1, nullptr);
+        if (nq > 0) wait(&bars[B_QK + s], (nq - 1) & 1);
+        if (nv > 0) wait(&bars[B_V + s], (nv - 1) & 1);
       }
     } else if (!STATES && warp == kMma && N > 0) {
       // --------------------------------------------------- MMA: X, Oi and Op
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       const uint64_t vd0 = tc::smem_desc_sw128(s0 + M::kQ + M::kTile, 16384, 1024);
       const uint64_t sd0 = tc::smem_desc_sw128(s0 + M::offS, 16384, 1024);
       const auto scores = [&](int s, int phase) {
-        if (!wait_all(&bars[B_QK + s], phase, err)) return false;
+        if (!wait_all(&bars[B_QK + s], phase)) return false;
         tc::fence_after();
         const uint64_t qd = tc::desc_add(qd0, s * M::kStage), kd = tc::desc_add(kd0, s * M::kStage);
 #pragma unroll
@@ -308,13 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         commit_if(leader, &bars[B_X]);
         return true;
       };
-      bool ok = scores(0, 0);
+      ok = scores(0, 0);
       int s = 0, phase = 0;
       for (int c = 0; c < N && ok; ++c) {
         const uint32_t sb = s * M::kStage;
         const int s1 = s + 1 == M::kStages ? 0 : s + 1, phase1 = s1 == 0 ? phase ^ 1 : phase;
-        if (!(ok = wait_all(&bars[B_S], c & 1, err))) break;
-        if (c >= 1 && !(ok = wait_all(&bars[B_OREAD], (c - 1) & 1, err))) break;
+        if (!(ok = wait_all(&bars[B_S], c & 1))) break;
+        if (c >= 1 && !(ok = wait_all(&bars[B_OREAD], (c - 1) & 1))) break;
         tc::fence_after();
         const uint64_t qd = tc::desc_add(qd0, sb), vd = tc::desc_add(vd0, sb);
 #pragma unroll
@@ -325,12 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         commit_if(leader, &bars[B_QKFREE + s]);
         // the next chunk's scores as soon as the last one's have been read
         if (c + 1 < N) {
-          if (!(ok = wait_all(&bars[B_XREAD], c & 1, err))) break;
+          if (!(ok = wait_all(&bars[B_XREAD], c & 1))) break;
           if (!(ok = scores(s1, phase1))) break;
         }
-        if (ragged_at(c) && !(ok = wait_all(&bars[B_CLEAN], 0, err))) break;
-        if (!(ok = wait_all(&bars[B_V + s], phase, err))) break;
-        if (!(ok = wait_all(&bars[B_P], c & 1, err))) break;
+        if (ragged_at(c) && !(ok = wait_all(&bars[B_CLEAN], 0))) break;
+        if (!(ok = wait_all(&bars[B_V + s], phase))) break;
+        if (!(ok = wait_all(&bars[B_P], c & 1))) break;
         tc::fence_after();
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         s = s1, phase = phase1;
       }
       commit_if(leader, &bars[B_DONE]);
-      wait_all(&bars[B_DONE], 0, err);
+      ok = wait_all(&bars[B_DONE], 0) && ok;
     } else if (warp == kMmaD && N > 0) {
       // --------------------------------------------------------- MMA: dS
       const uint32_t leader = lane == 0;
@@ -350,21 +352,20 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       // the parts of W V side by side along N
       const uint64_t kt0 = tc::smem_desc_sw128(s0 + M::kQ, 16384, 1024);
       const uint64_t wd0 = tc::smem_desc_sw128(s0 + M::offW, M::kPart, 1024);
-      bool ok = true;
       int s = 0, phase = 0;
       for (int c = 0; c < N; ++c) {
-        if (!(ok = wait_all(&bars[B_QK + s], phase, err))) break;
+        if (!(ok = wait_all(&bars[B_QK + s], phase))) break;
         if (c < updates) {
           if (STATES) {
-            if (c >= 2 && !(ok = wait_all(&bars[bar_dread<true>(c)], ((c - 2) >> 1) & 1, err))) break;
-          } else if (c >= 1 && !(ok = wait_all(&bars[B_DREAD], (c - 1) & 1, err))) {
+            if (c >= 2 && !(ok = wait_all(&bars[bar_dread<true>(c)], ((c - 2) >> 1) & 1))) break;
+          } else if (c >= 1 && !(ok = wait_all(&bars[B_DREAD], (c - 1) & 1))) {
             break;
           }
           const uint64_t kt = tc::desc_add(kt0, s * M::kStage);
 #pragma unroll
           for (int x = 0; x < 2 * M::kSteps && ok; ++x) {
             const int q = x >> 1, hf = x & 1;
-            if (!(ok = wait_all(&bars[B_W + hf], (c * M::kSteps + q) & 1, err))) break;
+            if (!(ok = wait_all(&bars[B_W + hf], (c * M::kSteps + q) & 1))) break;
             tc::fence_after();
 #pragma unroll
             for (int kk = 0; kk < M::kStep / 16; ++kk)
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         phase ^= s == 0;
       }
       commit_if(leader, &bars[B_DONE + 1]);
-      wait_all(&bars[B_DONE + 1], 0, err);
+      ok = wait_all(&bars[B_DONE + 1], 0) && ok;
     }
   } else if (warp < kState) {
     // -------------------------------------------------------------------- P
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       const int first = back ? w : 0, last = back ? 3 : w;
       for (int c = 0; c < N; ++c) {
         const int n = tokens_of(c);
-        if (!wait_all(&bars[B_X], c & 1, err)) break;
+        if (!(ok = wait_all(&bars[B_X], c & 1))) break;
         tc::fence_after();
 #pragma unroll 1
         for (int blk = first; blk <= last; ++blk) {
@@ -430,15 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 #pragma unroll
           for (int j = 0; j < 16; ++j) pk[j] = tc::pack_bf16x2(s[2 * j], s[2 * j + 1]);
           if (blk == first && c > 0) {  // the last chunk's P has been used
-            if (!wait_all(&bars[B_O], (c - 1) & 1, err)) {
-              c = N;
-              break;
-            }
+            if (!(ok = wait_all(&bars[B_O], (c - 1) & 1))) break;
             tc::fence_after();
           }
           tc::tmem_st16u(tp + 16 * blk, pk);
         }
-        if (c == N) break;
+        if (!ok) break;
         tc::tmem_st_wait();
         tc::fence_before();
         __syncwarp();
@@ -481,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       if (lane == 0) tc::mbar_arrive(&bars[B_S]);
     };
     if (!STATES) publish();
-    bool ok = true;
     for (int c = 0; c < updates; ++c) {
       const Carry carry(g, tokens_of(c));
       // the sum of the old state's part and dS's: gamma^n S first, while dS is on its way
@@ -497,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         for (int i = 0; i < kWidth; i += 2)
           tc::f2_unpack(tc::f2_mul(tc::f2_pack(S[i], S[i + 1]), m2), S[i], S[i + 1]);
       }
-      if (!(ok = wait_all(&bars[bar_d<STATES>(c)], STATES ? (c >> 1) & 1 : c & 1, err))) break;
+      if (!(ok = wait_all(&bars[bar_d<STATES>(c)], STATES ? (c >> 1) & 1 : c & 1))) break;
       tc::fence_after();
 #pragma unroll
       for (int o = 0; o < kWidth; o += 16) {
@@ -519,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
       }
       if (!STATES && c + 1 < N) {
-        if (!(ok = wait_all(&bars[B_SREAD], c & 1, err))) break;
+        if (!(ok = wait_all(&bars[B_SREAD], c & 1))) break;
         publish();
       }
     }
@@ -542,9 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const int n = tokens_of(c);
         const float wi = i < n ? pw(back ? n - 1 - i : i + 1) * a.scale : 0.f;
         const uint64_t wi2 = tc::f2_pack(wi, wi);
-        const bool ok = wait_all(&bars[B_O], c & 1, err);
+        ok = wait_all(&bars[B_O], c & 1);
         if (el == 0) tc::bulk_wait_read_all();  // the last chunk's tile has left
-        if (!tc::group_all(1, 128, ok)) break;
+        if (!(ok = tc::group_all(1, 128, ok))) break;
         tc::fence_after();
 #pragma unroll
         for (int qt = 0; qt < 4; ++qt) {
@@ -598,18 +595,17 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     float w[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) w[it] = weight(it, C);
-    bool ok = true;
     int s = 0, phase = 0;
     for (int c = 0; c < N && ok; ++c) {
       const int n = tokens_of(c);
       uint8_t* kt = smem + s * M::kStage + M::kQ;
       uint8_t* vt = kt + M::kTile;
-      ok = wait_all(&bars[B_V + s], phase, err);
+      ok = wait_all(&bars[B_V + s], phase);
       if (!ragged_at(c) && !ok) break;
       if (ragged_at(c)) {
         // tokens behind the end that the loads have brought along are taken out of K (once its scores have been
         // read) and V
-        ok = ok && (STATES ? wait_all(&bars[B_QK + s], phase, err) : wait_all(&bars[B_RAGGED], 0, err));
+        ok = ok && (STATES ? wait_all(&bars[B_QK + s], phase) : wait_all(&bars[B_RAGGED], 0));
         if (!(ok = tc::group_all(2, 256, ok))) break;
         for (int e = el; e < (C - n) * 8; e += 256) {
           *(uint4*)(vt + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -630,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
           uint4 in[kIts];
 #pragma unroll
           for (int it = 0; it < kIts; ++it) in[it] = *(const uint4*)(vt + piece(64 * hf + (q * kIts + it) * 16 + (e0 >> 3), e0 & 7));
-          if ((c > 0 || q > 0) && !(ok = wait_all(&bars[B_WFREE + hf], (c * M::kSteps + q - 1) & 1, err))) break;
+          if ((c > 0 || q > 0) && !(ok = wait_all(&bars[B_WFREE + hf], (c * M::kSteps + q - 1) & 1))) break;
 #pragma unroll
           for (int it = 0; it < kIts; ++it) {
             const float wj = w[q * kIts + it];
@@ -668,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       phase ^= s == 0;
     }
   }
+  if (!ok && lane == 0) g_expired = 1;
   tc::fence_before();
   __syncthreads();
   if (warp == kMma) {
