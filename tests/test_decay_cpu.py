@@ -154,3 +154,51 @@ def test_attn_recurrence():
         S = torch.exp(g)[:, None, None] * S + v[:, t, :, None] * k[:, t, None, :]
         assert (o[:, t] - 0.5 * (S @ q[:, t, :, None])[..., 0]).abs().max() < 1e-12
     assert (last - S).abs().max() < 1e-12 and (o[:, 7:] == 0).all()
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_decay_table(back):
+    """The tensor-core kernel's table of decays: four copies shifted by an entry each, read four entries at a time from a
+    16-byte boundary, give every row its decays to the columns of a block, and stay inside their copy."""
+    copy, g = 168, -0.1
+    tab = [0.0] * (4 * copy)
+    for e in range(4 * copy):
+        y = e % copy + e // copy
+        m = y - 31 if back else 127 - y
+        tab[e] = g * m if m >= 0 else None
+    for i in range(128):
+        at = (31 if back else 127) - i
+        w = i // 32
+        for blk in (range(w, 4) if back else range(w + 1)):
+            for j in range(0, 32, 4):
+                a = (at & 3) * copy + (at & ~3) + 32 * blk + j
+                assert a % 4 == 0 and (at & 3) * copy <= a and a + 3 < (at & 3) * copy + 160
+                for e in range(4):
+                    m = 32 * blk + j + e - i if back else i - 32 * blk - j - e
+                    assert tab[a + e] == (g * m if m >= 0 else None)
+
+
+@pytest.mark.parametrize("L", [1, 64, 127, 128, 129, 1000, 70000])
+@pytest.mark.parametrize("segs", [1, 2, 7])
+@pytest.mark.parametrize("C", [64, 128])
+def test_segments_cover(L, segs, C):
+    """Segments of whole chunks cover the tokens once, in both directions, whatever the length."""
+    chunks = -(-L // C)
+    per = -(-chunks // segs)
+    if -(-chunks // per) != segs:
+        return
+    for n in {0, 1, C - 1, C, L // 2, L}:
+        if n > L:
+            continue
+        seen = 0
+        for seg in range(segs):
+            t0, t1 = seg * per * C, min(seg * per * C + per * C, L)
+            m = max(0, min(t1, n) - t0)
+            N = -(-m // C)
+            assert t0 == seen or m == 0
+            for back in (False, True):
+                part_c, part_n = (0 if back else N - 1), m - (N - 1) * C
+                tokens = [part_n if c == part_c else C for c in range(N)]
+                assert sum(tokens) == m and all(0 < t <= C for t in tokens)
+            seen += m
+        assert seen == n

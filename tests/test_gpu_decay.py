@@ -256,6 +256,66 @@ def test_prompt_in_parts(nats):
     within(state[0], S, ref.state_bound(S_size, 700, False), "state")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_cut_padded_with_garbage(nats, d, dtype):
+    """Segments whose chunks end inside a tile, NaN behind them, forward and backward; lengths at a segment's edges."""
+    B, H, L = 5, 1, 2600
+    u, q, k, v = make(B, H, L, d, dtype, "heads", n=4)
+    lens = torch.tensor([2600, 2500, 1, 257, 1300], dtype=torch.int32, device="cuda")
+    for x in (u, q, k, v):
+        for b, n in enumerate(lens.tolist()):
+            x[b, :, n:] = float("nan")
+    gt = torch.full((1,), -0.01, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    st = [torch.randn(B, H, d, d, generator=gen, device="cuda") for _ in range(2)]
+    tc = dtype == torch.bfloat16
+    check_prompt(nats, q, k, v, gt, tc, lens=lens, state=st[0])
+    check_grad(nats, u, q, k, v, gt, tc, lens=lens, state=st[0], dstate=st[1])
+    nats.decay_attn_check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_shared_and_given(nats, dtype):
+    """Keys and values that all heads share (expanded), outputs in given tensors of other layouts, and a call without
+    a state, whose output is that of the call with one, but for the state's parts."""
+    B, H, L, d = 2, 5, 333, 64
+    q, k, v = make(B, H, L, d, dtype, "heads")
+    k, v = k[:, :1].expand(B, H, L, d), v[:, :1].expand(B, H, L, d)
+    g = log_decay(H)
+    want, _ = check_prompt(nats, q, k, v, g, False)
+    out = torch.full((B, L, 2, H, d), 7.0, dtype=dtype, device="cuda")
+    assert nats.decay_attn(q, k, v, g, out=out[:, :, 1].transpose(1, 2)).data_ptr() == out[:, :, 1].data_ptr()
+    assert torch.equal(out[:, :, 1].transpose(1, 2), want) and (out[:, :, 0] == 7).all()
+    q, k, v, u = make(B, H, L, d, dtype, "heads", n=4)
+    want = nats.decay_attn(q, k, v, g)
+    nats.decay_attn(q, k, v, g, out=out[:, :, 1].transpose(1, 2))
+    assert torch.equal(out[:, :, 1].transpose(1, 2), want) and (out[:, :, 0] == 7).all()
+    grads = nats.decay_attn_bwd(u, q, k, v, g)
+    buf = torch.full((B, L, 4, H, d), 7.0, dtype=dtype, device="cuda")
+    views = {n: buf[:, :, i].transpose(1, 2) for i, n in enumerate(("dq", "dk", "dv"))}
+    r = nats.decay_attn_bwd(u, q, k, v, g, **views)
+    assert all(torch.equal(r[n], grads[n]) for n in grads) and (buf[:, :, 3] == 7).all()
+    rows = ref.batch(lambda q, k, v, n: ref.attn(q, k, v, g.cpu(), d ** -0.5, n, None), q, k, v, lens=[L] * B, L=L)
+    for b, (o, size, _, _) in enumerate(rows):
+        within(want[b], o, ref.out_bound(o, size, d, L, dtype, dtype == torch.bfloat16) + size * 2.0 ** -16, b)
+
+
+def test_two_streams(nats):
+    """Two calls at once, each cut into segments with a workspace of its own."""
+    a, b = (make(1, 1, 4000, 128, torch.bfloat16, "heads", seed=s) for s in (1, 2))
+    g = torch.full((1,), -0.02, device="cuda")
+    want = [nats.decay_attn(*x, g, return_state=True) for x in (a, b)]
+    s = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got = [nats.decay_attn(*x, g, return_state=True, stream=t) for x, t in zip((a, b), s)]
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 def test_empty(nats):
     g = torch.zeros(3, device="cuda")
     for shape in ((0, 3, 5, 64), (2, 3, 0, 64)):
