@@ -793,9 +793,11 @@ nats_status nats_layer_norm_bwd(const nats_norm_dims* dims, const void* dout, co
  * that after lens[b] tokens.  Tokens that take part are expected finite: a NaN
  * or an infinity may reach every output of its head.
  * bf16 operands that TMA can address (rows at multiples of 16 bytes, no
- * expanded dimension) run on the tensor cores: scores and the state ahead of a
- * chunk enter their products in bf16, the state itself is summed from
- * exact products.  Others, and fp32, run in fp32 throughout. */
+ * expanded dimension): scores and the state ahead of a chunk enter their
+ * products in bf16, half a step each; a state that is given out is summed from
+ * exact products.  Others, and fp32: every factor as two tf32 numbers, 2^-24 of
+ * it, and fp32 sums.  Waits inside the bf16 kernels are bounded
+ * (nats_decay_attn_check).  The same inputs and sizes give the same bits. */
 typedef struct {
   int32_t B, H, L;
   int32_t d;     /* head size, 64 or 128 */

@@ -60,7 +60,7 @@ struct Args {
   float scale;
   int segs, seg;        // segments of a sequence, tokens of each (in the scan's order, counted from token 0 in both)
   int first_op, last_op;  // the scans of this launch
-  int vec;              // operands may be read and written four entries at a time (SIMT kernels)
+  int vec;              // operands may be read and written four entries at a time (decay_attn.cu)
 };
 
 // gamma^m; 1 for m = 0 whatever gamma is.

@@ -2,7 +2,11 @@
 // points of the prompt form and its gradient (nats_decay_attn,
 // nats_decay_attn_bwd), the split of long sequences into segments, and the
 // fp32 kernel, which also takes bf16 operands that TMA cannot address.
-// decay.cuh has the mathematics, decay_attn_tc.cu the tensor-core kernel.
+// decay.cuh has the mathematics, decay_attn_tc.cu the bf16 kernel.
+//
+// Measured on one GB300 (fp32, d = 64): 3 x 12 heads of 1021 tokens with states
+// 50 us, of which 15 the segments' states and their join; gradient of 2 x 12
+// heads 85 us.  Error 4.6e-7 of the outputs (plain fp32 operations 2.4e-7).
 #include <cmath>
 #include <type_traits>
 

@@ -19,6 +19,14 @@
 // Roles: four warps for P, four for the state, four for the output, eight for
 // W V, one for the loads, two that issue MMAs (X, Oi, Op; dS).
 // Every wait is bounded; an expired one sets g_expired.
+//
+// Measured on one GB300, 4 x 16 heads of 8192 tokens, d = 128: 118 us, 4.5 TB/s
+// of the tensors' own bytes (HBM copy rate 6.7), 1.8 us a chunk; the three scans
+// of its gradient 349 us.  Bound by the chain of a chunk's steps, not by a unit:
+// tensor pipe 45 %, issue slots 42 %; shared memory moves 370 KB a chunk, 2900 of
+// its 3300 cycles at 128 bytes each.  64
+// columns a CTA so that few heads fill the GPU and two stages of tiles fit; 128
+// tokens a chunk because an MMA of 64 rows takes as long as one of 128.
 #include <cmath>
 #include <mutex>
 

@@ -2,6 +2,8 @@
 // of each sequence on its kept state (nats_decay_attn_step):
 //   S <- e^g S + v k^T,  o = scale S q        (S [dv, dk] fp32, in place)
 // Bound by HBM: a state is read and written once, 8 d^2 bytes a head.
+// Measured on one GB300: 96 x 16 heads of d = 128, 35.4 us (5.7 TB/s; copy rate
+// 6.7); 16 heads 4.7 us, the launch.
 #include <cmath>
 
 #include "../../include/nats.h"

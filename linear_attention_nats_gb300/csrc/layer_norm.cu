@@ -8,6 +8,11 @@
 // then the squared distances from it: no cancellation for rows far from zero).
 // The gradient forms mean and r again from x, which it reads anyway, so the
 // forward has nothing to keep.
+//
+// Measured on one GB300 (HBM copy rate 6.7 TB/s): 32,768 rows of 2048, bf16,
+// forward 50 us (5.4 TB/s), gradient 78 us (5.2 TB/s) with its weights' sums;
+// fp32 79 us (6.8) and 145 us (5.6).  524,288 rows of 64, bf16: 30 and 47 us.
+// Odd rows, entry by entry (32,768 of 2047): 124 and 131 us.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -467,6 +472,8 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
 template <bool BWD, bool FULL, class T, int VEC, int G, int NV>
 cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
   if constexpr (!BWD && G <= 32 && NV == 1 && VEC > 1) {
+    // (rows enough for four CTAs' worth of groups on every SM; 524,288 rows of 64 one row a group 35 us, four 30,
+    // fp32 67 and 42)
     constexpr int R = 4;
     if (a.rows >= 32 * kSMs * (256 / G)) {
       const long long groups = ((long long)a.rows + R - 1) / R;
@@ -492,7 +499,7 @@ cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   // as many CTAs as fit, but no more than one an SM where their sums would be more than a quarter of the rows' bytes
-  // (1024 rows of 2048, bf16: see below)
+  // (as many as fit at 1024 rows of 2048, bf16: 7 MB of sums for 12 MB of rows)
   long long most = kSMs * (fit < kBwdCtas / kSMs ? fit : kBwdCtas / kSMs);
   const long long few = (long long)a.rows * sizeof(T) * 3 / 32;
   if (most > few) most = few > kSMs ? few : kSMs;

@@ -2,6 +2,9 @@
 norm, projection, attention, norm of each head's output, projection; its
 training step against a 64-bit one, and a prompt that goes on token by token."""
 
+import os
+import re
+
 import pytest
 import torch
 
@@ -105,3 +108,24 @@ def test_prompt_and_tokens(nats):
         x = torch.stack([c["x"][b, n + t] for b, n in enumerate(lens)])
         y = tail(nats.decay_attn_step(*heads(x), g, state))
         close(y, torch.stack([want[b, n + t] for b, n in enumerate(lens)]), ("token", t))
+
+
+def test_readme_layer(nats):
+    """The README's lines as they stand there."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    lines = re.search(r"a prompt and then a token:\n\n((?:    .*\n)+)", text).group(1)
+    p, _ = inputs()
+    gen = torch.Generator().manual_seed(5)
+    z = lambda *s: torch.randn(*s, generator=gen).cuda()
+    tok = z(3, B, H, 128)
+    env = dict(nats=nats, B=B, L=L, H=H, x=p["x"].cuda(), w=p["w1"].cuda(), b=p["b1"].cuda(), w_in=z(hidden, 3 * H * 128) / 16,
+               log_decay=-torch.rand(H, generator=gen).cuda(), lens=torch.tensor([200, 130], dtype=torch.int32, device="cuda"),
+               w_head=z(128), b_head=z(128), q1=tok[0], k1=tok[1], v1=tok[2])
+    exec("\n".join(x[4:] for x in lines.splitlines()), env)
+    o, state = nats.decay_attn(env["q"], env["k"], env["v"], env["log_decay"], lens=env["lens"], return_state=True)
+    assert torch.equal(env["o"], nats.layer_norm(o, env["w_head"], env["b_head"]))
+    a = torch.exp(env["log_decay"].double())[:, None, None]
+    S = state.double() * a + tok[2].double()[..., None] * tok[1].double()[..., None, :]
+    assert float((env["state"].double() - S).abs().max()) <= 4 * 2.0 ** -24 * float((state.abs().max() + 30))
+    close(env["o1"], nats.layer_norm(((S @ tok[0].double()[..., None])[..., 0] * 128 ** -0.5).float(), env["w_head"],
+                                     env["b_head"]).cpu().double(), "token")
