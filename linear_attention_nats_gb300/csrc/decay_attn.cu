@@ -5,8 +5,8 @@
 // decay.cuh has the mathematics, decay_attn_tc.cu the bf16 kernel.
 //
 // Measured on one GB300 (fp32, d = 64): 3 x 12 heads of 1021 tokens with states
-// 50 us, of which 15 the segments' states and their join; gradient of 2 x 12
-// heads 85 us.  Error 4.6e-7 of the outputs (plain fp32 operations 2.4e-7).
+// 43 us, of which 15 the segments' states and their join; gradient of 2 x 12
+// heads 72 us.  Error 4.6e-7 of the outputs (plain fp32 operations 2.4e-7).
 #include <cmath>
 #include <type_traits>
 
@@ -71,10 +71,13 @@ struct Split {
   static constexpr int kCtas = D == 64 ? 2 : 1;  // of an SM
 };
 
-// x as the sum of two tf32 numbers, off by half a step of the second: 2^-24.
+// x as the sum of two tf32 numbers, the first rounded, the second cut off by
+// the instruction, which reads 10 bits of the fraction: 2^-22 of x.  (By cvt.rna,
+// both rounded to 2^-24, at a fraction of the rate of integer operations:
+// 3 x 12 heads of 1021 tokens, d = 64, 50 us, so 43, with the same error.)
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -213,7 +216,8 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
     __syncthreads();
     if (!STATES) {
       const float *Qw = Qs + wr * M::kRow, *Kw = Ks + wc * M::kRow, *Pw = Ps + wr * M::kP;
-      if (wr + 15 >= wc) {  // (not a warp whose columns are all ahead of its rows)
+      // (not a warp whose rows are all behind the end, or whose columns are all ahead of its rows)
+      if (wr < n && wr + 15 >= wc) {
         float p[4][4] = {};
         add_product(p, D / 8, [&](int f, int r) { return Qw[r * M::kRow + f]; },
                     [&](int f, int j) { return Kw[j * M::kRow + f]; });
@@ -227,14 +231,16 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
       }
       __syncthreads();
       float acc[4][4] = {};
-      add_product(acc, D / 8, [&](int f, int r) { return Qw[r * M::kRow + f]; },
-                  [&](int f, int c) { return Ss[f * M::kCol + wc + c]; });
+      if (wr < n && (cc > 0 || a.segs > 1 || op.s_in)) {  // (a first state of zero adds nothing)
+        add_product(acc, D / 8, [&](int f, int r) { return Qw[r * M::kRow + f]; },
+                    [&](int f, int c) { return Ss[f * M::kCol + wc + c]; });
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][e] *= Ws[at_row(e) + 1 - (back ? 1 : 0)];
+          for (int e = 0; e < 4; ++e) acc[nt][e] *= Ws[at_row(e) + 1 - (back ? 1 : 0)];
+      }
       // (columns behind the warp's last row are zero)
-      add_product(acc, (wr + 16) / 8, [&](int j, int r) { return Pw[r * M::kP + j]; },
+      add_product(acc, wr < n ? (wr + 16) / 8 : 0, [&](int j, int r) { return Pw[r * M::kP + j]; },
                   [&](int j, int c) { return Vs[j * M::kCol + wc + c]; });
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
