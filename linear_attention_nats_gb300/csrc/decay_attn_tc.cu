@@ -191,10 +191,11 @@ __device__ __forceinline__ uint32_t piece(int r, int g) { return (uint32_t)(r * 
 __device__ __forceinline__ float lo16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Warps of each role; the four of a warpgroup share a register budget (the
-// launch's 80 a thread are dealt out anew).
+// First warp of each role (P from warp 0).  The four warps of a warpgroup share
+// a register budget: the launch's 80 a thread, 480 in six warpgroups, are dealt
+// out as 80 (P), 152 (state), 72 (output), 64 and 64 (W V), 40 (loads, MMAs).
 constexpr int kThreads = 768;
-constexpr int kP = 0, kState = 4, kOut = 8, kW = 12, kLoad = 20, kMma = 21, kMmaD = 22;
+constexpr int kState = 4, kOut = 8, kW = 12, kLoad = 20, kMma = 21, kMmaD = 22;
 template <int R>
 __device__ __forceinline__ void registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));

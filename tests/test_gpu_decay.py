@@ -301,6 +301,24 @@ def test_shared_and_given(nats, dtype):
         within(want[b], o, ref.out_bound(o, size, d, L, dtype, dtype == torch.bfloat16) + size * 2.0 ** -16, b)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("L", [200, 3333])
+def test_no_state_out(nats, L, d, dtype):
+    """Calls that give no state out, whole and cut into segments: decayed values as two bf16 numbers (2^-16)."""
+    u, q, k, v = make(1, 2, L, d, dtype, "packed", n=4)
+    g = torch.tensor([-0.002, -0.3], device="cuda")
+    tc = dtype == torch.bfloat16
+    out, r = nats.decay_attn(q, k, v, g), nats.decay_attn_bwd(u, q, k, v, g)
+    assert set(r) == {"dq", "dk", "dv"}
+    o, size, _, _ = ref.attn(q[0].cpu(), k[0].cpu(), v[0].cpu(), g.cpu(), d ** -0.5, L, None)
+    within(out[0], o, ref.out_bound(o, size, d, L, dtype, tc) + size * (2.0 ** -16 if tc else 0.0), "out")
+    grads = ref.attn_bwd(u[0].cpu(), q[0].cpu(), k[0].cpu(), v[0].cpu(), g.cpu(), d ** -0.5, L, None, None)
+    for name, (x, size) in zip(("dq", "dk", "dv"), grads):
+        within(r[name][0], x, ref.out_bound(x, size, d, L, dtype, tc) + size * (2.0 ** -16 if tc else 0.0), name)
+    nats.decay_attn_check()
+
+
 def test_two_streams(nats):
     """Two calls at once, each cut into segments with a workspace of its own."""
     a, b = (make(1, 1, 4000, 128, torch.bfloat16, "heads", seed=s) for s in (1, 2))
