@@ -194,6 +194,8 @@ __device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0
 // First warp of each role (P from warp 0).  The four warps of a warpgroup share
 // a register budget: the launch's 80 a thread, 480 in six warpgroups, are dealt
 // out as 80 (P), 152 (state), 72 (output), 64 and 64 (W V), 40 (loads, MMAs).
+// Nothing that a role calls may stay a function of its own: it would be compiled
+// for more registers than the warp has left.
 constexpr int kThreads = 768;
 constexpr int kState = 4, kOut = 8, kW = 12, kLoad = 20, kMma = 21, kMmaD = 22;
 template <int R>
