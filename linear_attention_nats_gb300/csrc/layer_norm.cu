@@ -10,7 +10,7 @@
 // forward has nothing to keep.
 //
 // Measured on one GB300 (HBM copy rate 6.7 TB/s): 32,768 rows of 2048, bf16,
-// forward 50 us (5.4 TB/s), gradient 78 us (5.2 TB/s) with its weights' sums;
+// forward 47 us (5.7 TB/s), gradient 78 us (5.2 TB/s) with its weights' sums;
 // fp32 79 us (6.8) and 145 us (5.6).  524,288 rows of 64, bf16: 30 and 47 us.
 // Odd rows, entry by entry (32,768 of 2047): 124 and 131 us.
 #include <atomic>
@@ -199,27 +199,33 @@ __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], cons
   return make_float2(mean, 1.f / sqrtf(fmaf(s[0], a.inv_d, a.eps)));
 }
 
-// Thread j of a group holds pieces j, j + G, .. of its row, NV of them.
-template <bool FULL, class T, int VEC, int G, int NV>
+// Thread j of a group holds pieces j, j + G, .. of its R rows, NV of each; the
+// weights are read once for all of them.
+template <bool FULL, class T, int VEC, int G, int NV, int R>
 __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs a) {
   begin();
   __shared__ float sums[G < 128 ? 128 / G : 1][kSums<G>];
   int flip = 0;
   const int j = threadIdx.x % G;
-  const long long at = (long long)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
-  const bool live = at < a.rows;
-  const Row row = row_of(a, live ? (int)at : a.rows - 1);
-  const T* x = (const T*)row_at(a.x, row);
-  Piece<T, VEC> in[NV];
+  const long long at = ((long long)blockIdx.x * (blockDim.x / G) + threadIdx.x / G) * R;
+  Piece<T, VEC> in[R][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * G + j) * VEC;
-    if (FULL || c < a.D) in[i].load(x + c);
-    else in[i].zero();
+  for (int r = 0; r < R; ++r) {
+    const T* x = (const T*)row_at(a.x, row_of(a, at + r < a.rows ? (int)at + r : a.rows - 1));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * G + j) * VEC;
+      if (FULL || c < a.D) in[r][i].load(x + c);
+      else in[r][i].zero();
+    }
   }
-  const float2 st = statistics<FULL, T, VEC, G, NV>(in, a, j, sums[threadIdx.x / G], flip);
-  if (!live) return;
-  T* y = (T*)row_at(a.y, row);
+  float2 st[R];
+  T* y[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    st[r] = statistics<FULL, T, VEC, G, NV>(in[r], a, j, sums[threadIdx.x / G], flip);
+    y[r] = (T*)row_at(a.y, row_of(a, at + r < a.rows ? (int)at + r : a.rows - 1));
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * G + j) * VEC;
@@ -228,8 +234,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) norm_kernel(const NormArgs 
     weights(a.w ? a.w + c : nullptr, w, 1.f);
     weights(a.bias ? a.bias + c : nullptr, b, 0.f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = fmaf((in[i][e] - st.x) * st.y, w[e], b[e]);
-    Piece<T, VEC>::store(y + c, v);
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = fmaf((in[r][i][e] - st[r].x) * st[r].y, w[e], b[e]);
+      if (at + r < a.rows) Piece<T, VEC>::store(y[r] + c, v);
+    }
   }
 }
 
@@ -481,10 +490,16 @@ cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
     }
   }
   if constexpr (!BWD) {
+    // rows enough for every SM, and of 32 entries a thread or more: two of them to a group (bf16, 32,768 rows of 2048
+    // one row 50 us, two 47; 65,536 of 1024 48 and 43)
+    constexpr int R = sizeof(T) == 2 && VEC == 8 && NV * VEC >= 32 ? 2 : 1;
     // few rows: a CTA each, so that more SMs have a part
-    const int block = G >= 128 ? G : a.rows < 8 * kSMs && G >= 32 ? G : 128;
+    const bool few = a.rows < 8 * kSMs;
+    const int block = G >= 128 ? G : few && G >= 32 ? G : 128;
     const int groups = block / G;
-    return after(norm_kernel<FULL, T, VEC, G, NV>, (unsigned)(((long long)a.rows + groups - 1) / groups), dim3(block), 0, st, 0, a);
+    const long long rows = (long long)groups * (few ? 1 : R);
+    return after(few ? norm_kernel<FULL, T, VEC, G, NV, 1> : norm_kernel<FULL, T, VEC, G, NV, R>,
+                 (unsigned)((a.rows + rows - 1) / rows), dim3(block), 0, st, 0, a);
   } else {
   constexpr int kBlock = kBwdBlock<G>, kGroups = kBlock / G;
   constexpr int smem = VEC * sizeof(T) == 16 ? kAhead<G, NV> * 2 * NV * kBlock * 16 : 0;
@@ -535,9 +550,9 @@ cudaError_t choose(const NormArgs& a, bool vec, bool pairs, int* ctas, cudaStrea
     } else {
       NATS_NORM(V, 32, M);
       NATS_NORM(V, 32, 2 * M);
-      NATS_NORM(V, 64, M);
-      NATS_NORM(V, 128, M);
-      NATS_NORM(V, 256, M);
+      NATS_NORM(V, 64, 2 * M);
+      NATS_NORM(V, 128, 2 * M);
+      NATS_NORM(V, 256, 2 * M);
     }
     NATS_NORM(V, 512, M);
     return cudaErrorInvalidValue;
