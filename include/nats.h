@@ -340,9 +340,17 @@ nats_status nats_hybrid_fwd_x_profiled(const nats_dims* dims, int32_t hidden, co
  * that nothing completes, gives up after limit_ns (1 .. 1e9) and sets *flag
  * (device int) to 1 -- the path every tensor-core kernel takes when one of
  * its bounded waits expires.  NATS_ERR_NULL / NATS_ERR_VALUE for bad
- * arguments. */
+ * arguments.
+ * nats_debug_decay_wait: in the next nats_decay_attn or nats_decay_attn_bwd of
+ * this host thread that launches anything, in every CTA of its bf16 kernels
+ * one warp takes its wait for the values of chunk `chunk` (128 tokens, counted
+ * from 0 in the scan's order in each segment) as having given up, so that the
+ * waits for its part run out (1.3 s each at most, side by side).  The kernels
+ * end, their outputs are not valid, and nats_decay_attn_check reports it.
+ * -1 cancels. */
 void nats_debug_fail_stage(int32_t stage);
 nats_status nats_debug_bounded_wait(int32_t* flag, int64_t limit_ns, nats_stream_t stream);
+void nats_debug_decay_wait(int32_t chunk);
 
 /* ------------------------------------------------------------------ decode
  * The same layer in decode mode: one new token per (b, h) per call, at

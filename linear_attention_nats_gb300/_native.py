@@ -38,7 +38,7 @@ EXPORTS = ("nats_status_string", "nats_last_cuda_error", "nats_workspace_size", 
            "nats_paged_evict",
            "nats_layer_norm", "nats_layer_norm_bwd_workspace_size", "nats_layer_norm_bwd",
            "nats_decay_attn_workspace_size", "nats_decay_attn", "nats_decay_attn_bwd_workspace_size",
-           "nats_decay_attn_bwd", "nats_decay_attn_check", "nats_decay_attn_step")
+           "nats_decay_attn_bwd", "nats_decay_attn_check", "nats_decay_attn_step", "nats_debug_decay_wait")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -215,6 +215,8 @@ def _load() -> ctypes.CDLL:
     lib.nats_decay_attn_step.restype = ctypes.c_int
     lib.nats_decay_attn_check.argtypes = [P]
     lib.nats_decay_attn_check.restype = ctypes.c_int
+    lib.nats_debug_decay_wait.argtypes = [I32]
+    lib.nats_debug_decay_wait.restype = None
     return lib
 
 

@@ -61,6 +61,7 @@ struct Args {
   int segs, seg;        // segments of a sequence, tokens of each (in the scan's order, counted from token 0 in both)
   int first_op, last_op;  // the scans of this launch
   int vec;              // operands may be read and written four entries at a time (decay_attn.cu)
+  int expire;           // the chunk whose values one warp takes for overdue (nats_debug_decay_wait); -1: none
 };
 
 // gamma^m; 1 for m = 0 whatever gamma is.

@@ -400,6 +400,9 @@ bool mapped(const Tokens& x, const nats_decay_dims* m) {
   return rows_at(x, m, 16) && ok(m->B, x.b) && ok(m->H, x.h) && ok(m->L, x.t);
 }
 
+// nats_debug_decay_wait: of the next call on this host thread
+thread_local int g_expire = -1;
+
 nats_status run(Args& a, const nats_decay_dims* m, const float* log_decay, const int32_t* lens, void* ws,
                 size_t ws_bytes, cudaStream_t st) {
   a.g = log_decay, a.lens = lens, a.B = m->B, a.H = m->H, a.L = m->L;
@@ -420,6 +423,8 @@ nats_status run(Args& a, const nats_decay_dims* m, const float* log_decay, const
     if (ws_bytes < workspace(m, nops)) return NATS_ERR_WORKSPACE;
   }
   a.segs = c.segs, a.seg = c.seg, a.vec = vec;
+  a.expire = g_expire;
+  g_expire = -1;
   // the scans for dk and dv carry the same states, one the other's transpose:
   // the last scan forms them for both
   for (int i = 0; i < nops; ++i) {
@@ -539,5 +544,7 @@ nats_status nats_decay_attn_check(nats_stream_t stream) {
   const int r = record_cuda_error(expired_waits(&expired, (cudaStream_t)stream));
   return r != NATS_OK ? (nats_status)r : expired ? NATS_ERR_INTERNAL : NATS_OK;
 }
+
+void nats_debug_decay_wait(int32_t chunk) { g_expire = chunk < 0 ? -1 : chunk; }
 
 }  // extern "C"

@@ -18,7 +18,9 @@
 //
 // Roles: four warps for P, four for the state, four for the output, eight for
 // W V, one for the loads, two that issue MMAs (X, Oi, Op; dS).
-// Every wait is bounded; an expired one sets g_expired.
+// Every wait on an mbarrier is bounded; an expired one sets g_expired.  A
+// barrier of several warps is met by all of them whether their waits have
+// ended or not (W V's, the output's), so that it ends too.
 //
 // Measured on one GB300, 4 x 16 heads of 8192 tokens, d = 128: 118 us, 4.5 TB/s
 // of the tensors' own bytes (HBM copy rate 6.7), 1.8 us a chunk; the three scans
@@ -162,16 +164,17 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 // Waits for the phase of parity `parity` to complete, asleep up to 10 us a
-// try; gives up after 2^18 tries (10 ms at the least, seconds at most; the
-// waits of a CTA are for its own work, microseconds) and records it.  The
+// try; gives up after 2^17 tries (5 ms at the least, 1.3 s at most; the waits
+// of a CTA are for its own work, microseconds).  The
 // loop is kept short: the roles' code goes through one instruction cache, and
 // what is unrolled is fetched again for every chunk (4 x 16 heads of 8192 tokens:
-// 125 us; unrolled by four 226, with a clock read in the loop 165).
+// 125 us; unrolled by four 226, with a clock read in the loop 165; with the
+// limit an argument of the launch 131,072 tokens of 8 heads 328 -> 347 us).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   const uint32_t at = tc::smem_u32(bar);
   uint32_t ok = 0;
 #pragma unroll 1
-  for (int i = 0; i < (1 << 18) && !ok; ++i)
+  for (int i = 0; i < (1 << 17) && !ok; ++i)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -607,16 +610,20 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 #pragma unroll
     for (int it = 0; it < 4; ++it) w[it] = weight(it, C);
     int s = 0, phase = 0;
+    // The eight warps meet once, ahead of the ragged chunk, whether their waits have ended or not: one that leaves
+    // the loop earlier is there too (behind it), so that the others' barrier ends.
+    bool meets = ragged_c >= 0;
     for (int c = 0; c < N && ok; ++c) {
       const int n = tokens_of(c);
       uint8_t* kt = smem + s * M::kStage + M::kQ;
       uint8_t* vt = kt + M::kTile;
-      ok = wait_all(&bars[B_V + s], phase);
+      ok = wait_all(&bars[B_V + s], phase) && !(c == a.expire && warp == kW);
       if (!ragged_at(c) && !ok) break;
       if (ragged_at(c)) {
         // tokens behind the end that the loads have brought along are taken out of K (once its scores have been
         // read) and V
         ok = ok && (STATES ? wait_all(&bars[B_QK + s], phase) : wait_all(&bars[B_RAGGED], 0));
+        meets = false;
         if (!(ok = tc::group_all(2, 256, ok))) break;
         for (int e = el; e < (C - n) * 8; e += 256) {
           *(uint4*)(vt + (n + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -674,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       s = s + 1 == M::kStages ? 0 : s + 1;
       phase ^= s == 0;
     }
+    if (meets) tc::group_all(2, 256, false);
   }
   if (!ok && lane == 0) g_expired = 1;
   tc::fence_before();
