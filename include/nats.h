@@ -834,7 +834,9 @@ nats_status nats_decay_attn(const nats_decay_dims* dims, const void* q, const na
  * the gradient of S_t (R_L = scale dout_L q_L^T + dstate_out),
  *   dq_t = scale S_t^T dout_t,  dk_t = R_t^T v_t,  dv_t = R_t k_t,
  *   dstate_in = gamma R_1 (fp32, or NULL: not wanted),
- * all overwritten.  The other arguments are the forward's; no output may
+ * all overwritten.  R is held as it is defined, so dstate_out keeps its digits
+ * at any scale; the scale times an entry of the operands has to stay in fp32's
+ * normal range.  The other arguments are the forward's; no output may
  * overlap an input or another output.  Errors as the forward
  * (NATS_ERR_VALUE also for dstate_in = dstate_out). */
 size_t nats_decay_attn_bwd_workspace_size(const nats_decay_dims* dims);

@@ -10,11 +10,14 @@
 //   dk_t = R_t^T v_t,  dv_t = R_t k_t,  R_t = scale u_t q_t^T + gamma R_(t+1):
 //                                   keys u / q, values q / u, queries v / k
 // so a training step is three scans in one launch.  A state's rows go with the
-// scan's keys, its columns with the values.
+// scan's keys, its columns with the values.  R takes the scale with what is
+// added to it and is read without, so that the gradients of the states go in
+// and out as they are, whatever the scale: with x = 1 and y = scale, and the
+// other way round in these two scans,
 //
 // A chunk of n tokens, i its i-th in the scan's order, takes
-//   o_i = scale (sum_(j <= i) gamma^(i - j) (q_i k_j) v_j + gamma^(i + 1 - e) S^T q_i)
-//   S  <- gamma^n S + sum_j gamma^(n - 1 - j + e) k_j v_j^T
+//   o_i = scale sum_(j <= i) gamma^(i - j) (q_i k_j) v_j + y gamma^(i + 1 - e) S^T q_i
+//   S  <- gamma^n S + x sum_j gamma^(n - 1 - j + e) k_j v_j^T
 // with e = 0 forward; e = 1 backward, where the state that is carried is the
 // gradient of the chunk's first state (one decay further), so that no factor
 // is ever divided by gamma.  All exponents are >= 0: no decay, however fast,
@@ -45,7 +48,7 @@ struct Op {
   const float* s_in;  // [B, H, d, d] or NULL (zero)
   float* s_out;       // or NULL
   long long s_r, s_c; // elements between a state's rows, columns
-  float in_scale, out_scale;  // taken into s_in, s_out
+  int scaled;         // the state takes the scale with what is added to it, and is read without
   float* part;        // [B H, segs, d, d]: the state ahead of each segment (columns outermost), with segs > 1
   int part_t;         // part belongs to another scan, whose rows are this one's columns
   int back;

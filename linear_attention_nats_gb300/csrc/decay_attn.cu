@@ -153,6 +153,8 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
   const int tid = threadIdx.x;
   const float g = a.g[h];
   const bool vec = a.vec != 0, back = op.back != 0;
+  // the scale goes in with the values, or out with the outputs
+  const float in_scale = op.scaled ? a.scale : 1.f, out_scale = op.scaled ? 1.f : a.scale;
   const T* q = (const T*)op.q.p + b * op.q.b + h * op.q.h;
   const T* k = (const T*)op.k.p + b * op.k.b + h * op.k.h;
   const T* v = (const T*)op.v.p + b * op.v.b + h * op.v.h + slice * kWidth;
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
           if (a.segs > 1)
             s = op.part[((long long)bh * a.segs + seg) * D * D + (op.part_t ? row * D + c : c * D + row)];
           else if (op.s_in)
-            s = op.s_in[(long long)bh * D * D + row * op.s_r + c * op.s_c] * op.in_scale;
+            s = op.s_in[(long long)bh * D * D + row * op.s_r + c * op.s_c];
         }
         S[gr][nt][e] = s;
       }
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
     const int base = t0 + c * kC, n = min(kC, n_seg - c * kC);
     __syncthreads();  // the chunk before has been read, S is in place
     // (all of a thread's reads of a tile are in flight at once)
-    const auto load = [&](const T* from, long long stride, float* to, int pitch, auto width) {
+    const auto load = [&](const T* from, long long stride, float* to, int pitch, auto width, float by) {
       constexpr int kW = decltype(width)::value / 4, kN = kC * kW / 256;
       float4 x[kN];
 #pragma unroll
@@ -199,12 +201,12 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
 #pragma unroll
       for (int u = 0; u < kN; ++u) {
         const int i = tid + 256 * u;
-        *(float4*)(to + i / kW * pitch + (i % kW) * 4) = x[u];
+        *(float4*)(to + i / kW * pitch + (i % kW) * 4) = make_float4(x[u].x * by, x[u].y * by, x[u].z * by, x[u].w * by);
       }
     };
-    load(k, op.k.t, Ks, M::kRow, std::integral_constant<int, D>{});
-    load(v, op.v.t, Vs, M::kCol, std::integral_constant<int, kWidth>{});
-    if (!STATES) load(q, op.q.t, Qs, M::kRow, std::integral_constant<int, D>{});
+    load(k, op.k.t, Ks, M::kRow, std::integral_constant<int, D>{}, 1.f);
+    load(v, op.v.t, Vs, M::kCol, std::integral_constant<int, kWidth>{}, in_scale);
+    if (!STATES) load(q, op.q.t, Qs, M::kRow, std::integral_constant<int, D>{}, 1.f);
     if (!STATES && cc == 0) {  // (the first state's reads run beside the first chunk's)
 #pragma unroll
       for (int gr = 0; gr < G; ++gr)
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
         T* to = o + (base + (back ? n - 1 - i : i)) * op.o.t;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
-          store2(to + at_col(nt, 0), a.scale * acc[nt][e], a.scale * acc[nt][e + 1], vec);
+          store2(to + at_col(nt, 0), out_scale * acc[nt][e], out_scale * acc[nt][e + 1], vec);
       }
       __syncthreads();  // Ss has been read
     }
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(256, Split<D>::kCtas) scan_split_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           op.s_out[(long long)bh * D * D + (64 * gr + at_row(e)) * op.s_r + (slice * kWidth + at_col(nt, e)) * op.s_c] =
-              S[gr][nt][e] * op.out_scale;
+              S[gr][nt][e];
   }
 }
 
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   const float g = a.g[bh % a.H];
   const int len = length(a, bh / a.H);
   float* part = op.part + (long long)bh * a.segs * D * D + at;
-  float S = op.s_in ? op.s_in[(long long)bh * D * D + r * op.s_r + c * op.s_c] * op.in_scale : 0.f;
+  float S = op.s_in ? op.s_in[(long long)bh * D * D + r * op.s_r + c * op.s_c] : 0.f;
   const auto seg_at = [&](int i) { return op.back ? a.segs - 1 - i : i; };
   part[(long long)seg_at(0) * D * D] = S;
   for (int i = 1; i < a.segs; i += 8) {
@@ -505,7 +507,7 @@ nats_status nats_decay_attn(const nats_decay_dims* dims, const void* q, const na
   Args a = {};
   a.nops = 1;
   a.op[0] = {tokens(q, q_st), tokens(k, k_st), tokens(v, v_st), tokens(out, out_st), state_in, state_out,
-             1, dims->d, 1.f, 1.f, nullptr, 0, 0};
+             1, dims->d, 0, nullptr, 0, 0};
   return run(a, dims, log_decay, lens, ws, workspace_bytes, st);
 }
 
@@ -528,14 +530,12 @@ nats_status nats_decay_attn_bwd(const nats_decay_dims* dims, const void* dout, c
       !dv || !dv_st)
     return NATS_ERR_NULL;
   const Tokens tu = tokens(dout, dout_st), tq = tokens(q, q_st), tk = tokens(k, k_st), tv = tokens(v, v_st);
-  const float scale = dims->scale > 0.f ? dims->scale : 1.0f / std::sqrt((float)dims->d);
   const long long d = dims->d;
   Args a = {};
   a.nops = 3;
-  // the state's gradient is carried without the scale of the outputs
-  a.op[0] = {tu, tv, tk, tokens(dq, dq_st), state_in, nullptr, d, 1, 1.f, 1.f, nullptr, 0, 0};
-  a.op[1] = {tv, tu, tq, tokens(dk, dk_st), dstate_out, nullptr, d, 1, 1.f / scale, scale, nullptr, 0, 1};
-  a.op[2] = {tk, tq, tu, tokens(dv, dv_st), dstate_out, dstate_in, 1, d, 1.f / scale, scale, nullptr, 0, 1};
+  a.op[0] = {tu, tv, tk, tokens(dq, dq_st), state_in, nullptr, d, 1, 0, nullptr, 0, 0};
+  a.op[1] = {tv, tu, tq, tokens(dk, dk_st), dstate_out, nullptr, d, 1, 1, nullptr, 0, 1};
+  a.op[2] = {tk, tq, tu, tokens(dv, dv_st), dstate_out, dstate_in, 1, d, 1, nullptr, 0, 1};
   return run(a, dims, log_decay, lens, ws, workspace_bytes, st);
 }
 

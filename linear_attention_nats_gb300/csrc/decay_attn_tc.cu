@@ -3,11 +3,11 @@
 //
 // One CTA walks the 128-token chunks of one segment of one (scan, sequence,
 // head) and 64 of the state's columns.  Per chunk, with Q, K, V its tiles, W
-// the tokens' weights gamma^(n - 1 - j + e), all rows in memory order:
+// the tokens' weights x gamma^(n - 1 - j + e), all rows in memory order:
 //   X  = Q K^T                    (128 x 128, K = d)
 //   P  = X * gamma^|i - j| on the past side, bf16, in TMEM
 //   Oi = Q S, Op = P V            (128 x 64)
-//   o  = scale (Op + gamma^(..) Oi)
+//   o  = scale Op + y gamma^(..) Oi
 //   dS = K^T (W V)                (d x 64, K = 128), a fresh sum every chunk
 //   S  <- gamma^n S + dS          (fp32, in registers; its bf16 copy feeds Oi)
 // W V goes in as three bf16 numbers whose sum is its fp32 value, so dS is
@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     const uint32_t lane_off = (uint32_t)(32 * w) << 16;
     const bool has = 32 * w < D;
     float S[kWidth];
-    // entry (r, column i) of a state: p[i * st]
+    // entry (r, column i) of a state is p[i * s_c]; as offsets of 32 bits from one address, which are less code than
+    // an address each (prompt 121 -> 117 us, 131,072 tokens of 8 heads 356 -> 328)
     const auto column0 = [&](long long base, long long s_r, long long s_c) {
       return base + r * s_r + slice * kWidth * s_c;
     };
@@ -474,9 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       const bool cut = a.segs > 1;
       const long long s_r = cut ? (op.part_t ? D : 1) : op.s_r, s_c = cut ? (op.part_t ? 1 : D) : op.s_c;
       const float* p = (cut ? op.part : op.s_in) + column0((cut ? (long long)bh * a.segs + seg : bh) * D * D, s_r, s_c);
-      const float by = cut ? 1.f : op.in_scale;
 #pragma unroll
-      for (int i = 0; i < kWidth; ++i, p += s_c) S[i] = *p * by;
+      for (int i = 0; i < kWidth; ++i) S[i] = p[i * (int)s_c];
     }
     const auto publish = [&]() {  // the bf16 copy that the queries meet
       if (has) {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         : op.s_out + column0((long long)bh * D * D, op.s_r, op.s_c);
       const long long s_c = STATES ? D : op.s_c;
 #pragma unroll
-      for (int i = 0; i < kWidth; ++i, p += s_c) *p = STATES ? S[i] : S[i] * op.out_scale;
+      for (int i = 0; i < kWidth; ++i) p[i * (int)s_c] = S[i];
     }
   } else if (warp < kW) {
     // --------------------------------------------------------------- output
@@ -549,9 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
       const uint32_t lane_off = (uint32_t)(el & 96) << 16;
       uint8_t* tile = smem + M::offO;
       const uint64_t sc2 = tc::f2_pack(a.scale, a.scale);
+      const float read = op.scaled ? 1.f : a.scale;
       for (int c = 0; c < N; ++c) {
         const int n = tokens_of(c);
-        const float wi = i < n ? pw(back ? n - 1 - i : i + 1) * a.scale : 0.f;
+        const float wi = i < n ? pw(back ? n - 1 - i : i + 1) * read : 0.f;
         const uint64_t wi2 = tc::f2_pack(wi, wi);
         ok = wait_all(&bars[B_O], c & 1);
         if (el == 0) tc::bulk_wait_read_all();  // the last chunk's tile has left
@@ -602,9 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     registers_down<64>();
     const int el = threadIdx.x - 32 * kW, hf = el >> 7, e0 = el & 127;
     // the weights of this thread's rows, 64 hf + 16 it + e0 / 8
+    const float add = op.scaled ? a.scale : 1.f;
     const auto weight = [&](int it, int n) {
       const int j = 64 * hf + 16 * it + (e0 >> 3);
-      return j < n ? pw(back ? j + 1 : n - 1 - j) : 0.f;
+      return j < n ? pw(back ? j + 1 : n - 1 - j) * add : 0.f;
     };
     float w[4];
 #pragma unroll
