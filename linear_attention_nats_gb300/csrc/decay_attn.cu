@@ -71,13 +71,16 @@ struct Split {
   static constexpr int kCtas = D == 64 ? 2 : 1;  // of an SM
 };
 
-// x as the sum of two tf32 numbers, the first rounded, the second cut off by
-// the instruction, which reads 10 bits of the fraction: 2^-22 of x.  (By cvt.rna,
-// both rounded to 2^-24, at a fraction of the rate of integer operations:
-// 3 x 12 heads of 1021 tokens, d = 64, 50 us, so 43, with the same error.)
+// x as the sum of two tf32 numbers (10 bits of the fraction, the other 13 zero):
+// the first is x rounded, and what is left of it, at most 2^12 units in x's last
+// place, is cut off to 11 bits: one unit at most, 2^-23 of x.  (A rounding there
+// would leave a unit too.  By cvt.rna, at a fraction of the rate of integer
+// operations, 3 x 12 heads of 1021 tokens, d = 64, took 50 us where 43 were
+// measured with these and without the products of rows behind the end or with a
+// state of zero.)
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -90,7 +93,8 @@ __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], cons
 // and b_at(k, column) read an entry; a lane's rows are lane / 4 and that + 8, its
 // columns of a tile of 8 lane / 4 as B's and 2 (lane % 4), + 1 as the sum's.
 // Each factor goes in as two tf32 numbers, the product of the two second ones
-// (2^-24) left out; the small products have a sum of their own.
+// (at most 2^-11 of their factors: 2^-22) left out; the small products have a sum
+// of their own.
 template <class A, class B>
 __device__ __forceinline__ void add_product(float (&acc)[4][4], int k8, const A& a_at, const B& b_at) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
