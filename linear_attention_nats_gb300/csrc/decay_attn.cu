@@ -356,20 +356,35 @@ cudaError_t launch_split(const Args& a, bool states, cudaStream_t st) {
 
 // --------------------------------------------------------------- the split
 
+// What a cut costs, in times of one chunk of a walk: a CTA's start, in the
+// launch that forms the segments' own states too; a chunk there, which is keys
+// and values alone; the two launches ahead of the scan's.
+struct Cost {
+  double start, states_start, states, launches;
+};
+// Fitted to the times of 1 to 64 segments (powers of two and some between) for
+// 28 shapes of the bf16 and 16 of the fp32 kernel: 1 to 160 heads of 1000 to
+// 131,072 tokens, both head sizes, forward and gradient.  The cut chosen takes
+// 1.004 and 1.01 times the best one's time on average, 1.08 and 1.03 at most.
+// (Without the starts, and with all scans counted where two are formed: 1.39 and
+// 1.06; bf16, 40 heads of 4096 tokens, d = 128: 32 segments 223 us, whole 61; 64
+// heads of 8192, d = 64: 64 segments 299, two 88, whole 96; gradient of 8 heads of
+// 32,768, d = 128: 64 segments 392, nine 235, whole 441.)
+constexpr Cost kCostTc = {1.5, 2.0, 0.8, 4.0}, kCostSplit = {0.3, 0.0, 0.5, 0.5};
+
 // How many segments a sequence of `chunks` chunks is cut into, for `units`
-// independent walks (scan, sequence, head, 64 state columns).  A CTA walks one
-// segment; the states ahead of the segments come from a launch that reads keys
-// and values alone, at about half a walk's time, which has to be worth it: the
-// cut that takes the fewest rounds of chunks over the SMs is chosen.
-int segments(long long units, int chunks, int ctas) {
+// independent walks (scan, sequence, head, 64 state columns), the states ahead
+// of the segments formed for `formed` of them.  A CTA walks one segment; the cut
+// that takes the least time in rounds over the SMs is chosen.
+int segments(long long units, long long formed, int chunks, int ctas, const Cost& k) {
   int best = 1;
   double least = 1e300;
   for (int s = 1; s <= kMaxSegs && s <= chunks; ++s) {
     const int per = (chunks + s - 1) / s;
     if ((chunks + per - 1) / per != s) continue;  // a cut with an empty last segment
-    const double rounds = std::ceil((double)units * s / ctas) * per;
-    const double before = s == 1 ? 0.0 : std::ceil((double)units * (s - 1) / ctas) * per * 0.5 + 4.0;
-    if (rounds + before < least) least = rounds + before, best = s;
+    double time = std::ceil((double)units * s / ctas) * (k.start + per);
+    if (s > 1) time += std::ceil((double)formed * (s - 1) / ctas) * (k.states_start + k.states * per) + k.launches;
+    if (time < least) least = time, best = s;
   }
   return best;
 }
@@ -382,8 +397,9 @@ struct Cut {
 Cut cut(const nats_decay_dims* m, int nops, bool tc) {
   const int C = tc ? kChunkTc : kC;
   const int chunks = (m->L + C - 1) / C;
-  const long long units = (long long)nops * m->B * m->H * (m->d / kWidth);
-  const int segs = segments(units, chunks, tc ? kSMs : kSMs * (m->d == 64 ? Split<64>::kCtas : Split<128>::kCtas));
+  const long long walks = (long long)m->B * m->H * (m->d / kWidth);
+  const int segs = segments(walks * nops, walks * (nops == 3 ? 2 : 1), chunks,
+                            tc ? kSMs : kSMs * (m->d == 64 ? Split<64>::kCtas : Split<128>::kCtas), tc ? kCostTc : kCostSplit);
   return {segs, (chunks + segs - 1) / segs * C};
 }
 
