@@ -747,9 +747,12 @@ nats_status nats_paged_evict(const nats_paged_cache* cache, const int32_t* out_t
  * Rows are indexed [B, H, L, D] through element strides (the last one is 1;
  * a plain [rows, D] has B = H = 1), so they may be the heads of a
  * [B, L, H, D] tensor.  Any D from 1 to 16384; rows that start at multiples
- * of 16 bytes with D a multiple of 16 bytes move in vectors, others entry by
- * entry.  Statistics and sums in fp32, the squared distances taken from the
- * mean itself. */
+ * of 16 bytes with D a multiple of 16 bytes move in vectors (the weights at
+ * multiples of 16 bytes too), bf16 rows of even length at multiples of 4 bytes
+ * in pairs, others entry by entry.  Statistics and sums in fp32: a first mean,
+ * the distances from it and their squares, whose means give the mean and the
+ * variance, so a row of one value gives the bias whatever the value (finite
+ * rows whose squared distances' sum stays in fp32's range). */
 typedef struct {
   int32_t B, H, L; /* rows: B H L of them, below 2^31 */
   int32_t D;       /* entries of a row */

@@ -4,15 +4,16 @@
 //   with u the gradient of y and t = w u:
 //   dx = r (t - mean(t) - z mean(t z)),  dw = sum over rows of u z,  db = sum of u
 // Bound by HBM: a row is held in the registers of a group of G threads, so it
-// is read once and its statistics take two passes over registers (the mean,
-// then the squared distances from it: no cancellation for rows far from zero).
+// is read once and its statistics take two passes over registers (a first mean,
+// then the distances from it and their squares: no cancellation for rows far from
+// zero, and a mean that is off by its own rounding alone).
 // The gradient forms mean and r again from x, which it reads anyway, so the
 // forward has nothing to keep.
 //
 // Measured on one GB300 (HBM copy rate 6.7 TB/s): 32,768 rows of 2048, bf16,
-// forward 47 us (5.7 TB/s), gradient 78 us (5.2 TB/s) with its weights' sums;
-// fp32 79 us (6.8) and 145 us (5.6).  524,288 rows of 64, bf16: 30 and 47 us.
-// Odd rows, entry by entry (32,768 of 2047): 124 and 131 us.
+// forward 47 us (5.7 TB/s), gradient 81 us (5.0 TB/s) with its weights' sums;
+// fp32 79 us (6.8) and 143 us (5.6).  524,288 rows of 64, bf16: 31 and 49 us.
+// Odd rows, entry by entry (32,768 of 2047): 129 and 132 us.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -171,6 +172,17 @@ __device__ __forceinline__ void each(F&& f) {
   }
 }
 
+// The mean of a row from a first one and the mean of the distances from that
+// (a sum of D entries far from zero is some of their last places off, as much as
+// the entries of a row of one value differ from its mean, whose z is 0: without
+// this, up to 0.97 for fp32 values of 1e3 to 1e5), and the variance from their mean
+// and their squares'.  It costs 1 % of the forward's time, 3 % of the gradient's
+// (32,768 rows of 2048, bf16: 46.1 -> 46.5 us, 78.1 -> 80.6).
+__device__ __forceinline__ float2 corrected(float mean, float d, float d2, float inv_d) {
+  const float by = d * inv_d;
+  return make_float2(mean + by, fmaxf(fmaf(d2, inv_d, -by * by), 0.f));
+}
+
 // The mean and 1 / standard deviation of the row whose pieces a group holds
 // (zero behind its end).
 template <bool FULL, class T, int VEC, int G, int NV>
@@ -182,6 +194,7 @@ __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], cons
   group_sum<G>(s, sm, flip);
   const float mean = s[0] * a.inv_d;
   const uint64_t less = both(-mean);
+  uint64_t l = 0;
   t[0] = t[1] = 0;
   each<kPairs>([&](auto k) {
     uint64_t d = tc::f2_add(pair_of<k>(in), less);
@@ -193,10 +206,12 @@ __device__ __forceinline__ float2 statistics(const Piece<T, VEC> (&in)[NV], cons
       d = 0;
     }
     t[k % 2] = tc::f2_fma(d, d, t[k % 2]);
+    l = tc::f2_add(l, d);
   });
-  s[0] = sum_of(tc::f2_add(t[0], t[1]));
-  group_sum<G>(s, sm, flip);
-  return make_float2(mean, 1.f / sqrtf(fmaf(s[0], a.inv_d, a.eps)));
+  float s2[2] = {sum_of(l), sum_of(tc::f2_add(t[0], t[1]))};
+  group_sum<G>(s2, sm, flip);
+  const float2 st = corrected(mean, s2[0], s2[1], a.inv_d);
+  return make_float2(st.x, 1.f / sqrtf(st.y + a.eps));
 }
 
 // Thread j of a group holds pieces j, j + G, .. of its R rows, NV of each; the
@@ -267,25 +282,26 @@ __global__ void __launch_bounds__(256) norm_short_kernel(const NormArgs a) {
     for (int e = 0; e < VEC; ++e) s[i] += in[i][e];
   }
   group_sum<G>(s, nullptr, flip);
-  float mean[R];
+  float mean[R], d[2 * R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    mean[i] = s[i] * a.inv_d, s[i] = 0.f;
+    mean[i] = s[i] * a.inv_d, d[2 * i] = d[2 * i + 1] = 0.f;
     if (mine)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float d = in[i][e] - mean[i];
-        s[i] = fmaf(d, d, s[i]);
+        const float x = in[i][e] - mean[i];
+        d[2 * i] += x, d[2 * i + 1] = fmaf(x, x, d[2 * i + 1]);
       }
   }
-  group_sum<G>(s, nullptr, flip);
+  group_sum<G>(d, nullptr, flip);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (!mine || (long long)at + (long long)i * step >= a.rows) continue;
-    const float r = 1.f / sqrtf(fmaf(s[i], a.inv_d, a.eps));
+    const float2 st = corrected(mean[i], d[2 * i], d[2 * i + 1], a.inv_d);
+    const float r = 1.f / sqrtf(st.y + a.eps);
     float v[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = fmaf((in[i][e] - mean[i]) * r, w[e], b[e]);
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf((in[i][e] - st.x) * r, w[e], b[e]);
     Piece<T, VEC>::store((T*)row_at(a.y, row_of(a, at + i * step)) + c, v);
   }
 }
