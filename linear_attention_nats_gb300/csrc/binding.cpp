@@ -9,6 +9,7 @@
 // the package has loaded is the one that is called.
 #include <Python.h>
 
+#include <ATen/MemoryOverlap.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
@@ -110,6 +111,21 @@ Heads heads_out(const Tensor& t, const char* name, ScalarType s, IntArrayRef sha
     TORCH_CHECK_VALUE(t.strides()[i] != 0 || t.sizes()[i] <= 1, name,
                       " is written and must not be an expanded tensor");
   return h;
+}
+
+// An output that must not share memory with another argument: overlaps that torch can tell (tensors without gaps), and
+// tensors that start at one address.  `same`: the argument itself (of the same shape), at the same strides, is allowed.
+void apart(const Tensor& out, const char* name, const Tensor& t, const char* other, bool same = false) {
+  if (out.numel() == 0 || t.numel() == 0) return;
+  const bool one = out.data_ptr() == t.data_ptr();
+  if (same && one) {
+    bool alike = true;
+    for (int64_t i = 0; i < out.dim(); ++i) alike = alike && (out.size(i) <= 1 || out.stride(i) == t.stride(i));
+    if (alike) return;
+  }
+  const auto s = at::get_overlap_status(out, t);
+  TORCH_CHECK_VALUE(!one && s != at::MemOverlapStatus::Full && s != at::MemOverlapStatus::Partial, name,
+                    " must not share memory with ", other, same ? " other than as the same tensor" : "");
 }
 
 struct Rotation {
@@ -552,6 +568,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Call call(dev, a[5]);
   const Tensor out = a[4] == Py_None ? call.empty(x.sizes(), s) : tensor(a[4], "out");
   rows(out, "out", s, x.sizes(), dev, true);
+  if (a[4] != Py_None) apart(out, "out", x, "x", true);
   const Tensor* const both[2] = {&x, &out};
   const Lead<2> l(both, "x");
   const nats_norm_dims dm = {extent(l.size[0], "x"), extent(l.size[1], "x"), extent(l.size[2], "x"), extent(D, "x"), code,
@@ -576,6 +593,10 @@ PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Call call(dev, a[7]);
   const Tensor dx = a[4] == Py_None ? call.empty(x.sizes(), s) : tensor(a[4], "dx");
   rows(dx, "dx", s, x.sizes(), dev, true);
+  if (a[4] != Py_None) {
+    apart(dx, "dx", u, "dout", true);
+    apart(dx, "dx", x, "x", true);
+  }
   const Tensor* const all[3] = {&u, &x, &dx};
   const Lead<3> l(all, "x");
   const nats_norm_dims dm = {extent(l.size[0], "x"), extent(l.size[1], "x"), extent(l.size[2], "x"), extent(D, "x"), code,
@@ -638,6 +659,12 @@ PyObject* decay_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     so = call.empty({B, H, d, d}, at::kFloat);
   const Tensor out = a[9] == Py_None ? call.empty(q.sizes(), s) : tensor(a[9], "out");
   const Heads ho = heads_out(out, "out", s, q.sizes(), dev);
+  if (a[9] != Py_None) {
+    apart(out, "out", q, "q");
+    apart(out, "out", k, "k");
+    apart(out, "out", v, "v");
+  }
+  if (has_out && s_in) apart(so, "state_out", THPVariable_Unpack(a[6]), "state", true);
   const Tensor ws = call.workspace(a[10], a[10] == Py_None ? fn.decay_ws(&dm) : 0);
   done(fn.decay(&dm, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, gp, lens, s_in, ho.p, &ho.st,
                 has_state ? (float*)so.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), call.stream),
@@ -672,6 +699,12 @@ PyObject* decay_attn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   for (int i = 0; i < 3; ++i) {
     grads[i] = a[10 + i] == Py_None ? call.empty(q.sizes(), s) : tensor(a[10 + i], names[i]);
     hg[i] = heads_out(grads[i], names[i], s, q.sizes(), dev);
+    if (a[10 + i] == Py_None) continue;
+    apart(grads[i], names[i], u, "dout");
+    apart(grads[i], names[i], q, "q");
+    apart(grads[i], names[i], k, "k");
+    apart(grads[i], names[i], v, "v");
+    for (int j = 0; j < i; ++j) apart(grads[i], names[i], grads[j], names[j]);
   }
   const Tensor ws = call.workspace(a[13], a[13] == Py_None ? fn.decay_bwd_ws(&dm) : 0);
   done(fn.decay_bwd(&dm, hu.p, &hu.st, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, gp, lens, s_in, ds_out, hg[0].p,
@@ -710,6 +743,11 @@ PyObject* decay_attn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Call call(dev, a[7]);
   const Tensor out = a[6] == Py_None ? call.empty(q.sizes(), s) : tensor(a[6], "out");
   const Heads ho = token(out, "out", s, q.sizes(), dev, true);
+  if (a[6] != Py_None) {
+    apart(out, "out", q, "q");
+    apart(out, "out", k, "k");
+    apart(out, "out", v, "v");
+  }
   done(fn.decay_step(&dm, hq.p, &hq.st, hk.p, &hk.st, hv.p, &hv.st, gp, S, ho.p, &ho.st, call.stream),
        "nats_decay_attn_step");
   call.uses(a[0], a[1], a[2], a[3], a[4], a[6]);

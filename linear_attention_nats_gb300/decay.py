@@ -24,9 +24,9 @@ def decay_attn(q, k, v, log_decay, *, scale: float = 0.0, lens=None, state=None,
     constant without gradient); scale 0 for 1 / sqrt(d); lens int32 [B]
     or None: the tokens of each sequence, those behind them take no part and
     their rows of the output are zero; state: the one ahead of the first
-    token (None: zero).  Returns out (contiguous, or the given tensor), or
-    (out, the state after the last token) with return_state or state_out,
-    which may be `state` itself."""
+    token (None: zero).  Returns out (contiguous, or the given tensor, which
+    must not share memory with q, k or v), or (out, the state after the last
+    token) with return_state or state_out, which may be `state` itself."""
     return _native.operators.decay_attn(q, k, v, log_decay, scale, lens, state, return_state, state_out, out, workspace,
                                         stream)
 
@@ -36,9 +36,10 @@ def decay_attn_bwd(dout, q, k, v, log_decay, *, scale: float = 0.0, lens=None, s
                    dv: Optional[torch.Tensor] = None, workspace=None, stream=None):
     """Gradient of decay_attn: dout, the gradient of its output (q's type), and
     dstate_out, that of its last state (fp32, or None: zero), give a dict of
-    dq, dk, dv (q's type, contiguous or the given tensors) and, with state_grad,
-    dstate, the gradient of `state` (fp32).  The other arguments are the
-    forward's.  Rows behind a sequence's end are zero."""
+    dq, dk, dv (q's type, contiguous or the given tensors, which must not share
+    memory with an input or one another) and, with state_grad, dstate, the
+    gradient of `state` (fp32).  The other arguments are the forward's.  Rows
+    behind a sequence's end are zero."""
     return _native.operators.decay_attn_bwd(dout, q, k, v, log_decay, scale, lens, state, dstate_out, state_grad, dq, dk, dv,
                                             workspace, stream)
 
@@ -46,7 +47,8 @@ def decay_attn_bwd(dout, q, k, v, log_decay, *, scale: float = 0.0, lens=None, s
 def decay_attn_step(q, k, v, log_decay, state, *, scale: float = 0.0, out: Optional[torch.Tensor] = None, stream=None):
     """One new token of each sequence: q, k, v [B, H, d] (any strides but the
     last) on `state`, fp32 [B, H, d, d], which is updated in place.  Returns
-    out [B, H, d] (contiguous, or the given tensor)."""
+    out [B, H, d] (contiguous, or the given tensor, which must not share memory
+    with q, k or v)."""
     return _native.operators.decay_attn_step(q, k, v, log_decay, state, scale, out, stream)
 
 

@@ -20,7 +20,8 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6, out: Optional[to
     (x - mean) / sqrt(var + eps) * weight + bias, weight and bias fp32 [D] or
     None (1 and 0).  Any strides but the last; the dimensions ahead of it must
     come down to three where neighbours that follow one another in memory are
-    one.  Returns a new contiguous tensor, or out (x itself for in place)."""
+    one.  Returns a new contiguous tensor, or out (x itself for in place; no
+    other memory of x)."""
     return _native.operators.layer_norm(x, weight, bias, eps, out, stream)
 
 
@@ -28,6 +29,6 @@ def layer_norm_bwd(dout, x, weight=None, *, eps: float = 1e-6, dx: Optional[torc
                    weight_grads: bool = True, workspace=None, stream=None):
     """Gradient of layer_norm: dout (x's type and shape) and the forward's x,
     weight and eps give a dict of dx (x's type; the given tensor, which may be
-    dout or x itself) and, with weight_grads, dw and db (fp32 [D], the
-    gradients of weight and bias)."""
+    dout or x itself, but no other memory of theirs) and, with weight_grads, dw
+    and db (fp32 [D], the gradients of weight and bias)."""
     return _native.operators.layer_norm_bwd(dout, x, weight, eps, dx, weight_grads, workspace, stream)
