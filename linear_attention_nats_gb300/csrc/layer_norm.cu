@@ -541,8 +541,10 @@ cudaError_t go(const NormArgs& a, int* ctas, cudaStream_t st) {
 }
 
 // Threads and pieces of a row by its length: up to 64 entries a thread forward,
-// so that the steps of the row's sums are few beside its entries; 16 in the
-// gradient, which keeps two sums and a weight for each.
+// so that the steps of the row's sums are few beside its entries; up to 32 in the
+// gradient, which keeps two sums and a weight for each (16 in rows of more than
+// 4096 to 8192 entries, on 512 threads, and wherever rows move in pairs or entry by
+// entry).
 template <bool BWD, class T>
 cudaError_t choose(const NormArgs& a, bool vec, bool pairs, int* ctas, cudaStream_t st) {
   constexpr int V = sizeof(T) == 2 ? 8 : 4;
@@ -558,11 +560,14 @@ cudaError_t choose(const NormArgs& a, bool vec, bool pairs, int* ctas, cudaStrea
     NATS_NORM(V, 32, 1);
     NATS_NORM(V, 32, 2);
     if constexpr (BWD) {
-      NATS_NORM(V, 32, M / 2);
+      if constexpr (M / 2 > 2) {
+        NATS_NORM(V, 32, M / 2);
+      }
       NATS_NORM(V, 32, M);
       NATS_NORM(V, 64, M);
       NATS_NORM(V, 128, M);
       NATS_NORM(V, 512, M / 2);
+      NATS_NORM(V, 512, M);
     } else {
       NATS_NORM(V, 32, M);
       NATS_NORM(V, 32, 2 * M);
@@ -570,7 +575,6 @@ cudaError_t choose(const NormArgs& a, bool vec, bool pairs, int* ctas, cudaStrea
       NATS_NORM(V, 128, 2 * M);
       NATS_NORM(V, 256, 2 * M);
     }
-    NATS_NORM(V, 512, M);
     return cudaErrorInvalidValue;
   }
   if constexpr (V == 8) {
