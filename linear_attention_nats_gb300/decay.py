@@ -6,6 +6,10 @@ Operands are [B, H, L, d] views with any strides but the last, so q, k and v
 may lie inside one projection's output, `qkv.view(B, L, 3, H, d)[:, :, 0].transpose(1, 2)`.
 States are fp32 [B, H, d, d], a value's entries as rows.  The checks of the
 arguments are in csrc/binding.cpp.
+
+bf16 operands go to the tensor cores where every row starts at a multiple of 16
+bytes and no dimension is expanded; others take the fp32 kernel, which is 5 to 20
+times slower, so that a contiguous copy of them first is cheaper.
 """
 
 from __future__ import annotations
@@ -55,6 +59,7 @@ def decay_attn_step(q, k, v, log_decay, state, *, scale: float = 0.0, out: Optio
 def decay_attn_check(stream=None) -> None:
     """Synchronises with `stream` (None: the current one) and raises NatsError
     if a kernel of decay_attn or decay_attn_bwd has given up on a bounded wait
-    on the current device since the last such report."""
+    on that stream's device since the last such report."""
     s = torch.cuda.current_stream() if stream is None else stream
-    _native.check(_native.lib.nats_decay_attn_check(s.cuda_stream), "nats_decay_attn_check")
+    with torch.cuda.device(s.device):
+        _native.check(_native.lib.nats_decay_attn_check(s.cuda_stream), "nats_decay_attn_check")

@@ -74,3 +74,15 @@ def test_cancelled(nats):
     expire(nats, -1)
     nats.decay_attn(q, k, v, g)
     nats.decay_attn_check()
+
+
+def test_check_on_a_stream(nats):
+    """The report is of the given stream's device, after the work on it."""
+    (q, k, v, u), g, lens = operands(2, 4, 500, 128, [500, 300])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    expire(nats, 1)
+    nats.decay_attn(q, k, v, g, lens=lens, stream=side)
+    with pytest.raises(nats.NatsError):
+        nats.decay_attn_check(side)
+    nats.decay_attn_check(side)
