@@ -806,10 +806,13 @@ nats_status nats_layer_norm_bwd(const nats_norm_dims* dims, const void* dout, co
  * bf16 operands that TMA can address (rows at multiples of 16 bytes, no
  * expanded dimension): scores and the state ahead of a chunk enter their
  * products in bf16, half a step each; a state that is given out is summed from
- * exact products.  Others, and fp32: every factor as two tf32 numbers, 2^-23 of
+ * exact products (the decayed values as three bf16 numbers; where no state is
+ * given out as two, 2^-16 of them).  Others, which run at a twentieth to a
+ * fifth of the speed, and fp32: every factor as two tf32 numbers, 2^-23 of
  * it (entries below 3.39e38: the first one is rounded up), without the product
  * of two second ones, 2^-22, and fp32 sums.  Waits inside the bf16 kernels are bounded
- * (nats_decay_attn_check).  The same inputs and sizes give the same bits. */
+ * (nats_decay_attn_check).  The same inputs and sizes, with the same states
+ * asked for, give the same bits. */
 typedef struct {
   int32_t B, H, L;
   int32_t d;     /* head size, 64 or 128 */

@@ -22,11 +22,11 @@
 // barrier of several warps is met by all of them whether their waits have
 // ended or not (W V's, the output's), so that it ends too.
 //
-// Measured on one GB300, 4 x 16 heads of 8192 tokens, d = 128: 118 us, 4.5 TB/s
-// of the tensors' own bytes (HBM copy rate 6.7), 1.8 us a chunk; the three scans
-// of its gradient 349 us.  Bound by the chain of a chunk's steps, not by a unit:
-// tensor pipe 45 %, issue slots 42 %; shared memory moves 370 KB a chunk, 2900 of
-// its 3300 cycles at 128 bytes each.  64
+// Measured on one GB300, 4 x 16 heads of 8192 tokens, d = 128: 117 to 121 us, 4.5
+// TB/s of the tensors' own bytes (HBM copy rate 6.7), 1.8 us a chunk; the three
+// scans of its gradient 344 to 355 us; d = 64 88 and 191 us.  Bound by shared memory
+// and the chain of a chunk's steps: 370 to 410 KB a chunk, 2900 to 3200 of its 3300
+// cycles at 128 bytes each (tensor pipe 45 %, issue slots 42 %).  64
 // columns a CTA so that few heads fill the GPU and two stages of tiles fit; 128
 // tokens a chunk because an MMA of 64 rows takes as long as one of 128.
 #include <cmath>

@@ -7,8 +7,9 @@ its fp32 value, so products are exact.  A chunk's sum is 8 steps of 16 products,
 each cut off at 2 U of the sum so far (U = 2^-24), U each on average and 8 U in
 all if the sum were whole from the first; the three parts' sums, the carry and
 the factor of a chunk round, U each, at random.  Below 16.8 U = 1e-6.  Two parts
-leave half a step of half a step out, 2^-17 of each value at most, over sqrt(3) in
-the mean and 0.7 as the values lie in their binade: 3e-6.
+leave half a step of half a step out, 2^-16 of each value at most; in the mean, what
+the first part leaves being anywhere in its half step and its own binade setting the
+second one's, 2^-16 / sqrt(21) / 1.5 = 2.2e-6.
 
 fp32 outputs: two factors of 2^-23 at most and a product of 2^-22 left out, less
 than half of that in the mean (below 4 U), sums as above without the cuts.
